@@ -143,6 +143,8 @@ typedef enum smla_kernel {
 #define SMLA_DEVERR_INDEX_OUT_OF_RANGE 0x1  /* index < -1 or >= pool rows: slot treated as masked */
 #define SMLA_DEVERR_TIMEOUT 0x2             /* a bounded on-device wait expired; outputs are invalid */
 #define SMLA_DEVERR_INTERNAL 0x4            /* an internal limit was hit; outputs are invalid */
+#define SMLA_DEVERR_OUT_OF_PAGES 0x8        /* smla_pages_resize: too few free pages; the last entries stay -1 */
+#define SMLA_DEVERR_PAGE_STATE 0x10         /* page calls: a length, parent, table entry or count that cannot be */
 
 /*
  * Arguments of one decode call.  Zero-initialise and fill what you use.
@@ -325,6 +327,182 @@ smla_status smla_decode(const smla_args* args, void* stream);
  */
 #define SMLA_STATIC_WORKSPACE_BYTES (64u << 20)
 smla_status smla_decode_static_workspace(const smla_args* args, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The paged latent cache: latent KV rows of 512 values held in E4M3 with one
+ * float32 scale per block of tokens (the latent row is the one KV head that
+ * every query head shares), addressed by per-request page tables.  Value d of
+ * the token at position j of request b is
+ *
+ *   code[page][j % page_size][d] * scale[page][(j % page_size) / block_rows],
+ *   page = block_tables[b][j / page_size].
+ *
+ * The calls that keep it follow the conventions above: caller-owned buffers,
+ * stream-ordered launches on the current device, host-detectable mistakes as
+ * statuses before any CUDA call, device-detected ones as bits of *error_word.
+ * They read and write what the tables and lengths on the device say, so a
+ * captured call replays on the values of that moment.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct smla_cache {
+  void* rows;                     /* E4M3 codes [num_pages, page_size, 512], 16-byte aligned */
+  int64_t row_stride;             /* bytes between the rows of a page [512], a multiple of 16 */
+  int64_t page_stride;            /* bytes between pages [page_size * row_stride], a multiple of 16, at least
+                                     (page_size - 1) * row_stride + 512 */
+  float* scales;                  /* [num_pages, page_size / block_rows]; finite, not negative; scales under 2^-64
+                                     weigh a row's values as 2^-64 would */
+  int64_t scale_stride;           /* elements between pages' scales [page_size / block_rows] */
+  int64_t num_pages;              /* pages of the pool, 1 .. 2^31 - 1 */
+  int32_t page_size;              /* tokens per page, a multiple of 8, at most 2^20 */
+  int32_t block_rows;             /* tokens that share a scale; divides page_size */
+  const int32_t* block_tables;    /* [batch, max_pages] pages of each request */
+  int64_t block_table_stride;     /* row stride in elements [max_pages] */
+  int32_t max_pages;              /* page-table columns >= 1; max_pages * page_size < 2^31 */
+  int32_t batch;                  /* requests B >= 1 */
+  const int32_t* seq_lens;        /* [B] tokens of each request, this call's new tokens included */
+  const int32_t* cum_seq_lens_q;  /* [B+1] offsets of each request's new tokens, or NULL = uniform sum_q / B */
+} smla_cache;
+
+/*
+ * Attention over the cache with a sliding window and visible first tokens.
+ * Query token i of request b (q_len_b new tokens) stands at position
+ * pos = seq_lens[b] - q_len_b + i and sees the rows
+ *
+ *   j <= pos  with  j > pos - window  or  j < first_tokens;
+ *
+ * O, LSE2, sinks and the scales are as for smla_decode, and a token that sees
+ * no row (pos < 0) gets O = 0 and LSE2 = -inf.  One call serves decode steps
+ * and prefill chunks of any mix of lengths (window >= the longest sequence is
+ * plain causal attention).  Rows that a token does not see are never used,
+ * whatever they hold.  A page outside the pool that a visible position needs
+ * is treated as masked and flagged with SMLA_DEVERR_INDEX_OUT_OF_RANGE, as is
+ * a position past the table's max_pages * page_size tokens.
+ */
+typedef struct smla_window_args {
+  smla_cache cache;
+  int32_t sum_q;                    /* flattened query tokens T (0 = nothing to do) */
+  int32_t num_heads;                /* H: 1 .. 128 */
+  int32_t window;                   /* >= 1 */
+  int32_t first_tokens;             /* >= 0 */
+  const void* q;                    /* [T, H, 512] BF16, heads and dims contiguous, 16-byte aligned */
+  int64_t q_stride_token;           /* elements [H * 512], a multiple of 8 */
+  const float* sinks;               /* [H] float32 sink logits (natural-log units), or NULL */
+  float bmm1_scale, bmm2_scale;     /* QK / softmax scale; output scale */
+  const float* bmm1_scale_dev;      /* optional device float32 overriding bmm1_scale */
+  const float* bmm2_scale_dev;      /* optional device float32 overriding bmm2_scale */
+  void* out;                        /* [T, H, 512] BF16, contiguous, 16-byte aligned */
+  float* out_lse;                   /* [T, H] float32 base-2 LSE, contiguous, or NULL */
+  void* workspace;                  /* >= smla_window_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  int32_t num_splits;               /* 0 = planner; else forced split count in [1, SMLA_MAX_SPLITS] */
+  int32_t* error_word;              /* optional device int32; kernels OR SMLA_DEVERR_* bits into it */
+} smla_window_args;
+
+/* Workspace bytes smla_window_attention will need for these shapes on `device` (pointers are not looked at). */
+smla_status smla_window_workspace_size(const smla_window_args* args, int device, size_t* bytes);
+
+smla_status smla_window_attention(const smla_window_args* args, void* stream);
+
+/*
+ * Append: quantises the T new latent rows of this call into the cache, row t
+ * at position seq_lens[b] - q_len_b + i of its request.  Each block that
+ * receives rows takes the scale
+ *
+ *   s = max(old, 2^k),  2^k the smallest power of two with amax <= 448 * 2^k,
+ *
+ * amax over the block's new finite values, k held to [-64, 64], old the
+ * block's scale when it already holds older tokens of the request, else 0.
+ * New codes are RN(x / s), saturated at 448; NaN stays NaN.  Where the scale
+ * grows, the older rows of the block are rounded onto it: RN(code * (old / s)),
+ * exact for power-of-two scales down to E4M3's subnormals.  Rows behind the
+ * last token of a request and blocks that receive no row are left as they
+ * were.  A block must be written by one request only (smla_pages_resize gives
+ * each growing request its own).  A position before 0 or past the table, or a
+ * page outside the pool, is skipped and flagged with
+ * SMLA_DEVERR_INDEX_OUT_OF_RANGE.
+ */
+typedef struct smla_append_args {
+  smla_cache cache;
+  int32_t sum_q;                    /* new tokens T (0 = nothing to do) */
+  const void* latent;               /* [T, 512] BF16, 16-byte aligned */
+  int64_t latent_stride;            /* elements between tokens [512], a multiple of 8 */
+  int32_t* error_word;
+} smla_append_args;
+
+smla_status smla_cache_append(const smla_append_args* args, void* stream);
+
+/*
+ * Pages.  ref_counts[p] counts the table entries that hold page p; a page with
+ * count 0 is free.  Request b holds the pages of columns
+ * c < ceil(len_b / page_size) of its table row, -1 behind them.  The calls
+ * change tables and counts in place and are deterministic: pages are taken
+ * lowest first, in order of (request, column).
+ *
+ * smla_pages_resize: every request goes from lens[b] to new_lens[b] tokens.
+ *   First the requests that shrink (to 0: they end) drop the pages behind
+ *   their new length; a page whose count falls to 0 is free, and the entry
+ *   becomes -1.  Then those that grow take the lowest free pages.  A growing
+ *   request whose partly filled last page is shared (count > 1 after the
+ *   shrinking) gets a page of its own for it first, and the pair
+ *   (shared, own) is added to the moves: copy them (smla_pages_copy) before
+ *   the cache is written.  With too few free pages the last entries stay as
+ *   they were (-1, or the shared page) and SMLA_DEVERR_OUT_OF_PAGES is set.
+ *   Needs move_capacity >= rows.
+ * smla_pages_fork: request b with parents[b] >= 0, which must hold nothing
+ *   (lens[b] == 0), takes its parent's pages, each counted once more; out_lens
+ *   receives lens[parents[b]], and lens[b] for the others.  Parents keep their
+ *   pages; a parent may have any number of children.
+ * smla_pages_compact: the n pages in use move to pages 0 .. n - 1: the k-th
+ *   page in use at or past n to the k-th free page before it.  Tables and
+ *   counts are renumbered and the pairs (from, to) written to the moves: copy
+ *   them before the cache is used again.  Needs move_capacity >= num_pages / 2.
+ * smla_pages_copy: pages move_src[i] of every pool are copied to move_dst[i],
+ *   i < *move_count.  No page is both a source and a destination.
+ *
+ * Lengths past max_pages * page_size count as that, negative ones as 0; they,
+ * a parent outside [0, rows), a child that holds pages, a table entry outside
+ * the pool and a count that would fall below 0 set SMLA_DEVERR_PAGE_STATE and
+ * are otherwise ignored.
+ */
+typedef struct smla_pages_args {
+  int32_t* block_tables;        /* [rows, max_pages] */
+  int64_t block_table_stride;   /* row stride in elements [max_pages] */
+  int32_t rows;                 /* requests (0 = nothing to do) */
+  int32_t max_pages;            /* >= 1 */
+  int32_t page_size;            /* tokens per page >= 1; max_pages * page_size < 2^31 */
+  int32_t* ref_counts;          /* [num_pages] */
+  int64_t num_pages;            /* 1 .. 2^31 - 1 */
+  const int32_t* lens;          /* [rows] tokens before the call */
+  const int32_t* new_lens;      /* [rows] resize: tokens after it */
+  const int32_t* parents;       /* [rows] fork: request to share with, or < 0 */
+  int32_t* out_lens;            /* [rows] fork: lengths after it; not lens itself */
+  int32_t* move_src;            /* [move_capacity] resize, compact */
+  int32_t* move_dst;            /* [move_capacity] */
+  int32_t* move_count;          /* [1] */
+  int64_t move_capacity;
+  void* workspace;              /* resize, compact: >= smla_pages_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  int32_t* error_word;
+} smla_pages_args;
+
+/* Workspace bytes of smla_pages_resize and smla_pages_compact for rows, max_pages and num_pages. */
+smla_status smla_pages_workspace_size(const smla_pages_args* args, size_t* bytes);
+smla_status smla_pages_resize(const smla_pages_args* args, void* stream);
+smla_status smla_pages_fork(const smla_pages_args* args, void* stream);
+smla_status smla_pages_compact(const smla_pages_args* args, void* stream);
+
+/* A page-indexed array: page p is the page_bytes bytes at base + p * page_stride. */
+typedef struct smla_pool {
+  void* base;
+  int64_t page_bytes;
+  int64_t page_stride;          /* bytes, >= page_bytes */
+} smla_pool;
+
+/* The pool descriptions are read on the host; moves of more pools than one launch takes run as several launches. */
+smla_status smla_pages_copy(const smla_pool* pools, int32_t num_pools, int64_t num_pages, const int32_t* move_src,
+                            const int32_t* move_dst, const int32_t* move_count, int64_t move_capacity,
+                            int32_t* error_word, void* stream);
 
 /* Static text for a status code. */
 const char* smla_status_string(smla_status status);

@@ -32,6 +32,10 @@ PACKED_ROW_BYTES = {SMLA_PACKED_FP8: 584, SMLA_NVFP4: 384}
  KERNEL_TCGEN05_TOKEN_PAIRS) = 0, 1, 2, 3, 4, 5
 SCHEDULE_AUTO, SCHEDULE_GRID, SCHEDULE_BALANCED = 0, 1, 2
 DEVERR_INDEX_OUT_OF_RANGE = 0x1
+DEVERR_TIMEOUT = 0x2
+DEVERR_INTERNAL = 0x4
+DEVERR_OUT_OF_PAGES = 0x8
+DEVERR_PAGE_STATE = 0x10
 
 _c_void_p = ctypes.c_void_p
 
@@ -92,6 +96,16 @@ EXPORTS = {
     "smla_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "smla_last_error": (ctypes.c_char_p, []),
     "smla_abi_version": (ctypes.c_int, []),
+    # the paged latent cache (argument structs in cache.py)
+    "smla_window_workspace_size": (ctypes.c_int, [_c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    "smla_window_attention": (ctypes.c_int, [_c_void_p, _c_void_p]),
+    "smla_cache_append": (ctypes.c_int, [_c_void_p, _c_void_p]),
+    "smla_pages_workspace_size": (ctypes.c_int, [_c_void_p, ctypes.POINTER(ctypes.c_size_t)]),
+    "smla_pages_resize": (ctypes.c_int, [_c_void_p, _c_void_p]),
+    "smla_pages_fork": (ctypes.c_int, [_c_void_p, _c_void_p]),
+    "smla_pages_compact": (ctypes.c_int, [_c_void_p, _c_void_p]),
+    "smla_pages_copy": (ctypes.c_int, [_c_void_p, ctypes.c_int32, ctypes.c_int64, _c_void_p, _c_void_p, _c_void_p,
+                                       ctypes.c_int64, _c_void_p, _c_void_p]),
 }
 
 

@@ -1,0 +1,107 @@
+// Shared definitions of the paged latent cache: kernel-side copies of the
+// argument structs (strides already defaulted) and the launchers.
+#pragma once
+
+#include "common.cuh"
+
+namespace smla {
+
+struct CacheView {
+  uint8_t* rows;
+  int64_t row_stride, page_stride;     // bytes
+  float* scales;
+  int64_t scale_stride;                // elements
+  int32_t num_pages, page_size, block_rows;
+  const int32_t* bt;
+  int64_t bt_stride;
+  int32_t max_pages, batch;
+  const int32_t* seq_lens;
+  const int32_t* cum;                  // nullptr: uniform
+  int32_t sum_q;
+};
+
+// Request b's new tokens: [first, first + count) of the flattened batch.
+__device__ __forceinline__ void request_tokens(const CacheView& c, int b, int* first, int* count) {
+  if (c.cum != nullptr) {
+    *first = __ldg(c.cum + b);
+    *count = __ldg(c.cum + b + 1) - *first;
+  } else {
+    const int q = c.sum_q / c.batch;
+    *first = b * q;
+    *count = q;
+  }
+}
+
+struct WindowParams {
+  CacheView c;
+  int32_t H, window, first_tokens, num_splits;
+  const __nv_bfloat16* q;
+  int64_t q_stride_token;
+  const float* sinks;
+  float bmm1, bmm2;
+  const float* bmm1_dev;
+  const float* bmm2_dev;
+  __nv_bfloat16* out;
+  float* out_lse;
+  float* part_o;      // [T, S, H, 512] fp32 normalised split partials (S > 1)
+  float* part_lse;    // [T, S, H] fp32 base-2 LSE of each partial (S > 1)
+  int32_t* err;
+};
+
+constexpr int kWindowHeads = 64;      // heads of one token that a CTA takes
+constexpr int kWindowTile = 128;      // cache rows of one tile
+
+cudaError_t launch_window_attention(const WindowParams& p, cudaStream_t stream);
+
+struct AppendParams {
+  CacheView c;
+  const __nv_bfloat16* latent;
+  int64_t latent_stride;
+  int32_t* err;
+};
+
+cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream);
+
+struct PagesParams {
+  int32_t* bt;
+  int64_t bt_stride;
+  int32_t rows, max_pages, page_size, num_pages;
+  int32_t* refs;
+  const int32_t* lens;
+  const int32_t* new_lens;
+  const int32_t* parents;
+  int32_t* out_lens;
+  int32_t* move_src;
+  int32_t* move_dst;
+  int32_t* move_count;
+  int32_t* ws;
+  int32_t* err;
+};
+
+// Workspace words of resize and compact: a header, then per-row words
+// (resize) or per-page words.
+constexpr int kPagesHeader = 64;
+inline int64_t pages_workspace_words(int64_t rows, int64_t num_pages) { return kPagesHeader + 2 * rows + num_pages; }
+
+cudaError_t launch_pages_resize(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagesParams& p, cudaStream_t stream);
+
+constexpr int kCopyPools = 64;        // pools of one copy launch (kernel parameters)
+struct CopyParams {
+  struct Pool {
+    uint8_t* base;
+    int64_t stride;
+    int32_t pieces;                   // pieces of `vec` bytes in a page
+    int32_t vec;                      // 16, 4 or 1: what base, stride and page size share
+  } pool[kCopyPools];
+  int32_t num_pools, num_pages;
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* count;
+  int32_t capacity;
+  int32_t* err;
+};
+cudaError_t launch_pages_copy(const CopyParams& p, int sms, cudaStream_t stream);
+
+}  // namespace smla

@@ -1,0 +1,151 @@
+// Append to the paged latent cache: BF16 rows quantised to E4M3 with one
+// power-of-two scale per block of tokens.
+//
+//   s = max(old, 2^k), 2^k the smallest power of two with amax <= 448 * 2^k;
+//   new code = RN(x / s), older code of the block = RN(code * (old / s)).
+//
+// 448 = 1.75 * 2^8, so for amax = m * 2^e (1 <= m < 2) k is e - 8, or e - 7
+// when m > 1.75.  A CTA takes one block of one request: its scale needs every
+// new row of the block first, and no other block's.  The rows stay in
+// registers between the maximum and the rounding (blocks of up to 16 new rows;
+// longer ones are read again, from L2), so DRAM sees each row once: 1 KB in,
+// 512 B out a token.
+#include "cache.cuh"
+
+namespace smla {
+namespace {
+
+constexpr int kThreads = 128;                    // two rows of 64 threads x 8 values at a time
+constexpr int kGroups = kThreads / 64;
+constexpr int kHeld = 8;                         // rows a thread holds in registers
+constexpr int kMinExp = -64, kMaxExp = 64;
+constexpr float kMaxCode = 448.f;
+
+// Largest finite magnitude among 8 BF16 values (as 2 x 4 packed pairs).
+__device__ __forceinline__ float amax8(uint4 v, float m) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = __uint_as_float((w[i] << 16) & 0x7fff0000u), b = __uint_as_float(w[i] & 0x7fff0000u);
+    if (a < INFINITY) m = fmaxf(m, a);           // false for infinities and NaN
+    if (b < INFINITY) m = fmaxf(m, b);
+  }
+  return m;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ uint2 quantise8(uint4 v, float s) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)                    // one correctly rounded division, then one rounding to E4M3
+    h[i] = e4m3x2(__fdiv_rn(__uint_as_float(w[i] << 16), s), __fdiv_rn(__uint_as_float(w[i] & 0xffff0000u), s));
+  return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+}
+
+__global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendParams p) {
+  const CacheView& c = p.c;
+  __shared__ float s_max[kThreads / 32];
+  // unit u -> (request, block): request b's units start at first(b) / block_rows + 2 b,
+  // which leaves room for the blocks its tokens can touch, count / block_rows + 2
+  const int64_t u = blockIdx.x;
+  int lo = 0, hi = c.batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    int f, n;
+    request_tokens(c, mid, &f, &n);
+    if ((int64_t)f / c.block_rows + 2 * (int64_t)mid <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  const int b = lo;
+  int first, count;
+  request_tokens(c, b, &first, &count);
+  if (first < 0 || count <= 0 || count > c.sum_q - first) return;       // (offsets that are none: nothing is written)
+  const int64_t start = (int64_t)__ldg(c.seq_lens + b) - count;         // position of the first new token
+  const int64_t end = start + count;
+  const int64_t i = u - (first / c.block_rows + 2 * (int64_t)b);        // block of the request's touched ones
+  const int64_t from0 = start < 0 ? 0 : start;
+  if (i == 0 && start < 0 && threadIdx.x == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
+  const int64_t block0 = (from0 / c.block_rows + i) * c.block_rows;     // first position of the block
+  if (block0 >= end) return;
+  const int64_t pos0 = block0 > from0 ? block0 : from0;                 // first new position in the block
+  const int64_t pos1 = block0 + c.block_rows < end ? block0 + c.block_rows : end;
+  const int64_t column = block0 / c.page_size;
+  const int page = column < c.max_pages ? __ldg(c.bt + (int64_t)b * c.bt_stride + column) : -1;
+  if (page < 0 || page >= c.num_pages) {
+    if (threadIdx.x == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
+    return;
+  }
+  const int row0 = (int)(block0 % c.page_size);                         // the block's first row in its page
+  uint8_t* dst = c.rows + (int64_t)page * c.page_stride + (int64_t)row0 * c.row_stride;
+  float* scale = c.scales + (int64_t)page * c.scale_stride + row0 / c.block_rows;
+  const int older = (int)(pos0 - block0), rows = (int)(pos1 - pos0);
+  const __nv_bfloat16* src = p.latent + (first + (pos0 - start)) * p.latent_stride;
+  const int group = threadIdx.x >> 6, lane8 = threadIdx.x & 63;         // row parity, 8 values
+
+  uint4 held[kHeld];
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int r = k * kGroups + group;
+    if (r < rows) held[k] = __ldg(reinterpret_cast<const uint4*>(src + r * p.latent_stride) + lane8);
+  }
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (k * kGroups + group < rows) m = amax8(held[k], m);
+  for (int r = kHeld * kGroups + group; r < rows; r += kGroups)
+    m = amax8(__ldg(reinterpret_cast<const uint4*>(src + r * p.latent_stride) + lane8), m);
+  const float old = older > 0 ? *scale : 0.f;
+  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));   // not negative: orders as integers
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+  __syncthreads();                                        // also: every thread has read the old scale
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, s_max[w]);
+
+  int k = kMinExp;
+  if (m > 0.f) {
+    int e;
+    const float f = frexpf(m, &e);                        // m = f 2^e, f in [0.5, 1); 448 = 0.875 * 2^9
+    k = min(max(f <= 0.875f ? e - 9 : e - 8, kMinExp), kMaxExp);
+  }
+  const float need = ldexpf(1.f, k);
+  const float base = old > 0.f && old < INFINITY ? old : 0.f;
+  const float s = fmaxf(base, need);
+  if (threadIdx.x == 0) *scale = s;
+  if (older > 0 && old != s) {
+    const float ratio = __fdiv_rn(base, s);
+    for (int r = group; r < older; r += kGroups) {
+      uint2* at = reinterpret_cast<uint2*>(dst + r * c.row_stride) + lane8;
+      const uint2 v = *at;
+      const uint32_t w[2] = {v.x, v.y};
+      uint32_t o[2];
+#pragma unroll
+      for (int i2 = 0; i2 < 2; ++i2)
+        o[i2] = e4m3x2(e4m3_value(w[i2]) * ratio, e4m3_value(w[i2] >> 8) * ratio) |
+                e4m3x2(e4m3_value(w[i2] >> 16) * ratio, e4m3_value(w[i2] >> 24) * ratio) << 16;
+      *at = make_uint2(o[0], o[1]);
+    }
+  }
+  dst += older * c.row_stride;
+#pragma unroll
+  for (int kk = 0; kk < kHeld; ++kk) {
+    const int r = kk * kGroups + group;
+    if (r < rows) reinterpret_cast<uint2*>(dst + r * c.row_stride)[lane8] = quantise8(held[kk], s);
+  }
+  for (int r = kHeld * kGroups + group; r < rows; r += kGroups)
+    reinterpret_cast<uint2*>(dst + r * c.row_stride)[lane8] =
+        quantise8(__ldg(reinterpret_cast<const uint4*>(src + r * p.latent_stride) + lane8), s);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream) {
+  const int64_t units = (int64_t)p.c.sum_q / p.c.block_rows + 2 * (int64_t)p.c.batch;
+  cache_append_kernel<<<(unsigned)units, kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace smla

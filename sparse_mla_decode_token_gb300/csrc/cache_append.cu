@@ -19,7 +19,6 @@ constexpr int kThreads = 128;                    // two rows of 64 threads x 8 v
 constexpr int kGroups = kThreads / 64;
 constexpr int kHeld = 8;                         // rows a thread holds in registers
 constexpr int kMinExp = -64, kMaxExp = 64;
-constexpr float kMaxCode = 448.f;
 
 // Largest finite magnitude among 8 BF16 values (as 2 x 4 packed pairs).
 __device__ __forceinline__ float amax8(uint4 v, float m) {

@@ -32,7 +32,7 @@
 // the denominator takes P_j / s_j: a block's scale is folded into P, never into
 // the tile.
 //
-// Rows come by TMA as chunks of 16 (or 8) consecutive rows of one page, 5-D
+// Rows come by TMA as chunks of 32 (16, 8) consecutive rows of one page, 5-D
 // boxes {128 B, 8 rows, 4 column blocks, groups, page}, which land as 8-row
 // atoms 4096 bytes apart: K-major for S^T, MN-major for O^T.  The visible rows
 // [0, first) and [pos - window + 1, pos] are a list of such chunks; rows of a
@@ -58,16 +58,19 @@ using namespace tc;
 
 constexpr int kNH = kWindowHeads;                 // 64 heads
 constexpr int kRows = kWindowTile;                // 128 cache rows a tile
-constexpr int kSoftmaxWarps = 4;
+constexpr int kSoftmaxWarps = 8;                  // two warpgroups: all 128 rows, 32 heads each
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
-constexpr int kMmaWarp = kSoftmaxWarps;           // issues the products; allocates and frees TMEM
-constexpr int kLoadWarp = kSoftmaxWarps + 1;
-constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
+constexpr int kHW = kNH / 2;                      // heads of a softmax thread
+constexpr int kScoreWarp = kSoftmaxWarps;         // issues the first products; allocates and frees TMEM
+constexpr int kOutWarp = kSoftmaxWarps + 1;       // issues the second products
+constexpr int kLoadWarp = kSoftmaxWarps + 2;      // looks up the units and loads the rows
+constexpr int kScaleWarp = kSoftmaxWarps + 3;     // looks up the rows' masks and block scales
+constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
+constexpr int kUnitReaders = kSoftmaxWarps + 3;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 0;                     // O^T: four blocks of 128 dims, 64 columns each
 constexpr uint32_t kSCol = 256;                   // S^T: two buffers of 64 hi + 64 lo columns
 constexpr float kHeadroom = 4.f;                  // log2: a logit may pass the reference by this
-constexpr float kUnset = 3e38f;                   // minus the reference before the first row
 constexpr float kMinScaleLog2 = -64.f;
 constexpr int kTileBytes = kRows * kHeadDim;      // 64 KB
 constexpr int kGroupBytes = 8 * kHeadDim;         // 8 rows x four 128-byte column blocks
@@ -78,44 +81,47 @@ constexpr int kOffK = kOffQ + 4 * kQBlock;
 constexpr int kOffP = kOffK + 2 * kTileBytes;
 constexpr int kOffSmall = kOffP + 4 * kPHalf;
 
-struct Small {
-  float qscale[kNH];                              // bmm1 log2(e) 2^-k of each head
-  float negref[kNH];                              // headroom - reference of each head
-  float factor[kNH];
-  float wmax[kSoftmaxWarps][kNH];
-  uint64_t k_full[2], pv_done[2], s_full[2], s_empty[2], p_full[2], q_full;
-  uint32_t tmem;
-  int32_t abort_flag;
-};
-constexpr int kSmemBytes = kOffSmall + sizeof(Small) + 1024;     // 1024: the base is aligned by hand
-static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
-static_assert(kNH * (kSoftmaxThreads + 1) * 4 <= kTileBytes, "the sums' transposition fits a tile buffer");
-static_assert(kNH * kHeadDim * 2 <= kTileBytes, "the staged output fits a tile buffer");
-
-struct KernelParams {
-  WindowParams p;
-  CUtensorMap map;
-  int32_t chunk;                                  // rows of a TMA box: 16 or 8
-  int32_t groups;                                 // head groups
-};
-
-// What one CTA works on: 64 heads of a token, a range of tiles of its chunk list.
+// What a CTA works on at a time: 64 heads of a token, a range of tiles of its chunk list.
 struct Unit {
   int t, h0, heads, split, b;
   int first_chunks, window_chunk, chunks;         // list: [0, first_chunks), then from window_chunk on
-  int64_t pos, lo;                                // last and first visible position of the window
+  int pos, lo;                                    // last and first visible position of the window
   int tile0, tiles;
+};
+
+struct alignas(16) Small {
+  float qscale[kNH];                              // bmm1 log2(e) 2^-k of each head
+  float negref[kNH];                              // headroom - reference of each head
+  float wmax[4][kNH];                             // maxima or sums of each lane quarter; a head's thread, having
+                                                  // read its four, puts the change of negref in row 0, a factor in row 1
+  float scale[2][kRows];                          // block scale of each row of a tile, negative: masked
+  Unit unit[2];
+  uint64_t k_full[2], k_free[2][4], s_full[2], s_empty[2], p_full[2], scale_full[2], unit_full[2], unit_empty[2];
+  uint64_t q_full, drained[2];
+  uint32_t tmem;
+  int32_t abort_flag;
+};
+constexpr int kSmemBytes = kOffSmall + sizeof(Small);
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+static_assert(kNH * 128 * 2 == 2 * kPHalf, "a P buffer stages 128 dims of the output");
+
+struct KernelParams {
+  WindowParams p;
+  CUtensorMap map, out_map;
+  int32_t chunk;                                  // rows of a TMA box: 32, 16 or 8
+  int32_t groups;                                 // head groups
+  int32_t units;
 };
 
 __device__ __forceinline__ int chunk_at(const Unit& u, int k) {
   return k < u.first_chunks ? k : u.window_chunk + (k - u.first_chunks);
 }
 
-__device__ __forceinline__ Unit make_unit(const KernelParams& kp) {
+// Unit x (whole warp; the same result in every lane).
+__device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lane) {
   const WindowParams& p = kp.p;
   const CacheView& c = p.c;
   Unit u;
-  int x = blockIdx.x;
   u.h0 = (x % kp.groups) * kNH;
   x /= kp.groups;
   u.split = x % p.num_splits;
@@ -123,25 +129,35 @@ __device__ __forceinline__ Unit make_unit(const KernelParams& kp) {
   u.heads = min(kNH, p.H - u.h0);
   int first, count;
   if (c.cum != nullptr) {
-    // requests that end at or before this token: all threads look at once
-    int n = 0;
-    for (int base = 0; base < c.batch; base += kThreads) {
-      const int b = base + threadIdx.x;
-      n += __syncthreads_count(b < c.batch && __ldg(c.cum + b + 1) <= u.t);
+    // the request is the number of ends cum[1 .. B - 1] at or before the token: 32 looks at a time
+    int lo = 0, n = c.batch - 1;                  // among ends lo + 1 .. lo + n
+    while (n > 0) {
+      const int step = (n + 31) / 32, at = lo + min(n, (lane + 1) * step);
+      const int hits = __popc(__ballot_sync(0xffffffffu, __ldg(c.cum + at) <= u.t));
+      // (the last lanes look at the same end: their hits count once the whole range is before the token)
+      const int passed = min(n, hits * step);
+      if (hits == 32) {
+        lo += n;
+        n = 0;
+      } else {
+        lo += passed;
+        n = min(n - passed, step - 1);
+      }
     }
-    u.b = min(n, c.batch - 1);
+    u.b = lo;
   } else {
     u.b = u.t / (c.sum_q / c.batch);
   }
   request_tokens(c, u.b, &first, &count);
-  u.pos = (int64_t)__ldg(c.seq_lens + u.b) - count + (u.t - first);
-  u.lo = u.pos - p.window + 1 > 0 ? u.pos - p.window + 1 : 0;
+  u.pos = __ldg(c.seq_lens + u.b) - count + (u.t - first);
+  u.lo = (int)max((int64_t)u.pos - p.window + 1, (int64_t)0);
   u.first_chunks = u.window_chunk = u.chunks = 0;
-  const int64_t last = min(u.pos, (int64_t)c.max_pages * c.page_size - 1);
+  const int cap = c.max_pages * c.page_size, last = min(u.pos, cap - 1);
+  if (u.pos >= cap && lane == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
   if (last >= 0) {
-    u.first_chunks = (int)((min((int64_t)p.first_tokens, last + 1) + kp.chunk - 1) / kp.chunk);
-    u.window_chunk = max((int)(u.lo / kp.chunk), u.first_chunks);
-    u.chunks = u.first_chunks + max(0, (int)(last / kp.chunk) - u.window_chunk + 1);
+    u.first_chunks = (min(p.first_tokens, last + 1) + kp.chunk - 1) / kp.chunk;
+    u.window_chunk = max(u.lo / kp.chunk, u.first_chunks);
+    u.chunks = u.first_chunks + max(0, last / kp.chunk - u.window_chunk + 1);
   }
   const int per_tile = kRows / kp.chunk;
   const int tiles = (u.chunks + per_tile - 1) / per_tile, per = (tiles + p.num_splits - 1) / p.num_splits;
@@ -154,23 +170,18 @@ __device__ __forceinline__ Unit make_unit(const KernelParams& kp) {
 __device__ __forceinline__ int chunk_page(const KernelParams& kp, const Unit& u, int k) {
   const CacheView& c = kp.p.c;
   if (k >= u.chunks) return -1;
-  const int page = __ldg(c.bt + u.b * c.bt_stride + (int64_t)chunk_at(u, k) * kp.chunk / c.page_size);
+  const int page = __ldg(c.bt + u.b * c.bt_stride + (uint32_t)(chunk_at(u, k) * kp.chunk) / (uint32_t)c.page_size);
   return page >= 0 && page < c.num_pages ? page : -1;
 }
 
-// The block scale of tile row r (0 <= r < 128) of list tile `tile`; negative: masked.
-__device__ __forceinline__ float row_scale(const KernelParams& kp, const Unit& u, int tile, int r) {
-  const CacheView& c = kp.p.c;
-  const int k = tile * (kRows / kp.chunk) + r / kp.chunk;
-  const int page = chunk_page(kp, u, k);
-  if (k >= u.chunks) return -1.f;
-  const int64_t j = (int64_t)chunk_at(u, k) * kp.chunk + r % kp.chunk;
-  if (j > u.pos || (j < u.lo && j >= kp.p.first_tokens)) return -1.f;
-  if (page < 0) {
-    if (kp.p.err) atomicOr(kp.p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
-    return -1.f;
-  }
-  return fabsf(__ldg(c.scales + (int64_t)page * c.scale_stride + (int)(j % c.page_size) / c.block_rows));
+// Two numbers of magnitude at most 2^8 to E4M3 pairs, hi = RN(p) and
+// lo = RN(p - hi), through fp16 (11 bits, its subnormals end at 2^-24).
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t* hi, uint32_t* lo) {
+  const __half2 p = __floats2half2_rn(a, b);
+  const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(p), __NV_SATFINITE, __NV_E4M3);
+  const __half2 back(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3));
+  *hi = h;
+  *lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(p, back)), __NV_SATFINITE, __NV_E4M3);
 }
 
 // Q of 64 heads as E4M3 pairs: rows 0-63 hi, 64-127 lo, K-major with 128-byte
@@ -212,11 +223,8 @@ __device__ __forceinline__ void split_query(const KernelParams& kp, const Unit& 
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const float a = __uint_as_float(w[x] << 16) * up, b = __uint_as_float(w[x] & 0xffff0000u) * up;
-          const uint32_t hv = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-          const float ra = a - e4m3_value(hv), rb = b - e4m3_value(hv >> 8);
-          hi[x] = finite ? hv : 0x7f7fu;          // a head with an infinity or NaN gets NaN everywhere
-          lo[x] = finite ? (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(ra, rb), __NV_SATFINITE, __NV_E4M3) : 0u;
+          split_pair(__uint_as_float(w[x] << 16) * up, __uint_as_float(w[x] & 0xffff0000u) * up, hi + x, lo + x);
+          if (!finite) hi[x] = 0x7f7fu, lo[x] = 0u;   // a head with an infinity or NaN gets NaN everywhere
         }
         const int idx = k * 32 + lane, block = idx >> 4, ch = (idx & 15) >> 1, half = (idx & 1) * 8;
         uint8_t* at = sq + block * kQBlock + half;
@@ -227,319 +235,430 @@ __device__ __forceinline__ void split_query(const KernelParams& kp, const Unit& 
   }
 }
 
-// Two weights to E4M3 pairs: hi = RN(p), lo = RN(p - hi), through fp16 (11 bits
-// of a weight of at most 2^8, its subnormals end at 2^-24).
-__device__ __forceinline__ void split_pair(float a, float b, uint32_t* hi, uint32_t* lo) {
-  const __half2 p = __floats2half2_rn(a, b);
-  const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(p), __NV_SATFINITE, __NV_E4M3);
-  const __half2 back(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3));
-  *hi = h;
-  *lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(p, back)), __NV_SATFINITE, __NV_E4M3);
-}
-
 __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_constant__ KernelParams kp) {
-  extern __shared__ uint8_t raw[];
-  uint8_t* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];
   Small& sm = *reinterpret_cast<Small*>(smem + kOffSmall);
   const WindowParams& p = kp.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t k_addr = smem_addr(smem + kOffK), q_addr = smem_addr(smem + kOffQ), p_addr = smem_addr(smem + kOffP);
   auto bar = [](uint64_t& b) { return smem_addr(&b); };
 
+  if (smem_addr(smem) & 1023u) {                  // the operands' swizzles count on the alignment asked for above
+    if (threadIdx.x == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INTERNAL);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(sm.k_full[i]), 1);
-      mbar_init(bar(sm.pv_done[i]), 1);
+      for (int k = 0; k < 4; ++k) mbar_init(bar(sm.k_free[i][k]), 1);
       mbar_init(bar(sm.s_full[i]), 1);
       mbar_init(bar(sm.s_empty[i]), kSoftmaxWarps);
       mbar_init(bar(sm.p_full[i]), kSoftmaxWarps);
+      mbar_init(bar(sm.scale_full[i]), 1);
+      mbar_init(bar(sm.unit_full[i]), 1);
+      mbar_init(bar(sm.unit_empty[i]), kUnitReaders);
+      mbar_init(bar(sm.drained[i]), 1);
     }
     mbar_init(bar(sm.q_full), kSoftmaxWarps);
     sm.abort_flag = 0;
     fence_mbar_init_cluster();
     fence_proxy_async_smem();
   }
-  const Unit u = make_unit(kp);
-  if (u.pos >= (int64_t)p.c.max_pages * p.c.page_size && threadIdx.x == 0 && p.err)
-    atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
-  const int64_t th = (int64_t)u.t * p.H + u.h0;                               // first (token, head) of the unit
-  const int64_t part = ((int64_t)u.t * p.num_splits + u.split) * p.H + u.h0;  // first partial
-  if (u.tiles == 0) {                             // no visible row (of this split)
-    if (p.num_splits > 1) {
-      if (threadIdx.x < u.heads) p.part_lse[part + threadIdx.x] = -INFINITY;
-      return;
-    }
-    uint4* o = reinterpret_cast<uint4*>(p.out + th * kHeadDim);
-    for (int i = threadIdx.x; i < u.heads * (kHeadDim / 8); i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
-    if (p.out_lse && threadIdx.x < u.heads) p.out_lse[th + threadIdx.x] = -INFINITY;
-    return;
-  }
-  if (warp == kMmaWarp) tmem_alloc(smem_addr(&sm.tmem), kTmemCols);
+  if (warp == kScoreWarp) tmem_alloc(smem_addr(&sm.tmem), kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   Ctx cx{&sm.abort_flag, p.err};
-  const int per_tile = kRows / kp.chunk;
+  // Tiles are numbered through all units of the CTA: tile n uses buffers n & 1,
+  // and completes phase n >> 1 of their barriers.  Its second product frees the
+  // tile 32 rows at a time; k_free[b][3] is also its end.
+  const int mine = (kp.units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
 
   if (warp == kLoadWarp) {
-    // ------------------------------------------------------------- loads
-    // a lane per list entry; the pages of 32 entries are looked up at once
-    const int chunk_groups = kp.chunk / 8;
-    int loaded = 0, pages = -1;
-    for (; loaded < u.tiles; ++loaded) {
-      const int entry = loaded * per_tile;                                    // of this split's list
-      if (entry % 32 == 0) {
-        const int mine = entry + lane;
-        pages = mine < u.tiles * per_tile ? chunk_page(kp, u, u.tile0 * per_tile + mine) : -1;
-      }
-      const int b = loaded & 1;
-      if (loaded >= 2 && !warp_wait(cx, bar(sm.pv_done[b]), ((loaded >> 1) - 1) & 1)) break;
-      const bool here = lane >= entry % 32 && lane < entry % 32 + per_tile && pages >= 0;
-      const uint32_t n = __popc(__ballot_sync(0xffffffffu, here));
-      if (lane == 0) mbar_arrive_expect_tx(bar(sm.k_full[b]), n * kp.chunk * kHeadDim);
-      __syncwarp();
-      if (here) {
-        const int slot = lane - entry % 32;
-        const int64_t j = (int64_t)chunk_at(u, u.tile0 * per_tile + entry + slot) * kp.chunk;
-        tma_load_5d(k_addr + b * kTileBytes + slot * chunk_groups * kGroupBytes, &kp.map, 0, 0, 0,
-                    (int)(j % p.c.page_size) / 8, pages, bar(sm.k_full[b]));
+    // ---------------------------------------------- units, rows and scales
+    const int per_tile = kRows / kp.chunk, per_quarter = per_tile / 4, chunk_groups = kp.chunk / 8;
+    int n = 0;
+    bool ok = true;
+    for (int x = 0; ok && x < mine; ++x) {
+      const Unit u = make_unit(kp, blockIdx.x + x * gridDim.x, lane);
+      if (x >= 2) ok = warp_wait(cx, bar(sm.unit_empty[x & 1]), ((x >> 1) - 1) & 1);
+      if (!ok) break;
+      if (lane == 0) {
+        sm.unit[x & 1] = u;
+        mbar_arrive(bar(sm.unit_full[x & 1]));
+        if (u.tiles > 0)
+          bulk_prefetch_l2(p.q + (int64_t)u.t * p.q_stride_token + (int64_t)u.h0 * kHeadDim, u.heads * kHeadDim * 2);
       }
       __syncwarp();
+      int pages = -1;
+      for (int i = 0; ok && i < u.tiles; ++i, ++n) {
+        const int entry = i * per_tile, at0 = entry & 31;   // of this split's list; its place among 32 looked up at once
+        if (at0 == 0) {
+          const int e = entry + lane;
+          pages = e < u.tiles * per_tile ? chunk_page(kp, u, u.tile0 * per_tile + e) : -1;
+        }
+        const int b = n & 1, slot = lane - at0;
+        const bool here = slot >= 0 && slot < per_tile && pages >= 0;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, here)) * kp.chunk * kHeadDim;
+        const int row = chunk_at(u, u.tile0 * per_tile + entry + (here ? slot : 0)) * kp.chunk % p.c.page_size;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (n >= 2) ok = ok && warp_wait(cx, bar(sm.k_free[b][k]), ((n >> 1) - 1) & 1);
+          if (!ok) break;
+          if (k == 0 && lane == 0) mbar_arrive_expect_tx(bar(sm.k_full[b]), bytes);
+          __syncwarp();
+          if (here && slot / per_quarter == k)
+            tma_load_5d(k_addr + b * kTileBytes + slot * chunk_groups * kGroupBytes, &kp.map, 0, 0, 0, row / 8, pages,
+                        bar(sm.k_full[b]));
+        }
+        __syncwarp();
+        if (!ok) break;
+      }
     }
     // after an abort the last copies may still be in flight
-    for (int i = max(0, loaded - 2); i < loaded; ++i) drain_wait(bar(sm.k_full[i & 1]), (i >> 1) & 1);
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------- products
-    constexpr uint32_t idesc_s = idesc(true, 128, 128, false);
-    constexpr uint32_t idesc_o = idesc(true, 128, kNH, true) | kIdescAMnMajor;
-    auto scores = [&](int i) {
-      const uint32_t tile = k_addr + (i & 1) * kTileBytes, d = tmem + kSCol + (i & 1) * 128;
-      if (lane == 0) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          mma<true>(d, desc_sw128(tile + (k >> 2) * 1024 + (k & 3) * 32, 16, kGroupBytes),
-                    desc_sw128(q_addr + (k >> 2) * kQBlock + (k & 3) * 32, 16, 1024), idesc_s, k > 0);
-        mma_commit(bar(sm.s_full[i & 1]));
-      }
+    for (int i = max(0, n - 2); i < n + (ok ? 0 : 1); ++i) drain_wait(bar(sm.k_full[i & 1]), (i >> 1) & 1);
+  } else if (warp == kScaleWarp) {
+    // -------------------------------------------------- the rows' scales
+    const int per_tile = kRows / kp.chunk;
+    int n = 0;
+    bool ok = true;
+    for (int x = 0; ok && x < mine; ++x) {
+      ok = warp_wait(cx, bar(sm.unit_full[x & 1]), (x >> 1) & 1);
+      const Unit u = sm.unit[x & 1];
       __syncwarp();
-    };
-    bool ok = warp_wait(cx, bar(sm.q_full), 0) && warp_wait(cx, bar(sm.k_full[0]), 0);
-    if (ok) {
-      tc_fence_after();
-      scores(0);
+      if (lane == 0) mbar_arrive(bar(sm.unit_empty[x & 1]));
+      for (int i = 0; ok && i < u.tiles; ++i, ++n) {
+        const int b = n & 1, first = (u.tile0 + i) * per_tile;
+        float s[kRows / 32];                      // four rows a lane
+#pragma unroll
+        for (int y = 0; y < kRows / 32; ++y) {
+          const int r = y * 32 + lane, k = first + r / kp.chunk;
+          s[y] = -1.f;
+          if (k < u.chunks) {
+            const int j = chunk_at(u, k) * kp.chunk + r % kp.chunk;
+            if (j <= u.pos && (j >= u.lo || j < p.first_tokens)) {
+              const int page = chunk_page(kp, u, k);
+              if (page >= 0)
+                s[y] = fabsf(__ldg(p.c.scales + (int64_t)page * p.c.scale_stride +
+                                   (uint32_t)j % (uint32_t)p.c.page_size / (uint32_t)p.c.block_rows));
+              else if (p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
+            }
+          }
+        }
+        // (the softmax has read this buffer's last scales before it gave its P)
+        if (n >= 2) ok = warp_wait(cx, bar(sm.p_full[b]), ((n >> 1) - 1) & 1);
+        if (!ok) break;
+#pragma unroll
+        for (int y = 0; y < kRows / 32; ++y) sm.scale[b][y * 32 + lane] = s[y];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sm.scale_full[b]));
+      }
     }
-    for (int i = 0; ok && i < u.tiles; ++i) {
-      if (i + 1 < u.tiles) {
-        const int n = i + 1, use = n >> 1;
-        ok = warp_wait(cx, bar(sm.k_full[n & 1]), use & 1);
-        if (ok && use > 0) ok = warp_wait(cx, bar(sm.s_empty[n & 1]), (use - 1) & 1);
+  } else if (warp == kScoreWarp) {
+    // ------------------------------------------------------ first products
+    constexpr uint32_t idesc_s = idesc(true, 128, 128, false);
+    int n = 0, q = 0;
+    bool ok = true;
+    for (int x = 0; ok && x < mine; ++x) {
+      ok = warp_wait(cx, bar(sm.unit_full[x & 1]), (x >> 1) & 1);
+      const int tiles = sm.unit[x & 1].tiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sm.unit_empty[x & 1]));
+      if (!ok || tiles == 0) continue;
+      ok = warp_wait(cx, bar(sm.q_full), q++ & 1);
+      for (int i = 0; ok && i < tiles; ++i, ++n) {
+        const int b = n & 1;
+        ok = warp_wait(cx, bar(sm.k_full[b]), (n >> 1) & 1);
+        if (ok && n >= 2) ok = warp_wait(cx, bar(sm.s_empty[b]), ((n >> 1) - 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        scores(n);
-      }
-      ok = warp_wait(cx, bar(sm.p_full[i & 1]), (i >> 1) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t tile = k_addr + (i & 1) * kTileBytes, pb = p_addr + (i & 1) * 2 * kPHalf;
+        if (lane == 0) {
+          const uint32_t tile = k_addr + b * kTileBytes;
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+          for (int k = 0; k < 16; ++k)
+            mma<true>(tmem + kSCol + b * 128, desc_sw128(tile + (k >> 2) * 1024 + (k & 3) * 32, 16, kGroupBytes),
+                      desc_sw128(q_addr + (k >> 2) * kQBlock + (k & 3) * 32, 16, 1024), idesc_s, k > 0);
+          mma_commit(bar(sm.s_full[b]));
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) mma_commit(bar(sm.drained[0]));
+    drain_wait(bar(sm.drained[0]), 0);
+  } else if (warp == kOutWarp) {
+    // ----------------------------------------------------- second products
+    constexpr uint32_t idesc_o = idesc(true, 128, kNH, true) | kIdescAMnMajor;
+    int n = 0;
+    bool ok = true;
+    for (int x = 0; ok && x < mine; ++x) {
+      ok = warp_wait(cx, bar(sm.unit_full[x & 1]), (x >> 1) & 1);
+      const int tiles = sm.unit[x & 1].tiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sm.unit_empty[x & 1]));
+      for (int i = 0; ok && i < tiles; ++i, ++n) {
+        const int b = n & 1;
+        ok = warp_wait(cx, bar(sm.p_full[b]), (n >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t tile = k_addr + b * kTileBytes, pb = p_addr + b * 2 * kPHalf;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint64_t a = desc_sw128(tile + m * 1024 + k * 4 * kGroupBytes, 1024, kGroupBytes);
-            mma<true>(tmem + kOCol + m * kNH, a, desc_sw64(pb + k * 32 * kNH, 512, 512), idesc_o, i > 0 || k > 0);
-            mma<true>(tmem + kOCol + m * kNH, a, desc_sw64(pb + kPHalf + k * 32 * kNH, 512, 512), idesc_o, 1u);
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+              for (int m = 0; m < 4; ++m)
+                mma<true>(tmem + kOCol + m * kNH, desc_sw128(tile + m * 1024 + k * 4 * kGroupBytes, 1024, kGroupBytes),
+                          desc_sw64(pb + half * kPHalf + k * 32 * kNH, 512, 512), idesc_o, i > 0 || k > 0 || half > 0);
+            mma_commit(bar(sm.k_free[b][k]));
           }
-        mma_commit(bar(sm.pv_done[i & 1]));
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
+    if (lane == 0) mma_commit(bar(sm.drained[1]));
+    drain_wait(bar(sm.drained[1]), 0);
   } else {
-    // ----------------------------------------------------------- softmax
-    split_query(kp, u, smem + kOffQ, sm, warp, lane);
-    if (threadIdx.x < kNH) sm.negref[threadIdx.x] = kUnset;
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(sm.q_full));
-    const int r = threadIdx.x;                    // row of the tile = TMEM lane
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    float sum[kNH];
-#pragma unroll
-    for (int h = 0; h < kNH; ++h) sum[h] = 0.f;
-    named_bar_sync(1, kSoftmaxThreads);           // qscale and negref are written
-    float scale = row_scale(kp, u, u.tile0, r);
-    bool failed = false;
-    for (int i = 0; i < u.tiles; ++i) {
-      const int b = i & 1;
-      const float s = scale;
-      if (i + 1 < u.tiles) scale = row_scale(kp, u, u.tile0 + i + 1, r);      // in flight during this tile
-      const bool seen = s >= 0.f;
-      const float ls = seen ? fmaxf(fast_log2(s), kMinScaleLog2) : 0.f;
-      const float inv = seen ? fast_exp2(-ls) : 0.f;
-      failed |= !warp_wait(cx, bar(sm.s_full[b]), (i >> 1) & 1);
-      tc_fence_after();
-      float d[kNH];                               // t - reference + headroom
-#pragma unroll
-      for (int g = 0; g < kNH; g += 32) {
-        uint32_t hi[32], lo[32];
-        tmem_ld32(tmem + lane_base + kSCol + b * 128 + g, hi);
-        tmem_ld32(tmem + lane_base + kSCol + b * 128 + kNH + g, lo);
-        tmem_wait_ld();
-#pragma unroll
-        for (int h = 0; h < 32; ++h) {
-          const float x = (__uint_as_float(hi[h]) + __uint_as_float(lo[h])) * sm.qscale[g + h];
-          d[g + h] = seen ? fmaf(x, s, ls) : -INFINITY;
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(sm.s_empty[b]));
-      float top = -INFINITY;
-#pragma unroll
-      for (int h = 0; h < kNH; ++h) top = fmaxf(top, d[h] + sm.negref[h]);
-      if (named_bar_or(1, kSoftmaxThreads, failed || top > 2.f * kHeadroom)) {
-        // ---- a new reference: the heads' maxima over the tile
-        if (named_bar_or(1, kSoftmaxThreads, failed)) break;
-#pragma unroll
-        for (int h = 0; h < kNH; ++h) {
-          const float m = warp_max(d[h]);
-          if (lane == (h & 31)) sm.wmax[warp][h] = m;
-        }
-        named_bar_sync(1, kSoftmaxThreads);
-        float neg = 0.f, a = 1.f;
-        if (r < kNH) {
-          float m = fmaxf(fmaxf(sm.wmax[0][r], sm.wmax[1][r]), fmaxf(sm.wmax[2][r], sm.wmax[3][r]));
-          const float old = sm.negref[r];
-          neg = m > -INFINITY ? fminf(old, kHeadroom - m) : old;
-          a = fast_exp2(neg - old);
-        }
-        named_bar_sync(1, kSoftmaxThreads);
-        if (r < kNH) {
-          sm.negref[r] = neg;
-          sm.factor[r] = a;
-        }
-        named_bar_sync(1, kSoftmaxThreads);
-#pragma unroll
-        for (int h = 0; h < kNH; ++h) sum[h] *= sm.factor[h];
-        if (i > 0) {
-          // O^T by column, once the products into it are done
-          failed |= !warp_wait(cx, bar(sm.pv_done[b ^ 1]), ((i - 1) >> 1) & 1);
-          tc_fence_after();
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            uint32_t o[32];
-            tmem_ld32(tmem + lane_base + kOCol + g * 32, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int h = 0; h < 32; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * sm.factor[(g & 1) * 32 + h]);
-            tmem_st32(tmem + lane_base + kOCol + g * 32, o);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-        }
-      }
-      // P in E4M3 pairs: row r of the MN-major operand is 64 bytes, heads along it
-      uint8_t* pb = smem + kOffP + b * 2 * kPHalf + r * kNH;
-#pragma unroll
-      for (int g = 0; g < kNH; g += 16) {
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int h = g + 2 * e;
-          const float x = fast_exp2(d[h] + sm.negref[h]), y = fast_exp2(d[h + 1] + sm.negref[h + 1]);
-          sum[h] = fmaf(x, inv, sum[h]);
-          sum[h + 1] = fmaf(y, inv, sum[h + 1]);
-          split_pair(x, y, hi + e, lo + e);
-        }
-        const int at = ((g >> 4) ^ ((r >> 1) & 3)) << 4;                      // 64-byte swizzle
-        *reinterpret_cast<uint4*>(pb + at) = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16,
-                                                        hi[6] | hi[7] << 16);
-        *reinterpret_cast<uint4*>(pb + kPHalf + at) = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16,
-                                                                 lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
-      }
-      if (!seen) {
-        // the first product has read the row (its commit is what s_full waited for); the second must find zeros
-        uint8_t* row = smem + kOffK + b * kTileBytes + (r >> 3) * kGroupBytes + (r & 7) * 128;
-        for (int cb = 0; cb < 4; ++cb)
-          for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4*>(row + cb * 1024 + x * 16) = make_uint4(0, 0, 0, 0);
-      }
+    // ------------------------------------------------------------- softmax
+    const int r = threadIdx.x & (kRows - 1);      // row of the tile = TMEM lane
+    const int hw = (threadIdx.x / kRows) * kHW;   // first of the thread's heads
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    uint64_t sum[kHW / 2];                        // of two heads each
+    int n = 0;
+    bool failed = !warp_wait(cx, bar(sm.unit_full[0]), 0);
+    if (!failed && sm.unit[0].tiles > 0) {
+      split_query(kp, sm.unit[0], smem + kOffQ, sm, warp, lane);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(sm.p_full[b]));
+      if (lane == 0) mbar_arrive(bar(sm.q_full));
     }
-
-    // ------------------------------------------------------------ results
-    const int n = u.tiles - 1;
-    failed |= !warp_wait(cx, bar(sm.pv_done[n & 1]), (n >> 1) & 1);
-    tc_fence_after();
-    if (!named_bar_or(1, kSoftmaxThreads, failed)) {
-      // sums over the rows: transposed through the second tile buffer
-      float* ts = reinterpret_cast<float*>(smem + kOffK + kTileBytes);
+    if (threadIdx.x < kNH) sm.negref[threadIdx.x] = 0.f;
+    for (int x = 0; x < mine; ++x) {
+      if (named_bar_or(1, kSoftmaxThreads, failed)) break;   // also: qscale and negref are written
+      const int tiles = sm.unit[x & 1].tiles;
 #pragma unroll
-      for (int h = 0; h < kNH; ++h) ts[h * (kSoftmaxThreads + 1) + r] = sum[h];
-      named_bar_sync(1, kSoftmaxThreads);
-      const int h2 = r >> 1;
+      for (int e = 0; e < kHW / 2; ++e) sum[e] = 0;
+      bool fresh = true;                          // some head has no reference yet
+      int i = 0;
+      for (; i < tiles; ++i, ++n) {
+        const int b = n & 1;
+        failed |= !warp_wait(cx, bar(sm.scale_full[b]), (n >> 1) & 1);
+        const float s = sm.scale[b][r];
+        const bool seen = s >= 0.f;
+        const float ls = fmaxf(fast_log2(s), kMinScaleLog2), inv = fast_exp2(-ls);
+        failed |= !warp_wait(cx, bar(sm.s_full[b]), (n >> 1) & 1);
+        tc_fence_after();
+        uint64_t d[kHW / 2];                      // t - reference + headroom
+        {
+          uint32_t hi[kHW], lo[kHW];
+          tmem_ld32(lane_base + kSCol + b * 128 + hw, hi);
+          tmem_ld32(lane_base + kSCol + b * 128 + kNH + hw, lo);
+          tmem_wait_ld();
+          const uint64_t s2 = f2_pack(s, s), ls2 = f2_pack(ls, ls);
+#pragma unroll
+          for (int e = 0; e < kHW / 2; e += 2) {
+            const ulonglong2 qs = *reinterpret_cast<const ulonglong2*>(sm.qscale + hw + 2 * e);
+            const ulonglong2 ng = *reinterpret_cast<const ulonglong2*>(sm.negref + hw + 2 * e);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int h = 2 * (e + k);
+              const uint64_t v = f2_add(f2_pack(__uint_as_float(hi[h]), __uint_as_float(hi[h + 1])),
+                                        f2_pack(__uint_as_float(lo[h]), __uint_as_float(lo[h + 1])));
+              d[e + k] = f2_add(f2_fma(f2_mul(v, k ? qs.y : qs.x), s2, ls2), k ? ng.y : ng.x);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sm.s_empty[b]));
+        float top = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kHW / 2; ++e) {
+          float v, w;
+          f2_unpack(d[e], v, w);
+          top = fmaxf(top, fmaxf(v, w));
+        }
+        if (i == 0 && threadIdx.x == 0) bulk_store_wait_read<0>();   // the last unit's output has left the P buffers
+        if (named_bar_or(1, kSoftmaxThreads, failed || fresh || (seen && top > 2.f * kHeadroom))) {
+          // ---- a new reference: the heads' maxima over the tile
+          if (named_bar_or(1, kSoftmaxThreads, failed)) break;
+#pragma unroll
+          for (int e = 0; e < kHW / 2; ++e) {
+            float v, w;
+            f2_unpack(d[e], v, w);
+            v = warp_max(seen ? v : -INFINITY);
+            w = warp_max(seen ? w : -INFINITY);
+            if (lane == e) *reinterpret_cast<float2*>(&sm.wmax[warp & 3][hw + 2 * e]) = make_float2(v, w);
+          }
+          named_bar_sync(1, kSoftmaxThreads);
+          bool unset = false;
+          if (threadIdx.x < kNH) {
+            const int h = threadIdx.x;
+            // by how much the tile's maximum passes the reference
+            const float m = fmaxf(fmaxf(sm.wmax[0][h], sm.wmax[1][h]), fmaxf(sm.wmax[2][h], sm.wmax[3][h])) - kHeadroom;
+            unset = fresh && m == -INFINITY;
+            const float up = m == -INFINITY ? 0.f : fresh ? m : fmaxf(m, 0.f);
+            sm.negref[h] -= up;
+            sm.wmax[0][h] = -up;
+            sm.wmax[1][h] = fresh ? 0.f : fast_exp2(-up);
+          }
+          fresh = named_bar_or(1, kSoftmaxThreads, unset);
+          if (i > 0) {
+            // O^T by column, once the products into it are done
+            failed |= !warp_wait(cx, bar(sm.k_free[b ^ 1][3]), ((n - 1) >> 1) & 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int m = 0; m < 4; ++m) {
+              uint32_t o[kHW];
+              tmem_ld32(lane_base + kOCol + m * kNH + hw, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int h = 0; h < kHW; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * sm.wmax[1][hw + h]);
+              tmem_st32(lane_base + kOCol + m * kNH + hw, o);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+#pragma unroll
+          for (int e = 0; e < kHW / 2; ++e) {
+            d[e] = f2_add(d[e], *reinterpret_cast<const uint64_t*>(sm.wmax[0] + hw + 2 * e));
+            sum[e] = f2_mul(sum[e], *reinterpret_cast<const uint64_t*>(sm.wmax[1] + hw + 2 * e));
+          }
+        }
+        // P in E4M3 pairs: row r of the MN-major operand is 64 bytes, heads along it
+        uint8_t* pb = smem + kOffP + b * 2 * kPHalf + r * kNH;
+        const uint64_t inv2 = f2_pack(inv, inv);
+#pragma unroll
+        for (int g = 0; g < kHW; g += 16) {
+          uint32_t hi[8] = {}, lo[8] = {};
+          if (seen) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float v, w;
+              f2_unpack(d[g / 2 + e], v, w);
+              v = fast_exp2(v);
+              w = fast_exp2(w);
+              sum[g / 2 + e] = f2_fma(f2_pack(v, w), inv2, sum[g / 2 + e]);
+              split_pair(v, w, hi + e, lo + e);
+            }
+          }
+          const int at = (((hw + g) >> 4) ^ ((r >> 1) & 3)) << 4;             // 64-byte swizzle
+          *reinterpret_cast<uint4*>(pb + at) = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16,
+                                                          hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
+          *reinterpret_cast<uint4*>(pb + kPHalf + at) = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16,
+                                                                   lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+        }
+        if (!seen) {
+          // the first product has read the row (its commit is what s_full waited for); the second must find zeros
+          uint8_t* row = smem + kOffK + b * kTileBytes + (r >> 3) * kGroupBytes + (r & 7) * 128 + (hw / kHW) * 2048;
+          for (int cb = 0; cb < 2; ++cb)
+            for (int y = 0; y < 8; ++y) *reinterpret_cast<uint4*>(row + cb * 1024 + y * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sm.p_full[b]));
+      }
+      if (i < tiles) break;                       // a wait gave up (all threads agreed)
+
+      // the next unit's queries, while the last products of this one run (their
+      // buffer is free: the last S of this unit has been read)
+      const int t = sm.unit[x & 1].t, h0 = sm.unit[x & 1].h0, heads = sm.unit[x & 1].heads, split = sm.unit[x & 1].split;
+      if (x + 1 < mine) {
+        failed |= !warp_wait(cx, bar(sm.unit_full[(x + 1) & 1]), ((x + 1) >> 1) & 1);
+        if (!failed && sm.unit[(x + 1) & 1].tiles > 0) {
+          split_query(kp, sm.unit[(x + 1) & 1], smem + kOffQ, sm, warp, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(sm.q_full));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sm.unit_empty[x & 1]));
+
+      // ---------------------------------------------------------- results
+      const int64_t th = (int64_t)t * p.H + h0;                               // first (token, head) of the unit
+      const int64_t part = ((int64_t)t * p.num_splits + split) * p.H + h0;  // first partial
+      if (tiles == 0) {                           // no visible row (of this split)
+        if (p.num_splits > 1) {
+          if (threadIdx.x < heads) p.part_lse[part + threadIdx.x] = -INFINITY;
+        } else {
+          uint4* o = reinterpret_cast<uint4*>(p.out + th * kHeadDim);
+          for (int k = threadIdx.x; k < heads * (kHeadDim / 8); k += kSoftmaxThreads) o[k] = make_uint4(0, 0, 0, 0);
+          if (p.out_lse && threadIdx.x < heads) p.out_lse[th + threadIdx.x] = -INFINITY;
+        }
+        continue;
+      }
+      // sums over the rows: a reduction over lanes and warps, one head at a time per thread
       float total = 0.f;
-      for (int k = 0; k < kSoftmaxThreads / 2; ++k)
-        total += ts[h2 * (kSoftmaxThreads + 1) + (r & 1) * (kSoftmaxThreads / 2) + k];
-      total += __shfl_xor_sync(0xffffffffu, total, 1);
-      if ((r & 1) == 0) {
+#pragma unroll
+      for (int e = 0; e < kHW / 2; ++e) {
+        float v, w;
+        f2_unpack(sum[e], v, w);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          v += __shfl_xor_sync(0xffffffffu, v, o);
+          w += __shfl_xor_sync(0xffffffffu, w, o);
+        }
+        if (lane == 2 * e) total = v;
+        if (lane == 2 * e + 1) total = w;
+      }
+      failed |= !warp_wait(cx, bar(sm.k_free[(n - 1) & 1][3]), ((n - 1) >> 1) & 1);
+      tc_fence_after();
+      if (named_bar_or(1, kSoftmaxThreads, failed)) break;
+      sm.wmax[warp & 3][hw + lane] = total;
+      named_bar_sync(1, kSoftmaxThreads);
+      if (threadIdx.x < kNH) {
+        const int h = threadIdx.x;
+        total = (sm.wmax[0][h] + sm.wmax[1][h]) + (sm.wmax[2][h] + sm.wmax[3][h]);
         float f = 0.f, lse = -INFINITY;
         if (!(total == 0.f)) {                    // NaN passes
-          lse = fast_log2(total) - sm.negref[h2];
+          lse = fast_log2(total) - sm.negref[h];
           f = 1.f / total;
           if (p.num_splits == 1) {
             f *= load_scale(p.bmm2, p.bmm2_dev);
-            if (p.sinks != nullptr && h2 < u.heads) f *= 1.f / (1.f + fast_exp2(__ldg(p.sinks + u.h0 + h2) * kLog2e - lse));
+            if (p.sinks != nullptr && h < heads) f *= 1.f / (1.f + fast_exp2(__ldg(p.sinks + h0 + h) * kLog2e - lse));
           }
         }
-        sm.factor[h2] = f;
-        if (h2 < u.heads) {
-          if (p.num_splits > 1) p.part_lse[part + h2] = lse;
-          else if (p.out_lse) p.out_lse[th + h2] = lse;
+        sm.wmax[1][h] = f;
+        sm.negref[h] = 0.f;                       // the next unit's
+        if (h < heads) {
+          if (p.num_splits > 1) p.part_lse[part + h] = lse;
+          else if (p.out_lse) p.out_lse[th + h] = lse;
         }
       }
       named_bar_sync(1, kSoftmaxThreads);
 #pragma unroll 1
-      for (int g = 0; g < 8; ++g) {               // dims 128 (g / 2) .. + 127, heads 32 (g % 2) .. + 31
-        uint32_t o[32];
-        tmem_ld32(tmem + lane_base + kOCol + g * 32, o);
+      for (int m = 0; m < 4; ++m) {               // dims 128 m .. + 127, one a thread
+        uint32_t o[kHW];
+        tmem_ld32(lane_base + kOCol + m * kNH + hw, o);
+        if (p.num_splits == 1 && m >= 2) {        // the staging buffer's last copy has been read
+          if (threadIdx.x == 0) bulk_store_wait_read<1>();
+          named_bar_sync(1, kSoftmaxThreads);
+        }
         tmem_wait_ld();
-        const int dim = (g >> 1) * 128 + r, hb = (g & 1) * 32;
         if (p.num_splits > 1) {
-          float* dst = p.part_o + (part + hb) * kHeadDim + dim;
+          float* dst = p.part_o + (part + hw) * kHeadDim + m * 128 + r;
 #pragma unroll
-          for (int h = 0; h < 32; ++h)
-            if (hb + h < u.heads) dst[h * kHeadDim] = __uint_as_float(o[h]) * sm.factor[hb + h];
+          for (int h = 0; h < kHW; ++h)
+            if (hw + h < heads) dst[h * kHeadDim] = __uint_as_float(o[h]) * sm.wmax[1][hw + h];
         } else {
-          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(smem + kOffK) + hb * kHeadDim + dim;
+          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(smem + kOffP + (m & 1) * 2 * kPHalf) + hw * 128 + r;
 #pragma unroll
-          for (int h = 0; h < 32; ++h) dst[h * kHeadDim] = __float2bfloat16_rn(__uint_as_float(o[h]) * sm.factor[hb + h]);
+          for (int h = 0; h < kHW; ++h) dst[h * 128] = __float2bfloat16_rn(__uint_as_float(o[h]) * sm.wmax[1][hw + h]);
+          fence_proxy_async_smem();
+          named_bar_sync(1, kSoftmaxThreads);
+          if (threadIdx.x == 0) tma_store_3d(&kp.out_map, m * 128, h0, t, p_addr + (m & 1) * 2 * kPHalf);
         }
       }
-      if (p.num_splits == 1) {
-        fence_proxy_async_smem();
-        named_bar_sync(1, kSoftmaxThreads);
-        if (r == 0) {
-          bulk_store(p.out + th * kHeadDim, k_addr, u.heads * kHeadDim * 2);
-          bulk_store_wait();
-        }
-      }
+      tc_fence_before();
     }
+    if (threadIdx.x == 0) bulk_store_wait();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) {
-    if (sm.abort_flag) {                          // products may still be in flight: their commit comes last
-      if (lane == 0) mma_commit(bar(sm.q_full));  // (phase 1 needs kSoftmaxWarps arrivals: one commit each)
-      if (lane == 0)
-        for (int k = 1; k < kSoftmaxWarps; ++k) mma_commit(bar(sm.q_full));
-      drain_wait(bar(sm.q_full), 1);
-    }
-    tmem_dealloc(tmem, kTmemCols);
-  }
+  if (warp == kScoreWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 // Merges the S normalised fp32 partials of every (token, head): weights
@@ -586,21 +705,29 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The pool as {128 bytes, 8 rows, 4 column blocks, row groups, pages}; box of
-// `chunk` rows.  The call's checks make the base 16-byte aligned, every stride a
-// multiple of 16 under 2^40 and page_size a multiple of 8.
-cudaError_t encode_cache_map(CUtensorMap* map, const CacheView& c, int chunk) {
-  static std::atomic<EncodeTiledFn> cached{nullptr};
+cudaError_t encode_fn(EncodeTiledFn* out) {
+  static std::atomic<EncodeTiledFn> cached{nullptr};   // looked up once; callers may be on several threads
   EncodeTiledFn fn = cached.load(std::memory_order_acquire);
   if (fn == nullptr) {
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult q;
-    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
     if (e != cudaSuccess) return e;
     if (q != cudaDriverEntryPointSuccess || ptr == nullptr) return cudaErrorNotSupported;
     fn = reinterpret_cast<EncodeTiledFn>(ptr);
     cached.store(fn, std::memory_order_release);
   }
+  *out = fn;
+  return cudaSuccess;
+}
+
+// The pool as {128 bytes, 8 rows, 4 column blocks, row groups, pages}; box of
+// `chunk` rows.  The call's checks make the base 16-byte aligned, every stride a
+// multiple of 16 under 2^40 and page_size a multiple of 8.
+cudaError_t encode_cache_map(CUtensorMap* map, const CacheView& c, int chunk) {
+  EncodeTiledFn fn = nullptr;
+  cudaError_t e = encode_fn(&fn);
+  if (e != cudaSuccess) return e;
   const cuuint64_t dims[5] = {128, 8, 4, (cuuint64_t)c.page_size / 8, (cuuint64_t)c.num_pages};
   const cuuint64_t strides[4] = {(cuuint64_t)c.row_stride, 128, (cuuint64_t)(8 * c.row_stride), (cuuint64_t)c.page_stride};
   const cuuint32_t box[5] = {128, 8, 4, (cuuint32_t)chunk / 8, 1};
@@ -611,19 +738,36 @@ cudaError_t encode_cache_map(CUtensorMap* map, const CacheView& c, int chunk) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// The output as [T, H, 512]; box of 128 dims x 64 heads of a token (heads past H are not written).
+cudaError_t encode_out_map(CUtensorMap* map, const WindowParams& p) {
+  EncodeTiledFn fn = nullptr;
+  cudaError_t e = encode_fn(&fn);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)p.H, (cuuint64_t)p.c.sum_q};
+  const cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)p.H * kHeadDim * 2};
+  const cuuint32_t box[3] = {128, (cuuint32_t)kNH, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.out, dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace
 
-cudaError_t launch_window_attention(const WindowParams& p, cudaStream_t stream) {
+cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t stream) {
   KernelParams kp;
   kp.p = p;
-  kp.chunk = p.c.page_size % 16 == 0 ? 16 : 8;
+  // a box is issued in some 250 cycles whatever its size: the largest that a page holds whole, up to a quarter tile
+  kp.chunk = p.c.page_size % 32 == 0 ? 32 : p.c.page_size % 16 == 0 ? 16 : 8;
   kp.groups = (p.H + kNH - 1) / kNH;
   cudaError_t e = encode_cache_map(&kp.map, p.c, kp.chunk);
+  if (e == cudaSuccess) e = encode_out_map(&kp.out_map, p);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(window_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  const int64_t grid = (int64_t)p.c.sum_q * kp.groups * p.num_splits;
-  window_kernel<<<(unsigned)grid, kThreads, kSmemBytes, stream>>>(kp);
+  kp.units = (int)((int64_t)p.c.sum_q * kp.groups * p.num_splits);
+  window_kernel<<<(unsigned)std::min(kp.units, sms), kThreads, kSmemBytes, stream>>>(kp);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.num_splits == 1) return e;
   // programmatic dependent launch: scheduled while the split kernel drains

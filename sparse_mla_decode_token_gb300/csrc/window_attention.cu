@@ -298,21 +298,24 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           const int e = entry + lane;
           pages = e < u.tiles * per_tile ? chunk_page(kp, u, u.tile0 * per_tile + e) : -1;
         }
-        const int b = n & 1, slot = lane - at0;
-        const bool here = slot >= 0 && slot < per_tile && pages >= 0;
+        const int b = n & 1;
+        const bool here = lane >= at0 && lane < at0 + per_tile && pages >= 0;
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, here)) * kp.chunk * kHeadDim;
-        const int row = chunk_at(u, u.tile0 * per_tile + entry + (here ? slot : 0)) * kp.chunk % p.c.page_size;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (n >= 2) ok = ok && warp_wait(cx, bar(sm.k_free[b][k]), ((n >> 1) - 1) & 1);
+        const int group = (uint32_t)(chunk_at(u, u.tile0 * per_tile + entry + (here ? lane - at0 : 0)) * kp.chunk) %
+                          (uint32_t)p.c.page_size / 8;
+        for (int k = 0; k < per_tile; ++k) {
+          if (n >= 2 && k % per_quarter == 0)
+            ok = ok && warp_wait(cx, bar(sm.k_free[b][k / per_quarter]), ((n >> 1) - 1) & 1);
           if (!ok) break;
-          if (k == 0 && lane == 0) mbar_arrive_expect_tx(bar(sm.k_full[b]), bytes);
+          const int page = __shfl_sync(0xffffffffu, pages, at0 + k), g = __shfl_sync(0xffffffffu, group, at0 + k);
+          if (elect_one()) {
+            if (k == 0) mbar_arrive_expect_tx(bar(sm.k_full[b]), bytes);
+            if (page >= 0)
+              tma_load_5d(k_addr + b * kTileBytes + k * chunk_groups * kGroupBytes, &kp.map, 0, 0, 0, g, page,
+                          bar(sm.k_full[b]));
+          }
           __syncwarp();
-          if (here && slot / per_quarter == k)
-            tma_load_5d(k_addr + b * kTileBytes + slot * chunk_groups * kGroupBytes, &kp.map, 0, 0, 0, row / 8, pages,
-                        bar(sm.k_full[b]));
         }
-        __syncwarp();
         if (!ok) break;
       }
     }
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         if (ok && n >= 2) ok = warp_wait(cx, bar(sm.s_empty[b]), ((n >> 1) - 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t tile = k_addr + b * kTileBytes;
 #pragma unroll
           for (int k = 0; k < 16; ++k)
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         __syncwarp();
       }
     }
-    if (lane == 0) mma_commit(bar(sm.drained[0]));
+    if (elect_one()) mma_commit(bar(sm.drained[0]));
     drain_wait(bar(sm.drained[0]), 0);
   } else if (warp == kOutWarp) {
     // ----------------------------------------------------- second products
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         ok = warp_wait(cx, bar(sm.p_full[b]), (n >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t tile = k_addr + b * kTileBytes, pb = p_addr + b * 2 * kPHalf;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         __syncwarp();
       }
     }
-    if (lane == 0) mma_commit(bar(sm.drained[1]));
+    if (elect_one()) mma_commit(bar(sm.drained[1]));
     drain_wait(bar(sm.drained[1]), 0);
   } else {
     // ------------------------------------------------------------- softmax
@@ -479,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           f2_unpack(d[e], v, w);
           top = fmaxf(top, fmaxf(v, w));
         }
-        if (i == 0 && threadIdx.x == 0) bulk_store_wait_read<0>();   // the last unit's output has left the P buffers
+        if (i == 0 && warp == 0 && elect_one()) bulk_store_wait_read<0>();   // the last unit's output has left the P buffers
         if (named_bar_or(1, kSoftmaxThreads, failed || fresh || (seen && top > 2.f * kHeadroom))) {
           // ---- a new reference: the heads' maxima over the tile
           if (named_bar_or(1, kSoftmaxThreads, failed)) break;
@@ -633,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         uint32_t o[kHW];
         tmem_ld32(lane_base + kOCol + m * kNH + hw, o);
         if (p.num_splits == 1 && m >= 2) {        // the staging buffer's last copy has been read
-          if (threadIdx.x == 0) bulk_store_wait_read<1>();
+          if (warp == 0 && elect_one()) bulk_store_wait_read<1>();
           named_bar_sync(1, kSoftmaxThreads);
         }
         tmem_wait_ld();
@@ -648,12 +651,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           for (int h = 0; h < kHW; ++h) dst[h * 128] = __float2bfloat16_rn(__uint_as_float(o[h]) * sm.wmax[1][hw + h]);
           fence_proxy_async_smem();
           named_bar_sync(1, kSoftmaxThreads);
-          if (threadIdx.x == 0) tma_store_3d(&kp.out_map, m * 128, h0, t, p_addr + (m & 1) * 2 * kPHalf);
+          if (warp == 0 && elect_one()) tma_store_3d(&kp.out_map, m * 128, h0, t, p_addr + (m & 1) * 2 * kPHalf);
         }
       }
       tc_fence_before();
     }
-    if (threadIdx.x == 0) bulk_store_wait();
+    if (warp == 0 && elect_one()) bulk_store_wait();
   }
   tc_fence_before();
   __syncthreads();

@@ -473,6 +473,23 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
+// 16 TMEM lanes x 16 columns as fragments: of each 8 columns, registers 0 and 1
+// hold lane T / 4, columns 2 (T % 4) and + 1, registers 2 and 3 lane T / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit elements to shared memory, transposed: lane
+// 8 i + k gives the address of column k of matrix i (16 bytes).
+__device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
 // True in one lane of the (converged) warp, the same one every time.  The
 // compiler knows that what it guards has one thread and issues the asynchronous
 // tensor instructions there without a loop over lanes: on a GB300 an MMA of 128

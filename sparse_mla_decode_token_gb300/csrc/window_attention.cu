@@ -58,9 +58,10 @@ using namespace tc;
 
 constexpr int kNH = kWindowHeads;                 // 64 heads
 constexpr int kRows = kWindowTile;                // 128 cache rows a tile
-constexpr int kSoftmaxWarps = 8;                  // two warpgroups: all 128 rows, 32 heads each
+constexpr int kSoftmaxWarps = 16;                 // four warpgroups: all 128 rows, 16 heads each
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
-constexpr int kHW = kNH / 2;                      // heads of a softmax thread
+constexpr int kHW = kNH / 4;                      // heads of a softmax thread
+static_assert(kHW == 16, "tmem_ld16, tmem_st16, tmem_ld_16x16");
 constexpr int kScoreWarp = kSoftmaxWarps;         // issues the first products; allocates and frees TMEM
 constexpr int kOutWarp = kSoftmaxWarps + 1;       // issues the second products
 constexpr int kLoadWarp = kSoftmaxWarps + 2;      // looks up the units and loads the rows
@@ -70,7 +71,8 @@ constexpr int kUnitReaders = kSoftmaxWarps + 3;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 0;                     // O^T: four blocks of 128 dims, 64 columns each
 constexpr uint32_t kSCol = 256;                   // S^T: two buffers of 64 hi + 64 lo columns
-constexpr float kHeadroom = 4.f;                  // log2: a logit may pass the reference by this
+constexpr float kHeadroom = 4.f;                  // log2 of P at the reference
+constexpr float kMaxLog2 = 8.75f;                 // a logit may go this high before the reference moves: P <= 431 < 448
 constexpr float kMinScaleLog2 = -64.f;
 constexpr int kTileBytes = kRows * kHeadDim;      // 64 KB
 constexpr int kGroupBytes = 8 * kHeadDim;         // 8 rows x four 128-byte column blocks
@@ -323,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     for (int i = max(0, n - 2); i < n + (ok ? 0 : 1); ++i) drain_wait(bar(sm.k_full[i & 1]), (i >> 1) & 1);
   } else if (warp == kScaleWarp) {
     // -------------------------------------------------- the rows' scales
+    // four rows a lane, looked up a tile before their buffer is free
     const int per_tile = kRows / kp.chunk;
     int n = 0;
     bool ok = true;
@@ -331,24 +334,38 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
       const Unit u = sm.unit[x & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sm.unit_empty[x & 1]));
-      for (int i = 0; ok && i < u.tiles; ++i, ++n) {
-        const int b = n & 1, first = (u.tile0 + i) * per_tile;
-        float s[kRows / 32];                      // four rows a lane
+      float next[kRows / 32];
+      // (every load is unconditional, at a clamped place: the four are in flight together)
+      auto look_up = [&](int i) {
+        constexpr int kY = kRows / 32;
+        int off[kY], page[kY];
+        bool seen[kY];
 #pragma unroll
-        for (int y = 0; y < kRows / 32; ++y) {
-          const int r = y * 32 + lane, k = first + r / kp.chunk;
-          s[y] = -1.f;
-          if (k < u.chunks) {
-            const int j = chunk_at(u, k) * kp.chunk + r % kp.chunk;
-            if (j <= u.pos && (j >= u.lo || j < p.first_tokens)) {
-              const int page = chunk_page(kp, u, k);
-              if (page >= 0)
-                s[y] = fabsf(__ldg(p.c.scales + (int64_t)page * p.c.scale_stride +
-                                   (uint32_t)j % (uint32_t)p.c.page_size / (uint32_t)p.c.block_rows));
-              else if (p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
-            }
-          }
+        for (int y = 0; y < kY; ++y) {
+          const int r = y * 32 + lane, k = (u.tile0 + i) * per_tile + r / kp.chunk;
+          const uint32_t j = (uint32_t)(chunk_at(u, min(k, u.chunks - 1)) * kp.chunk + r % kp.chunk);
+          seen[y] = k < u.chunks && (int)j <= u.pos && ((int)j >= u.lo || (int)j < p.first_tokens);
+          const uint32_t col = j / (uint32_t)p.c.page_size;
+          page[y] = __ldg(p.c.bt + u.b * p.c.bt_stride + col);
+          off[y] = (int)((j - col * (uint32_t)p.c.page_size) / (uint32_t)p.c.block_rows);
         }
+#pragma unroll
+        for (int y = 0; y < kY; ++y) {
+          const bool in = page[y] >= 0 && page[y] < p.c.num_pages;
+          if (seen[y] && !in && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
+          seen[y] = seen[y] && in;
+          next[y] = __ldg(p.c.scales + (int64_t)(in ? page[y] : 0) * p.c.scale_stride + off[y]);
+        }
+#pragma unroll
+        for (int y = 0; y < kY; ++y) next[y] = seen[y] ? fabsf(next[y]) : -1.f;
+      };
+      if (u.tiles > 0) look_up(0);
+      for (int i = 0; ok && i < u.tiles; ++i, ++n) {
+        const int b = n & 1;
+        float s[kRows / 32];
+#pragma unroll
+        for (int y = 0; y < kRows / 32; ++y) s[y] = next[y];
+        if (i + 1 < u.tiles) look_up(i + 1);
         // (the softmax has read this buffer's last scales before it gave its P)
         if (n >= 2) ok = warp_wait(cx, bar(sm.p_full[b]), ((n >> 1) - 1) & 1);
         if (!ok) break;
@@ -455,8 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         uint64_t d[kHW / 2];                      // t - reference + headroom
         {
           uint32_t hi[kHW], lo[kHW];
-          tmem_ld32(lane_base + kSCol + b * 128 + hw, hi);
-          tmem_ld32(lane_base + kSCol + b * 128 + kNH + hw, lo);
+          tmem_ld16(lane_base + kSCol + b * 128 + hw, hi);
+          tmem_ld16(lane_base + kSCol + b * 128 + kNH + hw, lo);
           tmem_wait_ld();
           const uint64_t s2 = f2_pack(s, s), ls2 = f2_pack(ls, ls);
 #pragma unroll
@@ -483,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           top = fmaxf(top, fmaxf(v, w));
         }
         if (i == 0 && warp == 0 && elect_one()) bulk_store_wait_read<0>();   // the last unit's output has left the P buffers
-        if (named_bar_or(1, kSoftmaxThreads, failed || fresh || (seen && top > 2.f * kHeadroom))) {
+        if (named_bar_or(1, kSoftmaxThreads, failed || fresh || (seen && top > kMaxLog2))) {
           // ---- a new reference: the heads' maxima over the tile
           if (named_bar_or(1, kSoftmaxThreads, failed)) break;
 #pragma unroll
@@ -514,11 +531,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 #pragma unroll 1
             for (int m = 0; m < 4; ++m) {
               uint32_t o[kHW];
-              tmem_ld32(lane_base + kOCol + m * kNH + hw, o);
+              tmem_ld16(lane_base + kOCol + m * kNH + hw, o);
               tmem_wait_ld();
 #pragma unroll
               for (int h = 0; h < kHW; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * sm.wmax[1][hw + h]);
-              tmem_st32(lane_base + kOCol + m * kNH + hw, o);
+              tmem_st16(lane_base + kOCol + m * kNH + hw, o);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -532,21 +549,20 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         // P in E4M3 pairs: row r of the MN-major operand is 64 bytes, heads along it
         uint8_t* pb = smem + kOffP + b * 2 * kPHalf + r * kNH;
         const uint64_t inv2 = f2_pack(inv, inv);
-#pragma unroll
-        for (int g = 0; g < kHW; g += 16) {
+        {
           uint32_t hi[8] = {}, lo[8] = {};
           if (seen) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               float v, w;
-              f2_unpack(d[g / 2 + e], v, w);
+              f2_unpack(d[e], v, w);
               v = fast_exp2(v);
               w = fast_exp2(w);
-              sum[g / 2 + e] = f2_fma(f2_pack(v, w), inv2, sum[g / 2 + e]);
+              sum[e] = f2_fma(f2_pack(v, w), inv2, sum[e]);
               split_pair(v, w, hi + e, lo + e);
             }
           }
-          const int at = (((hw + g) >> 4) ^ ((r >> 1) & 3)) << 4;             // 64-byte swizzle
+          const int at = ((hw >> 4) ^ ((r >> 1) & 3)) << 4;             // 64-byte swizzle
           *reinterpret_cast<uint4*>(pb + at) = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16,
                                                           hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
           *reinterpret_cast<uint4*>(pb + kPHalf + at) = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16,
@@ -554,9 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         }
         if (!seen) {
           // the first product has read the row (its commit is what s_full waited for); the second must find zeros
-          uint8_t* row = smem + kOffK + b * kTileBytes + (r >> 3) * kGroupBytes + (r & 7) * 128 + (hw / kHW) * 2048;
-          for (int cb = 0; cb < 2; ++cb)
-            for (int y = 0; y < 8; ++y) *reinterpret_cast<uint4*>(row + cb * 1024 + y * 16) = make_uint4(0, 0, 0, 0);
+          uint8_t* row = smem + kOffK + b * kTileBytes + (r >> 3) * kGroupBytes + (r & 7) * 128 + (hw / kHW) * 1024;
+          for (int y = 0; y < 8; ++y) *reinterpret_cast<uint4*>(row + y * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -592,24 +607,26 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         }
         continue;
       }
-      // sums over the rows: a reduction over lanes and warps, one head at a time per thread
-      float total = 0.f;
+      // sums over the rows: the warp's lanes halve the heads they hold at each
+      // step; lanes l and l + 16 end with head l's
+      float total;
+      {
+        float v[kHW];
 #pragma unroll
-      for (int e = 0; e < kHW / 2; ++e) {
-        float v, w;
-        f2_unpack(sum[e], v, w);
+        for (int e = 0; e < kHW / 2; ++e) f2_unpack(sum[e], v[2 * e], v[2 * e + 1]);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          v += __shfl_xor_sync(0xffffffffu, v, o);
-          w += __shfl_xor_sync(0xffffffffu, w, o);
-        }
-        if (lane == 2 * e) total = v;
-        if (lane == 2 * e + 1) total = w;
+        for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+          for (int h = 0; h < o; ++h) {
+            const float give = (lane & o) ? v[h] : v[h + o], keep = (lane & o) ? v[h + o] : v[h];
+            v[h] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+        total = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
       }
       failed |= !warp_wait(cx, bar(sm.k_free[(n - 1) & 1][3]), ((n - 1) >> 1) & 1);
       tc_fence_after();
       if (named_bar_or(1, kSoftmaxThreads, failed)) break;
-      sm.wmax[warp & 3][hw + lane] = total;
+      if (lane < kHW) sm.wmax[warp & 3][hw + lane] = total;
       named_bar_sync(1, kSoftmaxThreads);
       if (threadIdx.x < kNH) {
         const int h = threadIdx.x;
@@ -631,27 +648,54 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         }
       }
       named_bar_sync(1, kSoftmaxThreads);
+      if (p.num_splits > 1) {
 #pragma unroll 1
-      for (int m = 0; m < 4; ++m) {               // dims 128 m .. + 127, one a thread
-        uint32_t o[kHW];
-        tmem_ld32(lane_base + kOCol + m * kNH + hw, o);
-        if (p.num_splits == 1 && m >= 2) {        // the staging buffer's last copy has been read
-          if (warp == 0 && elect_one()) bulk_store_wait_read<1>();
-          named_bar_sync(1, kSoftmaxThreads);
-        }
-        tmem_wait_ld();
-        if (p.num_splits > 1) {
+        for (int m = 0; m < 4; ++m) {             // dims 128 m .. + 127, one a thread
+          uint32_t o[kHW];
+          tmem_ld16(lane_base + kOCol + m * kNH + hw, o);
+          tmem_wait_ld();
           float* dst = p.part_o + (part + hw) * kHeadDim + m * 128 + r;
 #pragma unroll
           for (int h = 0; h < kHW; ++h)
             if (hw + h < heads) dst[h * kHeadDim] = __uint_as_float(o[h]) * sm.wmax[1][hw + h];
-        } else {
-          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(smem + kOffP + (m & 1) * 2 * kPHalf) + hw * 128 + r;
+        }
+      } else {
+        // 8 x 8 fragments, transposed on their way into a P buffer: [64 heads][64 dims] BF16 twice, 128-byte
+        // swizzle, stored by TMA while the next 128 dims are read
+        float f[kHW / 4];                         // of this lane's heads: 8 j + 2 (lane % 4) and + 1
 #pragma unroll
-          for (int h = 0; h < kHW; ++h) dst[h * 128] = __float2bfloat16_rn(__uint_as_float(o[h]) * sm.wmax[1][hw + h]);
+        for (int j = 0; j < 2; ++j) {
+          f[2 * j] = sm.wmax[1][hw + 8 * j + 2 * (lane & 3)];
+          f[2 * j + 1] = sm.wmax[1][hw + 8 * j + 2 * (lane & 3) + 1];
+        }
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m) {
+          uint32_t o[2][8];
+          tmem_ld_16x16(lane_base + kOCol + m * kNH + hw, o[0]);
+          tmem_ld_16x16(lane_base + (16u << 16) + kOCol + m * kNH + hw, o[1]);
+          if (m >= 2) {                           // the buffer's last two stores have read it
+            if (warp == 0 && elect_one()) bulk_store_wait_read<2>();
+            named_bar_sync(1, kSoftmaxThreads);
+          }
+          tmem_wait_ld();
+          const uint32_t stage = p_addr + (m & 1) * 2 * kPHalf + ((warp & 3) >> 1) * (kNH * 128);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)           // dims 8 i .. + 7 of the warp's 32
+              v[i] = pack_bf16x2(__uint_as_float(o[i >> 1][4 * j + 2 * (i & 1)]) * f[2 * j],
+                                 __uint_as_float(o[i >> 1][4 * j + 2 * (i & 1) + 1]) * f[2 * j + 1]);
+            const int head = hw + 8 * j + (lane & 7), ch = (warp & 1) * 4 + (lane >> 3);
+            stmatrix4_trans(stage + head * 128 + ((ch ^ (head & 7)) << 4), v[0], v[1], v[2], v[3]);
+          }
           fence_proxy_async_smem();
           named_bar_sync(1, kSoftmaxThreads);
-          if (warp == 0 && elect_one()) tma_store_3d(&kp.out_map, m * 128, h0, t, p_addr + (m & 1) * 2 * kPHalf);
+          if (warp == 0 && elect_one()) {
+            const uint32_t from = p_addr + (m & 1) * 2 * kPHalf;
+            tma_store_3d(&kp.out_map, m * 128, h0, t, from);
+            tma_store_3d(&kp.out_map, m * 128 + 64, h0, t, from + kNH * 128);
+          }
         }
       }
       tc_fence_before();
@@ -741,17 +785,17 @@ cudaError_t encode_cache_map(CUtensorMap* map, const CacheView& c, int chunk) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// The output as [T, H, 512]; box of 128 dims x 64 heads of a token (heads past H are not written).
+// The output as [T, H, 512]; box of 64 dims x 64 heads of a token (heads past H are not written).
 cudaError_t encode_out_map(CUtensorMap* map, const WindowParams& p) {
   EncodeTiledFn fn = nullptr;
   cudaError_t e = encode_fn(&fn);
   if (e != cudaSuccess) return e;
   const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)p.H, (cuuint64_t)p.c.sum_q};
   const cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)p.H * kHeadDim * 2};
-  const cuuint32_t box[3] = {128, (cuuint32_t)kNH, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)kNH, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.out, dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

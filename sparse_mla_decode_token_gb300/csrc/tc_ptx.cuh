@@ -453,6 +453,13 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int 
       : "memory");
 }
 
+// Asks for a 5-D box to be brought into L2.
+__device__ __forceinline__ void tma_prefetch_5d(const void* tmap, int c0, int c1, int c2, int c3, int c4) {
+  asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];" ::"l"(tmap), "r"(c0),
+               "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+               : "memory");
+}
+
 // TMA tile store of a 3-D box from shared memory at src (what lies outside the
 // tensor is not written), and the wait until this thread's stores are done.
 __device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int z, uint32_t src) {

@@ -110,7 +110,7 @@ static_assert(kNH * 128 * 2 == 2 * kPHalf, "a P buffer stages 128 dims of the ou
 struct KernelParams {
   WindowParams p;
   CUtensorMap map, out_map;
-  int32_t chunk;                                  // rows of a TMA box: 32, 16 or 8
+  int32_t shift;                                  // log2 of a TMA box's rows: 5, 4 or 3
   int32_t groups;                                 // head groups
   int32_t units;
 };
@@ -157,12 +157,11 @@ __device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lan
   const int cap = c.max_pages * c.page_size, last = min(u.pos, cap - 1);
   if (u.pos >= cap && lane == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
   if (last >= 0) {
-    u.first_chunks = (min(p.first_tokens, last + 1) + kp.chunk - 1) / kp.chunk;
-    u.window_chunk = max(u.lo / kp.chunk, u.first_chunks);
-    u.chunks = u.first_chunks + max(0, last / kp.chunk - u.window_chunk + 1);
+    u.first_chunks = (min(p.first_tokens, last + 1) + (1 << kp.shift) - 1) >> kp.shift;
+    u.window_chunk = max(u.lo >> kp.shift, u.first_chunks);
+    u.chunks = u.first_chunks + max(0, (last >> kp.shift) - u.window_chunk + 1);
   }
-  const int per_tile = kRows / kp.chunk;
-  const int tiles = (u.chunks + per_tile - 1) / per_tile, per = (tiles + p.num_splits - 1) / p.num_splits;
+  const int tiles = (u.chunks + (kRows >> kp.shift) - 1) >> (7 - kp.shift), per = (tiles + p.num_splits - 1) / p.num_splits;
   u.tile0 = min(tiles, u.split * per);
   u.tiles = min(tiles, u.tile0 + per) - u.tile0;
   return u;
@@ -172,7 +171,7 @@ __device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lan
 __device__ __forceinline__ int chunk_page(const KernelParams& kp, const Unit& u, int k) {
   const CacheView& c = kp.p.c;
   if (k >= u.chunks) return -1;
-  const int page = __ldg(c.bt + u.b * c.bt_stride + (uint32_t)(chunk_at(u, k) * kp.chunk) / (uint32_t)c.page_size);
+  const int page = __ldg(c.bt + u.b * c.bt_stride + (uint32_t)(chunk_at(u, k) << kp.shift) / (uint32_t)c.page_size);
   return page >= 0 && page < c.num_pages ? page : -1;
 }
 
@@ -278,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
   const int mine = (kp.units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
 
   if (warp == kLoadWarp) {
-    // ---------------------------------------------- units, rows and scales
-    const int per_tile = kRows / kp.chunk, per_quarter = per_tile / 4, chunk_groups = kp.chunk / 8;
+    // ------------------------------------------------------ units and rows
+    const int per_tile = kRows >> kp.shift, quarter_shift = 5 - kp.shift;     // boxes of a tile; log2 of a quarter's
     int n = 0;
     bool ok = true;
     for (int x = 0; ok && x < mine; ++x) {
@@ -293,32 +292,35 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           bulk_prefetch_l2(p.q + (int64_t)u.t * p.q_stride_token + (int64_t)u.h0 * kHeadDim, u.heads * kHeadDim * 2);
       }
       __syncwarp();
-      int pages = -1;
-      for (int i = 0; ok && i < u.tiles; ++i, ++n) {
-        const int entry = i * per_tile, at0 = entry & 31;   // of this split's list; its place among 32 looked up at once
-        if (at0 == 0) {
-          const int e = entry + lane;
-          pages = e < u.tiles * per_tile ? chunk_page(kp, u, u.tile0 * per_tile + e) : -1;
-        }
+      // lane l looks up the box l places on from the tile's first
+      const int end = (u.tile0 + u.tiles) * per_tile;
+      int entry = u.tile0 * per_tile;
+      int page = entry + lane < end ? chunk_page(kp, u, entry + lane) : -1;
+      for (int i = 0; ok && i < u.tiles; ++i, ++n, entry += per_tile) {
         const int b = n & 1;
-        const bool here = lane >= at0 && lane < at0 + per_tile && pages >= 0;
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, here)) * kp.chunk * kHeadDim;
-        const int group = (uint32_t)(chunk_at(u, u.tile0 * per_tile + entry + (here ? lane - at0 : 0)) * kp.chunk) %
-                          (uint32_t)p.c.page_size / 8;
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, lane < per_tile && page >= 0)) * kHeadDim << kp.shift;
+        const int group = (uint32_t)(chunk_at(u, min(entry + lane, u.chunks - 1)) << kp.shift) % (uint32_t)p.c.page_size / 8;
         for (int k = 0; k < per_tile; ++k) {
-          if (n >= 2 && k % per_quarter == 0)
-            ok = ok && warp_wait(cx, bar(sm.k_free[b][k / per_quarter]), ((n >> 1) - 1) & 1);
+          const int pg = __shfl_sync(0xffffffffu, page, k), g = __shfl_sync(0xffffffffu, group, k);
+          if (n >= 2 && (k & ((1 << quarter_shift) - 1)) == 0)
+            ok = ok && warp_wait(cx, bar(sm.k_free[b][k >> quarter_shift]), ((n >> 1) - 1) & 1);
           if (!ok) break;
-          const int page = __shfl_sync(0xffffffffu, pages, at0 + k), g = __shfl_sync(0xffffffffu, group, at0 + k);
           if (elect_one()) {
             if (k == 0) mbar_arrive_expect_tx(bar(sm.k_full[b]), bytes);
-            if (page >= 0)
-              tma_load_5d(k_addr + b * kTileBytes + k * chunk_groups * kGroupBytes, &kp.map, 0, 0, 0, g, page,
-                          bar(sm.k_full[b]));
+            if (pg >= 0)
+              tma_load_5d(k_addr + b * kTileBytes + k * (kHeadDim << kp.shift), &kp.map, 0, 0, 0, g, pg, bar(sm.k_full[b]));
           }
           __syncwarp();
         }
         if (!ok) break;
+        // the next tile but one on its way to L2: DRAM's latency would otherwise
+        // stand between a tile's last product and the next one in its buffer
+        for (int k = i == 0 ? per_tile : 2 * per_tile; k < 3 * per_tile && k < 32; ++k) {
+          const int pg = __shfl_sync(0xffffffffu, page, k), g = __shfl_sync(0xffffffffu, group, k);
+          if (pg >= 0 && elect_one()) tma_prefetch_5d(&kp.map, 0, 0, 0, g, pg);
+          __syncwarp();
+        }
+        page = entry + per_tile + lane < end ? chunk_page(kp, u, entry + per_tile + lane) : -1;
       }
     }
     // after an abort the last copies may still be in flight
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
   } else if (warp == kScaleWarp) {
     // -------------------------------------------------- the rows' scales
     // four rows a lane, looked up a tile before their buffer is free
-    const int per_tile = kRows / kp.chunk;
+    const int per_tile = kRows >> kp.shift;
     int n = 0;
     bool ok = true;
     for (int x = 0; ok && x < mine; ++x) {
@@ -342,8 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         bool seen[kY];
 #pragma unroll
         for (int y = 0; y < kY; ++y) {
-          const int r = y * 32 + lane, k = (u.tile0 + i) * per_tile + r / kp.chunk;
-          const uint32_t j = (uint32_t)(chunk_at(u, min(k, u.chunks - 1)) * kp.chunk + r % kp.chunk);
+          const int r = y * 32 + lane, k = (u.tile0 + i) * per_tile + (r >> kp.shift);
+          const uint32_t j = (uint32_t)((chunk_at(u, min(k, u.chunks - 1)) << kp.shift) + (r & ((1 << kp.shift) - 1)));
           seen[y] = k < u.chunks && (int)j <= u.pos && ((int)j >= u.lo || (int)j < p.first_tokens);
           const uint32_t col = j / (uint32_t)p.c.page_size;
           page[y] = __ldg(p.c.bt + u.b * p.c.bt_stride + col);
@@ -806,9 +808,9 @@ cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t
   KernelParams kp;
   kp.p = p;
   // a box is issued in some 250 cycles whatever its size: the largest that a page holds whole, up to a quarter tile
-  kp.chunk = p.c.page_size % 32 == 0 ? 32 : p.c.page_size % 16 == 0 ? 16 : 8;
+  kp.shift = p.c.page_size % 32 == 0 ? 5 : p.c.page_size % 16 == 0 ? 4 : 3;
   kp.groups = (p.H + kNH - 1) / kNH;
-  cudaError_t e = encode_cache_map(&kp.map, p.c, kp.chunk);
+  cudaError_t e = encode_cache_map(&kp.map, p.c, 1 << kp.shift);
   if (e == cudaSuccess) e = encode_out_map(&kp.out_map, p);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(window_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);

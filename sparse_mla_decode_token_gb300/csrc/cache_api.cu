@@ -160,7 +160,7 @@ int head_groups(const smla_window_args* a) { return (a->num_heads + kWindowHeads
 int window_splits(const smla_window_args* a, int sms) {
   if (a->num_splits > 0) return a->num_splits;
   const int64_t rows = std::min((int64_t)a->cache.max_pages * a->cache.page_size,
-                                (int64_t)a->window + a->first_tokens + 96);   // chunks may start and end outside
+                                (int64_t)a->window + a->first_tokens + 192);   // chunks may start and end outside
   const int64_t tiles = (rows + kWindowTile - 1) / kWindowTile;
   const int64_t units = std::max<int64_t>(1, (int64_t)a->sum_q * head_groups(a));
   return (int)std::max<int64_t>(1, std::min<int64_t>({sms / units, tiles, SMLA_MAX_SPLITS}));

@@ -110,7 +110,6 @@ static_assert(kNH * 128 * 2 == 2 * kPHalf, "a P buffer stages 128 dims of the ou
 struct KernelParams {
   WindowParams p;
   CUtensorMap map, out_map;
-  int32_t shift;                                  // log2 of a TMA box's rows: 5, 4 or 3
   int32_t groups;                                 // head groups
   int32_t units;
 };
@@ -120,6 +119,7 @@ __device__ __forceinline__ int chunk_at(const Unit& u, int k) {
 }
 
 // Unit x (whole warp; the same result in every lane).
+template <int kShift>
 __device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lane) {
   const WindowParams& p = kp.p;
   const CacheView& c = p.c;
@@ -157,21 +157,22 @@ __device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lan
   const int cap = c.max_pages * c.page_size, last = min(u.pos, cap - 1);
   if (u.pos >= cap && lane == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
   if (last >= 0) {
-    u.first_chunks = (min(p.first_tokens, last + 1) + (1 << kp.shift) - 1) >> kp.shift;
-    u.window_chunk = max(u.lo >> kp.shift, u.first_chunks);
-    u.chunks = u.first_chunks + max(0, (last >> kp.shift) - u.window_chunk + 1);
+    u.first_chunks = (min(p.first_tokens, last + 1) + (1 << kShift) - 1) >> kShift;
+    u.window_chunk = max(u.lo >> kShift, u.first_chunks);
+    u.chunks = u.first_chunks + max(0, (last >> kShift) - u.window_chunk + 1);
   }
-  const int tiles = (u.chunks + (kRows >> kp.shift) - 1) >> (7 - kp.shift), per = (tiles + p.num_splits - 1) / p.num_splits;
+  const int tiles = (u.chunks + (kRows >> kShift) - 1) >> (7 - kShift), per = (tiles + p.num_splits - 1) / p.num_splits;
   u.tile0 = min(tiles, u.split * per);
   u.tiles = min(tiles, u.tile0 + per) - u.tile0;
   return u;
 }
 
 // Page of list entry k, or -1 (past the list, or no page of the pool).
+template <int kShift>
 __device__ __forceinline__ int chunk_page(const KernelParams& kp, const Unit& u, int k) {
   const CacheView& c = kp.p.c;
   if (k >= u.chunks) return -1;
-  const int page = __ldg(c.bt + u.b * c.bt_stride + (uint32_t)(chunk_at(u, k) << kp.shift) / (uint32_t)c.page_size);
+  const int page = __ldg(c.bt + u.b * c.bt_stride + (uint32_t)(chunk_at(u, k) << kShift) / (uint32_t)c.page_size);
   return page >= 0 && page < c.num_pages ? page : -1;
 }
 
@@ -236,6 +237,7 @@ __device__ __forceinline__ void split_query(const KernelParams& kp, const Unit& 
   }
 }
 
+template <int kShift>                             // log2 of a TMA box's rows
 __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_constant__ KernelParams kp) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Small& sm = *reinterpret_cast<Small*>(smem + kOffSmall);
@@ -278,11 +280,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------------ units and rows
-    const int per_tile = kRows >> kp.shift, quarter_shift = 5 - kp.shift;     // boxes of a tile; log2 of a quarter's
+    constexpr int kBoxes = kRows >> kShift;       // of a tile
     int n = 0;
     bool ok = true;
     for (int x = 0; ok && x < mine; ++x) {
-      const Unit u = make_unit(kp, blockIdx.x + x * gridDim.x, lane);
+      const Unit u = make_unit<kShift>(kp, blockIdx.x + x * gridDim.x, lane);
       if (x >= 2) ok = warp_wait(cx, bar(sm.unit_empty[x & 1]), ((x >> 1) - 1) & 1);
       if (!ok) break;
       if (lane == 0) {
@@ -292,35 +294,40 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           bulk_prefetch_l2(p.q + (int64_t)u.t * p.q_stride_token + (int64_t)u.h0 * kHeadDim, u.heads * kHeadDim * 2);
       }
       __syncwarp();
-      // lane l looks up the box l places on from the tile's first
-      const int end = (u.tile0 + u.tiles) * per_tile;
-      int entry = u.tile0 * per_tile;
-      int page = entry + lane < end ? chunk_page(kp, u, entry + lane) : -1;
-      for (int i = 0; ok && i < u.tiles; ++i, ++n, entry += per_tile) {
+      // Lane l looks up box l of the tile; one lane then holds all of them, so
+      // that nothing but the wait and the copy stands between a quarter of the
+      // buffer and its rows.
+      auto look_up = [&](int i, int* page, int* group) {
+        const int k = (u.tile0 + i) * kBoxes + lane;
+        *page = lane < kBoxes && i < u.tiles ? chunk_page<kShift>(kp, u, k) : -1;
+        *group = (uint32_t)(chunk_at(u, min(k, u.chunks - 1)) << kShift) % (uint32_t)p.c.page_size / 8;
+      };
+      int page = -1, group = 0;
+      if (u.tiles > 0) look_up(0, &page, &group);
+      for (int i = 0; ok && i < u.tiles; ++i, ++n) {
         const int b = n & 1;
-        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, lane < per_tile && page >= 0)) * kHeadDim << kp.shift;
-        const int group = (uint32_t)(chunk_at(u, min(entry + lane, u.chunks - 1)) << kp.shift) % (uint32_t)p.c.page_size / 8;
-        for (int k = 0; k < per_tile; ++k) {
-          const int pg = __shfl_sync(0xffffffffu, page, k), g = __shfl_sync(0xffffffffu, group, k);
-          if (n >= 2 && (k & ((1 << quarter_shift) - 1)) == 0)
-            ok = ok && warp_wait(cx, bar(sm.k_free[b][k >> quarter_shift]), ((n >> 1) - 1) & 1);
-          if (!ok) break;
-          if (elect_one()) {
-            if (k == 0) mbar_arrive_expect_tx(bar(sm.k_full[b]), bytes);
-            if (pg >= 0)
-              tma_load_5d(k_addr + b * kTileBytes + k * (kHeadDim << kp.shift), &kp.map, 0, 0, 0, g, pg, bar(sm.k_full[b]));
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, page >= 0)) * kHeadDim << kShift;
+        int pg[kBoxes], g[kBoxes];
+#pragma unroll
+        for (int k = 0; k < kBoxes; ++k) {
+          pg[k] = __shfl_sync(0xffffffffu, page, k);
+          g[k] = __shfl_sync(0xffffffffu, group, k);
+        }
+        look_up(i + 1, &page, &group);
+        bool good = true;
+        if (elect_one()) {
+          const uint32_t full = bar(sm.k_full[b]), dst = k_addr + b * kTileBytes;
+#pragma unroll
+          for (int k = 0; k < kBoxes; ++k) {
+            constexpr int kPerQuarter = kBoxes / 4;
+            if (k % kPerQuarter == 0 && n >= 2)
+              good = good && wait_bar(cx, bar(sm.k_free[b][k / kPerQuarter]), ((n >> 1) - 1) & 1, false);
+            if (!good) break;
+            if (k == 0) mbar_arrive_expect_tx(full, bytes);
+            if (pg[k] >= 0) tma_load_5d(dst + k * (kHeadDim << kShift), &kp.map, 0, 0, 0, g[k], pg[k], full);
           }
-          __syncwarp();
         }
-        if (!ok) break;
-        // the next tile but one on its way to L2: DRAM's latency would otherwise
-        // stand between a tile's last product and the next one in its buffer
-        for (int k = i == 0 ? per_tile : 2 * per_tile; k < 3 * per_tile && k < 32; ++k) {
-          const int pg = __shfl_sync(0xffffffffu, page, k), g = __shfl_sync(0xffffffffu, group, k);
-          if (pg >= 0 && elect_one()) tma_prefetch_5d(&kp.map, 0, 0, 0, g, pg);
-          __syncwarp();
-        }
-        page = entry + per_tile + lane < end ? chunk_page(kp, u, entry + per_tile + lane) : -1;
+        ok = __all_sync(0xffffffffu, good);
       }
     }
     // after an abort the last copies may still be in flight
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
   } else if (warp == kScaleWarp) {
     // -------------------------------------------------- the rows' scales
     // four rows a lane, looked up a tile before their buffer is free
-    const int per_tile = kRows >> kp.shift;
+    constexpr int per_tile = kRows >> kShift;
     int n = 0;
     bool ok = true;
     for (int x = 0; ok && x < mine; ++x) {
@@ -344,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         bool seen[kY];
 #pragma unroll
         for (int y = 0; y < kY; ++y) {
-          const int r = y * 32 + lane, k = (u.tile0 + i) * per_tile + (r >> kp.shift);
-          const uint32_t j = (uint32_t)((chunk_at(u, min(k, u.chunks - 1)) << kp.shift) + (r & ((1 << kp.shift) - 1)));
+          const int r = y * 32 + lane, k = (u.tile0 + i) * per_tile + (r >> kShift);
+          const uint32_t j = (uint32_t)((chunk_at(u, min(k, u.chunks - 1)) << kShift) + (r & ((1 << kShift) - 1)));
           seen[y] = k < u.chunks && (int)j <= u.pos && ((int)j >= u.lo || (int)j < p.first_tokens);
           const uint32_t col = j / (uint32_t)p.c.page_size;
           page[y] = __ldg(p.c.bt + u.b * p.c.bt_stride + col);
@@ -361,13 +368,32 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 #pragma unroll
         for (int y = 0; y < kY; ++y) next[y] = seen[y] ? fabsf(next[y]) : -1.f;
       };
-      if (u.tiles > 0) look_up(0);
+      // A tile on its way to L2 long before it is loaded: DRAM's latency would
+      // otherwise stand between a tile's last product and the next one in its buffer.
+      auto prefetch = [&](int i) {
+        const int k = (u.tile0 + i) * per_tile + lane;
+        const int page = lane < per_tile && i < u.tiles ? chunk_page<kShift>(kp, u, k) : -1;
+        const int group = (uint32_t)(chunk_at(u, min(k, u.chunks - 1)) << kShift) % (uint32_t)p.c.page_size / 8;
+#pragma unroll
+        for (int y = 0; y < per_tile; ++y) {
+          const int pg = __shfl_sync(0xffffffffu, page, y), g = __shfl_sync(0xffffffffu, group, y);
+          if (pg >= 0 && elect_one()) tma_prefetch_5d(&kp.map, 0, 0, 0, g, pg);
+          __syncwarp();
+        }
+      };
+      if (u.tiles > 0) {
+        look_up(0);
+        prefetch(2);
+      }
       for (int i = 0; ok && i < u.tiles; ++i, ++n) {
         const int b = n & 1;
         float s[kRows / 32];
 #pragma unroll
         for (int y = 0; y < kRows / 32; ++y) s[y] = next[y];
-        if (i + 1 < u.tiles) look_up(i + 1);
+        if (i + 1 < u.tiles) {
+          look_up(i + 1);
+          prefetch(i + 3);
+        }
         // (the softmax has read this buffer's last scales before it gave its P)
         if (n >= 2) ok = warp_wait(cx, bar(sm.p_full[b]), ((n >> 1) - 1) & 1);
         if (!ok) break;
@@ -807,17 +833,20 @@ cudaError_t encode_out_map(CUtensorMap* map, const WindowParams& p) {
 cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t stream) {
   KernelParams kp;
   kp.p = p;
-  // a box is issued in some 250 cycles whatever its size: the largest that a page holds whole, up to a quarter tile
-  kp.shift = p.c.page_size % 32 == 0 ? 5 : p.c.page_size % 16 == 0 ? 4 : 3;
   kp.groups = (p.H + kNH - 1) / kNH;
-  cudaError_t e = encode_cache_map(&kp.map, p.c, 1 << kp.shift);
+  kp.units = (int)((int64_t)p.c.sum_q * kp.groups * p.num_splits);
+  // the highest box that pages hold whole, up to a quarter of a tile: fewer copies to issue
+  const int shift = p.c.page_size % 32 == 0 ? 5 : p.c.page_size % 16 == 0 ? 4 : 3;
+  cudaError_t e = encode_cache_map(&kp.map, p.c, 1 << shift);
   if (e == cudaSuccess) e = encode_out_map(&kp.out_map, p);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(window_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return e;
-  kp.units = (int)((int64_t)p.c.sum_q * kp.groups * p.num_splits);
-  window_kernel<<<(unsigned)std::min(kp.units, sms), kThreads, kSmemBytes, stream>>>(kp);
-  e = cudaGetLastError();
+  auto launch = [&](auto kernel) -> cudaError_t {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (err != cudaSuccess) return err;
+    kernel<<<(unsigned)std::min(kp.units, sms), kThreads, kSmemBytes, stream>>>(kp);
+    return cudaGetLastError();
+  };
+  e = shift == 5 ? launch(window_kernel<5>) : shift == 4 ? launch(window_kernel<4>) : launch(window_kernel<3>);
   if (e != cudaSuccess || p.num_splits == 1) return e;
   // programmatic dependent launch: scheduled while the split kernel drains
   cudaLaunchConfig_t cfg = {};

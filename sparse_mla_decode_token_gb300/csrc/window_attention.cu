@@ -187,53 +187,46 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t* hi, uint3
 }
 
 // Q of 64 heads as E4M3 pairs: rows 0-63 hi, 64-127 lo, K-major with 128-byte
-// swizzle, column blocks of 128 dims.  One warp per head at a time.
+// swizzle, column blocks of 128 dims.  A warp takes four heads, a lane 16 dims
+// of each.
 __device__ __forceinline__ void split_query(const KernelParams& kp, const Unit& u, uint8_t* sq, Small& sm, int warp,
                                             int lane) {
   const WindowParams& p = kp.p;
-  const __nv_bfloat16* q = p.q + (int64_t)u.t * p.q_stride_token + (int64_t)u.h0 * kHeadDim;
+  constexpr int kHeads = kNH / kSoftmaxWarps;
+  const int h = warp * kHeads;
+  const __nv_bfloat16* q = p.q + (int64_t)u.t * p.q_stride_token + (int64_t)(u.h0 + h) * kHeadDim + lane * 16;
+  uint4 v[kHeads][2];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      v[i][k] = h + i < u.heads ? __ldg(reinterpret_cast<const uint4*>(q + i * kHeadDim) + k) : make_uint4(0, 0, 0, 0);
   const float scale = load_scale(p.bmm1, p.bmm1_dev) * kLog2e;
-  constexpr int kBatch = 4;
-  for (int h = warp * (kNH / kSoftmaxWarps); h < (warp + 1) * (kNH / kSoftmaxWarps); h += kBatch) {
-    uint4 v[kBatch][2];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
+  for (int i = 0; i < kHeads; ++i) {
+    const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+    uint32_t m2 = 0;                              // largest magnitudes as BF16 bits, even and odd dims
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        v[i][k] = h + i < u.heads ? __ldg(reinterpret_cast<const uint4*>(q + (h + i) * kHeadDim) + k * 32 + lane)
-                                  : make_uint4(0, 0, 0, 0);
+    for (int e = 0; e < 8; ++e) m2 = __vmaxu2(m2, w[e] & 0x7fff7fffu);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+    // 2^k that takes the largest element into [128, 256); BF16 exponent field e: magnitude in [2^(e-127), 2^(e-126))
+    const int e = min(max((int)(m >> 7), 8), 254);
+    const int k = 134 - e;
+    const float up = __uint_as_float((uint32_t)(k + 127) << 23), down = __uint_as_float((uint32_t)(127 - k) << 23);
+    if (lane == 0) sm.qscale[h + i] = scale * down;
+    uint32_t hi[8], lo[8];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      uint32_t m = 0;                             // largest magnitude as BF16 bits
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t w[4] = {v[i][k].x, v[i][k].y, v[i][k].z, v[i][k].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-      }
-      m = __reduce_max_sync(0xffffffffu, m);
-      const bool finite = m < 0x7f80u;
-      // 2^k that takes the largest element into [128, 256); BF16 exponent field e: magnitude in [2^(e-127), 2^(e-126))
-      const int e = min(max((int)(m >> 7), 8), 254);
-      const int k2 = 134 - e;
-      const float up = __uint_as_float((uint32_t)(k2 + 127) << 23), down = __uint_as_float((uint32_t)(127 - k2) << 23);
-      if (lane == 0) sm.qscale[h + i] = scale * down;
-      const int r = h + i;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t w[4] = {v[i][k].x, v[i][k].y, v[i][k].z, v[i][k].w};
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          split_pair(__uint_as_float(w[x] << 16) * up, __uint_as_float(w[x] & 0xffff0000u) * up, hi + x, lo + x);
-          if (!finite) hi[x] = 0x7f7fu, lo[x] = 0u;   // a head with an infinity or NaN gets NaN everywhere
-        }
-        const int idx = k * 32 + lane, block = idx >> 4, ch = (idx & 15) >> 1, half = (idx & 1) * 8;
-        uint8_t* at = sq + block * kQBlock + half;
-        *reinterpret_cast<uint2*>(at + sw128_offset(r, ch)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-        *reinterpret_cast<uint2*>(at + sw128_offset(r + kNH, ch)) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-      }
+    for (int x = 0; x < 8; ++x)
+      split_pair(__uint_as_float(w[x] << 16) * up, __uint_as_float(w[x] & 0xffff0000u) * up, hi + x, lo + x);
+    uint4 h16 = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
+    uint4 l16 = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+    if (m >= 0x7f80u) {                           // a head with an infinity or NaN gets NaN everywhere
+      h16 = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+      l16 = make_uint4(0, 0, 0, 0);
     }
+    uint8_t* at = sq + (lane >> 3) * kQBlock;     // column block; 16-byte chunk lane % 8 of it
+    *reinterpret_cast<uint4*>(at + sw128_offset(h + i, lane & 7)) = h16;
+    *reinterpret_cast<uint4*>(at + sw128_offset(h + i + kNH, lane & 7)) = l16;
   }
 }
 
@@ -599,7 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         if (!seen) {
           // the first product has read the row (its commit is what s_full waited for); the second must find zeros
           uint8_t* row = smem + kOffK + b * kTileBytes + (r >> 3) * kGroupBytes + (r & 7) * 128 + (hw / kHW) * 1024;
-          for (int y = 0; y < 8; ++y) *reinterpret_cast<uint4*>(row + y * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) *reinterpret_cast<uint4*>(row + ((y ^ (r & 7)) << 4)) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -609,6 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 
       // the next unit's queries, while the last products of this one run (their
       // buffer is free: the last S of this unit has been read)
+      float sink = -INFINITY;                     // of head threadIdx.x, in log2 units
+      if (p.sinks != nullptr && p.num_splits == 1 && threadIdx.x < sm.unit[x & 1].heads)
+        sink = __ldg(p.sinks + sm.unit[x & 1].h0 + threadIdx.x) * kLog2e;
+      const float out_scale = p.num_splits == 1 ? load_scale(p.bmm2, p.bmm2_dev) : 1.f;
       const int t = sm.unit[x & 1].t, h0 = sm.unit[x & 1].h0, heads = sm.unit[x & 1].heads, split = sm.unit[x & 1].split;
       if (x + 1 < mine) {
         failed |= !warp_wait(cx, bar(sm.unit_full[(x + 1) & 1]), ((x + 1) >> 1) & 1);
@@ -662,11 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         float f = 0.f, lse = -INFINITY;
         if (!(total == 0.f)) {                    // NaN passes
           lse = fast_log2(total) - sm.negref[h];
-          f = 1.f / total;
-          if (p.num_splits == 1) {
-            f *= load_scale(p.bmm2, p.bmm2_dev);
-            if (p.sinks != nullptr && h < heads) f *= 1.f / (1.f + fast_exp2(__ldg(p.sinks + h0 + h) * kLog2e - lse));
-          }
+          f = out_scale / (total + total * fast_exp2(sink - lse));
         }
         sm.wmax[1][h] = f;
         sm.negref[h] = 0.f;                       // the next unit's
@@ -697,33 +691,34 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           f[2 * j + 1] = sm.wmax[1][hw + 8 * j + 2 * (lane & 3) + 1];
         }
 #pragma unroll 1
-        for (int m = 0; m < 4; ++m) {
-          uint32_t o[2][8];
-          tmem_ld_16x16(lane_base + kOCol + m * kNH + hw, o[0]);
-          tmem_ld_16x16(lane_base + (16u << 16) + kOCol + m * kNH + hw, o[1]);
-          if (m >= 2) {                           // the buffer's last two stores have read it
-            if (warp == 0 && elect_one()) bulk_store_wait_read<2>();
+        for (int m = 0; m < 4; m += 2) {
+          if (m > 0) {                            // the buffers' first stores have read them
+            if (warp == 0 && elect_one()) bulk_store_wait_read<0>();
             named_bar_sync(1, kSoftmaxThreads);
           }
-          tmem_wait_ld();
-          const uint32_t stage = p_addr + (m & 1) * 2 * kPHalf + ((warp & 3) >> 1) * (kNH * 128);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t v[4];
+          for (int k = 0; k < 2; ++k) {
+            uint32_t o[2][8];
+            tmem_ld_16x16(lane_base + kOCol + (m + k) * kNH + hw, o[0]);
+            tmem_ld_16x16(lane_base + (16u << 16) + kOCol + (m + k) * kNH + hw, o[1]);
+            tmem_wait_ld();
+            const uint32_t stage = p_addr + k * 2 * kPHalf + ((warp & 3) >> 1) * (kNH * 128);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)           // dims 8 i .. + 7 of the warp's 32
-              v[i] = pack_bf16x2(__uint_as_float(o[i >> 1][4 * j + 2 * (i & 1)]) * f[2 * j],
-                                 __uint_as_float(o[i >> 1][4 * j + 2 * (i & 1) + 1]) * f[2 * j + 1]);
-            const int head = hw + 8 * j + (lane & 7), ch = (warp & 1) * 4 + (lane >> 3);
-            stmatrix4_trans(stage + head * 128 + ((ch ^ (head & 7)) << 4), v[0], v[1], v[2], v[3]);
+            for (int j = 0; j < 2; ++j) {
+              uint32_t v[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)         // dims 8 i .. + 7 of the warp's 32
+                v[i] = pack_bf16x2(__uint_as_float(o[i >> 1][4 * j + 2 * (i & 1)]) * f[2 * j],
+                                   __uint_as_float(o[i >> 1][4 * j + 2 * (i & 1) + 1]) * f[2 * j + 1]);
+              const int head = hw + 8 * j + (lane & 7), ch = (warp & 1) * 4 + (lane >> 3);
+              stmatrix4_trans(stage + head * 128 + ((ch ^ (head & 7)) << 4), v[0], v[1], v[2], v[3]);
+            }
           }
           fence_proxy_async_smem();
           named_bar_sync(1, kSoftmaxThreads);
-          if (warp == 0 && elect_one()) {
-            const uint32_t from = p_addr + (m & 1) * 2 * kPHalf;
-            tma_store_3d(&kp.out_map, m * 128, h0, t, from);
-            tma_store_3d(&kp.out_map, m * 128 + 64, h0, t, from + kNH * 128);
-          }
+          if (warp == 0 && elect_one())
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tma_store_3d(&kp.out_map, m * 128 + k * 64, h0, t, p_addr + k * (kNH * 128));
         }
       }
       tc_fence_before();

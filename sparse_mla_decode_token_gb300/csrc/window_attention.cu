@@ -195,16 +195,23 @@ __device__ __forceinline__ void split_query(const KernelParams& kp, const Unit& 
   constexpr int kHeads = kNH / kSoftmaxWarps;
   const int h = warp * kHeads;
   const __nv_bfloat16* q = p.q + (int64_t)u.t * p.q_stride_token + (int64_t)(u.h0 + h) * kHeadDim + lane * 16;
-  uint4 v[kHeads][2];
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i)
+  const float scale = load_scale(p.bmm1, p.bmm1_dev) * kLog2e;
+  auto load = [&](int i, uint4* v) {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      v[i][k] = h + i < u.heads ? __ldg(reinterpret_cast<const uint4*>(q + i * kHeadDim) + k) : make_uint4(0, 0, 0, 0);
-  const float scale = load_scale(p.bmm1, p.bmm1_dev) * kLog2e;
-#pragma unroll
+      v[k] = h + i < u.heads ? __ldg(reinterpret_cast<const uint4*>(q + i * kHeadDim) + k) : make_uint4(0, 0, 0, 0);
+  };
+  uint4 next[2][2];                               // two heads ahead
+  load(0, next[0]);
+  load(1, next[1]);
+  // (a loop, not unrolled: this runs once a unit, and what it costs is its instructions' way to the SM)
+#pragma unroll 1
   for (int i = 0; i < kHeads; ++i) {
-    const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+    const uint32_t w[8] = {next[0][0].x, next[0][0].y, next[0][0].z, next[0][0].w,
+                           next[0][1].x, next[0][1].y, next[0][1].z, next[0][1].w};
+    next[0][0] = next[1][0];
+    next[0][1] = next[1][1];
+    if (i + 2 < kHeads) load(i + 2, next[1]);
     uint32_t m2 = 0;                              // largest magnitudes as BF16 bits, even and odd dims
 #pragma unroll
     for (int e = 0; e < 8; ++e) m2 = __vmaxu2(m2, w[e] & 0x7fff7fffu);
@@ -276,17 +283,29 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     constexpr int kBoxes = kRows >> kShift;       // of a tile
     int n = 0;
     bool ok = true;
+    Unit ahead = make_unit<kShift>(kp, blockIdx.x, lane);
+    auto prefetch_query = [&](const Unit& u) {
+      if (u.tiles > 0 && elect_one())
+        bulk_prefetch_l2(p.q + (int64_t)u.t * p.q_stride_token + (int64_t)u.h0 * kHeadDim, u.heads * kHeadDim * 2);
+      __syncwarp();
+    };
+    prefetch_query(ahead);
     for (int x = 0; ok && x < mine; ++x) {
-      const Unit u = make_unit<kShift>(kp, blockIdx.x + x * gridDim.x, lane);
+      const Unit u = ahead;
       if (x >= 2) ok = warp_wait(cx, bar(sm.unit_empty[x & 1]), ((x >> 1) - 1) & 1);
       if (!ok) break;
       if (lane == 0) {
         sm.unit[x & 1] = u;
         mbar_arrive(bar(sm.unit_full[x & 1]));
-        if (u.tiles > 0)
-          bulk_prefetch_l2(p.q + (int64_t)u.t * p.q_stride_token + (int64_t)u.h0 * kHeadDim, u.heads * kHeadDim * 2);
       }
       __syncwarp();
+      auto look_ahead = [&] {                     // the next unit and its queries' way to L2
+        if (x + 1 < mine) {
+          ahead = make_unit<kShift>(kp, blockIdx.x + (x + 1) * gridDim.x, lane);
+          prefetch_query(ahead);
+        }
+      };
+      if (u.tiles < 2) look_ahead();
       // Lane l looks up box l of the tile; one lane then holds all of them, so
       // that nothing but the wait and the copy stands between a quarter of the
       // buffer and its rows.
@@ -321,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           }
         }
         ok = __all_sync(0xffffffffu, good);
+        if (i == 1) look_ahead();
       }
     }
     // after an abort the last copies may still be in flight

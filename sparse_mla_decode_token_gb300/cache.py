@@ -86,22 +86,43 @@ def new_moves(capacity: int, device) -> PageMoves:
                      torch.zeros(1, dtype=torch.int32, device=device))
 
 
+# A decode step makes these calls once a layer, so their checks are written as
+# one condition each, in the order that costs least; what fails it is looked
+# for, and named, in the functions that raise.
+
 def _words(name: str, t: Optional[torch.Tensor], need: int, dtype=torch.int32) -> None:
     """An array that the kernels index: its type, contiguous, long enough."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.is_contiguous() and t.numel() >= need):
         return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.numel() < need:
-        raise ValueError(f"{name} has {t.numel()} entries; the call reads {need}")
+    raise ValueError(f"{name} has {t.numel()} entries; the call reads {need}")
 
 
-def _placed(device, **tensors) -> None:
-    for name, t in tensors.items():
-        if isinstance(t, torch.Tensor) and (t.device.type != "cuda" or t.device != device):
-            raise ValueError(f"{name} is on {t.device}; every tensor must be on one CUDA device ({device})")
+def _on(index: int, tensors, names) -> None:
+    """Every tensor (of those given) is on CUDA device ``index``."""
+    for t in tensors:
+        if t is not None and t.get_device() != index or index < 0:
+            break
+    else:
+        return
+    for name, t in zip(names, tensors):
+        if t is not None and (t.device.type != "cuda" or t.get_device() != index):
+            raise ValueError(f"{name} is on {t.device}; every tensor must be on one CUDA device"
+                             + (f" (cuda:{index})" if index >= 0 else ""))
+
+
+def _call(function, index: int, stream: Optional[int], *args) -> None:
+    """The entry point on the tensors' device and stream."""
+    if torch.cuda.current_device() == index:
+        status = function(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
+    else:
+        with torch.cuda.device(index):
+            status = function(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
+    if status:
+        _check(status)
 
 
 def _table(name: str, t: torch.Tensor) -> None:
@@ -113,17 +134,8 @@ def _table(name: str, t: torch.Tensor) -> None:
         raise ValueError(f"{name}: rows overlap")
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    """Stride of the leading dim (a single row has none that matters: the dense one)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _stream(stream: Optional[int]):
-    return _c_void_p(torch.cuda.current_stream().cuda_stream if stream is None else stream)
-
-
-def _cache(rows: torch.Tensor, scales: torch.Tensor, tables: torch.Tensor, seq_lens: torch.Tensor,
-           cum: Optional[torch.Tensor]) -> SmlaCache:
+def _check_cache(rows: torch.Tensor, scales: torch.Tensor, tables: torch.Tensor) -> None:
+    """Raises what is wrong with a cache's layout."""
     if rows.dtype not in (torch.float8_e4m3fn, torch.uint8):
         raise TypeError(f"cache rows are float8_e4m3fn (or its bytes); got {rows.dtype}")
     if rows.dim() != 3 or rows.shape[2] != HEAD_DIM or rows.stride(2) != 1:
@@ -137,40 +149,45 @@ def _cache(rows: torch.Tensor, scales: torch.Tensor, tables: torch.Tensor, seq_l
     if rows.shape[0] < 1 or rows.shape[1] % scales.shape[1] != 0:
         raise ValueError(f"{scales.shape[1]} scales do not divide a page of {rows.shape[1]} rows")
     if (rows.shape[0] > 1 and rows.stride(0) <= 0) or (rows.shape[1] > 1 and rows.stride(1) <= 0) or \
-            (scales.shape[0] > 1 and scales.stride(0) <= 0):
+            (scales.shape[0] > 1 and scales.stride(0) < scales.shape[1]):
         raise ValueError("cache pages must not share memory")
     _table("block_tables", tables)
     if tables.shape[0] < 1:
         raise ValueError("block_tables has no rows")
-    batch = tables.shape[0]
+
+
+def _cache(rows: torch.Tensor, scales: torch.Tensor, tables: torch.Tensor, seq_lens: torch.Tensor,
+           cum: Optional[torch.Tensor]) -> SmlaCache:
+    rs, ss, ts = rows.shape, scales.shape, tables.shape
+    rt, st, tt = rows.stride(), scales.stride(), tables.stride()
+    dense = rs[1:] and ss[1:] and ts[1:] and len(rs) == 3 and len(ss) == 2 and len(ts) == 2
+    if not (dense and (rows.dtype is torch.float8_e4m3fn or rows.dtype is torch.uint8)
+            and scales.dtype is torch.float32 and tables.dtype is torch.int32
+            and rs[2] == HEAD_DIM and rt[2] == st[1] == tt[1] == 1 and ss[0] == rs[0] > 0
+            and rs[1] % ss[1] == 0 and rt[0] > 0 and rt[1] > 0 and st[0] >= ss[1] and tt[0] >= ts[1] and ts[0] > 0):
+        _check_cache(rows, scales, tables)     # raises, or the odd strides are those of dims of one entry
+    num_pages, page_size = rs[0], rs[1]
+    batch, max_pages = ts
     _words("seq_lens", seq_lens, batch)
-    _words("cum_seq_lens_q", cum, batch + 1)
-    c = SmlaCache()
-    c.num_pages, c.page_size = rows.shape[0], rows.shape[1]
-    c.block_rows = rows.shape[1] // scales.shape[1]
-    c.rows = rows.data_ptr()
-    c.row_stride = rows.stride(1) if rows.shape[1] > 1 else HEAD_DIM
-    c.page_stride = rows.stride(0) if rows.shape[0] > 1 else 0
-    c.scales, c.scale_stride = scales.data_ptr(), _row_stride(scales)
-    c.block_tables, c.block_table_stride = tables.data_ptr(), _row_stride(tables)
-    c.max_pages, c.batch = tables.shape[1], batch
-    c.seq_lens, c.cum_seq_lens_q = seq_lens.data_ptr(), _ptr(cum)
-    return c
+    if cum is not None:
+        _words("cum_seq_lens_q", cum, batch + 1)
+    return SmlaCache(rows.data_ptr(), rt[1] if page_size > 1 else HEAD_DIM, rt[0] if num_pages > 1 else 0,
+                     scales.data_ptr(), st[0] if num_pages > 1 else ss[1], num_pages, page_size, page_size // ss[1],
+                     tables.data_ptr(), tt[0] if batch > 1 else max_pages, max_pages, batch,
+                     seq_lens.data_ptr(), None if cum is None else cum.data_ptr())
 
 
 def _window_args(q, rows, scales, tables, seq_lens, cum, sinks, window, first_tokens, num_splits) -> SmlaWindowArgs:
-    if q.dtype != torch.bfloat16:
+    qs, qt = q.shape, q.stride()
+    if q.dtype is not torch.bfloat16:
         raise TypeError(f"q must be bfloat16; got {q.dtype}")
-    if q.dim() != 3 or q.shape[2] != HEAD_DIM or q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != HEAD_DIM):
-        raise ValueError(f"q must be [T, H, {HEAD_DIM}] with contiguous heads; got {tuple(q.shape)}")
-    a = SmlaWindowArgs()
-    a.cache = _cache(rows, scales, tables, seq_lens, cum)
-    a.sum_q, a.num_heads = q.shape[0], q.shape[1]
-    a.window, a.first_tokens, a.num_splits = int(window), int(first_tokens), int(num_splits)
-    a.q, a.q_stride_token = q.data_ptr(), q.stride(0) if q.shape[0] > 1 else 0
-    _words("sinks", sinks, a.num_heads, torch.float32)
-    a.sinks = _ptr(sinks)
-    return a
+    if len(qs) != 3 or qs[2] != HEAD_DIM or qt[2] != 1 or (qs[1] > 1 and qt[1] != HEAD_DIM):
+        raise ValueError(f"q must be [T, H, {HEAD_DIM}] with contiguous heads; got {tuple(qs)}")
+    if sinks is not None:
+        _words("sinks", sinks, qs[1], torch.float32)
+    return SmlaWindowArgs(_cache(rows, scales, tables, seq_lens, cum), qs[0], qs[1], int(window), int(first_tokens),
+                          q.data_ptr(), qt[0] if qs[0] > 1 else 0, None if sinks is None else sinks.data_ptr(),
+                          1.0, 1.0, None, None, None, None, None, 0, int(num_splits), None)
 
 
 def window_workspace_size(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block_tables: torch.Tensor,
@@ -182,6 +199,10 @@ def window_workspace_size(q: torch.Tensor, rows: torch.Tensor, scales: torch.Ten
     n = ctypes.c_size_t(0)
     _check(_b.lib().smla_window_workspace_size(ctypes.byref(a), device, ctypes.byref(n)))
     return int(n.value)
+
+
+_WINDOW_TENSORS = ("q", "rows", "scales", "block_tables", "seq_lens", "workspace", "cum_seq_lens_q", "sinks", "bmm1_scale",
+                   "bmm2_scale", "out", "out_lse", "error_word")
 
 
 def window_attention(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block_tables: torch.Tensor,
@@ -198,32 +219,41 @@ def window_attention(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, 
     T, H = a.sum_q, a.num_heads
     if out is None:
         out = torch.empty((T, H, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
+    elif out.dtype != torch.bfloat16 or not out.is_contiguous() or out.numel() != T * H * HEAD_DIM:
+        raise ValueError("out must be a contiguous bfloat16 tensor of T*H*512 elements")
     if out_lse is None:
         out_lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    if out.dtype != torch.bfloat16 or not out.is_contiguous() or out.numel() != T * H * HEAD_DIM:
-        raise ValueError("out must be a contiguous bfloat16 tensor of T*H*512 elements")
-    if out_lse.dtype != torch.float32 or not out_lse.is_contiguous() or out_lse.numel() != T * H:
+    elif out_lse.dtype != torch.float32 or not out_lse.is_contiguous() or out_lse.numel() != T * H:
         raise ValueError("out_lse must be a contiguous float32 tensor of T*H elements")
     _words("error_word", error_word, 1)
-    for name, val in (("bmm1", bmm1_scale), ("bmm2", bmm2_scale)):
-        if isinstance(val, torch.Tensor):
-            _words(f"{name}_scale", val, 1, torch.float32)
-            setattr(a, f"{name}_scale_dev", val.data_ptr())
-            setattr(a, f"{name}_scale", 1.0)
-        else:
-            setattr(a, f"{name}_scale", float(val))
-    a.out, a.out_lse, a.error_word = out.data_ptr(), out_lse.data_ptr(), _ptr(error_word)
+    scale1 = scale2 = None
+    if isinstance(bmm1_scale, torch.Tensor):
+        scale1 = bmm1_scale
+        _words("bmm1_scale", scale1, 1, torch.float32)
+        a.bmm1_scale_dev = scale1.data_ptr()
+    else:
+        a.bmm1_scale = float(bmm1_scale)
+    if isinstance(bmm2_scale, torch.Tensor):
+        scale2 = bmm2_scale
+        _words("bmm2_scale", scale2, 1, torch.float32)
+        a.bmm2_scale_dev = scale2.data_ptr()
+    else:
+        a.bmm2_scale = float(bmm2_scale)
+    a.out, a.out_lse = out.data_ptr(), out_lse.data_ptr()
+    if error_word is not None:
+        a.error_word = error_word.data_ptr()
     if workspace_buffer is not None:
         if not workspace_buffer.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        a.workspace = workspace_buffer.data_ptr()
-        a.workspace_bytes = workspace_buffer.numel() * workspace_buffer.element_size()
-    _placed(q.device, q=q, rows=rows, scales=scales, block_tables=block_tables, seq_lens=seq_lens,
-            workspace=workspace_buffer, cum_seq_lens_q=cum_seq_lens_q, sinks=sinks, bmm1_scale=bmm1_scale,
-            bmm2_scale=bmm2_scale, out=out, out_lse=out_lse, error_word=error_word)
-    with torch.cuda.device(q.device):
-        _check(_b.lib().smla_window_attention(ctypes.byref(a), _stream(stream)))
+        a.workspace, a.workspace_bytes = workspace_buffer.data_ptr(), workspace_buffer.nbytes
+    index = q.get_device()
+    _on(index, (q, rows, scales, block_tables, seq_lens, workspace_buffer, cum_seq_lens_q, sinks, scale1, scale2, out,
+                out_lse, error_word), _WINDOW_TENSORS)
+    _call(_b.lib().smla_window_attention, index, stream, ctypes.byref(a))
     return out, out_lse
+
+
+_APPEND_TENSORS = ("latent", "rows", "scales", "block_tables", "seq_lens", "cum_seq_lens_q", "error_word")
 
 
 def append(latent: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block_tables: torch.Tensor,
@@ -231,44 +261,44 @@ def append(latent: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block
            error_word: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> None:
     """Quantises the new latent rows ``[T, 512]`` (BF16) into the cache, at the
     last positions of their requests (``seq_lens`` counts them)."""
-    if latent.dtype != torch.bfloat16:
+    ls, lt = latent.shape, latent.stride()
+    if latent.dtype is not torch.bfloat16:
         raise TypeError(f"latent must be bfloat16; got {latent.dtype}")
-    if latent.dim() != 2 or latent.shape[1] != HEAD_DIM or latent.stride(1) != 1:
-        raise ValueError(f"latent must be [T, {HEAD_DIM}] with contiguous rows; got {tuple(latent.shape)}")
-    a = SmlaAppendArgs()
-    a.cache = _cache(rows, scales, block_tables, seq_lens, cum_seq_lens_q)
-    a.sum_q, a.latent = latent.shape[0], latent.data_ptr()
-    a.latent_stride = latent.stride(0) if latent.shape[0] > 1 else HEAD_DIM
+    if len(ls) != 2 or ls[1] != HEAD_DIM or lt[1] != 1:
+        raise ValueError(f"latent must be [T, {HEAD_DIM}] with contiguous rows; got {tuple(ls)}")
     _words("error_word", error_word, 1)
-    a.error_word = _ptr(error_word)
-    _placed(latent.device, latent=latent, rows=rows, scales=scales, block_tables=block_tables, seq_lens=seq_lens,
-            cum_seq_lens_q=cum_seq_lens_q, error_word=error_word)
-    with torch.cuda.device(latent.device):
-        _check(_b.lib().smla_cache_append(ctypes.byref(a), _stream(stream)))
+    a = SmlaAppendArgs(_cache(rows, scales, block_tables, seq_lens, cum_seq_lens_q), ls[0], latent.data_ptr(),
+                       lt[0] if ls[0] > 1 else HEAD_DIM, None if error_word is None else error_word.data_ptr())
+    index = latent.get_device()
+    _on(index, (latent, rows, scales, block_tables, seq_lens, cum_seq_lens_q, error_word), _APPEND_TENSORS)
+    _call(_b.lib().smla_cache_append, index, stream, ctypes.byref(a))
 
 
-def _pages_args(tables, ref_counts, lens, page_size, error_word) -> SmlaPagesArgs:
-    _table("block_tables", tables)
+def _pages_args(tables, ref_counts, lens, page_size, error_word, new_lens=None, parents=None, out_lens=None,
+                moves=(None, None, None), workspace=None) -> SmlaPagesArgs:
+    ts, tt = tables.shape, tables.stride()
+    if not (len(ts) == 2 and tables.dtype is torch.int32 and tt[1] == 1 and tt[0] >= ts[1] > 0):
+        _table("block_tables", tables)         # raises, or the odd stride is that of a dim of one entry
+    rows, max_pages = ts
     _words("ref_counts", ref_counts, 1)
-    _words("lens", lens, tables.shape[0])
+    _words("lens", lens, rows)
     _words("error_word", error_word, 1)
-    a = SmlaPagesArgs()
-    a.block_tables, a.block_table_stride = tables.data_ptr(), _row_stride(tables)
-    a.rows, a.max_pages, a.page_size = tables.shape[0], tables.shape[1], int(page_size)
-    a.ref_counts, a.num_pages = ref_counts.data_ptr(), ref_counts.numel()
-    a.lens, a.error_word = lens.data_ptr(), _ptr(error_word)
-    return a
-
-
-def _with_moves(a: SmlaPagesArgs, moves, workspace: torch.Tensor) -> None:
+    _words("new_lens", new_lens, rows)
+    _words("parents", parents, rows)
+    _words("out_lens", out_lens, rows)
     src, dst, count = moves
-    _words("moves.src", src, 0)
-    _words("moves.dst", dst, src.numel())
-    _words("moves.count", count, 1)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    a.move_src, a.move_dst, a.move_count, a.move_capacity = src.data_ptr(), dst.data_ptr(), count.data_ptr(), src.numel()
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    capacity = 0
+    if src is not None:
+        capacity = src.numel()
+        _words("moves.src", src, 0)
+        _words("moves.dst", dst, capacity)
+        _words("moves.count", count, 1)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    return SmlaPagesArgs(tables.data_ptr(), tt[0] if rows > 1 else max_pages, rows, max_pages, int(page_size),
+                         ref_counts.data_ptr(), ref_counts.numel(), lens.data_ptr(), _ptr(new_lens), _ptr(parents),
+                         _ptr(out_lens), _ptr(src), _ptr(dst), _ptr(count), capacity, _ptr(workspace),
+                         0 if workspace is None else workspace.nbytes, _ptr(error_word))
 
 
 def pages_workspace_size(block_tables: torch.Tensor, ref_counts: torch.Tensor, page_size: int) -> int:
@@ -281,21 +311,21 @@ def pages_workspace_size(block_tables: torch.Tensor, ref_counts: torch.Tensor, p
     return int(n.value)
 
 
+_PAGES_TENSORS = ("block_tables", "ref_counts", "lens", "new_lens", "workspace", "move_src", "move_dst", "move_count",
+                  "error_word")
+
+
 def pages_resize(block_tables: torch.Tensor, ref_counts: torch.Tensor, lens: torch.Tensor, new_lens: torch.Tensor,
                  workspace_buffer: torch.Tensor, *, page_size: int, moves,
                  error_word: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> None:
     """Takes each request from ``lens`` to ``new_lens`` tokens: pages dropped,
     then the lowest free pages handed out; ``moves`` receives the shared pages
     that a growing request got a copy of (``pages_copy`` them)."""
-    a = _pages_args(block_tables, ref_counts, lens, page_size, error_word)
-    _words("new_lens", new_lens, a.rows)
-    a.new_lens = new_lens.data_ptr()
-    _with_moves(a, moves, workspace_buffer)
-    _placed(block_tables.device, block_tables=block_tables, ref_counts=ref_counts, lens=lens, new_lens=new_lens,
-            workspace=workspace_buffer, move_src=moves[0], move_dst=moves[1], move_count=moves[2],
-            error_word=error_word)
-    with torch.cuda.device(block_tables.device):
-        _check(_b.lib().smla_pages_resize(ctypes.byref(a), _stream(stream)))
+    a = _pages_args(block_tables, ref_counts, lens, page_size, error_word, new_lens=new_lens, moves=moves,
+                    workspace=workspace_buffer)
+    index = block_tables.get_device()
+    _on(index, (block_tables, ref_counts, lens, new_lens, workspace_buffer, *moves, error_word), _PAGES_TENSORS)
+    _call(_b.lib().smla_pages_resize, index, stream, ctypes.byref(a))
 
 
 def pages_fork(block_tables: torch.Tensor, ref_counts: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor,
@@ -303,14 +333,11 @@ def pages_fork(block_tables: torch.Tensor, ref_counts: torch.Tensor, lens: torch
                stream: Optional[int] = None) -> None:
     """Requests with ``parents[b] >= 0`` (which hold nothing) share their
     parent's pages; ``out_lens`` receives every request's length after it."""
-    a = _pages_args(block_tables, ref_counts, lens, page_size, error_word)
-    _words("parents", parents, a.rows)
-    _words("out_lens", out_lens, a.rows)
-    a.parents, a.out_lens = parents.data_ptr(), out_lens.data_ptr()
-    _placed(block_tables.device, block_tables=block_tables, ref_counts=ref_counts, lens=lens, parents=parents,
-            out_lens=out_lens, error_word=error_word)
-    with torch.cuda.device(block_tables.device):
-        _check(_b.lib().smla_pages_fork(ctypes.byref(a), _stream(stream)))
+    a = _pages_args(block_tables, ref_counts, lens, page_size, error_word, parents=parents, out_lens=out_lens)
+    index = block_tables.get_device()
+    _on(index, (block_tables, ref_counts, lens, parents, out_lens, error_word),
+        ("block_tables", "ref_counts", "lens", "parents", "out_lens", "error_word"))
+    _call(_b.lib().smla_pages_fork, index, stream, ctypes.byref(a))
 
 
 def pages_compact(block_tables: torch.Tensor, ref_counts: torch.Tensor, lens: torch.Tensor,
@@ -318,13 +345,10 @@ def pages_compact(block_tables: torch.Tensor, ref_counts: torch.Tensor, lens: to
                   error_word: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> None:
     """Renumbers the pages in use to the front of the pool; ``moves`` receives
     the pages to copy (``pages_copy``) before the cache is used again."""
-    a = _pages_args(block_tables, ref_counts, lens, page_size, error_word)
-    _with_moves(a, moves, workspace_buffer)
-    _placed(block_tables.device, block_tables=block_tables, ref_counts=ref_counts, lens=lens,
-            workspace=workspace_buffer, move_src=moves[0], move_dst=moves[1], move_count=moves[2],
-            error_word=error_word)
-    with torch.cuda.device(block_tables.device):
-        _check(_b.lib().smla_pages_compact(ctypes.byref(a), _stream(stream)))
+    a = _pages_args(block_tables, ref_counts, lens, page_size, error_word, moves=moves, workspace=workspace_buffer)
+    index = block_tables.get_device()
+    _on(index, (block_tables, ref_counts, lens, None, workspace_buffer, *moves, error_word), _PAGES_TENSORS)
+    _call(_b.lib().smla_pages_compact, index, stream, ctypes.byref(a))
 
 
 def pages_copy(pools: Sequence[torch.Tensor], moves, *, error_word: Optional[torch.Tensor] = None,
@@ -333,24 +357,26 @@ def pages_copy(pools: Sequence[torch.Tensor], moves, *, error_word: Optional[tor
     ...]`` of any type whose pages are contiguous (rows and scales of all
     layers in one call)."""
     src, dst, count = moves
+    capacity = src.numel()
     _words("moves.src", src, 0)
-    _words("moves.dst", dst, src.numel())
+    _words("moves.dst", dst, capacity)
     _words("moves.count", count, 1)
     _words("error_word", error_word, 1)
-    array = (SmlaPool * max(1, len(pools)))()
-    for i, t in enumerate(pools):
-        if t.dim() < 1 or t.shape[0] != pools[0].shape[0]:
-            raise ValueError(f"pool {i} must be [num_pages, ...] with the first pool's {pools[0].shape[0]} pages")
-        if t.shape[0] < 1 or t.numel() == 0 or not t[0].is_contiguous():
-            raise ValueError(f"pool {i}: pages must be contiguous and not empty")
-        page = t[0].numel() * t.element_size()
-        array[i].base, array[i].page_bytes = t.data_ptr(), page
-        array[i].page_stride = t.stride(0) * t.element_size() if t.shape[0] > 1 else page
-        _placed(src.device, **{f"pool {i}": t})
     if not pools:
         return
-    _placed(src.device, move_src=src, move_dst=dst, move_count=count, error_word=error_word)
-    with torch.cuda.device(src.device):
-        _check(_b.lib().smla_pages_copy(ctypes.byref(array), len(pools), pools[0].shape[0], src.data_ptr(),
-                                        dst.data_ptr(), count.data_ptr(), src.numel(), _ptr(error_word),
-                                        _stream(stream)))
+    index = src.get_device()
+    num_pages = pools[0].shape[0] if pools[0].dim() else 0
+    described = []
+    for i, t in enumerate(pools):
+        if t.dim() < 1 or t.shape[0] != num_pages:
+            raise ValueError(f"pool {i} must be [num_pages, ...] with the first pool's {num_pages} pages")
+        if num_pages < 1 or t.numel() == 0 or not (t.is_contiguous() or t[0].is_contiguous()):
+            raise ValueError(f"pool {i}: pages must be contiguous and not empty")
+        page = t.nbytes // num_pages
+        described.append((t.data_ptr(), page, t.stride(0) * t.element_size() if num_pages > 1 else page))
+        if t.get_device() != index:
+            _on(index, (t,), (f"pool {i}",))
+    _on(index, (src, dst, count, error_word), ("move_src", "move_dst", "move_count", "error_word"))
+    array = (SmlaPool * len(described))(*described)
+    _call(_b.lib().smla_pages_copy, index, stream, ctypes.byref(array), len(described), num_pages, src.data_ptr(),
+          dst.data_ptr(), count.data_ptr(), capacity, _ptr(error_word))

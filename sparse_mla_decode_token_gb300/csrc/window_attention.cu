@@ -853,7 +853,7 @@ cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t
   // the highest box that pages hold whole, up to a quarter of a tile: fewer copies to issue
   const int shift = p.c.page_size % 32 == 0 ? 5 : p.c.page_size % 16 == 0 ? 4 : 3;
   cudaError_t e = encode_cache_map(&kp.map, p.c, 1 << shift);
-  if (e == cudaSuccess) e = encode_out_map(&kp.out_map, p);
+  if (e == cudaSuccess && p.num_splits == 1) e = encode_out_map(&kp.out_map, p);   // (partials are stored by threads)
   if (e != cudaSuccess) return e;
   auto launch = [&](auto kernel) -> cudaError_t {
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);

@@ -32,6 +32,22 @@ __device__ __forceinline__ void request_tokens(const CacheView& c, int b, int* f
   }
 }
 
+// The last request b of `batch` for which before(b) holds (before(0) is taken to;
+// it holds up to some b and not behind it).  Whole warp, 32 requests looked at at
+// a time, so that a batch of a thousand costs two trips to L2.
+template <class F>
+__device__ __forceinline__ int last_request(int batch, int lane, F before) {
+  int lo = 0, n = batch - 1;                        // the answer is among lo .. lo + n
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int hits = __popc(__ballot_sync(0xffffffffu, before(lo + min(n, (lane + 1) * step))));
+    if (hits == 32) return lo + n;                  // (the last lanes look at lo + n)
+    lo += hits * step;
+    n = min(n - hits * step, step - 1);             // lo + step is known to be behind it
+  }
+  return lo;
+}
+
 struct WindowParams {
   CacheView c;
   int32_t H, window, first_tokens, num_splits;
@@ -78,10 +94,12 @@ struct PagesParams {
   int32_t* err;
 };
 
-// Workspace words of resize and compact: a header, then per-row words
-// (resize) or per-page words.
+// Workspace words of resize and compact: a header, per-row words (resize),
+// per-page words, a count per 1024 pages.
 constexpr int kPagesHeader = 64;
-inline int64_t pages_workspace_words(int64_t rows, int64_t num_pages) { return kPagesHeader + 2 * rows + num_pages; }
+inline int64_t pages_workspace_words(int64_t rows, int64_t num_pages) {
+  return kPagesHeader + 2 * rows + num_pages + (num_pages + 1023) / 1024;
+}
 
 cudaError_t launch_pages_resize(const PagesParams& p, cudaStream_t stream);
 cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream);

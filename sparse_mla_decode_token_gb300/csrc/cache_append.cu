@@ -10,6 +10,8 @@
 // registers between the maximum and the rounding (blocks of up to 16 new rows;
 // longer ones are read again, from L2), so DRAM sees each row once: 1 KB in,
 // 512 B out a token.
+#include <type_traits>
+
 #include "cache.cuh"
 
 namespace smla {
@@ -36,12 +38,18 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
+// x / s and one rounding to E4M3.  For a power of two (kPow2; every scale that
+// this call makes) s holds the exact reciprocal; a scale that the caller's own
+// blocks came with takes a correctly rounded division.
+template <bool kPow2>
 __device__ __forceinline__ uint2 quantise8(uint4 v, float s) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)                    // one correctly rounded division, then one rounding to E4M3
-    h[i] = e4m3x2(__fdiv_rn(__uint_as_float(w[i] << 16), s), __fdiv_rn(__uint_as_float(w[i] & 0xffff0000u), s));
+  for (int i = 0; i < 4; ++i) {
+    const float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xffff0000u);
+    h[i] = kPow2 ? e4m3x2(a * s, b * s) : e4m3x2(__fdiv_rn(a, s), __fdiv_rn(b, s));
+  }
   return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
 }
 
@@ -51,37 +59,27 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
   // unit u -> (request, block): request b's units start at first(b) / block_rows + 2 b,
   // which leaves room for the blocks its tokens can touch, count / block_rows + 2
   const int64_t u = blockIdx.x;
-  int lo = 0, hi = c.batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
+  const int b = last_request(c.batch, threadIdx.x & 31, [&](int at) {
     int f, n;
-    request_tokens(c, mid, &f, &n);
-    if ((int64_t)f / c.block_rows + 2 * (int64_t)mid <= u) lo = mid;
-    else hi = mid - 1;
-  }
-  const int b = lo;
+    request_tokens(c, at, &f, &n);
+    return (int64_t)(f / c.block_rows) + 2 * (int64_t)at <= u;
+  });
   int first, count;
   request_tokens(c, b, &first, &count);
   if (first < 0 || count <= 0 || count > c.sum_q - first) return;       // (offsets that are none: nothing is written)
-  const int64_t start = (int64_t)__ldg(c.seq_lens + b) - count;         // position of the first new token
-  const int64_t end = start + count;
-  const int64_t i = u - (first / c.block_rows + 2 * (int64_t)b);        // block of the request's touched ones
-  const int64_t from0 = start < 0 ? 0 : start;
+  const int start = __ldg(c.seq_lens + b) - count;                      // position of the first new token
+  const int end = start + count, from0 = max(start, 0);
+  const int i = (int)(u - (first / c.block_rows + 2 * (int64_t)b));     // block of the request's touched ones
   if (i == 0 && start < 0 && threadIdx.x == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
-  const int64_t block0 = (from0 / c.block_rows + i) * c.block_rows;     // first position of the block
+  const int64_t block0 = ((int64_t)(from0 / c.block_rows) + i) * c.block_rows;   // first position of the block
   if (block0 >= end) return;
-  const int64_t pos0 = block0 > from0 ? block0 : from0;                 // first new position in the block
-  const int64_t pos1 = block0 + c.block_rows < end ? block0 + c.block_rows : end;
-  const int64_t column = block0 / c.page_size;
+  const int pos0 = max((int)block0, from0);                             // first new position in the block
+  const int pos1 = (int)min(block0 + c.block_rows, (int64_t)end);
+  const int column = (int)block0 / c.page_size;
+  const int row0 = (int)block0 - column * c.page_size;                  // the block's first row in its page
+  // (the page is on its way while the rows are read)
   const int page = column < c.max_pages ? __ldg(c.bt + (int64_t)b * c.bt_stride + column) : -1;
-  if (page < 0 || page >= c.num_pages) {
-    if (threadIdx.x == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
-    return;
-  }
-  const int row0 = (int)(block0 % c.page_size);                         // the block's first row in its page
-  uint8_t* dst = c.rows + (int64_t)page * c.page_stride + (int64_t)row0 * c.row_stride;
-  float* scale = c.scales + (int64_t)page * c.scale_stride + row0 / c.block_rows;
-  const int older = (int)(pos0 - block0), rows = (int)(pos1 - pos0);
+  const int older = pos0 - (int)block0, rows = pos1 - pos0;
   const __nv_bfloat16* src = p.latent + (first + (pos0 - start)) * p.latent_stride;
   const int group = threadIdx.x >> 6, lane8 = threadIdx.x & 63;         // row parity, 8 values
 
@@ -92,12 +90,18 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
     const int r = k * kGroups + group;
     if (r < rows) held[k] = __ldg(reinterpret_cast<const uint4*>(src + r * p.latent_stride) + lane8);
   }
+  if (page < 0 || page >= c.num_pages) {
+    if (threadIdx.x == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
+    return;
+  }
+  uint8_t* dst = c.rows + (int64_t)page * c.page_stride + (int64_t)row0 * c.row_stride;
+  float* scale = c.scales + (int64_t)page * c.scale_stride + row0 / c.block_rows;
+  const float old = older > 0 ? *scale : 0.f;
 #pragma unroll
   for (int k = 0; k < kHeld; ++k)
     if (k * kGroups + group < rows) m = amax8(held[k], m);
   for (int r = kHeld * kGroups + group; r < rows; r += kGroups)
     m = amax8(__ldg(reinterpret_cast<const uint4*>(src + r * p.latent_stride) + lane8), m);
-  const float old = older > 0 ? *scale : 0.f;
   m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));   // not negative: orders as integers
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();                                        // also: every thread has read the old scale
@@ -129,14 +133,23 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
     }
   }
   dst += older * c.row_stride;
+  auto store = [&](auto pow2, float by) {
+    constexpr bool kPow2 = decltype(pow2)::value;
 #pragma unroll
-  for (int kk = 0; kk < kHeld; ++kk) {
-    const int r = kk * kGroups + group;
-    if (r < rows) reinterpret_cast<uint2*>(dst + r * c.row_stride)[lane8] = quantise8(held[kk], s);
-  }
-  for (int r = kHeld * kGroups + group; r < rows; r += kGroups)
-    reinterpret_cast<uint2*>(dst + r * c.row_stride)[lane8] =
-        quantise8(__ldg(reinterpret_cast<const uint4*>(src + r * p.latent_stride) + lane8), s);
+    for (int kk = 0; kk < kHeld; ++kk) {
+      const int r = kk * kGroups + group;
+      if (r < rows) reinterpret_cast<uint2*>(dst + r * c.row_stride)[lane8] = quantise8<kPow2>(held[kk], by);
+    }
+    for (int r = kHeld * kGroups + group; r < rows; r += kGroups)
+      reinterpret_cast<uint2*>(dst + r * c.row_stride)[lane8] =
+          quantise8<kPow2>(__ldg(reinterpret_cast<const uint4*>(src + r * p.latent_stride) + lane8), by);
+  };
+  const uint32_t bits = __float_as_uint(s);
+  // a normal power of two whose reciprocal is one too
+  if ((bits & 0x7fffffu) == 0 && bits >= 0x00800000u && bits <= 0x7e800000u)
+    store(std::true_type{}, __uint_as_float(0x7f000000u - bits));
+  else
+    store(std::false_type{}, s);
 }
 
 }  // namespace

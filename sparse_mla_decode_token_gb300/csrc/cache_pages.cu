@@ -3,12 +3,14 @@
 //
 // The state is a count per page (a page with count 0 is free) and a table row
 // per request.  Ranking the free (or live) pages in order is a prefix sum over
-// the counts: resize and compact run it inside one cluster of CTAs, each warp
-// owning one contiguous segment of the pool, so that the whole call is one
-// launch with cluster barriers in between, and every page's rank (hence who
-// gets it) depends on nothing but the state.  What bounds them is latency: the
-// counts (4 bytes a page) are read once or twice, the rest is a few dependent
-// L2 round trips.
+// the counts: resize and compact run it inside one cluster of CTAs, so that a
+// call is one launch (two for compact) with cluster barriers in between, and
+// every page's rank, hence who gets it, depends on nothing but the state.
+// Pages are counted in chunks of 1024, a warp per chunk, the chunks dealt out
+// to all warps of the cluster in turn (those that hold the lowest free pages
+// would otherwise be one CTA's); each CTA then sums the chunks' counts itself.
+// What bounds the calls is latency: the counts (4 bytes a page) are read once,
+// and again where pages are handed out; the rest is a few dependent trips to L2.
 #include "cache.cuh"
 #include "tc_ptx.cuh"
 
@@ -49,103 +51,180 @@ __device__ __forceinline__ void drop_ref(const PagesParams& p, int page) {
   }
 }
 
-// Segment [begin, end) of the pool that warp w of the cluster ranks.
-__device__ __forceinline__ void segment(int num_pages, int w, int* begin, int* end) {
-  const int64_t per = (((int64_t)num_pages + kClusterWarps - 1) / kClusterWarps + 31) / 32 * 32;
-  *begin = (int)min((int64_t)num_pages, per * w);
-  *end = (int)min((int64_t)num_pages, per * (w + 1));
+constexpr int kChunk = 1024;                          // pages a warp counts at a time: 8 x 4 a lane
+
+// Counts of pages [4 i, 4 i + 3] past `base` (pages past the pool: `pad`).
+__device__ __forceinline__ int4 load_counts(const PagesParams& p, int64_t base, int i, int pad) {
+  const int64_t at = base + 4 * (int64_t)i;
+  const int32_t* r = p.refs + at;
+  if (at + 3 < p.num_pages && (reinterpret_cast<uintptr_t>(r) & 15u) == 0)
+    return __ldcg(reinterpret_cast<const int4*>(r));
+  int4 v = make_int4(pad, pad, pad, pad);
+  if (at < p.num_pages) v.x = __ldcg(r);
+  if (at + 1 < p.num_pages) v.y = __ldcg(r + 1);
+  if (at + 2 < p.num_pages) v.z = __ldcg(r + 2);
+  if (at + 3 < p.num_pages) v.w = __ldcg(r + 3);
+  return v;
 }
 
-// Pages of [begin, end) with a count above 0 (whole warp; same result in every lane).
-__device__ __forceinline__ int count_live(const int32_t* refs, int begin, int end, int lane) {
-  constexpr int kUnroll = 8;                            // loads in flight per lane
+// Pages of a chunk that are in use, before page `end` (whole warp; the same in every lane).
+__device__ __forceinline__ int count_live(const PagesParams& p, int64_t base, int64_t end, int lane) {
+  int4 v[kChunk / 128];
+#pragma unroll
+  for (int k = 0; k < kChunk / 128; ++k) v[k] = load_counts(p, base, k * 32 + lane, 0);
   int n = 0;
-  for (int base = begin; base < end; base += 32 * kUnroll) {
-    int r[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = base + u * 32 + lane;
-      r[u] = i < end ? __ldcg(refs + i) : 0;
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) n += r[u] > 0;
+  for (int k = 0; k < kChunk / 128; ++k) {
+    const int64_t at = base + 4 * (k * 32 + lane);
+    n += (v[k].x > 0 && at < end) + (v[k].y > 0 && at + 1 < end) + (v[k].z > 0 && at + 2 < end) +
+         (v[k].w > 0 && at + 3 < end);
   }
   return __reduce_add_sync(0xffffffffu, n);
 }
 
-// Calls f(page, live, live pages before it in the segment) for each page of
-// [begin, end); f returns false (warp-uniformly) to stop early.
+// Calls f(page, count, pages in use before it in the chunk) for each page of a chunk.
 template <class F>
-__device__ __forceinline__ void walk(const int32_t* refs, int begin, int end, int lane, F f) {
-  constexpr int kUnroll = 4;
+__device__ __forceinline__ void walk(const PagesParams& p, int64_t base, int lane, F f) {
+  int4 v[kChunk / 128];
+#pragma unroll
+  for (int k = 0; k < kChunk / 128; ++k) v[k] = load_counts(p, base, k * 32 + lane, 0);
   int before = 0;
-  for (int base = begin; base < end; base += 32 * kUnroll) {
-    int r[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = base + u * 32 + lane;
-      r[u] = i < end ? __ldcg(refs + i) : 0;
-    }
+  for (int k = 0; k < kChunk / 128; ++k) {
+    const int r[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    int mine = 0, all = 0;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = base + u * 32 + lane;
-      const uint32_t m = __ballot_sync(0xffffffffu, r[u] > 0);
-      if (i < end) f(i, r[u], before + __popc(m & ((1u << lane) - 1u)));
-      before += __popc(m);
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t m = __ballot_sync(0xffffffffu, r[e] > 0);
+      mine += __popc(m & ((1u << lane) - 1u));
+      all += __popc(m);
     }
+    mine += before;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t page = base + 4 * (k * 32 + lane) + e;
+      if (page < p.num_pages) f((int)page, r[e], mine);
+      mine += r[e] > 0;
+    }
+    before += all;
   }
 }
 
-// Live pages before each warp's segment, for the whole cluster: returns this
-// warp's, and the total.  One cluster barrier.
-__device__ __forceinline__ int live_before(int live, int rank, int warp, int lane, int32_t* s_count, int* total) {
-  if (lane == 0) s_count[warp] = live;
-  ptx::cluster_sync();
-  // the counts of all warps of all CTAs, read from their shared memory
-  int before = 0, all = 0;
-  for (int c = 0; c < kClusterCtas; ++c) {
-    const uint32_t a = ptx::map_to_rank(ptx::smem_addr(s_count + lane), c);
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    all += v;
-    if (c < rank || (c == rank && lane < warp)) before += v;
+// Every warp of the cluster counts its chunks into `counts` (chunk c is warp
+// c % kClusterWarps's).  Visible to the cluster after its next barrier.
+__device__ __forceinline__ void count_chunks(const PagesParams& p, int32_t* counts, int chunks, int gw, int lane) {
+  for (int c = gw; c < chunks; c += kClusterWarps) {
+    const int n = count_live(p, (int64_t)c * kChunk, p.num_pages, lane);
+    if (lane == 0) counts[c] = n;
   }
-  static_assert(kWarps == 32, "one lane per warp");
-  *total = __reduce_add_sync(0xffffffffu, all);
-  return __reduce_add_sync(0xffffffffu, before);
+}
+
+// The whole CTA walks its share of the chunks that `wanted(pages in use before
+// the chunk, first page)` takes; f as for walk, with the pages in use before the
+// page in the whole pool.
+template <class W, class F>
+__device__ __forceinline__ void walk_chunks(const PagesParams& p, const int32_t* counts, int chunks, int gw, int lane,
+                                            int32_t* s_prefix, int32_t* s_warp, W wanted, F f) {
+  const int warp = threadIdx.x >> 5;
+  int before = 0;                                     // pages in use before this batch of chunks
+  for (int c0 = 0; c0 < chunks; c0 += kPlanThreads) {
+    const int c = c0 + threadIdx.x;
+    const int n = c < chunks ? __ldcg(counts + c) : 0;
+    int sum = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += x;
+    }
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    s_prefix[threadIdx.x] = before + sum - n + __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0);
+    before += __reduce_add_sync(0xffffffffu, s_warp[lane]);
+    __syncthreads();
+    const int batch = min(kPlanThreads, chunks - c0);
+    for (int k = (gw - c0 % kClusterWarps + kClusterWarps) % kClusterWarps; k < batch; k += kClusterWarps) {
+      const int live = s_prefix[k];
+      const int64_t base = (int64_t)(c0 + k) * kChunk;
+      if (wanted(live, base)) walk(p, base, lane, [&](int page, int count, int in_chunk) { f(page, count, live + in_chunk); });
+    }
+    __syncthreads();
+  }
+}
+
+// Pages in use in the whole pool: every CTA sums the chunks' counts.
+__device__ __forceinline__ int sum_counts(const int32_t* counts, int chunks, int lane, int32_t* s_warp) {
+  int n = 0;
+  for (int c = threadIdx.x; c < chunks; c += kPlanThreads) n += __ldcg(counts + c);
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) s_warp[threadIdx.x >> 5] = n;
+  __syncthreads();
+  n = __reduce_add_sync(0xffffffffu, s_warp[lane]);
+  __syncthreads();
+  return n;
+}
+
+// Calls f(row, first column, one past the last) for pieces of up to 128 table
+// entries of the rows' ranges [range(row).x, range(row).y), dealt out to the
+// cluster's warps.
+template <class R, class F>
+__device__ __forceinline__ void pieces(const PagesParams& p, int gw, R range, F f) {
+  const int per_row = (p.max_pages + 127) / 128;
+  const int64_t all = (int64_t)p.rows * per_row;
+  for (int64_t i = gw; i < all; i += kClusterWarps) {
+    const int b = (int)(i / per_row), c0 = (int)(i - (int64_t)b * per_row) * 128;
+    const int2 r = range(b);
+    const int from = max(r.x, c0), to = min(r.y, c0 + 128);
+    if (from < to) f(b, from, to);
+  }
 }
 
 // ---------------------------------------------------------------- resize
 // ws: [0] pages needed in all; rows words at kPagesHeader: first needed entry
 // of the row (x 2 + copy-on-write bit); rows words behind: copies before it;
-// num_pages words behind: the free pages taken, in order.
+// num_pages words behind: the free pages taken, in order; then the chunks' counts.
 __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
 pages_resize_kernel(const PagesParams p) {
-  __shared__ int32_t s_count[kWarps];
   __shared__ int32_t s_scan[2][kWarps];
+  __shared__ int32_t s_prefix[kPlanThreads];
   const int rank = (int)ptx::cluster_rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gw = rank * kWarps + warp;
+  const int gw = rank + warp * kClusterCtas;              // neighbouring work on different SMs
   int32_t* off = p.ws + kPagesHeader;
   int32_t* cows = off + p.rows;
   int32_t* list = cows + p.rows;
+  int32_t* counts = list + p.num_pages;
+  const int chunks = (int)(((int64_t)p.num_pages + kChunk - 1) / kChunk);
 
   // 1. what shrinks
   if (rank == 0 && threadIdx.x == 0) *p.move_count = 0;
-  for (int b = gw; b < p.rows; b += kClusterWarps) {
-    bool bad = false;
-    const int co = page_columns(p, __ldg(p.lens + b), &bad), cn = page_columns(p, __ldg(p.new_lens + b), &bad);
-    if (bad) flag(p.err, SMLA_DEVERR_PAGE_STATE);
-    int32_t* row = p.bt + (int64_t)b * p.bt_stride;
-    for (int c = cn + lane; c < co; c += 32) {
-      drop_ref(p, row[c]);
-      row[c] = -1;
-    }
-  }
+  pieces(p, gw,
+         [&](int b) {
+           bool bad = false;
+           const int co = page_columns(p, __ldg(p.lens + b), &bad), cn = page_columns(p, __ldg(p.new_lens + b), &bad);
+           if (bad) flag(p.err, SMLA_DEVERR_PAGE_STATE);
+           return make_int2(cn, co);
+         },
+         [&](int b, int from, int to) {
+           int32_t* row = p.bt + (int64_t)b * p.bt_stride;
+           int page[4];
+#pragma unroll
+           for (int k = 0; k < 4; ++k) {
+             const int c = from + k * 32 + lane;
+             page[k] = c < to ? row[c] : 0;
+           }
+#pragma unroll
+           for (int k = 0; k < 4; ++k) {
+             const int c = from + k * 32 + lane;
+             if (c < to) {
+               drop_ref(p, page[k]);
+               row[c] = -1;
+             }
+           }
+         });
   __threadfence();
   ptx::cluster_sync();
 
   // 2. what the growing rows need, in order of the rows (the first CTA), and
-  // how many pages of each segment are free
+  // how many pages of each chunk are in use
   if (rank == 0) {
     int need0 = 0, cow0 = 0;
     for (int base = 0; base < p.rows; base += kPlanThreads) {
@@ -183,53 +262,67 @@ pages_resize_kernel(const PagesParams p) {
       __syncthreads();
     }
     if (threadIdx.x == 0) p.ws[0] = need0;
-    __threadfence();
   }
-  int begin, end, live_all;
-  segment(p.num_pages, gw, &begin, &end);
-  const int live = live_before(count_live(p.refs, begin, end, lane), rank, warp, lane, s_count, &live_all);
-  const int need_all = __ldcg(p.ws), free_all = p.num_pages - live_all;
-  if (need_all > free_all && rank == 0 && threadIdx.x == 0) flag(p.err, SMLA_DEVERR_OUT_OF_PAGES);
-
-  // 3. the lowest free pages, in order
-  const int take = min(need_all, free_all);
-  const int rank0 = begin - live;                         // free pages before the segment
-  if (rank0 < take) {
-    walk(p.refs, begin, end, lane, [&](int page, int count, int live_in_segment) {
-      const int k = rank0 + (page - begin) - live_in_segment;
-      if (count <= 0 && k < take) {
-        list[k] = page;
-        p.refs[page] = 1;
-      }
-    });
-  }
+  count_chunks(p, counts, chunks, gw, lane);
   __threadfence();
   ptx::cluster_sync();
 
-  // 4. handed out
-  for (int b = gw; b < p.rows; b += kClusterWarps) {
-    bool bad = false;
-    const int old = clamped_len(p, __ldg(p.lens + b)), now = clamped_len(p, __ldg(p.new_lens + b));
-    if (now <= old) continue;
-    const int co = page_columns(p, old, &bad), cn = page_columns(p, now, &bad);
-    const int o = __ldcg(off + b), cow = o & 1;
-    int k = o >> 1;
-    int32_t* row = p.bt + (int64_t)b * p.bt_stride;
-    if (cow) {
-      if (lane == 0 && k < take) {
-        const int from = __ldcg(row + old / p.page_size), to = __ldcg(list + k);
-        row[old / p.page_size] = to;
-        atomicSub(p.refs + from, 1);
-        const int m = __ldcg(cows + b);
-        p.move_src[m] = from;
-        p.move_dst[m] = to;
-        atomicMax(p.move_count, m + 1);                   // the rows that got a page are the first ones
-      }
-      ++k;
-    }
-    for (int c = co + lane; c < cn; c += 32) {
-      const int i = k + (c - co);
-      row[c] = i < take ? __ldcg(list + i) : -1;
+  // 3. the lowest free pages, in order
+  const int need_all = __ldcg(p.ws);
+  int take = 0;
+  if (need_all > 0) {
+    const int free_all = p.num_pages - sum_counts(counts, chunks, lane, s_scan[0]);
+    if (need_all > free_all && rank == 0 && threadIdx.x == 0) flag(p.err, SMLA_DEVERR_OUT_OF_PAGES);
+    take = min(need_all, free_all);
+    walk_chunks(p, counts, chunks, gw, lane, s_prefix, s_scan[0],
+                [&](int live, int64_t base) { return base - live < take; },   // free pages before the chunk
+                [&](int page, int count, int live) {
+                  const int k = page - live;
+                  if (count <= 0 && k < take) {
+                    list[k] = page;
+                    p.refs[page] = 1;
+                  }
+                });
+    __threadfence();
+  }
+  ptx::cluster_sync();
+  if (need_all == 0) return;
+
+  // 4. handed out: the pages of growing rows, a piece's first column giving the row's rank
+  pieces(p, gw,
+         [&](int b) {
+           bool bad = false;
+           const int old = clamped_len(p, __ldg(p.lens + b)), now = clamped_len(p, __ldg(p.new_lens + b));
+           return now > old ? make_int2(page_columns(p, old, &bad), page_columns(p, now, &bad)) : make_int2(0, 0);
+         },
+         [&](int b, int from, int to) {
+           bool bad = false;
+           const int co = page_columns(p, clamped_len(p, __ldg(p.lens + b)), &bad);
+           const int o = __ldcg(off + b), k0 = (o >> 1) + (o & 1) - co;
+           int32_t* row = p.bt + (int64_t)b * p.bt_stride;
+           int page[4];
+#pragma unroll
+           for (int k = 0; k < 4; ++k) {
+             const int c = from + k * 32 + lane;
+             page[k] = c < to && k0 + c < take ? __ldcg(list + k0 + c) : -1;
+           }
+#pragma unroll
+           for (int k = 0; k < 4; ++k) {
+             const int c = from + k * 32 + lane;
+             if (c < to) row[c] = page[k];
+           }
+         });
+  // and the copies of shared pages
+  for (int b = rank * kPlanThreads + threadIdx.x; b < p.rows; b += kClusterCtas * kPlanThreads) {
+    const int o = __ldcg(off + b), k = o >> 1;
+    if ((o & 1) != 0 && k < take) {
+      int32_t* at = p.bt + (int64_t)b * p.bt_stride + clamped_len(p, __ldg(p.lens + b)) / p.page_size;
+      const int from = __ldcg(at), to = __ldcg(list + k), m = __ldcg(cows + b);
+      *at = to;
+      atomicSub(p.refs + from, 1);
+      p.move_src[m] = from;
+      p.move_dst[m] = to;
+      atomicMax(p.move_count, m + 1);                     // the rows that got a page are the first ones
     }
   }
 }
@@ -264,36 +357,41 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(const PagesParams p) {
 
 // --------------------------------------------------------------- compact
 // ws: [0] pages in use n, [1] pages in use before page n; num_pages words at
-// kPagesHeader: the move of each page in use at or past n.
+// kPagesHeader: the move of each page in use at or past n; then the chunks' counts.
 __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
 pages_compact_kernel(const PagesParams p) {
-  __shared__ int32_t s_count[kWarps];
+  __shared__ int32_t s_warp[kWarps];
+  __shared__ int32_t s_prefix[kPlanThreads];
   const int rank = (int)ptx::cluster_rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gw = rank + warp * kClusterCtas;
   int32_t* move_of = p.ws + kPagesHeader;
-  int begin, end, n;
-  segment(p.num_pages, rank * kWarps + warp, &begin, &end);
-  const int live = live_before(count_live(p.refs, begin, end, lane), rank, warp, lane, s_count, &n);
-  // the pages in use before page n: counted by the warp whose segment n ends or lies in
-  if ((n > begin && n <= end) || (n == 0 && rank == 0 && warp == 0)) {
-    const int low = n == 0 ? 0 : live + count_live(p.refs, begin, n, lane);
-    if (lane == 0) {
-      p.ws[0] = n;
-      p.ws[1] = low;
-      *p.move_count = n - low;
-    }
-  }
+  int32_t* counts = move_of + p.num_pages;
+  const int chunks = (int)(((int64_t)p.num_pages + kChunk - 1) / kChunk);
+  count_chunks(p, counts, chunks, gw, lane);
   __threadfence();
   ptx::cluster_sync();
-  const int low = __ldcg(p.ws + 1), moves = n - low;
-  walk(p.refs, begin, end, lane, [&](int page, int count, int live_in_segment) {
-    const int l = live + live_in_segment;                 // pages in use before this one
-    if (count <= 0 && page < n) {
-      p.move_dst[page - l] = page;
-    } else if (count > 0 && page >= n) {
-      p.move_src[l - low] = page;
-      move_of[page] = l - low;
-    }
-  });
+  const int n = sum_counts(counts, chunks, lane, s_warp);
+  // pages in use before page n: the chunks before its own, and those before it there
+  const int own = n / kChunk;
+  int low = sum_counts(counts, min(own, chunks), lane, s_warp);
+  if (own < chunks) low += count_live(p, (int64_t)own * kChunk, n, lane);
+  const int moves = n - low;
+  if (rank == 0 && threadIdx.x == 0) {
+    p.ws[0] = n;
+    p.ws[1] = low;
+    *p.move_count = moves;
+  }
+  if (moves > 0)
+    walk_chunks(p, counts, chunks, gw, lane, s_prefix, s_warp,
+                [&](int live, int64_t base) { return base < n || live < n; },
+                [&](int page, int count, int live) {      // live: pages in use before this one
+                  if (count <= 0 && page < n) {
+                    p.move_dst[page - live] = page;
+                  } else if (count > 0 && page >= n) {
+                    p.move_src[live - low] = page;
+                    move_of[page] = live - low;
+                  }
+                });
   __threadfence();
   ptx::cluster_sync();
   for (int k = (rank * kPlanThreads) + threadIdx.x; k < moves; k += kClusterCtas * kPlanThreads) {

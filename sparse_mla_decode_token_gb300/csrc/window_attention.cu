@@ -130,26 +130,8 @@ __device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lan
   u.t = x / p.num_splits;
   u.heads = min(kNH, p.H - u.h0);
   int first, count;
-  if (c.cum != nullptr) {
-    // the request is the number of ends cum[1 .. B - 1] at or before the token: 32 looks at a time
-    int lo = 0, n = c.batch - 1;                  // among ends lo + 1 .. lo + n
-    while (n > 0) {
-      const int step = (n + 31) / 32, at = lo + min(n, (lane + 1) * step);
-      const int hits = __popc(__ballot_sync(0xffffffffu, __ldg(c.cum + at) <= u.t));
-      // (the last lanes look at the same end: their hits count once the whole range is before the token)
-      const int passed = min(n, hits * step);
-      if (hits == 32) {
-        lo += n;
-        n = 0;
-      } else {
-        lo += passed;
-        n = min(n - passed, step - 1);
-      }
-    }
-    u.b = lo;
-  } else {
-    u.b = u.t / (c.sum_q / c.batch);
-  }
+  u.b = c.cum != nullptr ? last_request(c.batch, lane, [&](int b) { return __ldg(c.cum + b) <= u.t; })
+                         : u.t / (c.sum_q / c.batch);
   request_tokens(c, u.b, &first, &count);
   u.pos = __ldg(c.seq_lens + u.b) - count + (u.t - first);
   u.lo = (int)max((int64_t)u.pos - p.window + 1, (int64_t)0);

@@ -95,15 +95,15 @@ struct PagesParams {
 };
 
 // Workspace words of resize and compact: a header, per-row words (resize),
-// per-page words, a count per 1024 pages.
+// per-page words, a count per 512 pages.
 constexpr int kPagesHeader = 64;
 inline int64_t pages_workspace_words(int64_t rows, int64_t num_pages) {
-  return kPagesHeader + 2 * rows + num_pages + (num_pages + 1023) / 1024;
+  return kPagesHeader + 2 * rows + num_pages + (num_pages + 511) / 512;
 }
 
-cudaError_t launch_pages_resize(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_resize(const PagesParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream);
-cudaError_t launch_pages_compact(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t stream);
 
 constexpr int kCopyPools = 64;        // pools of one copy launch (kernel parameters)
 struct CopyParams {

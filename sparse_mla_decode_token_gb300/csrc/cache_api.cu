@@ -340,7 +340,9 @@ smla_status smla_pages_resize(const smla_pages_args* a, void* stream) {
   SMLA_TRY(check_page_pointers(a));
   SMLA_TRY(need_words("new_lens", a->new_lens, true));
   SMLA_TRY(check_moves(a, a->rows));
-  return launched("pages resize", launch_pages_resize(pages_params(a), static_cast<cudaStream_t>(stream)));
+  int sms = 0;
+  SMLA_TRY(current_sms(&sms));
+  return launched("pages resize", launch_pages_resize(pages_params(a), sms, static_cast<cudaStream_t>(stream)));
 }
 
 smla_status smla_pages_fork(const smla_pages_args* a, void* stream) {
@@ -358,7 +360,9 @@ smla_status smla_pages_compact(const smla_pages_args* a, void* stream) {
   if (a->rows == 0) return SMLA_OK;
   SMLA_TRY(check_page_pointers(a));
   SMLA_TRY(check_moves(a, a->num_pages / 2));
-  return launched("pages compact", launch_pages_compact(pages_params(a), static_cast<cudaStream_t>(stream)));
+  int sms = 0;
+  SMLA_TRY(current_sms(&sms));
+  return launched("pages compact", launch_pages_compact(pages_params(a), sms, static_cast<cudaStream_t>(stream)));
 }
 
 smla_status smla_pages_copy(const smla_pool* pools, int32_t num_pools, int64_t num_pages, const int32_t* move_src,

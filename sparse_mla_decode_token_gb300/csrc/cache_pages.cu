@@ -3,14 +3,20 @@
 //
 // The state is a count per page (a page with count 0 is free) and a table row
 // per request.  Ranking the free (or live) pages in order is a prefix sum over
-// the counts: resize and compact run it inside one cluster of CTAs, so that a
-// call is one launch (two for compact) with cluster barriers in between, and
-// every page's rank, hence who gets it, depends on nothing but the state.
-// Pages are counted in chunks of 1024, a warp per chunk, the chunks dealt out
-// to all warps of the cluster in turn (those that hold the lowest free pages
-// would otherwise be one CTA's); each CTA then sums the chunks' counts itself.
-// What bounds the calls is latency: the counts (4 bytes a page) are read once,
-// and again where pages are handed out; the rest is a few dependent trips to L2.
+// the counts, so every page's rank, hence who gets it, depends on nothing but
+// the state.  Pages are counted in chunks of 512, a warp per chunk, the chunks
+// dealt out to all warps in turn (those that hold the lowest free pages would
+// otherwise be one CTA's); each CTA then sums the chunks' counts itself.
+//
+// A call is a few phases, each needing all of the one before.  Small calls run
+// them in one launch, in one cluster of eight CTAs with cluster barriers between
+// (resize of 128 requests x 128 pages in a pool of 16 thousand: 13 us, of which
+// no phase is more than 4); where tables and pool together pass
+// kClusterEntries, eight SMs are too few and the phases are launches of their
+// own over the whole GPU, each overlapping its start with the end of the one
+// before (1024 requests x 1024 pages in a pool of a million: 71 us in a cluster).
+// What bounds both is latency: the counts (4 bytes a page) are read once, and
+// again where pages are handed out; the rest is dependent trips to L2.
 #include "cache.cuh"
 #include "tc_ptx.cuh"
 
@@ -20,7 +26,7 @@ namespace {
 constexpr int kClusterCtas = 8;                       // portable cluster size
 constexpr int kPlanThreads = 1024;
 constexpr int kWarps = kPlanThreads / 32;
-constexpr int kClusterWarps = kClusterCtas * kWarps;
+constexpr int64_t kClusterEntries = 1 << 17;           // table entries + pages that one cluster takes
 
 __device__ __forceinline__ void flag(int32_t* err, int bit) {
   if (err != nullptr) atomicOr(err, bit);
@@ -51,7 +57,7 @@ __device__ __forceinline__ void drop_ref(const PagesParams& p, int page) {
   }
 }
 
-constexpr int kChunk = 1024;                          // pages a warp counts at a time: 8 x 4 a lane
+constexpr int kChunk = 512;                           // pages a warp counts at a time: 4 x 4 a lane
 
 // Counts of pages [4 i, 4 i + 3] past `base` (pages past the pool: `pad`).
 __device__ __forceinline__ int4 load_counts(const PagesParams& p, int64_t base, int i, int pad) {
@@ -110,10 +116,24 @@ __device__ __forceinline__ void walk(const PagesParams& p, int64_t base, int lan
   }
 }
 
-// Every warp of the cluster counts its chunks into `counts` (chunk c is warp
-// c % kClusterWarps's).  Visible to the cluster after its next barrier.
-__device__ __forceinline__ void count_chunks(const PagesParams& p, int32_t* counts, int chunks, int gw, int lane) {
-  for (int c = gw; c < chunks; c += kClusterWarps) {
+// Who works: warp gw of `warps`, in CTA `cta` of `ctas`; neighbouring work goes
+// to different SMs.
+struct Team {
+  int cta, ctas, gw, warps, lane;
+};
+__device__ __forceinline__ Team team(int cta, int ctas) {
+  return {cta, ctas, cta + (int)(threadIdx.x >> 5) * ctas, ctas * kWarps, (int)(threadIdx.x & 31)};
+}
+
+struct Shared {
+  int32_t scan[2][kWarps];
+  int32_t prefix[kPlanThreads];
+};
+
+// Counts the pages in use of each chunk (chunk c is warp c % warps's).
+__device__ __forceinline__ void count_chunks(const PagesParams& p, int32_t* counts, int chunks, const Team& w) {
+  const int lane = w.lane;
+  for (int c = w.gw; c < chunks; c += w.warps) {
     const int n = count_live(p, (int64_t)c * kChunk, p.num_pages, lane);
     if (lane == 0) counts[c] = n;
   }
@@ -123,9 +143,11 @@ __device__ __forceinline__ void count_chunks(const PagesParams& p, int32_t* coun
 // the chunk, first page)` takes; f as for walk, with the pages in use before the
 // page in the whole pool.
 template <class W, class F>
-__device__ __forceinline__ void walk_chunks(const PagesParams& p, const int32_t* counts, int chunks, int gw, int lane,
-                                            int32_t* s_prefix, int32_t* s_warp, W wanted, F f) {
-  const int warp = threadIdx.x >> 5;
+__device__ __forceinline__ void walk_chunks(const PagesParams& p, const int32_t* counts, int chunks, const Team& w,
+                                            Shared& sh, W wanted, F f) {
+  const int warp = threadIdx.x >> 5, lane = w.lane;
+  int32_t* s_warp = sh.scan[0];
+  int32_t* s_prefix = sh.prefix;
   int before = 0;                                     // pages in use before this batch of chunks
   for (int c0 = 0; c0 < chunks; c0 += kPlanThreads) {
     const int c = c0 + threadIdx.x;
@@ -142,7 +164,7 @@ __device__ __forceinline__ void walk_chunks(const PagesParams& p, const int32_t*
     before += __reduce_add_sync(0xffffffffu, s_warp[lane]);
     __syncthreads();
     const int batch = min(kPlanThreads, chunks - c0);
-    for (int k = (gw - c0 % kClusterWarps + kClusterWarps) % kClusterWarps; k < batch; k += kClusterWarps) {
+    for (int k = (w.gw - c0 % w.warps + w.warps) % w.warps; k < batch; k += w.warps) {
       const int live = s_prefix[k];
       const int64_t base = (int64_t)(c0 + k) * kChunk;
       if (wanted(live, base)) walk(p, base, lane, [&](int page, int count, int in_chunk) { f(page, count, live + in_chunk); });
@@ -152,7 +174,9 @@ __device__ __forceinline__ void walk_chunks(const PagesParams& p, const int32_t*
 }
 
 // Pages in use in the whole pool: every CTA sums the chunks' counts.
-__device__ __forceinline__ int sum_counts(const int32_t* counts, int chunks, int lane, int32_t* s_warp) {
+__device__ __forceinline__ int sum_counts(const int32_t* counts, int chunks, Shared& sh) {
+  const int lane = threadIdx.x & 31;
+  int32_t* s_warp = sh.scan[0];
   int n = 0;
   for (int c = threadIdx.x; c < chunks; c += kPlanThreads) n += __ldcg(counts + c);
   n = __reduce_add_sync(0xffffffffu, n);
@@ -164,13 +188,12 @@ __device__ __forceinline__ int sum_counts(const int32_t* counts, int chunks, int
 }
 
 // Calls f(row, first column, one past the last) for pieces of up to 128 table
-// entries of the rows' ranges [range(row).x, range(row).y), dealt out to the
-// cluster's warps.
+// entries of the rows' ranges [range(row).x, range(row).y), dealt out to the warps.
 template <class R, class F>
-__device__ __forceinline__ void pieces(const PagesParams& p, int gw, R range, F f) {
+__device__ __forceinline__ void pieces(const PagesParams& p, const Team& w, R range, F f) {
   const int per_row = (p.max_pages + 127) / 128;
   const int64_t all = (int64_t)p.rows * per_row;
-  for (int64_t i = gw; i < all; i += kClusterWarps) {
+  for (int64_t i = w.gw; i < all; i += w.warps) {
     const int b = (int)(i / per_row), c0 = (int)(i - (int64_t)b * per_row) * 128;
     const int2 r = range(b);
     const int from = max(r.x, c0), to = min(r.y, c0 + 128);
@@ -182,21 +205,24 @@ __device__ __forceinline__ void pieces(const PagesParams& p, int gw, R range, F 
 // ws: [0] pages needed in all; rows words at kPagesHeader: first needed entry
 // of the row (x 2 + copy-on-write bit); rows words behind: copies before it;
 // num_pages words behind: the free pages taken, in order; then the chunks' counts.
-__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
-pages_resize_kernel(const PagesParams p) {
-  __shared__ int32_t s_scan[2][kWarps];
-  __shared__ int32_t s_prefix[kPlanThreads];
-  const int rank = (int)ptx::cluster_rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gw = rank + warp * kClusterCtas;              // neighbouring work on different SMs
-  int32_t* off = p.ws + kPagesHeader;
-  int32_t* cows = off + p.rows;
-  int32_t* list = cows + p.rows;
-  int32_t* counts = list + p.num_pages;
-  const int chunks = (int)(((int64_t)p.num_pages + kChunk - 1) / kChunk);
+struct Resize {
+  int32_t *off, *cows, *list, *counts;
+  int chunks;
+};
+__device__ __forceinline__ Resize resize_state(const PagesParams& p) {
+  Resize r;
+  r.off = p.ws + kPagesHeader;
+  r.cows = r.off + p.rows;
+  r.list = r.cows + p.rows;
+  r.counts = r.list + p.num_pages;
+  r.chunks = (int)(((int64_t)p.num_pages + kChunk - 1) / kChunk);
+  return r;
+}
 
-  // 1. what shrinks
-  if (rank == 0 && threadIdx.x == 0) *p.move_count = 0;
-  pieces(p, gw,
+// 1. what shrinks
+__device__ __forceinline__ void resize_drop(const PagesParams& p, const Team& w) {
+  if (w.cta == 0 && threadIdx.x == 0) *p.move_count = 0;
+  pieces(p, w,
          [&](int b) {
            bool bad = false;
            const int co = page_columns(p, __ldg(p.lens + b), &bad), cn = page_columns(p, __ldg(p.new_lens + b), &bad);
@@ -208,88 +234,88 @@ pages_resize_kernel(const PagesParams p) {
            int page[4];
 #pragma unroll
            for (int k = 0; k < 4; ++k) {
-             const int c = from + k * 32 + lane;
+             const int c = from + k * 32 + w.lane;
              page[k] = c < to ? row[c] : 0;
            }
 #pragma unroll
            for (int k = 0; k < 4; ++k) {
-             const int c = from + k * 32 + lane;
+             const int c = from + k * 32 + w.lane;
              if (c < to) {
                drop_ref(p, page[k]);
                row[c] = -1;
              }
            }
          });
-  __threadfence();
-  ptx::cluster_sync();
+}
 
-  // 2. what the growing rows need, in order of the rows (the first CTA), and
-  // how many pages of each chunk are in use
-  if (rank == 0) {
-    int need0 = 0, cow0 = 0;
-    for (int base = 0; base < p.rows; base += kPlanThreads) {
-      const int b = base + threadIdx.x;
-      int need = 0, cow = 0;
-      if (b < p.rows) {
-        bool bad = false;
-        const int old = clamped_len(p, __ldg(p.lens + b)), now = clamped_len(p, __ldg(p.new_lens + b));
-        if (now > old) {
-          need = page_columns(p, now, &bad) - page_columns(p, old, &bad);
-          if (old % p.page_size != 0) {
-            const int page = __ldcg(p.bt + (int64_t)b * p.bt_stride + old / p.page_size);
-            if (in_pool(p, page)) cow = __ldcg(p.refs + page) > 1;
-            else flag(p.err, SMLA_DEVERR_PAGE_STATE);
-          }
-          need += cow;
+// 2. what the growing rows need, in order of the rows (one CTA)
+__device__ __forceinline__ void resize_rows(const PagesParams& p, const Resize& r, Shared& sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int need0 = 0, cow0 = 0;
+  for (int base = 0; base < p.rows; base += kPlanThreads) {
+    const int b = base + threadIdx.x;
+    int need = 0, cow = 0;
+    if (b < p.rows) {
+      bool bad = false;
+      const int old = clamped_len(p, __ldg(p.lens + b)), now = clamped_len(p, __ldg(p.new_lens + b));
+      if (now > old) {
+        need = page_columns(p, now, &bad) - page_columns(p, old, &bad);
+        if (old % p.page_size != 0) {
+          const int page = __ldcg(p.bt + (int64_t)b * p.bt_stride + old / p.page_size);
+          if (in_pool(p, page)) cow = __ldcg(p.refs + page) > 1;
+          else flag(p.err, SMLA_DEVERR_PAGE_STATE);
         }
+        need += cow;
       }
-      int sn = need, sc = cow;                            // inclusive sums over the block
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, sn, d), y = __shfl_up_sync(0xffffffffu, sc, d);
-        if (lane >= d) sn += x, sc += y;
-      }
-      if (lane == 31) s_scan[0][warp] = sn, s_scan[1][warp] = sc;
-      __syncthreads();
-      const int wn = __reduce_add_sync(0xffffffffu, lane < warp ? s_scan[0][lane] : 0);
-      const int wc = __reduce_add_sync(0xffffffffu, lane < warp ? s_scan[1][lane] : 0);
-      if (b < p.rows) {
-        off[b] = 2 * (need0 + wn + sn - need) + cow;
-        cows[b] = cow0 + wc + sc - cow;
-      }
-      need0 += __reduce_add_sync(0xffffffffu, s_scan[0][lane]);
-      cow0 += __reduce_add_sync(0xffffffffu, s_scan[1][lane]);
-      __syncthreads();
     }
-    if (threadIdx.x == 0) p.ws[0] = need0;
+    int sn = need, sc = cow;                              // inclusive sums over the block
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sn, d), y = __shfl_up_sync(0xffffffffu, sc, d);
+      if (lane >= d) sn += x, sc += y;
+    }
+    if (lane == 31) sh.scan[0][warp] = sn, sh.scan[1][warp] = sc;
+    __syncthreads();
+    const int wn = __reduce_add_sync(0xffffffffu, lane < warp ? sh.scan[0][lane] : 0);
+    const int wc = __reduce_add_sync(0xffffffffu, lane < warp ? sh.scan[1][lane] : 0);
+    if (b < p.rows) {
+      r.off[b] = 2 * (need0 + wn + sn - need) + cow;
+      r.cows[b] = cow0 + wc + sc - cow;
+    }
+    need0 += __reduce_add_sync(0xffffffffu, sh.scan[0][lane]);
+    cow0 += __reduce_add_sync(0xffffffffu, sh.scan[1][lane]);
+    __syncthreads();
   }
-  count_chunks(p, counts, chunks, gw, lane);
-  __threadfence();
-  ptx::cluster_sync();
+  if (threadIdx.x == 0) p.ws[0] = need0;
+}
 
-  // 3. the lowest free pages, in order
-  const int need_all = __ldcg(p.ws);
-  int take = 0;
-  if (need_all > 0) {
-    const int free_all = p.num_pages - sum_counts(counts, chunks, lane, s_scan[0]);
-    if (need_all > free_all && rank == 0 && threadIdx.x == 0) flag(p.err, SMLA_DEVERR_OUT_OF_PAGES);
-    take = min(need_all, free_all);
-    walk_chunks(p, counts, chunks, gw, lane, s_prefix, s_scan[0],
-                [&](int live, int64_t base) { return base - live < take; },   // free pages before the chunk
-                [&](int page, int count, int live) {
-                  const int k = page - live;
-                  if (count <= 0 && k < take) {
-                    list[k] = page;
-                    p.refs[page] = 1;
-                  }
-                });
-    __threadfence();
-  }
-  ptx::cluster_sync();
-  if (need_all == 0) return;
+// Pages that can be handed out: the smaller of what is needed and what is free.
+__device__ __forceinline__ int resize_take(const PagesParams& p, const Resize& r, const Team& w, Shared& sh) {
+  const int need = __ldcg(p.ws);
+  if (need == 0) return 0;
+  const int have = p.num_pages - sum_counts(r.counts, r.chunks, sh);
+  if (need > have && w.cta == 0 && threadIdx.x == 0) flag(p.err, SMLA_DEVERR_OUT_OF_PAGES);
+  return min(need, have);
+}
 
-  // 4. handed out: the pages of growing rows, a piece's first column giving the row's rank
-  pieces(p, gw,
+// 3. the lowest free pages, in order
+__device__ __forceinline__ void resize_list(const PagesParams& p, const Resize& r, const Team& w, Shared& sh, int take) {
+  if (take == 0) return;
+  walk_chunks(p, r.counts, r.chunks, w, sh,
+              [&](int live, int64_t base) { return base - live < take; },     // free pages before the chunk
+              [&](int page, int count, int live) {
+                const int k = page - live;
+                if (count <= 0 && k < take) {
+                  r.list[k] = page;
+                  p.refs[page] = 1;
+                }
+              });
+}
+
+// 4. handed out: the pages of growing rows, then the copies of shared pages
+__device__ __forceinline__ void resize_assign(const PagesParams& p, const Resize& r, const Team& w, int take) {
+  if (__ldcg(p.ws) == 0) return;
+  pieces(p, w,
          [&](int b) {
            bool bad = false;
            const int old = clamped_len(p, __ldg(p.lens + b)), now = clamped_len(p, __ldg(p.new_lens + b));
@@ -298,32 +324,72 @@ pages_resize_kernel(const PagesParams p) {
          [&](int b, int from, int to) {
            bool bad = false;
            const int co = page_columns(p, clamped_len(p, __ldg(p.lens + b)), &bad);
-           const int o = __ldcg(off + b), k0 = (o >> 1) + (o & 1) - co;
+           const int o = __ldcg(r.off + b), k0 = (o >> 1) + (o & 1) - co;     // rank of column 0, as it were
            int32_t* row = p.bt + (int64_t)b * p.bt_stride;
            int page[4];
 #pragma unroll
            for (int k = 0; k < 4; ++k) {
-             const int c = from + k * 32 + lane;
-             page[k] = c < to && k0 + c < take ? __ldcg(list + k0 + c) : -1;
+             const int c = from + k * 32 + w.lane;
+             page[k] = c < to && k0 + c < take ? __ldcg(r.list + k0 + c) : -1;
            }
 #pragma unroll
            for (int k = 0; k < 4; ++k) {
-             const int c = from + k * 32 + lane;
+             const int c = from + k * 32 + w.lane;
              if (c < to) row[c] = page[k];
            }
          });
-  // and the copies of shared pages
-  for (int b = rank * kPlanThreads + threadIdx.x; b < p.rows; b += kClusterCtas * kPlanThreads) {
-    const int o = __ldcg(off + b), k = o >> 1;
+  for (int b = w.cta * kPlanThreads + threadIdx.x; b < p.rows; b += w.ctas * kPlanThreads) {
+    const int o = __ldcg(r.off + b), k = o >> 1;
     if ((o & 1) != 0 && k < take) {
       int32_t* at = p.bt + (int64_t)b * p.bt_stride + clamped_len(p, __ldg(p.lens + b)) / p.page_size;
-      const int from = __ldcg(at), to = __ldcg(list + k), m = __ldcg(cows + b);
+      const int from = __ldcg(at), to = __ldcg(r.list + k), m = __ldcg(r.cows + b);
       *at = to;
       atomicSub(p.refs + from, 1);
       p.move_src[m] = from;
       p.move_dst[m] = to;
       atomicMax(p.move_count, m + 1);                     // the rows that got a page are the first ones
     }
+  }
+}
+
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
+pages_resize_kernel(const PagesParams p) {
+  __shared__ Shared sh;
+  const Team w = team((int)ptx::cluster_rank(), kClusterCtas);
+  const Resize r = resize_state(p);
+  resize_drop(p, w);
+  __threadfence();
+  ptx::cluster_sync();
+  if (w.cta == 0) resize_rows(p, r, sh);
+  count_chunks(p, r.counts, r.chunks, w);
+  __threadfence();
+  ptx::cluster_sync();
+  const int take = resize_take(p, r, w, sh);
+  resize_list(p, r, w, sh, take);
+  __threadfence();
+  ptx::cluster_sync();
+  resize_assign(p, r, w, take);
+}
+
+// The same phases as launches over the whole GPU (kPhase 0 .. 3).
+template <int kPhase>
+__global__ void __launch_bounds__(kPlanThreads, 1) pages_resize_phase_kernel(const PagesParams p) {
+  __shared__ Shared sh;
+  const Team w = team(blockIdx.x, gridDim.x);
+  const Resize r = resize_state(p);
+  if constexpr (kPhase > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (kPhase < 3) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (kPhase == 0) {
+    resize_drop(p, w);
+  } else if constexpr (kPhase == 1) {
+    if (w.cta == 0) resize_rows(p, r, sh);
+    count_chunks(p, r.counts, r.chunks, w);
+  } else if constexpr (kPhase == 2) {
+    const int take = resize_take(p, r, w, sh);
+    if (w.cta == 0 && threadIdx.x == 0) p.ws[1] = take;
+    resize_list(p, r, w, sh, take);
+  } else {
+    resize_assign(p, r, w, __ldcg(p.ws + 1));
   }
 }
 
@@ -358,47 +424,78 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(const PagesParams p) {
 // --------------------------------------------------------------- compact
 // ws: [0] pages in use n, [1] pages in use before page n; num_pages words at
 // kPagesHeader: the move of each page in use at or past n; then the chunks' counts.
-__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
-pages_compact_kernel(const PagesParams p) {
-  __shared__ int32_t s_warp[kWarps];
-  __shared__ int32_t s_prefix[kPlanThreads];
-  const int rank = (int)ptx::cluster_rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gw = rank + warp * kClusterCtas;
-  int32_t* move_of = p.ws + kPagesHeader;
-  int32_t* counts = move_of + p.num_pages;
-  const int chunks = (int)(((int64_t)p.num_pages + kChunk - 1) / kChunk);
-  count_chunks(p, counts, chunks, gw, lane);
-  __threadfence();
-  ptx::cluster_sync();
-  const int n = sum_counts(counts, chunks, lane, s_warp);
+struct Compact {
+  int32_t *move_of, *counts;
+  int chunks;
+};
+__device__ __forceinline__ Compact compact_state(const PagesParams& p) {
+  Compact c;
+  c.move_of = p.ws + kPagesHeader;
+  c.counts = c.move_of + p.num_pages;
+  c.chunks = (int)(((int64_t)p.num_pages + kChunk - 1) / kChunk);
+  return c;
+}
+
+// The moves, from the chunks' counts; returns how many.
+__device__ __forceinline__ int compact_moves(const PagesParams& p, const Compact& c, const Team& w, Shared& sh) {
+  const int n = sum_counts(c.counts, c.chunks, sh);
   // pages in use before page n: the chunks before its own, and those before it there
   const int own = n / kChunk;
-  int low = sum_counts(counts, min(own, chunks), lane, s_warp);
-  if (own < chunks) low += count_live(p, (int64_t)own * kChunk, n, lane);
-  const int moves = n - low;
-  if (rank == 0 && threadIdx.x == 0) {
+  int low = sum_counts(c.counts, min(own, c.chunks), sh);
+  if (own < c.chunks) low += count_live(p, (int64_t)own * kChunk, n, w.lane);
+  if (w.cta == 0 && threadIdx.x == 0) {
     p.ws[0] = n;
     p.ws[1] = low;
-    *p.move_count = moves;
+    *p.move_count = n - low;
   }
-  if (moves > 0)
-    walk_chunks(p, counts, chunks, gw, lane, s_prefix, s_warp,
+  if (n > low)
+    walk_chunks(p, c.counts, c.chunks, w, sh,
                 [&](int live, int64_t base) { return base < n || live < n; },
                 [&](int page, int count, int live) {      // live: pages in use before this one
                   if (count <= 0 && page < n) {
                     p.move_dst[page - live] = page;
                   } else if (count > 0 && page >= n) {
                     p.move_src[live - low] = page;
-                    move_of[page] = live - low;
+                    c.move_of[page] = live - low;
                   }
                 });
-  __threadfence();
-  ptx::cluster_sync();
-  for (int k = (rank * kPlanThreads) + threadIdx.x; k < moves; k += kClusterCtas * kPlanThreads) {
+  return n - low;
+}
+
+__device__ __forceinline__ void compact_counts(const PagesParams& p, const Team& w, int moves) {
+  for (int k = w.cta * kPlanThreads + threadIdx.x; k < moves; k += w.ctas * kPlanThreads) {
     const int from = __ldcg(p.move_src + k), to = __ldcg(p.move_dst + k);
     p.refs[to] = __ldcg(p.refs + from);
     p.refs[from] = 0;
   }
+}
+
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
+pages_compact_kernel(const PagesParams p) {
+  __shared__ Shared sh;
+  const Team w = team((int)ptx::cluster_rank(), kClusterCtas);
+  const Compact c = compact_state(p);
+  count_chunks(p, c.counts, c.chunks, w);
+  __threadfence();
+  ptx::cluster_sync();
+  const int moves = compact_moves(p, c, w, sh);
+  __threadfence();
+  ptx::cluster_sync();
+  compact_counts(p, w, moves);
+}
+
+// The same phases as launches over the whole GPU (kPhase 0 .. 2; the counts may
+// move only when nobody ranks them any more).
+template <int kPhase>
+__global__ void __launch_bounds__(kPlanThreads, 1) pages_compact_phase_kernel(const PagesParams p) {
+  __shared__ Shared sh;
+  const Team w = team(blockIdx.x, gridDim.x);
+  const Compact c = compact_state(p);
+  if constexpr (kPhase > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (kPhase < 2) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (kPhase == 0) count_chunks(p, c.counts, c.chunks, w);
+  else if constexpr (kPhase == 1) compact_moves(p, c, w, sh);
+  else compact_counts(p, w, __ldcg(p.ws) - __ldcg(p.ws + 1));
 }
 
 // Renumbers the tables after the moves are known: one warp per 32 columns of a row.
@@ -475,9 +572,44 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
 
 }  // namespace
 
-cudaError_t launch_pages_resize(const PagesParams& p, cudaStream_t stream) {
-  pages_resize_kernel<<<kClusterCtas, kPlanThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+namespace {
+
+bool one_cluster(const PagesParams& p) { return (int64_t)p.rows * p.max_pages + p.num_pages <= kClusterEntries; }
+
+// CTAs of a phase over the whole GPU: one an SM, no more than there is work for.
+int phase_ctas(int64_t warps, int sms) {
+  const int64_t n = (warps + kWarps - 1) / kWarps;
+  return (int)(n < 1 ? 1 : n < sms ? n : sms);
+}
+
+template <class K>
+cudaError_t launch_phase(K kernel, int ctas, bool dependent, const PagesParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_pages_resize(const PagesParams& p, int sms, cudaStream_t stream) {
+  if (one_cluster(p)) {
+    pages_resize_kernel<<<kClusterCtas, kPlanThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
+  const int tables = phase_ctas((int64_t)p.rows * ((p.max_pages + 127) / 128), sms);
+  const int pages = phase_ctas(((int64_t)p.num_pages + kChunk - 1) / kChunk, sms);
+  cudaError_t e = launch_phase(pages_resize_phase_kernel<0>, tables, false, p, stream);
+  if (e == cudaSuccess) e = launch_phase(pages_resize_phase_kernel<1>, pages, true, p, stream);
+  if (e == cudaSuccess) e = launch_phase(pages_resize_phase_kernel<2>, pages, true, p, stream);
+  if (e == cudaSuccess) e = launch_phase(pages_resize_phase_kernel<3>, tables, true, p, stream);
+  return e;
 }
 
 cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream) {
@@ -485,9 +617,17 @@ cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_pages_compact(const PagesParams& p, cudaStream_t stream) {
-  pages_compact_kernel<<<kClusterCtas, kPlanThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t stream) {
+  cudaError_t e = cudaSuccess;
+  if (one_cluster(p)) {
+    pages_compact_kernel<<<kClusterCtas, kPlanThreads, 0, stream>>>(p);
+    e = cudaGetLastError();
+  } else {
+    const int pages = phase_ctas(((int64_t)p.num_pages + kChunk - 1) / kChunk, sms);
+    e = launch_phase(pages_compact_phase_kernel<0>, pages, false, p, stream);
+    if (e == cudaSuccess) e = launch_phase(pages_compact_phase_kernel<1>, pages, true, p, stream);
+    if (e == cudaSuccess) e = launch_phase(pages_compact_phase_kernel<2>, pages, true, p, stream);
+  }
   if (e != cudaSuccess) return e;
   const int cols = (p.max_pages + 255) / 256;
   pages_renumber_kernel<<<dim3((unsigned)p.rows, (unsigned)(cols < 64 ? cols : 64)), 256, 0, stream>>>(p);

@@ -181,7 +181,7 @@ def _window_args(q, rows, scales, tables, seq_lens, cum, sinks, window, first_to
     qs, qt = q.shape, q.stride()
     if q.dtype is not torch.bfloat16:
         raise TypeError(f"q must be bfloat16; got {q.dtype}")
-    if len(qs) != 3 or qs[2] != HEAD_DIM or qt[2] != 1 or (qs[1] > 1 and qt[1] != HEAD_DIM):
+    if len(qs) != 3 or qs[2] != HEAD_DIM or (qs[0] > 0 and (qt[2] != 1 or (qs[1] > 1 and qt[1] != HEAD_DIM))):
         raise ValueError(f"q must be [T, H, {HEAD_DIM}] with contiguous heads; got {tuple(qs)}")
     if sinks is not None:
         _words("sinks", sinks, qs[1], torch.float32)
@@ -264,7 +264,7 @@ def append(latent: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block
     ls, lt = latent.shape, latent.stride()
     if latent.dtype is not torch.bfloat16:
         raise TypeError(f"latent must be bfloat16; got {latent.dtype}")
-    if len(ls) != 2 or ls[1] != HEAD_DIM or lt[1] != 1:
+    if len(ls) != 2 or ls[1] != HEAD_DIM or (lt[1] != 1 and ls[0] > 0):
         raise ValueError(f"latent must be [T, {HEAD_DIM}] with contiguous rows; got {tuple(ls)}")
     _words("error_word", error_word, 1)
     a = SmlaAppendArgs(_cache(rows, scales, block_tables, seq_lens, cum_seq_lens_q), ls[0], latent.data_ptr(),

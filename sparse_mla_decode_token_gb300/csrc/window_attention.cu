@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         const int b = n & 1;
         failed |= !warp_wait(cx, bar(sm.scale_full[b]), (n >> 1) & 1);
         const float s = sm.scale[b][r];
-        const bool seen = s >= 0.f;
+        const bool seen = !(s < 0.f);             // (a NaN scale is seen, and makes the result NaN)
         const float ls = fmaxf(fast_log2(s), kMinScaleLog2), inv = fast_exp2(-ls);
         failed |= !warp_wait(cx, bar(sm.s_full[b]), (n >> 1) & 1);
         tc_fence_after();

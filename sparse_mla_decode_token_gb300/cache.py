@@ -218,7 +218,7 @@ def window_attention(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, 
     a = _window_args(q, rows, scales, block_tables, seq_lens, cum_seq_lens_q, sinks, window, first_tokens, num_splits)
     T, H = a.sum_q, a.num_heads
     if out is None:
-        out = torch.empty((T, H, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.dtype != torch.bfloat16 or not out.is_contiguous() or out.numel() != T * H * HEAD_DIM:
         raise ValueError("out must be a contiguous bfloat16 tensor of T*H*512 elements")
     if out_lse is None:

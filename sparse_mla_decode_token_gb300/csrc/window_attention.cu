@@ -118,17 +118,20 @@ __device__ __forceinline__ int chunk_at(const Unit& u, int k) {
   return k < u.first_chunks ? k : u.window_chunk + (k - u.first_chunks);
 }
 
-// Unit x (whole warp; the same result in every lane).
+// Unit x: its heads, and (whole warp; the same result in every lane) its rows.
+__device__ __forceinline__ void unit_heads(const KernelParams& kp, int x, Unit* u) {
+  u->h0 = (x % kp.groups) * kNH;
+  x /= kp.groups;
+  u->split = x % kp.p.num_splits;
+  u->t = x / kp.p.num_splits;
+  u->heads = min(kNH, kp.p.H - u->h0);
+}
 template <int kShift>
 __device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lane) {
   const WindowParams& p = kp.p;
   const CacheView& c = p.c;
   Unit u;
-  u.h0 = (x % kp.groups) * kNH;
-  x /= kp.groups;
-  u.split = x % p.num_splits;
-  u.t = x / p.num_splits;
-  u.heads = min(kNH, p.H - u.h0);
+  unit_heads(kp, x, &u);
   int first, count;
   u.b = c.cum != nullptr ? last_request(c.batch, lane, [&](int b) { return __ldg(c.cum + b) <= u.t; })
                          : u.t / (c.sum_q / c.batch);
@@ -408,8 +411,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
       const int tiles = sm.unit[x & 1].tiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sm.unit_empty[x & 1]));
+      // (the first unit's queries come in any case, and a phase that nobody waited for would pass for the next)
+      if (ok && (tiles > 0 || x == 0)) ok = warp_wait(cx, bar(sm.q_full), q++ & 1);
       if (!ok || tiles == 0) continue;
-      ok = warp_wait(cx, bar(sm.q_full), q++ & 1);
       for (int i = 0; ok && i < tiles; ++i, ++n) {
         const int b = n & 1;
         ok = warp_wait(cx, bar(sm.k_full[b]), (n >> 1) & 1);
@@ -469,20 +473,23 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     uint64_t sum[kHW / 2];                        // of two heads each
     int n = 0;
-    bool failed = !warp_wait(cx, bar(sm.unit_full[0]), 0);
-    if (!failed && sm.unit[0].tiles > 0) {
-      split_query(kp, sm.unit[0], smem + kOffQ, sm, warp, lane);
+    {
+      // the first unit's queries, while its rows are looked up (a unit without any leaves them unused)
+      Unit u;
+      unit_heads(kp, blockIdx.x, &u);
+      split_query(kp, u, smem + kOffQ, sm, warp, lane);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sm.q_full));
     }
+    bool failed = !warp_wait(cx, bar(sm.unit_full[0]), 0);
     if (threadIdx.x < kNH) sm.negref[threadIdx.x] = 0.f;
     for (int x = 0; x < mine; ++x) {
       if (named_bar_or(1, kSoftmaxThreads, failed)) break;   // also: qscale and negref are written
       const int tiles = sm.unit[x & 1].tiles;
 #pragma unroll
       for (int e = 0; e < kHW / 2; ++e) sum[e] = 0;
-      bool fresh = true;                          // some head has no reference yet
+      bool fresh = true;                          // no row seen, so no reference yet
       int i = 0;
       for (; i < tiles; ++i, ++n) {
         const int b = n & 1;
@@ -535,18 +542,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             if (lane == e) *reinterpret_cast<float2*>(&sm.wmax[warp & 3][hw + 2 * e]) = make_float2(v, w);
           }
           named_bar_sync(1, kSoftmaxThreads);
-          bool unset = false;
           if (threadIdx.x < kNH) {
             const int h = threadIdx.x;
             // by how much the tile's maximum passes the reference
             const float m = fmaxf(fmaxf(sm.wmax[0][h], sm.wmax[1][h]), fmaxf(sm.wmax[2][h], sm.wmax[3][h])) - kHeadroom;
-            unset = fresh && m == -INFINITY;
             const float up = m == -INFINITY ? 0.f : fresh ? m : fmaxf(m, 0.f);
             sm.negref[h] -= up;
             sm.wmax[0][h] = -up;
             sm.wmax[1][h] = fresh ? 0.f : fast_exp2(-up);
           }
-          fresh = named_bar_or(1, kSoftmaxThreads, unset);
+          // (by the rows, not by the maxima: a head of NaN has none, and the others keep theirs)
+          fresh = !named_bar_or(1, kSoftmaxThreads, seen) && fresh;
           if (i > 0) {
             // O^T by column, once the products into it are done
             failed |= !warp_wait(cx, bar(sm.k_free[b ^ 1][3]), ((n - 1) >> 1) & 1);

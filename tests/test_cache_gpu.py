@@ -253,14 +253,15 @@ def test_window_nan_and_infinity():
     cache, q, _ = make(18, [200, 200], [1, 1])
     qb = bf16(q)[0]
     qb[0, 3, 17], qb[0, 5, 100] = float("nan"), float("inf")
-    got = run(cache, q, window=150, q_gpu=qb)
-    assert np.isnan(got[0][0, [3, 5]]).all() and np.isnan(got[1][0, [3, 5]]).all()
     keep = [h for h in range(64) if h not in (3, 5)]
     out, lse, tol_o, tol_l = R.window(cache, bf16(q)[1], window=150, bmm1=1 / math.sqrt(512))
-    assert np.all(np.abs(got[0][0, keep] - out[0, keep]) <= tol_o[0, keep])
-    assert np.all(np.abs(got[0][1] - out[1]) <= tol_o[1])
+    for splits in (1, 2, 0):
+        got = run(cache, q, window=150, q_gpu=qb, splits=splits)
+        assert np.isnan(got[0][0, [3, 5]]).all() and np.isnan(got[1][0, [3, 5]]).all()
+        assert np.all(np.abs(got[0][0, keep] - out[0, keep]) <= tol_o[0, keep])
+        assert np.all(np.abs(got[0][1] - out[1]) <= tol_o[1])
     cache.rows[cache.page(0, 190), 190 % 64, 5] = 0x7F
-    for splits in (1, 2):
+    for splits in (1, 2, 0):
         got = run(cache, q, window=150, splits=splits)
         assert np.isnan(got[1][0]).all() and np.isnan(got[0][0, :, 5]).all()
         assert np.all(np.abs(got[0][1] - out[1]) <= tol_o[1])

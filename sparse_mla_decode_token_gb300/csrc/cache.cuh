@@ -50,7 +50,8 @@ __device__ __forceinline__ int last_request(int batch, int lane, F before) {
 
 struct WindowParams {
   CacheView c;
-  int32_t H, window, first_tokens, num_splits;
+  int32_t H, window, first_tokens;
+  int32_t whole, num_splits;   // (token, head group) pairs done whole, splits of each of the others
   const __nv_bfloat16* q;
   int64_t q_stride_token;
   const float* sinks;
@@ -59,8 +60,8 @@ struct WindowParams {
   const float* bmm2_dev;
   __nv_bfloat16* out;
   float* out_lse;
-  float* part_o;      // [T, S, H, 512] fp32 normalised split partials (S > 1)
-  float* part_lse;    // [T, S, H] fp32 base-2 LSE of each partial (S > 1)
+  float* part_o;      // [pairs not whole, S, 64 heads, 512] fp32 normalised split partials
+  float* part_lse;    // [pairs not whole, S, 64 heads] fp32 base-2 LSE of each
   int32_t* err;
 };
 

@@ -155,24 +155,26 @@ smla_status check_window(const smla_window_args* a) {
 
 int head_groups(const smla_window_args* a) { return (a->num_heads + kWindowHeads - 1) / kWindowHeads; }
 
-// Splits of a token's tiles; shapes only.  At most as many CTAs as the GPU holds
-// at once (one an SM).  Measured on a GB300, a tile costs a CTA 2.1 us, and a
-// second split the merge: 1.3 tiles' time and a 7000th of one for each partial of
-// 512 values (1 token x 64 heads, 2 tiles: 12.7 us whole, 13.7 in two; 3 tiles:
-// 16.1 against 14.8 in three; 32 x 128, 5 tiles: 21.5 against 22.9 in two, 9 tiles:
-// 30.1 against 27.8).
-int window_splits(const smla_window_args* a, int sms) {
-  if (a->num_splits > 0) return a->num_splits;
-  const int64_t page = a->cache.page_size, chunk = page % 32 == 0 ? 32 : page % 16 == 0 ? 16 : 8;   // rows of a box
-  const int64_t all = ((int64_t)a->cache.max_pages * page + chunk - 1) / chunk;
-  const int64_t seen = ((int64_t)a->window + chunk - 2) / chunk + 1 + ((int64_t)a->first_tokens + chunk - 1) / chunk;
-  const int64_t tiles = (std::min(all, seen) * chunk + kWindowTile - 1) / kWindowTile;
-  const int64_t units = std::max<int64_t>(1, (int64_t)a->sum_q * head_groups(a));
-  const int64_t most = std::min<int64_t>({sms / units, tiles, SMLA_MAX_SPLITS});
+// How the (token, head group) pairs are worked through: the first `whole` each by
+// one CTA, the others in `splits` ranges of their tiles that a second kernel
+// merges.  Shapes only.
+struct WindowPlan {
+  int64_t whole, units;
+  int splits;
+  size_t lse, bytes;   // workspace: offset of the partials' LSEs, all of it
+};
+
+// Splits that cost `pairs` pairs of `tiles` tiles least on `sms` SMs, one CTA each
+// at a time.  Measured on a GB300, a tile costs a CTA 2.1 us, and a second split
+// the merge: 1.3 tiles' time and a 7000th of one for each partial row of 512 values
+// (1 token x 64 heads, 2 tiles: 12.7 us whole, 13.7 in two; 3 tiles: 16.1 against
+// 14.8 in three; 32 x 128, 5 tiles: 21.5 against 22.9 in two, 9: 30.1 against 27.8).
+int cheapest_splits(int64_t pairs, int64_t tiles, int sms) {
+  const int64_t most = std::min<int64_t>({sms / pairs, tiles, SMLA_MAX_SPLITS});
   int best = 1;
   double cost = (double)tiles;
   for (int64_t s = 2; s <= most; ++s) {
-    const double c = (double)((tiles + s - 1) / s) + 1.3 + (double)a->sum_q * a->num_heads * s / 7000.0;
+    const double c = (double)((tiles + s - 1) / s) + 1.3 + (double)pairs * kWindowHeads * s / 7000.0;
     if (c < cost) {
       cost = c;
       best = (int)s;
@@ -181,10 +183,28 @@ int window_splits(const smla_window_args* a, int sms) {
   return best;
 }
 
-size_t window_workspace(const smla_window_args* a, int splits) {
-  if (splits <= 1) return 0;
-  const size_t rows = (size_t)a->sum_q * a->num_heads * splits;
-  return align_up(rows * kHeadDim * sizeof(float), 256) + align_up(rows * sizeof(float), 256);
+WindowPlan window_plan(const smla_window_args* a, int sms) {
+  WindowPlan w;
+  const int64_t pairs = (int64_t)a->sum_q * head_groups(a);
+  if (a->num_splits > 0) {
+    w.splits = a->num_splits;
+    w.whole = w.splits > 1 ? 0 : pairs;
+  } else {
+    const int64_t page = a->cache.page_size, chunk = page % 32 == 0 ? 32 : page % 16 == 0 ? 16 : 8;   // rows of a box
+    const int64_t all = ((int64_t)a->cache.max_pages * page + chunk - 1) / chunk;
+    const int64_t seen = ((int64_t)a->window + chunk - 2) / chunk + 1 + ((int64_t)a->first_tokens + chunk - 1) / chunk;
+    const int64_t tiles = (std::min(all, seen) * chunk + kWindowTile - 1) / kWindowTile;
+    // The pairs of the last, partly filled turn of the SMs are the ones worth splitting (160 pairs of 9 tiles: 54 us
+    // whole, 43 so); behind four full turns the turns' own spread hides it (5672 of 6: 626 us whole, 641 so).
+    const int64_t rest = pairs % sms;
+    w.splits = rest > 0 && pairs < 4 * (int64_t)sms ? cheapest_splits(rest, tiles, sms) : 1;
+    w.whole = w.splits > 1 ? pairs - rest : pairs;
+  }
+  w.units = w.whole + (pairs - w.whole) * w.splits;
+  const size_t rows = (size_t)(pairs - w.whole) * w.splits * kWindowHeads;
+  w.lse = align_up(rows * kHeadDim * sizeof(float), 256);
+  w.bytes = w.lse + align_up(rows * sizeof(float), 256);
+  return w;
 }
 
 // ------------------------------------------------------------------ pages
@@ -268,7 +288,7 @@ smla_status smla_window_workspace_size(const smla_window_args* args, int device,
   SMLA_TRY(check_window(args));
   int sms = 0;
   SMLA_TRY(device_sms(device, &sms));
-  *bytes = window_workspace(args, window_splits(args, sms));
+  *bytes = window_plan(args, sms).bytes;
   return SMLA_OK;
 }
 
@@ -285,14 +305,13 @@ smla_status smla_window_attention(const smla_window_args* a, void* stream) {
   SMLA_TRY(need_words("error_word", a->error_word, false));
   int sms = 0;
   SMLA_TRY(current_sms(&sms));
-  const int splits = window_splits(a, sms);
-  const int64_t grid = (int64_t)a->sum_q * head_groups(a) * splits;
-  if (grid > 0x7fffffff) return fail(SMLA_ERR_UNSUPPORTED, "grid of %lld CTAs is too large", (long long)grid);
-  const size_t bytes = window_workspace(a, splits);
-  if (bytes > 0) {
-    if (a->workspace == nullptr || a->workspace_bytes < bytes)
+  const WindowPlan plan = window_plan(a, sms);
+  if (plan.units > 0x7fffffff || (int64_t)a->sum_q * head_groups(a) > 0x7fffffff / kWindowHeads)
+    return fail(SMLA_ERR_UNSUPPORTED, "%lld units are too many", (long long)plan.units);
+  if (plan.bytes > 0) {
+    if (a->workspace == nullptr || a->workspace_bytes < plan.bytes)
       return fail(SMLA_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes given, %zu needed",
-                  a->workspace ? a->workspace_bytes : (size_t)0, bytes);
+                  a->workspace ? a->workspace_bytes : (size_t)0, plan.bytes);
     if (!aligned(a->workspace, 256)) return fail(SMLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   }
   WindowParams p;
@@ -301,7 +320,8 @@ smla_status smla_window_attention(const smla_window_args* a, void* stream) {
   p.H = a->num_heads;
   p.window = a->window;
   p.first_tokens = a->first_tokens;
-  p.num_splits = splits;
+  p.whole = (int32_t)plan.whole;
+  p.num_splits = plan.splits;
   p.q = static_cast<const __nv_bfloat16*>(a->q);
   p.q_stride_token = a->q_stride_token ? a->q_stride_token : (int64_t)a->num_heads * kHeadDim;
   p.sinks = a->sinks;
@@ -312,11 +332,9 @@ smla_status smla_window_attention(const smla_window_args* a, void* stream) {
   p.out = static_cast<__nv_bfloat16*>(a->out);
   p.out_lse = a->out_lse;
   p.err = a->error_word;
-  if (splits > 1) {
-    const size_t rows = (size_t)a->sum_q * a->num_heads * splits;
+  if (plan.bytes > 0) {
     p.part_o = static_cast<float*>(a->workspace);
-    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(a->workspace) +
-                                          align_up(rows * kHeadDim * sizeof(float), 256));
+    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + plan.lse);
   }
   return launched("window attention", launch_window_attention(p, sms, static_cast<cudaStream_t>(stream)));
 }

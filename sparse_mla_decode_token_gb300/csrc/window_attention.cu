@@ -85,7 +85,7 @@ constexpr int kOffSmall = kOffP + 4 * kPHalf;
 
 // What a CTA works on at a time: 64 heads of a token, a range of tiles of its chunk list.
 struct Unit {
-  int t, h0, heads, split, b;
+  int t, h0, heads, part, b;                      // part: its partial's number, or -1 (it writes the output)
   int first_chunks, window_chunk, chunks;         // list: [0, first_chunks), then from window_chunk on
   int pos, lo;                                    // last and first visible position of the window
   int tile0, tiles;
@@ -119,19 +119,22 @@ __device__ __forceinline__ int chunk_at(const Unit& u, int k) {
 }
 
 // Unit x: its heads, and (whole warp; the same result in every lane) its rows.
+// Units 0 .. whole - 1 are (token, head group) pairs, the others splits of the pairs behind those.
+template <bool kParts>
 __device__ __forceinline__ void unit_heads(const KernelParams& kp, int x, Unit* u) {
-  u->h0 = (x % kp.groups) * kNH;
-  x /= kp.groups;
-  u->split = x % kp.p.num_splits;
-  u->t = x / kp.p.num_splits;
-  u->heads = min(kNH, kp.p.H - u->h0);
+  const WindowParams& p = kp.p;
+  u->part = !kParts || x < p.whole ? -1 : x - p.whole;
+  const int pair = !kParts || x < p.whole ? x : p.whole + u->part / p.num_splits;
+  u->h0 = (pair % kp.groups) * kNH;
+  u->t = pair / kp.groups;
+  u->heads = min(kNH, p.H - u->h0);
 }
-template <int kShift>
+template <int kShift, bool kParts>
 __device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lane) {
   const WindowParams& p = kp.p;
   const CacheView& c = p.c;
   Unit u;
-  unit_heads(kp, x, &u);
+  unit_heads<kParts>(kp, x, &u);
   int first, count;
   u.b = c.cum != nullptr ? last_request(c.batch, lane, [&](int b) { return __ldg(c.cum + b) <= u.t; })
                          : u.t / (c.sum_q / c.batch);
@@ -146,9 +149,14 @@ __device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lan
     u.window_chunk = max(u.lo >> kShift, u.first_chunks);
     u.chunks = u.first_chunks + max(0, (last >> kShift) - u.window_chunk + 1);
   }
-  const int tiles = (u.chunks + (kRows >> kShift) - 1) >> (7 - kShift), per = (tiles + p.num_splits - 1) / p.num_splits;
-  u.tile0 = min(tiles, u.split * per);
-  u.tiles = min(tiles, u.tile0 + per) - u.tile0;
+  const int tiles = (u.chunks + (kRows >> kShift) - 1) >> (7 - kShift);
+  u.tile0 = 0;
+  u.tiles = tiles;
+  if (kParts && u.part >= 0) {
+    const int per = (tiles + p.num_splits - 1) / p.num_splits;
+    u.tile0 = min(tiles, u.part % p.num_splits * per);
+    u.tiles = min(tiles, u.tile0 + per) - u.tile0;
+  }
   return u;
 }
 
@@ -222,7 +230,10 @@ __device__ __forceinline__ void split_query(const KernelParams& kp, const Unit& 
   }
 }
 
-template <int kShift>                             // log2 of a TMA box's rows
+// kShift: log2 of a TMA box's rows; kParts: some units are splits (without their code
+// the kernel is 3 % faster where units are many: what runs once a unit comes through
+// the instruction cache every time)
+template <int kShift, bool kParts>
 __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_constant__ KernelParams kp) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Small& sm = *reinterpret_cast<Small*>(smem + kOffSmall);
@@ -268,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     constexpr int kBoxes = kRows >> kShift;       // of a tile
     int n = 0;
     bool ok = true;
-    Unit ahead = make_unit<kShift>(kp, blockIdx.x, lane);
+    Unit ahead = make_unit<kShift, kParts>(kp, blockIdx.x, lane);
     auto prefetch_query = [&](const Unit& u) {
       if (u.tiles > 0 && elect_one())
         bulk_prefetch_l2(p.q + (int64_t)u.t * p.q_stride_token + (int64_t)u.h0 * kHeadDim, u.heads * kHeadDim * 2);
@@ -286,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
       __syncwarp();
       auto look_ahead = [&] {                     // the next unit and its queries' way to L2
         if (x + 1 < mine) {
-          ahead = make_unit<kShift>(kp, blockIdx.x + (x + 1) * gridDim.x, lane);
+          ahead = make_unit<kShift, kParts>(kp, blockIdx.x + (x + 1) * gridDim.x, lane);
           prefetch_query(ahead);
         }
       };
@@ -476,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     {
       // the first unit's queries, while its rows are looked up (a unit without any leaves them unused)
       Unit u;
-      unit_heads(kp, blockIdx.x, &u);
+      unit_heads<kParts>(kp, blockIdx.x, &u);
       split_query(kp, u, smem + kOffQ, sm, warp, lane);
       fence_proxy_async_smem();
       __syncwarp();
@@ -530,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           top = fmaxf(top, fmaxf(v, w));
         }
         if (i == 0 && warp == 0 && elect_one()) bulk_store_wait_read<0>();   // the last unit's output has left the P buffers
-        if (named_bar_or(1, kSoftmaxThreads, failed || fresh || (seen && top > kMaxLog2))) {
+        if (__builtin_expect(named_bar_or(1, kSoftmaxThreads, failed || fresh || (seen && top > kMaxLog2)), 0)) {
           // ---- a new reference: the heads' maxima over the tile
           if (named_bar_or(1, kSoftmaxThreads, failed)) break;
 #pragma unroll
@@ -597,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           *reinterpret_cast<uint4*>(pb + kPHalf + at) = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16,
                                                                    lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
         }
-        if (!seen) {
+        if (__builtin_expect(!seen, 0)) {
           // the first product has read the row (its commit is what s_full waited for); the second must find zeros
           uint8_t* row = smem + kOffK + b * kTileBytes + (r >> 3) * kGroupBytes + (r & 7) * 128 + (hw / kHW) * 1024;
 #pragma unroll
@@ -612,10 +623,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
       // the next unit's queries, while the last products of this one run (their
       // buffer is free: the last S of this unit has been read)
       float sink = -INFINITY;                     // of head threadIdx.x, in log2 units
-      if (p.sinks != nullptr && p.num_splits == 1 && threadIdx.x < sm.unit[x & 1].heads)
+      if (p.sinks != nullptr && (!kParts || sm.unit[x & 1].part < 0) && threadIdx.x < sm.unit[x & 1].heads)
         sink = __ldg(p.sinks + sm.unit[x & 1].h0 + threadIdx.x) * kLog2e;
-      const float out_scale = p.num_splits == 1 ? load_scale(p.bmm2, p.bmm2_dev) : 1.f;
-      const int t = sm.unit[x & 1].t, h0 = sm.unit[x & 1].h0, heads = sm.unit[x & 1].heads, split = sm.unit[x & 1].split;
+      const float out_scale = !kParts || sm.unit[x & 1].part < 0 ? load_scale(p.bmm2, p.bmm2_dev) : 1.f;
+      const int t = sm.unit[x & 1].t, h0 = sm.unit[x & 1].h0, heads = sm.unit[x & 1].heads;
+      const bool whole = !kParts || sm.unit[x & 1].part < 0;
+      const int64_t part = (int64_t)sm.unit[x & 1].part * kNH;                // its first partial row
       if (x + 1 < mine) {
         failed |= !warp_wait(cx, bar(sm.unit_full[(x + 1) & 1]), ((x + 1) >> 1) & 1);
         if (!failed && sm.unit[(x + 1) & 1].tiles > 0) {
@@ -630,9 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 
       // ---------------------------------------------------------- results
       const int64_t th = (int64_t)t * p.H + h0;                               // first (token, head) of the unit
-      const int64_t part = ((int64_t)t * p.num_splits + split) * p.H + h0;  // first partial
-      if (tiles == 0) {                           // no visible row (of this split)
-        if (p.num_splits > 1) {
+      if (__builtin_expect(tiles == 0, 0)) {      // no visible row (of this split)
+        if (!whole) {
           if (threadIdx.x < heads) p.part_lse[part + threadIdx.x] = -INFINITY;
         } else {
           uint4* o = reinterpret_cast<uint4*>(p.out + th * kHeadDim);
@@ -673,12 +685,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         sm.wmax[1][h] = f;
         sm.negref[h] = 0.f;                       // the next unit's
         if (h < heads) {
-          if (p.num_splits > 1) p.part_lse[part + h] = lse;
+          if (!whole) p.part_lse[part + h] = lse;
           else if (p.out_lse) p.out_lse[th + h] = lse;
         }
       }
       named_bar_sync(1, kSoftmaxThreads);
-      if (p.num_splits > 1) {
+      if (__builtin_expect(!whole, 0)) {
 #pragma unroll 1
         for (int m = 0; m < 4; ++m) {             // dims 128 m .. + 127, one a thread
           uint32_t o[kHW];
@@ -739,30 +751,33 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
   if (warp == kScoreWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Merges the S normalised fp32 partials of every (token, head): weights
+// Merges the S normalised fp32 partials of a split pair's heads: weights
 // 2^(LSE_s - LSE), then the sink and bmm2.
-constexpr int kMergeThreads = 128;                // one (token, head): four dims a thread
+constexpr int kMergeThreads = 128;                // one head: four dims a thread
 
-__global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const WindowParams p) {
-  const int64_t th = blockIdx.x;
-  const int t = (int)(th / p.H), h = (int)(th % p.H), d = threadIdx.x * 4;
+__global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const WindowParams p, int groups) {
+  const int pair = blockIdx.x / kNH, hl = blockIdx.x % kNH, d = threadIdx.x * 4;
+  const int t = (p.whole + pair) / groups, h = (p.whole + pair) % groups * kNH + hl;
+  if (h >= p.H) return;
+  const int64_t th = (int64_t)t * p.H + h;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float* lse_s = p.part_lse + (int64_t)t * p.num_splits * p.H + h;
-  const float* o_s = p.part_o + ((int64_t)t * p.num_splits * p.H + h) * kHeadDim + d;
+  const int64_t row = (int64_t)pair * p.num_splits * kNH + hl;
+  const float* lse_s = p.part_lse + row;
+  const float* o_s = p.part_o + row * kHeadDim + d;
   float mx = -INFINITY;
   bool nan = false;
   for (int s = 0; s < p.num_splits; ++s) {
-    const float l = __ldg(lse_s + (int64_t)s * p.H);
+    const float l = __ldg(lse_s + s * kNH);
     nan |= isnan(l);
     mx = fmaxf(mx, l);
   }
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float wsum = 0.f;
   for (int s = 0; s < p.num_splits; ++s) {
-    const float l = __ldg(lse_s + (int64_t)s * p.H);
+    const float l = __ldg(lse_s + s * kNH);
     if (l == -INFINITY) continue;                 // an empty partial is not written
     const float w = fast_exp2(l - mx);
-    const float4 o = __ldg(reinterpret_cast<const float4*>(o_s + (int64_t)s * p.H * kHeadDim));
+    const float4 o = __ldg(reinterpret_cast<const float4*>(o_s + (int64_t)s * kNH * kHeadDim));
     acc.x = fmaf(w, o.x, acc.x), acc.y = fmaf(w, o.y, acc.y), acc.z = fmaf(w, o.z, acc.z), acc.w = fmaf(w, o.w, acc.w);
     wsum += w;
   }
@@ -837,11 +852,12 @@ cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t
   KernelParams kp;
   kp.p = p;
   kp.groups = (p.H + kNH - 1) / kNH;
-  kp.units = (int)((int64_t)p.c.sum_q * kp.groups * p.num_splits);
+  const int pairs = (int)((int64_t)p.c.sum_q * kp.groups);
+  kp.units = p.whole + (pairs - p.whole) * p.num_splits;
   // the highest box that pages hold whole, up to a quarter of a tile: fewer copies to issue
   const int shift = p.c.page_size % 32 == 0 ? 5 : p.c.page_size % 16 == 0 ? 4 : 3;
   cudaError_t e = encode_cache_map(&kp.map, p.c, 1 << shift);
-  if (e == cudaSuccess && p.num_splits == 1) e = encode_out_map(&kp.out_map, p);   // (partials are stored by threads)
+  if (e == cudaSuccess && p.whole > 0) e = encode_out_map(&kp.out_map, p);   // (partials are stored by threads)
   if (e != cudaSuccess) return e;
   auto launch = [&](auto kernel) -> cudaError_t {
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
@@ -849,11 +865,14 @@ cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t
     kernel<<<(unsigned)std::min(kp.units, sms), kThreads, kSmemBytes, stream>>>(kp);
     return cudaGetLastError();
   };
-  e = shift == 5 ? launch(window_kernel<5>) : shift == 4 ? launch(window_kernel<4>) : launch(window_kernel<3>);
-  if (e != cudaSuccess || p.num_splits == 1) return e;
+  const bool parts = pairs > p.whole;
+  if (shift == 5) e = parts ? launch(window_kernel<5, true>) : launch(window_kernel<5, false>);
+  else if (shift == 4) e = parts ? launch(window_kernel<4, true>) : launch(window_kernel<4, false>);
+  else e = parts ? launch(window_kernel<3, true>) : launch(window_kernel<3, false>);
+  if (e != cudaSuccess || !parts) return e;
   // programmatic dependent launch: scheduled while the split kernel drains
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.c.sum_q * (int64_t)p.H));
+  cfg.gridDim = dim3((unsigned)((pairs - p.whole) * (int64_t)kNH));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -861,7 +880,7 @@ cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, window_merge_kernel, p);
+  return cudaLaunchKernelEx(&cfg, window_merge_kernel, p, kp.groups);
 }
 
 }  // namespace smla

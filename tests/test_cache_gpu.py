@@ -170,11 +170,13 @@ def test_window_prefill_many_units():
     check(cache, q, run(cache, q, window=100, first=1), window=100, first=1)
 
 
-def test_window_many_units_of_many_tiles():
-    """Every CTA takes two units of up to eight tiles: buffers and barriers go through many turns between them."""
+@pytest.mark.parametrize("splits", [1, 0])
+def test_window_many_units_of_many_tiles(splits):
+    """CTAs take two units of up to eight tiles: buffers and barriers go through many turns between them.  On its
+    own the call splits the last few units and does the others whole."""
     lens = [600 + 5 * k for k in range(80)]
     cache, q, _ = make(22, lens, [1] * 80, heads=128)
-    check(cache, q, run(cache, q, window=900, first=4, splits=1), window=900, first=4)
+    check(cache, q, run(cache, q, window=900, first=4, splits=splits), window=900, first=4)
 
 
 def test_window_longer_than_the_sequence_is_causal():

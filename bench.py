@@ -146,15 +146,17 @@ def code_only(text: str) -> str:
 # packing.  What they decide about a launch (kernel, splits, grid, block, shared
 # memory) is matched through the plan stored with each traffic record instead.
 HOST_ONLY_SOURCES = ("smla_api.cu",)
+# Sources of the paged-cache calls, which no decode launches.
+OTHER_SOURCES = ("cache.cuh", "cache_api.cu", "cache_append.cu", "cache_pages.cu", "cache_ptx.cuh", "window_attention.cu")
 PLAN_KEYS = ("kernel", "num_splits", "ctas_per_split", "grid", "threads", "smem_bytes", "clusters")
 
 
 def kernel_sources_sha() -> str:
-    """Hash of the device-code sources (comments and whitespace ignored)."""
+    """Hash of the decode's device-code sources (comments and whitespace ignored)."""
     csrc = os.path.join(ROOT, "sparse_mla_decode_token_gb300", "csrc")
     h = hashlib.sha256()
     for f in sorted(os.listdir(csrc)):
-        if f.endswith((".cu", ".cuh", ".h")) and f not in HOST_ONLY_SOURCES:
+        if f.endswith((".cu", ".cuh", ".h")) and f not in HOST_ONLY_SOURCES + OTHER_SOURCES:
             h.update(f.encode())
             h.update(code_only(open(os.path.join(csrc, f)).read()).encode())
     return h.hexdigest()[:16]

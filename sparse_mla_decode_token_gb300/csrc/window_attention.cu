@@ -47,6 +47,7 @@
 #include <atomic>
 
 #include "cache.cuh"
+#include "cache_ptx.cuh"
 #include "tc_common.cuh"
 #include "tc_ptx.cuh"
 

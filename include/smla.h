@@ -361,7 +361,9 @@ typedef struct smla_cache {
   int32_t max_pages;              /* page-table columns >= 1; max_pages * page_size < 2^31 */
   int32_t batch;                  /* requests B >= 1 */
   const int32_t* seq_lens;        /* [B] tokens of each request, this call's new tokens included */
-  const int32_t* cum_seq_lens_q;  /* [B+1] offsets of each request's new tokens, or NULL = uniform sum_q / B */
+  const int32_t* cum_seq_lens_q;  /* [B+1] offsets of each request's new tokens, or NULL = uniform sum_q / B; tokens before the
+                                     first offset and from the last one on (a padded batch) are no request's: the
+                                     calls write nothing for them */
 } smla_cache;
 
 /*
@@ -468,7 +470,7 @@ smla_status smla_cache_append(const smla_append_args* args, void* stream);
 typedef struct smla_pages_args {
   int32_t* block_tables;        /* [rows, max_pages] */
   int64_t block_table_stride;   /* row stride in elements [max_pages] */
-  int32_t rows;                 /* requests (0 = nothing to do) */
+  int32_t rows;                 /* requests (0 = nothing to do but *move_count = 0) */
   int32_t max_pages;            /* >= 1 */
   int32_t page_size;            /* tokens per page >= 1; max_pages * page_size < 2^31 */
   int32_t* ref_counts;          /* [num_pages] */
@@ -476,7 +478,7 @@ typedef struct smla_pages_args {
   const int32_t* lens;          /* [rows] tokens before the call */
   const int32_t* new_lens;      /* [rows] resize: tokens after it */
   const int32_t* parents;       /* [rows] fork: request to share with, or < 0 */
-  int32_t* out_lens;            /* [rows] fork: lengths after it; not lens itself */
+  int32_t* out_lens;            /* [rows] fork: lengths after it; does not overlap lens */
   int32_t* move_src;            /* [move_capacity] resize, compact */
   int32_t* move_dst;            /* [move_capacity] */
   int32_t* move_count;          /* [1] */

@@ -293,8 +293,8 @@ def _pages_args(tables, ref_counts, lens, page_size, error_word, new_lens=None, 
         _words("moves.src", src, 0)
         _words("moves.dst", dst, capacity)
         _words("moves.count", count, 1)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
+        if workspace is None or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor")
     return SmlaPagesArgs(tables.data_ptr(), tt[0] if rows > 1 else max_pages, rows, max_pages, int(page_size),
                          ref_counts.data_ptr(), ref_counts.numel(), lens.data_ptr(), _ptr(new_lens), _ptr(parents),
                          _ptr(out_lens), _ptr(src), _ptr(dst), _ptr(count), capacity, _ptr(workspace),

@@ -40,8 +40,9 @@ __device__ __forceinline__ int last_request(int batch, int lane, F before) {
   int lo = 0, n = batch - 1;                        // the answer is among lo .. lo + n
   while (n > 0) {
     const int step = (n + 31) / 32;
-    const int hits = __popc(__ballot_sync(0xffffffffu, before(lo + min(n, (lane + 1) * step))));
-    if (hits == 32) return lo + n;                  // (the last lanes look at lo + n)
+    const uint32_t miss = ~__ballot_sync(0xffffffffu, before(lo + min(n, (lane + 1) * step)));
+    if (miss == 0) return lo + n;                   // (the last lanes look at lo + n)
+    const int hits = __ffs(miss) - 1;               // the first miss, not a count: in range for offsets that fall, too
     lo += hits * step;
     n = min(n - hits * step, step - 1);             // lo + step is known to be behind it
   }

@@ -254,6 +254,14 @@ smla_status check_moves(const smla_pages_args* a, int64_t need) {
   return SMLA_OK;
 }
 
+// A call without requests: what a copy of its moves would find.
+smla_status no_moves(const smla_pages_args* a, void* stream) {
+  SMLA_TRY(need_words("move_count", a->move_count, true));
+  const cudaError_t e = cudaMemsetAsync(a->move_count, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(SMLA_ERR_CUDA, "move_count: %s", cudaGetErrorString(e));
+  return SMLA_OK;
+}
+
 PagesParams pages_params(const smla_pages_args* a) {
   PagesParams p;
   memset(&p, 0, sizeof(p));
@@ -369,7 +377,7 @@ smla_status smla_pages_workspace_size(const smla_pages_args* args, size_t* bytes
 
 smla_status smla_pages_resize(const smla_pages_args* a, void* stream) {
   SMLA_TRY(check_pages(a));
-  if (a->rows == 0) return SMLA_OK;
+  if (a->rows == 0) return no_moves(a, stream);
   SMLA_TRY(check_page_pointers(a));
   SMLA_TRY(need_words("new_lens", a->new_lens, true));
   SMLA_TRY(check_moves(a, a->rows));
@@ -384,13 +392,15 @@ smla_status smla_pages_fork(const smla_pages_args* a, void* stream) {
   SMLA_TRY(check_page_pointers(a));
   SMLA_TRY(need_words("parents", a->parents, true));
   SMLA_TRY(need_words("out_lens", a->out_lens, true));
-  if (a->out_lens == a->lens) return fail(SMLA_ERR_INVALID_ARG, "out_lens must not be lens");
+  const uintptr_t out = reinterpret_cast<uintptr_t>(a->out_lens), in = reinterpret_cast<uintptr_t>(a->lens);
+  if ((out > in ? out - in : in - out) < (uintptr_t)a->rows * sizeof(int32_t))
+    return fail(SMLA_ERR_INVALID_ARG, "out_lens must not be lens or overlap it");
   return launched("pages fork", launch_pages_fork(pages_params(a), static_cast<cudaStream_t>(stream)));
 }
 
 smla_status smla_pages_compact(const smla_pages_args* a, void* stream) {
   SMLA_TRY(check_pages(a));
-  if (a->rows == 0) return SMLA_OK;
+  if (a->rows == 0) return no_moves(a, stream);
   SMLA_TRY(check_page_pointers(a));
   SMLA_TRY(check_moves(a, a->num_pages / 2));
   int sms = 0;

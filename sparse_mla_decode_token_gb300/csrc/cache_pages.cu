@@ -37,7 +37,7 @@ __device__ __forceinline__ int page_columns(const PagesParams& p, int len, bool*
   const int64_t cap = (int64_t)p.max_pages * p.page_size;
   if (len < 0 || len > cap) *bad = true;
   len = (int)min((int64_t)max(len, 0), cap);
-  return (len + p.page_size - 1) / p.page_size;
+  return len / p.page_size + (len % p.page_size != 0);
 }
 __device__ __forceinline__ int clamped_len(const PagesParams& p, int len) {
   return (int)min((int64_t)max(len, 0), (int64_t)p.max_pages * p.page_size);

@@ -140,7 +140,9 @@ __device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lan
   u.b = c.cum != nullptr ? last_request(c.batch, lane, [&](int b) { return __ldg(c.cum + b) <= u.t; })
                          : u.t / (c.sum_q / c.batch);
   request_tokens(c, u.b, &first, &count);
-  u.pos = __ldg(c.seq_lens + u.b) - count + (u.t - first);
+  const bool owned = u.t >= first && u.t - first < count;   // else a token of no request: its outputs are left alone
+  if (!owned) u.heads = 0;
+  u.pos = owned ? __ldg(c.seq_lens + u.b) - count + (u.t - first) : -1;
   u.lo = (int)max((int64_t)u.pos - p.window + 1, (int64_t)0);
   u.first_chunks = u.window_chunk = u.chunks = 0;
   const int cap = c.max_pages * c.page_size, last = min(u.pos, cap - 1);
@@ -759,7 +761,7 @@ constexpr int kMergeThreads = 128;                // one head: four dims a threa
 __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const WindowParams p, int groups) {
   const int pair = blockIdx.x / kNH, hl = blockIdx.x % kNH, d = threadIdx.x * 4;
   const int t = (p.whole + pair) / groups, h = (p.whole + pair) % groups * kNH + hl;
-  if (h >= p.H) return;
+  if (h >= p.H || (p.c.cum != nullptr && (t < __ldg(p.c.cum) || t >= __ldg(p.c.cum + p.c.batch)))) return;
   const int64_t th = (int64_t)t * p.H + h;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t row = (int64_t)pair * p.num_splits * kNH + hl;

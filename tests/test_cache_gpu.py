@@ -303,6 +303,59 @@ def test_window_is_deterministic_and_replays_from_a_graph():
                 first = out.clone()
 
 
+@pytest.mark.parametrize("splits", [0, 1, 3])
+@pytest.mark.parametrize("heads", [64, 80])
+def test_window_padded_batch(splits, heads):
+    """Tokens before the first offset and behind the last one are no request's: their outputs stay as they were."""
+    cache, q, rng = make(26, [700, 40, 300], [2, 0, 3], heads=heads)
+    lead, behind = 2, 4
+    pad = rng.normal(size=(lead + behind, heads, 512))
+    q_all = np.concatenate([pad[:lead], q, pad[lead:]])
+    g = on_gpu(cache)
+    cum = i32(np.concatenate([cache.cum + lead, [5 + lead]]))      # (and a request without tokens at the end)
+    g["block_tables"] = torch.cat([g["block_tables"], torch.full_like(g["block_tables"][:1], -77)])
+    g["seq_lens"] = torch.cat([g["seq_lens"], i32([900])])
+    qt = bf16(q_all)[0]
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = workspace(qt, g, window=500, first_tokens=5, cum_seq_lens_q=cum, num_splits=splits)
+    ws.fill_(0xFF)
+    out, lse = torch.full_like(qt, 7.0), torch.full(qt.shape[:2], 7.0, device=DEV)
+    C.window_attention(qt, g["rows"], g["scales"], g["block_tables"], g["seq_lens"], ws, window=500, first_tokens=5,
+                       cum_seq_lens_q=cum, num_splits=splits, bmm1_scale=1 / math.sqrt(512), out=out, out_lse=lse,
+                       error_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for part in (slice(0, lead), slice(lead + 5, None)):
+        assert bool((out[part] == 7).all()) and bool((lse[part] == 7).all())
+    own = slice(lead, lead + 5)
+    check(cache, q, (out[own].double().cpu().numpy(), lse[own].double().cpu().numpy()), window=500, first=5)
+
+
+def test_offsets_that_fall_stay_inside_the_arrays():
+    """Offsets that are none give no result that counts, but write nothing outside the call's own tensors."""
+    rng = np.random.default_rng(27)
+    batch = 70
+    cache, _, _ = make(27, [64] * batch, [1] * batch, junk=False)
+    g = on_gpu(cache)
+    qt, x = bf16(rng.normal(size=(batch, 64, 512)))[0], bf16(rng.normal(size=(batch, 512)))[0]
+    for cum in (np.arange(batch, -1, -1), rng.integers(-5, 90, size=batch + 1), rng.permutation(batch + 1)):
+        # the arrays lie inside larger ones: what is read behind them would be impossible pages
+        wide = torch.full((3 * batch + 1,), 1 << 30, dtype=torch.int32, device=DEV)
+        wide[batch:2 * batch + 1] = i32(cum)
+        lens = torch.full((3 * batch,), 1 << 30, dtype=torch.int32, device=DEV)
+        lens[batch:2 * batch] = 64
+        before = wide.clone()
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        for splits in (1, 2):
+            ws = workspace(qt, g, window=64, cum_seq_lens_q=wide[batch:2 * batch + 1], num_splits=splits)
+            C.window_attention(qt, g["rows"], g["scales"], g["block_tables"], lens[batch:2 * batch], ws, window=64,
+                               cum_seq_lens_q=wide[batch:2 * batch + 1], num_splits=splits, error_word=err)
+        C.append(x, g["rows"], g["scales"], g["block_tables"], lens[batch:2 * batch],
+                 cum_seq_lens_q=wide[batch:2 * batch + 1], error_word=err)
+        torch.cuda.synchronize()
+        assert torch.equal(before, wide) and not int(err.item()) & B.DEVERR_TIMEOUT
+
+
 def test_window_workspace_too_small_is_refused():
     cache, q, _ = make(20, [1000], [1])
     g, qt = on_gpu(cache), bf16(q)[0]
@@ -404,6 +457,13 @@ def test_append_skips_and_flags_what_has_no_place():
     cache, _, _ = make(45, [300, 100, 64], [5, 40, 1], junk=False)
     cache.tables = cache.tables[:, :2].copy()              # the first request is longer than its table
     append_both(cache, x, expect_flag=B.DEVERR_INDEX_OUT_OF_RANGE)
+
+
+def test_append_padded_batch():
+    cache, _, rng = make(49, [200, 33], [30, 2])
+    x = rng.normal(size=(40, 512))
+    x[32:] = np.nan                                        # behind the last offset: not looked at
+    append_both(cache, x)
 
 
 def test_append_strided_tensors():
@@ -544,6 +604,29 @@ def test_pages_state_errors_are_flagged():
     torch.cuda.synchronize()
     assert int(b.err.item()) == B.DEVERR_PAGE_STATE and int(refs.min()) >= 0
     assert tables[0].tolist() == [-1] * 3 and tables[1].tolist() == [-1] * 3
+
+
+def test_pages_without_requests_leave_no_moves():
+    """A copy behind a call of no requests finds no moves, whatever the call before left."""
+    moves = C.PageMoves(i32([0] * 8), i32([1] * 8), i32([5]))
+    none = torch.empty(0, 4, dtype=torch.int32, device=DEV)
+    refs, ws = i32([1] * 16), torch.empty(4096, dtype=torch.uint8, device=DEV)
+    C.pages_resize(none, refs, i32([]), i32([]), ws, page_size=8, moves=moves)
+    assert int(moves.count.item()) == 0
+    moves.count.fill_(5)
+    C.pages_compact(none, refs, i32([]), ws, page_size=8, moves=moves)
+    assert int(moves.count.item()) == 0 and refs.tolist() == [1] * 16
+
+
+def test_pages_of_lengths_near_the_end_of_32_bits():
+    size = (1 << 30) + 1                                   # one page more than half of what a length can count
+    tables, refs = i32([[-1], [-1]]), i32([0, 0, 0])
+    ws = torch.empty(C.pages_workspace_size(tables, refs, size), dtype=torch.uint8, device=DEV)
+    moves, err = C.new_moves(2, DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    C.pages_resize(tables, refs, i32([0, 0]), i32([size, size - 1]), ws, page_size=size, moves=moves, error_word=err)
+    assert tables.tolist() == [[0], [1]] and refs.tolist() == [1, 1, 0] and int(err.item()) == 0
+    C.pages_resize(tables, refs, i32([size, size - 1]), i32([0, size]), ws, page_size=size, moves=moves, error_word=err)
+    assert tables.tolist() == [[-1], [1]] and refs.tolist() == [0, 1, 0] and int(err.item()) == 0
 
 
 def test_pages_replay_from_a_graph_and_share_a_workspace():

@@ -153,8 +153,10 @@ def test_append_errors_and_empty_calls(lib):
     w.sum_q = p.rows = a.sum_q = 0
     assert lib.smla_window_attention(ctypes.byref(w), None) == B.SMLA_OK
     assert lib.smla_cache_append(ctypes.byref(a), None) == B.SMLA_OK
-    for f in (lib.smla_pages_resize, lib.smla_pages_fork, lib.smla_pages_compact):
-        assert f(ctypes.byref(p), None) == B.SMLA_OK
+    assert lib.smla_pages_fork(ctypes.byref(p), None) == B.SMLA_OK
+    p.move_count = None                                    # (these two set it to 0 on the device)
+    for f in (lib.smla_pages_resize, lib.smla_pages_compact):
+        refused(f(ctypes.byref(p), None), B.SMLA_ERR_INVALID_ARG, "move_count is required")
 
 
 @pytest.mark.parametrize("call,field,value,code,needle", [
@@ -179,6 +181,8 @@ def test_append_errors_and_empty_calls(lib):
     ("fork", "parents", None, B.SMLA_ERR_INVALID_ARG, "parents"),
     ("fork", "out_lens", None, B.SMLA_ERR_INVALID_ARG, "out_lens"),
     ("fork", "out_lens", 0x30000, B.SMLA_ERR_INVALID_ARG, "must not be lens"),
+    ("fork", "out_lens", 0x30004, B.SMLA_ERR_INVALID_ARG, "overlap"),
+    ("fork", "out_lens", 0x2fffc, B.SMLA_ERR_INVALID_ARG, "overlap"),
     ("fork", "error_word", 0x60002, B.SMLA_ERR_INVALID_ARG, "error_word"),
 ])
 def test_pages_errors(lib, call, field, value, code, needle):
@@ -258,6 +262,8 @@ def test_binding_refuses_host_tensors_in_every_call():
     two = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA device"):
         C.pages_resize(**t, new_lens=two, workspace_buffer=ws, page_size=16, moves=moves)
+    with pytest.raises(ValueError, match="workspace"):
+        C.pages_resize(**t, new_lens=two, workspace_buffer=None, page_size=16, moves=moves)
     with pytest.raises(ValueError, match="new_lens has 1"):
         C.pages_resize(**t, new_lens=two[:1], workspace_buffer=ws, page_size=16, moves=moves)
     with pytest.raises(ValueError, match="CUDA device"):

@@ -41,6 +41,28 @@
 // hold (NaN codes of memory never written) reaches O.
 //
 // Sums and maxima are fp32, O accumulates in fp32; split partials are fp32.
+//
+// CTAs are persistent, one an SM, and take units (64 heads of a token, a range
+// of its tiles) in turn.  Sixteen warps do the softmax (all 128 rows, 16 heads
+// a thread); four others issue the first products, issue the second ones, load
+// rows, and look up scales.  Two tiles are in flight: while one is in the
+// softmax, the other's products run, and each second product frees its tile by
+// quarters, so that the next rows land behind it.
+//
+// What bounds it: a tile costs a CTA 2.1 us (4000 clocks), of which its tensor
+// instructions take 2670 (16 first products of 67 clocks; 32 second ones of 50,
+// not 32: with N = 64 they wait for their A operand out of shared memory).  The
+// rest is the chain second product -> free quarter -> rows -> first product ->
+// softmax of a buffer, which two 64 KB tiles (Q takes 64 KB, P 32) cannot hide
+// whole, and 7 us a unit for its query, sums and results.  Measured on a GB300:
+// 128 requests of one token, 128 heads, 2052 rows: 92 us, 744 TFLOP/s of the
+// plain products' count; 2836 tokens of four prompts, 128 heads, a window of 512:
+// 582 us, 476 TFLOP/s; two requests of 64 heads and 2 tiles: 13 us.
+//
+// Tried and slower (at these sizes): both products issued by one warp (decode
+// 114 us against 98), warps of their own for the query (prefill 688 against
+// 577), waits that poll (613 against 606), two or four times less headroom in
+// the reference (prefill 552 to 564, at twice the error).
 #include <cuda.h>
 
 #include <algorithm>

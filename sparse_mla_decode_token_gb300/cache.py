@@ -1,5 +1,9 @@
 """The paged latent cache: tensor-level calls (argument marshalling only).
 
+A call whose tensors are plain goes through the extension module of
+``csrc/cache_torch.cpp``; the functions below take the others: they name what is
+wrong, or handle what is legal but unusual.
+
 A cache is what the caller owns: E4M3 rows ``[num_pages, page_size, 512]``,
 float32 scales ``[num_pages, page_size // block_rows]`` (one per block of
 tokens), int32 page tables ``[requests, max_pages]``, lengths ``[requests]``
@@ -17,6 +21,8 @@ stream unless ``stream`` is given, and none waits.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -86,9 +92,31 @@ def new_moves(capacity: int, device) -> PageMoves:
                      torch.zeros(1, dtype=torch.int32, device=device))
 
 
-# A decode step makes these calls once a layer, so their checks are written as
-# one condition each, in the order that costs least; what fails it is looked
-# for, and named, in the functions that raise.
+_extension = None
+EXTENSION_PATH = os.path.join(os.path.dirname(_b.LIB_PATH), "smla_torch.so")
+
+
+def extension():
+    """The extension module (raises if it has not been built)."""
+    global _extension
+    if _extension is None:
+        if not os.path.exists(EXTENSION_PATH):
+            raise ImportError(f"smla_torch.so is not built ({EXTENSION_PATH}); run "
+                              "sparse_mla_decode_token_gb300.build.build() first")
+        _b.lib()
+        spec = importlib.util.spec_from_file_location("smla_torch", EXTENSION_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _extension = module
+    return _extension
+
+
+def _int32(name: str, value) -> int:
+    value = int(value)
+    if not -(1 << 31) <= value < 1 << 31:
+        raise ValueError(f"{name} {value} is not a 32-bit integer")
+    return value
+
 
 def _words(name: str, t: Optional[torch.Tensor], need: int, dtype=torch.int32) -> None:
     """An array that the kernels index: its type, contiguous, long enough."""
@@ -116,13 +144,8 @@ def _on(index: int, tensors, names) -> None:
 
 def _call(function, index: int, stream: Optional[int], *args) -> None:
     """The entry point on the tensors' device and stream."""
-    if torch.cuda.current_device() == index:
-        status = function(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
-    else:
-        with torch.cuda.device(index):
-            status = function(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
-    if status:
-        _check(status)
+    with torch.cuda.device(index):
+        _check(function(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream))
 
 
 def _table(name: str, t: torch.Tensor) -> None:
@@ -158,14 +181,9 @@ def _check_cache(rows: torch.Tensor, scales: torch.Tensor, tables: torch.Tensor)
 
 def _cache(rows: torch.Tensor, scales: torch.Tensor, tables: torch.Tensor, seq_lens: torch.Tensor,
            cum: Optional[torch.Tensor]) -> SmlaCache:
+    _check_cache(rows, scales, tables)
     rs, ss, ts = rows.shape, scales.shape, tables.shape
     rt, st, tt = rows.stride(), scales.stride(), tables.stride()
-    dense = rs[1:] and ss[1:] and ts[1:] and len(rs) == 3 and len(ss) == 2 and len(ts) == 2
-    if not (dense and (rows.dtype is torch.float8_e4m3fn or rows.dtype is torch.uint8)
-            and scales.dtype is torch.float32 and tables.dtype is torch.int32
-            and rs[2] == HEAD_DIM and rt[2] == st[1] == tt[1] == 1 and ss[0] == rs[0] > 0
-            and rs[1] % ss[1] == 0 and rt[0] > 0 and rt[1] > 0 and st[0] >= ss[1] and tt[0] >= ts[1] and ts[0] > 0):
-        _check_cache(rows, scales, tables)     # raises, or the odd strides are those of dims of one entry
     num_pages, page_size = rs[0], rs[1]
     batch, max_pages = ts
     _words("seq_lens", seq_lens, batch)
@@ -185,9 +203,10 @@ def _window_args(q, rows, scales, tables, seq_lens, cum, sinks, window, first_to
         raise ValueError(f"q must be [T, H, {HEAD_DIM}] with contiguous heads; got {tuple(qs)}")
     if sinks is not None:
         _words("sinks", sinks, qs[1], torch.float32)
-    return SmlaWindowArgs(_cache(rows, scales, tables, seq_lens, cum), qs[0], qs[1], int(window), int(first_tokens),
+    return SmlaWindowArgs(_cache(rows, scales, tables, seq_lens, cum), qs[0], qs[1], _int32("window", window),
+                          _int32("first_tokens", first_tokens),
                           q.data_ptr(), qt[0] if qs[0] > 1 else 0, None if sinks is None else sinks.data_ptr(),
-                          1.0, 1.0, None, None, None, None, None, 0, int(num_splits), None)
+                          1.0, 1.0, None, None, None, None, None, 0, _int32("num_splits", num_splits), None)
 
 
 def window_workspace_size(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block_tables: torch.Tensor,
@@ -215,6 +234,13 @@ def window_attention(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, 
     """Attention of BF16 queries ``[T, H, 512]`` over the last ``window`` cached
     tokens of their request up to their own position, and its first
     ``first_tokens``; returns ``(out, out_lse)``, allocated when not given."""
+    done = (_extension or extension()).window_attention(
+        q, rows, scales, block_tables, seq_lens, workspace_buffer, cum_seq_lens_q, sinks, window, first_tokens, num_splits,
+        bmm1_scale, bmm2_scale, out, out_lse, error_word, stream)
+    if done.__class__ is tuple:
+        return done
+    if done is not None:
+        _check(done)
     a = _window_args(q, rows, scales, block_tables, seq_lens, cum_seq_lens_q, sinks, window, first_tokens, num_splits)
     T, H = a.sum_q, a.num_heads
     if out is None:
@@ -261,6 +287,10 @@ def append(latent: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block
            error_word: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> None:
     """Quantises the new latent rows ``[T, 512]`` (BF16) into the cache, at the
     last positions of their requests (``seq_lens`` counts them)."""
+    status = (_extension or extension()).append(latent, rows, scales, block_tables, seq_lens, cum_seq_lens_q, error_word,
+                                                stream)
+    if status is not None:
+        return _check(status) if status else None
     ls, lt = latent.shape, latent.stride()
     if latent.dtype is not torch.bfloat16:
         raise TypeError(f"latent must be bfloat16; got {latent.dtype}")
@@ -276,10 +306,8 @@ def append(latent: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block
 
 def _pages_args(tables, ref_counts, lens, page_size, error_word, new_lens=None, parents=None, out_lens=None,
                 moves=(None, None, None), workspace=None) -> SmlaPagesArgs:
-    ts, tt = tables.shape, tables.stride()
-    if not (len(ts) == 2 and tables.dtype is torch.int32 and tt[1] == 1 and tt[0] >= ts[1] > 0):
-        _table("block_tables", tables)         # raises, or the odd stride is that of a dim of one entry
-    rows, max_pages = ts
+    _table("block_tables", tables)
+    rows, max_pages = tables.shape
     _words("ref_counts", ref_counts, 1)
     _words("lens", lens, rows)
     _words("error_word", error_word, 1)
@@ -295,7 +323,8 @@ def _pages_args(tables, ref_counts, lens, page_size, error_word, new_lens=None, 
         _words("moves.count", count, 1)
         if workspace is None or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor")
-    return SmlaPagesArgs(tables.data_ptr(), tt[0] if rows > 1 else max_pages, rows, max_pages, int(page_size),
+    return SmlaPagesArgs(tables.data_ptr(), tables.stride(0) if rows > 1 else max_pages, rows, max_pages,
+                         _int32("page_size", page_size),
                          ref_counts.data_ptr(), ref_counts.numel(), lens.data_ptr(), _ptr(new_lens), _ptr(parents),
                          _ptr(out_lens), _ptr(src), _ptr(dst), _ptr(count), capacity, _ptr(workspace),
                          0 if workspace is None else workspace.nbytes, _ptr(error_word))
@@ -304,7 +333,7 @@ def _pages_args(tables, ref_counts, lens, page_size, error_word, new_lens=None, 
 def pages_workspace_size(block_tables: torch.Tensor, ref_counts: torch.Tensor, page_size: int) -> int:
     """Workspace bytes of ``pages_resize`` and ``pages_compact`` (no device memory is read)."""
     a = SmlaPagesArgs()
-    a.rows, a.max_pages, a.page_size = block_tables.shape[0], block_tables.shape[1], int(page_size)
+    a.rows, a.max_pages, a.page_size = block_tables.shape[0], block_tables.shape[1], _int32("page_size", page_size)
     a.num_pages = ref_counts.numel()
     n = ctypes.c_size_t(0)
     _check(_b.lib().smla_pages_workspace_size(ctypes.byref(a), ctypes.byref(n)))
@@ -321,6 +350,10 @@ def pages_resize(block_tables: torch.Tensor, ref_counts: torch.Tensor, lens: tor
     """Takes each request from ``lens`` to ``new_lens`` tokens: pages dropped,
     then the lowest free pages handed out; ``moves`` receives the shared pages
     that a growing request got a copy of (``pages_copy`` them)."""
+    status = (_extension or extension()).pages_resize(block_tables, ref_counts, lens, new_lens, workspace_buffer, page_size,
+                                                      moves, error_word, stream)
+    if status is not None:
+        return _check(status) if status else None
     a = _pages_args(block_tables, ref_counts, lens, page_size, error_word, new_lens=new_lens, moves=moves,
                     workspace=workspace_buffer)
     index = block_tables.get_device()
@@ -333,6 +366,10 @@ def pages_fork(block_tables: torch.Tensor, ref_counts: torch.Tensor, lens: torch
                stream: Optional[int] = None) -> None:
     """Requests with ``parents[b] >= 0`` (which hold nothing) share their
     parent's pages; ``out_lens`` receives every request's length after it."""
+    status = (_extension or extension()).pages_fork(block_tables, ref_counts, lens, parents, out_lens, page_size, error_word,
+                                                    stream)
+    if status is not None:
+        return _check(status) if status else None
     a = _pages_args(block_tables, ref_counts, lens, page_size, error_word, parents=parents, out_lens=out_lens)
     index = block_tables.get_device()
     _on(index, (block_tables, ref_counts, lens, parents, out_lens, error_word),
@@ -345,6 +382,10 @@ def pages_compact(block_tables: torch.Tensor, ref_counts: torch.Tensor, lens: to
                   error_word: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> None:
     """Renumbers the pages in use to the front of the pool; ``moves`` receives
     the pages to copy (``pages_copy``) before the cache is used again."""
+    status = (_extension or extension()).pages_compact(block_tables, ref_counts, lens, workspace_buffer, page_size, moves,
+                                                       error_word, stream)
+    if status is not None:
+        return _check(status) if status else None
     a = _pages_args(block_tables, ref_counts, lens, page_size, error_word, moves=moves, workspace=workspace_buffer)
     index = block_tables.get_device()
     _on(index, (block_tables, ref_counts, lens, None, workspace_buffer, *moves, error_word), _PAGES_TENSORS)
@@ -356,6 +397,9 @@ def pages_copy(pools: Sequence[torch.Tensor], moves, *, error_word: Optional[tor
     """Copies the pages of ``moves`` within every pool: tensors ``[num_pages,
     ...]`` of any type whose pages are contiguous (rows and scales of all
     layers in one call)."""
+    status = (_extension or extension()).pages_copy(pools, moves, error_word, stream)
+    if status is not None:
+        return _check(status) if status else None
     src, dst, count = moves
     capacity = src.numel()
     _words("moves.src", src, 0)

@@ -759,3 +759,71 @@ def test_calls_on_another_stream_and_device_index():
                        bmm1_scale=1 / math.sqrt(512), stream=side.cuda_stream)
     side.synchronize()
     check(cache, q, (out.to(torch.float64).cpu().numpy(), lse.to(torch.float64).cpu().numpy()), window=256)
+
+
+class NoExtension:
+    """Answers every call with None: the Python functions do all of it."""
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+def all_calls():
+    """Results of every call once, on one state."""
+    cache, q, rng = make(50, [700, 40, 300], [2, 1, 3], heads=80)
+    g, cum = on_gpu(cache), i32([0, 2, 3, 6])
+    qt, x = bf16(q)[0], bf16(rng.normal(size=(6, 512)))[0]
+    ws = workspace(qt, g, window=500, cum_seq_lens_q=cum)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    sinks, two = torch.linspace(-2, 2, 80, device=DEV), torch.tensor([2.0], device=DEV)
+    C.append(x, g["rows"], g["scales"], g["block_tables"], g["seq_lens"], cum_seq_lens_q=cum, error_word=err)
+    o, l = C.window_attention(qt, g["rows"], g["scales"], g["block_tables"], g["seq_lens"], ws, window=500, first_tokens=3,
+                              cum_seq_lens_q=cum, sinks=sinks, bmm1_scale=0.05, bmm2_scale=two, error_word=err)
+    o2, l2 = torch.empty_like(o), torch.empty_like(l)
+    assert C.window_attention(qt, g["rows"], g["scales"], g["block_tables"], g["seq_lens"], ws, window=500, first_tokens=3,
+                              cum_seq_lens_q=cum, sinks=sinks, bmm1_scale=0.05, bmm2_scale=two, out=o2, out_lse=l2,
+                              num_splits=2, stream=torch.cuda.current_stream().cuda_stream) == (o2, l2)
+    tables, refs = torch.full((4, 6), -1, dtype=torch.int32, device=DEV), torch.zeros(20, dtype=torch.int32, device=DEV)
+    pws, moves = torch.empty(C.pages_workspace_size(tables, refs, 16), dtype=torch.uint8, device=DEV), C.new_moves(10, DEV)
+    C.pages_resize(tables, refs, i32([0] * 4), i32([40, 20, 0, 0]), pws, page_size=16, moves=moves, error_word=err)
+    lens = torch.empty(4, dtype=torch.int32, device=DEV)
+    C.pages_fork(tables, refs, i32([40, 20, 0, 0]), i32([-1, -1, 0, 0]), lens, page_size=16, error_word=err)
+    C.pages_resize(tables, refs, lens.clone(), i32([0, 21, 41, 41]), pws, page_size=16, moves=moves, error_word=err)
+    pool = torch.arange(20 * 6, device=DEV).view(20, 2, 3).clone()
+    C.pages_copy([pool], moves, error_word=err)
+    kept = [m.clone() for m in moves]
+    C.pages_compact(tables, refs, i32([0, 21, 41, 41]), pws, page_size=16, moves=moves, error_word=err)
+    C.pages_copy((pool, pool.new_zeros(20, 1)), moves, error_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    return [g["rows"], g["scales"], o, l, o2, l2, tables, refs, lens, pool, moves.count] + kept
+
+
+def test_both_ways_into_the_library(monkeypatch):
+    """Plain tensors take the extension all the way; without it the Python functions give the same."""
+    C.extension()
+    with monkeypatch.context() as m:
+        for name in ("_window_args", "_cache", "_pages_args", "_call"):
+            m.setattr(C, name, lambda *a, **k: pytest.fail("not through the extension"))
+        m.setattr(C, "window_workspace_size", lambda *a, **k: 1 << 24)
+        m.setattr(C, "pages_workspace_size", lambda *a, **k: 1 << 16)
+        fast = all_calls()
+    monkeypatch.setattr(C, "_extension", NoExtension())
+    for a, b in zip(fast, all_calls()):
+        a, b = (t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t for t in (a, b))
+        assert torch.equal(a.nan_to_num() if a.is_floating_point() else a, b.nan_to_num() if b.is_floating_point() else b)
+
+
+def test_refusals_through_the_extension():
+    cache, q, _ = make(51, [100], [1])
+    g, qt = on_gpu(cache), bf16(q)[0]
+    call = lambda **k: C.window_attention(**{**dict(q=qt, workspace_buffer=None, window=4, **g), **k})
+    for over, exc, match in ((dict(window=0), B.SmlaError, "window"), (dict(window=1 << 40), ValueError, "32-bit"),
+                             (dict(num_splits=2), B.SmlaError, "workspace"), (dict(q=qt.float()), TypeError, "bfloat16"),
+                             (dict(seq_lens=g["seq_lens"].long()), TypeError, "int32"),
+                             (dict(seq_lens=g["seq_lens"].cpu()), ValueError, "CUDA device"),
+                             (dict(out=torch.empty(1, 64, 511, dtype=torch.bfloat16, device=DEV)), ValueError, "out must"),
+                             (dict(bmm1_scale=torch.ones(1, dtype=torch.float64, device=DEV)), TypeError, "float32")):
+        with pytest.raises(exc, match=match):
+            call(**over)
+    out, _ = call(bmm1_scale=1, bmm2_scale=True)            # numbers of other kinds
+    assert torch.isfinite(out.float()).all()

@@ -342,3 +342,30 @@ def test_reference_pages_by_hand():
     assert p.compact(np.array([7, 5, 7])) == [(5, 1)] and p.tables[2].tolist() == [0, 1, -1, -1]
     _, short = p.resize(np.array([7, 5, 7]), np.array([16, 16, 7]))
     assert short and p.tables[0].tolist() == [0, 3, 5, 6] and p.tables[1].tolist() == [2, 4, 7, -1]
+
+
+def test_numbers_past_32_bits_are_refused():
+    for name in ("window", "first_tokens", "num_splits"):
+        with pytest.raises(ValueError, match=f"{name} .* 32-bit"):
+            C.window_attention(**host_tensors(**{name: (1 << 32) + 5}))
+    with pytest.raises(ValueError, match="page_size .* 32-bit"):
+        C.pages_workspace_size(torch.zeros(2, 4, dtype=torch.int32), torch.zeros(9, dtype=torch.int32), (1 << 32) + 8)
+
+
+def test_missing_extension_raises(monkeypatch, tmp_path):
+    monkeypatch.setattr(C, "_extension", None)
+    monkeypatch.setattr(C, "EXTENSION_PATH", str(tmp_path / "missing.so"))
+    with pytest.raises(ImportError, match="not built"):
+        C.window_attention(**host_tensors())
+
+
+def test_extension_leaves_what_is_not_plain_to_the_python_functions():
+    """No tensors, host tensors and odd numbers of arguments never reach an entry point."""
+    e = C.extension()
+    x = torch.zeros(4, 512, dtype=torch.bfloat16)
+    for f, n in ((e.window_attention, 17), (e.append, 8), (e.pages_resize, 9), (e.pages_fork, 8), (e.pages_compact, 8),
+                 (e.pages_copy, 4)):
+        assert f(*[None] * n) is None and f(*[x] * n) is None and f(*[3] * n) is None and f(*[[x]] * n) is None
+        assert f(*[(x, x, x)] * n) is None
+        with pytest.raises(TypeError, match="arguments"):
+            f(*[None] * (n - 1))

@@ -20,11 +20,42 @@ struct CacheView {
   int32_t sum_q;
 };
 
+// The calls of a step follow one another on a stream, most of them short, so each
+// kernel is launched while the one before it ends (programmatic dependent
+// launch): it waits for all of that one's writes before it reads anything, and
+// lets the next come as soon as it runs itself.
+__device__ __forceinline__ void await_prior_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void admit_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// A load of what a kernel before may have written.  Not by the read-only path,
+// which holds its lines for a kernel's whole life: that began before those writes.
+template <class T>
+__device__ __forceinline__ T fetch(const T* p) {
+  return *p;
+}
+__device__ __forceinline__ float fetch_scale(float value, const float* dev) { return dev != nullptr ? fetch(dev) : value; }
+
+template <class... P, class... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                              const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Request b's new tokens: [first, first + count) of the flattened batch.
 __device__ __forceinline__ void request_tokens(const CacheView& c, int b, int* first, int* count) {
   if (c.cum != nullptr) {
-    *first = __ldg(c.cum + b);
-    *count = __ldg(c.cum + b + 1) - *first;
+    *first = fetch(c.cum + b);
+    *count = fetch(c.cum + b + 1) - *first;
   } else {
     const int q = c.sum_q / c.batch;
     *first = b * q;

@@ -63,6 +63,8 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
   // unit u -> (request, block): request b's units start at first(b) / block_rows + 2 b,
   // which leaves room for the blocks its tokens can touch, count / block_rows + 2
   const int64_t u = blockIdx.x;
+  await_prior_kernel();
+  admit_next_kernel();
   const int b = last_request(c.batch, threadIdx.x & 31, [&](int at) {
     int f, n;
     request_tokens(c, at, &f, &n);
@@ -71,7 +73,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
   int first, count;
   request_tokens(c, b, &first, &count);
   if (first < 0 || count <= 0 || count > c.sum_q - first) return;       // (offsets that are none: nothing is written)
-  const int start = __ldg(c.seq_lens + b) - count;                      // position of the first new token
+  const int start = fetch(c.seq_lens + b) - count;                      // position of the first new token
   const int end = start + count, from0 = max(start, 0);
   const int i = (int)(u - (first / c.block_rows + 2 * (int64_t)b));     // block of the request's touched ones
   if (i == 0 && start < 0 && threadIdx.x == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
   const int column = (int)block0 / c.page_size;
   const int row0 = (int)block0 - column * c.page_size;                  // the block's first row in its page
   // (the page is on its way while the rows are read)
-  const int page = column < c.max_pages ? __ldg(c.bt + (int64_t)b * c.bt_stride + column) : -1;
+  const int page = column < c.max_pages ? fetch(c.bt + (int64_t)b * c.bt_stride + column) : -1;
   const int older = pos0 - (int)block0, rows = pos1 - pos0;
   const __nv_bfloat16* src = p.latent + (first + (pos0 - start)) * p.latent_stride;
   const int group = threadIdx.x >> 6, lane8 = threadIdx.x & 63;         // row parity, 8 values
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) {
     const int r = k * kGroups + group;
-    if (r < rows) held[k] = __ldg(reinterpret_cast<const uint4*>(src + r * p.latent_stride) + lane8);
+    if (r < rows) held[k] = fetch(reinterpret_cast<const uint4*>(src + r * p.latent_stride) + lane8);
   }
   if (page < 0 || page >= c.num_pages) {
     if (threadIdx.x == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
   for (int k = 0; k < kHeld; ++k)
     if (k * kGroups + group < rows) m = amax8(held[k], m);
   for (int r = kHeld * kGroups + group; r < rows; r += kGroups)
-    m = amax8(__ldg(reinterpret_cast<const uint4*>(src + r * p.latent_stride) + lane8), m);
+    m = amax8(fetch(reinterpret_cast<const uint4*>(src + r * p.latent_stride) + lane8), m);
   m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));   // not negative: orders as integers
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();                                        // also: every thread has read the old scale
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
     }
     for (int r = kHeld * kGroups + group; r < rows; r += kGroups)
       reinterpret_cast<uint2*>(dst + r * c.row_stride)[lane8] =
-          quantise8<kPow2>(__ldg(reinterpret_cast<const uint4*>(src + r * p.latent_stride) + lane8), by);
+          quantise8<kPow2>(fetch(reinterpret_cast<const uint4*>(src + r * p.latent_stride) + lane8), by);
   };
   const uint32_t bits = __float_as_uint(s);
   // a normal power of two whose reciprocal is one too
@@ -160,8 +162,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
 
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream) {
   const int64_t units = (int64_t)p.c.sum_q / p.c.block_rows + 2 * (int64_t)p.c.batch;
-  cache_append_kernel<<<(unsigned)units, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(cache_append_kernel, dim3((unsigned)units), kThreads, 0, stream, p);
 }
 
 }  // namespace smla

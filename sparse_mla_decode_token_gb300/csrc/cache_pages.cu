@@ -226,7 +226,7 @@ __device__ __forceinline__ void resize_drop(const PagesParams& p, const Team& w)
   pieces(p, w,
          [&](int b) {
            bool bad = false;
-           const int co = page_columns(p, __ldg(p.lens + b), &bad), cn = page_columns(p, __ldg(p.new_lens + b), &bad);
+           const int co = page_columns(p, fetch(p.lens + b), &bad), cn = page_columns(p, fetch(p.new_lens + b), &bad);
            if (bad) flag(p.err, SMLA_DEVERR_PAGE_STATE);
            return make_int2(cn, co);
          },
@@ -258,7 +258,7 @@ __device__ __forceinline__ void resize_rows(const PagesParams& p, const Resize& 
     int need = 0, cow = 0;
     if (b < p.rows) {
       bool bad = false;
-      const int old = clamped_len(p, __ldg(p.lens + b)), now = clamped_len(p, __ldg(p.new_lens + b));
+      const int old = clamped_len(p, fetch(p.lens + b)), now = clamped_len(p, fetch(p.new_lens + b));
       if (now > old) {
         need = page_columns(p, now, &bad) - page_columns(p, old, &bad);
         if (old % p.page_size != 0) {
@@ -319,12 +319,12 @@ __device__ __forceinline__ void resize_assign(const PagesParams& p, const Resize
   pieces(p, w,
          [&](int b) {
            bool bad = false;
-           const int old = clamped_len(p, __ldg(p.lens + b)), now = clamped_len(p, __ldg(p.new_lens + b));
+           const int old = clamped_len(p, fetch(p.lens + b)), now = clamped_len(p, fetch(p.new_lens + b));
            return now > old ? make_int2(page_columns(p, old, &bad), page_columns(p, now, &bad)) : make_int2(0, 0);
          },
          [&](int b, int from, int to) {
            bool bad = false;
-           const int co = page_columns(p, clamped_len(p, __ldg(p.lens + b)), &bad);
+           const int co = page_columns(p, clamped_len(p, fetch(p.lens + b)), &bad);
            const int o = __ldcg(r.off + b), k0 = (o >> 1) + (o & 1) - co;     // rank of column 0, as it were
            int32_t* row = p.bt + (int64_t)b * p.bt_stride;
            int page[4];
@@ -342,7 +342,7 @@ __device__ __forceinline__ void resize_assign(const PagesParams& p, const Resize
   for (int b = w.cta * kPlanThreads + threadIdx.x; b < p.rows; b += w.ctas * kPlanThreads) {
     const int o = __ldcg(r.off + b), k = o >> 1;
     if ((o & 1) != 0 && k < take) {
-      int32_t* at = p.bt + (int64_t)b * p.bt_stride + clamped_len(p, __ldg(p.lens + b)) / p.page_size;
+      int32_t* at = p.bt + (int64_t)b * p.bt_stride + clamped_len(p, fetch(p.lens + b)) / p.page_size;
       const int from = __ldcg(at), to = __ldcg(r.list + k), m = __ldcg(r.cows + b);
       *at = to;
       atomicSub(p.refs + from, 1);
@@ -358,6 +358,8 @@ pages_resize_kernel(const PagesParams p) {
   __shared__ Shared sh;
   const Team w = team((int)ptx::cluster_rank(), kClusterCtas);
   const Resize r = resize_state(p);
+  await_prior_kernel();
+  admit_next_kernel();
   resize_drop(p, w);
   __threadfence();
   ptx::cluster_sync();
@@ -378,8 +380,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_resize_phase_kernel(con
   __shared__ Shared sh;
   const Team w = team(blockIdx.x, gridDim.x);
   const Resize r = resize_state(p);
-  if constexpr (kPhase > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if constexpr (kPhase < 3) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  await_prior_kernel();
+  admit_next_kernel();
   if constexpr (kPhase == 0) {
     resize_drop(p, w);
   } else if constexpr (kPhase == 1) {
@@ -398,13 +400,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_resize_phase_kernel(con
 __global__ void __launch_bounds__(256) pages_fork_kernel(const PagesParams p) {
   const int b = (int)((blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
   if (b >= p.rows) return;
-  const int parent = __ldg(p.parents + b), own_len = __ldg(p.lens + b);
+  await_prior_kernel();
+  admit_next_kernel();
+  const int parent = fetch(p.parents + b), own_len = fetch(p.lens + b);
   int len = own_len;
   if (parent >= 0) {
     if (parent >= p.rows || own_len != 0) {
       if (lane == 0) flag(p.err, SMLA_DEVERR_PAGE_STATE);
     } else {
-      len = __ldg(p.lens + parent);
+      len = fetch(p.lens + parent);
       bool bad = false;
       const int n = page_columns(p, len, &bad);
       if (bad && lane == 0) flag(p.err, SMLA_DEVERR_PAGE_STATE);
@@ -476,6 +480,8 @@ pages_compact_kernel(const PagesParams p) {
   __shared__ Shared sh;
   const Team w = team((int)ptx::cluster_rank(), kClusterCtas);
   const Compact c = compact_state(p);
+  await_prior_kernel();
+  admit_next_kernel();
   count_chunks(p, c.counts, c.chunks, w);
   __threadfence();
   ptx::cluster_sync();
@@ -492,8 +498,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_compact_phase_kernel(co
   __shared__ Shared sh;
   const Team w = team(blockIdx.x, gridDim.x);
   const Compact c = compact_state(p);
-  if constexpr (kPhase > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if constexpr (kPhase < 2) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  await_prior_kernel();
+  admit_next_kernel();
   if constexpr (kPhase == 0) count_chunks(p, c.counts, c.chunks, w);
   else if constexpr (kPhase == 1) compact_moves(p, c, w, sh);
   else compact_counts(p, w, __ldcg(p.ws) - __ldcg(p.ws + 1));
@@ -503,7 +509,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_compact_phase_kernel(co
 __global__ void __launch_bounds__(256) pages_renumber_kernel(const PagesParams p) {
   const int b = blockIdx.x;
   bool bad = false;
-  const int n = page_columns(p, __ldg(p.lens + b), &bad);
+  await_prior_kernel();
+  admit_next_kernel();
+  const int n = page_columns(p, fetch(p.lens + b), &bad);
   if (bad && threadIdx.x == 0 && blockIdx.y == 0) flag(p.err, SMLA_DEVERR_PAGE_STATE);
   const int live = __ldcg(p.ws), moves = live - __ldcg(p.ws + 1);
   const int32_t* move_of = p.ws + kPagesHeader;
@@ -542,7 +550,7 @@ __device__ __forceinline__ void copy_unit(const CopyParams& p, const CopyParams:
     to[u] = nullptr;
     if (first + i < total) {
       const uint32_t dm = (r0 + i) / (uint32_t)pool.pieces, r = r0 + i - dm * (uint32_t)pool.pieces;
-      const int src = __ldg(p.src + m0 + dm), dst = __ldg(p.dst + m0 + dm);
+      const int src = fetch(p.src + m0 + dm), dst = fetch(p.dst + m0 + dm);
       if (src >= 0 && src < p.num_pages && dst >= 0 && dst < p.num_pages) {
         v[u] = *reinterpret_cast<const V*>(pool.base + (int64_t)src * pool.stride + (int64_t)r * sizeof(V));
         to[u] = pool.base + (int64_t)dst * pool.stride + (int64_t)r * sizeof(V);
@@ -557,7 +565,9 @@ __device__ __forceinline__ void copy_unit(const CopyParams& p, const CopyParams:
 }
 
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ CopyParams p) {
-  const int64_t moves = min(max(__ldg(p.count), 0), p.capacity);
+  await_prior_kernel();
+  admit_next_kernel();
+  const int64_t moves = min(max(fetch(p.count), 0), p.capacity);
   int64_t unit = blockIdx.x, done = 0;                    // units of the pools before this one
   for (int k = 0; k < p.num_pools; ++k) {
     const CopyParams::Pool& pool = p.pool[k];
@@ -579,61 +589,42 @@ namespace {
 bool one_cluster(const PagesParams& p) { return (int64_t)p.rows * p.max_pages + p.num_pages <= kClusterEntries; }
 
 // CTAs of a phase over the whole GPU: one an SM, no more than there is work for.
-int phase_ctas(int64_t warps, int sms) {
+unsigned phase_ctas(int64_t warps, int sms) {
   const int64_t n = (warps + kWarps - 1) / kWarps;
-  return (int)(n < 1 ? 1 : n < sms ? n : sms);
-}
-
-template <class K>
-cudaError_t launch_phase(K kernel, int ctas, bool dependent, const PagesParams& p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return (unsigned)(n < 1 ? 1 : n < sms ? n : sms);
 }
 
 }  // namespace
 
 cudaError_t launch_pages_resize(const PagesParams& p, int sms, cudaStream_t stream) {
-  if (one_cluster(p)) {
-    pages_resize_kernel<<<kClusterCtas, kPlanThreads, 0, stream>>>(p);
-    return cudaGetLastError();
-  }
-  const int tables = phase_ctas((int64_t)p.rows * ((p.max_pages + 127) / 128), sms);
-  const int pages = phase_ctas(((int64_t)p.num_pages + kChunk - 1) / kChunk, sms);
-  cudaError_t e = launch_phase(pages_resize_phase_kernel<0>, tables, false, p, stream);
-  if (e == cudaSuccess) e = launch_phase(pages_resize_phase_kernel<1>, pages, true, p, stream);
-  if (e == cudaSuccess) e = launch_phase(pages_resize_phase_kernel<2>, pages, true, p, stream);
-  if (e == cudaSuccess) e = launch_phase(pages_resize_phase_kernel<3>, tables, true, p, stream);
+  if (one_cluster(p)) return launch_overlapped(pages_resize_kernel, dim3(kClusterCtas), kPlanThreads, 0, stream, p);
+  const dim3 tables(phase_ctas((int64_t)p.rows * ((p.max_pages + 127) / 128), sms));
+  const dim3 pages(phase_ctas(((int64_t)p.num_pages + kChunk - 1) / kChunk, sms));
+  cudaError_t e = launch_overlapped(pages_resize_phase_kernel<0>, tables, kPlanThreads, 0, stream, p);
+  if (e == cudaSuccess) e = launch_overlapped(pages_resize_phase_kernel<1>, pages, kPlanThreads, 0, stream, p);
+  if (e == cudaSuccess) e = launch_overlapped(pages_resize_phase_kernel<2>, pages, kPlanThreads, 0, stream, p);
+  if (e == cudaSuccess) e = launch_overlapped(pages_resize_phase_kernel<3>, tables, kPlanThreads, 0, stream, p);
   return e;
 }
 
 cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream) {
-  pages_fork_kernel<<<(unsigned)((p.rows + 7) / 8), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(pages_fork_kernel, dim3((unsigned)((p.rows + 7) / 8)), 256, 0, stream, p);
 }
 
 cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (one_cluster(p)) {
-    pages_compact_kernel<<<kClusterCtas, kPlanThreads, 0, stream>>>(p);
-    e = cudaGetLastError();
+    e = launch_overlapped(pages_compact_kernel, dim3(kClusterCtas), kPlanThreads, 0, stream, p);
   } else {
-    const int pages = phase_ctas(((int64_t)p.num_pages + kChunk - 1) / kChunk, sms);
-    e = launch_phase(pages_compact_phase_kernel<0>, pages, false, p, stream);
-    if (e == cudaSuccess) e = launch_phase(pages_compact_phase_kernel<1>, pages, true, p, stream);
-    if (e == cudaSuccess) e = launch_phase(pages_compact_phase_kernel<2>, pages, true, p, stream);
+    const dim3 pages(phase_ctas(((int64_t)p.num_pages + kChunk - 1) / kChunk, sms));
+    e = launch_overlapped(pages_compact_phase_kernel<0>, pages, kPlanThreads, 0, stream, p);
+    if (e == cudaSuccess) e = launch_overlapped(pages_compact_phase_kernel<1>, pages, kPlanThreads, 0, stream, p);
+    if (e == cudaSuccess) e = launch_overlapped(pages_compact_phase_kernel<2>, pages, kPlanThreads, 0, stream, p);
   }
   if (e != cudaSuccess) return e;
   const int cols = (p.max_pages + 255) / 256;
-  pages_renumber_kernel<<<dim3((unsigned)p.rows, (unsigned)(cols < 64 ? cols : 64)), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(pages_renumber_kernel, dim3((unsigned)p.rows, (unsigned)(cols < 64 ? cols : 64)), 256, 0, stream,
+                           p);
 }
 
 cudaError_t launch_pages_copy(const CopyParams& p, int sms, cudaStream_t stream) {
@@ -642,8 +633,7 @@ cudaError_t launch_pages_copy(const CopyParams& p, int sms, cudaStream_t stream)
   for (int k = 0; k < p.num_pools; ++k) pieces += ((int64_t)p.capacity * p.pool[k].pieces + kCopyUnit - 1) / kCopyUnit;
   const int64_t grid = pieces < (int64_t)sms * 16 ? pieces : (int64_t)sms * 16;
   if (grid == 0) return cudaSuccess;
-  pages_copy_kernel<<<(unsigned)grid, kCopyThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(pages_copy_kernel, dim3((unsigned)grid), kCopyThreads, 0, stream, p);
 }
 
 }  // namespace smla

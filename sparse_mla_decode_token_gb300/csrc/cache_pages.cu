@@ -10,12 +10,11 @@
 //
 // A call is a few phases, each needing all of the one before.  Small calls run
 // them in one launch, in one cluster of eight CTAs with cluster barriers between
-// (resize of 128 requests x 128 pages in a pool of 16 thousand: 12 us, of which
-// no phase is more than 4); where tables and pool together pass
-// kClusterEntries, eight SMs are too few and the phases are launches of their
-// own over the whole GPU, each overlapping its start with the end of the one
-// before (1024 requests x 1024 pages in a pool of a million: 71 us in a cluster,
-// 20 so).
+// (resize of 128 requests x 128 pages in a pool of 16 thousand: 9.4 us; 10.9 with
+// fences before the barriers, and with one CTA counting pages after summing the
+// requests' needs); where tables and pool together pass kClusterEntries, eight
+// SMs are too few and the phases are launches of their own over the whole GPU
+// (1024 requests x 1024 pages in a pool of a million: 71 us in a cluster, 20 so).
 // What bounds both is latency: the counts (4 bytes a page) are read once, and
 // again where pages are handed out; the rest is dependent trips to L2.
 #include "cache.cuh"
@@ -140,36 +139,47 @@ __device__ __forceinline__ void count_chunks(const PagesParams& p, int32_t* coun
   }
 }
 
-// The whole CTA walks its share of the chunks that `wanted(pages in use before
+// Ranks a batch of up to kPlanThreads chunks from c0 on, `before` pages being in
+// use before them: sh.prefix holds those before each chunk, the result counts the
+// batch in.  Whole CTA.
+__device__ __forceinline__ int rank_batch(const int32_t* counts, int chunks, int c0, int before, Shared& sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = c0 + threadIdx.x;
+  const int n = c < chunks ? __ldcg(counts + c) : 0;
+  int sum = n;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, sum, d);
+    if (lane >= d) sum += x;
+  }
+  if (lane == 31) sh.scan[0][warp] = sum;
+  __syncthreads();
+  sh.prefix[threadIdx.x] = before + sum - n + __reduce_add_sync(0xffffffffu, lane < warp ? sh.scan[0][lane] : 0);
+  before += __reduce_add_sync(0xffffffffu, sh.scan[0][lane]);
+  __syncthreads();
+  return before;
+}
+
+// The CTA's share of the chunks of a ranked batch that `wanted(pages in use before
 // the chunk, first page)` takes; f as for walk, with the pages in use before the
 // page in the whole pool.
 template <class W, class F>
+__device__ __forceinline__ void walk_batch(const PagesParams& p, int chunks, int c0, const Team& w, const Shared& sh, W wanted,
+                                           F f) {
+  const int batch = min(kPlanThreads, chunks - c0);
+  for (int k = (w.gw - c0 % w.warps + w.warps) % w.warps; k < batch; k += w.warps) {
+    const int live = sh.prefix[k];
+    const int64_t base = (int64_t)(c0 + k) * kChunk;
+    if (wanted(live, base)) walk(p, base, w.lane, [&](int page, int count, int in_chunk) { f(page, count, live + in_chunk); });
+  }
+}
+
+template <class W, class F>
 __device__ __forceinline__ void walk_chunks(const PagesParams& p, const int32_t* counts, int chunks, const Team& w,
                                             Shared& sh, W wanted, F f) {
-  const int warp = threadIdx.x >> 5, lane = w.lane;
-  int32_t* s_warp = sh.scan[0];
-  int32_t* s_prefix = sh.prefix;
   int before = 0;                                     // pages in use before this batch of chunks
   for (int c0 = 0; c0 < chunks; c0 += kPlanThreads) {
-    const int c = c0 + threadIdx.x;
-    const int n = c < chunks ? __ldcg(counts + c) : 0;
-    int sum = n;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, sum, d);
-      if (lane >= d) sum += x;
-    }
-    if (lane == 31) s_warp[warp] = sum;
-    __syncthreads();
-    s_prefix[threadIdx.x] = before + sum - n + __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0);
-    before += __reduce_add_sync(0xffffffffu, s_warp[lane]);
-    __syncthreads();
-    const int batch = min(kPlanThreads, chunks - c0);
-    for (int k = (w.gw - c0 % w.warps + w.warps) % w.warps; k < batch; k += w.warps) {
-      const int live = s_prefix[k];
-      const int64_t base = (int64_t)(c0 + k) * kChunk;
-      if (wanted(live, base)) walk(p, base, lane, [&](int page, int count, int in_chunk) { f(page, count, live + in_chunk); });
-    }
+    before = rank_batch(counts, chunks, c0, before, sh);
+    walk_batch(p, chunks, c0, w, sh, wanted, f);
     __syncthreads();
   }
 }
@@ -290,27 +300,26 @@ __device__ __forceinline__ void resize_rows(const PagesParams& p, const Resize& 
   if (threadIdx.x == 0) p.ws[0] = need0;
 }
 
-// Pages that can be handed out: the smaller of what is needed and what is free.
-__device__ __forceinline__ int resize_take(const PagesParams& p, const Resize& r, const Team& w, Shared& sh) {
+// 3. the lowest free pages, in order: the smaller of what is needed and what is free
+__device__ __forceinline__ int resize_list(const PagesParams& p, const Resize& r, const Team& w, Shared& sh) {
   const int need = __ldcg(p.ws);
-  if (need == 0) return 0;
-  const int have = p.num_pages - sum_counts(r.counts, r.chunks, sh);
-  if (need > have && w.cta == 0 && threadIdx.x == 0) flag(p.err, SMLA_DEVERR_OUT_OF_PAGES);
-  return min(need, have);
-}
-
-// 3. the lowest free pages, in order
-__device__ __forceinline__ void resize_list(const PagesParams& p, const Resize& r, const Team& w, Shared& sh, int take) {
-  if (take == 0) return;
-  walk_chunks(p, r.counts, r.chunks, w, sh,
-              [&](int live, int64_t base) { return base - live < take; },     // free pages before the chunk
-              [&](int page, int count, int live) {
-                const int k = page - live;
-                if (count <= 0 && k < take) {
-                  r.list[k] = page;
-                  p.refs[page] = 1;
-                }
-              });
+  // (one batch, which a cluster's pools are, is ranked and summed in one)
+  const bool one = r.chunks <= kPlanThreads;
+  const int live_all = one ? rank_batch(r.counts, r.chunks, 0, 0, sh) : need > 0 ? sum_counts(r.counts, r.chunks, sh) : 0;
+  const int take = min(need, p.num_pages - live_all);
+  if (need > take && w.cta == 0 && threadIdx.x == 0) flag(p.err, SMLA_DEVERR_OUT_OF_PAGES);
+  if (take == 0) return 0;
+  const auto wanted = [&](int live, int64_t base) { return base - live < take; };   // free pages before the chunk
+  const auto give = [&](int page, int count, int live) {
+    const int k = page - live;
+    if (count <= 0 && k < take) {
+      r.list[k] = page;
+      p.refs[page] = 1;
+    }
+  };
+  if (one) walk_batch(p, r.chunks, 0, w, sh, wanted, give);
+  else walk_chunks(p, r.counts, r.chunks, w, sh, wanted, give);
+  return take;
 }
 
 // 4. handed out: the pages of growing rows, then the copies of shared pages
@@ -339,7 +348,8 @@ __device__ __forceinline__ void resize_assign(const PagesParams& p, const Resize
              if (c < to) row[c] = page[k];
            }
          });
-  for (int b = w.cta * kPlanThreads + threadIdx.x; b < p.rows; b += w.ctas * kPlanThreads) {
+  // (from the CTA's last warp on, which the pieces reach last)
+  for (int b = w.cta + (kPlanThreads - 1 - (int)threadIdx.x) * w.ctas; b < p.rows; b += w.ctas * kPlanThreads) {
     const int o = __ldcg(r.off + b), k = o >> 1;
     if ((o & 1) != 0 && k < take) {
       int32_t* at = p.bt + (int64_t)b * p.bt_stride + clamped_len(p, fetch(p.lens + b)) / p.page_size;
@@ -361,15 +371,11 @@ pages_resize_kernel(const PagesParams p) {
   await_prior_kernel();
   admit_next_kernel();
   resize_drop(p, w);
-  __threadfence();
   ptx::cluster_sync();
-  if (w.cta == 0) resize_rows(p, r, sh);
-  count_chunks(p, r.counts, r.chunks, w);
-  __threadfence();
+  if (w.cta == 0) resize_rows(p, r, sh);              // beside the others' counting
+  else count_chunks(p, r.counts, r.chunks, team(w.cta - 1, kClusterCtas - 1));
   ptx::cluster_sync();
-  const int take = resize_take(p, r, w, sh);
-  resize_list(p, r, w, sh, take);
-  __threadfence();
+  const int take = resize_list(p, r, w, sh);
   ptx::cluster_sync();
   resize_assign(p, r, w, take);
 }
@@ -388,9 +394,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_resize_phase_kernel(con
     if (w.cta == 0) resize_rows(p, r, sh);
     count_chunks(p, r.counts, r.chunks, w);
   } else if constexpr (kPhase == 2) {
-    const int take = resize_take(p, r, w, sh);
+    const int take = resize_list(p, r, w, sh);
     if (w.cta == 0 && threadIdx.x == 0) p.ws[1] = take;
-    resize_list(p, r, w, sh, take);
   } else {
     resize_assign(p, r, w, __ldcg(p.ws + 1));
   }
@@ -483,10 +488,8 @@ pages_compact_kernel(const PagesParams p) {
   await_prior_kernel();
   admit_next_kernel();
   count_chunks(p, c.counts, c.chunks, w);
-  __threadfence();
   ptx::cluster_sync();
   const int moves = compact_moves(p, c, w, sh);
-  __threadfence();
   ptx::cluster_sync();
   compact_counts(p, w, moves);
 }

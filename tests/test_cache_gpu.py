@@ -827,3 +827,95 @@ def test_refusals_through_the_extension():
             call(**over)
     out, _ = call(bmm1_scale=1, bmm2_scale=True)            # numbers of other kinds
     assert torch.isfinite(out.float()).all()
+
+
+def chain(sync, steps=40, layers=2):
+    """A run of every call, one behind another without a host wait between (or with one): all it leaves."""
+    rng = np.random.default_rng(60)
+    rows, pages, size = 24, 200, 16
+    tables = torch.full((rows, 40), -1, dtype=torch.int32, device=DEV)
+    refs = torch.zeros(pages, dtype=torch.int32, device=DEV)
+    pool = [torch.zeros(pages, size, 512, dtype=torch.uint8, device=DEV) for _ in range(layers)]
+    scales = [torch.zeros(pages, size // 8, device=DEV) for _ in range(layers)]
+    ws = torch.empty(C.pages_workspace_size(tables, refs, size), dtype=torch.uint8, device=DEV)
+    wws = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+    moves, err = C.new_moves(pages, DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    latent = bf16(rng.normal(size=(steps, rows, 512)) * 2.0 ** rng.integers(-3, 4, size=(steps, rows, 1)))[0]
+    q = bf16(rng.normal(size=(steps, rows, 64, 512)))[0]
+    plan, lens = [], np.zeros(rows, dtype=np.int32)
+    for s in range(steps):                                 # ends, forks and growth by one token, all known beforehand
+        keep = np.where(rng.random(rows) < 0.1, 0, lens)
+        parents = np.full(rows, -1, dtype=np.int32)
+        alive = np.flatnonzero(keep > 0)
+        for b in np.flatnonzero(keep == 0):
+            if len(alive) and rng.random() < 0.5:
+                parents[b] = rng.choice(alive)
+        forked = np.where(parents >= 0, keep[np.maximum(parents, 0)], keep)
+        plan.append([i32(a) for a in (lens, keep, parents, forked + 1)])
+        lens = (forked + 1).astype(np.int32)
+    after, outs = torch.empty(rows, dtype=torch.int32, device=DEV), []
+    pause = torch.cuda.synchronize if sync else (lambda: None)
+    torch.cuda.synchronize()
+    for s, (old, keep, parents, new) in enumerate(plan):
+        C.pages_resize(tables, refs, old, keep, ws, page_size=size, moves=moves, error_word=err), pause()
+        C.pages_fork(tables, refs, keep, parents, after, page_size=size, error_word=err), pause()
+        C.pages_resize(tables, refs, after, new, ws, page_size=size, moves=moves, error_word=err), pause()
+        C.pages_copy(pool + scales, moves, error_word=err), pause()
+        for k in range(layers):
+            C.append(latent[s], pool[k], scales[k], tables, new, error_word=err), pause()
+            outs.append(C.window_attention(q[s], pool[k], scales[k], tables, new, wws, window=24, first_tokens=3,
+                                           num_splits=s % 3, bmm1_scale=0.04, error_word=err)), pause()
+        if s % 7 == 6:
+            C.pages_compact(tables, refs, new, ws, page_size=size, moves=moves, error_word=err), pause()
+            C.pages_copy(pool + scales, moves, error_word=err), pause()
+    torch.cuda.synchronize()
+    return [tables, refs, *pool, *scales, err] + [t for pair in outs for t in pair]
+
+
+def test_calls_behind_one_another_are_calls_one_by_one():
+    """Kernels start while the ones before them end; none may see less than all of what those wrote."""
+    one_by_one = chain(True)
+    assert int(one_by_one[6].item()) == 0
+    for _ in range(3):
+        for a, b in zip(one_by_one, chain(False)):
+            assert torch.equal(a, b)
+
+
+def test_captured_behind_two_streams():
+    """Calls captured behind work of two streams, and before work of both."""
+    cache, _, rng = make(61, [90, 200, 33], [1, 1, 1])
+    g, start = on_gpu(cache), torch.cuda.Stream()
+    x, q = bf16(rng.normal(size=(3, 512)))[0], bf16(rng.normal(size=(3, 64, 512)))[0]
+    latent, query, out, lse = torch.zeros_like(x), torch.zeros_like(q), torch.empty_like(q), torch.empty(3, 64, device=DEV)
+    lens, ws = torch.zeros_like(g["seq_lens"]), torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    sums = torch.zeros(2, device=DEV)
+    other = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=start):
+        other.wait_stream(start)
+        with torch.cuda.stream(other):
+            query.copy_(q * 1.0)
+            torch.add(g["seq_lens"], 0, out=lens)
+        torch.mul(x, 1.0, out=latent)
+        start.wait_stream(other)
+        C.append(latent, g["rows"], g["scales"], g["block_tables"], lens)
+        C.window_attention(query, g["rows"], g["scales"], g["block_tables"], lens, ws, window=64, num_splits=2, out=out, out_lse=lse)
+        other.wait_stream(start)
+        with torch.cuda.stream(other):
+            sums[0] = out.float().sum()
+        sums[1] = lse.sum()
+        start.wait_stream(other)
+    plain = on_gpu(cache)
+    for turn in range(4):
+        x.copy_(bf16(rng.normal(size=(3, 512)) * 2.0 ** turn)[0])
+        q.copy_(bf16(rng.normal(size=(3, 64, 512)))[0])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        C.append(x, plain["rows"], plain["scales"], plain["block_tables"], plain["seq_lens"])
+        o, l = C.window_attention(q, plain["rows"], plain["scales"], plain["block_tables"], plain["seq_lens"], ws, window=64,
+                                  num_splits=2)
+        torch.cuda.synchronize()
+        assert torch.equal(plain["rows"], g["rows"]) and torch.equal(o, out) and torch.equal(l, lse)
+        assert torch.allclose(sums, torch.stack([o.float().sum(), l.sum()]), rtol=1e-3, atol=1e-2)

@@ -480,6 +480,19 @@ __device__ __forceinline__ void compact_counts(const PagesParams& p, const Team&
   }
 }
 
+// One table entry, once the moves are known.
+__device__ __forceinline__ void renumber(const PagesParams& p, const int32_t* move_of, int live, int moves, int32_t* at) {
+  const int page = *at;
+  if (!in_pool(p, page)) {
+    flag(p.err, SMLA_DEVERR_PAGE_STATE);
+  } else if (page >= live) {
+    // a page that was not in use has no move of its own
+    const int k = __ldcg(move_of + page);
+    if (k >= 0 && k < moves && __ldcg(p.move_src + k) == page) *at = __ldcg(p.move_dst + k);
+    else flag(p.err, SMLA_DEVERR_PAGE_STATE);
+  }
+}
+
 __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
 pages_compact_kernel(const PagesParams p) {
   __shared__ Shared sh;
@@ -492,6 +505,17 @@ pages_compact_kernel(const PagesParams p) {
   const int moves = compact_moves(p, c, w, sh);
   ptx::cluster_sync();
   compact_counts(p, w, moves);
+  const int live = __ldcg(p.ws);
+  pieces(p, w,
+         [&](int b) {
+           bool bad = false;
+           const int n = page_columns(p, fetch(p.lens + b), &bad);
+           if (bad) flag(p.err, SMLA_DEVERR_PAGE_STATE);
+           return make_int2(0, n);
+         },
+         [&](int b, int from, int to) {
+           for (int at = from + w.lane; at < to; at += 32) renumber(p, c.move_of, live, moves, p.bt + (int64_t)b * p.bt_stride + at);
+         });
 }
 
 // The same phases as launches over the whole GPU (kPhase 0 .. 2; the counts may
@@ -508,7 +532,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_compact_phase_kernel(co
   else compact_counts(p, w, __ldcg(p.ws) - __ldcg(p.ws + 1));
 }
 
-// Renumbers the tables after the moves are known: one warp per 32 columns of a row.
+// Then the tables, 256 columns of a row a CTA.
 __global__ void __launch_bounds__(256) pages_renumber_kernel(const PagesParams p) {
   const int b = blockIdx.x;
   bool bad = false;
@@ -517,19 +541,8 @@ __global__ void __launch_bounds__(256) pages_renumber_kernel(const PagesParams p
   const int n = page_columns(p, fetch(p.lens + b), &bad);
   if (bad && threadIdx.x == 0 && blockIdx.y == 0) flag(p.err, SMLA_DEVERR_PAGE_STATE);
   const int live = __ldcg(p.ws), moves = live - __ldcg(p.ws + 1);
-  const int32_t* move_of = p.ws + kPagesHeader;
-  int32_t* row = p.bt + (int64_t)b * p.bt_stride;
-  for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < n; c += gridDim.y * blockDim.x) {
-    const int page = row[c];
-    if (!in_pool(p, page)) {
-      flag(p.err, SMLA_DEVERR_PAGE_STATE);
-    } else if (page >= live) {
-      // a page that was not in use has no move of its own
-      const int k = __ldcg(move_of + page);
-      if (k >= 0 && k < moves && __ldcg(p.move_src + k) == page) row[c] = __ldcg(p.move_dst + k);
-      else flag(p.err, SMLA_DEVERR_PAGE_STATE);
-    }
-  }
+  for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < n; c += gridDim.y * blockDim.x)
+    renumber(p, p.ws + kPagesHeader, live, moves, p.bt + (int64_t)b * p.bt_stride + c);
 }
 
 // ------------------------------------------------------------------ copy
@@ -615,15 +628,11 @@ cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t stream) {
-  cudaError_t e = cudaSuccess;
-  if (one_cluster(p)) {
-    e = launch_overlapped(pages_compact_kernel, dim3(kClusterCtas), kPlanThreads, 0, stream, p);
-  } else {
-    const dim3 pages(phase_ctas(((int64_t)p.num_pages + kChunk - 1) / kChunk, sms));
-    e = launch_overlapped(pages_compact_phase_kernel<0>, pages, kPlanThreads, 0, stream, p);
-    if (e == cudaSuccess) e = launch_overlapped(pages_compact_phase_kernel<1>, pages, kPlanThreads, 0, stream, p);
-    if (e == cudaSuccess) e = launch_overlapped(pages_compact_phase_kernel<2>, pages, kPlanThreads, 0, stream, p);
-  }
+  if (one_cluster(p)) return launch_overlapped(pages_compact_kernel, dim3(kClusterCtas), kPlanThreads, 0, stream, p);
+  const dim3 pages(phase_ctas(((int64_t)p.num_pages + kChunk - 1) / kChunk, sms));
+  cudaError_t e = launch_overlapped(pages_compact_phase_kernel<0>, pages, kPlanThreads, 0, stream, p);
+  if (e == cudaSuccess) e = launch_overlapped(pages_compact_phase_kernel<1>, pages, kPlanThreads, 0, stream, p);
+  if (e == cudaSuccess) e = launch_overlapped(pages_compact_phase_kernel<2>, pages, kPlanThreads, 0, stream, p);
   if (e != cudaSuccess) return e;
   const int cols = (p.max_pages + 255) / 256;
   return launch_overlapped(pages_renumber_kernel, dim3((unsigned)p.rows, (unsigned)(cols < 64 ? cols : 64)), 256, 0, stream,

@@ -14,7 +14,7 @@
 // fences before the barriers, and with one CTA counting pages after summing the
 // requests' needs); where tables and pool together pass kClusterEntries, eight
 // SMs are too few and the phases are launches of their own over the whole GPU
-// (1024 requests x 1024 pages in a pool of a million: 71 us in a cluster, 20 so).
+// (1024 requests x 1024 pages in a pool of a million: 71 us in a cluster, 18 so).
 // What bounds both is latency: the counts (4 bytes a page) are read once, and
 // again where pages are handed out; the rest is dependent trips to L2.
 #include "cache.cuh"
@@ -125,9 +125,11 @@ __device__ __forceinline__ Team team(int cta, int ctas) {
   return {cta, ctas, cta + (int)(threadIdx.x >> 5) * ctas, ctas * kWarps, (int)(threadIdx.x & 31)};
 }
 
+constexpr int kRanked = 4;                            // chunks that a thread ranks
+constexpr int kBatch = kPlanThreads * kRanked;        // of two million pages
 struct Shared {
   int32_t scan[2][kWarps];
-  int32_t prefix[kPlanThreads];
+  int32_t prefix[kBatch];
 };
 
 // Counts the pages in use of each chunk (chunk c is warp c % warps's).
@@ -139,13 +141,17 @@ __device__ __forceinline__ void count_chunks(const PagesParams& p, int32_t* coun
   }
 }
 
-// Ranks a batch of up to kPlanThreads chunks from c0 on, `before` pages being in
-// use before them: sh.prefix holds those before each chunk, the result counts the
+// Ranks a batch of up to kBatch chunks from c0 on, `before` pages being in use
+// before them: sh.prefix holds those before each chunk, the result counts the
 // batch in.  Whole CTA.
 __device__ __forceinline__ int rank_batch(const int32_t* counts, int chunks, int c0, int before, Shared& sh) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = c0 + threadIdx.x;
-  const int n = c < chunks ? __ldcg(counts + c) : 0;
-  int sum = n;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = c0 + (int)threadIdx.x * kRanked;
+  int n[kRanked], sum = 0;
+#pragma unroll
+  for (int k = 0; k < kRanked; ++k) n[k] = c + k < chunks ? __ldcg(counts + c + k) : 0;
+#pragma unroll
+  for (int k = 0; k < kRanked; ++k) sum += n[k];
+  const int own = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, sum, d);
@@ -153,7 +159,12 @@ __device__ __forceinline__ int rank_batch(const int32_t* counts, int chunks, int
   }
   if (lane == 31) sh.scan[0][warp] = sum;
   __syncthreads();
-  sh.prefix[threadIdx.x] = before + sum - n + __reduce_add_sync(0xffffffffu, lane < warp ? sh.scan[0][lane] : 0);
+  int at = before + sum - own + __reduce_add_sync(0xffffffffu, lane < warp ? sh.scan[0][lane] : 0);
+#pragma unroll
+  for (int k = 0; k < kRanked; ++k) {
+    sh.prefix[threadIdx.x * kRanked + k] = at;
+    at += n[k];
+  }
   before += __reduce_add_sync(0xffffffffu, sh.scan[0][lane]);
   __syncthreads();
   return before;
@@ -165,7 +176,7 @@ __device__ __forceinline__ int rank_batch(const int32_t* counts, int chunks, int
 template <class W, class F>
 __device__ __forceinline__ void walk_batch(const PagesParams& p, int chunks, int c0, const Team& w, const Shared& sh, W wanted,
                                            F f) {
-  const int batch = min(kPlanThreads, chunks - c0);
+  const int batch = min(kBatch, chunks - c0);
   for (int k = (w.gw - c0 % w.warps + w.warps) % w.warps; k < batch; k += w.warps) {
     const int live = sh.prefix[k];
     const int64_t base = (int64_t)(c0 + k) * kChunk;
@@ -177,7 +188,7 @@ template <class W, class F>
 __device__ __forceinline__ void walk_chunks(const PagesParams& p, const int32_t* counts, int chunks, const Team& w,
                                             Shared& sh, W wanted, F f) {
   int before = 0;                                     // pages in use before this batch of chunks
-  for (int c0 = 0; c0 < chunks; c0 += kPlanThreads) {
+  for (int c0 = 0; c0 < chunks; c0 += kBatch) {
     before = rank_batch(counts, chunks, c0, before, sh);
     walk_batch(p, chunks, c0, w, sh, wanted, f);
     __syncthreads();
@@ -300,11 +311,18 @@ __device__ __forceinline__ void resize_rows(const PagesParams& p, const Resize& 
   if (threadIdx.x == 0) p.ws[0] = need0;
 }
 
+// The needs, and the pages in use beside them.
+__device__ __forceinline__ void resize_needs(const PagesParams& p, const Resize& r, const Team& w, Shared& sh) {
+  if (w.cta == 0) resize_rows(p, r, sh);
+  if (w.ctas == 1) count_chunks(p, r.counts, r.chunks, w);
+  else if (w.cta > 0) count_chunks(p, r.counts, r.chunks, team(w.cta - 1, w.ctas - 1));
+}
+
 // 3. the lowest free pages, in order: the smaller of what is needed and what is free
 __device__ __forceinline__ int resize_list(const PagesParams& p, const Resize& r, const Team& w, Shared& sh) {
   const int need = __ldcg(p.ws);
-  // (one batch, which a cluster's pools are, is ranked and summed in one)
-  const bool one = r.chunks <= kPlanThreads;
+  // (one batch is ranked and summed in one)
+  const bool one = r.chunks <= kBatch;
   const int live_all = one ? rank_batch(r.counts, r.chunks, 0, 0, sh) : need > 0 ? sum_counts(r.counts, r.chunks, sh) : 0;
   const int take = min(need, p.num_pages - live_all);
   if (need > take && w.cta == 0 && threadIdx.x == 0) flag(p.err, SMLA_DEVERR_OUT_OF_PAGES);
@@ -372,8 +390,7 @@ pages_resize_kernel(const PagesParams p) {
   admit_next_kernel();
   resize_drop(p, w);
   ptx::cluster_sync();
-  if (w.cta == 0) resize_rows(p, r, sh);              // beside the others' counting
-  else count_chunks(p, r.counts, r.chunks, team(w.cta - 1, kClusterCtas - 1));
+  resize_needs(p, r, w, sh);
   ptx::cluster_sync();
   const int take = resize_list(p, r, w, sh);
   ptx::cluster_sync();
@@ -391,8 +408,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_resize_phase_kernel(con
   if constexpr (kPhase == 0) {
     resize_drop(p, w);
   } else if constexpr (kPhase == 1) {
-    if (w.cta == 0) resize_rows(p, r, sh);
-    count_chunks(p, r.counts, r.chunks, w);
+    resize_needs(p, r, w, sh);
   } else if constexpr (kPhase == 2) {
     const int take = resize_list(p, r, w, sh);
     if (w.cta == 0 && threadIdx.x == 0) p.ws[1] = take;

@@ -584,6 +584,28 @@ def test_pages_out_of_pages_in_order():
     assert (b.ref.tables[3, 1] == b.ref.tables[2, 1]) or (b.ref.tables[:, 2:] >= 0).any()
 
 
+def test_pages_of_a_pool_ranked_in_several_batches():
+    """Pages past two million: ranks go on over the batches in which chunks are ranked."""
+    pages, used, size = 2 * (1 << 21) + 9000, 2 * (1 << 21) + 300, 8
+    refs, tables = torch.zeros(pages, dtype=torch.int32, device=DEV), torch.full((3, 20), -1, dtype=torch.int32, device=DEV)
+    refs[:used] = 1
+    ws = torch.empty(C.pages_workspace_size(tables, refs, size), dtype=torch.uint8, device=DEV)
+    moves, err = C.new_moves(pages // 2, DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    lens = i32([80, 40, 56])
+    C.pages_resize(tables, refs, i32([0, 0, 0]), lens, ws, page_size=size, moves=moves, error_word=err)
+    want = np.full((3, 20), -1)
+    want[0, :10], want[1, :5], want[2, :7] = used + np.arange(10), used + 10 + np.arange(5), used + 15 + np.arange(7)
+    assert tables.cpu().numpy().tolist() == want.tolist() and int(refs.sum()) == used + 22
+    holes = [5, 1 << 20, (1 << 21) + 7]                    # in both batches; the last three pages in use fill them
+    refs[i32(holes).long()] = 0
+    C.pages_compact(tables, refs, lens, ws, page_size=size, moves=moves, error_word=err)
+    assert int(moves.count.item()) == 3 and moves.dst[:3].tolist() == holes
+    assert moves.src[:3].tolist() == [used + 19, used + 20, used + 21]
+    want[2, 4:7] = holes
+    assert tables.cpu().numpy().tolist() == want.tolist() and int(err.item()) == 0
+    assert int(refs[:used + 19].min()) == 1 and int(refs[used + 19:].max()) == 0
+
+
 def test_pages_state_errors_are_flagged():
     b = Both(4, 3, 8, 10, lens=[9, 8, 0, 0])
     out = torch.empty(4, dtype=torch.int32, device=DEV)

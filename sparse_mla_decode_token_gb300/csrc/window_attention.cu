@@ -55,9 +55,13 @@
 // rest is the chain second product -> free quarter -> rows -> first product ->
 // softmax of a buffer, which two 64 KB tiles (Q takes 64 KB, P 32) cannot hide
 // whole, and 7 us a unit for its query, sums and results.  Measured on a GB300:
-// 128 requests of one token, 128 heads, 2052 rows: 92 us, 744 TFLOP/s of the
+// 128 requests of one token, 128 heads, 2052 rows: 90 us, 765 TFLOP/s of the
 // plain products' count; 2836 tokens of four prompts, 128 heads, a window of 512:
-// 582 us, 476 TFLOP/s; two requests of 64 heads and 2 tiles: 13 us.
+// 550 us, 504 TFLOP/s; two requests of 64 heads and 2 tiles: 13 us.
+//
+// Five kinds of warps share an instruction cache that a unit's code overflows, so
+// code that need not be long is not: the products' loops are rolled to four and
+// eight instructions, each look-up stands once (prompts 583 -> 548 us).
 //
 // Tried and slower (at these sizes): both products issued by one warp (decode
 // 114 us against 98), warps of their own for the query (prefill 688 against
@@ -322,13 +326,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         mbar_arrive(bar(sm.unit_full[x & 1]));
       }
       __syncwarp();
-      auto look_ahead = [&] {                     // the next unit and its queries' way to L2
-        if (x + 1 < mine) {
-          ahead = make_unit<kShift, kParts>(kp, blockIdx.x + (x + 1) * gridDim.x, lane);
-          prefetch_query(ahead);
-        }
-      };
-      if (u.tiles < 2) look_ahead();
       // Lane l looks up box l of the tile; one lane then holds all of them, so
       // that nothing but the wait and the copy stands between a quarter of the
       // buffer and its rows.
@@ -338,8 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         *group = (uint32_t)(chunk_at(u, min(k, u.chunks - 1)) << kShift) % (uint32_t)p.c.page_size / 8;
       };
       int page = -1, group = 0;
-      if (u.tiles > 0) look_up(0, &page, &group);
-      for (int i = 0; ok && i < u.tiles; ++i, ++n) {
+      for (int i = -1; ok && i < u.tiles; ++i) {
         const int b = n & 1;
         const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, page >= 0)) * kHeadDim << kShift;
         int pg[kBoxes], g[kBoxes];
@@ -348,9 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           pg[k] = __shfl_sync(0xffffffffu, page, k);
           g[k] = __shfl_sync(0xffffffffu, group, k);
         }
-        look_up(i + 1, &page, &group);
+        if (i + 1 < u.tiles) look_up(i + 1, &page, &group);
         bool good = true;
-        if (elect_one()) {
+        if (i >= 0 && elect_one()) {
           const uint32_t full = bar(sm.k_full[b]), dst = k_addr + b * kTileBytes;
 #pragma unroll
           for (int k = 0; k < kBoxes; ++k) {
@@ -363,7 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           }
         }
         ok = __all_sync(0xffffffffu, good);
-        if (i == 1) look_ahead();
+        n += i >= 0;
+        if (i == min(1, u.tiles - 1) && x + 1 < mine) {       // the next unit and its queries' way to L2
+          ahead = make_unit<kShift, kParts>(kp, blockIdx.x + (x + 1) * gridDim.x, lane);
+          prefetch_query(ahead);
+        }
       }
     }
     // after an abort the last copies may still be in flight
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
       const Unit u = sm.unit[x & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sm.unit_empty[x & 1]));
-      float next[kRows / 32];
+      float next[kRows / 32] = {};
       // (every load is unconditional, at a clamped place: the four are in flight together)
       auto look_up = [&](int i) {
         constexpr int kY = kRows / 32;
@@ -411,18 +411,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         const int k = (u.tile0 + i) * per_tile + lane;
         const int page = lane < per_tile && i < u.tiles ? chunk_page<kShift>(kp, u, k) : -1;
         const int group = (uint32_t)(chunk_at(u, min(k, u.chunks - 1)) << kShift) % (uint32_t)p.c.page_size / 8;
-#pragma unroll
+#pragma unroll 1
         for (int y = 0; y < per_tile; ++y) {
           const int pg = __shfl_sync(0xffffffffu, page, y), g = __shfl_sync(0xffffffffu, group, y);
           if (pg >= 0 && elect_one()) tma_prefetch_5d(&kp.map, 0, 0, 0, g, pg);
           __syncwarp();
         }
       };
-      if (u.tiles > 0) {
-        look_up(0);
-        prefetch(2);
-      }
-      for (int i = 0; ok && i < u.tiles; ++i, ++n) {
+      for (int i = -1; ok && i < u.tiles; ++i) {
         const int b = n & 1;
         float s[kRows / 32];
 #pragma unroll
@@ -431,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           look_up(i + 1);
           prefetch(i + 3);
         }
+        if (i < 0) continue;
         // (the softmax has read this buffer's last scales before it gave its P)
         if (n >= 2) ok = warp_wait(cx, bar(sm.p_full[b]), ((n >> 1) - 1) & 1);
         if (!ok) break;
@@ -438,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         for (int y = 0; y < kRows / 32; ++y) sm.scale[b][y * 32 + lane] = s[y];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sm.scale_full[b]));
+        ++n;
       }
     }
   } else if (warp == kScoreWarp) {
@@ -461,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         tc_fence_after();
         if (elect_one()) {
           const uint32_t tile = k_addr + b * kTileBytes;
-#pragma unroll
+#pragma unroll 4
           for (int k = 0; k < 16; ++k)
             mma<true>(tmem + kSCol + b * 128, desc_sw128(tile + (k >> 2) * 1024 + (k & 3) * 32, 16, kGroupBytes),
                       desc_sw128(q_addr + (k >> 2) * kQBlock + (k & 3) * 32, 16, 1024), idesc_s, k > 0);
@@ -489,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         tc_fence_after();
         if (elect_one()) {
           const uint32_t tile = k_addr + b * kTileBytes, pb = p_addr + b * 2 * kPHalf;
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < 4; ++k) {
 #pragma unroll
             for (int half = 0; half < 2; ++half)

@@ -342,7 +342,11 @@ smla_status smla_decode_static_workspace(const smla_args* args, void* stream);
  * stream-ordered launches on the current device, host-detectable mistakes as
  * statuses before any CUDA call, device-detected ones as bits of *error_word.
  * They read and write what the tables and lengths on the device say, so a
- * captured call replays on the values of that moment.
+ * captured call replays on the values of that moment.  Their kernels are
+ * launched while the work before them on the stream ends, and wait on the
+ * device for all of it (programmatic dependent launch).  Nothing is kept
+ * between calls: a workspace may serve all calls that are ordered one behind
+ * another, captured ones included.
  * ---------------------------------------------------------------------------
  */
 typedef struct smla_cache {

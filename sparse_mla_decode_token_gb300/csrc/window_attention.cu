@@ -56,7 +56,7 @@
 // softmax of a buffer, which two 64 KB tiles (Q takes 64 KB, P 32) cannot hide
 // whole, and 7 us a unit for its query, sums and results.  Measured on a GB300:
 // 128 requests of one token, 128 heads, 2052 rows: 90 us, 765 TFLOP/s of the
-// plain products' count; 2836 tokens of four prompts, 128 heads, a window of 512:
+// plain products' count; 2049 tokens of four prompts, 128 heads, a window of 512:
 // 550 us, 504 TFLOP/s; two requests of 64 heads and 2 tiles: 13 us.
 //
 // Five kinds of warps share an instruction cache that a unit's code overflows, so
@@ -66,7 +66,7 @@
 // Tried and slower (at these sizes): both products issued by one warp (decode
 // 114 us against 98), warps of their own for the query (prefill 688 against
 // 577), waits that poll (613 against 606), two or four times less headroom in
-// the reference (prefill 552 to 564, at twice the error).
+// the reference (prefill 552 to 564 against 576, at up to twice the error).
 #include <cuda.h>
 
 #include <algorithm>

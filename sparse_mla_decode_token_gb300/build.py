@@ -8,6 +8,7 @@ library; ``csrc/cache_torch.cpp`` (host code) is compiled beside them.  Set ``SM
 from __future__ import annotations
 
 import concurrent.futures as cf
+import fcntl
 import os
 import shutil
 import subprocess
@@ -95,18 +96,20 @@ def build(force: bool = False, verbose: bool | None = None) -> str:
     if verbose is None:
         verbose = os.environ.get("SMLA_PTXAS_VERBOSE", "0") == "1"
     os.makedirs(BUILD, exist_ok=True)
-    if not force and not verbose and not _stale(LIB, _deps()) and not _stale(TORCH_EXT, _deps()):
+    with open(os.path.join(BUILD, "lock"), "w") as lock:
+        fcntl.flock(lock, fcntl.LOCK_EX)              # processes that find it stale together build it once
+        if not force and not verbose and not _stale(LIB, _deps()) and not _stale(TORCH_EXT, _deps()):
+            return LIB
+        srcs = sources()
+        with cf.ThreadPoolExecutor(max_workers=max(2, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+            ext = ex.submit(_compile_torch_ext)
+            objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+            ext_obj = ext.result()
+        tmp = LIB + ".tmp"
+        _run("link", [nvcc()] + GENCODE + ["-shared", "-o", tmp] + objs)
+        os.replace(tmp, LIB)
+        _link_torch_ext(ext_obj)
         return LIB
-    srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=max(2, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        ext = ex.submit(_compile_torch_ext)
-        objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        ext_obj = ext.result()
-    tmp = LIB + ".tmp"
-    _run("link", [nvcc()] + GENCODE + ["-shared", "-o", tmp] + objs)
-    os.replace(tmp, LIB)
-    _link_torch_ext(ext_obj)
-    return LIB
 
 
 if __name__ == "__main__":

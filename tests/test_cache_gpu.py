@@ -941,3 +941,66 @@ def test_captured_behind_two_streams():
         torch.cuda.synchronize()
         assert torch.equal(plain["rows"], g["rows"]) and torch.equal(o, out) and torch.equal(l, lse)
         assert torch.allclose(sums, torch.stack([o.float().sum(), l.sum()]), rtol=1e-3, atol=1e-2)
+
+
+def test_pages_past_four_gigabytes():
+    """Pages behind 2^32 bytes give what the same pages give in a small pool."""
+    cache, q, rng = make(62, [300, 120], [3, 70], junk=False)
+    small, cum = on_gpu(cache), i32(cache.cum)
+    n, used = 140_000, cache.rows.shape[0]                 # 4.6 GB of rows
+    shift = n - used
+    big = dict(small, rows=torch.empty(n, 64, 512, dtype=torch.uint8, device=DEV), scales=torch.zeros(n, 4, device=DEV),
+               block_tables=torch.where(small["block_tables"] >= 0, small["block_tables"] + shift, -1).to(torch.int32))
+    big["rows"][shift:], big["scales"][shift:] = small["rows"], small["scales"]
+    qt, x = bf16(q)[0], bf16(rng.normal(size=(73, 512)))[0]
+    got = []
+    for g in (small, big):
+        C.append(x, g["rows"], g["scales"], g["block_tables"], g["seq_lens"], cum_seq_lens_q=cum)
+        for splits in (1, 2):
+            got.append(C.window_attention(qt, g["rows"], g["scales"], g["block_tables"], g["seq_lens"],
+                                          workspace(qt, g, window=200, num_splits=splits, cum_seq_lens_q=cum), window=200,
+                                          cum_seq_lens_q=cum, num_splits=splits, bmm1_scale=0.04))
+    assert torch.equal(small["rows"], big["rows"][shift:]) and torch.equal(small["scales"], big["scales"][shift:])
+    for (a, b), (c, d) in zip(got[:2], got[2:]):
+        assert torch.equal(a, c) and torch.equal(b, d)
+    moves = C.PageMoves(i32([n - 1, 1]), i32([0, n - 2]), i32([2]))
+    big["rows"][1] = 7
+    C.pages_copy([big["rows"], big["scales"]], moves)
+    assert torch.equal(big["rows"][0], big["rows"][n - 1]) and bool((big["rows"][n - 2] == 7).all())
+
+
+@pytest.mark.parametrize("T,window,first,splits", [(1, 1 << 30, 0, 0), (3, 1 << 30, 0, 0), (3, 1 << 30, 0, 1),
+                                                   (3, 131072, 70000, 0), (3, 1, 250000, 64)])
+def test_window_over_a_long_sequence(T, window, first, splits):
+    """A quarter of a million rows, against 64 bits on the GPU."""
+    n, H, size = 262_144 + 5, 64, 256
+    gen = torch.Generator(DEV).manual_seed(63)
+    pages = -(-n // size)
+    rows = torch.randn(pages, size, 512, device=DEV, generator=gen).to(torch.float8_e4m3fn)
+    scales = torch.exp2(torch.randint(-3, 1, (pages, size // 32), device=DEV, generator=gen).float())
+    tables = torch.randperm(pages, device=DEV, generator=gen).to(torch.int32).view(1, -1)
+    q = torch.randn(T, H, 512, device=DEV, generator=gen).to(torch.bfloat16)
+    g = dict(rows=rows, scales=scales, block_tables=tables, seq_lens=i32([n]))
+    bmm1 = 0.05
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = C.window_attention(q, *g.values(), workspace(q, g, window=window, first_tokens=first, num_splits=splits),
+                                  window=window, first_tokens=first, num_splits=splits, bmm1_scale=bmm1, error_word=err)
+    order = tables[0].long()
+    kv = (rows[order].double() * scales[order].double().repeat_interleave(32, 1)[..., None]).view(-1, 512)[:n]
+    j = torch.arange(n, device=DEV)
+    assert int(err.item()) == 0
+    for t in range(T):
+        pos = n - T + t
+        seen = kv[(j <= pos) & ((j > pos - window) | (j < first))]
+        x = q[t].double()
+        l = x @ seen.T * bmm1
+        # the logits' bound of the reference: fp32 sums, and the query's split
+        off = (2.0 ** -18 * (x.abs() @ seen.abs().T) + 2.0 ** -17 * x.abs().amax(1, keepdim=True) * seen.abs().sum(1)) * bmm1
+        p = torch.softmax(l, 1)
+        want, want_lse = p @ seen, torch.logsumexp(l, 1) / math.log(2.0)
+        # (sums of a thread's rows: 2049 tiles at most, 2^-24 each; a merge of 152)
+        tol = 1.4427 * ((p * 2 * off).sum(1) + 2.0 ** -18 + 2201 * 2.0 ** -24) + 2.0 ** -21 * want_lse.abs()
+        assert bool(((lse[t].double() - want_lse).abs() <= tol).all())
+        # rounding errors of either sign: P's 2^-8 over the weights, the result's 2^-9
+        spread = ((p ** 2) @ (seen ** 2)).sqrt()
+        assert ((out[t].double() - want) ** 2).mean().sqrt() <= 2.0 ** -8 * (spread.square().mean() + want.square().mean()).sqrt()

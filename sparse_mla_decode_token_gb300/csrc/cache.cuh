@@ -99,6 +99,7 @@ struct WindowParams {
 
 constexpr int kWindowHeads = 64;      // heads of one token that a CTA takes
 constexpr int kWindowTile = 128;      // cache rows of one tile
+constexpr int kMaxWindowSplits = 256;
 
 cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t stream);
 

@@ -15,6 +15,8 @@
 namespace smla {
 namespace {
 
+static_assert(SMLA_MAX_SPLITS <= kMaxWindowSplits, "forced splits");
+
 smla_status fail(smla_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 smla_status fail(smla_status st, const char* fmt, ...) {
   char buf[512];
@@ -170,7 +172,7 @@ struct WindowPlan {
 // (1 token x 64 heads, 2 tiles: 12.7 us whole, 13.7 in two; 3 tiles: 16.1 against
 // 14.8 in three; 32 x 128, 5 tiles: 21.5 against 22.9 in two, 9: 30.1 against 27.8).
 int cheapest_splits(int64_t pairs, int64_t tiles, int sms) {
-  const int64_t most = std::min<int64_t>(sms / pairs, tiles);
+  const int64_t most = std::min<int64_t>({sms / pairs, tiles, kMaxWindowSplits});
   int best = 1;
   double cost = (double)tiles;
   for (int64_t s = 2; s <= most; ++s) {

@@ -779,11 +779,21 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 }
 
 // Merges the S normalised fp32 partials of a split pair's heads: weights
-// 2^(LSE_s - LSE), then the sink and bmm2.
-constexpr int kMergeThreads = 128;                // one head: four dims a thread
+// 2^(LSE_s - LSE), then the sink and bmm2.  The weights first, a split a thread;
+// then no partial's load waits for another's.  Up to four teams of threads share
+// many splits (64 heads over 32768 rows in 128 splits: 31.5 us of both kernels with
+// one team, 21.6 with four; over 262144 rows 63.5 and 51.5).
+constexpr int kMergeThreads = 128;                // of a team; one head: four dims a thread
+constexpr int kMergeTeams = 4;
 
-__global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const WindowParams p, int groups) {
-  const int pair = blockIdx.x / kNH, hl = blockIdx.x % kNH, d = threadIdx.x * 4;
+template <int kTeams>
+__global__ void __launch_bounds__(kMergeThreads * kTeams) window_merge_kernel(const WindowParams p, int groups) {
+  constexpr int kThreads = kMergeThreads * kTeams;
+  __shared__ float weight[kMaxWindowSplits];
+  __shared__ float warp_top[kThreads / 32], warp_sum[kThreads / 32];
+  __shared__ float4 share[kTeams][kMergeThreads];
+  const int pair = blockIdx.x / kNH, hl = blockIdx.x % kNH, warp = threadIdx.x / 32;
+  const int team = threadIdx.x / kMergeThreads, lane4 = threadIdx.x % kMergeThreads, d = lane4 * 4;
   const int t = (p.whole + pair) / groups, h = (p.whole + pair) % groups * kNH + hl;
   if (h >= p.H) return;
   const int64_t th = (int64_t)t * p.H + h;
@@ -791,29 +801,55 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Windo
   admit_next_kernel();
   if (p.c.cum != nullptr && (t < fetch(p.c.cum) || t >= fetch(p.c.cum + p.c.batch))) return;   // no request's
   const int64_t row = (int64_t)pair * p.num_splits * kNH + hl;
-  const float* lse_s = p.part_lse + row;
-  const float* o_s = p.part_o + row * kHeadDim + d;
-  float mx = -INFINITY;
+  float top = -INFINITY;
   bool nan = false;
-  for (int s = 0; s < p.num_splits; ++s) {
-    const float l = fetch(lse_s + s * kNH);
+  for (int s = threadIdx.x; s < p.num_splits; s += kThreads) {
+    const float l = fetch(p.part_lse + row + s * kNH);
+    weight[s] = l;
     nan |= isnan(l);
-    mx = fmaxf(mx, l);
+    top = fmaxf(top, l);
   }
+  top = warp_max(top);
+  if ((threadIdx.x & 31) == 0) warp_top[warp] = top;
+  nan = __syncthreads_or(nan);
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, warp_top[w]);
+  float sum = 0.f;
+  for (int s = threadIdx.x; s < p.num_splits; s += kThreads) {
+    const float w = weight[s] == -INFINITY ? 0.f : fast_exp2(weight[s] - top);
+    weight[s] = w;
+    sum += w;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((threadIdx.x & 31) == 0) warp_sum[warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) sum += warp_sum[w];
+  const float* o_s = p.part_o + row * kHeadDim + d;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float wsum = 0.f;
-  for (int s = 0; s < p.num_splits; ++s) {
-    const float l = fetch(lse_s + s * kNH);
-    if (l == -INFINITY) continue;                 // an empty partial is not written
-    const float w = fast_exp2(l - mx);
-    const float4 o = fetch(reinterpret_cast<const float4*>(o_s + (int64_t)s * kNH * kHeadDim));
+#pragma unroll 8
+  for (int s = team; s < p.num_splits; s += kTeams) {
+    const float w = weight[s];
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);   // an empty partial is not written
+    if (w != 0.f) o = fetch(reinterpret_cast<const float4*>(o_s + (int64_t)s * kNH * kHeadDim));
     acc.x = fmaf(w, o.x, acc.x), acc.y = fmaf(w, o.y, acc.y), acc.z = fmaf(w, o.z, acc.z), acc.w = fmaf(w, o.w, acc.w);
-    wsum += w;
+  }
+  if constexpr (kTeams > 1) {
+    share[team][lane4] = acc;
+    __syncthreads();
+    if (team > 0) return;
+#pragma unroll
+    for (int w = 1; w < kTeams; ++w) {
+      const float4 o = share[w][lane4];
+      acc.x += o.x, acc.y += o.y, acc.z += o.z, acc.w += o.w;
+    }
   }
   float lse = -INFINITY, f = 0.f;
-  if (mx != -INFINITY || nan) {
-    lse = nan ? NAN : mx + fast_log2(wsum);
-    f = fetch_scale(p.bmm2, p.bmm2_dev) / wsum;
+  if (top != -INFINITY || nan) {
+    lse = nan ? NAN : top + fast_log2(sum);
+    f = fetch_scale(p.bmm2, p.bmm2_dev) / sum;
     if (p.sinks != nullptr) f *= 1.f / (1.f + fast_exp2(fetch(p.sinks + h) * kLog2e - lse));
   }
   uint2 v;
@@ -898,8 +934,10 @@ cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t
   else if (shift == 4) e = parts ? launch(window_kernel<4, true>) : launch(window_kernel<4, false>);
   else e = parts ? launch(window_kernel<3, true>) : launch(window_kernel<3, false>);
   if (e != cudaSuccess || !parts) return e;
-  return launch_overlapped(window_merge_kernel, dim3((unsigned)((pairs - p.whole) * (int64_t)kNH)), kMergeThreads, 0, stream,
-                           p, kp.groups);
+  const dim3 heads((unsigned)((pairs - p.whole) * (int64_t)kNH));
+  if (p.num_splits > 8)                           // what one team loads at a time
+    return launch_overlapped(window_merge_kernel<kMergeTeams>, heads, kMergeThreads * kMergeTeams, 0, stream, p, kp.groups);
+  return launch_overlapped(window_merge_kernel<1>, heads, kMergeThreads, 0, stream, p, kp.groups);
 }
 
 }  // namespace smla

@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kThreads, 8) cache_append_kernel(const AppendP
   const int start = fetch(c.seq_lens + b) - count;                      // position of the first new token
   const int end = start + count, from0 = max(start, 0);
   const int i = (int)(u - (first / c.block_rows + 2 * (int64_t)b));     // block of the request's touched ones
+  if (i < 0) return;                                                    // (the units of a batch padded in front)
   if (i == 0 && start < 0 && threadIdx.x == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
   const int64_t block0 = ((int64_t)(from0 / c.block_rows) + i) * c.block_rows;   // first position of the block
   if (block0 >= end) return;

@@ -201,6 +201,8 @@ def _window_args(q, rows, scales, tables, seq_lens, cum, sinks, window, first_to
         raise TypeError(f"q must be bfloat16; got {q.dtype}")
     if len(qs) != 3 or qs[2] != HEAD_DIM or (qs[0] > 0 and (qt[2] != 1 or (qs[1] > 1 and qt[1] != HEAD_DIM))):
         raise ValueError(f"q must be [T, H, {HEAD_DIM}] with contiguous heads; got {tuple(qs)}")
+    if qs[0] > 1 and qt[0] <= 0:                       # (0 would stand for the packed stride)
+        raise ValueError("the tokens of q must not share memory")
     if sinks is not None:
         _words("sinks", sinks, qs[1], torch.float32)
     return SmlaWindowArgs(_cache(rows, scales, tables, seq_lens, cum), qs[0], qs[1], _int32("window", window),
@@ -296,6 +298,8 @@ def append(latent: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block
         raise TypeError(f"latent must be bfloat16; got {latent.dtype}")
     if len(ls) != 2 or ls[1] != HEAD_DIM or (lt[1] != 1 and ls[0] > 0):
         raise ValueError(f"latent must be [T, {HEAD_DIM}] with contiguous rows; got {tuple(ls)}")
+    if ls[0] > 1 and lt[0] <= 0:                       # (0 would stand for the packed stride)
+        raise ValueError("the tokens of latent must not share memory")
     _words("error_word", error_word, 1)
     a = SmlaAppendArgs(_cache(rows, scales, block_tables, seq_lens, cum_seq_lens_q), ls[0], latent.data_ptr(),
                        lt[0] if ls[0] > 1 else HEAD_DIM, None if error_word is None else error_word.data_ptr())

@@ -153,7 +153,8 @@ PyObject* window_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& q = call.tensor(a[0]);
     need(q.scalar_type() == c10::kBFloat16 && q.dim() == 3);
     const int64_t T = q.size(0), H = q.size(1);
-    need(T > 0 && H > 0 && q.size(2) == kDim && q.stride(2) == 1 && (H == 1 || q.stride(1) == kDim));
+    need(T > 0 && H > 0 && q.size(2) == kDim && q.stride(2) == 1 && (H == 1 || q.stride(1) == kDim) &&
+         (T == 1 || q.stride(0) > 0));
     w.cache = cache(call, a[1], a[2], a[3], a[4], a[6]);
     w.workspace = call.bytes(a[5], &w.workspace_bytes);
     w.sinks = static_cast<const float*>(call.array(a[7], c10::kFloat, H, true));
@@ -200,7 +201,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Call call;
     smla_append_args p = {};
     const at::Tensor& x = call.tensor(a[0]);
-    need(x.scalar_type() == c10::kBFloat16 && x.dim() == 2 && x.size(0) > 0 && x.size(1) == kDim && x.stride(1) == 1);
+    need(x.scalar_type() == c10::kBFloat16 && x.dim() == 2 && x.size(0) > 0 && x.size(1) == kDim && x.stride(1) == 1 &&
+         (x.size(0) == 1 || x.stride(0) > 0));
     p.cache = cache(call, a[1], a[2], a[3], a[4], a[5]);
     p.sum_q = int32(x.size(0));
     p.latent = x.data_ptr();

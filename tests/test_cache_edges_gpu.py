@@ -52,3 +52,16 @@ def test_append_batch_padded_in_front(lead, page_size, block, lens, q_lens):
     assert np.array_equal(scales.cpu().numpy(), cache.scales, equal_nan=True)
     for whole, value, n in ((rows_all, 0x55, rows.numel()), (scales_all, 0.0, scales.numel())):
         assert bool((whole[:n] == value).all()) and bool((whole[2 * n:] == value).all())
+
+
+# ---------------------------------------------------------------- refusals
+
+def test_broadcast_tensors_never_reach_the_library():
+    """Both ways into the library, the extension's and Python's, refuse tokens that share memory."""
+    cache, q, rng = make(61, [40, 30], [2, 2])
+    g = on_gpu(cache)
+    q1, x1 = bf16(q[:1])[0], bf16(rng.normal(size=(1, 512)))[0]
+    with pytest.raises(ValueError, match="share memory"):
+        C.window_attention(q1.expand(4, -1, -1), g["rows"], g["scales"], g["block_tables"], g["seq_lens"], None, window=16)
+    with pytest.raises(ValueError, match="share memory"):
+        C.append(x1.expand(4, -1), g["rows"], g["scales"], g["block_tables"], g["seq_lens"])

@@ -243,6 +243,8 @@ def _rows_and_stride(kv: torch.Tensor, row: int = HEAD_DIM) -> tuple[int, int]:
     flat = kv.reshape(-1, row) if kv.dim() != 2 else kv
     if flat.data_ptr() != kv.data_ptr():
         raise ValueError("KV pool view cannot be flattened to rows without a copy")
+    if flat.shape[0] > 1 and flat.stride(0) == 0:
+        raise ValueError("KV pool: the rows must not share memory")
     return flat.shape[0], flat.stride(0)
 
 
@@ -321,6 +323,11 @@ def make_args(*, q: torch.Tensor, swa_kv: torch.Tensor, compressed_kv: torch.Ten
         raise ValueError("sparse_indices must be [T, W] with a contiguous last dim")
     if sparse_indices.shape[0] < T:
         raise ValueError(f"sparse_indices has {sparse_indices.shape[0]} rows for {T} query tokens")
+
+    # (a stride of 0, as expand() makes it, would stand for the packed one in the struct)
+    for name, t in (("query", q), ("sparse_indices", sparse_indices), ("comp_block_tables", comp_block_tables)):
+        if t is not None and T > 1 and t.stride(0) == 0:
+            raise ValueError(f"{name}: the rows must not share memory")
 
     kv_code = _kv_dtype_code(q, swa_kv)
     if _kv_dtype_code(q, compressed_kv) != kv_code:

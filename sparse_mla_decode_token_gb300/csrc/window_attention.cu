@@ -6,11 +6,11 @@
 //
 // Both products take the codes as they lie in the cache, at the E4M3 rate, and
 // still keep BF16's precision for the other operand: a BF16 number has eight
-// significant bits, an E4M3 number four, so q 2^k = hi + lo with two E4M3
-// numbers, hi the rounded value and lo the rest (at most eight units in the
-// last place, hence exact above 2^-18 of the head's largest element, where
-// lo's subnormals end).  P is split the same way (its error is then below
-// BF16's).  Two E4M3 products cost what one BF16 product would, without
+// significant bits, an E4M3 number four, so q 2^k = hi + 2^-5 lo with two E4M3
+// numbers, hi the rounded value and lo the rest, which has sums of its own and
+// so a scale of its own: exact down to 2^-14 of the head's largest element, an
+// absolute error of at most 2^-22 of that element below.  P is split the same
+// way, with one scale (its error is then below BF16's).  Two E4M3 products cost what one BF16 product would, without
 // widening the cache's rows in shared memory.
 //
 // Layout: one CTA takes 64 heads of one token and one split of its rows, and
@@ -209,6 +209,20 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t* hi, uint3
   *lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(p, back)), __NV_SATFINITE, __NV_E4M3);
 }
 
+// Two query values, scaled to magnitudes under 2^8, to E4M3 pairs hi = RN(q) and
+// lo = 2^5 (q - hi), at most 2^8: the rest of a value of 8 bits has four, so lo
+// is exact where hi and lo end above their subnormals' step of 2^-9, that is down
+// to q = 2^-7; below, q - hi is off by half of 2^-14 at most.
+constexpr float kLowScale = 1.f / 32;
+__device__ __forceinline__ void split_query_pair(float a, float b, uint32_t* hi, uint32_t* lo) {
+  const __half2 q = __floats2half2_rn(a, b);
+  const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(q), __NV_SATFINITE, __NV_E4M3);
+  const __half2 back(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3));
+  const __half2 rest = __hmul2(__hsub2(q, back), __float2half2_rn(1.f / kLowScale));
+  *hi = h;
+  *lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
+}
+
 // Q of 64 heads as E4M3 pairs: rows 0-63 hi, 64-127 lo, K-major with 128-byte
 // swizzle, column blocks of 128 dims.  A warp takes four heads, a lane 16 dims
 // of each.
@@ -247,7 +261,7 @@ __device__ __forceinline__ void split_query(const KernelParams& kp, const Unit& 
     uint32_t hi[8], lo[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x)
-      split_pair(__uint_as_float(w[x] << 16) * up, __uint_as_float(w[x] & 0xffff0000u) * up, hi + x, lo + x);
+      split_query_pair(__uint_as_float(w[x] << 16) * up, __uint_as_float(w[x] & 0xffff0000u) * up, hi + x, lo + x);
     uint4 h16 = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
     uint4 l16 = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
     if (m >= 0x7f80u) {                           // a head with an infinity or NaN gets NaN everywhere
@@ -542,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           tmem_ld16(lane_base + kSCol + b * 128 + hw, hi);
           tmem_ld16(lane_base + kSCol + b * 128 + kNH + hw, lo);
           tmem_wait_ld();
-          const uint64_t s2 = f2_pack(s, s), ls2 = f2_pack(ls, ls);
+          const uint64_t s2 = f2_pack(s, s), ls2 = f2_pack(ls, ls), low2 = f2_pack(kLowScale, kLowScale);
 #pragma unroll
           for (int e = 0; e < kHW / 2; e += 2) {
             const ulonglong2 qs = *reinterpret_cast<const ulonglong2*>(sm.qscale + hw + 2 * e);
@@ -550,8 +564,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int h = 2 * (e + k);
-              const uint64_t v = f2_add(f2_pack(__uint_as_float(hi[h]), __uint_as_float(hi[h + 1])),
-                                        f2_pack(__uint_as_float(lo[h]), __uint_as_float(lo[h + 1])));
+              const uint64_t v = f2_fma(f2_pack(__uint_as_float(lo[h]), __uint_as_float(lo[h + 1])), low2,
+                                        f2_pack(__uint_as_float(hi[h]), __uint_as_float(hi[h + 1])));
               d[e + k] = f2_add(f2_fma(f2_mul(v, k ? qs.y : qs.x), s2, ls2), k ? ng.y : ng.x);
             }
           }

@@ -65,3 +65,37 @@ def test_broadcast_tensors_never_reach_the_library():
         C.window_attention(q1.expand(4, -1, -1), g["rows"], g["scales"], g["block_tables"], g["seq_lens"], None, window=16)
     with pytest.raises(ValueError, match="share memory"):
         C.append(x1.expand(4, -1), g["rows"], g["scales"], g["block_tables"], g["seq_lens"])
+
+
+# --------------------------------------------------------------- attention
+
+def test_window_query_elements_beside_large_ones():
+    """Heads with a few dims of 2^0 to 2^12 times the others, where the rows hold nothing: the logits are the other
+    dims' alone.  An element is off by at most 2^-22 of its head's largest one; as evenly spread errors of 448 dims
+    that is 0.0013 of a logit's deviation here (0.0022 in natural units) at 2^12, under the result's own 2^-8."""
+    rng = np.random.default_rng(62)
+    n, heads, scale, bmm1 = 500, 64, 2.0 ** -6, 512 ** -0.5
+    codes = rng.normal(size=(8 * 64, 512)) * 85
+    codes[:, ::8] = 0
+    rows = R.to_e4m3(codes)
+    q = rng.normal(size=(1, heads, 512))
+    power = np.arange(heads) % 13
+    q[0, :, ::8] *= 2.0 ** power[:, None]
+    g = dict(rows=torch.from_numpy(rows.reshape(8, 64, 512)).to(DEV), scales=torch.full((8, 4), scale, device=DEV),
+             block_tables=i32(np.arange(8)[None]), seq_lens=i32([n]))
+    qt, qv = bf16(q)
+    kv = R.e4m3(rows)[:n] * scale
+    logits = qv[0] @ kv.T * bmm1
+    top = logits.max(axis=1, keepdims=True)
+    p = np.exp(logits - top)
+    want, lse = p @ kv / p.sum(axis=1, keepdims=True), (top[:, 0] + np.log(p.sum(axis=1))) / np.log(2)
+    for splits in (1, 2):
+        ws = torch.empty(C.window_workspace_size(qt, *g.values(), window=n, num_splits=splits) + 256, dtype=torch.uint8,
+                         device=DEV)
+        out, got = C.window_attention(qt, *g.values(), ws, window=n, num_splits=splits, bmm1_scale=bmm1)
+        err = np.sqrt(((out[0].double().cpu().numpy() - want) ** 2).mean(axis=1) / (want ** 2).mean(axis=1))
+        assert err.max() <= 2.0 ** -8, err.round(5).tolist()
+        # every logit off by its worst case, and 2^-18 of the products' sum for the fp32 additions
+        off = bmm1 * (2.0 ** -22 * np.abs(qv[0]).max(axis=1) * np.abs(kv).sum(axis=1).max()
+                      + 2.0 ** -18 * (np.abs(qv[0]) @ np.abs(kv).T).max(axis=1))
+        assert np.all(np.abs(got[0].double().cpu().numpy() - lse) <= 1.4427 * off + 2.0 ** -16)

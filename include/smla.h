@@ -384,6 +384,12 @@ typedef struct smla_cache {
  * whatever they hold.  A page outside the pool that a visible position needs
  * is treated as masked and flagged with SMLA_DEVERR_INDEX_OUT_OF_RANGE, as is
  * a position past the table's max_pages * page_size tokens.
+ *
+ * Precision: sums and maxima in fp32; the weights e^l are rounded as to BF16,
+ * each relative to itself (those whose part of O lies under 2^-10 of the
+ * largest part of a row: to 2^-18 of that one); a query element is held to
+ * BF16's eight bits or to 2^-22 of its head's largest, whichever is coarser;
+ * O is rounded once to BF16.
  */
 typedef struct smla_window_args {
   smla_cache cache;

@@ -108,8 +108,10 @@ __device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr, uint32_t lbo_bytes
   return d;
 }
 
-// Instruction descriptor bit of an MN-major A operand (OR it into idesc()).
+// Instruction descriptor bits of an MN-major A operand and of a B operand in E5M2
+// beside an A in E4M3 (OR them into idesc()).
 constexpr uint32_t kIdescAMnMajor = 1u << 15;
+constexpr uint32_t kIdescBE5M2 = 1u << 10;
 
 }  // namespace ptx
 }  // namespace smla

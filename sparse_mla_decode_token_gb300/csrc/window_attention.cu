@@ -9,9 +9,10 @@
 // significant bits, an E4M3 number four, so q 2^k = hi + 2^-5 lo with two E4M3
 // numbers, hi the rounded value and lo the rest, which has sums of its own and
 // so a scale of its own: exact down to 2^-14 of the head's largest element, an
-// absolute error of at most 2^-22 of that element below.  P is split the same
-// way, with one scale (its error is then below BF16's).  Two E4M3 products cost what one BF16 product would, without
-// widening the cache's rows in shared memory.
+// absolute error of at most 2^-22 of that element below.  P is hi in E4M3 + lo in
+// E5M2 with one scale: BF16's rounding from 2^-6 up (split_weights).  Two such
+// products cost what one BF16 product would, without widening the cache's rows in
+// shared memory.
 //
 // Layout: one CTA takes 64 heads of one token and one split of its rows, and
 // computes transposed products, rows by heads and dims by heads:
@@ -23,14 +24,27 @@
 // 64 heads' O^T takes 256 columns and two S^T buffers the other 256, so no
 // second CTA and no exchange is needed.  The row of a logit is its thread:
 // masks and block scales are per thread, and the running maximum is needed per
-// head only when some logit passes the reference by more than 2^4 (one
-// barrier-vote a tile); then the maxima are taken over lanes and warps, and O
-// is rescaled.
+// head only when the reference has to move (one barrier-vote a tile); then the
+// maxima are taken over lanes and warps, and O is rescaled.
 //
-// With t_j = log2(e) l_j + log2 s_j and the reference m (a running maximum of
-// t to within 2^4), P_j = 2^(t_j - m + 4) <= 2^8 weighs the raw code c_j, and
-// the denominator takes P_j / s_j: a block's scale is folded into P, never into
-// the tile.
+// With t_j = log2(e) l_j + log2 s_j and the reference m, P_j = 2^(t_j - m + 4)
+// weighs the raw code c_j, and the denominator takes P_j / s_j: a block's scale is
+// folded into P, never into the tile.  P has a floor (what lies under 2^-6 has
+// fewer bits than BF16, under 2^-17 it is nothing), and one row may hold nearly
+// all of the weight and little of the value, as first tokens do.  So
+//   - m puts the largest weight of a tile between 2^-6 and 2^8.75 (P <= 431 < 448),
+//     in both directions: O and the sums are fp32 and bear a smaller reference as
+//     well as a larger one (up to 2^24 below its highest, and not for tiles that are
+//     nothing beside what set it);
+//   - the weights that set m are those of rows with a code of 16 or more: where m
+//     moves up, a row of smaller codes is multiplied up in the tile by a power of
+//     two, exactly, and its weights divided by it.
+// A row's contribution to O is then off by at most 2^-8 of itself, BF16's rounding,
+// or 2^-18 of the one that m was set by.  (With a reference that only rises and a
+// floor of 2^-14 of the largest weight, a first token with 95 % of the weight and
+// small values took 14 % of the output of 2048 rows with it; now a head is off by 0.2 to
+// 0.3 %, the roundings of P and of the output.  It costs 9 to 11 % of the time: the look at
+// each tile's lightest head, tiles that move m down, a look at 16 codes a thread.)
 //
 // Rows come by TMA as chunks of 32 (16, 8) consecutive rows of one page, 5-D
 // boxes {128 B, 8 rows, 4 column blocks, groups, page}, which land as 8-row
@@ -49,15 +63,15 @@
 // softmax, the other's products run, and each second product frees its tile by
 // quarters, so that the next rows land behind it.
 //
-// What bounds it: a tile costs a CTA 2.1 us (4000 clocks), of which its tensor
+// What bounds it: a tile costs a CTA 2.3 us (4400 clocks), of which its tensor
 // instructions take 2670 (16 first products of 67 clocks; 32 second ones of 50,
 // not 32: with N = 64 they wait for their A operand out of shared memory).  The
 // rest is the chain second product -> free quarter -> rows -> first product ->
 // softmax of a buffer, which two 64 KB tiles (Q takes 64 KB, P 32) cannot hide
 // whole, and 7 us a unit for its query, sums and results.  Measured on a GB300:
-// 128 requests of one token, 128 heads, 2052 rows: 90 us, 765 TFLOP/s of the
+// 128 requests of one token, 128 heads, 2052 rows: 99 us, 696 TFLOP/s of the
 // plain products' count; 2049 tokens of four prompts, 128 heads, a window of 512:
-// 550 us, 504 TFLOP/s; two requests of 64 heads and 2 tiles: 13 us.
+// 620 us, 447 TFLOP/s; two requests of 64 heads and 2 tiles: 13 us.
 //
 // Five kinds of warps share an instruction cache that a unit's code overflows, so
 // code that need not be long is not: the products' loops are rolled to four and
@@ -99,7 +113,9 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 0;                     // O^T: four blocks of 128 dims, 64 columns each
 constexpr uint32_t kSCol = 256;                   // S^T: two buffers of 64 hi + 64 lo columns
 constexpr float kHeadroom = 4.f;                  // log2 of P at the reference
-constexpr float kMaxLog2 = 8.75f;                 // a logit may go this high before the reference moves: P <= 431 < 448
+constexpr float kMaxLog2 = 8.75f;                 // a weight may go this high before the reference moves: P <= 431 < 448
+constexpr float kMinLog2 = -6.f;                  // a tile's largest may lie this low: below, P has fewer bits than BF16
+constexpr float kMaxDrop = 24.f;                  // log2 that the reference may fall below its highest place
 constexpr float kMinScaleLog2 = -64.f;
 constexpr int kTileBytes = kRows * kHeadDim;      // 64 KB
 constexpr int kGroupBytes = 8 * kHeadDim;         // 8 rows x four 128-byte column blocks
@@ -124,6 +140,8 @@ struct alignas(16) Small {
   float wmax[4][kNH];                             // maxima or sums of each lane quarter; a head's thread, having
                                                   // read its four, puts the change of negref in row 0, a factor in row 1
   float scale[2][kRows];                          // block scale of each row of a tile, negative: masked
+  uint32_t light[2][kSoftmaxWarps];               // per lane quarter and warpgroup: its heads (bits) whose weights all lie
+                                                  // under 2^kMinLog2; bit 16: no row of the quarter is seen, 17: none is small, 18: no wait has given up
   Unit unit[2];
   uint64_t k_full[2], k_free[2][4], s_full[2], s_empty[2], p_full[2], scale_full[2], unit_full[2], unit_empty[2];
   uint64_t q_full, drained[2];
@@ -199,14 +217,40 @@ __device__ __forceinline__ int chunk_page(const KernelParams& kp, const Unit& u,
   return page >= 0 && page < c.num_pages ? page : -1;
 }
 
-// Two numbers of magnitude at most 2^8 to E4M3 pairs, hi = RN(p) and
-// lo = RN(p - hi), through fp16 (11 bits, its subnormals end at 2^-24).
-__device__ __forceinline__ void split_pair(float a, float b, uint32_t* hi, uint32_t* lo) {
+// Two weights of at most 431 to hi = RN(p) in E4M3 and lo = RN(p - hi) in E5M2,
+// through fp16 (11 bits, its subnormals end at 2^-24).  The rest of a p in
+// [2^e, 2^(e+1)) is at most 2^(e-4), three bits of it leave 2^(e-8): BF16's
+// rounding, down to 2^-6 where E4M3's subnormals begin.  Below, p is off by 2^-14
+// at most, under 2^-10 (where lo holds it alone) by an eighth of itself, under
+// 2^-14 by 2^-17.
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t* hi, uint32_t* lo) {
   const __half2 p = __floats2half2_rn(a, b);
   const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(p), __NV_SATFINITE, __NV_E4M3);
   const __half2 back(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3));
   *hi = h;
-  *lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(p, back)), __NV_SATFINITE, __NV_E4M3);
+  *lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(p, back)), __NV_SATFINITE, __NV_E5M2);
+}
+
+// The larger of m and the magnitude bits of the largest of 16 codes.
+__device__ __forceinline__ uint32_t largest_code(uint32_t m, uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m2 = __vmaxu2(m2, __vmaxu2(w[k] & 0x7f007f00u, w[k] << 8 & 0x7f007f00u));
+  return max(m, max(m2 >> 16, m2 & 0xffffu) >> 8);
+}
+
+// The power of two that takes a row with codes of magnitude bits up to `most` under
+// kLargeCode into [128, 256); 40 for a row of zeros.
+constexpr uint32_t kLargeCode = 0x58;             // 16
+__device__ __forceinline__ int small_row_exponent(uint32_t most) { return most == 0 ? 40 : 14 - (int)(most >> 3); }
+
+// Codes times 2^k, which the caller knows to be exact.
+__device__ __forceinline__ uint32_t scale_codes(uint32_t w, __half2 by) {
+  const __half2 lo(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3));
+  const __half2 hi(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3));
+  return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hmul2(lo, by)), __NV_SATFINITE, __NV_E4M3) |
+         (uint32_t)__nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hmul2(hi, by)), __NV_SATFINITE, __NV_E4M3) << 16;
 }
 
 // Two query values, scaled to magnitudes under 2^8, to E4M3 pairs hi = RN(q) and
@@ -487,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
   } else if (warp == kOutWarp) {
     // ----------------------------------------------------- second products
     constexpr uint32_t idesc_o = idesc(true, 128, kNH, true) | kIdescAMnMajor;
+    constexpr uint32_t idesc_half[2] = {idesc_o, idesc_o | kIdescBE5M2};
     int n = 0;
     bool ok = true;
     for (int x = 0; ok && x < mine; ++x) {
@@ -508,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 #pragma unroll
               for (int m = 0; m < 4; ++m)
                 mma<true>(tmem + kOCol + m * kNH, desc_sw128(tile + m * 1024 + k * 4 * kGroupBytes, 1024, kGroupBytes),
-                          desc_sw64(pb + half * kPHalf + k * 32 * kNH, 512, 512), idesc_o, i > 0 || k > 0 || half > 0);
+                          desc_sw64(pb + half * kPHalf + k * 32 * kNH, 512, 512), idesc_half[half], i > 0 || k > 0 || half > 0);
             mma_commit(bar(sm.k_free[b][k]));
           }
         }
@@ -523,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     const int hw = (threadIdx.x / kRows) * kHW;   // first of the thread's heads
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     uint64_t sum[kHW / 2];                        // of two heads each
+    float drop = 0.f;                             // how far head threadIdx.x's reference lies below its highest place
     int n = 0;
     {
       // the first unit's queries, while its rows are looked up (a unit without any leaves them unused)
@@ -547,7 +593,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         failed |= !warp_wait(cx, bar(sm.scale_full[b]), (n >> 1) & 1);
         const float s = sm.scale[b][r];
         const bool seen = !(s < 0.f);             // (a NaN scale is seen, and makes the result NaN)
-        const float ls = fmaxf(fast_log2(s), kMinScaleLog2), inv = fast_exp2(-ls);
+        const float ls = fmaxf(fast_log2(s), kMinScaleLog2);
+        float inv = fast_exp2(-ls);
+        // Is the row one of small codes?  (While its first product runs; of most, 16 codes of the thread's block say no.)
+        failed |= !warp_wait(cx, bar(sm.k_full[b]), (n >> 1) & 1);
+        uint8_t* const codes = smem + kOffK + b * kTileBytes + (r >> 3) * kGroupBytes + (r & 7) * 128 + (hw / kHW) * 1024;
+        auto codes16 = [&](int y) { return reinterpret_cast<uint4*>(codes + ((y ^ (r & 7)) << 4)); };
+        uint32_t most = largest_code(0, *codes16(0));
         failed |= !warp_wait(cx, bar(sm.s_full[b]), (n >> 1) & 1);
         tc_fence_after();
         uint64_t d[kHW / 2];                      // t - reference + headroom
@@ -574,37 +626,77 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sm.s_empty[b]));
         float top = -INFINITY;
+        uint32_t light = most >= kLargeCode;      // then: signs of d - kMinLog2, first head highest (NaN is not light)
 #pragma unroll
         for (int e = 0; e < kHW / 2; ++e) {
           float v, w;
           f2_unpack(d[e], v, w);
           top = fmaxf(top, fmaxf(v, w));
+          f2_unpack(f2_add(d[e], f2_pack(-kMinLog2, -kMinLog2)), v, w);
+          light = __funnelshift_l(__float_as_uint(v), light, 1);
+          light = __funnelshift_l(__float_as_uint(w), light, 1);
         }
+        light = __reduce_and_sync(0xffffffffu, (seen ? (light & 0xffffu) | (light >> 16) << 17 : 0x3ffffu) | (failed ? 0u : 0x40000u));
+        if (lane == 0) sm.light[b][(warp & 3) * 4 + hw / kHW] = light;
         if (i == 0 && warp == 0 && elect_one()) bulk_store_wait_read<0>();   // the last unit's output has left the P buffers
-        if (__builtin_expect(named_bar_or(1, kSoftmaxThreads, failed || fresh || (seen && top > kMaxLog2)), 0)) {
-          // ---- a new reference: the heads' maxima over the tile
-          if (named_bar_or(1, kSoftmaxThreads, failed)) break;
+        bool move = named_bar_or(1, kSoftmaxThreads, failed || fresh || (seen && top > kMaxLog2));
+        uint4 all = reinterpret_cast<const uint4*>(sm.light[b])[0];
+#pragma unroll
+        for (int y = 1; y < 4; ++y) {
+          const uint4 a = reinterpret_cast<const uint4*>(sm.light[b])[y];
+          all.x &= a.x, all.y &= a.y, all.z &= a.z, all.w &= a.w;
+        }
+        const bool any = (all.x & 0x10000u) == 0;      // (the same in all threads)
+        if (__builtin_expect(move || (any && ((all.x | all.y | all.z | all.w) & 0xffffu) != 0), 0)) {
+          // ---- a new reference, by what the rows can add to O at most: their weights times their largest codes
+          const uint32_t every = all.x & all.y & all.z & all.w;
+          if (every < 0x40000u) break;
+          int up = 0;                             // (a light tile's small rows are nothing beside what set the reference)
+          if (move && (every & 0x20000u) == 0) {
+            uint32_t* const row = reinterpret_cast<uint32_t*>(smem + kOffP + b * 2 * kPHalf) + r;   // (P comes behind barriers)
+#pragma unroll 1
+            for (int y = 1; y < 8; ++y) most = largest_code(most, *codes16(y));
+            reinterpret_cast<uint8_t*>(row)[hw / kHW] = (uint8_t)most;
+            named_bar_sync(1, kSoftmaxThreads);
+            const uint32_t m4 = *row;
+            if (seen && (m4 + (0x80u - kLargeCode) * 0x01010101u & 0x80808080u) == 0)   // no byte of kLargeCode or more
+              up = small_row_exponent(max(max(m4 & 0xffu, m4 >> 8 & 0xffu), max(m4 >> 16 & 0xffu, m4 >> 24)));
+          }
+          const uint64_t down2 = f2_pack(-(float)up, -(float)up);
 #pragma unroll
           for (int e = 0; e < kHW / 2; ++e) {
             float v, w;
-            f2_unpack(d[e], v, w);
+            f2_unpack(f2_add(d[e], down2), v, w);
             v = warp_max(seen ? v : -INFINITY);
             w = warp_max(seen ? w : -INFINITY);
             if (lane == e) *reinterpret_cast<float2*>(&sm.wmax[warp & 3][hw + 2 * e]) = make_float2(v, w);
           }
           named_bar_sync(1, kSoftmaxThreads);
+          float by = 0.f;                         // by how much the reference of head threadIdx.x moves
           if (threadIdx.x < kNH) {
             const int h = threadIdx.x;
-            // by how much the tile's maximum passes the reference
             const float m = fmaxf(fmaxf(sm.wmax[0][h], sm.wmax[1][h]), fmaxf(sm.wmax[2][h], sm.wmax[3][h])) - kHeadroom;
-            const float up = m == -INFINITY ? 0.f : fresh ? m : fmaxf(m, 0.f);
-            sm.negref[h] -= up;
-            sm.wmax[0][h] = -up;
-            sm.wmax[1][h] = fresh ? 0.f : fast_exp2(-up);
+            if (fresh) {
+              if (m != -INFINITY) by = m;
+              drop = 0.f;
+            } else if (m > 0.f) {
+              by = m;
+              drop = fmaxf(drop - by, 0.f);
+            } else if (m < kMinLog2 - kHeadroom &&
+                       m > drop - kHeadroom - 10.f - fast_log2((float)(sm.unit[x & 1].chunks << kShift))) {
+              // (as many rows as there are of less than that, with codes of 448, are under 2^-9 of one at the
+              // highest reference with 16)
+              by = fmaxf(m, drop - kMaxDrop);
+              drop -= by;
+            }
+            sm.negref[h] -= by;
+            sm.wmax[0][h] = -by;
+            sm.wmax[1][h] = fresh ? 0.f : fast_exp2(-by);
           }
+          const bool moved = named_bar_or(1, kSoftmaxThreads, by != 0.f);
           // (by the rows, not by the maxima: a head of NaN has none, and the others keep theirs)
-          fresh = !named_bar_or(1, kSoftmaxThreads, seen) && fresh;
-          if (i > 0) {
+          fresh = fresh && !any;
+          if (moved && i > 0) {
             // O^T by column, once the products into it are done
             failed |= !warp_wait(cx, bar(sm.k_free[b ^ 1][3]), ((n - 1) >> 1) & 1);
             tc_fence_after();
@@ -620,13 +712,31 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             tmem_wait_st();
             tc_fence_before();
           }
+          if (moved) {
 #pragma unroll
-          for (int e = 0; e < kHW / 2; ++e) {
-            d[e] = f2_add(d[e], *reinterpret_cast<const uint64_t*>(sm.wmax[0] + hw + 2 * e));
-            sum[e] = f2_mul(sum[e], *reinterpret_cast<const uint64_t*>(sm.wmax[1] + hw + 2 * e));
+            for (int e = 0; e < kHW / 2; ++e) {
+              d[e] = f2_add(d[e], *reinterpret_cast<const uint64_t*>(sm.wmax[0] + hw + 2 * e));
+              sum[e] = f2_mul(sum[e], *reinterpret_cast<const uint64_t*>(sm.wmax[1] + hw + 2 * e));
+            }
+          }
+          if (up != 0) {
+            // a row of small codes: the codes up, exactly, its weights down, which may be too large for P
+#pragma unroll
+            for (int e = 0; e < kHW / 2; ++e) d[e] = f2_add(d[e], down2);
+            inv *= __uint_as_float((uint32_t)(127 + up) << 23);
+            if (up < 40) {
+              const __half2 factor = __half2half2(__ushort_as_half((unsigned short)((15 + up) << 10)));
+#pragma unroll 1
+              for (int y = 0; y < 8; ++y) {
+                uint4* const at = codes16(y);
+                const uint4 v = *at;
+                *at = make_uint4(scale_codes(v.x, factor), scale_codes(v.y, factor), scale_codes(v.z, factor),
+                                 scale_codes(v.w, factor));
+              }
+            }
           }
         }
-        // P in E4M3 pairs: row r of the MN-major operand is 64 bytes, heads along it
+        // P in pairs: row r of the MN-major operand is 64 bytes, heads along it
         uint8_t* pb = smem + kOffP + b * 2 * kPHalf + r * kNH;
         const uint64_t inv2 = f2_pack(inv, inv);
         {
@@ -639,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
               v = fast_exp2(v);
               w = fast_exp2(w);
               sum[e] = f2_fma(f2_pack(v, w), inv2, sum[e]);
-              split_pair(v, w, hi + e, lo + e);
+              split_weights(v, w, hi + e, lo + e);
             }
           }
           const int at = ((hw >> 4) ^ ((r >> 1) & 3)) << 4;             // 64-byte swizzle

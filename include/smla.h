@@ -386,8 +386,9 @@ typedef struct smla_cache {
  * a position past the table's max_pages * page_size tokens.
  *
  * Precision: sums and maxima in fp32; the weights e^l are rounded as to BF16,
- * each relative to itself (those whose part of O lies under 2^-10 of the
- * largest part of a row: to 2^-18 of that one); a query element is held to
+ * each relative to itself, or, where that is finer, to 2^-13 of the largest
+ * part of O that one row has (its weight times its largest value); a query
+ * element is held to
  * BF16's eight bits or to 2^-22 of its head's largest, whichever is coarser;
  * O is rounded once to BF16.
  */

@@ -40,7 +40,7 @@
 //     moves up, a row of smaller codes is multiplied up in the tile by a power of
 //     two, exactly, and its weights divided by it.
 // A row's contribution to O is then off by at most 2^-8 of itself, BF16's rounding,
-// or 2^-18 of the one that m was set by.  (With a reference that only rises and a
+// or 2^-14 * 448 against the 2^4 * 16 or more of the one that m was set by.  (With a reference that only rises and a
 // floor of 2^-14 of the largest weight, a first token with 95 % of the weight and
 // small values took 14 % of the output of 2048 rows with it; now a head is off by 0.2 to
 // 0.3 %, the roundings of P and of the output.  It costs 9 to 11 % of the time: the look at

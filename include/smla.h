@@ -385,12 +385,10 @@ typedef struct smla_cache {
  * is treated as masked and flagged with SMLA_DEVERR_INDEX_OUT_OF_RANGE, as is
  * a position past the table's max_pages * page_size tokens.
  *
- * Precision: sums and maxima in fp32; the weights e^l are rounded as to BF16,
- * each relative to itself, or, where that is finer, to 2^-13 of the largest
- * part of O that one row has (its weight times its largest value); a query
- * element is held to
- * BF16's eight bits or to 2^-22 of its head's largest, whichever is coarser;
- * O is rounded once to BF16.
+ * Precision: sums and maxima in fp32; a weight e^l is rounded as to BF16, or to
+ * 2^-13 of the largest part of O that one row has (its weight times its largest
+ * value), whichever is coarser; a query element is held to BF16's eight bits or
+ * to 2^-22 of its head's largest, whichever is coarser; O is rounded once to BF16.
  */
 typedef struct smla_window_args {
   smla_cache cache;

@@ -144,7 +144,7 @@ struct alignas(16) Small {
                                                   // under 2^kMinLog2; bit 16: no row of the quarter is seen, 17: none is small, 18: no wait has given up
   Unit unit[2];
   uint64_t k_full[2], k_free[2][4], s_full[2], s_empty[2], p_full[2], scale_full[2], unit_full[2], unit_empty[2];
-  uint64_t q_full, drained[2];
+  uint64_t q_full[2], drained[2];
   uint32_t tmem;
   int32_t abort_flag;
 };
@@ -344,9 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
       mbar_init(bar(sm.scale_full[i]), 1);
       mbar_init(bar(sm.unit_full[i]), 1);
       mbar_init(bar(sm.unit_empty[i]), kUnitReaders);
+      mbar_init(bar(sm.q_full[i]), kSoftmaxWarps);
       mbar_init(bar(sm.drained[i]), 1);
     }
-    mbar_init(bar(sm.q_full), kSoftmaxWarps);
     sm.abort_flag = 0;
     fence_mbar_init_cluster();
     fence_proxy_async_smem();
@@ -360,7 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
   Ctx cx{&sm.abort_flag, p.err};
   // Tiles are numbered through all units of the CTA: tile n uses buffers n & 1,
   // and completes phase n >> 1 of their barriers.  Its second product frees the
-  // tile 32 rows at a time; k_free[b][3] is also its end.
+  // tile 32 rows at a time; k_free[b][3] is also its end.  Queries are numbered
+  // too, and take q_full in turn: behind a first unit without tiles the second
+  // unit's may be there before the first products' warp has waited for the first
+  // one's, but no third is before it has waited for both.
   const int mine = (kp.units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
 
   if (warp == kLoadWarp) {
@@ -506,8 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
       const int tiles = sm.unit[x & 1].tiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sm.unit_empty[x & 1]));
-      // (the first unit's queries come in any case, and a phase that nobody waited for would pass for the next)
-      if (ok && (tiles > 0 || x == 0)) ok = warp_wait(cx, bar(sm.q_full), q++ & 1);
+      // (the first unit's queries come in any case)
+      if (ok && (tiles > 0 || x == 0)) {
+        ok = warp_wait(cx, bar(sm.q_full[q & 1]), (q >> 1) & 1);
+        ++q;
+      }
       if (!ok || tiles == 0) continue;
       for (int i = 0; ok && i < tiles; ++i, ++n) {
         const int b = n & 1;
@@ -569,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     uint64_t sum[kHW / 2];                        // of two heads each
     float drop = 0.f;                             // how far head threadIdx.x's reference lies below its highest place
-    int n = 0;
+    int n = 0, q = 0;
     {
       // the first unit's queries, while its rows are looked up (a unit without any leaves them unused)
       Unit u;
@@ -577,7 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
       split_query(kp, u, smem + kOffQ, sm, warp, lane);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(sm.q_full));
+      if (lane == 0) mbar_arrive(bar(sm.q_full[0]));
+      ++q;
     }
     bool failed = !warp_wait(cx, bar(sm.unit_full[0]), 0);
     if (threadIdx.x < kNH) sm.negref[threadIdx.x] = 0.f;
@@ -785,7 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           split_query(kp, sm.unit[(x + 1) & 1], smem + kOffQ, sm, warp, lane);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(sm.q_full));
+          if (lane == 0) mbar_arrive(bar(sm.q_full[q & 1]));
+          ++q;
         }
       }
       __syncwarp();

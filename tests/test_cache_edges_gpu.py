@@ -99,3 +99,35 @@ def test_window_query_elements_beside_large_ones():
         off = bmm1 * (2.0 ** -22 * np.abs(qv[0]).max(axis=1) * np.abs(kv).sum(axis=1).max()
                       + 2.0 ** -18 * (np.abs(qv[0]) @ np.abs(kv).T).max(axis=1))
         assert np.all(np.abs(got[0].double().cpu().numpy() - lse) <= 1.4427 * off + 2.0 ** -16)
+
+
+@pytest.mark.parametrize("splits", [1, 0, 2])
+@pytest.mark.parametrize("empty", [1, 200, 500])
+def test_window_units_without_rows_in_front(empty, splits):
+    """A CTA's first units see nothing (positions below 0, tokens before the first offset), later ones do: the first
+    products' queries stay in step with their units."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    tail = 40
+    cache, q, rng = make(63, [empty, 300 + tail], [2 * empty, tail])      # the first request's first half lies below 0
+    lead = sms - 1                                                       # and tokens of no request before it
+    q_all = np.concatenate([rng.normal(size=(lead, 64, 512)), q])
+    cum = i32(cache.cum + lead)
+    g, qt = on_gpu(cache), bf16(q_all)[0]
+    size = C.window_workspace_size(qt, *g.values(), window=200, first_tokens=2, cum_seq_lens_q=cum, num_splits=splits)
+    for _ in range(3):
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        ws = torch.full((size + 256,), 0xFF, dtype=torch.uint8, device=DEV)
+        out, lse = torch.full_like(qt, 7.0), torch.full(qt.shape[:2], 7.0, device=DEV)
+        C.window_attention(qt, *g.values(), ws, window=200, first_tokens=2, cum_seq_lens_q=cum, num_splits=splits,
+                           bmm1_scale=512 ** -0.5, out=out, out_lse=lse, error_word=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        assert bool((out[:lead] == 7).all()) and bool((lse[:lead] == 7).all())
+        own = out[lead:].double().cpu().numpy(), lse[lead:].double().cpu().numpy()
+        assert np.all(own[0][:empty] == 0) and np.all(np.isneginf(own[1][:empty]))
+        # the last request's tokens, and those of the first that see something: a sample of both
+        for t in [empty, 2 * empty - 1] + list(range(2 * empty, 2 * empty + tail, 9)):
+            b, i = (0, t - 2 * empty) if t < 2 * empty else (1, t - 2 * empty - tail)
+            part = R.Cache(cache.rows, cache.scales, cache.tables[b:b + 1], cache.lens[b:b + 1] + i + 1, tokens=1)
+            want, wlse, tol_o, tol_l = R.window(part, bf16(q[t:t + 1])[1], window=200, first=2, bmm1=512 ** -0.5)
+            assert np.all(np.abs(own[0][t] - want[0]) <= tol_o[0]) and np.all(np.abs(own[1][t] - wlse[0]) <= tol_l[0])

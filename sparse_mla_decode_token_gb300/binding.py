@@ -11,6 +11,7 @@ the FlashInfer ``trtllm_batch_decode_sparse_mla_dsv4`` signature.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -218,6 +219,18 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _allocate_for(stream: Optional[int], index: int):
+    """Context in which outputs are allocated: what a call writes on ``stream`` must be that stream's memory, not what
+    the current stream may still use or reuse."""
+    if stream is None or index < 0 or stream == torch.cuda.current_stream(index).cuda_stream:
+        return contextlib.nullcontext()
+    if stream in (0, 1):                   # the default stream and its other name
+        return torch.cuda.stream(torch.cuda.default_stream(index))
+    if stream == 2:                        # the per-thread default stream, which has no memory of its own in torch
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=index))
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return SMLA_BF16
@@ -408,7 +421,8 @@ def sparse_mla_decode(query: torch.Tensor, swa_kv_cache: torch.Tensor, workspace
                       hca_seq_lens: Optional[torch.Tensor] = None,
                       comp_page_size: Optional[int] = None,
                       width: Optional[int] = None):
-    """Decode; returns ``(out, out_lse)``.  ``out`` / ``out_lse`` are allocated when not given.
+    """Decode; returns ``(out, out_lse)``.  ``out`` / ``out_lse`` are allocated when not given (as ``stream``'s memory,
+    where that is another than the current one).
 
     With ``hca_compressed_block_tables`` the compressed segment is given as
     page tables; ``comp_page_size`` defaults to the compressed cache view's
@@ -419,10 +433,11 @@ def sparse_mla_decode(query: torch.Tensor, swa_kv_cache: torch.Tensor, workspace
         comp_page_size = compressed_kv_cache.shape[-2]
     T = query.shape[0] if query.dim() == 3 else query.shape[0] * query.shape[1]
     H = query.shape[-2]
-    if out is None:
-        out = torch.empty((T, H, HEAD_DIM), dtype=torch.bfloat16, device=query.device)
-    if out_lse is None:
-        out_lse = torch.empty((T, H), dtype=torch.float32, device=query.device)
+    with _allocate_for(stream, query.get_device()):
+        if out is None:
+            out = torch.empty((T, H, HEAD_DIM), dtype=torch.bfloat16, device=query.device)
+        if out_lse is None:
+            out_lse = torch.empty((T, H), dtype=torch.float32, device=query.device)
     args = make_args(q=query, swa_kv=swa_kv_cache, compressed_kv=compressed_kv_cache,
                      sparse_indices=sparse_indices, seq_lens=seq_lens, out=out,
                      sparse_topk_lens=sparse_topk_lens, cum_seq_lens_q=cum_seq_lens_q,

@@ -235,7 +235,8 @@ def window_attention(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, 
                      stream: Optional[int] = None):
     """Attention of BF16 queries ``[T, H, 512]`` over the last ``window`` cached
     tokens of their request up to their own position, and its first
-    ``first_tokens``; returns ``(out, out_lse)``, allocated when not given."""
+    ``first_tokens``; returns ``(out, out_lse)``, allocated when not given (as
+    ``stream``'s memory, where that is another than the current one)."""
     done = (_extension or extension()).window_attention(
         q, rows, scales, block_tables, seq_lens, workspace_buffer, cum_seq_lens_q, sinks, window, first_tokens, num_splits,
         bmm1_scale, bmm2_scale, out, out_lse, error_word, stream)
@@ -245,12 +246,15 @@ def window_attention(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, 
         _check(done)
     a = _window_args(q, rows, scales, block_tables, seq_lens, cum_seq_lens_q, sinks, window, first_tokens, num_splits)
     T, H = a.sum_q, a.num_heads
+    with _b._allocate_for(stream, q.get_device()):
+        new_out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else None
+        new_lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if out_lse is None else None
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = new_out
     elif out.dtype != torch.bfloat16 or not out.is_contiguous() or out.numel() != T * H * HEAD_DIM:
         raise ValueError("out must be a contiguous bfloat16 tensor of T*H*512 elements")
     if out_lse is None:
-        out_lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        out_lse = new_lse
     elif out_lse.dtype != torch.float32 or not out_lse.is_contiguous() or out_lse.numel() != T * H:
         raise ValueError("out_lse must be a contiguous float32 tensor of T*H elements")
     _words("error_word", error_word, 1)

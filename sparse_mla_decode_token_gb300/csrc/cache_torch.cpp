@@ -169,6 +169,8 @@ PyObject* window_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     w.q_stride_token = T > 1 ? q.stride(0) : 0;
     w.error_word = static_cast<int32_t*>(call.words(a[15], 1, true));
     void* const stream = call.stream(a[16]);
+    // (outputs of a call on another stream than the current one have to be that stream's memory)
+    need((a[13] != Py_None && a[14] != Py_None) || stream == call.stream(Py_None));
     at::Tensor out, lse;                    // those that are not given
     if (a[13] == Py_None) {
       out = at::empty_like(q, q.options(), c10::MemoryFormat::Contiguous);

@@ -131,3 +131,58 @@ def test_window_units_without_rows_in_front(empty, splits):
             part = R.Cache(cache.rows, cache.scales, cache.tables[b:b + 1], cache.lens[b:b + 1] + i + 1, tokens=1)
             want, wlse, tol_o, tol_l = R.window(part, bf16(q[t:t + 1])[1], window=200, first=2, bmm1=512 ** -0.5)
             assert np.all(np.abs(own[0][t] - want[0]) <= tol_o[0]) and np.all(np.abs(own[1][t] - wlse[0]) <= tol_l[0])
+
+
+# ----------------------------------------------------------------- streams
+
+def test_outputs_belong_to_the_stream_of_the_call():
+    """Outputs that a call allocates are written on the stream that it was given: memory of the current stream, free
+    there but not behind that stream's work, must not serve."""
+    cache, q, _ = make(64, [300, 200], [2, 1], heads=64)
+    g, qt, cum = on_gpu(cache), bf16(q)[0], i32(cache.cum)
+    ws = torch.empty(C.window_workspace_size(qt, *g.values(), window=200, cum_seq_lens_q=cum) + 256, dtype=torch.uint8,
+                     device=DEV)
+    args = dict(window=200, cum_seq_lens_q=cum, bmm1_scale=512 ** -0.5)
+    want, want_lse = C.window_attention(qt, *g.values(), ws, **args)
+    side = torch.cuda.Stream()
+
+    def freed(shape, dtype):
+        """Addresses of two blocks that the current stream has just given back."""
+        a, b = torch.empty(shape, dtype=dtype, device=DEV), torch.empty(shape, dtype=dtype, device=DEV)
+        return {a.data_ptr(), b.data_ptr()}
+    for k in range(3):
+        out_only = torch.empty_like(want) if k == 1 else None
+        lse_only = torch.empty_like(want_lse) if k == 2 else None
+        torch.cuda.synchronize()
+        mine = freed(want.shape, torch.bfloat16) | freed(want_lse.shape, torch.float32)
+        out, lse = C.window_attention(qt, *g.values(), ws, stream=side.cuda_stream, out=out_only, out_lse=lse_only, **args)
+        torch.cuda.synchronize()
+        assert (k == 1 or out.data_ptr() not in mine) and (k == 2 or lse.data_ptr() not in mine)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    # on the current stream, named or not, the current stream's memory does
+    here = torch.cuda.current_stream().cuda_stream
+    for stream in (None, here):
+        mine = freed(want.shape, torch.bfloat16)
+        assert C.window_attention(qt, *g.values(), ws, stream=stream, **args)[0].data_ptr() in mine
+
+
+def test_decode_outputs_belong_to_the_stream_of_the_call():
+    from sparse_mla_decode_token_gb300 import binding as B
+    T, H = 3, 128
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    q, kv = (torch.randn(n, 512, generator=gen, device=DEV).to(torch.bfloat16) for n in (T * H, 512))
+    idx = torch.randint(0, 512, (T, 256), generator=gen, device=DEV, dtype=torch.int32)
+    lens, seq = torch.full((T,), 256, dtype=torch.int32, device=DEV), torch.full((T,), 5000, dtype=torch.int32, device=DEV)
+    q = q.view(T, H, 512)
+    ws = torch.empty(B.workspace_size(q, idx, seq) + 256, dtype=torch.uint8, device=DEV)
+    want, want_lse = B.sparse_mla_decode(q, kv, ws, idx, kv, lens, seq, bmm1_scale=512 ** -0.5)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a, b = torch.empty_like(want), torch.empty_like(want_lse)
+    mine = {a.data_ptr(), b.data_ptr()}
+    del a, b
+    out, lse = B.sparse_mla_decode(q, kv, ws, idx, kv, lens, seq, bmm1_scale=512 ** -0.5, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert out.data_ptr() not in mine and lse.data_ptr() not in mine
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)

@@ -214,10 +214,13 @@ def _window_args(q, rows, scales, tables, seq_lens, cum, sinks, window, first_to
 def window_workspace_size(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block_tables: torch.Tensor,
                           seq_lens: torch.Tensor, *, window: int, first_tokens: int = 0,
                           cum_seq_lens_q: Optional[torch.Tensor] = None, num_splits: int = 0,
-                          device: int = 0) -> int:
-    """Workspace bytes of ``window_attention`` for these shapes (no device memory is read)."""
+                          device: Optional[int] = None) -> int:
+    """Workspace bytes of ``window_attention`` for these shapes (no device memory is
+    read), on ``device``, by default q's."""
     a = _window_args(q, rows, scales, block_tables, seq_lens, cum_seq_lens_q, None, window, first_tokens, num_splits)
     n = ctypes.c_size_t(0)
+    if device is None:
+        device = max(q.get_device(), 0)
     _check(_b.lib().smla_window_workspace_size(ctypes.byref(a), device, ctypes.byref(n)))
     return int(n.value)
 

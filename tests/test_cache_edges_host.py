@@ -26,3 +26,26 @@ def test_broadcast_latents_are_refused(lib):
     with pytest.raises(ValueError, match="share memory"):
         C.append(torch.zeros(1, 512, dtype=torch.bfloat16).expand(4, 512), t["rows"], t["scales"], t["block_tables"],
                  t["seq_lens"])
+
+
+def test_window_workspace_is_sized_for_the_device_of_the_queries(lib, monkeypatch):
+    """The call plans for q's device, which need not be device 0."""
+    asked = []
+
+    class Library:
+        def smla_window_workspace_size(self, args, device, bytes_out):
+            asked.append(device)
+            return 0
+
+    class Elsewhere(torch.Tensor):
+        def get_device(self):
+            return 3
+
+    monkeypatch.setattr(C._b, "lib", lambda: Library())
+    kw = host_tensors()
+    kw.pop("workspace_buffer")
+    C.window_workspace_size(**kw)
+    kw["q"] = kw["q"].as_subclass(Elsewhere)
+    C.window_workspace_size(**kw)
+    C.window_workspace_size(**kw, device=1)
+    assert asked == [0, 3, 1]

@@ -458,7 +458,10 @@ smla_status smla_cache_append(const smla_append_args* args, void* stream);
  *   shrinking) gets a page of its own for it first, and the pair
  *   (shared, own) is added to the moves: copy them (smla_pages_copy) before
  *   the cache is written.  With too few free pages the last entries stay as
- *   they were (-1, or the shared page) and SMLA_DEVERR_OUT_OF_PAGES is set.
+ *   they were (-1, or the shared page) and SMLA_DEVERR_OUT_OF_PAGES is set:
+ *   such a step must not be appended (smla_cache_append knows no counts and
+ *   would write into the page that the request still shares), so a host that
+ *   cannot rule it out looks at the error word between the two.
  *   Needs move_capacity >= rows.
  * smla_pages_fork: request b with parents[b] >= 0, which must hold nothing
  *   (lens[b] == 0), takes its parent's pages, each counted once more; out_lens

@@ -360,7 +360,9 @@ def pages_resize(block_tables: torch.Tensor, ref_counts: torch.Tensor, lens: tor
                  error_word: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> None:
     """Takes each request from ``lens`` to ``new_lens`` tokens: pages dropped,
     then the lowest free pages handed out; ``moves`` receives the shared pages
-    that a growing request got a copy of (``pages_copy`` them)."""
+    that a growing request got a copy of (``pages_copy`` them).  Where pages run
+    out (``DEVERR_OUT_OF_PAGES`` in ``error_word``) a request may be left with a
+    page that it still shares, which ``append`` would write into: look at it first."""
     status = (_extension or extension()).pages_resize(block_tables, ref_counts, lens, new_lens, workspace_buffer, page_size,
                                                       moves, error_word, stream)
     if status is not None:

@@ -696,7 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
               by = fmaxf(m, drop - kMaxDrop);
               drop -= by;
             }
-            sm.negref[h] -= by;
+            // (by what it is rounded to, as the sums are: they would drift apart from it over many moves)
+            const float now = sm.negref[h], then = now - by;
+            by = now - then;
+            sm.negref[h] = then;
             sm.wmax[0][h] = -by;
             sm.wmax[1][h] = fresh ? 0.f : fast_exp2(-by);
           }

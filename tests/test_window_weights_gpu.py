@@ -180,3 +180,17 @@ def test_window_heavy_first_token_in_a_prompt(heads):
         for t in range(0, tokens, 7):
             pos = n - tokens + t
             check((out[t], lse[t]), q[t:t + 1], kv[:pos + 1][visible(pos + 1, window, first)])
+
+
+@pytest.mark.parametrize("code,scale", [(0x00, 2.0 ** -64), (0x38, 2.0 ** -64), (0x00, 1.0), (0x38, 1.0)])
+def test_window_reference_and_sums_stay_in_step(code, scale):
+    """Thousands of tiles that each move the reference by a rounding or nothing: the LSE of n equal rows is log2 n, off
+    by fp32 additions of a few thousand terms (2^-14) at most."""
+    n, page = 300000, 64
+    pages = -(-n // page)
+    rows = torch.full((pages, page, 512), code, dtype=torch.uint8, device=DEV)
+    g = dict(rows=rows, scales=torch.full((pages, 4), scale, device=DEV), block_tables=i32(np.arange(pages)[None]),
+             seq_lens=i32([n]))
+    for splits in (1, 2, 0):
+        _, lse = call(g, np.zeros((1, 64, 512)), n, 0, splits)
+        assert np.abs(lse - math.log2(n)).max() <= 2.0 ** -14

@@ -354,8 +354,8 @@ typedef struct smla_cache {
   int64_t row_stride;             /* bytes between the rows of a page [512], a multiple of 16 */
   int64_t page_stride;            /* bytes between pages [page_size * row_stride], a multiple of 16, at least
                                      (page_size - 1) * row_stride + 512 */
-  float* scales;                  /* [num_pages, page_size / block_rows]; finite, not negative; scales under 2^-64
-                                     weigh a row's values as 2^-64 would */
+  float* scales;                  /* [num_pages, page_size / block_rows]; not negative, at most 2^90; scales under
+                                     2^-64 weigh a row's values as 2^-64 would */
   int64_t scale_stride;           /* elements between pages' scales [page_size / block_rows] */
   int64_t num_pages;              /* pages of the pool, 1 .. 2^31 - 1 */
   int32_t page_size;              /* tokens per page, a multiple of 8, at most 2^20 */
@@ -387,8 +387,9 @@ typedef struct smla_cache {
  *
  * Precision: sums and maxima in fp32; a weight e^l is rounded as to BF16, or to
  * 2^-13 of the largest part of O that one row has (its weight times its largest
- * value), whichever is coarser; a query element is held to BF16's eight bits or
- * to 2^-22 of its head's largest, whichever is coarser; O is rounded once to BF16.
+ * value; of a row of zeros, 2^-40 of its weight), whichever is coarser; a query
+ * element is held to BF16's eight bits or to 2^-22 of its head's largest,
+ * whichever is coarser; O is rounded once to BF16.
  */
 typedef struct smla_window_args {
   smla_cache cache;

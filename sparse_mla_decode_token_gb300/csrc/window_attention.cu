@@ -38,7 +38,7 @@
 //     nothing beside what set it);
 //   - the weights that set m are those of rows with a code of 16 or more: where m
 //     moves up, a row of smaller codes is multiplied up in the tile by a power of
-//     two, exactly, and its weights divided by it.
+//     two, exactly, and its weights divided by it (a row of zeros counts as 2^-40).
 // A row's contribution to O is then off by at most 2^-8 of itself, BF16's rounding,
 // or 2^-14 * 448 against the 2^4 * 16 or more of the one that m was set by.  (With a reference that only rises and a
 // floor of 2^-14 of the largest weight, a first token with 95 % of the weight and
@@ -116,6 +116,8 @@ constexpr float kHeadroom = 4.f;                  // log2 of P at the reference
 constexpr float kMaxLog2 = 8.75f;                 // a weight may go this high before the reference moves: P <= 431 < 448
 constexpr float kMinLog2 = -6.f;                  // a tile's largest may lie this low: below, P has fewer bits than BF16
 constexpr float kMaxDrop = 24.f;                  // log2 that the reference may fall below its highest place
+constexpr float kSumShift = 32.f;                 // log2 by which the sums of P / s are held down: blocks of 2^-64, rows of
+                                                  // zeros (2^40) and a low reference (2^24) take them up to 2^104 a row
 constexpr float kMinScaleLog2 = -64.f;
 constexpr int kTileBytes = kRows * kHeadDim;      // 64 KB
 constexpr int kGroupBytes = 8 * kHeadDim;         // 8 rows x four 128-byte column blocks
@@ -601,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         const float s = sm.scale[b][r];
         const bool seen = !(s < 0.f);             // (a NaN scale is seen, and makes the result NaN)
         const float ls = fmaxf(fast_log2(s), kMinScaleLog2);
-        float inv = fast_exp2(-ls);
+        float inv = fast_exp2(-ls - kSumShift);
         // Is the row one of small codes?  (While its first product runs; of most, 16 codes of the thread's block say no.)
         failed |= !warp_wait(cx, bar(sm.k_full[b]), (n >> 1) & 1);
         uint8_t* const codes = smem + kOffK + b * kTileBytes + (r >> 3) * kGroupBytes + (r & 7) * 128 + (hw / kHW) * 1024;
@@ -840,8 +842,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         total = (sm.wmax[0][h] + sm.wmax[1][h]) + (sm.wmax[2][h] + sm.wmax[3][h]);
         float f = 0.f, lse = -INFINITY;
         if (!(total == 0.f)) {                    // NaN passes
-          lse = fast_log2(total) - sm.negref[h];
-          f = out_scale / (total + total * fast_exp2(sink - lse));
+          lse = fast_log2(total) + kSumShift - sm.negref[h];
+          f = out_scale * (1.f / (1ull << (int)kSumShift)) / (total + total * fast_exp2(sink - lse));
         }
         sm.wmax[1][h] = f;
         sm.negref[h] = 0.f;                       // the next unit's

@@ -182,6 +182,38 @@ def test_window_heavy_first_token_in_a_prompt(heads):
             check((out[t], lse[t]), q[t:t + 1], kv[:pos + 1][visible(pos + 1, window, first)])
 
 
+@pytest.mark.parametrize("zeros,size", [(3000, 3400), (600000, 600100)])
+def test_window_rows_of_zeros_at_the_smallest_scale(zeros, size):
+    """Zero latents as the append holds them, codes of 0 with a scale of 2^-64, in front of rows whose logits lie up to
+    75 below theirs: the sums of weights over scales stay finite and in step with the reference, so the LSE is right,
+    and so is the output of what lies above 2^-44 of a row of zeros (which counts as a part of 2^-40)."""
+    page, heads = 64, 64
+    pages = -(-size // page)
+    rng = np.random.default_rng(31)
+    rows = torch.zeros(pages, page, 512, dtype=torch.uint8, device=DEV)
+    scales = torch.full((pages, 4), 2.0 ** -64, device=DEV)
+    codes = R.to_e4m3((rng.normal(size=(size - zeros, 512)) * 0.3 + np.abs(rng.normal(size=512))) * 60)
+    flat = rows.view(-1, 512)
+    at = zeros // 16 * 16                                  # whole blocks from here on (their first rows stay zeros)
+    flat[zeros:size] = torch.from_numpy(codes).to(DEV)
+    scales.view(-1)[at // 16:] = 2.0 ** -6
+    g = dict(rows=rows, scales=scales, block_tables=i32(np.arange(pages)[None]), seq_lens=i32([size]))
+    kv = R.e4m3(codes) * 2.0 ** -6
+    mean = kv.mean(axis=0)
+    fall = np.linspace(1.0, 75.0, heads)                   # nats by which the others lie below the zeros, per head
+    q = (-fall[:, None] * mean[None] / (mean @ mean * BMM1))[None]
+    qv = bf16(q)[1][0]
+    l = torch.from_numpy(qv @ kv.T * BMM1)
+    total = torch.logsumexp(torch.cat([l, torch.full((heads, 1), math.log(zeros), dtype=torch.float64)], dim=1), dim=1)
+    want = (torch.exp(l - total[:, None]) @ torch.from_numpy(kv)).numpy()
+    for splits in (1, 0):
+        out, lse = call(g, q, size, 0, splits)
+        assert np.abs(lse - total.numpy() / math.log(2)).max() <= 2e-3
+        err = np.sqrt(((out - want) ** 2).mean(axis=1)) / np.sqrt((want ** 2).mean(axis=1))
+        seen = fall < 44 * math.log(2)
+        assert err[seen].max() <= 2.0 ** -8, err.round(5).tolist()
+
+
 @pytest.mark.parametrize("code,scale", [(0x00, 2.0 ** -64), (0x38, 2.0 ** -64), (0x00, 1.0), (0x38, 1.0)])
 def test_window_reference_and_sums_stay_in_step(code, scale):
     """Thousands of tiles that each move the reference by a rounding or nothing: the LSE of n equal rows is log2 n, off

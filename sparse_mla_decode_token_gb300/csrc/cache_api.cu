@@ -167,10 +167,10 @@ struct WindowPlan {
 };
 
 // Splits that cost `pairs` pairs of `tiles` tiles least on `sms` SMs, one CTA each
-// at a time.  Measured on a GB300, a tile costs a CTA 2.1 us, and a second split
+// at a time.  Measured on a GB300, a tile costs a CTA 2.3 us, and a second split
 // the merge: 1.3 tiles' time and a 7000th of one for each partial row of 512 values
-// (1 token x 64 heads, 2 tiles: 12.7 us whole, 13.7 in two; 3 tiles: 16.1 against
-// 14.8 in three; 32 x 128, 5 tiles: 21.5 against 22.9 in two, 9: 30.1 against 27.8).
+// (1 token x 64 heads, 2 tiles: 12.3 us whole, 12.9 in two; 3 tiles: 15.8 against
+// 13.5 in three; 32 x 128, 5 tiles: 22.5 against 24.2 in two, 9: 33.2 against 30.0).
 int cheapest_splits(int64_t pairs, int64_t tiles, int sms) {
   const int64_t most = std::min<int64_t>({sms / pairs, tiles, kMaxWindowSplits});
   int best = 1;
@@ -196,10 +196,11 @@ WindowPlan window_plan(const smla_window_args* a, int sms) {
     const int64_t all = ((int64_t)a->cache.max_pages * page + chunk - 1) / chunk;
     const int64_t seen = ((int64_t)a->window + chunk - 2) / chunk + 1 + ((int64_t)a->first_tokens + chunk - 1) / chunk;
     const int64_t tiles = (std::min(all, seen) * chunk + kWindowTile - 1) / kWindowTile;
-    // The pairs of the last, partly filled turn of the SMs are the ones worth splitting (160 pairs of 9 tiles: 54 us
-    // whole, 43 so); behind four full turns the turns' own spread hides it (5672 of 6: 626 us whole, 641 so).
+    // The pairs of the last, partly filled turn of the SMs are the ones worth splitting (160 pairs of 9 tiles: 61 us
+    // whole, 49 so; 772: 182 and 171; 1232 of 5: 170.5 and 168.5).  Behind more turns they are a small part, and the
+    // kernel with splits is 3 % slower (1864 of 5: 240 us whole, 243 so; 2448: 305 and 307; of 9: 382 and 372, 485 and 479).
     const int64_t rest = pairs % sms;
-    w.splits = rest > 0 && pairs < 4 * (int64_t)sms ? cheapest_splits(rest, tiles, sms) : 1;
+    w.splits = rest > 0 && pairs < 10 * (int64_t)sms ? cheapest_splits(rest, tiles, sms) : 1;
     w.whole = w.splits > 1 ? pairs - rest : pairs;
   }
   w.units = w.whole + (pairs - w.whole) * w.splits;

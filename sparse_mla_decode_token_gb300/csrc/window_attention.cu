@@ -36,9 +36,10 @@
 //     in both directions: O and the sums are fp32 and bear a smaller reference as
 //     well as a larger one (up to 2^24 below its highest, and not for tiles that are
 //     nothing beside what set it);
-//   - the weights that set m are those of rows with a code of 16 or more: where m
-//     moves up, a row of smaller codes is multiplied up in the tile by a power of
-//     two, exactly, and its weights divided by it (a row of zeros counts as 2^-40).
+//   - where m moves up, a row of small codes (under 16 beside large ones; else under
+//     a sixteenth of the tile's largest) is multiplied up in the tile by a power of
+//     two, exactly, and its weights divided by it, so that m is set by what rows can
+//     add to O (a row of zeros counts as 2^-40).
 // A row's contribution to O is then off by at most 2^-8 of itself, BF16's rounding,
 // or 2^-14 * 448 against the 2^4 * 16 or more of the one that m was set by.  (With a reference that only rises and a
 // floor of 2^-14 of the largest weight, a first token with 95 % of the weight and
@@ -242,10 +243,15 @@ __device__ __forceinline__ uint32_t largest_code(uint32_t m, uint4 v) {
   return max(m, max(m2 >> 16, m2 & 0xffffu) >> 8);
 }
 
-// The power of two that takes a row with codes of magnitude bits up to `most` under
-// kLargeCode into [128, 256); 40 for a row of zeros.
+// log2 by which a row with codes of magnitude bits up to `most` falls short of
+// [128, 256), if they all lie under kLargeCode; 40 for a row of zeros.
 constexpr uint32_t kLargeCode = 0x58;             // 16
-__device__ __forceinline__ int small_row_exponent(uint32_t most) { return most == 0 ? 40 : 14 - (int)(most >> 3); }
+__device__ __forceinline__ int shortfall(uint32_t most) {
+  return most >= kLargeCode ? 0 : most == 0 ? 40 : 14 - (int)(most >> 3);
+}
+__device__ __forceinline__ uint32_t largest_byte(uint32_t w) {
+  return max(max(w & 0xffu, w >> 8 & 0xffu), max(w >> 16 & 0xffu, w >> 24));
+}
 
 // Codes times 2^k, which the caller knows to be exact.
 __device__ __forceinline__ uint32_t scale_codes(uint32_t w, __half2 by) {
@@ -576,7 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     const int hw = (threadIdx.x / kRows) * kHW;   // first of the thread's heads
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     uint64_t sum[kHW / 2];                        // of two heads each
-    float drop = 0.f;                             // how far head threadIdx.x's reference lies below its highest place
+    float drop = 0.f;                             // how far head threadIdx.x's reference lies below its highest place,
+                                                  // counted for rows with a code of 16 or more
     int n = 0, q = 0;
     {
       // the first unit's queries, while its rows are looked up (a unit without any leaves them unused)
@@ -660,16 +667,20 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
           // ---- a new reference, by what the rows can add to O at most: their weights times their largest codes
           const uint32_t every = all.x & all.y & all.z & all.w;
           if (every < 0x40000u) break;
-          int up = 0;                             // (a light tile's small rows are nothing beside what set the reference)
+          // (a light tile's small rows are nothing beside what set the reference)
+          int up = 0, low = 0;                    // by how much the row's codes are small beside the tile's, and the tile's
           if (move && (every & 0x20000u) == 0) {
-            uint32_t* const row = reinterpret_cast<uint32_t*>(smem + kOffP + b * 2 * kPHalf) + r;   // (P comes behind barriers)
+            uint32_t* const rows = reinterpret_cast<uint32_t*>(smem + kOffP + b * 2 * kPHalf);      // (P comes behind barriers)
 #pragma unroll 1
             for (int y = 1; y < 8; ++y) most = largest_code(most, *codes16(y));
-            reinterpret_cast<uint8_t*>(row)[hw / kHW] = (uint8_t)most;
+            reinterpret_cast<uint8_t*>(rows + r)[hw / kHW] = (uint8_t)(seen ? most : 0u);
             named_bar_sync(1, kSoftmaxThreads);
-            const uint32_t m4 = *row;
-            if (seen && (m4 + (0x80u - kLargeCode) * 0x01010101u & 0x80808080u) == 0)   // no byte of kLargeCode or more
-              up = small_row_exponent(max(max(m4 & 0xffu, m4 >> 8 & 0xffu), max(m4 >> 16 & 0xffu, m4 >> 24)));
+            uint32_t largest = 0;
+#pragma unroll
+            for (int y = 0; y < kRows / 32; ++y) largest = max(largest, largest_byte(rows[y * 32 + lane]));
+            low = shortfall(__reduce_max_sync(0xffffffffu, largest));
+            up = seen ? shortfall(largest_byte(rows[r])) - low : 0;
+            if (up < 4) up = 0;                   // (as 16 and 448 are both large)
           }
           const uint64_t down2 = f2_pack(-(float)up, -(float)up);
 #pragma unroll
@@ -687,10 +698,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
             const float m = fmaxf(fmaxf(sm.wmax[0][h], sm.wmax[1][h]), fmaxf(sm.wmax[2][h], sm.wmax[3][h])) - kHeadroom;
             if (fresh) {
               if (m != -INFINITY) by = m;
-              drop = 0.f;
+              drop = -(float)low;
             } else if (m > 0.f) {
               by = m;
-              drop = fmaxf(drop - by, 0.f);
+              drop = fmaxf(drop - by, -(float)low);
             } else if (m < kMinLog2 - kHeadroom &&
                        m > drop - kHeadroom - 10.f - fast_log2((float)(sm.unit[x & 1].chunks << kShift))) {
               // (as many rows as there are of less than that, with codes of 448, are under 2^-9 of one at the
@@ -736,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 #pragma unroll
             for (int e = 0; e < kHW / 2; ++e) d[e] = f2_add(d[e], down2);
             inv *= __uint_as_float((uint32_t)(127 + up) << 23);
-            if (up < 40) {
+            if (up <= 14) {                       // (more: a row of zeros)
               const __half2 factor = __half2half2(__ushort_as_half((unsigned short)((15 + up) << 10)));
 #pragma unroll 1
               for (int y = 0; y < 8; ++y) {

@@ -226,3 +226,21 @@ def test_window_reference_and_sums_stay_in_step(code, scale):
     for splits in (1, 2, 0):
         _, lse = call(g, np.zeros((1, 64, 512)), n, 0, splits)
         assert np.abs(lse - math.log2(n)).max() <= 2.0 ** -14
+
+
+def test_window_rows_of_zeros_among_rows_of_small_codes():
+    """Rows of zeros, of E4M3's smallest numbers and of codes under 8 in one tile: whatever is multiplied up stays exact."""
+    rng = np.random.default_rng(33)
+    n, page = 500, 64
+    codes = rng.normal(size=(512, 512)) * 1.5 + rng.normal(size=512)
+    codes[::7] = 0
+    codes[1::7] *= 2.0 ** -9
+    codes[2::7] *= 2.0 ** -5
+    rows = R.to_e4m3(codes)
+    g = dict(rows=torch.from_numpy(rows.reshape(8, page, 512)).to(DEV), scales=torch.ones(8, 4, device=DEV),
+             block_tables=i32(np.arange(8)[None]), seq_lens=i32([n]))
+    kv = R.e4m3(rows)[:n]
+    q = rng.normal(size=(1, 64, 512)) * np.linspace(0, 6, 64)[None, :, None]
+    q[0, 32:] -= 3 * kv[3::7].mean(axis=0)                 # (half of the heads put the zeros first)
+    for splits in (1, 3, 0):
+        check(call(g, q, n, 0, splits), q, kv)

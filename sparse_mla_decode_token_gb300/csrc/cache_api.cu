@@ -167,7 +167,7 @@ struct WindowPlan {
 };
 
 // Splits that cost `pairs` pairs of `tiles` tiles least on `sms` SMs, one CTA each
-// at a time.  Measured on a GB300, a tile costs a CTA 2.3 us, and a second split
+// at a time.  Measured on a GB300, a tile costs a CTA 2.5 us, and a second split
 // the merge: 1.3 tiles' time and a 7000th of one for each partial row of 512 values
 // (1 token x 64 heads, 2 tiles: 12.3 us whole, 12.9 in two; 3 tiles: 15.8 against
 // 13.5 in three; 32 x 128, 5 tiles: 22.5 against 24.2 in two, 9: 33.2 against 30.0).

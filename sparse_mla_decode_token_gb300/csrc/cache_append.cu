@@ -11,11 +11,13 @@
 // longer ones are read again, from L2), so DRAM sees each row once: 1 KB in,
 // 512 B out a token.  Its floor is that traffic; what it takes beyond is the chain
 // offsets -> rows and page -> scale -> codes of a CTA, which many small CTAs an
-// SM overlap, and the instructions: the maximum is taken over packed BF16
-// magnitudes, two a lane (value by value: 11.3 us against 9.2 below), and eight
-// CTAs fit an SM (64 registers; 80: 9.2 us, ten with spills: 10.3).  Measured on a
-// GB300: 32 thousand tokens of 8 prompts 8.8 us (5.8 TB/s), 131 thousand 32.7 us
-// (6.2 TB/s); 128 requests of one token 3.2 us behind another kernel.
+// SM overlap, and the instructions.  Measured on a GB300, inputs from DRAM (four
+// states in turn): 33.7 thousand tokens of 8 prompts 11.3 us (4.6 TB/s), 132 thousand
+// of 32 33.1 us (6.1 TB/s): the shorter call does not reach the longer one's rate, and
+// why is not known.  One state again and again, its 50 MB in L2: 8.2 us; so were
+// measured: the maximum over packed BF16 magnitudes, two a lane (value by value 11.3 us
+// against 9.2), and eight CTAs an SM (64 registers 8.8 us, 80 9.2, ten with spills
+// 10.3).  128 requests of one token: 3.3 us behind another kernel.
 #include <type_traits>
 
 #include "cache.cuh"

@@ -14,7 +14,9 @@
 // fences before the barriers, and with one CTA counting pages after summing the
 // requests' needs); where tables and pool together pass kClusterEntries, eight
 // SMs are too few and the phases are launches of their own over the whole GPU
-// (1024 requests x 1024 pages in a pool of a million: 71 us in a cluster, 18 so).
+// (resize, entries and pages together 34 thousand: 9.5 us in a cluster, 10.7 so; 67
+// thousand 10.0 and 10.5; 132 thousand 12.3 and 11.3; 263 thousand 16.6 and 11.7; two
+// million: 71 and 18.  Compaction crosses there too: 15.6 and 16.2, 19.9 and 16.4).
 // What bounds both is latency: the counts (4 bytes a page) are read once, and
 // again where pages are handed out; the rest is dependent trips to L2.
 #include "cache.cuh"

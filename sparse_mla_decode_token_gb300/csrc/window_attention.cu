@@ -44,7 +44,7 @@
 // or 2^-14 * 448 against the 2^4 * 16 or more of the one that m was set by.  (With a reference that only rises and a
 // floor of 2^-14 of the largest weight, a first token with 95 % of the weight and
 // small values took 14 % of the output of 2048 rows with it; now a head is off by 0.2 to
-// 0.3 %, the roundings of P and of the output.  It costs 9 to 11 % of the time: the look at
+// 0.3 %, the roundings of P and of the output.  It costs 8 to 12 % of the time: the look at
 // each tile's lightest head, tiles that move m down, a look at 16 codes a thread.)
 //
 // Rows come by TMA as chunks of 32 (16, 8) consecutive rows of one page, 5-D
@@ -64,7 +64,8 @@
 // softmax, the other's products run, and each second product frees its tile by
 // quarters, so that the next rows land behind it.
 //
-// What bounds it: a tile costs a CTA 2.3 us (4400 clocks), of which its tensor
+// What bounds it: a tile costs a CTA 2.5 us (4800 clocks, a fourth of the tiles moving
+// the reference, which the others do not), of which its tensor
 // instructions take 2670 (16 first products of 67 clocks; 32 second ones of 50,
 // not 32: with N = 64 they wait for their A operand out of shared memory).  The
 // rest is the chain second product -> free quarter -> rows -> first product ->
@@ -72,13 +73,15 @@
 // whole, and 7 us a unit for its query, sums and results.  Measured on a GB300:
 // 128 requests of one token, 128 heads, 2052 rows: 99 us, 696 TFLOP/s of the
 // plain products' count; 2049 tokens of four prompts, 128 heads, a window of 512:
-// 620 us, 447 TFLOP/s; two requests of 64 heads and 2 tiles: 13 us.
+// 613 us, 452 TFLOP/s; two requests of 64 heads and 2 tiles: 12.4 us.  Logits so wide
+// that nearly every tile moves the reference (queries twice as long): decode 112 us;
+// codes all under 16, which takes a look at whole rows where it moves: 111 us.
 //
 // Five kinds of warps share an instruction cache that a unit's code overflows, so
 // code that need not be long is not: the products' loops are rolled to four and
-// eight instructions, each look-up stands once (prompts 583 -> 548 us).
+// eight instructions, each look-up stands once (prompts 583 -> 548 us, before the same).
 //
-// Tried and slower (at these sizes): both products issued by one warp (decode
+// Tried and slower (at these sizes, before the reference moved both ways): both products issued by one warp (decode
 // 114 us against 98), warps of their own for the query (prefill 688 against
 // 577), waits that poll (613 against 606), two or four times less headroom in
 // the reference (prefill 552 to 564 against 576, at up to twice the error).
@@ -929,8 +932,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
 // Merges the S normalised fp32 partials of a split pair's heads: weights
 // 2^(LSE_s - LSE), then the sink and bmm2.  The weights first, a split a thread;
 // then no partial's load waits for another's.  Up to four teams of threads share
-// many splits (64 heads over 32768 rows in 128 splits: 31.5 us of both kernels with
-// one team, 21.6 with four; over 262144 rows 63.5 and 51.5).
+// many splits (64 heads over 32768 rows in 128 splits: 34.6 us of both kernels with
+// one team, 24.2 with four; over 262144 rows 72.0 and 60.1).
 constexpr int kMergeThreads = 128;                // of a team; one head: four dims a thread
 constexpr int kMergeTeams = 4;
 

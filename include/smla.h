@@ -144,6 +144,8 @@ typedef enum smla_kernel {
 #define SMLA_DEVERR_TIMEOUT 0x2             /* a bounded on-device wait expired; outputs are invalid */
 #define SMLA_DEVERR_INTERNAL 0x4            /* an internal limit was hit; outputs are invalid */
 #define SMLA_DEVERR_OUT_OF_PAGES 0x8        /* smla_pages_resize: too few free pages; the last entries stay -1 */
+#define SMLA_DEVERR_TOO_MANY_TOKENS 0x20    /* smla_token_slots: a step of more tokens than its outputs hold */
+#define SMLA_DEVERR_BAD_LOGITS 0x40         /* smla_beam_select: NaN or +infinity in a row's logits or scores */
 #define SMLA_DEVERR_PAGE_STATE 0x10         /* page calls: a length, parent, table entry or count that cannot be */
 
 /*
@@ -468,6 +470,17 @@ smla_status smla_cache_append(const smla_append_args* args, void* stream);
  *   (lens[b] == 0), takes its parent's pages, each counted once more; out_lens
  *   receives lens[parents[b]], and lens[b] for the others.  Parents keep their
  *   pages; a parent may have any number of children.
+ * smla_pages_reorder: every request b at once becomes what parents[b] was, as
+ *   beams do after each choice: its table row takes the pages of request
+ *   parents[b] and out_lens[b] its length; parents[b] < 0 drops b's pages
+ *   (length 0).  Any request may be the parent of any number of them, itself
+ *   included; the counts follow, and a page that nobody holds any more is free.
+ *   Behind it, smla_pages_resize gives those that grow pages of their own.
+ * smla_pages_shared_prefix: prefix_lens[g] = the tokens of the leading whole
+ *   pages that all requests of group g, group_starts[g] <= b <
+ *   group_starts[g + 1], with lens[b] > 0 hold in the same columns (the shortest
+ *   one's whole pages at most; 0 for a group without such a request).  Looks at
+ *   block_tables, lens and page_size only; num_pages and ref_counts are not used.
  * smla_pages_compact: the n pages in use move to pages 0 .. n - 1: the k-th
  *   page in use at or past n to the k-th free page before it.  Tables and
  *   counts are renumbered and the pairs (from, to) written to the moves: copy
@@ -490,13 +503,14 @@ typedef struct smla_pages_args {
   int64_t num_pages;            /* 1 .. 2^31 - 1 */
   const int32_t* lens;          /* [rows] tokens before the call */
   const int32_t* new_lens;      /* [rows] resize: tokens after it */
-  const int32_t* parents;       /* [rows] fork: request to share with, or < 0 */
-  int32_t* out_lens;            /* [rows] fork: lengths after it; does not overlap lens */
+  const int32_t* parents;       /* [rows] fork: request to share with, or < 0; reorder: request to become, or < 0 */
+  int32_t* out_lens;            /* [rows] fork, reorder: lengths after it; does not overlap lens */
   int32_t* move_src;            /* [move_capacity] resize, compact */
   int32_t* move_dst;            /* [move_capacity] */
   int32_t* move_count;          /* [1] */
   int64_t move_capacity;
-  void* workspace;              /* resize, compact: >= smla_pages_workspace_size() bytes, 256-byte aligned */
+  void* workspace;              /* resize, compact: >= smla_pages_workspace_size() bytes, 256-byte aligned;
+                                   reorder: >= smla_pages_reorder_workspace_size() */
   size_t workspace_bytes;
   int32_t* error_word;
 } smla_pages_args;
@@ -506,6 +520,11 @@ smla_status smla_pages_workspace_size(const smla_pages_args* args, size_t* bytes
 smla_status smla_pages_resize(const smla_pages_args* args, void* stream);
 smla_status smla_pages_fork(const smla_pages_args* args, void* stream);
 smla_status smla_pages_compact(const smla_pages_args* args, void* stream);
+/* Workspace bytes of smla_pages_reorder for rows and max_pages. */
+smla_status smla_pages_reorder_workspace_size(const smla_pages_args* args, size_t* bytes);
+smla_status smla_pages_reorder(const smla_pages_args* args, void* stream);
+smla_status smla_pages_shared_prefix(const smla_pages_args* args, const int32_t* group_starts, int32_t num_groups,
+                                     int32_t* prefix_lens, void* stream);
 
 /* A page-indexed array: page p is the page_bytes bytes at base + p * page_stride. */
 typedef struct smla_pool {
@@ -518,6 +537,126 @@ typedef struct smla_pool {
 smla_status smla_pages_copy(const smla_pool* pools, int32_t num_pools, int64_t num_pages, const int32_t* move_src,
                             const int32_t* move_dst, const int32_t* move_count, int64_t move_capacity,
                             int32_t* error_word, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * What a step of a server needs beside the attention.  The conventions are
+ * those of the paged latent cache.
+ * ---------------------------------------------------------------------------
+ *
+ * Token slots: a step takes request b from lens[b] to new_lens[b] tokens, so it
+ * has q_b = max(0, new_lens[b] - max(0, lens[b])) new ones.
+ *
+ *   cum_seq_lens_q[b] = q_0 + .. + q_(b-1)
+ *   for the i-th new token t = cum_seq_lens_q[b] + i of request b:
+ *     requests[t] = b, positions[t] = max(0, lens[b]) + i,
+ *     slots[t] = block_tables[b][positions[t] / page_size] * page_size + positions[t] % page_size
+ *
+ * and -1 in all three for t from the step's last token to max_tokens.  A
+ * position past the table, or one whose entry is negative, has slot -1
+ * (SMLA_DEVERR_INDEX_OUT_OF_RANGE).  More new tokens than max_tokens set
+ * SMLA_DEVERR_TOO_MANY_TOKENS; the offsets are then still those of the whole
+ * step (2^31 - 1 at most).
+ */
+typedef struct smla_token_slots_args {
+  const int32_t* lens;          /* [batch] tokens before the step */
+  const int32_t* new_lens;      /* [batch] tokens after it */
+  int32_t batch;                /* requests >= 0 */
+  int32_t max_tokens;           /* >= 0 */
+  const int32_t* block_tables;  /* [batch, max_pages], or NULL without slots */
+  int64_t block_table_stride;   /* row stride in elements [max_pages] */
+  int32_t max_pages;            /* >= 1; max_pages * page_size < 2^31 */
+  int32_t page_size;            /* >= 1 */
+  int32_t* cum_seq_lens_q;      /* [batch + 1] */
+  int32_t* requests;            /* [max_tokens], or NULL */
+  int32_t* positions;           /* [max_tokens], or NULL */
+  int64_t* slots;               /* [max_tokens], 8-byte aligned, or NULL; needs block_tables */
+  int32_t* error_word;
+} smla_token_slots_args;
+
+smla_status smla_token_slots(const smla_token_slots_args* args, void* stream);
+
+/*
+ * Sparse slots: the index table of smla_decode from page tables.  Token t, at
+ * position pos of request b (as in the cache's calls), gets
+ *
+ *   column j < 128:  the row of position max(0, pos - 127) + j through swa_tables[b], -1 past pos;
+ *   column 128 + k:  the row of compressed position c = selected[t][k] (k without `selected`)
+ *                    through comp_tables[b], -1 unless 0 <= c < (pos + 1) / compress_ratio;
+ *   topk_lens[t] = 128 + (the last k that is not -1) + 1, or 128 if there is none,
+ *
+ * where the row of position j is table[j / page_size] * page_size + j % page_size.
+ * A token of no request (a padded batch) and one with pos < 0 get -1 everywhere
+ * and topk_lens 0.  A position past its table, an entry that is negative or a
+ * row that is no 32-bit number is -1 and sets SMLA_DEVERR_INDEX_OUT_OF_RANGE
+ * (as smla_decode does for rows past its pools).
+ */
+typedef struct smla_sparse_slots_args {
+  int32_t sum_q, batch;             /* tokens (0 = nothing to do), requests >= 1 */
+  const int32_t* seq_lens;          /* [batch] tokens, the step's included */
+  const int32_t* cum_seq_lens_q;    /* [batch + 1], or NULL = uniform sum_q / batch */
+  const int32_t* swa_tables;        /* [batch, swa_max_pages] */
+  int64_t swa_table_stride;         /* [swa_max_pages] */
+  int32_t swa_max_pages, swa_page_size;
+  const int32_t* comp_tables;       /* [batch, comp_max_pages]; not needed for num_selected = 0 */
+  int64_t comp_table_stride;        /* [comp_max_pages] */
+  int32_t comp_max_pages, comp_page_size;
+  int32_t compress_ratio;           /* tokens of a compressed row >= 1 */
+  int32_t num_selected;             /* compressed columns >= 0 */
+  const int32_t* selected;          /* [sum_q, num_selected] compressed positions, or NULL = the first ones */
+  int64_t selected_stride;          /* [num_selected] */
+  int32_t* sparse_indices;          /* [sum_q, 128 + num_selected] */
+  int64_t indices_row_stride;       /* [128 + num_selected] */
+  int32_t* topk_lens;               /* [sum_q] */
+  int32_t* error_word;
+} smla_sparse_slots_args;
+
+smla_status smla_sparse_slots(const smla_sparse_slots_args* args, void* stream);
+
+/*
+ * Beam selection: request r has `beams` rows of logits, r * beams + i, with
+ * scores s_i; token v continues beam i with
+ *
+ *   s_i + x[i][v] - log sum_w e^{x[i][w]}
+ *
+ * and a finished beam has one continuation, end_token, with its own score.  The
+ * num_out best, in order, go to out_scores, out_parents (the row r * beams + i)
+ * and out_tokens; among equal ones the lower (i, v) is first.  Scores that agree
+ * to 2^-45 of their logit or of s_i - log sum, whichever is larger, may count as
+ * equal.  Continuations of -infinity are none; places that none is left for
+ * hold -infinity, -1 and -1.  A beam with a score of -infinity (an empty place)
+ * has no continuation, and its logits are not read; nor are a finished beam's.
+ * A NaN or +infinity among the logits or for the score leaves the beam without
+ * continuations and sets SMLA_DEVERR_BAD_LOGITS.  Deterministic.
+ */
+#define SMLA_LOGITS_BF16 0
+#define SMLA_LOGITS_FP16 1
+#define SMLA_LOGITS_FP32 2
+#define SMLA_MAX_BEAMS 64
+#define SMLA_MAX_BEAM_OUT 64
+
+typedef struct smla_beam_args {
+  int32_t batch;                /* requests (0 = nothing to do) */
+  int32_t beams;                /* rows of a request, 1 .. SMLA_MAX_BEAMS */
+  int32_t vocab;                /* >= 1 */
+  int32_t num_out;              /* 1 .. SMLA_MAX_BEAM_OUT */
+  int32_t dtype;                /* SMLA_LOGITS_* */
+  const void* logits;           /* [batch * beams, vocab], aligned to its elements */
+  int64_t logits_stride;        /* elements between rows [vocab], at least vocab */
+  const float* scores;          /* [batch * beams] */
+  const uint8_t* finished;      /* [batch * beams], not 0 = finished, or NULL */
+  int32_t end_token;            /* token of a finished beam */
+  float* out_scores;            /* [batch, num_out] */
+  int32_t* out_parents;         /* [batch, num_out] */
+  int32_t* out_tokens;          /* [batch, num_out] */
+  void* workspace;              /* >= smla_beam_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  int32_t* error_word;
+} smla_beam_args;
+
+/* Workspace bytes of smla_beam_select for these shapes and dtype on `device` (pointers are not looked at). */
+smla_status smla_beam_workspace_size(const smla_beam_args* args, int device, size_t* bytes);
+smla_status smla_beam_select(const smla_beam_args* args, void* stream);
 
 /* Static text for a status code. */
 const char* smla_status_string(smla_status status);

@@ -37,6 +37,8 @@ DEVERR_TIMEOUT = 0x2
 DEVERR_INTERNAL = 0x4
 DEVERR_OUT_OF_PAGES = 0x8
 DEVERR_PAGE_STATE = 0x10
+DEVERR_TOO_MANY_TOKENS = 0x20
+DEVERR_BAD_LOGITS = 0x40
 
 _c_void_p = ctypes.c_void_p
 
@@ -107,6 +109,14 @@ EXPORTS = {
     "smla_pages_compact": (ctypes.c_int, [_c_void_p, _c_void_p]),
     "smla_pages_copy": (ctypes.c_int, [_c_void_p, ctypes.c_int32, ctypes.c_int64, _c_void_p, _c_void_p, _c_void_p,
                                        ctypes.c_int64, _c_void_p, _c_void_p]),
+    "smla_pages_reorder_workspace_size": (ctypes.c_int, [_c_void_p, ctypes.POINTER(ctypes.c_size_t)]),
+    "smla_pages_reorder": (ctypes.c_int, [_c_void_p, _c_void_p]),
+    "smla_pages_shared_prefix": (ctypes.c_int, [_c_void_p, _c_void_p, ctypes.c_int32, _c_void_p, _c_void_p]),
+    # a step's calls beside the attention (argument structs in slots.py and search.py)
+    "smla_token_slots": (ctypes.c_int, [_c_void_p, _c_void_p]),
+    "smla_sparse_slots": (ctypes.c_int, [_c_void_p, _c_void_p]),
+    "smla_beam_workspace_size": (ctypes.c_int, [_c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    "smla_beam_select": (ctypes.c_int, [_c_void_p, _c_void_p]),
 }
 
 

@@ -390,6 +390,59 @@ def pages_fork(block_tables: torch.Tensor, ref_counts: torch.Tensor, lens: torch
     _call(_b.lib().smla_pages_fork, index, stream, ctypes.byref(a))
 
 
+def reorder_workspace_size(block_tables: torch.Tensor) -> int:
+    """Workspace bytes of ``pages_reorder`` (no device memory is read)."""
+    a = SmlaPagesArgs()
+    a.rows, a.max_pages, a.page_size = block_tables.shape[0], block_tables.shape[1], 1
+    n = ctypes.c_size_t(0)
+    _check(_b.lib().smla_pages_reorder_workspace_size(ctypes.byref(a), ctypes.byref(n)))
+    return int(n.value)
+
+
+def pages_reorder(block_tables: torch.Tensor, ref_counts: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor,
+                  out_lens: torch.Tensor, workspace_buffer: torch.Tensor, *, page_size: int,
+                  error_word: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> None:
+    """Every request at once becomes what ``parents[b]`` was (pages and length,
+    to ``out_lens``); ``parents[b] < 0`` ends it.  Pages follow by their counts
+    alone; behind it ``pages_resize`` gives those that grow pages of their own."""
+    status = (_extension or extension()).pages_reorder(block_tables, ref_counts, lens, parents, out_lens, workspace_buffer,
+                                                       page_size, error_word, stream)
+    if status is not None:
+        return _check(status) if status else None
+    if not workspace_buffer.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor")
+    a = _pages_args(block_tables, ref_counts, lens, page_size, error_word, parents=parents, out_lens=out_lens,
+                    workspace=workspace_buffer)
+    index = block_tables.get_device()
+    _on(index, (block_tables, ref_counts, lens, parents, out_lens, workspace_buffer, error_word),
+        ("block_tables", "ref_counts", "lens", "parents", "out_lens", "workspace", "error_word"))
+    _call(_b.lib().smla_pages_reorder, index, stream, ctypes.byref(a))
+
+
+def pages_shared_prefix(block_tables: torch.Tensor, lens: torch.Tensor, group_starts: torch.Tensor, prefix_lens: torch.Tensor,
+                        *, page_size: int, error_word: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> None:
+    """``prefix_lens[g]``: tokens of the leading whole pages that all requests of
+    group ``g`` with tokens share, ``group_starts[g] <= b < group_starts[g + 1]``."""
+    status = (_extension or extension()).pages_shared_prefix(block_tables, lens, group_starts, prefix_lens, page_size,
+                                                             error_word, stream)
+    if status is not None:
+        return _check(status) if status else None
+    _table("block_tables", block_tables)
+    _words("lens", lens, block_tables.shape[0])
+    _words("prefix_lens", prefix_lens, 0)
+    _words("group_starts", group_starts, prefix_lens.numel() + 1)
+    _words("error_word", error_word, 1)
+    a = SmlaPagesArgs()
+    a.rows, a.max_pages, a.page_size = block_tables.shape[0], block_tables.shape[1], _int32("page_size", page_size)
+    a.block_tables, a.lens, a.error_word = block_tables.data_ptr(), lens.data_ptr(), _ptr(error_word)
+    a.block_table_stride = block_tables.stride(0) if a.rows > 1 else a.max_pages
+    index = block_tables.get_device()
+    _on(index, (block_tables, lens, group_starts, prefix_lens, error_word),
+        ("block_tables", "lens", "group_starts", "prefix_lens", "error_word"))
+    _call(_b.lib().smla_pages_shared_prefix, index, stream, ctypes.byref(a), group_starts.data_ptr(), prefix_lens.numel(),
+          prefix_lens.data_ptr())
+
+
 def pages_compact(block_tables: torch.Tensor, ref_counts: torch.Tensor, lens: torch.Tensor,
                   workspace_buffer: torch.Tensor, *, page_size: int, moves,
                   error_word: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> None:

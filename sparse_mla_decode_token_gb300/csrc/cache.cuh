@@ -137,6 +137,9 @@ inline int64_t pages_workspace_words(int64_t rows, int64_t num_pages) {
 
 cudaError_t launch_pages_resize(const PagesParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_reorder(const PagesParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_pages_shared_prefix(const PagesParams& p, const int32_t* group_starts, int num_groups, int32_t* prefix_lens,
+                                       cudaStream_t stream);
 cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t stream);
 
 constexpr int kCopyPools = 64;        // pools of one copy launch (kernel parameters)

@@ -2,77 +2,17 @@
 // the window attention, launches.  Shapes and pointers are checked before any
 // CUDA call; no device memory is read, nothing is allocated, nothing
 // synchronises.
-#include <stdarg.h>
-#include <stdio.h>
 #include <string.h>
 
 #include <algorithm>
-#include <atomic>
 
+#include "api_checks.h"
 #include "cache.cuh"
-#include "kernels.h"
 
 namespace smla {
 namespace {
 
 static_assert(SMLA_MAX_SPLITS <= kMaxWindowSplits, "forced splits");
-
-smla_status fail(smla_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-smla_status fail(smla_status st, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  return record_error(st, buf);
-}
-
-#define SMLA_TRY(expr)                  \
-  do {                                  \
-    smla_status st_ = (expr);           \
-    if (st_ != SMLA_OK) return st_;     \
-  } while (0)
-
-bool aligned(const void* ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-smla_status need_words(const char* name, const void* ptr, bool required) {
-  if (ptr == nullptr) return required ? fail(SMLA_ERR_INVALID_ARG, "%s is required", name) : SMLA_OK;
-  if (!aligned(ptr, 4)) return fail(SMLA_ERR_INVALID_ARG, "%s must be 4-byte aligned", name);
-  return SMLA_OK;
-}
-
-smla_status need_rows(const char* name, const void* ptr) {
-  if (ptr == nullptr) return fail(SMLA_ERR_INVALID_ARG, "%s is required", name);
-  if (!aligned(ptr, 16)) return fail(SMLA_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
-  return SMLA_OK;
-}
-
-std::atomic<int> g_sms[64];   // per device; 0 = not queried yet
-
-smla_status device_sms(int device, int* out) {
-  if (device < 0 || device >= 64) return fail(SMLA_ERR_INVALID_ARG, "device %d out of range", device);
-  int n = g_sms[device].load(std::memory_order_relaxed);
-  if (n == 0) {
-    cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device);
-    if (e != cudaSuccess) return fail(SMLA_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(e));
-    g_sms[device].store(n, std::memory_order_relaxed);
-  }
-  *out = n;
-  return SMLA_OK;
-}
-
-smla_status current_sms(int* out) {
-  int device = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return fail(SMLA_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
-  return device_sms(device, out);
-}
-
-smla_status launched(const char* what, cudaError_t e) {
-  if (e != cudaSuccess) return fail(SMLA_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
-  return SMLA_OK;
-}
 
 // ------------------------------------------------------------------ cache
 
@@ -212,7 +152,7 @@ WindowPlan window_plan(const smla_window_args* a, int sms) {
 
 // ------------------------------------------------------------------ pages
 
-smla_status check_pages(const smla_pages_args* a) {
+smla_status check_tables(const smla_pages_args* a) {
   if (a == nullptr) return fail(SMLA_ERR_INVALID_ARG, "args is NULL");
   if (a->rows < 0) return fail(SMLA_ERR_INVALID_ARG, "rows %d is negative", a->rows);
   if (a->max_pages < 1) return fail(SMLA_ERR_INVALID_ARG, "max_pages %d < 1", a->max_pages);
@@ -221,11 +161,16 @@ smla_status check_pages(const smla_pages_args* a) {
     return fail(SMLA_ERR_INVALID_ARG, "max_pages %d: a request holds 1 .. 2^31 - 1 tokens", a->max_pages);
   if ((int64_t)a->rows * ((int64_t)a->max_pages + 1) > 0x3fffffff)
     return fail(SMLA_ERR_UNSUPPORTED, "%d rows of %d pages: the tables hold under 2^30 entries", a->rows, a->max_pages);
-  if (a->num_pages < 1 || a->num_pages > 0x7fffffff)
-    return fail(SMLA_ERR_INVALID_ARG, "num_pages %lld is outside 1 .. 2^31 - 1", (long long)a->num_pages);
   if (a->block_table_stride != 0 && a->block_table_stride < a->max_pages)
     return fail(SMLA_ERR_INVALID_ARG, "block_table_stride %lld < max_pages %d", (long long)a->block_table_stride,
                 a->max_pages);
+  return SMLA_OK;
+}
+
+smla_status check_pages(const smla_pages_args* a) {
+  SMLA_TRY(check_tables(a));
+  if (a->num_pages < 1 || a->num_pages > 0x7fffffff)
+    return fail(SMLA_ERR_INVALID_ARG, "num_pages %lld is outside 1 .. 2^31 - 1", (long long)a->num_pages);
   return SMLA_OK;
 }
 
@@ -240,6 +185,19 @@ smla_status check_page_pointers(const smla_pages_args* a) {
   return need_words("error_word", a->error_word, false);
 }
 
+smla_status check_parents(const smla_pages_args* a) {
+  SMLA_TRY(need_words("parents", a->parents, true));
+  SMLA_TRY(need_words("out_lens", a->out_lens, true));
+  const uintptr_t out = reinterpret_cast<uintptr_t>(a->out_lens), in = reinterpret_cast<uintptr_t>(a->lens);
+  if ((out > in ? out - in : in - out) < (uintptr_t)a->rows * sizeof(int32_t))
+    return fail(SMLA_ERR_INVALID_ARG, "out_lens must not be lens or overlap it");
+  return SMLA_OK;
+}
+
+size_t reorder_workspace(const smla_pages_args* a) {
+  return align_up((size_t)a->rows * a->max_pages * sizeof(int32_t), 256);
+}
+
 smla_status check_moves(const smla_pages_args* a, int64_t need) {
   if (a->move_capacity < need || a->move_capacity > 0x7fffffff)
     return fail(SMLA_ERR_INVALID_ARG, "move_capacity %lld: this call may write %lld moves", (long long)a->move_capacity,
@@ -249,12 +207,7 @@ smla_status check_moves(const smla_pages_args* a, int64_t need) {
     SMLA_TRY(need_words("move_dst", a->move_dst, true));
   }
   SMLA_TRY(need_words("move_count", a->move_count, true));
-  const size_t bytes = pages_workspace(a);
-  if (a->workspace == nullptr || a->workspace_bytes < bytes)
-    return fail(SMLA_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes given, %zu needed",
-                a->workspace ? a->workspace_bytes : (size_t)0, bytes);
-  if (!aligned(a->workspace, 256)) return fail(SMLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  return SMLA_OK;
+  return need_workspace(a->workspace, a->workspace_bytes, pages_workspace(a));
 }
 
 // A call without requests: what a copy of its moves would find.
@@ -319,12 +272,7 @@ smla_status smla_window_attention(const smla_window_args* a, void* stream) {
   const WindowPlan plan = window_plan(a, sms);
   if (plan.units > 0x7fffffff || (int64_t)a->sum_q * head_groups(a) > 0x7fffffff / kWindowHeads)
     return fail(SMLA_ERR_UNSUPPORTED, "%lld units are too many", (long long)plan.units);
-  if (plan.bytes > 0) {
-    if (a->workspace == nullptr || a->workspace_bytes < plan.bytes)
-      return fail(SMLA_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes given, %zu needed",
-                  a->workspace ? a->workspace_bytes : (size_t)0, plan.bytes);
-    if (!aligned(a->workspace, 256)) return fail(SMLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  }
+  SMLA_TRY(need_workspace(a->workspace, a->workspace_bytes, plan.bytes));
   WindowParams p;
   memset(&p, 0, sizeof(p));
   p.c = view(a->cache, a->sum_q);
@@ -393,12 +341,42 @@ smla_status smla_pages_fork(const smla_pages_args* a, void* stream) {
   SMLA_TRY(check_pages(a));
   if (a->rows == 0) return SMLA_OK;
   SMLA_TRY(check_page_pointers(a));
-  SMLA_TRY(need_words("parents", a->parents, true));
-  SMLA_TRY(need_words("out_lens", a->out_lens, true));
-  const uintptr_t out = reinterpret_cast<uintptr_t>(a->out_lens), in = reinterpret_cast<uintptr_t>(a->lens);
-  if ((out > in ? out - in : in - out) < (uintptr_t)a->rows * sizeof(int32_t))
-    return fail(SMLA_ERR_INVALID_ARG, "out_lens must not be lens or overlap it");
+  SMLA_TRY(check_parents(a));
   return launched("pages fork", launch_pages_fork(pages_params(a), static_cast<cudaStream_t>(stream)));
+}
+
+smla_status smla_pages_reorder_workspace_size(const smla_pages_args* args, size_t* bytes) {
+  if (bytes == nullptr) return fail(SMLA_ERR_INVALID_ARG, "bytes is NULL");
+  SMLA_TRY(check_tables(args));
+  *bytes = reorder_workspace(args);
+  return SMLA_OK;
+}
+
+smla_status smla_pages_reorder(const smla_pages_args* a, void* stream) {
+  SMLA_TRY(check_pages(a));
+  if (a->rows == 0) return SMLA_OK;
+  SMLA_TRY(check_page_pointers(a));
+  SMLA_TRY(check_parents(a));
+  SMLA_TRY(need_workspace(a->workspace, a->workspace_bytes, reorder_workspace(a)));
+  int sms = 0;
+  SMLA_TRY(current_sms(&sms));
+  return launched("pages reorder", launch_pages_reorder(pages_params(a), sms, static_cast<cudaStream_t>(stream)));
+}
+
+smla_status smla_pages_shared_prefix(const smla_pages_args* a, const int32_t* group_starts, int32_t num_groups,
+                                     int32_t* prefix_lens, void* stream) {
+  SMLA_TRY(check_tables(a));
+  if (num_groups < 0) return fail(SMLA_ERR_INVALID_ARG, "num_groups %d is negative", num_groups);
+  if (num_groups == 0) return SMLA_OK;
+  SMLA_TRY(need_words("group_starts", group_starts, true));
+  SMLA_TRY(need_words("prefix_lens", prefix_lens, true));
+  SMLA_TRY(need_words("error_word", a->error_word, false));
+  if (a->rows > 0) {
+    SMLA_TRY(need_words("block_tables", a->block_tables, true));
+    SMLA_TRY(need_words("lens", a->lens, true));
+  }
+  return launched("pages shared prefix", launch_pages_shared_prefix(pages_params(a), group_starts, num_groups, prefix_lens,
+                                                                    static_cast<cudaStream_t>(stream)));
 }
 
 smla_status smla_pages_compact(const smla_pages_args* a, void* stream) {

@@ -449,6 +449,178 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(const PagesParams p) {
   if (lane == 0) p.out_lens[b] = len;
 }
 
+// --------------------------------------------------------------- reorder
+// Every row takes its parent's entries at once.  A beam keeps most of what it
+// has (its prompt's pages are its parent's, too), so only entries that differ
+// are counted and written.
+//   1. the parents' entries into the workspace, the pages that a row did not
+//      hold at that column counted once more;
+//   2. rows overwritten from there, the pages given up counted once less (after
+//      all of 1, so that no page that stays in use passes through 0).
+// Both phases compare the same two entries: a row is changed by the thread that
+// compared it only.
+constexpr int kReorderPer = 4;                        // columns a lane takes at a time
+
+// Row b's parent, b itself for one that stays (one that is not a row is flagged), -1 for one that ends.
+__device__ __forceinline__ int parent_of(const PagesParams& p, int b, bool* bad) {
+  const int parent = fetch(p.parents + b);
+  if (parent >= p.rows) {
+    *bad = true;
+    return b;
+  }
+  return max(parent, -1);
+}
+
+// Columns of row b's parent and of itself.
+struct Reorder {
+  int parent, theirs, mine;
+};
+__device__ __forceinline__ Reorder reorder_row(const PagesParams& p, int b) {
+  bool bad = false;
+  Reorder r;
+  r.parent = parent_of(p, b, &bad);
+  r.mine = page_columns(p, fetch(p.lens + b), &bad);
+  r.theirs = r.parent >= 0 ? page_columns(p, fetch(p.lens + r.parent), &bad) : 0;
+  if (bad) flag(p.err, SMLA_DEVERR_PAGE_STATE);
+  return r;
+}
+
+__device__ __forceinline__ void reorder_save(const PagesParams& p, const Team& w) {
+  pieces(p, w,
+         [&](int b) {
+           const Reorder r = reorder_row(p, b);
+           return make_int2(0, r.parent == b ? 0 : r.theirs);
+         },
+         [&](int b, int from, int to) {
+           const Reorder r = reorder_row(p, b);
+           const int32_t* theirs = p.bt + (int64_t)r.parent * p.bt_stride;
+           const int32_t* mine = p.bt + (int64_t)b * p.bt_stride;
+           int now[kReorderPer], old[kReorderPer];
+#pragma unroll
+           for (int k = 0; k < kReorderPer; ++k) {
+             const int c = from + k * 32 + w.lane;
+             now[k] = c < to ? __ldcg(theirs + c) : 0;
+             old[k] = c < to && c < r.mine ? __ldcg(mine + c) : -1;
+           }
+#pragma unroll
+           for (int k = 0; k < kReorderPer; ++k) {
+             const int c = from + k * 32 + w.lane;
+             if (c >= to) continue;
+             p.ws[(int64_t)b * p.max_pages + c] = now[k];
+             if (c < r.mine && old[k] == now[k]) continue;
+             if (in_pool(p, now[k])) atomicAdd(p.refs + now[k], 1);
+             else flag(p.err, SMLA_DEVERR_PAGE_STATE);
+           }
+         });
+}
+
+__device__ __forceinline__ void reorder_write(const PagesParams& p, const Team& w) {
+  pieces(p, w,
+         [&](int b) {
+           const Reorder r = reorder_row(p, b);
+           return make_int2(0, r.parent == b ? 0 : max(r.mine, r.theirs));
+         },
+         [&](int b, int from, int to) {
+           const Reorder r = reorder_row(p, b);
+           int32_t* mine = p.bt + (int64_t)b * p.bt_stride;
+           int now[kReorderPer], old[kReorderPer];
+#pragma unroll
+           for (int k = 0; k < kReorderPer; ++k) {
+             const int c = from + k * 32 + w.lane;
+             now[k] = c < to && c < r.theirs ? __ldcg(p.ws + (int64_t)b * p.max_pages + c) : -1;
+             old[k] = c < to && c < r.mine ? __ldcg(mine + c) : -1;
+           }
+#pragma unroll
+           for (int k = 0; k < kReorderPer; ++k) {
+             const int c = from + k * 32 + w.lane;
+             if (c >= to || (c < r.mine && c < r.theirs && old[k] == now[k])) continue;
+             if (c < r.mine) drop_ref(p, old[k]);
+             mine[c] = now[k];
+           }
+         });
+  for (int b = w.cta * kPlanThreads + (int)threadIdx.x; b < p.rows; b += w.ctas * kPlanThreads) {
+    bool bad = false;
+    const int parent = parent_of(p, b, &bad);
+    p.out_lens[b] = parent >= 0 ? fetch(p.lens + parent) : 0;
+  }
+}
+
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
+pages_reorder_kernel(const PagesParams p) {
+  const Team w = team((int)ptx::cluster_rank(), kClusterCtas);
+  await_prior_kernel();
+  admit_next_kernel();
+  reorder_save(p, w);
+  ptx::cluster_sync();
+  reorder_write(p, w);
+}
+
+template <int kPhase>
+__global__ void __launch_bounds__(kPlanThreads, 1) pages_reorder_phase_kernel(const PagesParams p) {
+  const Team w = team(blockIdx.x, gridDim.x);
+  await_prior_kernel();
+  admit_next_kernel();
+  if constexpr (kPhase == 0) reorder_save(p, w);
+  else reorder_write(p, w);
+}
+
+// --------------------------------------------------------- shared prefix
+// Group g's rows with tokens hold `columns` whole pages each at least; the
+// first column where one of them differs from the first ends the prefix.
+// A CTA a group, its warps a row each, 128 columns at a time from the front, so
+// that what lies behind an early difference is hardly read.
+constexpr int kPrefixThreads = 512;
+__global__ void __launch_bounds__(kPrefixThreads)
+pages_shared_prefix_kernel(const PagesParams p, const int32_t* group_starts, int32_t* prefix_lens) {
+  __shared__ int s_columns, s_first;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    s_columns = p.max_pages;
+    s_first = p.rows;
+  }
+  __syncthreads();
+  await_prior_kernel();
+  admit_next_kernel();
+  const int lo = min(max(fetch(group_starts + blockIdx.x), 0), p.rows);
+  const int hi = min(fetch(group_starts + blockIdx.x + 1), p.rows);
+  for (int b = lo + (int)threadIdx.x; b < hi; b += kPrefixThreads) {
+    const int len = fetch(p.lens + b), n = clamped_len(p, len);
+    if (n != len) flag(p.err, SMLA_DEVERR_PAGE_STATE);
+    if (n > 0) {
+      atomicMin(&s_columns, n / p.page_size);
+      atomicMin(&s_first, b);
+    }
+  }
+  __syncthreads();
+  const int first = s_first, columns = s_columns;
+  if (first < p.rows) {
+    const int32_t* lead = p.bt + (int64_t)first * p.bt_stride;
+    for (int b = first + warp; b < hi; b += kPrefixThreads / 32) {
+      if (clamped_len(p, fetch(p.lens + b)) == 0) continue;
+      const int32_t* row = p.bt + (int64_t)b * p.bt_stride;
+      for (int c0 = 0; c0 < columns; c0 += 128) {
+        if (c0 >= __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_columns), 0)) break;
+        int miss = columns;
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+          const int c = c0 + k * 32 + lane;
+          if (c < columns) {
+            const int page = __ldcg(lead + c);
+            if (page < 0 || __ldcg(row + c) != page) miss = c;
+          }
+        }
+        miss = __reduce_min_sync(0xffffffffu, miss);
+        if (miss < columns) {
+          if (lane == 0) atomicMin(&s_columns, miss);
+          break;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) prefix_lens[blockIdx.x] = first < p.rows ? s_columns * p.page_size : 0;
+}
+
 // --------------------------------------------------------------- compact
 // ws: [0] pages in use n, [1] pages in use before page n; num_pages words at
 // kPagesHeader: the move of each page in use at or past n; then the chunks' counts.
@@ -643,6 +815,21 @@ cudaError_t launch_pages_resize(const PagesParams& p, int sms, cudaStream_t stre
 
 cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream) {
   return launch_overlapped(pages_fork_kernel, dim3((unsigned)((p.rows + 7) / 8)), 256, 0, stream, p);
+}
+
+cudaError_t launch_pages_reorder(const PagesParams& p, int sms, cudaStream_t stream) {
+  if ((int64_t)p.rows * p.max_pages <= kClusterEntries)
+    return launch_overlapped(pages_reorder_kernel, dim3(kClusterCtas), kPlanThreads, 0, stream, p);
+  const dim3 tables(phase_ctas((int64_t)p.rows * ((p.max_pages + 127) / 128), sms));
+  cudaError_t e = launch_overlapped(pages_reorder_phase_kernel<0>, tables, kPlanThreads, 0, stream, p);
+  if (e == cudaSuccess) e = launch_overlapped(pages_reorder_phase_kernel<1>, tables, kPlanThreads, 0, stream, p);
+  return e;
+}
+
+cudaError_t launch_pages_shared_prefix(const PagesParams& p, const int32_t* group_starts, int num_groups, int32_t* prefix_lens,
+                                       cudaStream_t stream) {
+  return launch_overlapped(pages_shared_prefix_kernel, dim3((unsigned)num_groups), kPrefixThreads, 0, stream, p, group_starts,
+                           prefix_lens);
 }
 
 cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t stream) {

@@ -215,15 +215,19 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+int32_t* table(Call& call, PyObject* o, int32_t* rows, int32_t* max_pages, int64_t* stride) {
+  const at::Tensor& t = call.tensor(o);
+  need(t.scalar_type() == c10::kInt && t.dim() == 2 && t.size(0) > 0 && t.size(1) > 0 && t.stride(1) == 1 &&
+       t.stride(0) >= t.size(1));
+  *rows = int32(t.size(0));
+  *max_pages = int32(t.size(1));
+  *stride = *rows > 1 ? t.stride(0) : *max_pages;
+  return static_cast<int32_t*>(t.data_ptr());
+}
+
 smla_pages_args pages(Call& call, PyObject* tables_o, PyObject* refs, PyObject* lens, PyObject* page_size, PyObject* error) {
   smla_pages_args p = {};
-  const at::Tensor& tables = call.tensor(tables_o);
-  need(tables.scalar_type() == c10::kInt && tables.dim() == 2 && tables.size(0) > 0 && tables.size(1) > 0 &&
-       tables.stride(1) == 1 && tables.stride(0) >= tables.size(1));
-  p.block_tables = static_cast<int32_t*>(tables.data_ptr());
-  p.rows = int32(tables.size(0));
-  p.max_pages = int32(tables.size(1));
-  p.block_table_stride = p.rows > 1 ? tables.stride(0) : p.max_pages;
+  p.block_tables = table(call, tables_o, &p.rows, &p.max_pages, &p.block_table_stride);
   p.page_size = int32(page_size);
   p.ref_counts = static_cast<int32_t*>(call.words(refs, 1));
   p.num_pages = THPVariable_Unpack(refs).numel();
@@ -262,6 +266,36 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.out_lens = static_cast<int32_t*>(call.words(a[4], p.rows));
     void* const stream = call.stream(a[7]);
     return PyLong_FromLong(unlocked([&] { return smla_pages_fork(&p, stream); }));
+  });
+}
+
+// (block_tables, ref_counts, lens, parents, out_lens, workspace, page_size, error_word, stream) -> status or None
+PyObject* pages_reorder(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    Call call;
+    smla_pages_args p = pages(call, a[0], a[1], a[2], a[6], a[7]);
+    p.parents = static_cast<const int32_t*>(call.words(a[3], p.rows));
+    p.out_lens = static_cast<int32_t*>(call.words(a[4], p.rows));
+    p.workspace = call.bytes(a[5], &p.workspace_bytes);
+    void* const stream = call.stream(a[8]);
+    return PyLong_FromLong(unlocked([&] { return smla_pages_reorder(&p, stream); }));
+  });
+}
+
+// (block_tables, lens, group_starts, prefix_lens, page_size, error_word, stream) -> status or None
+PyObject* pages_shared_prefix(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 7, [&]() -> PyObject* {
+    Call call;
+    smla_pages_args p = {};
+    p.block_tables = table(call, a[0], &p.rows, &p.max_pages, &p.block_table_stride);
+    p.lens = static_cast<const int32_t*>(call.words(a[1], p.rows));
+    int32_t* const prefix = static_cast<int32_t*>(call.words(a[3], 1));
+    const int32_t groups = int32(THPVariable_Unpack(a[3]).numel());
+    const int32_t* const starts = static_cast<const int32_t*>(call.words(a[2], groups + 1));
+    p.page_size = int32(a[4]);
+    p.error_word = static_cast<int32_t*>(call.words(a[5], 1, true));
+    void* const stream = call.stream(a[6]);
+    return PyLong_FromLong(unlocked([&] { return smla_pages_shared_prefix(&p, starts, groups, prefix, stream); }));
   });
 }
 
@@ -313,6 +347,183 @@ PyObject* pages_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A tensor or a new one of this type and these sizes; its memory.
+struct Output {
+  at::Tensor fresh;
+  PyObject* given = nullptr;
+  void* data = nullptr;
+
+  void set(Call& call, PyObject* o, c10::ScalarType type, at::IntArrayRef sizes, int64_t entries, const at::Tensor& like) {
+    if (o != nullptr) {
+      data = call.array(o, type, entries, false);
+      given = o;
+    } else {
+      fresh = at::empty(sizes, like.options().dtype(type));
+      data = fresh.data_ptr();
+    }
+  }
+  PyObject* wrap() const { return fresh.defined() ? THPVariable_Wrap(fresh) : Py_NewRef(given != nullptr ? given : Py_None); }
+};
+
+PyObject* tuple_of(const Output* outputs, Py_ssize_t n) {
+  PyObject* all = PyTuple_New(n);
+  for (Py_ssize_t i = 0; all != nullptr && i < n; ++i) {
+    PyObject* o = outputs[i].wrap();
+    if (o == nullptr) {
+      Py_CLEAR(all);
+      break;
+    }
+    PyTuple_SET_ITEM(all, i, o);
+  }
+  return all;
+}
+
+// Outputs that a call allocates are the current stream's memory.
+void need_own_stream(Call& call, bool allocates, void* stream) { need(!allocates || stream == call.stream(Py_None)); }
+
+// (lens, new_lens, block_tables, max_tokens, page_size, out, error_word, stream) ->
+// (cum_seq_lens_q, requests, positions, slots), a status that is not 0, or None
+PyObject* token_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject* {
+    Call call;
+    smla_token_slots_args p = {};
+    const at::Tensor& lens = call.tensor(a[0]);
+    p.batch = int32(lens.numel());
+    p.lens = static_cast<const int32_t*>(call.words(a[0], 0));
+    p.new_lens = static_cast<const int32_t*>(call.words(a[1], p.batch));
+    p.max_tokens = int32(a[3]);
+    need(p.max_tokens >= 0);
+    const bool tables = a[2] != Py_None, given = a[5] != Py_None;
+    if (tables) {
+      int32_t rows = 0;
+      p.block_tables = table(call, a[2], &rows, &p.max_pages, &p.block_table_stride);
+      p.page_size = int32(a[4]);
+      need(rows >= p.batch);
+    }
+    need(!given || (PyTuple_Check(a[5]) && PyTuple_GET_SIZE(a[5]) == 4));
+    const auto item = [&](Py_ssize_t i) { return given ? PyTuple_GET_ITEM(a[5], i) : nullptr; };
+    p.error_word = static_cast<int32_t*>(call.words(a[6], 1, true));
+    void* const stream = call.stream(a[7]);
+    need_own_stream(call, !given, stream);
+    Output out[4];
+    out[0].set(call, item(0), c10::kInt, {p.batch + (int64_t)1}, p.batch + (int64_t)1, lens);
+    out[1].set(call, item(1), c10::kInt, {p.max_tokens}, p.max_tokens, lens);
+    out[2].set(call, item(2), c10::kInt, {p.max_tokens}, p.max_tokens, lens);
+    if (tables) out[3].set(call, item(3), c10::kLong, {p.max_tokens}, p.max_tokens, lens);
+    else need(!given || item(3) == Py_None);
+    p.cum_seq_lens_q = static_cast<int32_t*>(out[0].data);
+    p.requests = static_cast<int32_t*>(out[1].data);
+    p.positions = static_cast<int32_t*>(out[2].data);
+    p.slots = static_cast<int64_t*>(out[3].data);
+    const smla_status s = unlocked([&] { return smla_token_slots(&p, stream); });
+    return s != SMLA_OK ? PyLong_FromLong(s) : tuple_of(out, 4);
+  });
+}
+
+// (seq_lens, swa_tables, num_tokens, page_size, cum_seq_lens_q, selected, num_selected, compressed_tables,
+//  compressed_page_size, compress_ratio, sparse_indices, topk_lens, error_word, stream) ->
+// (sparse_indices, topk_lens), a status that is not 0, or None
+PyObject* sparse_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&]() -> PyObject* {
+    Call call;
+    smla_sparse_slots_args p = {};
+    p.swa_tables = table(call, a[1], &p.batch, &p.swa_max_pages, &p.swa_table_stride);
+    p.seq_lens = static_cast<const int32_t*>(call.words(a[0], p.batch));
+    p.sum_q = int32(a[2]);
+    need(p.sum_q > 0);
+    p.swa_page_size = int32(a[3]);
+    p.cum_seq_lens_q = static_cast<const int32_t*>(call.words(a[4], p.batch + (int64_t)1, true));
+    p.num_selected = int32(a[6]);
+    if (a[5] != Py_None) {
+      const at::Tensor& t = call.tensor(a[5]);
+      need(t.scalar_type() == c10::kInt && t.dim() == 2 && t.size(0) == p.sum_q && t.size(1) > 0 && t.stride(1) == 1 &&
+           (p.sum_q == 1 || t.stride(0) >= t.size(1)));
+      p.selected = static_cast<const int32_t*>(t.data_ptr());
+      p.num_selected = int32(t.size(1));
+      p.selected_stride = p.sum_q > 1 ? t.stride(0) : 0;
+    }
+    need(p.num_selected >= 0 && (p.num_selected == 0 || a[7] != Py_None));
+    if (a[7] != Py_None) {
+      int32_t rows = 0;
+      p.comp_tables = table(call, a[7], &rows, &p.comp_max_pages, &p.comp_table_stride);
+      p.comp_page_size = int32(a[8]);
+      need(rows == p.batch);
+    }
+    p.compress_ratio = int32(a[9]);
+    p.error_word = static_cast<int32_t*>(call.words(a[12], 1, true));
+    void* const stream = call.stream(a[13]);
+    need_own_stream(call, a[10] == Py_None || a[11] == Py_None, stream);
+    const int64_t columns = SMLA_SWA_COLS + (int64_t)p.num_selected;
+    Output out[2];
+    if (a[10] == Py_None) {
+      out[0].set(call, nullptr, c10::kInt, {p.sum_q, columns}, 0, call.tensor(a[1]));
+      p.indices_row_stride = columns;
+    } else {
+      const at::Tensor& t = call.tensor(a[10]);
+      need(t.scalar_type() == c10::kInt && t.dim() == 2 && t.size(0) == p.sum_q && t.size(1) == columns && t.stride(1) == 1 &&
+           (p.sum_q == 1 || t.stride(0) >= columns));
+      out[0].given = a[10];
+      out[0].data = t.data_ptr();
+      p.indices_row_stride = p.sum_q > 1 ? t.stride(0) : columns;
+    }
+    out[1].set(call, a[11] == Py_None ? nullptr : a[11], c10::kInt, {p.sum_q}, p.sum_q, call.tensor(a[1]));
+    p.sparse_indices = static_cast<int32_t*>(out[0].data);
+    p.topk_lens = static_cast<int32_t*>(out[1].data);
+    const smla_status s = unlocked([&] { return smla_sparse_slots(&p, stream); });
+    return s != SMLA_OK ? PyLong_FromLong(s) : tuple_of(out, 2);
+  });
+}
+
+// (logits, scores, workspace, num_out, finished, end_token, out, error_word, stream) ->
+// (scores, parents, tokens), a status that is not 0, or None
+PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    Call call;
+    smla_beam_args p = {};
+    const at::Tensor &logits = call.tensor(a[0]), &scores = call.tensor(a[1]);
+    need(logits.dim() == 2 && scores.dim() == 2 && scores.scalar_type() == c10::kFloat && scores.is_contiguous() &&
+         logits.size(0) == scores.numel() && logits.size(0) > 0 && logits.size(1) > 0 && logits.stride(1) == 1 &&
+         (logits.size(0) == 1 || logits.stride(0) >= logits.size(1)));
+    switch (logits.scalar_type()) {
+      case c10::kBFloat16: p.dtype = SMLA_LOGITS_BF16; break;
+      case c10::kHalf: p.dtype = SMLA_LOGITS_FP16; break;
+      case c10::kFloat: p.dtype = SMLA_LOGITS_FP32; break;
+      default: need(false);
+    }
+    p.batch = int32(scores.size(0));
+    p.beams = int32(scores.size(1));
+    p.vocab = int32(logits.size(1));
+    p.num_out = a[3] == Py_None ? p.beams : int32(a[3]);
+    need(p.num_out > 0 && p.num_out <= SMLA_MAX_BEAM_OUT);
+    p.logits = logits.data_ptr();
+    p.logits_stride = logits.size(0) > 1 ? logits.stride(0) : p.vocab;
+    p.scores = static_cast<const float*>(scores.data_ptr());
+    p.workspace = call.bytes(a[2], &p.workspace_bytes);
+    if (a[4] != Py_None) {
+      const at::Tensor& t = call.tensor(a[4]);
+      need((t.scalar_type() == c10::kBool || t.scalar_type() == c10::kByte) && t.is_contiguous() &&
+           t.numel() == scores.numel());
+      p.finished = static_cast<const uint8_t*>(t.data_ptr());
+    }
+    p.end_token = int32(a[5]);
+    const bool given = a[6] != Py_None;
+    need(!given || (PyTuple_Check(a[6]) && PyTuple_GET_SIZE(a[6]) == 3));
+    p.error_word = static_cast<int32_t*>(call.words(a[7], 1, true));
+    void* const stream = call.stream(a[8]);
+    need_own_stream(call, !given, stream);
+    const int64_t entries = (int64_t)p.batch * p.num_out;
+    Output out[3];
+    for (int i = 0; i < 3; ++i)
+      out[i].set(call, given ? PyTuple_GET_ITEM(a[6], i) : nullptr, i == 0 ? c10::kFloat : c10::kInt, {p.batch, p.num_out},
+                 entries, scores);
+    p.out_scores = static_cast<float*>(out[0].data);
+    p.out_parents = static_cast<int32_t*>(out[1].data);
+    p.out_tokens = static_cast<int32_t*>(out[2].data);
+    const smla_status s = unlocked([&] { return smla_beam_select(&p, stream); });
+    return s != SMLA_OK ? PyLong_FromLong(s) : tuple_of(out, 3);
+  });
+}
+
 template <class F>
 PyCFunction fast(F f) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f));
@@ -323,8 +534,13 @@ PyMethodDef methods[] = {
     {"append", fast(append), METH_FASTCALL, nullptr},
     {"pages_resize", fast(pages_resize), METH_FASTCALL, nullptr},
     {"pages_fork", fast(pages_fork), METH_FASTCALL, nullptr},
+    {"pages_reorder", fast(pages_reorder), METH_FASTCALL, nullptr},
+    {"pages_shared_prefix", fast(pages_shared_prefix), METH_FASTCALL, nullptr},
     {"pages_compact", fast(pages_compact), METH_FASTCALL, nullptr},
     {"pages_copy", fast(pages_copy), METH_FASTCALL, nullptr},
+    {"token_slots", fast(token_slots), METH_FASTCALL, nullptr},
+    {"sparse_slots", fast(sparse_slots), METH_FASTCALL, nullptr},
+    {"beam_select", fast(beam_select), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "smla_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

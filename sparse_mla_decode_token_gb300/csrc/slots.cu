@@ -1,0 +1,190 @@
+// Slot maps of a step: offsets, positions and physical slots of its new tokens
+// from the requests' lengths, and the sparse decode's index table from page
+// tables.  Integer arithmetic and look-ups: bound by latency at a decode step's
+// size, by the index table's bytes for prompts.
+#include "step.cuh"
+
+namespace smla {
+namespace {
+
+__device__ __forceinline__ void flag(int32_t* err, int bit) {
+  if (err != nullptr) atomicOr(err, bit);
+}
+
+// --------------------------------------------------------------- token slots
+// Every CTA sums the requests' new tokens itself, a thousand requests at a time
+// (a scan over the CTA; the lengths come out of L2), and looks its own tokens up
+// in the offsets; the first one also writes them.
+constexpr int kSlotThreads = 1024;
+
+__global__ void __launch_bounds__(kSlotThreads) token_slots_kernel(const TokenSlotsParams p) {
+  __shared__ int64_t s_cum[kSlotThreads + 1];
+  __shared__ int64_t s_warp[kSlotThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kSlotThreads + threadIdx.x;
+  const int64_t last = min((int64_t)(blockIdx.x + 1) * kSlotThreads, (int64_t)p.max_tokens);   // behind the CTA's tokens
+  await_prior_kernel();
+  admit_next_kernel();
+  int request = -1, position = -1;
+  int64_t before = 0;                             // new tokens of the requests before this batch of them
+  for (int base = 0; base < p.batch && (blockIdx.x == 0 || before < last); base += kSlotThreads) {
+    const int b = base + threadIdx.x;
+    int64_t n = 0;
+    if (b < p.batch) {
+      const int32_t old = fetch(p.lens + b), now = fetch(p.new_lens + b);
+      if (old < 0 || now < 0) flag(p.err, SMLA_DEVERR_PAGE_STATE);
+      n = max(0, now - max(0, old));
+    }
+    int64_t sum = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += x;
+    }
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      int64_t all = s_warp[lane];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, all, d);
+        if (lane >= d) all += x;
+      }
+      s_warp[lane] = all;
+    }
+    __syncthreads();
+    sum += before + (warp > 0 ? s_warp[warp - 1] : 0);
+    s_cum[threadIdx.x + 1] = sum;
+    if (threadIdx.x == 0) s_cum[0] = before;
+    __syncthreads();
+    if (blockIdx.x == 0 && b < p.batch) p.cum[b + 1] = (int32_t)min(sum, (int64_t)0x7fffffff);
+    if (request < 0 && t < last && t >= s_cum[0] && t < s_cum[kSlotThreads]) {
+      int lo = 0, hi = kSlotThreads - 1;          // the last request that begins at or before t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (s_cum[mid] <= t) lo = mid;
+        else hi = mid - 1;
+      }
+      request = base + lo;
+      position = max(0, fetch(p.lens + request)) + (int)(t - s_cum[lo]);
+    }
+    before = s_cum[kSlotThreads];
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    p.cum[0] = 0;
+    if (before > p.max_tokens) flag(p.err, SMLA_DEVERR_TOO_MANY_TOKENS);
+  }
+  if (t >= p.max_tokens) return;
+  if (p.requests != nullptr) p.requests[t] = request;
+  if (p.positions != nullptr) p.positions[t] = position;
+  if (p.slots != nullptr) {
+    int64_t slot = -1;
+    if (request >= 0) {
+      const int column = position / p.page_size;
+      const int page = column < p.max_pages ? fetch(p.bt + request * p.bt_stride + column) : -1;
+      if (page >= 0) slot = (int64_t)page * p.page_size + (position - column * p.page_size);
+      else flag(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
+    }
+    p.slots[t] = slot;
+  }
+}
+
+// -------------------------------------------------------------- sparse slots
+// A CTA a token: its columns, four a thread at a time (one 16-byte store where
+// the table's rows allow it).
+constexpr int kSparseThreads = 256;
+
+// Row of position j >= 0, or -1 (*bad set).
+__device__ __forceinline__ int slot_row(const SlotTable& t, const int32_t* row, int j, bool* bad) {
+  const int column = t.shift >= 0 ? j >> t.shift : j / t.page_size;
+  const int page = column < t.max_pages ? fetch(row + column) : -1;
+  const int64_t at = (int64_t)page * t.page_size + (j - column * t.page_size);
+  if (page >= 0 && at <= 0x7fffffff) return (int)at;
+  *bad = true;
+  return -1;
+}
+
+template <bool kVector>
+__global__ void __launch_bounds__(kSparseThreads) sparse_slots_kernel(const SparseSlotsParams p) {
+  __shared__ int s_last[kSparseThreads / 32];
+  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  await_prior_kernel();
+  admit_next_kernel();
+  int b, first, count;
+  if (p.cum != nullptr) {
+    b = last_request(p.batch, lane, [&](int x) { return fetch(p.cum + x) <= t; });
+    first = fetch(p.cum + b);
+    count = fetch(p.cum + b + 1) - first;
+  } else {
+    count = p.sum_q / p.batch;
+    b = t / count;
+    first = b * count;
+  }
+  const bool owned = t >= first && t - first < count;
+  const int pos = owned ? fetch(p.seq_lens + b) - count + (t - first) : -1;
+  const int lo = max(0, pos - (kSwaCols - 1));
+  const int limit = pos >= 0 ? (int)(((int64_t)pos + 1) / p.ratio) : 0;
+  const int32_t* swa = p.swa.bt + b * p.swa.stride;
+  const int32_t* comp = p.comp.bt + b * p.comp.stride;
+  const int32_t* pick = p.selected + t * p.selected_stride;
+  int32_t* out = p.out + t * p.out_stride;
+  const int columns = kSwaCols + p.num_selected;
+  int last = 0;
+  bool bad = false;
+  for (int c0 = threadIdx.x * 4; c0 < columns; c0 += kSparseThreads * 4) {
+    int v[4], c[4];
+    if (c0 < kSwaCols) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = lo + c0 + e <= pos ? lo + c0 + e : -1;
+    } else if (p.selected == nullptr) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = c0 - kSwaCols + e;
+    } else if (kVector) {
+      const int4 q = *reinterpret_cast<const int4*>(pick + (c0 - kSwaCols));
+      c[0] = q.x, c[1] = q.y, c[2] = q.z, c[3] = q.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = c0 + e < columns ? fetch(pick + (c0 - kSwaCols + e)) : -1;
+    }
+    const bool window = c0 < kSwaCols;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool seen = window ? c[e] >= 0 : c[e] >= 0 && c[e] < limit && c0 + e < columns;
+      v[e] = seen ? slot_row(window ? p.swa : p.comp, window ? swa : comp, c[e], &bad) : -1;
+      if (!window && v[e] >= 0) last = max(last, c0 + e + 1 - kSwaCols);
+    }
+    if (kVector) {
+      *reinterpret_cast<int4*>(out + c0) = make_int4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c0 + e < columns) out[c0 + e] = v[e];
+    }
+  }
+  if (bad) flag(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
+  last = __reduce_max_sync(0xffffffffu, last);
+  if (lane == 0) s_last[warp] = last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kSparseThreads / 32; ++w) last = max(last, s_last[w]);
+    p.topk[t] = pos >= 0 ? kSwaCols + last : 0;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_token_slots(const TokenSlotsParams& p, cudaStream_t stream) {
+  const unsigned ctas = (unsigned)(((int64_t)p.max_tokens + kSlotThreads - 1) / kSlotThreads);
+  return launch_overlapped(token_slots_kernel, dim3(ctas > 0 ? ctas : 1), kSlotThreads, 0, stream, p);
+}
+
+cudaError_t launch_sparse_slots(const SparseSlotsParams& p, cudaStream_t stream) {
+  auto whole = [](const void* at, int64_t stride) { return reinterpret_cast<uintptr_t>(at) % 16 == 0 && stride % 4 == 0; };
+  const bool vector = p.num_selected % 4 == 0 && whole(p.out, p.out_stride) &&
+                      (p.selected == nullptr || whole(p.selected, p.selected_stride));
+  return launch_overlapped(vector ? sparse_slots_kernel<true> : sparse_slots_kernel<false>, dim3((unsigned)p.sum_q),
+                           kSparseThreads, 0, stream, p);
+}
+
+}  // namespace smla

@@ -148,7 +148,7 @@ def code_only(text: str) -> str:
 HOST_ONLY_SOURCES = ("smla_api.cu",)
 # Sources of the calls around it, which no decode launches.
 OTHER_SOURCES = ("api_checks.h", "beam_select.cu", "cache.cuh", "cache_api.cu", "cache_append.cu", "cache_pages.cu", "cache_ptx.cuh",
-                 "slots.cu", "step.cuh", "step_api.cu", "window_attention.cu")
+                 "prefix_attention.cu", "slots.cu", "step.cuh", "step_api.cu", "window_attention.cu")
 PLAN_KEYS = ("kernel", "num_splits", "ctas_per_split", "grid", "threads", "smem_bytes", "clusters")
 
 

@@ -419,6 +419,50 @@ smla_status smla_window_workspace_size(const smla_window_args* args, int device,
 smla_status smla_window_attention(const smla_window_args* args, void* stream);
 
 /*
+ * Attention of a batch whose groups share long prefixes: plain causal attention
+ * (token i of request b sees the rows j <= pos = seq_lens[b] - q_len_b + i), for
+ * which the first P_g rows of every request of group g, group_starts[g] <= b <
+ * group_starts[g + 1], are read through the page table of the group's first
+ * request, once for all of them where that saves work (H not a multiple of 64);
+ *
+ *   P_g = min(prefix_lens[g], seq_lens[b] - q_len_b + 1 over the group's requests with new tokens),
+ *
+ * not negative: a prefix ends at the latest where all tokens of the group see
+ * it.  Requests whose tables begin with the same pages (smla_pages_fork,
+ * smla_pages_reorder; smla_pages_shared_prefix tells how many) get what
+ * smla_window_attention with a window of the whole sequence gives, but for
+ * roundings.  Requests outside every group have no prefix; prefix_lens of 0 is
+ * none.  Group starts that fall or lie outside 0 .. batch set
+ * SMLA_DEVERR_PAGE_STATE, and the call shares nothing.  O, LSE2, sinks, scales,
+ * masks, flags and precision are as for smla_window_attention; so are tokens of
+ * no request.
+ */
+typedef struct smla_prefix_args {
+  smla_cache cache;
+  int32_t sum_q;                    /* flattened query tokens T (0 = nothing to do) */
+  int32_t num_heads;                /* H: 1 .. 128 */
+  int32_t num_groups;               /* >= 0 */
+  const int32_t* group_starts;      /* [num_groups + 1] first request of each group */
+  const int32_t* prefix_lens;       /* [num_groups] tokens */
+  const void* q;                    /* [T, H, 512] BF16, heads and dims contiguous, 16-byte aligned */
+  int64_t q_stride_token;           /* elements [H * 512], a multiple of 8 */
+  const float* sinks;               /* [H] float32 sink logits (natural-log units), or NULL */
+  float bmm1_scale, bmm2_scale;     /* QK / softmax scale; output scale */
+  const float* bmm1_scale_dev;      /* optional device float32 overriding bmm1_scale */
+  const float* bmm2_scale_dev;      /* optional device float32 overriding bmm2_scale */
+  void* out;                        /* [T, H, 512] BF16, contiguous, 16-byte aligned */
+  float* out_lse;                   /* [T, H] float32 base-2 LSE, contiguous, or NULL */
+  void* workspace;                  /* >= smla_prefix_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  int32_t* error_word;              /* optional device int32; kernels OR SMLA_DEVERR_* bits into it */
+} smla_prefix_args;
+
+/* Workspace bytes smla_prefix_attention will need for these shapes on `device` (pointers are not looked at). */
+smla_status smla_prefix_workspace_size(const smla_prefix_args* args, int device, size_t* bytes);
+
+smla_status smla_prefix_attention(const smla_prefix_args* args, void* stream);
+
+/*
  * Append: quantises the T new latent rows of this call into the cache, row t
  * at position seq_lens[b] - q_len_b + i of its request.  Each block that
  * receives rows takes the scale

@@ -102,6 +102,8 @@ EXPORTS = {
     # the paged latent cache (argument structs in cache.py)
     "smla_window_workspace_size": (ctypes.c_int, [_c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
     "smla_window_attention": (ctypes.c_int, [_c_void_p, _c_void_p]),
+    "smla_prefix_workspace_size": (ctypes.c_int, [_c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    "smla_prefix_attention": (ctypes.c_int, [_c_void_p, _c_void_p]),
     "smla_cache_append": (ctypes.c_int, [_c_void_p, _c_void_p]),
     "smla_pages_workspace_size": (ctypes.c_int, [_c_void_p, ctypes.POINTER(ctypes.c_size_t)]),
     "smla_pages_resize": (ctypes.c_int, [_c_void_p, _c_void_p]),

@@ -9,7 +9,7 @@ float32 scales ``[num_pages, page_size // block_rows]`` (one per block of
 tokens), int32 page tables ``[requests, max_pages]``, lengths ``[requests]``
 and, for the page calls, a count per page (0 = free).  The calls are the
 ``smla_window_*``, ``smla_cache_*`` and ``smla_pages_*`` entry points of
-``include/smla.h``, which defines them; all work on the device, on the current
+``include/smla.h``, which defines them (``smla_prefix_*`` among them); all work on the device, on the current
 stream unless ``stream`` is given, and none waits.
 
     pages_resize(tables, refs, lens, new_lens, ws, page_size=64, moves=moves)   # pages for the new tokens
@@ -53,6 +53,19 @@ class SmlaWindowArgs(ctypes.Structure):
         ("out", _c_void_p), ("out_lse", _c_void_p),
         ("workspace", _c_void_p), ("workspace_bytes", _size),
         ("num_splits", _i32), ("error_word", _c_void_p),
+    ]
+
+
+class SmlaPrefixArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", SmlaCache),
+        ("sum_q", _i32), ("num_heads", _i32), ("num_groups", _i32),
+        ("group_starts", _c_void_p), ("prefix_lens", _c_void_p),
+        ("q", _c_void_p), ("q_stride_token", _i64), ("sinks", _c_void_p),
+        ("bmm1_scale", ctypes.c_float), ("bmm2_scale", ctypes.c_float),
+        ("bmm1_scale_dev", _c_void_p), ("bmm2_scale_dev", _c_void_p),
+        ("out", _c_void_p), ("out_lse", _c_void_p),
+        ("workspace", _c_void_p), ("workspace_bytes", _size), ("error_word", _c_void_p),
     ]
 
 
@@ -195,7 +208,8 @@ def _cache(rows: torch.Tensor, scales: torch.Tensor, tables: torch.Tensor, seq_l
                      seq_lens.data_ptr(), None if cum is None else cum.data_ptr())
 
 
-def _window_args(q, rows, scales, tables, seq_lens, cum, sinks, window, first_tokens, num_splits) -> SmlaWindowArgs:
+def _attention_args(a, q, sinks) -> None:
+    """The queries of an attention call: what it checks of them, and their fields of its struct."""
     qs, qt = q.shape, q.stride()
     if q.dtype is not torch.bfloat16:
         raise TypeError(f"q must be bfloat16; got {q.dtype}")
@@ -205,49 +219,12 @@ def _window_args(q, rows, scales, tables, seq_lens, cum, sinks, window, first_to
         raise ValueError("the tokens of q must not share memory")
     if sinks is not None:
         _words("sinks", sinks, qs[1], torch.float32)
-    return SmlaWindowArgs(_cache(rows, scales, tables, seq_lens, cum), qs[0], qs[1], _int32("window", window),
-                          _int32("first_tokens", first_tokens),
-                          q.data_ptr(), qt[0] if qs[0] > 1 else 0, None if sinks is None else sinks.data_ptr(),
-                          1.0, 1.0, None, None, None, None, None, 0, _int32("num_splits", num_splits), None)
+    a.sum_q, a.num_heads, a.bmm1_scale, a.bmm2_scale = qs[0], qs[1], 1.0, 1.0
+    a.q, a.q_stride_token, a.sinks = q.data_ptr(), qt[0] if qs[0] > 1 else 0, None if sinks is None else sinks.data_ptr()
 
 
-def window_workspace_size(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block_tables: torch.Tensor,
-                          seq_lens: torch.Tensor, *, window: int, first_tokens: int = 0,
-                          cum_seq_lens_q: Optional[torch.Tensor] = None, num_splits: int = 0,
-                          device: Optional[int] = None) -> int:
-    """Workspace bytes of ``window_attention`` for these shapes (no device memory is
-    read), on ``device``, by default q's."""
-    a = _window_args(q, rows, scales, block_tables, seq_lens, cum_seq_lens_q, None, window, first_tokens, num_splits)
-    n = ctypes.c_size_t(0)
-    if device is None:
-        device = max(q.get_device(), 0)
-    _check(_b.lib().smla_window_workspace_size(ctypes.byref(a), device, ctypes.byref(n)))
-    return int(n.value)
-
-
-_WINDOW_TENSORS = ("q", "rows", "scales", "block_tables", "seq_lens", "workspace", "cum_seq_lens_q", "sinks", "bmm1_scale",
-                   "bmm2_scale", "out", "out_lse", "error_word")
-
-
-def window_attention(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block_tables: torch.Tensor,
-                     seq_lens: torch.Tensor, workspace_buffer: Optional[torch.Tensor], *, window: int,
-                     first_tokens: int = 0, cum_seq_lens_q: Optional[torch.Tensor] = None,
-                     sinks: Optional[torch.Tensor] = None, bmm1_scale=1.0, bmm2_scale=1.0,
-                     out: Optional[torch.Tensor] = None, out_lse: Optional[torch.Tensor] = None,
-                     num_splits: int = 0, error_word: Optional[torch.Tensor] = None,
-                     stream: Optional[int] = None):
-    """Attention of BF16 queries ``[T, H, 512]`` over the last ``window`` cached
-    tokens of their request up to their own position, and its first
-    ``first_tokens``; returns ``(out, out_lse)``, allocated when not given (as
-    ``stream``'s memory, where that is another than the current one)."""
-    done = (_extension or extension()).window_attention(
-        q, rows, scales, block_tables, seq_lens, workspace_buffer, cum_seq_lens_q, sinks, window, first_tokens, num_splits,
-        bmm1_scale, bmm2_scale, out, out_lse, error_word, stream)
-    if done.__class__ is tuple:
-        return done
-    if done is not None:
-        _check(done)
-    a = _window_args(q, rows, scales, block_tables, seq_lens, cum_seq_lens_q, sinks, window, first_tokens, num_splits)
+def _attention_call(a, function, names, q, tensors, workspace_buffer, bmm1_scale, bmm2_scale, out, out_lse, error_word, stream):
+    """The outputs, scales and workspace of an attention call, and the call."""
     T, H = a.sum_q, a.num_heads
     with _b._allocate_for(stream, q.get_device()):
         new_out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else None
@@ -282,10 +259,109 @@ def window_attention(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, 
             raise ValueError("workspace must be contiguous")
         a.workspace, a.workspace_bytes = workspace_buffer.data_ptr(), workspace_buffer.nbytes
     index = q.get_device()
-    _on(index, (q, rows, scales, block_tables, seq_lens, workspace_buffer, cum_seq_lens_q, sinks, scale1, scale2, out,
-                out_lse, error_word), _WINDOW_TENSORS)
-    _call(_b.lib().smla_window_attention, index, stream, ctypes.byref(a))
+    _on(index, (q, *tensors, workspace_buffer, scale1, scale2, out, out_lse, error_word),
+        ("q", *names, "workspace", "bmm1_scale", "bmm2_scale", "out", "out_lse", "error_word"))
+    _call(function, index, stream, ctypes.byref(a))
     return out, out_lse
+
+
+def _window_args(q, rows, scales, tables, seq_lens, cum, sinks, window, first_tokens, num_splits) -> SmlaWindowArgs:
+    a = SmlaWindowArgs()
+    _attention_args(a, q, sinks)
+    a.cache = _cache(rows, scales, tables, seq_lens, cum)
+    a.window, a.first_tokens, a.num_splits = _int32("window", window), _int32("first_tokens", first_tokens), \
+        _int32("num_splits", num_splits)
+    return a
+
+
+def window_workspace_size(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block_tables: torch.Tensor,
+                          seq_lens: torch.Tensor, *, window: int, first_tokens: int = 0,
+                          cum_seq_lens_q: Optional[torch.Tensor] = None, num_splits: int = 0,
+                          device: Optional[int] = None) -> int:
+    """Workspace bytes of ``window_attention`` for these shapes (no device memory is
+    read), on ``device``, by default q's."""
+    a = _window_args(q, rows, scales, block_tables, seq_lens, cum_seq_lens_q, None, window, first_tokens, num_splits)
+    n = ctypes.c_size_t(0)
+    if device is None:
+        device = max(q.get_device(), 0)
+    _check(_b.lib().smla_window_workspace_size(ctypes.byref(a), device, ctypes.byref(n)))
+    return int(n.value)
+
+
+_CACHE_TENSORS = ("rows", "scales", "block_tables", "seq_lens", "cum_seq_lens_q", "sinks")
+
+
+def window_attention(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block_tables: torch.Tensor,
+                     seq_lens: torch.Tensor, workspace_buffer: Optional[torch.Tensor], *, window: int,
+                     first_tokens: int = 0, cum_seq_lens_q: Optional[torch.Tensor] = None,
+                     sinks: Optional[torch.Tensor] = None, bmm1_scale=1.0, bmm2_scale=1.0,
+                     out: Optional[torch.Tensor] = None, out_lse: Optional[torch.Tensor] = None,
+                     num_splits: int = 0, error_word: Optional[torch.Tensor] = None,
+                     stream: Optional[int] = None):
+    """Attention of BF16 queries ``[T, H, 512]`` over the last ``window`` cached
+    tokens of their request up to their own position, and its first
+    ``first_tokens``; returns ``(out, out_lse)``, allocated when not given (as
+    ``stream``'s memory, where that is another than the current one)."""
+    done = (_extension or extension()).window_attention(
+        q, rows, scales, block_tables, seq_lens, workspace_buffer, cum_seq_lens_q, sinks, window, first_tokens, num_splits,
+        bmm1_scale, bmm2_scale, out, out_lse, error_word, stream)
+    if done.__class__ is tuple:
+        return done
+    if done is not None:
+        _check(done)
+    a = _window_args(q, rows, scales, block_tables, seq_lens, cum_seq_lens_q, sinks, window, first_tokens, num_splits)
+    return _attention_call(a, _b.lib().smla_window_attention, _CACHE_TENSORS, q,
+                           (rows, scales, block_tables, seq_lens, cum_seq_lens_q, sinks), workspace_buffer, bmm1_scale,
+                           bmm2_scale, out, out_lse, error_word, stream)
+
+
+def _prefix_args(q, rows, scales, tables, seq_lens, cum, sinks, group_starts, prefix_lens) -> SmlaPrefixArgs:
+    a = SmlaPrefixArgs()
+    _attention_args(a, q, sinks)
+    a.cache = _cache(rows, scales, tables, seq_lens, cum)
+    _words("group_starts", group_starts, 1)
+    a.num_groups, a.group_starts = group_starts.numel() - 1, group_starts.data_ptr()
+    if prefix_lens is not None:
+        _words("prefix_lens", prefix_lens, a.num_groups)
+        a.prefix_lens = prefix_lens.data_ptr()
+    return a
+
+
+def prefix_workspace_size(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block_tables: torch.Tensor,
+                          seq_lens: torch.Tensor, *, group_starts: torch.Tensor,
+                          cum_seq_lens_q: Optional[torch.Tensor] = None, device: Optional[int] = None) -> int:
+    """Workspace bytes of ``prefix_attention`` for these shapes (no device memory is
+    read), on ``device``, by default q's."""
+    a = _prefix_args(q, rows, scales, block_tables, seq_lens, cum_seq_lens_q, None, group_starts, None)
+    n = ctypes.c_size_t(0)
+    if device is None:
+        device = max(q.get_device(), 0)
+    _check(_b.lib().smla_prefix_workspace_size(ctypes.byref(a), device, ctypes.byref(n)))
+    return int(n.value)
+
+
+def prefix_attention(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, block_tables: torch.Tensor,
+                     seq_lens: torch.Tensor, workspace_buffer: torch.Tensor, *, group_starts: torch.Tensor,
+                     prefix_lens: torch.Tensor, cum_seq_lens_q: Optional[torch.Tensor] = None,
+                     sinks: Optional[torch.Tensor] = None, bmm1_scale=1.0, bmm2_scale=1.0,
+                     out: Optional[torch.Tensor] = None, out_lse: Optional[torch.Tensor] = None,
+                     error_word: Optional[torch.Tensor] = None, stream: Optional[int] = None):
+    """Causal attention of BF16 queries ``[T, H, 512]`` over the cached tokens of
+    their request, of which the requests ``group_starts[g] <= b <
+    group_starts[g + 1]`` share the first ``prefix_lens[g]`` (read through the
+    first one's table, once for all); returns ``(out, out_lse)``, allocated when
+    not given (as ``stream``'s memory, where that is another than the current one)."""
+    done = (_extension or extension()).prefix_attention(
+        q, rows, scales, block_tables, seq_lens, workspace_buffer, cum_seq_lens_q, sinks, group_starts, prefix_lens,
+        bmm1_scale, bmm2_scale, out, out_lse, error_word, stream)
+    if done.__class__ is tuple:
+        return done
+    if done is not None:
+        _check(done)
+    a = _prefix_args(q, rows, scales, block_tables, seq_lens, cum_seq_lens_q, sinks, group_starts, prefix_lens)
+    return _attention_call(a, _b.lib().smla_prefix_attention, _CACHE_TENSORS + ("group_starts", "prefix_lens"), q,
+                           (rows, scales, block_tables, seq_lens, cum_seq_lens_q, sinks, group_starts, prefix_lens),
+                           workspace_buffer, bmm1_scale, bmm2_scale, out, out_lse, error_word, stream)
 
 
 _APPEND_TENSORS = ("latent", "rows", "scales", "block_tables", "seq_lens", "cum_seq_lens_q", "error_word")

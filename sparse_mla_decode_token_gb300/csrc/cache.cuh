@@ -101,6 +101,28 @@ constexpr int kWindowHeads = 64;      // heads of one token that a CTA takes
 constexpr int kWindowTile = 128;      // cache rows of one tile
 constexpr int kMaxWindowSplits = 256;
 
+// log2 of a TMA box's rows: the highest box that pages hold whole, up to a quarter
+// of a tile (fewer copies to issue).
+__host__ __device__ inline int cache_box_shift(int page_size) { return page_size % 32 == 0 ? 5 : page_size % 16 == 0 ? 4 : 3; }
+
+// Plan of a batch whose groups share prefixes, made on the device (prefix_attention.cu).
+constexpr int kPlanPer = 0, kPlanParts = 1, kPlanUnits = 2, kPlanPieces = 3, kPlanHeader = 16;
+struct PrefixPlan {
+  int32_t groups, max_parts, max_units;
+  const int32_t* group_starts;          // [groups + 1] first request of each
+  const int32_t* prefix_lens;           // [groups]
+  int32_t* header;                      // tiles of a piece, partial units, all units, most pieces of a list
+  int32_t* part_of;                     // [groups + T + 1] first partial unit of a group's prefix, of a token
+  int32_t* whole_of;                    // [T + 1] first of the units that are no partial ones
+  int4* group;                          // [groups] first request, first token, (token, head) rows, prefix (0: not shared)
+  int4* token;                          // [T] request, its group's first one (sign: the prefix is the group's), position, prefix
+  int4* request;                        // [batch] tokens, tiles of the last one, group or -1, the second word of its tokens
+  int32_t* limit;                       // [groups] positions that all the group's tokens see
+};
+
+cudaError_t launch_planned_attention(const WindowParams& p, const PrefixPlan& plan, int sms, cudaStream_t stream);
+cudaError_t launch_prefix_attention(const WindowParams& p, const PrefixPlan& plan, int sms, cudaStream_t stream);
+
 cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t stream);
 
 struct AppendParams {

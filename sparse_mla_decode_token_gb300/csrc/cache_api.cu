@@ -80,16 +80,54 @@ CacheView view(const smla_cache& c, int32_t sum_q) {
 
 // ----------------------------------------------------------------- window
 
-smla_status check_window(const smla_window_args* a) {
+// What the two attention calls have alike.
+template <class Args>
+smla_status check_attention(const Args* a) {
   if (a == nullptr) return fail(SMLA_ERR_INVALID_ARG, "args is NULL");
   SMLA_TRY(check_cache(a->cache, a->sum_q));
   if (a->num_heads < 1 || a->num_heads > 128)
     return fail(SMLA_ERR_UNSUPPORTED, "num_heads %d is outside 1 .. 128", a->num_heads);
-  if (a->window < 1) return fail(SMLA_ERR_INVALID_ARG, "window %d < 1", a->window);
-  if (a->first_tokens < 0) return fail(SMLA_ERR_INVALID_ARG, "first_tokens %d is negative", a->first_tokens);
   if (a->q_stride_token != 0 && (a->q_stride_token < (int64_t)a->num_heads * kHeadDim || a->q_stride_token % 8 != 0))
     return fail(SMLA_ERR_INVALID_ARG, "q_stride_token %lld: at least H * 512 elements, a multiple of 8",
                 (long long)a->q_stride_token);
+  return SMLA_OK;
+}
+
+template <class Args>
+smla_status check_attention_pointers(const Args* a) {
+  SMLA_TRY(check_cache_pointers(a->cache));
+  SMLA_TRY(need_rows("q", a->q));
+  SMLA_TRY(need_rows("out", a->out));
+  SMLA_TRY(need_words("out_lse", a->out_lse, false));
+  SMLA_TRY(need_words("sinks", a->sinks, false));
+  SMLA_TRY(need_words("bmm1_scale_dev", a->bmm1_scale_dev, false));
+  SMLA_TRY(need_words("bmm2_scale_dev", a->bmm2_scale_dev, false));
+  return need_words("error_word", a->error_word, false);
+}
+
+template <class Args>
+WindowParams attention_params(const Args* a) {
+  WindowParams p;
+  memset(&p, 0, sizeof(p));
+  p.c = view(a->cache, a->sum_q);
+  p.H = a->num_heads;
+  p.q = static_cast<const __nv_bfloat16*>(a->q);
+  p.q_stride_token = a->q_stride_token ? a->q_stride_token : (int64_t)a->num_heads * kHeadDim;
+  p.sinks = a->sinks;
+  p.bmm1 = a->bmm1_scale;
+  p.bmm2 = a->bmm2_scale;
+  p.bmm1_dev = a->bmm1_scale_dev;
+  p.bmm2_dev = a->bmm2_scale_dev;
+  p.out = static_cast<__nv_bfloat16*>(a->out);
+  p.out_lse = a->out_lse;
+  p.err = a->error_word;
+  return p;
+}
+
+smla_status check_window(const smla_window_args* a) {
+  SMLA_TRY(check_attention(a));
+  if (a->window < 1) return fail(SMLA_ERR_INVALID_ARG, "window %d < 1", a->window);
+  if (a->first_tokens < 0) return fail(SMLA_ERR_INVALID_ARG, "first_tokens %d is negative", a->first_tokens);
   if (a->num_splits < 0 || a->num_splits > SMLA_MAX_SPLITS)
     return fail(SMLA_ERR_INVALID_ARG, "num_splits %d is outside 0 .. %d", a->num_splits, SMLA_MAX_SPLITS);
   return SMLA_OK;
@@ -148,6 +186,51 @@ WindowPlan window_plan(const smla_window_args* a, int sms) {
   w.lse = align_up(rows * kHeadDim * sizeof(float), 256);
   w.bytes = w.lse + align_up(rows * sizeof(float), 256);
   return w;
+}
+
+// ----------------------------------------------------------------- prefix
+
+smla_status check_prefix(const smla_prefix_args* a) {
+  SMLA_TRY(check_attention(a));
+  if (a->num_groups < 0) return fail(SMLA_ERR_INVALID_ARG, "num_groups %d is negative", a->num_groups);
+  if ((int64_t)a->num_groups + a->sum_q > 0x3fffffff)
+    return fail(SMLA_ERR_UNSUPPORTED, "%d groups of %d tokens are too many", a->num_groups, a->sum_q);
+  return SMLA_OK;
+}
+
+// Most units that a plan on the device may need, and the workspace's parts: fp32
+// partials, then the plan.  A shared prefix takes at least a partial for each 64
+// rows of its group and each token; what more may be split is bounded here, at
+// four pieces for each SM.
+struct PrefixLayout {
+  int64_t parts, units;
+  size_t lse, header, part_of, whole_of, group, token, request, limit, bytes;
+};
+PrefixLayout prefix_layout(const smla_prefix_args* a, int sms) {
+  const int64_t T = a->sum_q, heads = (a->num_heads + kWindowHeads - 1) / kWindowHeads;
+  PrefixLayout l;
+  l.parts = 4 * (int64_t)sms;
+  if (a->num_heads % kWindowHeads != 0 && a->num_groups > 0)
+    l.parts += T * heads + T * a->num_heads / kWindowHeads + a->num_groups;
+  l.units = l.parts + T * heads;
+  const size_t rows = (size_t)l.parts * kWindowHeads;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t from = at;
+    at = align_up(at + bytes, 256);
+    return from;
+  };
+  take(rows * kHeadDim * sizeof(float));
+  l.lse = take(rows * sizeof(float));
+  l.header = take(kPlanHeader * sizeof(int32_t));
+  l.part_of = take((a->num_groups + T + 1) * sizeof(int32_t));
+  l.whole_of = take((T + 1) * sizeof(int32_t));
+  l.group = take((size_t)a->num_groups * sizeof(int4));
+  l.token = take((size_t)T * sizeof(int4));
+  l.request = take((size_t)a->cache.batch * sizeof(int4));
+  l.limit = take((size_t)a->num_groups * sizeof(int32_t));
+  l.bytes = at;
+  return l;
 }
 
 // ------------------------------------------------------------------ pages
@@ -259,43 +342,64 @@ smla_status smla_window_workspace_size(const smla_window_args* args, int device,
 smla_status smla_window_attention(const smla_window_args* a, void* stream) {
   SMLA_TRY(check_window(a));
   if (a->sum_q == 0) return SMLA_OK;
-  SMLA_TRY(check_cache_pointers(a->cache));
-  SMLA_TRY(need_rows("q", a->q));
-  SMLA_TRY(need_rows("out", a->out));
-  SMLA_TRY(need_words("out_lse", a->out_lse, false));
-  SMLA_TRY(need_words("sinks", a->sinks, false));
-  SMLA_TRY(need_words("bmm1_scale_dev", a->bmm1_scale_dev, false));
-  SMLA_TRY(need_words("bmm2_scale_dev", a->bmm2_scale_dev, false));
-  SMLA_TRY(need_words("error_word", a->error_word, false));
+  SMLA_TRY(check_attention_pointers(a));
   int sms = 0;
   SMLA_TRY(current_sms(&sms));
   const WindowPlan plan = window_plan(a, sms);
   if (plan.units > 0x7fffffff || (int64_t)a->sum_q * head_groups(a) > 0x7fffffff / kWindowHeads)
     return fail(SMLA_ERR_UNSUPPORTED, "%lld units are too many", (long long)plan.units);
   SMLA_TRY(need_workspace(a->workspace, a->workspace_bytes, plan.bytes));
-  WindowParams p;
-  memset(&p, 0, sizeof(p));
-  p.c = view(a->cache, a->sum_q);
-  p.H = a->num_heads;
+  WindowParams p = attention_params(a);
   p.window = a->window;
   p.first_tokens = a->first_tokens;
   p.whole = (int32_t)plan.whole;
   p.num_splits = plan.splits;
-  p.q = static_cast<const __nv_bfloat16*>(a->q);
-  p.q_stride_token = a->q_stride_token ? a->q_stride_token : (int64_t)a->num_heads * kHeadDim;
-  p.sinks = a->sinks;
-  p.bmm1 = a->bmm1_scale;
-  p.bmm2 = a->bmm2_scale;
-  p.bmm1_dev = a->bmm1_scale_dev;
-  p.bmm2_dev = a->bmm2_scale_dev;
-  p.out = static_cast<__nv_bfloat16*>(a->out);
-  p.out_lse = a->out_lse;
-  p.err = a->error_word;
   if (plan.bytes > 0) {
     p.part_o = static_cast<float*>(a->workspace);
     p.part_lse = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + plan.lse);
   }
   return launched("window attention", launch_window_attention(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+smla_status smla_prefix_workspace_size(const smla_prefix_args* args, int device, size_t* bytes) {
+  if (bytes == nullptr) return fail(SMLA_ERR_INVALID_ARG, "bytes is NULL");
+  SMLA_TRY(check_prefix(args));
+  int sms = 0;
+  SMLA_TRY(device_sms(device, &sms));
+  *bytes = args->sum_q == 0 ? 0 : prefix_layout(args, sms).bytes;
+  return SMLA_OK;
+}
+
+smla_status smla_prefix_attention(const smla_prefix_args* a, void* stream) {
+  SMLA_TRY(check_prefix(a));
+  if (a->sum_q == 0) return SMLA_OK;
+  SMLA_TRY(check_attention_pointers(a));
+  SMLA_TRY(need_words("group_starts", a->group_starts, a->num_groups > 0));
+  SMLA_TRY(need_words("prefix_lens", a->prefix_lens, a->num_groups > 0));
+  int sms = 0;
+  SMLA_TRY(current_sms(&sms));
+  const PrefixLayout l = prefix_layout(a, sms);
+  if (l.units > 0x7fffffff / kWindowHeads) return fail(SMLA_ERR_UNSUPPORTED, "%lld units are too many", (long long)l.units);
+  SMLA_TRY(need_workspace(a->workspace, a->workspace_bytes, l.bytes));
+  WindowParams p = attention_params(a);
+  char* const ws = static_cast<char*>(a->workspace);
+  p.part_o = static_cast<float*>(a->workspace);
+  p.part_lse = reinterpret_cast<float*>(ws + l.lse);
+  PrefixPlan plan;
+  memset(&plan, 0, sizeof(plan));
+  plan.groups = a->num_groups;
+  plan.max_parts = (int32_t)l.parts;
+  plan.max_units = (int32_t)l.units;
+  plan.group_starts = a->group_starts;
+  plan.prefix_lens = a->prefix_lens;
+  plan.header = reinterpret_cast<int32_t*>(ws + l.header);
+  plan.part_of = reinterpret_cast<int32_t*>(ws + l.part_of);
+  plan.whole_of = reinterpret_cast<int32_t*>(ws + l.whole_of);
+  plan.group = reinterpret_cast<int4*>(ws + l.group);
+  plan.token = reinterpret_cast<int4*>(ws + l.token);
+  plan.request = reinterpret_cast<int4*>(ws + l.request);
+  plan.limit = reinterpret_cast<int32_t*>(ws + l.limit);
+  return launched("prefix attention", launch_prefix_attention(p, plan, sms, static_cast<cudaStream_t>(stream)));
 }
 
 smla_status smla_cache_append(const smla_append_args* a, void* stream) {

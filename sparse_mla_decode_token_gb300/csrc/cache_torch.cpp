@@ -144,56 +144,83 @@ smla_status unlocked(F f) {
   return s;
 }
 
-// (q, rows, scales, block_tables, seq_lens, workspace, cum_seq_lens_q, sinks, window, first_tokens, num_splits,
-//  bmm1_scale, bmm2_scale, out, out_lse, error_word, stream) -> (out, out_lse), a status that is not 0, or None
+// What the two attention calls have alike: (q, rows, scales, block_tables, seq_lens, workspace, cum_seq_lens_q, sinks,
+// then what the caller sets, then from a[at] on bmm1_scale, bmm2_scale, out, out_lse, error_word, stream) ->
+// (out, out_lse), a status that is not 0, or None
+template <class Args, class Set, class Run>
+PyObject* attention(PyObject* const* a, int at, Set set, Run run) {
+  Call call;
+  Args w = {};
+  const at::Tensor& q = call.tensor(a[0]);
+  need(q.scalar_type() == c10::kBFloat16 && q.dim() == 3);
+  const int64_t T = q.size(0), H = q.size(1);
+  need(T > 0 && H > 0 && q.size(2) == kDim && q.stride(2) == 1 && (H == 1 || q.stride(1) == kDim) &&
+       (T == 1 || q.stride(0) > 0));
+  w.cache = cache(call, a[1], a[2], a[3], a[4], a[6]);
+  w.workspace = call.bytes(a[5], &w.workspace_bytes);
+  w.sinks = static_cast<const float*>(call.array(a[7], c10::kFloat, H, true));
+  set(call, w);
+  a += at;
+  scale(call, a[0], &w.bmm1_scale, &w.bmm1_scale_dev);
+  scale(call, a[1], &w.bmm2_scale, &w.bmm2_scale_dev);
+  w.sum_q = int32(T);
+  w.num_heads = int32(H);
+  w.q = q.data_ptr();
+  w.q_stride_token = T > 1 ? q.stride(0) : 0;
+  w.error_word = static_cast<int32_t*>(call.words(a[4], 1, true));
+  void* const stream = call.stream(a[5]);
+  // (outputs of a call on another stream than the current one have to be that stream's memory)
+  need((a[2] != Py_None && a[3] != Py_None) || stream == call.stream(Py_None));
+  at::Tensor out, lse;                      // those that are not given
+  if (a[2] == Py_None) {
+    out = at::empty_like(q, q.options(), c10::MemoryFormat::Contiguous);
+    w.out = out.data_ptr();
+  } else {
+    w.out = call.array(a[2], c10::kBFloat16, T * H * kDim, false);
+    need(THPVariable_Unpack(a[2]).numel() == T * H * kDim);
+  }
+  if (a[3] == Py_None) {
+    lse = at::empty({T, H}, q.options().dtype(c10::kFloat));
+    w.out_lse = static_cast<float*>(lse.data_ptr());
+  } else {
+    w.out_lse = static_cast<float*>(call.array(a[3], c10::kFloat, T * H, false));
+    need(THPVariable_Unpack(a[3]).numel() == T * H);
+  }
+  const smla_status s = unlocked([&] { return run(&w, stream); });
+  if (s != SMLA_OK) return PyLong_FromLong(s);
+  PyObject* o = out.defined() ? THPVariable_Wrap(out) : Py_NewRef(a[2]);
+  PyObject* l = lse.defined() ? THPVariable_Wrap(lse) : Py_NewRef(a[3]);
+  PyObject* both = o != nullptr && l != nullptr ? PyTuple_Pack(2, o, l) : nullptr;
+  Py_XDECREF(o);
+  Py_XDECREF(l);
+  return both;
+}
+
+// (.., window, first_tokens, num_splits, ..)
 PyObject* window_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 17, [&]() -> PyObject* {
-    Call call;
-    smla_window_args w = {};
-    const at::Tensor& q = call.tensor(a[0]);
-    need(q.scalar_type() == c10::kBFloat16 && q.dim() == 3);
-    const int64_t T = q.size(0), H = q.size(1);
-    need(T > 0 && H > 0 && q.size(2) == kDim && q.stride(2) == 1 && (H == 1 || q.stride(1) == kDim) &&
-         (T == 1 || q.stride(0) > 0));
-    w.cache = cache(call, a[1], a[2], a[3], a[4], a[6]);
-    w.workspace = call.bytes(a[5], &w.workspace_bytes);
-    w.sinks = static_cast<const float*>(call.array(a[7], c10::kFloat, H, true));
-    w.window = int32(a[8]);
-    w.first_tokens = int32(a[9]);
-    w.num_splits = int32(a[10]);
-    scale(call, a[11], &w.bmm1_scale, &w.bmm1_scale_dev);
-    scale(call, a[12], &w.bmm2_scale, &w.bmm2_scale_dev);
-    w.sum_q = int32(T);
-    w.num_heads = int32(H);
-    w.q = q.data_ptr();
-    w.q_stride_token = T > 1 ? q.stride(0) : 0;
-    w.error_word = static_cast<int32_t*>(call.words(a[15], 1, true));
-    void* const stream = call.stream(a[16]);
-    // (outputs of a call on another stream than the current one have to be that stream's memory)
-    need((a[13] != Py_None && a[14] != Py_None) || stream == call.stream(Py_None));
-    at::Tensor out, lse;                    // those that are not given
-    if (a[13] == Py_None) {
-      out = at::empty_like(q, q.options(), c10::MemoryFormat::Contiguous);
-      w.out = out.data_ptr();
-    } else {
-      w.out = call.array(a[13], c10::kBFloat16, T * H * kDim, false);
-      need(THPVariable_Unpack(a[13]).numel() == T * H * kDim);
-    }
-    if (a[14] == Py_None) {
-      lse = at::empty({T, H}, q.options().dtype(c10::kFloat));
-      w.out_lse = static_cast<float*>(lse.data_ptr());
-    } else {
-      w.out_lse = static_cast<float*>(call.array(a[14], c10::kFloat, T * H, false));
-      need(THPVariable_Unpack(a[14]).numel() == T * H);
-    }
-    const smla_status s = unlocked([&] { return smla_window_attention(&w, stream); });
-    if (s != SMLA_OK) return PyLong_FromLong(s);
-    PyObject* o = out.defined() ? THPVariable_Wrap(out) : Py_NewRef(a[13]);
-    PyObject* l = lse.defined() ? THPVariable_Wrap(lse) : Py_NewRef(a[14]);
-    PyObject* both = o != nullptr && l != nullptr ? PyTuple_Pack(2, o, l) : nullptr;
-    Py_XDECREF(o);
-    Py_XDECREF(l);
-    return both;
+    return attention<smla_window_args>(
+        a, 11,
+        [&](Call&, smla_window_args& w) {
+          w.window = int32(a[8]);
+          w.first_tokens = int32(a[9]);
+          w.num_splits = int32(a[10]);
+        },
+        smla_window_attention);
+  });
+}
+
+// (.., group_starts, prefix_lens, ..)
+PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 16, [&]() -> PyObject* {
+    return attention<smla_prefix_args>(
+        a, 10,
+        [&](Call& call, smla_prefix_args& w) {
+          w.group_starts = static_cast<const int32_t*>(call.words(a[8], 1));
+          w.num_groups = int32(THPVariable_Unpack(a[8]).numel() - 1);
+          w.prefix_lens = static_cast<const int32_t*>(call.words(a[9], w.num_groups));
+        },
+        smla_prefix_attention);
   });
 }
 
@@ -531,6 +558,7 @@ PyCFunction fast(F f) {
 
 PyMethodDef methods[] = {
     {"window_attention", fast(window_attention), METH_FASTCALL, nullptr},
+    {"prefix_attention", fast(prefix_attention), METH_FASTCALL, nullptr},
     {"append", fast(append), METH_FASTCALL, nullptr},
     {"pages_resize", fast(pages_resize), METH_FASTCALL, nullptr},
     {"pages_fork", fast(pages_fork), METH_FASTCALL, nullptr},

@@ -132,9 +132,16 @@ constexpr int kOffK = kOffQ + 4 * kQBlock;
 constexpr int kOffP = kOffK + 2 * kTileBytes;
 constexpr int kOffSmall = kOffP + 4 * kPHalf;
 
+// How the work is cut: each pair of a token and 64 heads by one CTA; some pairs in
+// splits; by the plan of a batch whose groups share prefixes (prefix_attention.cu).
+constexpr int kPairs = 0, kSplitPairs = 1, kPlanned = 2;
+
 // What a CTA works on at a time: 64 heads of a token, a range of tiles of its chunk list.
+// In a plan, also 64 (token, head) rows of a group, and lists whose first chunks are
+// another request's.
 struct Unit {
   int t, h0, heads, part, b;                      // part: its partial's number, or -1 (it writes the output)
+  int b0, first;                                  // plan: the request of the list's first chunks, their rows
   int first_chunks, window_chunk, chunks;         // list: [0, first_chunks), then from window_chunk on
   int pos, lo;                                    // last and first visible position of the window
   int tile0, tiles;
@@ -163,6 +170,7 @@ struct KernelParams {
   CUtensorMap map, out_map;
   int32_t groups;                                 // head groups
   int32_t units;
+  PrefixPlan plan;                                // kPlanned
 };
 
 __device__ __forceinline__ int chunk_at(const Unit& u, int k) {
@@ -180,8 +188,66 @@ __device__ __forceinline__ void unit_heads(const KernelParams& kp, int x, Unit* 
   u->t = pair / kp.groups;
   u->heads = min(kNH, p.H - u->h0);
 }
-template <int kShift, bool kParts>
+
+// Unit x of a plan: partial ones first, by segment (the groups' prefixes, then the
+// tokens), a segment's by piece and then by 64 of its rows, so that neighbours read
+// the same cache rows; then the tokens that are done whole.
+template <int kShift>
+__device__ __forceinline__ Unit planned_unit(const KernelParams& kp, int x, int lane) {
+  const WindowParams& p = kp.p;
+  const CacheView& c = p.c;
+  const PrefixPlan& plan = kp.plan;
+  const int per = __ldcg(plan.header + kPlanPer), parts = __ldcg(plan.header + kPlanParts);
+  Unit u;
+  u.part = x < parts ? x : -1;
+  int segment, i, blocks = kp.groups, piece = 0;
+  if (x < parts) {
+    segment = last_request(plan.groups + c.sum_q, lane, [&](int s) { return __ldcg(plan.part_of + s) <= x; });
+    i = x - __ldcg(plan.part_of + segment);
+  } else {
+    const int t = last_request(c.sum_q, lane, [&](int s) { return __ldcg(plan.whole_of + s) <= x - parts; });
+    segment = plan.groups + t;
+    i = x - parts - __ldcg(plan.whole_of + t);
+  }
+  if (segment < plan.groups) {                    // a group's prefix
+    const int4 g = __ldcg(plan.group + segment);
+    blocks = (g.z + kNH - 1) / kNH;
+    piece = i / blocks;
+    const int row = g.y * p.H + (i - piece * blocks) * kNH;
+    u.t = row / p.H;
+    u.h0 = row - u.t * p.H;
+    u.heads = min(kNH, g.z - (i - piece * blocks) * kNH);
+    u.b = u.b0 = g.x;
+    u.first = g.w;
+    u.pos = -1;
+    u.lo = 0;
+  } else {
+    const int4 r = __ldcg(plan.token + (segment - plan.groups));
+    piece = u.part >= 0 ? i / blocks : 0;
+    u.t = segment - plan.groups;
+    u.h0 = (i - piece * blocks) * kNH;
+    u.heads = min(kNH, p.H - u.h0);
+    u.b = r.x;
+    u.b0 = r.y & 0x7fffffff;
+    u.first = r.y < 0 ? 0 : r.w;                  // (a shared prefix is its group's)
+    u.pos = r.z;
+    u.lo = r.w;
+  }
+  const int last = min(u.pos, c.max_pages * c.page_size - 1);
+  if (u.pos > last && lane == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
+  u.first_chunks = (u.first + (1 << kShift) - 1) >> kShift;
+  u.window_chunk = u.lo >> kShift;
+  u.chunks = u.first_chunks + (last >= u.lo ? (last >> kShift) - u.window_chunk + 1 : 0);
+  const int tiles = (u.chunks + (kRows >> kShift) - 1) >> (7 - kShift);
+  u.tile0 = u.part >= 0 ? min(tiles, piece * per) : 0;
+  u.tiles = u.part >= 0 ? min(tiles - u.tile0, per) : tiles;
+  return u;
+}
+
+template <int kShift, int kMode>
 __device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lane) {
+  if constexpr (kMode == kPlanned) return planned_unit<kShift>(kp, x, lane);
+  constexpr bool kParts = kMode != kPairs;
   const WindowParams& p = kp.p;
   const CacheView& c = p.c;
   Unit u;
@@ -215,11 +281,15 @@ __device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lan
 
 // Page of list entry k, or -1 (past the list, or no page of the pool).  Tables are
 // read past L1, of which the tiles leave a few KB (by L1: prompts 593 us against 581).
-template <int kShift>
+template <int kMode>
+__device__ __forceinline__ const int32_t* chunk_table(const KernelParams& kp, const Unit& u, int k) {
+  return kp.p.c.bt + (kMode == kPlanned && k < u.first_chunks ? u.b0 : u.b) * kp.p.c.bt_stride;
+}
+template <int kShift, int kMode>
 __device__ __forceinline__ int chunk_page(const KernelParams& kp, const Unit& u, int k) {
   const CacheView& c = kp.p.c;
   if (k >= u.chunks) return -1;
-  const int page = __ldcg(c.bt + u.b * c.bt_stride + (uint32_t)(chunk_at(u, k) << kShift) / (uint32_t)c.page_size);
+  const int page = __ldcg(chunk_table<kMode>(kp, u, k) + (uint32_t)(chunk_at(u, k) << kShift) / (uint32_t)c.page_size);
   return page >= 0 && page < c.num_pages ? page : -1;
 }
 
@@ -281,17 +351,23 @@ __device__ __forceinline__ void split_query_pair(float a, float b, uint32_t* hi,
 // Q of 64 heads as E4M3 pairs: rows 0-63 hi, 64-127 lo, K-major with 128-byte
 // swizzle, column blocks of 128 dims.  A warp takes four heads, a lane 16 dims
 // of each.
+template <int kMode>
 __device__ __forceinline__ void split_query(const KernelParams& kp, const Unit& u, uint8_t* sq, Small& sm, int warp,
                                             int lane) {
   const WindowParams& p = kp.p;
   constexpr int kHeads = kNH / kSoftmaxWarps;
   const int h = warp * kHeads;
   const __nv_bfloat16* q = p.q + (int64_t)u.t * p.q_stride_token + (int64_t)(u.h0 + h) * kHeadDim + lane * 16;
+  auto at = [&](int i) {                          // the lane's dims of the unit's row h + i
+    if constexpr (kMode != kPlanned) return q + i * kHeadDim;
+    const int row = u.h0 + h + i, t = row / p.H;  // (a plan's rows may run through several tokens)
+    return p.q + (int64_t)(u.t + t) * p.q_stride_token + (int64_t)(row - t * p.H) * kHeadDim + lane * 16;
+  };
   const float scale = fetch_scale(p.bmm1, p.bmm1_dev) * kLog2e;
   auto load = [&](int i, uint4* v) {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      v[k] = h + i < u.heads ? fetch(reinterpret_cast<const uint4*>(q + i * kHeadDim) + k) : make_uint4(0, 0, 0, 0);
+      v[k] = h + i < u.heads ? fetch(reinterpret_cast<const uint4*>(at(i)) + k) : make_uint4(0, 0, 0, 0);
   };
   uint4 next[2][2];                               // two heads ahead
   load(0, next[0]);
@@ -323,18 +399,19 @@ __device__ __forceinline__ void split_query(const KernelParams& kp, const Unit& 
       h16 = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
       l16 = make_uint4(0, 0, 0, 0);
     }
-    uint8_t* at = sq + (lane >> 3) * kQBlock;     // column block; 16-byte chunk lane % 8 of it
-    *reinterpret_cast<uint4*>(at + sw128_offset(h + i, lane & 7)) = h16;
-    *reinterpret_cast<uint4*>(at + sw128_offset(h + i + kNH, lane & 7)) = l16;
+    uint8_t* to = sq + (lane >> 3) * kQBlock;     // column block; 16-byte chunk lane % 8 of it
+    *reinterpret_cast<uint4*>(to + sw128_offset(h + i, lane & 7)) = h16;
+    *reinterpret_cast<uint4*>(to + sw128_offset(h + i + kNH, lane & 7)) = l16;
   }
 }
 
-// kShift: log2 of a TMA box's rows; kParts: some units are splits (without their code
-// the kernel is 3 % faster where units are many: what runs once a unit comes through
-// the instruction cache every time)
-template <int kShift, bool kParts>
+// kShift: log2 of a TMA box's rows; kMode: without the code of splits the kernel is
+// 3 % faster where units are many (what runs once a unit comes through the
+// instruction cache every time)
+template <int kShift, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_constant__ KernelParams kp) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr bool kParts = kMode != kPairs;
   Small& sm = *reinterpret_cast<Small*>(smem + kOffSmall);
   const WindowParams& p = kp.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -375,15 +452,28 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
   // too, and take q_full in turn: behind a first unit without tiles the second
   // unit's may be there before the first products' warp has waited for the first
   // one's, but no third is before it has waited for both.
-  const int mine = (kp.units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int units = kMode == kPlanned ? __ldcg(kp.plan.header + kPlanUnits) : kp.units;
+  const int mine = (units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  if (kMode == kPlanned && mine <= 0) {           // (the grid is what a plan may need at most)
+    if (warp == kScoreWarp) tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------------ units and rows
     constexpr int kBoxes = kRows >> kShift;       // of a tile
     int n = 0;
     bool ok = true;
-    Unit ahead = make_unit<kShift, kParts>(kp, blockIdx.x, lane);
+    Unit ahead = make_unit<kShift, kMode>(kp, blockIdx.x, lane);
     auto prefetch_query = [&](const Unit& u) {
+      if constexpr (kMode == kPlanned) {          // rows of several tokens: one by one
+        for (int i = lane; u.tiles > 0 && i < u.heads; i += 32) {
+          const int t = (u.h0 + i) / p.H, head = u.h0 + i - t * p.H;
+          bulk_prefetch_l2(p.q + (int64_t)(u.t + t) * p.q_stride_token + (int64_t)head * kHeadDim, kHeadDim * 2);
+        }
+        __syncwarp();
+        return;
+      }
       if (u.tiles > 0 && elect_one())
         bulk_prefetch_l2(p.q + (int64_t)u.t * p.q_stride_token + (int64_t)u.h0 * kHeadDim, u.heads * kHeadDim * 2);
       __syncwarp();
@@ -403,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
       // buffer and its rows.
       auto look_up = [&](int i, int* page, int* group) {
         const int k = (u.tile0 + i) * kBoxes + lane;
-        *page = lane < kBoxes && i < u.tiles ? chunk_page<kShift>(kp, u, k) : -1;
+        *page = lane < kBoxes && i < u.tiles ? chunk_page<kShift, kMode>(kp, u, k) : -1;
         *group = (uint32_t)(chunk_at(u, min(k, u.chunks - 1)) << kShift) % (uint32_t)p.c.page_size / 8;
       };
       int page = -1, group = 0;
@@ -433,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         ok = __all_sync(0xffffffffu, good);
         n += i >= 0;
         if (i == min(1, u.tiles - 1) && x + 1 < mine) {       // the next unit and its queries' way to L2
-          ahead = make_unit<kShift, kParts>(kp, blockIdx.x + (x + 1) * gridDim.x, lane);
+          ahead = make_unit<kShift, kMode>(kp, blockIdx.x + (x + 1) * gridDim.x, lane);
           prefetch_query(ahead);
         }
       }
@@ -461,9 +551,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         for (int y = 0; y < kY; ++y) {
           const int r = y * 32 + lane, k = (u.tile0 + i) * per_tile + (r >> kShift);
           const uint32_t j = (uint32_t)((chunk_at(u, min(k, u.chunks - 1)) << kShift) + (r & ((1 << kShift) - 1)));
-          seen[y] = k < u.chunks && (int)j <= u.pos && ((int)j >= u.lo || (int)j < p.first_tokens);
+          if constexpr (kMode == kPlanned)
+            seen[y] = k < u.chunks && (k < u.first_chunks ? (int)j < u.first : (int)j >= u.lo && (int)j <= u.pos);
+          else
+            seen[y] = k < u.chunks && (int)j <= u.pos && ((int)j >= u.lo || (int)j < p.first_tokens);
           const uint32_t col = j / (uint32_t)p.c.page_size;
-          page[y] = __ldcg(p.c.bt + u.b * p.c.bt_stride + col);
+          page[y] = __ldcg(chunk_table<kMode>(kp, u, k) + col);
           off[y] = (int)((j - col * (uint32_t)p.c.page_size) / (uint32_t)p.c.block_rows);
         }
 #pragma unroll
@@ -481,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
       // otherwise stand between a tile's last product and the next one in its buffer.
       auto prefetch = [&](int i) {
         const int k = (u.tile0 + i) * per_tile + lane;
-        const int page = lane < per_tile && i < u.tiles ? chunk_page<kShift>(kp, u, k) : -1;
+        const int page = lane < per_tile && i < u.tiles ? chunk_page<kShift, kMode>(kp, u, k) : -1;
         const int group = (uint32_t)(chunk_at(u, min(k, u.chunks - 1)) << kShift) % (uint32_t)p.c.page_size / 8;
 #pragma unroll 1
         for (int y = 0; y < per_tile; ++y) {
@@ -588,17 +681,24 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     float drop = 0.f;                             // how far head threadIdx.x's reference lies below its highest place,
                                                   // counted for rows with a code of 16 or more
     int n = 0, q = 0;
+    bool failed = false;
     {
       // the first unit's queries, while its rows are looked up (a unit without any leaves them unused)
       Unit u;
-      unit_heads<kParts>(kp, blockIdx.x, &u);
-      split_query(kp, u, smem + kOffQ, sm, warp, lane);
+      if constexpr (kMode == kPlanned) {
+        failed = !warp_wait(cx, bar(sm.unit_full[0]), 0);
+        u = sm.unit[0];
+        if (failed) u.heads = 0;
+      } else {
+        unit_heads<kParts>(kp, blockIdx.x, &u);
+      }
+      split_query<kMode>(kp, u, smem + kOffQ, sm, warp, lane);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sm.q_full[0]));
       ++q;
     }
-    bool failed = !warp_wait(cx, bar(sm.unit_full[0]), 0);
+    if constexpr (kMode != kPlanned) failed = !warp_wait(cx, bar(sm.unit_full[0]), 0);
     if (threadIdx.x < kNH) sm.negref[threadIdx.x] = 0.f;
     for (int x = 0; x < mine; ++x) {
       if (named_bar_or(1, kSoftmaxThreads, failed)) break;   // also: qscale and negref are written
@@ -808,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
       if (x + 1 < mine) {
         failed |= !warp_wait(cx, bar(sm.unit_full[(x + 1) & 1]), ((x + 1) >> 1) & 1);
         if (!failed && sm.unit[(x + 1) & 1].tiles > 0) {
-          split_query(kp, sm.unit[(x + 1) & 1], smem + kOffQ, sm, warp, lane);
+          split_query<kMode>(kp, sm.unit[(x + 1) & 1], smem + kOffQ, sm, warp, lane);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(sm.q_full[q & 1]));
@@ -1070,8 +1170,7 @@ cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t
   kp.groups = (p.H + kNH - 1) / kNH;
   const int pairs = (int)((int64_t)p.c.sum_q * kp.groups);
   kp.units = p.whole + (pairs - p.whole) * p.num_splits;
-  // the highest box that pages hold whole, up to a quarter of a tile: fewer copies to issue
-  const int shift = p.c.page_size % 32 == 0 ? 5 : p.c.page_size % 16 == 0 ? 4 : 3;
+  const int shift = cache_box_shift(p.c.page_size);
   cudaError_t e = encode_cache_map(&kp.map, p.c, 1 << shift);
   if (e == cudaSuccess && p.whole > 0) e = encode_out_map(&kp.out_map, p);   // (partials are stored by threads)
   if (e != cudaSuccess) return e;
@@ -1081,14 +1180,34 @@ cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t
     return launch_overlapped(kernel, dim3((unsigned)std::min(kp.units, sms)), kThreads, kSmemBytes, stream, kp);
   };
   const bool parts = pairs > p.whole;
-  if (shift == 5) e = parts ? launch(window_kernel<5, true>) : launch(window_kernel<5, false>);
-  else if (shift == 4) e = parts ? launch(window_kernel<4, true>) : launch(window_kernel<4, false>);
-  else e = parts ? launch(window_kernel<3, true>) : launch(window_kernel<3, false>);
+  if (shift == 5) e = parts ? launch(window_kernel<5, kSplitPairs>) : launch(window_kernel<5, kPairs>);
+  else if (shift == 4) e = parts ? launch(window_kernel<4, kSplitPairs>) : launch(window_kernel<4, kPairs>);
+  else e = parts ? launch(window_kernel<3, kSplitPairs>) : launch(window_kernel<3, kPairs>);
   if (e != cudaSuccess || !parts) return e;
   const dim3 heads((unsigned)((pairs - p.whole) * (int64_t)kNH));
   if (p.num_splits > 8)                           // what one team loads at a time
     return launch_overlapped(window_merge_kernel<kMergeTeams>, heads, kMergeThreads * kMergeTeams, 0, stream, p, kp.groups);
   return launch_overlapped(window_merge_kernel<1>, heads, kMergeThreads, 0, stream, p, kp.groups);
+}
+
+cudaError_t launch_planned_attention(const WindowParams& p, const PrefixPlan& plan, int sms, cudaStream_t stream) {
+  KernelParams kp;
+  kp.p = p;
+  kp.plan = plan;
+  kp.groups = (p.H + kNH - 1) / kNH;
+  kp.units = plan.max_units;
+  const int shift = cache_box_shift(p.c.page_size);
+  cudaError_t e = encode_cache_map(&kp.map, p.c, 1 << shift);
+  if (e == cudaSuccess) e = encode_out_map(&kp.out_map, p);
+  if (e != cudaSuccess) return e;
+  auto launch = [&](auto kernel) -> cudaError_t {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (err != cudaSuccess) return err;
+    return launch_overlapped(kernel, dim3((unsigned)std::min(kp.units, sms)), kThreads, kSmemBytes, stream, kp);
+  };
+  if (shift == 5) return launch(window_kernel<5, kPlanned>);
+  if (shift == 4) return launch(window_kernel<4, kPlanned>);
+  return launch(window_kernel<3, kPlanned>);
 }
 
 }  // namespace smla

@@ -244,3 +244,41 @@ def test_slot_references_by_hand():
     out, topk = S.sparse_slots([6, 2], cum, 6, tables, 4, np.array([[1], [3]]), 8, 2, np.array([[0, 3]] * 6))
     assert out[2, :7].tolist() == [28, 29, 30, 31, 8, 9, -1] and topk.tolist() == [129, 129, 129, 128, 129, 0]
     assert out[2, 128:].tolist() == [8, -1] and out[4, 128:].tolist() == [24, -1]
+
+
+def prefix_struct():
+    a = C.SmlaPrefixArgs()
+    a.cache.rows, a.cache.scales, a.cache.block_tables, a.cache.seq_lens = 0x10000, 0x20000, 0x30000, 0x40000
+    a.cache.num_pages, a.cache.page_size, a.cache.block_rows, a.cache.max_pages, a.cache.batch = 10, 64, 16, 4, 2
+    a.sum_q, a.num_heads, a.num_groups, a.group_starts, a.prefix_lens = 4, 16, 1, 0x70000, 0x80000
+    a.q, a.out = 0x50000, 0x60000
+    return a
+
+
+@pytest.mark.parametrize("field,value,code,needle", [
+    ("sum_q", -1, INVALID, "sum_q"), ("sum_q", 5, INVALID, "multiple of batch"), ("num_heads", 129, UNSUPPORTED, "num_heads"),
+    ("num_groups", -1, INVALID, "num_groups"), ("group_starts", None, INVALID, "group_starts is required"),
+    ("prefix_lens", 0x2, INVALID, "prefix_lens must be"), ("q", 0x50008, INVALID, "q must be 16-byte"),
+    ("q_stride_token", 16 * 512 - 8, INVALID, "q_stride_token"), ("out", None, INVALID, "out is required"),
+    ("out_lse", 0x2, INVALID, "out_lse must be"), ("sinks", 0x2, INVALID, "sinks must be"),
+    ("error_word", 0x2, INVALID, "error_word must be"),
+])
+def test_prefix_errors(lib, field, value, code, needle):
+    a = prefix_struct()
+    setattr(a, field, value)
+    refused(lib.smla_prefix_attention(ctypes.byref(a), None), code, needle)
+
+
+def test_prefix_layout_and_empty_calls(lib, tmp_path):
+    src = tmp_path / "layout.c"
+    fields = [f for f, _ in C.SmlaPrefixArgs._fields_]
+    src.write_text("\n".join(["#include <stdio.h>", "#include <stddef.h>", f'#include "{os.path.join(ROOT, "include", "smla.h")}"',
+                              "int main(void) {", '  printf("%zu\\n", sizeof(smla_prefix_args));'] +
+                             [f'  printf("%zu\\n", offsetof(smla_prefix_args, {f}));' for f in fields] + ["  return 0;", "}"]))
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", str(src), "-o", str(tmp_path / "layout")], check=True)
+    out = subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True, check=True).stdout.split()
+    assert [int(v) for v in out] == [ctypes.sizeof(C.SmlaPrefixArgs)] + [getattr(C.SmlaPrefixArgs, f).offset for f in fields]
+    a = prefix_struct()
+    a.sum_q, a.q = 0, None
+    assert lib.smla_prefix_attention(ctypes.byref(a), None) == B.SMLA_OK
+    assert lib.smla_prefix_attention(None, None) == INVALID

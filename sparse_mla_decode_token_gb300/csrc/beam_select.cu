@@ -7,16 +7,19 @@
 // maximum (a word for 512 bytes).  Blocks rank like their maxima, so the K best
 // elements lie in the K best blocks: K blocks with larger maxima (or equal ones
 // and lower indices) hold K better elements than any element of another block.
-// A second kernel ranks a request's blocks and looks at the elements of the best
-// K of them only.
+// The same holds for the units of up to 32 blocks that a warp takes.  A second
+// kernel ranks a request's units, the blocks of the best K, then the elements of
+// the best K of those: some thousand keys in place of a million logits.
 //
 // Ranks are over (score, index) with the score as an unevaluated sum of two fp32
 // numbers (48 bits): what does not depend on v is computed in 64 bits, and x added
-// to it without an error.  Sums are fp32 over at most 256 terms a lane, then 64 bits over the
-// units; e^x is off by 2^-22 of itself.
+// to it without an error.  Sums are fp32 over at most 256 terms a lane, then 64 bits
+// over the units; e^x is off by 2^-22 of itself.
 //
 // What bounds it: the first kernel reads each logit once.
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "cache_ptx.cuh"
 #include "step.cuh"
@@ -71,16 +74,28 @@ __device__ __forceinline__ Row<T> logits_row(const BeamParams& p, int64_t row) {
   return {x - before, before};
 }
 
-// The lane's elements of a block (-infinity where there are none).
+// The lane's 16 bytes of a block, from element `at` of the row's base on; -infinity
+// in place of elements before its first and from `end` on.
 template <class T>
-__device__ __forceinline__ void load_lane(const Row<T>& r, int64_t at, int64_t end, float (&x)[Vec<T>::kLane]) {
-  if (at >= r.before && at + Vec<T>::kLane <= end) {
-    unpack(*reinterpret_cast<const uint4*>(r.base + at), x, r.base);
-  } else {
+__device__ __forceinline__ uint4 load_lane(const Row<T>& r, int64_t at, int64_t end) {
+  if (at >= r.before && at + Vec<T>::kLane <= end) return __ldcs(reinterpret_cast<const uint4*>(r.base + at));
+  uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < Vec<T>::kLane; ++e)
-      x[e] = at + e >= r.before && at + e < end ? element(r.base + at + e) : -INFINITY;
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      w[k] = at + k >= r.before && at + k < end ? reinterpret_cast<const uint32_t*>(r.base)[at + k] : 0xff800000u;
+    } else {
+      constexpr uint32_t none = std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
+      uint32_t v[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int64_t i = at + 2 * k + e;
+        v[e] = i >= r.before && i < end ? reinterpret_cast<const uint16_t*>(r.base)[i] : none;
+      }
+      w[k] = v[0] | v[1] << 16;
+    }
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Is the beam of this row one whose logits count?
@@ -107,26 +122,37 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamParam
     if (!live_beam(p, row)) continue;
     const Row<T> r = logits_row<T>(p, row);
     const int64_t end = (int64_t)r.before + p.vocab;
-    float m = -INFINITY, sum = 0.f, keep = -INFINITY;
-    for (int j = j0; j < j1; j += kScanBatch) {
-      float x[kScanBatch][kLane];
+    auto load = [&](int j, uint4 (&v)[kScanBatch]) {
       const int64_t at = (int64_t)j * Vec<T>::kBlock + lane * kLane;
       if (j > 0 && j + kScanBatch <= j1 && (int64_t)(j + kScanBatch) * Vec<T>::kBlock <= end) {
-        uint4 v[kScanBatch];
 #pragma unroll
         for (int k = 0; k < kScanBatch; ++k) v[k] = __ldcs(reinterpret_cast<const uint4*>(r.base + at + k * Vec<T>::kBlock));
-#pragma unroll
-        for (int k = 0; k < kScanBatch; ++k) unpack(v[k], x[k], r.base);
       } else {
+#pragma unroll 1
+        for (int k = 0; k < kScanBatch; ++k) {
+          const uint4 x = load_lane(r, at + k * Vec<T>::kBlock, j + k < j1 ? end : 0);
 #pragma unroll
-        for (int k = 0; k < kScanBatch; ++k) load_lane(r, at + k * Vec<T>::kBlock, j + k < j1 ? end : 0, x[k]);
+          for (int i = 0; i < kScanBatch; ++i)
+            if (i == k) v[i] = x;
+        }
       }
+    };
+    float m = -INFINITY, sum = 0.f, keep = -INFINITY;
+    uint4 next[kScanBatch];                       // a batch ahead, so that loads are always in flight
+    load(j0, next);
+    for (int j = j0; j < j1; j += kScanBatch) {
+      uint4 v[kScanBatch];
+#pragma unroll
+      for (int k = 0; k < kScanBatch; ++k) v[k] = next[k];
+      if (j + kScanBatch < j1) load(j + kScanBatch, next);
       float top = m;
 #pragma unroll
       for (int k = 0; k < kScanBatch; ++k) {
-        float t = x[k][0];
+        float x[kLane];
+        unpack(v[k], x, r.base);
+        float t = x[0];
 #pragma unroll
-        for (int e = 1; e < kLane; ++e) t = fmaxf(t, x[k][e]);
+        for (int e = 1; e < kLane; ++e) t = fmaxf(t, x[e]);
         t = ptx::warp_max(t);
         if (lane == j + k - j0) keep = t;
         top = fmaxf(top, t);
@@ -138,14 +164,15 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamParam
       }
 #pragma unroll
       for (int k = 0; k < kScanBatch; ++k) {
-        float t[kLane];
+        float x[kLane];
+        unpack(v[k], x, r.base);
 #pragma unroll
-        for (int e = 0; e < kLane; ++e) t[e] = fast_exp2((x[k][e] - ref) * kLog2e);
+        for (int e = 0; e < kLane; ++e) x[e] = fast_exp2((x[e] - ref) * kLog2e);
 #pragma unroll
         for (int d = 1; d < kLane; d *= 2)
 #pragma unroll
-          for (int e = 0; e < kLane; e += 2 * d) t[e] += t[e + d];
-        sum += t[0];
+          for (int e = 0; e < kLane; e += 2 * d) x[e] += x[e + d];
+        sum += x[0];
       }
     }
 #pragma unroll
@@ -163,7 +190,7 @@ struct Rank {
   uint64_t key;
   uint32_t index;
 };
-__device__ __forceinline__ bool better(const Rank& a, const Rank& b) {
+__device__ __forceinline__ bool better(Rank a, Rank b) {
   return a.key > b.key || (a.key == b.key && a.index < b.index);
 }
 
@@ -195,26 +222,32 @@ __device__ __forceinline__ uint64_t score_key(const Beam& c, float x) {
 }
 
 constexpr int kPickThreads = 1024;
-constexpr int kGroups = 256;                      // whose best ones bound the K-th best of all
-constexpr int kTile = 32768;                      // keys ranked at a time
-constexpr int kList = SMLA_MAX_BEAM_OUT * (kTile / kGroups);   // that may reach the bound
+constexpr int kGroups = 128;                      // whose best ones bound the K-th best of all
+constexpr int kTile = 8192;                       // keys ranked at a time
+constexpr int kReach = SMLA_MAX_BEAM_OUT * (kTile / kGroups);   // of them that may reach the bound
+constexpr int kGathered = kMaxUnitBlocks * SMLA_MAX_BEAM_OUT;   // keys gathered by a bound that is known
+constexpr int kDirect = 256;                      // keys ranked without a bound of their own
+static_assert(kGathered + SMLA_MAX_BEAM_OUT * (kGathered / kGroups) <= kReach, "both lists of settle()");
 
 struct Pick {
-  Rank list[kList + SMLA_MAX_BEAM_OUT];
+  uint64_t key[kReach + SMLA_MAX_BEAM_OUT];
+  uint32_t index[kReach + SMLA_MAX_BEAM_OUT];
   Rank group[kPickThreads];
-  Rank best[SMLA_MAX_BEAM_OUT], chosen[SMLA_MAX_BEAM_OUT];
+  Rank best[SMLA_MAX_BEAM_OUT];
   Rank bound;
+  uint32_t chosen[SMLA_MAX_BEAM_OUT];
   Beam beam[SMLA_MAX_BEAMS];
   bool single[SMLA_MAX_BEAMS];                    // finished: one continuation
   int count, found;
 };
 
-// The K best of n keys (any order) to sh.best, in order; sh.found of them.  Each
-// of 256 groups of keys has a best one; the K-th best of those bounds the K-th
-// best of all from below, and what reaches it is at most K groups' keys: K * n /
-// 256, and for keys in no particular order hardly more than K.  Whole CTA.
+// The keys among n (any order) that reach a lower bound of their K-th best one, to
+// the list from `to` on; sh.count of them.  Each of 128 groups of keys has a best
+// one; the K-th best of those is the bound, and at most K groups have keys that
+// reach it: K * n / 128, and for keys in no particular order hardly more than K.
+// Whole CTA.
 template <class F>
-__device__ __forceinline__ void pick_tile(Pick& sh, int keep, int n, Rank* list, F key) {
+__device__ __forceinline__ void reach(Pick& sh, int keep, int n, int to, F key) {
   const Rank none = {0, 0xffffffffu};
   Rank mine = none;
   for (int i = threadIdx.x; i < n; i += kPickThreads) {
@@ -227,55 +260,113 @@ __device__ __forceinline__ void pick_tile(Pick& sh, int keep, int n, Rank* list,
     sh.bound = none;
   }
   __syncthreads();
-  if (threadIdx.x < kGroups) {
+  // eight threads a group: its best one, and a share of the comparisons with the others
+  constexpr int kEach = kPickThreads / kGroups;
+  const int group = threadIdx.x / kEach, lane = threadIdx.x % kEach;
+  mine = sh.group[lane * kGroups + group];
 #pragma unroll
-    for (int k = 1; k < kPickThreads / kGroups; ++k) {
-      const Rank r = sh.group[threadIdx.x + k * kGroups];
-      if (better(r, mine)) mine = r;
-    }
+  for (int o = 1; o < kEach; o *= 2) {
+    const Rank r = {__shfl_xor_sync(0xffffffffu, mine.key, o), __shfl_xor_sync(0xffffffffu, mine.index, o)};
+    if (better(r, mine)) mine = r;
   }
   __syncthreads();
-  if (threadIdx.x < kGroups) sh.group[threadIdx.x] = mine;
+  if (lane == 0) sh.group[group] = mine;
   __syncthreads();
-  if (threadIdx.x < kGroups && mine.key != 0) {
-    int rank = 0;
-    for (int k = 0; k < kGroups; ++k) rank += better(sh.group[k], mine);
-    if (rank == keep - 1) sh.bound = mine;
-  }
+  int rank = 0;
+#pragma unroll
+  for (int k = lane; k < kGroups; k += kEach) rank += better(sh.group[k], mine);
+#pragma unroll
+  for (int o = 1; o < kEach; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+  if (lane == 0 && rank == keep - 1 && mine.key != 0) sh.bound = mine;
   __syncthreads();
   const Rank bound = sh.bound;
   for (int i = threadIdx.x; i < n; i += kPickThreads) {
     const Rank r = key(i);
-    if (r.key != 0 && !better(bound, r)) list[atomicAdd(&sh.count, 1)] = r;
+    if (r.key != 0 && !better(bound, r)) {
+      const int at = to + atomicAdd(&sh.count, 1);
+      sh.key[at] = r.key;
+      sh.index[at] = r.index;
+    }
   }
   __syncthreads();
 }
 
-// Ranks the `count` keys of the list by counting the better ones of each.
-__device__ __forceinline__ void rank_list(Pick& sh, int keep, const Rank* list, int count) {
-  for (int i = threadIdx.x; i < count; i += kPickThreads) {
-    const Rank mine = list[i];
+// The K best of the list's entries [from, from + count), in order, to sh.best: each
+// entry's rank is the number of better ones, counted by eight threads.
+__device__ __forceinline__ void rank_list(Pick& sh, int keep, int from, int count) {
+  constexpr int kEach = 8;
+  const int lane = threadIdx.x % kEach;
+  for (int base = 0; base < count; base += kPickThreads / kEach) {
+    const int i = base + (int)threadIdx.x / kEach;
+    const Rank mine = {sh.key[from + min(i, count - 1)], sh.index[from + min(i, count - 1)]};
     int rank = 0;
-    for (int k = 0; k < count && rank < keep; ++k) rank += better(list[k], mine);
-    if (rank < keep) sh.best[rank] = mine;
+    for (int k = lane; k < count; k += kEach) rank += better({sh.key[from + k], sh.index[from + k]}, mine);
+#pragma unroll
+    for (int o = 1; o < kEach; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (lane == 0 && i < count && rank < keep) sh.best[rank] = mine;
   }
+  if (threadIdx.x == 0) sh.found = min(keep, count);
   __syncthreads();
 }
 
+// The K best of n keys, a tile at a time beside the best ones so far.
 template <class F>
 __device__ __forceinline__ void pick(Pick& sh, int keep, int64_t n, F key) {
   int found = 0;
-  for (int64_t base = 0; base < n || base == 0; base += kTile) {
-    const int tile = (int)min((int64_t)kTile, n - base);
-    pick_tile(sh, keep, tile, sh.list, [&](int i) { return key(base + i); });
-    int count = sh.count;
-    if (threadIdx.x < found) sh.list[count + threadIdx.x] = sh.best[threadIdx.x];
+  for (int64_t base = 0; base < n; base += kTile) {
+    reach(sh, keep, (int)min((int64_t)kTile, n - base), 0, [&](int i) { return key(base + i); });
+    const int count = sh.count;
+    if (threadIdx.x < found) {
+      sh.key[count + threadIdx.x] = sh.best[threadIdx.x].key;
+      sh.index[count + threadIdx.x] = sh.best[threadIdx.x].index;
+    }
     __syncthreads();
-    count += found;
-    rank_list(sh, keep, sh.list, count);
-    found = min(keep, count);
+    rank_list(sh, keep, 0, count + found);
+    found = sh.found;
   }
   if (threadIdx.x == 0) sh.found = found;
+  __syncthreads();
+}
+
+// The K best of n keys of which at least K are `least` or more, if it is not 0: those
+// are gathered, and what is left to rank is little more than K, but for ties.
+template <class F>
+__device__ __forceinline__ void pick_from(Pick& sh, int keep, int n, uint64_t least, F key) {
+  if (threadIdx.x == 0) sh.count = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kPickThreads) {
+    const Rank r = key(i);
+    if (r.key != 0 && r.key >= least) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kGathered) {
+        sh.key[at] = r.key;
+        sh.index[at] = r.index;
+      }
+    }
+  }
+  __syncthreads();
+  const int count = sh.count;
+  __syncthreads();
+  if (count <= kDirect) {
+    rank_list(sh, keep, 0, count);
+  } else if (count <= kGathered) {
+    reach(sh, keep, count, kGathered, [&](int i) -> Rank { return {sh.key[i], sh.index[i]}; });
+    rank_list(sh, keep, kGathered, sh.count);
+  } else {
+    pick(sh, keep, n, [&](int64_t i) { return key((int)i); });
+  }
+}
+
+// sh.best's indices in rising order to sh.chosen; so that positions in what they
+// stand for compare like (beam, token).
+__device__ __forceinline__ void sort_chosen(Pick& sh) {
+  const int found = sh.found;
+  if (threadIdx.x < found) {
+    const uint32_t mine = sh.best[threadIdx.x].index;
+    int at = 0;
+    for (int k = 0; k < found; ++k) at += sh.best[k].index < mine;
+    sh.chosen[at] = mine;
+  }
   __syncthreads();
 }
 
@@ -321,49 +412,48 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
   }
   __syncthreads();
 
-  // the best blocks
-  const float* top = p.block_max + row0 * p.plan.blocks;
-  pick(sh, p.num_out, (int64_t)p.beams * p.plan.blocks, [&](int64_t at) -> Rank {
-    const int i = (int)(at / p.plan.blocks);
+  // the best units, the best blocks of those, the best elements of those
+  const int keep = p.num_out, per = p.plan.unit_blocks, units = p.plan.units;
+  const float2* part = p.partial + row0 * units;
+  pick(sh, keep, (int64_t)p.beams * units, [&](int64_t at) -> Rank {
+    const uint32_t i = (uint32_t)at / (uint32_t)units;
     const Beam c = sh.beam[i];
-    if (isnan(c.hi)) return {0, 0xffffffffu};
-    if (sh.single[i]) return {at % p.plan.blocks == 0 ? score_key(c, 0.f) : 0, (uint32_t)at};
-    return {score_key(c, fetch(top + at)), (uint32_t)at};
+    if (isnan(c.hi)) return {0, 0};
+    if (sh.single[i]) return {at == (int64_t)i * units ? score_key(c, 0.f) : 0, (uint32_t)at};
+    return {score_key(c, fetch(&part[at].x)), (uint32_t)at};
   });
-  const int blocks = sh.found;
-  const Rank worst = blocks == p.num_out ? sh.best[blocks - 1] : Rank{0, 0xffffffffu};
-  // in order of their indices, so that their elements' indices compare like (beam, token)
-  if (threadIdx.x < blocks) {
-    const Rank mine = sh.best[threadIdx.x];
-    int at = 0;
-    for (int k = 0; k < blocks; ++k) at += sh.best[k].index < mine.index;
-    sh.chosen[at] = mine;
-  }
-  __syncthreads();
-
-  // the best elements of those blocks
+  uint64_t least = sh.found == keep ? sh.best[keep - 1].key : 0;
+  sort_chosen(sh);
+  const float* top = p.block_max + row0 * p.plan.blocks;
+  pick_from(sh, keep, sh.found * per, least, [&](int at) -> Rank {
+    const uint32_t unit = sh.chosen[at / per], i = unit / (uint32_t)units;
+    const int j = (int)(unit - i * units) * per + at % per;
+    Rank r = {0, i * (uint32_t)p.plan.blocks + j};
+    if (sh.single[i]) r.key = j == 0 ? score_key(sh.beam[i], 0.f) : 0;
+    else if (j < p.plan.blocks) r.key = score_key(sh.beam[i], fetch(top + r.index));
+    return r;
+  });
+  least = sh.found == keep ? sh.best[keep - 1].key : 0;
+  sort_chosen(sh);
   constexpr int kBlock = Vec<T>::kBlock;
-  pick(sh, p.num_out, (int64_t)blocks * kBlock, [&](int64_t at) -> Rank {
-    const int k = (int)at / kBlock, e = (int)at % kBlock;
-    const uint32_t block = sh.chosen[k].index;
-    const int i = (int)(block / (uint32_t)p.plan.blocks);
-    const Beam c = sh.beam[i];
+  pick_from(sh, keep, sh.found * kBlock, least, [&](int at) -> Rank {
+    const uint32_t block = sh.chosen[at / kBlock], i = block / (uint32_t)p.plan.blocks;
     Rank r = {0, (uint32_t)at};
     if (sh.single[i]) {
-      if (e == 0) r.key = score_key(c, 0.f);
+      if (at % kBlock == 0) r.key = score_key(sh.beam[i], 0.f);
     } else {
       const Row<T> row = logits_row<T>(p, row0 + i);
-      const int64_t j = (int64_t)(block % (uint32_t)p.plan.blocks) * kBlock + e;
-      if (j >= row.before && j < (int64_t)row.before + p.vocab) r.key = score_key(c, element(row.base + j));
+      const int64_t j = (int64_t)(block - i * p.plan.blocks) * kBlock + at % kBlock;
+      if (j >= row.before && j < (int64_t)row.before + p.vocab) r.key = score_key(sh.beam[i], element(row.base + j));
     }
-    return r.key >= worst.key ? r : Rank{0, (uint32_t)at};
+    return r;
   });
   if (threadIdx.x < p.num_out) {
     float score = -INFINITY;
     int parent = -1, token = -1;
     if (threadIdx.x < sh.found) {
       const Rank r = sh.best[threadIdx.x];
-      const uint32_t block = sh.chosen[r.index / kBlock].index;
+      const uint32_t block = sh.chosen[r.index / kBlock];
       const int i = (int)(block / (uint32_t)p.plan.blocks);
       score = unordered((uint32_t)(r.key >> 32));
       parent = (int)(row0 + i);

@@ -106,22 +106,32 @@ constexpr int kMaxWindowSplits = 256;
 __host__ __device__ inline int cache_box_shift(int page_size) { return page_size % 32 == 0 ? 5 : page_size % 16 == 0 ? 4 : 3; }
 
 // Plan of a batch whose groups share prefixes, made on the device (prefix_attention.cu).
-constexpr int kPlanPer = 0, kPlanParts = 1, kPlanUnits = 2, kPlanPieces = 3, kPlanHeader = 16;
+// Units are blocks of 64 (token, head) rows: those of the groups' shared prefixes,
+// then those of the tokens, all laid end to end by cost and cut into a share for each
+// SM.  Partials are numbered: two for each share (a block that its beginning, or
+// only its end, cuts), then for shared prefixes and their tokens by unit and share.
+constexpr int kPlanTile = 4, kPlanUnit = 11;      // cost of a tile; of a unit's query, sums and results
+constexpr int kMaxShares = 256;
+constexpr int kFewPieces = 16;
+__host__ __device__ inline int64_t plan_cost(int tiles) { return kPlanUnit + (int64_t)(tiles > 0 ? tiles : 1) * kPlanTile; }
 struct PrefixPlan {
-  int32_t groups, max_parts, max_units;
+  int32_t groups, shares;
   const int32_t* group_starts;          // [groups + 1] first request of each
   const int32_t* prefix_lens;           // [groups]
-  int32_t* header;                      // tiles of a piece, partial units, all units, most pieces of a list
-  int32_t* part_of;                     // [groups + T + 1] first partial unit of a group's prefix, of a token
-  int32_t* whole_of;                    // [T + 1] first of the units that are no partial ones
+  int64_t* share_cost;                  // [1]
+  uint64_t* share_by;                   // [1] 2^64 / share_cost, rounded up
+  int32_t* few;                         // [1] no block in more than kFewPieces
+  int64_t* cost_of;                     // [groups + T + 1] where a group's prefix, a token begins
+  int32_t* unit_of;                     // [groups + T + 1] its first unit
+  int32_t* shared_of;                   // [groups + T] the units of shared prefixes and their tokens before it
+  int4* share;                          // [shares] first unit, units, the first one's segment
   int4* group;                          // [groups] first request, first token, (token, head) rows, prefix (0: not shared)
-  int4* token;                          // [T] request, its group's first one (sign: the prefix is the group's), position, prefix
-  int4* request;                        // [batch] tokens, tiles of the last one, group or -1, the second word of its tokens
+  int4* token;                          // [T] request, its group's first one (or sign and group: shared), position, prefix
   int32_t* limit;                       // [groups] positions that all the group's tokens see
 };
 
-cudaError_t launch_planned_attention(const WindowParams& p, const PrefixPlan& plan, int sms, cudaStream_t stream);
-cudaError_t launch_prefix_attention(const WindowParams& p, const PrefixPlan& plan, int sms, cudaStream_t stream);
+cudaError_t launch_planned_attention(const WindowParams& p, const PrefixPlan& plan, cudaStream_t stream);
+cudaError_t launch_prefix_attention(const WindowParams& p, const PrefixPlan& plan, cudaStream_t stream);
 
 cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t stream);
 

@@ -198,22 +198,21 @@ smla_status check_prefix(const smla_prefix_args* a) {
   return SMLA_OK;
 }
 
-// Most units that a plan on the device may need, and the workspace's parts: fp32
-// partials, then the plan.  A shared prefix takes at least a partial for each 64
-// rows of its group and each token; what more may be split is bounded here, at
-// four pieces for each SM.
+// The workspace's parts: fp32 partials (two for each SM; where prefixes can be
+// shared, one more for each block of 64 rows and each cut through them), then the plan.
 struct PrefixLayout {
-  int64_t parts, units;
-  size_t lse, header, part_of, whole_of, group, token, request, limit, bytes;
+  int64_t parts;
+  int shares;
+  size_t lse, header, cost_of, unit_of, shared_of, share, group, token, limit, bytes;
 };
 PrefixLayout prefix_layout(const smla_prefix_args* a, int sms) {
   const int64_t T = a->sum_q, heads = (a->num_heads + kWindowHeads - 1) / kWindowHeads;
   PrefixLayout l;
-  l.parts = 4 * (int64_t)sms;
+  l.shares = std::min(sms, kMaxShares);
+  l.parts = 2 * (int64_t)l.shares;
   if (a->num_heads % kWindowHeads != 0 && a->num_groups > 0)
-    l.parts += T * heads + T * a->num_heads / kWindowHeads + a->num_groups;
-  l.units = l.parts + T * heads;
-  const size_t rows = (size_t)l.parts * kWindowHeads;
+    l.parts += T * heads + T * a->num_heads / kWindowHeads + a->num_groups + l.shares;
+  const size_t rows = (size_t)l.parts * kWindowHeads, segments = (size_t)a->num_groups + T;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t from = at;
@@ -222,12 +221,13 @@ PrefixLayout prefix_layout(const smla_prefix_args* a, int sms) {
   };
   take(rows * kHeadDim * sizeof(float));
   l.lse = take(rows * sizeof(float));
-  l.header = take(kPlanHeader * sizeof(int32_t));
-  l.part_of = take((a->num_groups + T + 1) * sizeof(int32_t));
-  l.whole_of = take((T + 1) * sizeof(int32_t));
+  l.header = take(2 * sizeof(int64_t) + sizeof(int32_t));
+  l.cost_of = take((segments + 1) * sizeof(int64_t));
+  l.unit_of = take((segments + 1) * sizeof(int32_t));
+  l.shared_of = take(segments * sizeof(int32_t));
+  l.share = take((size_t)l.shares * sizeof(int4));
   l.group = take((size_t)a->num_groups * sizeof(int4));
   l.token = take((size_t)T * sizeof(int4));
-  l.request = take((size_t)a->cache.batch * sizeof(int4));
   l.limit = take((size_t)a->num_groups * sizeof(int32_t));
   l.bytes = at;
   return l;
@@ -379,7 +379,8 @@ smla_status smla_prefix_attention(const smla_prefix_args* a, void* stream) {
   int sms = 0;
   SMLA_TRY(current_sms(&sms));
   const PrefixLayout l = prefix_layout(a, sms);
-  if (l.units > 0x7fffffff / kWindowHeads) return fail(SMLA_ERR_UNSUPPORTED, "%lld units are too many", (long long)l.units);
+  if (l.parts + 2 * (int64_t)a->sum_q > 0x7fffffff / kWindowHeads)
+    return fail(SMLA_ERR_UNSUPPORTED, "%d tokens are too many", a->sum_q);
   SMLA_TRY(need_workspace(a->workspace, a->workspace_bytes, l.bytes));
   WindowParams p = attention_params(a);
   char* const ws = static_cast<char*>(a->workspace);
@@ -388,18 +389,20 @@ smla_status smla_prefix_attention(const smla_prefix_args* a, void* stream) {
   PrefixPlan plan;
   memset(&plan, 0, sizeof(plan));
   plan.groups = a->num_groups;
-  plan.max_parts = (int32_t)l.parts;
-  plan.max_units = (int32_t)l.units;
+  plan.shares = l.shares;
   plan.group_starts = a->group_starts;
   plan.prefix_lens = a->prefix_lens;
-  plan.header = reinterpret_cast<int32_t*>(ws + l.header);
-  plan.part_of = reinterpret_cast<int32_t*>(ws + l.part_of);
-  plan.whole_of = reinterpret_cast<int32_t*>(ws + l.whole_of);
+  plan.share_cost = reinterpret_cast<int64_t*>(ws + l.header);
+  plan.share_by = reinterpret_cast<uint64_t*>(ws + l.header + sizeof(int64_t));
+  plan.few = reinterpret_cast<int32_t*>(ws + l.header + 2 * sizeof(int64_t));
+  plan.cost_of = reinterpret_cast<int64_t*>(ws + l.cost_of);
+  plan.unit_of = reinterpret_cast<int32_t*>(ws + l.unit_of);
+  plan.shared_of = reinterpret_cast<int32_t*>(ws + l.shared_of);
+  plan.share = reinterpret_cast<int4*>(ws + l.share);
   plan.group = reinterpret_cast<int4*>(ws + l.group);
   plan.token = reinterpret_cast<int4*>(ws + l.token);
-  plan.request = reinterpret_cast<int4*>(ws + l.request);
   plan.limit = reinterpret_cast<int32_t*>(ws + l.limit);
-  return launched("prefix attention", launch_prefix_attention(p, plan, sms, static_cast<cudaStream_t>(stream)));
+  return launched("prefix attention", launch_prefix_attention(p, plan, static_cast<cudaStream_t>(stream)));
 }
 
 smla_status smla_cache_append(const smla_append_args* a, void* stream) {

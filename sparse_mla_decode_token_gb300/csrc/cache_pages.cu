@@ -567,9 +567,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_reorder_phase_kernel(co
 // --------------------------------------------------------- shared prefix
 // Group g's rows with tokens hold `columns` whole pages each at least; the
 // first column where one of them differs from the first ends the prefix.
-// A CTA a group, its warps a row each, 128 columns at a time from the front, so
-// that what lies behind an early difference is hardly read.
-constexpr int kPrefixThreads = 512;
+// A CTA a group, its warps 256 columns of a row at a time, the front ones first,
+// so that what lies behind an early difference is hardly read.
+constexpr int kPrefixThreads = 1024;
+constexpr int kPrefixPer = 8;                         // columns a lane takes at a time
 __global__ void __launch_bounds__(kPrefixThreads)
 pages_shared_prefix_kernel(const PagesParams p, const int32_t* group_starts, int32_t* prefix_lens) {
   __shared__ int s_columns, s_first;
@@ -595,27 +596,29 @@ pages_shared_prefix_kernel(const PagesParams p, const int32_t* group_starts, int
   const int first = s_first, columns = s_columns;
   if (first < p.rows) {
     const int32_t* lead = p.bt + (int64_t)first * p.bt_stride;
-    for (int b = first + warp; b < hi; b += kPrefixThreads / 32) {
+    const int members = hi - first - 1;               // rows to compare with the first one
+    const int64_t all = (int64_t)members * ((columns + 32 * kPrefixPer - 1) / (32 * kPrefixPer));
+    for (int64_t i = warp; i < all; i += kPrefixThreads / 32) {
+      const int c0 = (int)(i / members) * 32 * kPrefixPer, b = first + 1 + (int)(i % members);
+      if (c0 >= __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_columns), 0)) break;
       if (clamped_len(p, fetch(p.lens + b)) == 0) continue;
       const int32_t* row = p.bt + (int64_t)b * p.bt_stride;
-      for (int c0 = 0; c0 < columns; c0 += 128) {
-        if (c0 >= __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_columns), 0)) break;
-        int miss = columns;
+      int page[kPrefixPer], other[kPrefixPer];
 #pragma unroll
-        for (int k = 3; k >= 0; --k) {
-          const int c = c0 + k * 32 + lane;
-          if (c < columns) {
-            const int page = __ldcg(lead + c);
-            if (page < 0 || __ldcg(row + c) != page) miss = c;
-          }
-        }
-        miss = __reduce_min_sync(0xffffffffu, miss);
-        if (miss < columns) {
-          if (lane == 0) atomicMin(&s_columns, miss);
-          break;
-        }
+      for (int k = 0; k < kPrefixPer; ++k) {
+        const int c = c0 + k * 32 + lane;
+        page[k] = c < columns ? __ldcg(lead + c) : 0;
+        other[k] = c < columns ? __ldcg(row + c) : 0;
       }
+      int miss = columns;
+#pragma unroll
+      for (int k = kPrefixPer - 1; k >= 0; --k)
+        if (other[k] != page[k]) miss = c0 + k * 32 + lane;
+      miss = __reduce_min_sync(0xffffffffu, miss);
+      if (miss < columns && lane == 0) atomicMin(&s_columns, miss);
     }
+    for (int c = threadIdx.x; c < columns; c += kPrefixThreads)
+      if (__ldcg(lead + c) < 0) atomicMin(&s_columns, c);
   }
   __syncthreads();
   if (threadIdx.x == 0) prefix_lens[blockIdx.x] = first < p.rows ? s_columns * p.page_size : 0;

@@ -13,10 +13,11 @@
 // token, there is nothing to save, and its tokens go through one list of rows, the
 // prefix through the table of the group's first request.
 //
-// The lengths are on the device, so the plan is made there: one CTA finds each
-// group's prefix, chooses the tiles of a piece out of 32 candidates (a warp each;
-// a turn of the SMs costs its largest pieces and 2.8 tiles' time for each unit's
-// query, sums and results) and numbers the units.
+// The lengths are on the device, so the plan is made there, by one CTA.  Each block
+// of 64 rows costs 2.75 tiles' time for its query, sums and results and one for each
+// tile; all blocks laid end to end are cut into equal shares, one for each SM (a
+// tile is the CTA's in whose share it begins).  A block that a cut goes through is
+// given in pieces and merged.
 #include <algorithm>
 
 #include "cache.cuh"
@@ -28,8 +29,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr float kUnitTiles = 2.8f;                // what a unit costs beside its tiles, in tiles
-constexpr int kMaxPieces = 480;                   // of one list
+constexpr int kNearGroups = 512, kNearSegments = 2048;   // of which the plan's arrays lie in shared memory
 
 __device__ __forceinline__ void flag(int32_t* err, int bit) {
   if (err != nullptr) atomicOr(err, bit);
@@ -43,15 +43,16 @@ __device__ __forceinline__ int tiles_of(int first, int lo, int pos, int cap, int
   return (chunks + (kWindowTile >> shift) - 1) >> (7 - shift);
 }
 
-// The group of request b, or -1 (starts in order).
-__device__ __forceinline__ int group_of(const PrefixPlan& plan, int b) {
-  int lo = -1, hi = plan.groups - 1;              // the last group that begins at or before b
+// The last s of 0 .. n - 1 with before(s); -1 if there is none.
+template <class F>
+__device__ __forceinline__ int last_of(int n, F before) {
+  int lo = -1, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (fetch(plan.group_starts + mid) <= b) lo = mid;
+    if (before(mid)) lo = mid;
     else hi = mid - 1;
   }
-  return lo >= 0 && b < fetch(plan.group_starts + lo + 1) ? lo : -1;
+  return lo;
 }
 
 struct Request {
@@ -67,259 +68,284 @@ __device__ __forceinline__ Request request_of(const CacheView& c, int b) {
   return r;
 }
 
-__global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParams p, const PrefixPlan plan, int shift, int sms) {
-  __shared__ float s_cost[kWarps];
-  __shared__ int64_t s_scan[kWarps];
-  __shared__ int s_most, s_pieces;
-  const CacheView& c = p.c;
+// a and b become the sums of those of the threads before; *all_a, *all_b of all.
+struct Scan {
+  int64_t a[kWarps], b[kWarps];
+};
+__device__ __forceinline__ void scan(Scan& sh, int64_t& a, int64_t& b, int64_t* all_a, int64_t* all_b) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int heads = blocks_of(p.H), cap = c.max_pages * c.page_size, T = c.sum_q;
+  const int64_t a0 = a, b0 = b;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, a, d), y = __shfl_up_sync(0xffffffffu, b, d);
+    if (lane >= d) a += x, b += y;
+  }
+  if (lane == 31) sh.a[warp] = a, sh.b[warp] = b;
+  __syncthreads();
+  int64_t wa = sh.a[lane], wb = sh.b[lane];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, wa, d), y = __shfl_up_sync(0xffffffffu, wb, d);
+    if (lane >= d) wa += x, wb += y;
+  }
+  *all_a = __shfl_sync(0xffffffffu, wa, 31);
+  *all_b = __shfl_sync(0xffffffffu, wb, 31);
+  const int64_t before_a = __shfl_sync(0xffffffffu, wa, max(warp - 1, 0)), before_b = __shfl_sync(0xffffffffu, wb, max(warp - 1, 0));
+  a += (warp > 0 ? before_a : 0) - a0;
+  b += (warp > 0 ? before_b : 0) - b0;
+  __syncthreads();
+}
+
+// at / share_cost: exact by multiplication where at * share_cost < 2^64 (`by` is 0 where that is not sure)
+__device__ __forceinline__ int share_of(int64_t at, int64_t share_cost, uint64_t by) {
+  return by != 0 ? (int)__umul64hi((uint64_t)at, by) : (int)(at / share_cost);
+}
+
+__global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParams p, const PrefixPlan plan, int shift) {
+  __shared__ int s_starts[kNearGroups + 1], s_limit[kNearGroups];
+  __shared__ int4 s_group[kNearGroups];
+  __shared__ int64_t s_cost[kNearSegments + 1];
+  __shared__ int s_unit[kNearSegments + 1];
+  __shared__ int s_first[kMaxShares + 1], s_end[kMaxShares + 1], s_segment[kMaxShares + 1];
+  __shared__ Scan s_scan;
+  __shared__ int s_most;
+  const CacheView& c = p.c;
+  const int lane = threadIdx.x & 31;
+  const int sms = plan.shares, heads = blocks_of(p.H), cap = c.max_pages * c.page_size, T = c.sum_q, segments = plan.groups + T;
   await_prior_kernel();
   admit_next_kernel();
+  const bool near = plan.groups <= kNearGroups;
+  const int* const starts = near ? s_starts : plan.group_starts;
+  int* const limit = near ? s_limit : plan.limit;
 
   // what is out of order shares nothing
   bool bad = false, unordered = false;
   for (int g = threadIdx.x; g < plan.groups; g += kThreads) {
     const int lo = fetch(plan.group_starts + g), hi = fetch(plan.group_starts + g + 1);
     bad |= lo < 0 || hi < lo || hi > c.batch;
-    plan.limit[g] = 0x7fffffff;
+    limit[g] = 0x7fffffff;
+    if (near) {
+      s_starts[g] = lo;
+      s_starts[g + 1] = hi;                       // (both threads that write it write the same)
+    }
   }
   if (c.cum != nullptr)
     for (int b = threadIdx.x; b < c.batch; b += kThreads) unordered |= fetch(c.cum + b) > fetch(c.cum + b + 1);
   for (int t = threadIdx.x; t < T; t += kThreads) plan.token[t] = make_int4(-1, 0, -1, 0);
-  if (threadIdx.x == 0) s_most = s_pieces = 0;
+  if (threadIdx.x == 0) s_most = 1;
   if (bad) flag(p.err, SMLA_DEVERR_PAGE_STATE);
-  bad = __syncthreads_or(bad);
-  unordered = __syncthreads_or(unordered);
-  const int groups = bad || unordered ? 0 : plan.groups;
+  const int groups = __syncthreads_or(bad || unordered) ? 0 : plan.groups;
+  auto group_of = [&](int b) {
+    const int g = last_of(groups, [&](int x) { return starts[x] <= b; });
+    return g >= 0 && b < starts[g + 1] ? g : -1;
+  };
 
   // the positions that all of a group's tokens see
   for (int b = threadIdx.x; b < c.batch && groups > 0; b += kThreads) {
     const Request r = request_of(c, b);
-    const int g = r.t1 > r.t0 ? group_of(plan, b) : -1;
-    if (g >= 0) atomicMin(plan.limit + g, max(0, r.len - r.count + 1));
+    const int g = r.t1 > r.t0 ? group_of(b) : -1;
+    if (g >= 0) atomicMin(limit + g, max(0, r.len - r.count + 1));
   }
   __syncthreads();
   for (int g = threadIdx.x; g < plan.groups; g += kThreads) {
     int4 v = make_int4(0, 0, 0, 0);
     int prefix = 0;
-    if (groups > 0) {
-      const int lo = fetch(plan.group_starts + g), hi = fetch(plan.group_starts + g + 1);
-      const int limit = __ldcg(plan.limit + g);
-      if (limit != 0x7fffffff) {
-        prefix = min(min(max(fetch(plan.prefix_lens + g), 0), limit), cap);
-        int t0 = lo * (T / c.batch), t1 = hi * (T / c.batch);
-        if (c.cum != nullptr) t0 = fetch(c.cum + lo), t1 = fetch(c.cum + hi);
-        t0 = min(max(t0, 0), T), t1 = min(max(t1, t0), T);
-        const int tiles = tiles_of(prefix, 0, -1, cap, shift), blocks = blocks_of((t1 - t0) * p.H);
-        v = make_int4(lo, t0, (t1 - t0) * p.H, 0);
-        if ((int64_t)((t1 - t0) * heads - blocks) * tiles > 3 * (int64_t)blocks) {
-          v.w = prefix;
-          atomicMax(&s_most, tiles);
-        }
+    if (groups > 0 && limit[g] != 0x7fffffff) {
+      const int lo = starts[g], hi = starts[g + 1];
+      prefix = min(min(max(fetch(plan.prefix_lens + g), 0), limit[g]), cap);
+      int t0 = lo * (T / c.batch), t1 = hi * (T / c.batch);
+      if (c.cum != nullptr) t0 = fetch(c.cum + lo), t1 = fetch(c.cum + hi);
+      t0 = min(max(t0, 0), T), t1 = min(max(t1, t0), T);
+      const int tiles = tiles_of(prefix, 0, -1, cap, shift), blocks = blocks_of((t1 - t0) * p.H);
+      v = make_int4(lo, t0, (t1 - t0) * p.H, 0);
+      if ((int64_t)((t1 - t0) * heads - blocks) * tiles > 3 * (int64_t)blocks) {
+        v.w = prefix;
+        atomicMax(&s_most, tiles);
       }
     }
     plan.group[g] = v;
-    plan.limit[g] = prefix;
+    if (near) s_group[g] = v;
+    limit[g] = prefix;
   }
   __syncthreads();
+  const int4* const group = near ? s_group : plan.group;
 
-  // the requests and their tokens
+  // the requests' tokens
   for (int base = 0; base < c.batch; base += kThreads) {
     const int b = base + threadIdx.x;
     Request r = {0, 0, 0, 0, 0};
-    int g = -1, prefix = 0, from = 0;
+    int prefix = 0, from = 0;
     if (b < c.batch) {
       r = request_of(c, b);
       if (r.t1 > r.t0) {
-        g = groups > 0 ? group_of(plan, b) : -1;
-        prefix = g >= 0 ? __ldcg(plan.limit + g) : 0;
-        const int4 v = g >= 0 ? __ldcg(plan.group + g) : make_int4(b, 0, 0, 0);
-        from = v.w > 0 ? v.x | (int)0x80000000 : v.x;
+        const int g = group_of(b);
+        prefix = g >= 0 ? limit[g] : 0;
+        const int4 v = g >= 0 ? group[g] : make_int4(b, 0, 0, 0);
+        from = v.w > 0 ? g | (int)0x80000000 : v.x;
+        atomicMax(&s_most, tiles_of(from < 0 ? 0 : prefix, prefix, r.len - r.count + (r.t1 - 1 - r.first), cap, shift));
       }
-      const int tiles = tiles_of(from < 0 ? 0 : prefix, prefix, r.len - r.count + (r.t1 - 1 - r.first), cap, shift);
-      plan.request[b] = make_int4(r.t1 - r.t0, r.t1 > r.t0 ? tiles : 0, g, from);
-      if (r.t1 > r.t0) atomicMax(&s_most, tiles);
     }
     const int pos0 = r.len - r.count - r.first;
     const bool many = r.t1 - r.t0 > 8;
     if (!many)
       for (int t = r.t0; t < r.t1; ++t) plan.token[t] = make_int4(b, from, pos0 + t, prefix);
     for (uint32_t left = __ballot_sync(0xffffffffu, many); left != 0; left &= left - 1) {
-      const int from_lane = __ffs(left) - 1;
-      const int t0 = __shfl_sync(0xffffffffu, r.t0, from_lane), t1 = __shfl_sync(0xffffffffu, r.t1, from_lane);
-      const int4 v = make_int4(__shfl_sync(0xffffffffu, b, from_lane), __shfl_sync(0xffffffffu, from, from_lane),
-                               __shfl_sync(0xffffffffu, pos0, from_lane), __shfl_sync(0xffffffffu, prefix, from_lane));
+      const int at = __ffs(left) - 1;
+      const int t0 = __shfl_sync(0xffffffffu, r.t0, at), t1 = __shfl_sync(0xffffffffu, r.t1, at);
+      const int4 v = make_int4(__shfl_sync(0xffffffffu, b, at), __shfl_sync(0xffffffffu, from, at),
+                               __shfl_sync(0xffffffffu, pos0, at), __shfl_sync(0xffffffffu, prefix, at));
       for (int t = t0 + lane; t < t1; t += 32) plan.token[t] = make_int4(v.x, v.y, v.z + t, v.w);
     }
   }
   __syncthreads();
 
-  // the tiles of a piece: candidate `warp`, from the fewest to all of the longest list
-  const int most = max(s_most, 1), least = (most + kMaxPieces - 1) / kMaxPieces;
-  auto candidate = [&](int i) {
-    if (i == kWarps - 1) return most;
-    const int v = (int)ceilf(exp2f(log2f((float)most) * ((float)i / (kWarps - 1))));
-    return min(max(v, least), most);
-  };
-  {
-    const int per = candidate(warp);
-    float units1 = 0, tiles1 = 0, units2 = 0, tiles2 = 0, rows = 0;
-    int64_t parts = 0;
-    for (int g = lane; g < groups; g += 32) {
-      const int4 v = __ldcg(plan.group + g);
-      if (v.w == 0) continue;
-      const int blocks = blocks_of(v.z), tiles = tiles_of(v.w, 0, -1, cap, shift), pieces = (tiles + per - 1) / per;
-      units1 += (float)blocks * pieces;
-      tiles1 += (float)blocks * tiles;
-      rows += (float)v.z * pieces;
-      parts += (int64_t)blocks * pieces;
-    }
-    for (int b = lane; b < c.batch; b += 32) {
-      const int4 v = __ldcg(plan.request + b);
-      const int pieces = (v.y + per - 1) / per;
-      units2 += (float)v.x * heads * max(pieces, 1);
-      tiles2 += (float)v.x * heads * v.y;
-      if (pieces > 1 || v.w < 0) {
-        rows += (float)v.x * p.H * pieces;
-        parts += (int64_t)v.x * heads * pieces;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      units1 += __shfl_xor_sync(0xffffffffu, units1, o);
-      tiles1 += __shfl_xor_sync(0xffffffffu, tiles1, o);
-      units2 += __shfl_xor_sync(0xffffffffu, units2, o);
-      tiles2 += __shfl_xor_sync(0xffffffffu, tiles2, o);
-      rows += __shfl_xor_sync(0xffffffffu, rows, o);
-      parts += __shfl_xor_sync(0xffffffffu, parts, o);
-    }
-    // turns of the prefixes' pieces, then those of the tokens' that do not fit beside the last of them
-    const float turns = ceilf(units1 / sms), rest = fmaxf(0.f, units2 - (turns * sms - units1));
-    float cost = turns * (tiles1 / fmaxf(units1, 1.f) + kUnitTiles) +
-                 ceilf(rest / sms) * (tiles2 / fmaxf(units2, 1.f) + kUnitTiles) + rows / 7000.f + (rows > 0 ? 1.3f : 0.f);
-    if (parts > plan.max_parts || (unordered && warp < kWarps - 1)) cost = INFINITY;
-    if (lane == 0) s_cost[warp] = cost;
-  }
-  __syncthreads();
-  int pick = kWarps - 1;
-  for (int i = kWarps - 2; i >= 0; --i)
-    if (s_cost[i] < s_cost[pick]) pick = i;
-  const int per = candidate(pick);
-
-  // the units' numbers: partial ones in the low word, whole ones in the high one
-  int64_t before = 0;
-  for (int base = 0; base < plan.groups + T; base += kThreads) {
+  // where the segments begin: in cost, in units (blocks of 64 rows), in units whose results are partial in any case
+  const bool near_segments = segments <= kNearSegments;
+  int64_t* const cost_of = near_segments ? s_cost : plan.cost_of;
+  int* const unit_of = near_segments ? s_unit : plan.unit_of;
+  int64_t cost0 = 0;
+  int unit0 = 0, shared0 = 0;
+  for (int base = 0; base < segments; base += kThreads) {
     const int s = base + threadIdx.x;
-    int64_t n = 0;
-    int pieces = 0;
+    int tiles = 0, units = 0;
+    bool shared = false;
     if (s < plan.groups) {
-      const int4 v = __ldcg(plan.group + s);
-      if (v.w > 0) {
-        pieces = (tiles_of(v.w, 0, -1, cap, shift) + per - 1) / per;
-        n = (int64_t)blocks_of(v.z) * pieces;
+      const int4 v = group[s];
+      shared = v.w > 0;
+      if (shared) {
+        tiles = tiles_of(v.w, 0, -1, cap, shift);
+        units = blocks_of(v.z);
       }
-    } else if (s < plan.groups + T) {
-      const int4 v = __ldcg(plan.token + (s - plan.groups));
+    } else if (s < segments) {
+      const int4 v = plan.token[s - plan.groups];
       if (v.x >= 0) {
-        const int tiles = tiles_of(v.y < 0 ? 0 : v.w, v.w, v.z, cap, shift);
-        pieces = (tiles + per - 1) / per;
-        if (v.y < 0 || pieces > 1) n = (int64_t)heads * pieces;
-        else n = (int64_t)heads << 32;
+        shared = v.y < 0;
+        tiles = tiles_of(shared ? 0 : v.w, v.w, v.z, cap, shift);
+        units = shared && tiles == 0 ? 0 : heads;
       }
     }
-    if (pieces > 0) atomicMax(&s_pieces, pieces);
-    int64_t sum = n;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, sum, d);
-      if (lane >= d) sum += x;
+    // (units and shared units in one word: both are under 2^31)
+    int64_t cost = (int64_t)units * plan_cost(tiles), counts = units | (int64_t)(shared ? units : 0) << 32;
+    int64_t all_cost, all_counts;
+    scan(s_scan, cost, counts, &all_cost, &all_counts);
+    if (s < segments) {
+      const int unit = unit0 + (int)(counts & 0xffffffff);
+      plan.cost_of[s] = cost_of[s] = cost0 + cost;
+      plan.unit_of[s] = unit_of[s] = unit;
+      plan.shared_of[s] = shared0 + (int)(counts >> 32);
     }
-    if (lane == 31) s_scan[warp] = sum;
-    __syncthreads();
-    if (warp == 0) {
-      int64_t all = s_scan[lane];
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, all, d);
-        if (lane >= d) all += x;
-      }
-      s_scan[lane] = all;
-    }
-    __syncthreads();
-    const int64_t at = before + sum - n + (warp > 0 ? s_scan[warp - 1] : 0);
-    if (s < plan.groups + T) {
-      plan.part_of[s] = (int)(at & 0xffffffff);
-      if (s >= plan.groups) plan.whole_of[s - plan.groups] = (int)(at >> 32);
-    }
-    before += s_scan[kWarps - 1];
-    __syncthreads();
+    cost0 += all_cost;
+    unit0 += (int)(all_counts & 0xffffffff);
+    shared0 += (int)(all_counts >> 32);
   }
   if (threadIdx.x == 0) {
-    const int parts = (int)(before & 0xffffffff), whole = (int)(before >> 32);
-    plan.part_of[plan.groups + T] = parts;
-    plan.whole_of[T] = whole;
-    plan.header[kPlanPer] = per;
-    plan.header[kPlanParts] = parts;
-    plan.header[kPlanUnits] = parts + whole;
-    plan.header[kPlanPieces] = s_pieces;
+    plan.cost_of[segments] = cost_of[segments] = cost0;
+    plan.unit_of[segments] = unit_of[segments] = unit0;
+  }
+  __syncthreads();
+
+  // the shares: the first unit that has a tile in share c or behind it, and the units that have one before it
+  const int64_t share = max((cost0 + sms - 1) / sms, (int64_t)kPlanTile);
+  for (int i = threadIdx.x; i <= sms; i += kThreads) {
+    const int64_t x = i * share;
+    int first = unit0, end = unit0, s = 0;
+    if (x < cost0) {
+      s = last_of(segments, [&](int k) { return cost_of[k] <= x; });
+      const int units = unit_of[s + 1] - unit_of[s];
+      const int64_t all = cost_of[s + 1] - cost_of[s], in_segment = x - cost_of[s];
+      const int64_t each = all >> 31 == 0 ? (uint32_t)all / (uint32_t)units : all / units;
+      const int block = all >> 31 == 0 ? (uint32_t)in_segment / (uint32_t)each : (int)(in_segment / each);
+      const int64_t in = in_segment - block * each;              // into the block
+      first = unit_of[s] + block + (in > each - kPlanTile);      // its last tile begins there
+      end = unit_of[s] + block + (in > kPlanUnit);
+      while (first >= unit_of[s + 1] && s + 1 < segments) ++s;   // (behind a segment's last unit)
+    }
+    s_first[i] = first;
+    s_end[i] = end;
+    s_segment[i] = s;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < sms; i += kThreads)
+    plan.share[i] = make_int4(s_first[i], max(0, s_end[i + 1] - s_first[i]), s_segment[i], 0);
+  if (threadIdx.x == 0) {
+    *plan.share_cost = share;
+    *plan.share_by = cost0 >> 34 == 0 && share >> 29 == 0 ? ~0ull / (uint64_t)share + 1 : 0;
+    *plan.few = (int64_t)s_most * kPlanTile / share + 2 <= kFewPieces;
   }
 }
 
 // ------------------------------------------------------------------- merge
 // Weights 2^(LSE_s - LSE) of a head's partials, then the sink and bmm2.  A warp a
-// head, 16 dims a lane, where no list has more than kFew pieces; else the eight
-// warps of a CTA share a head's partials.
+// head, 16 dims a lane, where no list has more than kFewPieces; else the eight warps
+// of a CTA share a head's partials.
 constexpr int kMergeWarps = 8;
-constexpr int kFew = 16;
 
+// A head's partials: of the prefix, then of the token's own list; one for each share
+// that the block has tiles in.
 struct Partials {
-  int prefix, stride, prefixes;                   // first partial of the prefix, partials between its pieces, pieces
-  int own, own_stride, owns;                      // the same of the token
+  int prefix, prefixes, own, owns;                // number of the first one, how many
+  int own_first, own_step;                        // own list: shift of its first one, step between them
   int prefix_row, own_row;                        // the head's row of each
 };
 
 __device__ __forceinline__ int64_t partial_row(const Partials& q, int s) {
-  return s < q.prefixes ? (int64_t)(q.prefix + s * q.stride) * kWindowHeads + q.prefix_row
-                        : (int64_t)(q.own + (s - q.prefixes) * q.own_stride) * kWindowHeads + q.own_row;
+  if (s < q.prefixes) return (int64_t)(q.prefix + s) * kWindowHeads + q.prefix_row;
+  s -= q.prefixes;
+  return (int64_t)(q.own + s * q.own_step + (s == 0 ? q.own_first : 0)) * kWindowHeads + q.own_row;
 }
 
 __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const WindowParams p, const PrefixPlan plan) {
-  __shared__ float s_weight[kMergeWarps][2 * kFew];
-  __shared__ float s_all[2 * kMaxPieces + 2];
+  __shared__ float s_weight[kMergeWarps][2 * kFewPieces];
+  __shared__ float s_all[2 * kMaxShares];
   __shared__ float4 s_share[kMergeWarps][kHeadDim / 4];
   __shared__ float s_top[kMergeWarps], s_sum[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int heads = blocks_of(p.H), T = p.c.sum_q;
+  const int sms = plan.shares, T = p.c.sum_q;
+  const int shift = cache_box_shift(p.c.page_size), cap = p.c.max_pages * p.c.page_size;
   await_prior_kernel();
   admit_next_kernel();
-  if (__ldcg(plan.header + kPlanParts) == 0) return;
-  const bool few = __ldcg(plan.header + kPlanPieces) <= kFew;
-  const int per = __ldcg(plan.header + kPlanPer), shift = cache_box_shift(p.c.page_size), cap = p.c.max_pages * p.c.page_size;
+  const int64_t share = __ldcg(plan.share_cost);
+  const uint64_t by = __ldcg(plan.share_by);
+  const bool few = __ldcg(plan.few) != 0;
   const int each = few ? kMergeWarps : 1, items = (p.H + each - 1) / each;      // heads of a CTA, of a token
   for (int64_t i = blockIdx.x; i < (int64_t)T * items; i += gridDim.x) {
     const int t = (int)(i / items), h = (int)(i - (int64_t)t * items) * each + (few ? warp : 0);
     const int4 v = __ldcg(plan.token + t);
-    if (v.x < 0) continue;
-    Partials q;
-    q.own = __ldcg(plan.part_of + plan.groups + t);
-    q.own_stride = heads;
-    q.owns = (__ldcg(plan.part_of + plan.groups + t + 1) - q.own) / heads;
-    q.own_row = h % kWindowHeads;
-    q.own += h / kWindowHeads;
-    q.prefix = q.stride = q.prefixes = q.prefix_row = 0;
+    const int64_t cost = __ldcg(plan.cost_of + plan.groups + t);
+    const int unit = __ldcg(plan.unit_of + plan.groups + t), shared = __ldcg(plan.shared_of + plan.groups + t);
+    if (v.x < 0 || (few && h >= p.H)) continue;
+    Partials q = {};
+    const int tiles = tiles_of(v.y < 0 ? 0 : v.w, v.w, v.z, cap, shift);
+    if (tiles > 0) {
+      const int block = h / kWindowHeads;
+      const int64_t at = cost + block * plan_cost(tiles) + kPlanUnit;
+      const int c0 = share_of(at, share, by), c1 = share_of(at + (int64_t)(tiles - 1) * kPlanTile, share, by);
+      q.own_row = h % kWindowHeads;
+      q.owns = c1 - c0 + 1;
+      if (v.y < 0) {
+        q.own = 2 * sms + shared + block + c0;
+        q.own_step = 1;
+      } else if (q.owns == 1) {
+        q.owns = 0;                               // done whole
+      } else {
+        q.own = 2 * c0;
+        q.own_step = 2;
+        q.own_first = __ldcg(plan.share + c0).x != unit + block;
+      }
+    }
     if (v.y < 0) {
-      const int g = __ldcg(plan.request + v.x).z;
+      const int g = v.y & 0x7fffffff;
       const int4 w = __ldcg(plan.group + g);
-      const int row = (t - w.y) * p.H + h;
-      q.prefix = __ldcg(plan.part_of + g) + row / kWindowHeads;
-      q.stride = blocks_of(w.z);
-      q.prefixes = (tiles_of(w.w, 0, -1, cap, shift) + per - 1) / per;
+      const int row = (t - w.y) * p.H + h, block = row / kWindowHeads;
+      const int n = tiles_of(w.w, 0, -1, cap, shift);
+      const int64_t at = __ldcg(plan.cost_of + g) + block * plan_cost(n) + kPlanUnit;
+      const int c0 = share_of(at, share, by);
+      q.prefixes = share_of(at + (int64_t)(n - 1) * kPlanTile, share, by) - c0 + 1;
+      q.prefix = 2 * sms + __ldcg(plan.shared_of + g) + block + c0;
       q.prefix_row = row % kWindowHeads;
     }
     const int n = q.prefixes + q.owns;
     if (n == 0) continue;
-    if (few && h >= p.H) continue;
     const int first = few ? lane : (int)threadIdx.x, step = few ? 32 : kMergeWarps * 32;
     float* const weight = few ? s_weight[warp] : s_all;
     float top = -INFINITY, sum = 0.f;
@@ -404,12 +430,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Wi
 
 }  // namespace
 
-cudaError_t launch_prefix_attention(const WindowParams& p, const PrefixPlan& plan, int sms, cudaStream_t stream) {
-  cudaError_t e = launch_overlapped(prefix_plan_kernel, dim3(1), kThreads, 0, stream, p, plan, cache_box_shift(p.c.page_size), sms);
-  if (e == cudaSuccess) e = launch_planned_attention(p, plan, sms, stream);
+cudaError_t launch_prefix_attention(const WindowParams& p, const PrefixPlan& plan, cudaStream_t stream) {
+  cudaError_t e = launch_overlapped(prefix_plan_kernel, dim3(1), kThreads, 0, stream, p, plan, cache_box_shift(p.c.page_size));
+  if (e == cudaSuccess) e = launch_planned_attention(p, plan, stream);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)p.c.sum_q * p.H;
-  return launch_overlapped(prefix_merge_kernel, dim3((unsigned)std::min<int64_t>(rows, (int64_t)sms * 8)), kMergeWarps * 32, 0,
+  return launch_overlapped(prefix_merge_kernel, dim3((unsigned)std::min<int64_t>(rows, (int64_t)plan.shares * 8)), kMergeWarps * 32, 0,
                            stream, p, plan);
 }
 

@@ -91,9 +91,9 @@ __global__ void __launch_bounds__(kSlotThreads) token_slots_kernel(const TokenSl
 }
 
 // -------------------------------------------------------------- sparse slots
-// A CTA a token: its columns, four a thread at a time (one 16-byte store where
+// kWarps warps a token: its columns, four a lane at a time (one 16-byte store where
 // the table's rows allow it).
-constexpr int kSparseThreads = 256;
+constexpr int kSparseThreads = 512;
 
 // Row of position j >= 0, or -1 (*bad set).
 __device__ __forceinline__ int slot_row(const SlotTable& t, const int32_t* row, int j, bool* bad) {
@@ -105,12 +105,17 @@ __device__ __forceinline__ int slot_row(const SlotTable& t, const int32_t* row, 
   return -1;
 }
 
-template <bool kVector>
+template <bool kVector, int kWarps>
 __global__ void __launch_bounds__(kSparseThreads) sparse_slots_kernel(const SparseSlotsParams p) {
   __shared__ int s_last[kSparseThreads / 32];
-  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * (kSparseThreads / 32 / kWarps) + warp / kWarps;
   await_prior_kernel();
   admit_next_kernel();
+  if (kWarps < kSparseThreads / 32 && t >= p.sum_q) {
+    if constexpr (kWarps > 1) __syncthreads();
+    return;
+  }
   int b, first, count;
   if (p.cum != nullptr) {
     b = last_request(p.batch, lane, [&](int x) { return fetch(p.cum + x) <= t; });
@@ -132,7 +137,8 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_slots_kernel(const Spar
   const int columns = kSwaCols + p.num_selected;
   int last = 0;
   bool bad = false;
-  for (int c0 = threadIdx.x * 4; c0 < columns; c0 += kSparseThreads * 4) {
+#pragma unroll 2
+  for (int c0 = (warp % kWarps * 32 + lane) * 4; c0 < columns; c0 += kWarps * 128) {
     int v[4], c[4];
     if (c0 < kSwaCols) {
 #pragma unroll
@@ -164,12 +170,13 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_slots_kernel(const Spar
   }
   if (bad) flag(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
   last = __reduce_max_sync(0xffffffffu, last);
-  if (lane == 0) s_last[warp] = last;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kSparseThreads / 32; ++w) last = max(last, s_last[w]);
-    p.topk[t] = pos >= 0 ? kSwaCols + last : 0;
+  if constexpr (kWarps > 1) {
+    if (lane == 0) s_last[warp] = last;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) last = max(last, s_last[warp / kWarps * kWarps + w]);
   }
+  if (warp % kWarps == 0 && lane == 0) p.topk[t] = pos >= 0 ? kSwaCols + last : 0;
 }
 
 }  // namespace
@@ -179,12 +186,22 @@ cudaError_t launch_token_slots(const TokenSlotsParams& p, cudaStream_t stream) {
   return launch_overlapped(token_slots_kernel, dim3(ctas > 0 ? ctas : 1), kSlotThreads, 0, stream, p);
 }
 
-cudaError_t launch_sparse_slots(const SparseSlotsParams& p, cudaStream_t stream) {
+cudaError_t launch_sparse_slots(const SparseSlotsParams& p, int sms, cudaStream_t stream) {
   auto whole = [](const void* at, int64_t stride) { return reinterpret_cast<uintptr_t>(at) % 16 == 0 && stride % 4 == 0; };
   const bool vector = p.num_selected % 4 == 0 && whole(p.out, p.out_stride) &&
                       (p.selected == nullptr || whole(p.selected, p.selected_stride));
-  return launch_overlapped(vector ? sparse_slots_kernel<true> : sparse_slots_kernel<false>, dim3((unsigned)p.sum_q),
-                           kSparseThreads, 0, stream, p);
+  // as many warps a token as its columns feed and the GPU holds at once
+  auto launch = [&](auto kernel, int warps) {
+    const int each = kSparseThreads / 32 / warps;
+    return launch_overlapped(kernel, dim3((unsigned)((p.sum_q + each - 1) / each)), kSparseThreads, 0, stream, p);
+  };
+  const int chunks = (kSwaCols + p.num_selected + 127) / 128;
+  const int64_t room = (int64_t)sms * 64;
+  if (chunks > 8 && p.sum_q * 16ll <= room)
+    return vector ? launch(sparse_slots_kernel<true, 16>, 16) : launch(sparse_slots_kernel<false, 16>, 16);
+  if (chunks > 2 && p.sum_q * 4ll <= room)
+    return vector ? launch(sparse_slots_kernel<true, 4>, 4) : launch(sparse_slots_kernel<false, 4>, 4);
+  return vector ? launch(sparse_slots_kernel<true, 1>, 1) : launch(sparse_slots_kernel<false, 1>, 1);
 }
 
 }  // namespace smla

@@ -40,7 +40,7 @@ struct SparseSlotsParams {
   int32_t* topk;
   int32_t* err;
 };
-cudaError_t launch_sparse_slots(const SparseSlotsParams& p, cudaStream_t stream);
+cudaError_t launch_sparse_slots(const SparseSlotsParams& p, int sms, cudaStream_t stream);
 
 // How a call's logits are cut: blocks of the 512 bytes that a warp loads at once,
 // of which only the maxima are kept; units of `unit_blocks` consecutive blocks of

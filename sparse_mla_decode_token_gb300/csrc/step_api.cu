@@ -155,7 +155,9 @@ smla_status smla_sparse_slots(const smla_sparse_slots_args* a, void* stream) {
   p.out_stride = a->indices_row_stride ? a->indices_row_stride : columns;
   p.topk = a->topk_lens;
   p.err = a->error_word;
-  return launched("sparse slots", launch_sparse_slots(p, static_cast<cudaStream_t>(stream)));
+  int sms = 0;
+  SMLA_TRY(current_sms(&sms));
+  return launched("sparse slots", launch_sparse_slots(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 smla_status smla_beam_workspace_size(const smla_beam_args* args, int device, size_t* bytes) {

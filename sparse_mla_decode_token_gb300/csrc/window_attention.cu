@@ -189,47 +189,43 @@ __device__ __forceinline__ void unit_heads(const KernelParams& kp, int x, Unit* 
   u->heads = min(kNH, p.H - u->h0);
 }
 
-// Unit x of a plan: partial ones first, by segment (the groups' prefixes, then the
-// tokens), a segment's by piece and then by 64 of its rows, so that neighbours read
-// the same cache rows; then the tokens that are done whole.
+// Unit x of the CTA's share of a plan.
 template <int kShift>
 __device__ __forceinline__ Unit planned_unit(const KernelParams& kp, int x, int lane) {
   const WindowParams& p = kp.p;
   const CacheView& c = p.c;
   const PrefixPlan& plan = kp.plan;
-  const int per = __ldcg(plan.header + kPlanPer), parts = __ldcg(plan.header + kPlanParts);
+  const int share = blockIdx.x;
+  const int4 mine = __ldcg(plan.share + share);
+  const int64_t share_cost = __ldcg(plan.share_cost);
+  const int unit = mine.x + x;
+  int segment = mine.z;
+  if (x > 0)
+    segment += last_request(plan.groups + c.sum_q - segment, lane, [&](int s) { return __ldcg(plan.unit_of + mine.z + s) <= unit; });
+  const int block = unit - __ldcg(plan.unit_of + segment);
+  const int shared = __ldcg(plan.shared_of + segment);
+  int64_t at = __ldcg(plan.cost_of + segment);
   Unit u;
-  u.part = x < parts ? x : -1;
-  int segment, i, blocks = kp.groups, piece = 0;
-  if (x < parts) {
-    segment = last_request(plan.groups + c.sum_q, lane, [&](int s) { return __ldcg(plan.part_of + s) <= x; });
-    i = x - __ldcg(plan.part_of + segment);
-  } else {
-    const int t = last_request(c.sum_q, lane, [&](int s) { return __ldcg(plan.whole_of + s) <= x - parts; });
-    segment = plan.groups + t;
-    i = x - parts - __ldcg(plan.whole_of + t);
-  }
+  u.h0 = block * kNH;
+  bool partial = true;
   if (segment < plan.groups) {                    // a group's prefix
     const int4 g = __ldcg(plan.group + segment);
-    blocks = (g.z + kNH - 1) / kNH;
-    piece = i / blocks;
-    const int row = g.y * p.H + (i - piece * blocks) * kNH;
+    const int row = g.y * p.H + u.h0;
+    u.heads = min(kNH, g.z - u.h0);
     u.t = row / p.H;
     u.h0 = row - u.t * p.H;
-    u.heads = min(kNH, g.z - (i - piece * blocks) * kNH);
     u.b = u.b0 = g.x;
     u.first = g.w;
     u.pos = -1;
     u.lo = 0;
   } else {
     const int4 r = __ldcg(plan.token + (segment - plan.groups));
-    piece = u.part >= 0 ? i / blocks : 0;
+    partial = r.y < 0;
     u.t = segment - plan.groups;
-    u.h0 = (i - piece * blocks) * kNH;
     u.heads = min(kNH, p.H - u.h0);
     u.b = r.x;
-    u.b0 = r.y & 0x7fffffff;
-    u.first = r.y < 0 ? 0 : r.w;                  // (a shared prefix is its group's)
+    u.b0 = partial ? r.x : r.y;
+    u.first = partial ? 0 : r.w;                  // (a shared prefix is its group's)
     u.pos = r.z;
     u.lo = r.w;
   }
@@ -239,8 +235,13 @@ __device__ __forceinline__ Unit planned_unit(const KernelParams& kp, int x, int 
   u.window_chunk = u.lo >> kShift;
   u.chunks = u.first_chunks + (last >= u.lo ? (last >> kShift) - u.window_chunk + 1 : 0);
   const int tiles = (u.chunks + (kRows >> kShift) - 1) >> (7 - kShift);
-  u.tile0 = u.part >= 0 ? min(tiles, piece * per) : 0;
-  u.tiles = u.part >= 0 ? min(tiles - u.tile0, per) : tiles;
+  at += block * plan_cost(tiles) + kPlanUnit;     // where its first tile begins
+  auto from = [&](int s) {                        // its first tile that begins in share s or behind it
+    return (int)min(max((s * share_cost - at + kPlanTile - 1) / kPlanTile, (int64_t)0), (int64_t)tiles);
+  };
+  u.tile0 = from(share);
+  u.tiles = from(share + 1) - u.tile0;
+  u.part = partial ? 2 * plan.shares + shared + block + share : u.tiles < tiles ? 2 * share + (x > 0) : -1;
   return u;
 }
 
@@ -452,9 +453,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
   // too, and take q_full in turn: behind a first unit without tiles the second
   // unit's may be there before the first products' warp has waited for the first
   // one's, but no third is before it has waited for both.
-  const int units = kMode == kPlanned ? __ldcg(kp.plan.header + kPlanUnits) : kp.units;
-  const int mine = (units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
-  if (kMode == kPlanned && mine <= 0) {           // (the grid is what a plan may need at most)
+  const int mine = kMode == kPlanned ? __ldcg(kp.plan.share + blockIdx.x).y
+                                     : (kp.units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  if (kMode == kPlanned && mine <= 0) {
     if (warp == kScoreWarp) tmem_dealloc(tmem, kTmemCols);
     return;
   }
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     constexpr int kBoxes = kRows >> kShift;       // of a tile
     int n = 0;
     bool ok = true;
-    Unit ahead = make_unit<kShift, kMode>(kp, blockIdx.x, lane);
+    Unit ahead = make_unit<kShift, kMode>(kp, kMode == kPlanned ? 0 : blockIdx.x, lane);
     auto prefetch_query = [&](const Unit& u) {
       if constexpr (kMode == kPlanned) {          // rows of several tokens: one by one
         for (int i = lane; u.tiles > 0 && i < u.heads; i += 32) {
@@ -523,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         ok = __all_sync(0xffffffffu, good);
         n += i >= 0;
         if (i == min(1, u.tiles - 1) && x + 1 < mine) {       // the next unit and its queries' way to L2
-          ahead = make_unit<kShift, kMode>(kp, blockIdx.x + (x + 1) * gridDim.x, lane);
+          ahead = make_unit<kShift, kMode>(kp, kMode == kPlanned ? x + 1 : blockIdx.x + (x + 1) * gridDim.x, lane);
           prefetch_query(ahead);
         }
       }
@@ -1190,12 +1191,12 @@ cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t
   return launch_overlapped(window_merge_kernel<1>, heads, kMergeThreads, 0, stream, p, kp.groups);
 }
 
-cudaError_t launch_planned_attention(const WindowParams& p, const PrefixPlan& plan, int sms, cudaStream_t stream) {
+cudaError_t launch_planned_attention(const WindowParams& p, const PrefixPlan& plan, cudaStream_t stream) {
   KernelParams kp;
   kp.p = p;
   kp.plan = plan;
   kp.groups = (p.H + kNH - 1) / kNH;
-  kp.units = plan.max_units;
+  kp.units = 0;
   const int shift = cache_box_shift(p.c.page_size);
   cudaError_t e = encode_cache_map(&kp.map, p.c, 1 << shift);
   if (e == cudaSuccess) e = encode_out_map(&kp.out_map, p);
@@ -1203,7 +1204,7 @@ cudaError_t launch_planned_attention(const WindowParams& p, const PrefixPlan& pl
   auto launch = [&](auto kernel) -> cudaError_t {
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (err != cudaSuccess) return err;
-    return launch_overlapped(kernel, dim3((unsigned)std::min(kp.units, sms)), kThreads, kSmemBytes, stream, kp);
+    return launch_overlapped(kernel, dim3((unsigned)plan.shares), kThreads, kSmemBytes, stream, kp);
   };
   if (shift == 5) return launch(window_kernel<5, kPlanned>);
   if (shift == 4) return launch(window_kernel<4, kPlanned>);

@@ -308,6 +308,9 @@ def test_shared_prefix_of_empty_and_odd_groups():
     C.pages_shared_prefix(t[:4], i32([12, 12, 0, 12]), i32([0, 4]), one, page_size=4)     # one without tokens does not count
     torch.cuda.synchronize()
     assert one.item() == 8
+    C.pages_shared_prefix(i32([[1, -1, 3], [9, 9, 9]]), i32([12, 0]), i32([0, 2]), one, page_size=4)   # an entry of none ends it
+    torch.cuda.synchronize()
+    assert one.item() == 4
 
 
 # ----------------------------------------------------------------------- slot maps

@@ -669,7 +669,8 @@ smla_status smla_sparse_slots(const smla_sparse_slots_args* args, void* stream);
  * to 2^-45 of their logit or of s_i - log sum, whichever is larger, may count as
  * equal.  Continuations of -infinity are none; places that none is left for
  * hold -infinity, -1 and -1.  A beam with a score of -infinity (an empty place)
- * has no continuation, and its logits are not read; nor are a finished beam's.
+ * has no continuation; its logits do not count, whatever they are, nor do a
+ * finished beam's.
  * A NaN or +infinity among the logits or for the score leaves the beam without
  * continuations and sets SMLA_DEVERR_BAD_LOGITS.  Deterministic.
  */

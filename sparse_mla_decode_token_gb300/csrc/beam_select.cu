@@ -7,18 +7,20 @@
 // maximum (a word for 512 bytes).  Blocks rank like their maxima, so the K best
 // elements lie in the K best blocks: K blocks with larger maxima (or equal ones
 // and lower indices) hold K better elements than any element of another block.
-// The same holds for the units of up to 32 blocks that a warp takes.  A second
+// The same holds for the units of up to 16 blocks that a warp takes.  A second
 // kernel ranks a request's units, the blocks of the best K, then the elements of
 // the best K of those: some thousand keys in place of a million logits.
 //
 // Ranks are over (score, index) with the score as an unevaluated sum of two fp32
-// numbers (48 bits): what does not depend on v is computed in 64 bits, and x added
-// to it without an error.  Sums are fp32 over at most 256 terms a lane, then 64 bits
-// over the units; e^x is off by 2^-22 of itself.
+// numbers (48 bits), to which x adds without an error.  Sums are fp32 over at most 64
+// terms a lane, then such pairs over the units; e^x is off by 2^-22 of itself.  (In
+// fp64, which has a fiftieth of fp32's rate, the second kernel takes 15 us for the
+// 32 beams of a request alone.)
 //
 // What bounds it: the first kernel reads each logit once.
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "cache_ptx.cuh"
@@ -27,8 +29,10 @@
 namespace smla {
 namespace {
 
-constexpr int kScanThreads = 256;
-constexpr int kScanBatch = 4;                     // blocks a warp has in flight
+constexpr int kScanThreads = 256, kScanCtas = 4;  // threads of a CTA, CTAs of an SM
+constexpr int kScanBatch = 4;                     // blocks that a warp takes at a time
+constexpr int kScanStages = 3;                    // batches in its ring
+constexpr int kScanSmem = kScanThreads / 32 * kScanStages * kScanBatch * kBeamBlockBytes;
 
 template <class T>
 struct Vec {
@@ -74,23 +78,22 @@ __device__ __forceinline__ Row<T> logits_row(const BeamParams& p, int64_t row) {
   return {x - before, before};
 }
 
-// The lane's 16 bytes of a block, from element `at` of the row's base on; -infinity
-// in place of elements before its first and from `end` on.
+// The lane's 16 bytes from element `at` of the row's base on; -infinity in place of
+// elements before its first and from `end` on.
 template <class T>
-__device__ __forceinline__ uint4 load_lane(const Row<T>& r, int64_t at, int64_t end) {
-  if (at >= r.before && at + Vec<T>::kLane <= end) return __ldcs(reinterpret_cast<const uint4*>(r.base + at));
+__device__ __noinline__ uint4 load_edge(const T* base, int before, uint32_t at, uint32_t end) {
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if constexpr (sizeof(T) == 4) {
-      w[k] = at + k >= r.before && at + k < end ? reinterpret_cast<const uint32_t*>(r.base)[at + k] : 0xff800000u;
+      w[k] = at + k >= before && at + k < end ? reinterpret_cast<const uint32_t*>(base)[at + k] : 0xff800000u;
     } else {
       constexpr uint32_t none = std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
       uint32_t v[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int64_t i = at + 2 * k + e;
-        v[e] = i >= r.before && i < end ? reinterpret_cast<const uint16_t*>(r.base)[i] : none;
+        const uint32_t i = at + 2 * k + e;
+        v[e] = i >= before && i < end ? reinterpret_cast<const uint16_t*>(base)[i] : none;
       }
       w[k] = v[0] | v[1] << 16;
     }
@@ -105,93 +108,145 @@ __device__ __forceinline__ bool live_beam(const BeamParams& p, int64_t row) {
   return s > -INFINITY && s < INFINITY;
 }
 
-// One warp a unit: maxima of its blocks, and the sum of e^(x - m) with the
-// largest of them as m.
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
+
+// Where a warp stands: a batch of blocks of one of its units.
 template <class T>
-__global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamParams p) {
-  constexpr int kLane = Vec<T>::kLane;
-  const int lane = threadIdx.x & 31;
-  const int64_t all = (int64_t)p.batch * p.beams * p.plan.units;
-  const int64_t warps = (int64_t)gridDim.x * (kScanThreads / 32);
+struct Cursor {
+  uint32_t unit, row;                             // unit >= all: no more
+  int j0, j1, j;                                  // the unit's blocks, the batch's first
+
+  // The unit, or the next one `step` away whose logits count.
+  __device__ __forceinline__ void settle(const BeamParams& p, uint32_t all, uint32_t step) {
+    for (; unit < all; unit += step) {
+      row = unit / (uint32_t)p.plan.units;
+      if (live_beam(p, row)) break;
+    }
+    j = j0 = (int)(unit - row * p.plan.units) << p.plan.unit_shift;
+    j1 = min(j0 + (1 << p.plan.unit_shift), p.plan.blocks);
+  }
+  __device__ __forceinline__ bool next(const BeamParams& p, uint32_t all, uint32_t step) {
+    j += kScanBatch;
+    if (j < j1) return false;
+    unit += step;
+    settle(p, all, step);
+    return true;
+  }
+};
+
+// Maxima of a unit's blocks, and the sum of e^(x - m) with the largest of them as m.
+// Each lane copies 16 bytes of every block into a ring of its warp's and reads them
+// there itself, so nothing but its own copies is waited for; the copies run two
+// batches ahead, through the ends of units.
+template <class T>
+__global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan_kernel(const BeamParams p) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr int kLane = Vec<T>::kLane, kStage = kScanBatch * kBeamBlockBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* const mine = ring + warp * (kScanStages * kStage) + lane * 16;
+  const uint32_t all = (uint32_t)(p.batch * p.beams) * p.plan.units;
+  // (units that follow one another go to different CTAs)
+  const uint32_t step = gridDim.x * (kScanThreads / 32);
   await_prior_kernel();
   admit_next_kernel();
-  for (int64_t u = (int64_t)blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5); u < all; u += warps) {
-    const int64_t row = u / p.plan.units;
-    const int j0 = (int)(u - row * p.plan.units) * p.plan.unit_blocks;
-    const int j1 = min(j0 + p.plan.unit_blocks, p.plan.blocks);
-    if (!live_beam(p, row)) continue;
-    const Row<T> r = logits_row<T>(p, row);
-    const int64_t end = (int64_t)r.before + p.vocab;
-    auto load = [&](int j, uint4 (&v)[kScanBatch]) {
-      const int64_t at = (int64_t)j * Vec<T>::kBlock + lane * kLane;
-      if (j > 0 && j + kScanBatch <= j1 && (int64_t)(j + kScanBatch) * Vec<T>::kBlock <= end) {
+  Cursor<T> ahead, at;
+  ahead.unit = warp * gridDim.x + blockIdx.x;
+  ahead.settle(p, all, step);
+  at = ahead;
+  Row<T> r = {};
+  if (ahead.unit < all) r = logits_row<T>(p, ahead.row);
+  auto load = [&](int stage) {
+    if (ahead.unit < all) {
+      const uint32_t end = (uint32_t)r.before + (uint32_t)p.vocab;
+      uint8_t* const to = mine + stage * kStage;
+      uint32_t e = (uint32_t)ahead.j * Vec<T>::kBlock + lane * kLane;
 #pragma unroll
-        for (int k = 0; k < kScanBatch; ++k) v[k] = __ldcs(reinterpret_cast<const uint4*>(r.base + at + k * Vec<T>::kBlock));
-      } else {
-#pragma unroll 1
-        for (int k = 0; k < kScanBatch; ++k) {
-          const uint4 x = load_lane(r, at + k * Vec<T>::kBlock, j + k < j1 ? end : 0);
-#pragma unroll
-          for (int i = 0; i < kScanBatch; ++i)
-            if (i == k) v[i] = x;
-        }
+      for (int k = 0; k < kScanBatch; ++k, e += Vec<T>::kBlock) {
+        if (ahead.j + k < ahead.j1 && e >= r.before && e + kLane <= end)
+          copy_async(ptx::smem_addr(to + k * kBeamBlockBytes), r.base + e);
+        else
+          *reinterpret_cast<uint4*>(to + k * kBeamBlockBytes) = load_edge(r.base, r.before, e, ahead.j + k < ahead.j1 ? end : 0);
       }
-    };
-    float m = -INFINITY, sum = 0.f, keep = -INFINITY;
-    uint4 next[kScanBatch];                       // a batch ahead, so that loads are always in flight
-    load(j0, next);
-    for (int j = j0; j < j1; j += kScanBatch) {
-      uint4 v[kScanBatch];
-#pragma unroll
-      for (int k = 0; k < kScanBatch; ++k) v[k] = next[k];
-      if (j + kScanBatch < j1) load(j + kScanBatch, next);
-      float top = m;
-#pragma unroll
-      for (int k = 0; k < kScanBatch; ++k) {
-        float x[kLane];
-        unpack(v[k], x, r.base);
-        float t = x[0];
-#pragma unroll
-        for (int e = 1; e < kLane; ++e) t = fmaxf(t, x[e]);
-        t = ptx::warp_max(t);
-        if (lane == j + k - j0) keep = t;
-        top = fmaxf(top, t);
-      }
-      const float ref = top == -INFINITY ? 0.f : top;
-      if (top > m) {                              // (the same in all lanes)
-        sum *= fast_exp2((m - ref) * kLog2e);
-        m = top;
-      }
-#pragma unroll
-      for (int k = 0; k < kScanBatch; ++k) {
-        float x[kLane];
-        unpack(v[k], x, r.base);
-#pragma unroll
-        for (int e = 0; e < kLane; ++e) x[e] = fast_exp2((x[e] - ref) * kLog2e);
-#pragma unroll
-        for (int d = 1; d < kLane; d *= 2)
-#pragma unroll
-          for (int e = 0; e < kLane; e += 2 * d) x[e] += x[e + d];
-        sum += x[0];
-      }
+      if (ahead.next(p, all, step) && ahead.unit < all) r = logits_row<T>(p, ahead.row);
     }
+    copy_commit();
+  };
+#pragma unroll 1
+  for (int k = 0; k < kScanStages - 1; ++k) load(k);
+  float m = -INFINITY, keep = -INFINITY;
+  uint64_t sum = 0;                               // two sums
+  for (int stage = 0; at.unit < all;) {
+    load(stage == 0 ? kScanStages - 1 : stage - 1);
+    copy_wait<kScanStages - 1>();
+    const uint8_t* const from = mine + stage * kStage;
+    uint4 v[kScanBatch];
+    float top = m;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (j0 + lane < j1) p.block_max[row * p.plan.blocks + j0 + lane] = keep;
-    if (lane == 0) p.partial[u] = make_float2(m, sum);
+    for (int k = 0; k < kScanBatch; ++k) {
+      v[k] = *reinterpret_cast<const uint4*>(from + k * kBeamBlockBytes);
+      float x[kLane];
+      unpack(v[k], x, r.base);
+      float t = x[0];
+#pragma unroll
+      for (int e = 1; e < kLane; ++e) t = fmaxf(t, x[e]);
+      t = ptx::warp_max(t);
+      if (lane == at.j + k - at.j0) keep = t;
+      top = fmaxf(top, t);
+    }
+    const float ref = top == -INFINITY ? 0.f : top;
+    if (top > m) {                                // (the same in all lanes)
+      const float by = fast_exp2((m - ref) * kLog2e);
+      sum = ptx::f2_mul(sum, ptx::f2_pack(by, by));
+      m = top;
+    }
+    const uint64_t ref2 = ptx::f2_pack(-ref, -ref), log2e2 = ptx::f2_pack(kLog2e, kLog2e);
+#pragma unroll
+    for (int k = 0; k < kScanBatch; ++k) {
+      float x[kLane];
+      unpack(v[k], x, r.base);
+      uint64_t y[kLane / 2];
+#pragma unroll
+      for (int e = 0; e < kLane / 2; ++e) {
+        float a, b;
+        ptx::f2_unpack(ptx::f2_mul(ptx::f2_add(ptx::f2_pack(x[2 * e], x[2 * e + 1]), ref2), log2e2), a, b);
+        y[e] = ptx::f2_pack(fast_exp2(a), fast_exp2(b));
+      }
+#pragma unroll
+      for (int d = 1; d < kLane / 2; d *= 2)
+#pragma unroll
+        for (int e = 0; e < kLane / 2; e += 2 * d) y[e] = ptx::f2_add(y[e], y[e + d]);
+      sum = ptx::f2_add(sum, y[0]);
+    }
+    if (at.j + kScanBatch >= at.j1) {             // the unit is done
+      float total, other;
+      ptx::f2_unpack(sum, total, other);
+      total += other;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      if (at.j0 + lane < at.j1) p.block_max[(int64_t)at.row * p.plan.blocks + at.j0 + lane] = keep;
+      if (lane == 0) p.partial[at.unit] = make_float2(m, total);
+      m = keep = -INFINITY;
+      sum = 0;
+    }
+    at.next(p, all, step);
+    stage = stage == kScanStages - 1 ? 0 : stage + 1;
   }
 }
 
 // ---------------------------------------------------------------- choice
 
-// (score, index) in the order of the choice: larger keys are better, among equal
-// ones lower indices.  Key 0 is none.
+// Scores as whole numbers in the same order: the first of a score's two numbers, then
+// the second; among equal ones lower indices are better.  hi = 0 is none.
 struct Rank {
-  uint64_t key;
-  uint32_t index;
+  uint32_t hi, lo, index;
 };
-__device__ __forceinline__ bool better(Rank a, Rank b) {
-  return a.key > b.key || (a.key == b.key && a.index < b.index);
+__device__ __forceinline__ bool better(const Rank& a, const Rank& b) {
+  return a.hi > b.hi || (a.hi == b.hi && (a.lo > b.lo || (a.lo == b.lo && a.index < b.index)));
 }
 
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -208,166 +263,214 @@ __device__ __forceinline__ float unordered(uint32_t b) {
 struct Beam {
   float hi, lo, top;
 };
-// The score's key: the sum of four numbers as two, the first one rounded.
-__device__ __forceinline__ uint64_t score_key(const Beam& c, float x) {
-  if (!(x > -INFINITY) || isnan(c.hi)) return 0;
+// The score's rank: the sum of four numbers as two, the first one rounded.
+__device__ __noinline__ Rank score_rank(Beam c, float x, uint32_t index) {
+  if (!(x > -INFINITY) || isnan(c.hi)) return {0, 0, index};
   const float d = __fsub_rn(x, c.top), dx = __fadd_rn(d, c.top);
   const float s = __fadd_rn(c.hi, d), b = __fsub_rn(s, c.hi);
-  if (!(fabsf(s) < INFINITY)) return 0;
+  if (!(fabsf(s) < INFINITY)) return {0, 0, index};
   const float e = __fadd_rn(__fsub_rn(x, dx), __fsub_rn(__fsub_rn(dx, d), c.top));   // (x - top) - d
   const float f = __fadd_rn(__fsub_rn(c.hi, __fsub_rn(s, b)), __fsub_rn(d, b));      // (hi + d) - s
   const float t = __fadd_rn(__fadd_rn(f, e), c.lo);
   const float hi = __fadd_rn(s, t), lo = __fsub_rn(t, __fsub_rn(hi, s));
-  return (uint64_t)ordered(hi) << 32 | ordered(lo);
+  return {ordered(hi), ordered(lo), index};
 }
+
+// hi + lo += x, the rounding of hi kept in lo.
+__device__ __forceinline__ void add_exact(float& hi, float& lo, float x) {
+  const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
+  lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b));
+  hi = s;
+}
+// log 2: its first 16 bits, with which small whole numbers multiply exactly, and the rest.
+constexpr float kLog2Hi = 45426.f / 65536.f, kLog2Lo = (float)(0.69314718055994531 - 45426.0 / 65536.0);
 
 constexpr int kPickThreads = 1024;
-constexpr int kGroups = 128;                      // whose best ones bound the K-th best of all
-constexpr int kTile = 8192;                       // keys ranked at a time
-constexpr int kReach = SMLA_MAX_BEAM_OUT * (kTile / kGroups);   // of them that may reach the bound
-constexpr int kGathered = kMaxUnitBlocks * SMLA_MAX_BEAM_OUT;   // keys gathered by a bound that is known
-constexpr int kDirect = 256;                      // keys ranked without a bound of their own
-static_assert(kGathered + SMLA_MAX_BEAM_OUT * (kGathered / kGroups) <= kReach, "both lists of settle()");
+constexpr int kGroups = kPickThreads / 8;         // of entries, whose best ones bound the K-th best of all
+constexpr int kDirect = 64;                       // entries ranked without such a bound
+constexpr int kMany = 512;                        // entries that are not ranked before equal ones are told apart
+constexpr int kTile = 4096;                       // keys gathered at a time
+constexpr int kGathered = kTile + SMLA_MAX_BEAM_OUT;
+static_assert(kGroups >= SMLA_MAX_BEAM_OUT, "a K-th best group");
 
-struct Pick {
-  uint64_t key[kReach + SMLA_MAX_BEAM_OUT];
-  uint32_t index[kReach + SMLA_MAX_BEAM_OUT];
-  Rank group[kPickThreads];
-  Rank best[SMLA_MAX_BEAM_OUT];
-  Rank bound;
-  uint32_t chosen[SMLA_MAX_BEAM_OUT];
-  Beam beam[SMLA_MAX_BEAMS];
-  bool single[SMLA_MAX_BEAMS];                    // finished: one continuation
-  int count, found;
+struct List {
+  uint32_t hi[kGathered], lo[kGathered], index[kGathered];
+
+  __device__ __forceinline__ Rank get(int i) const { return {hi[i], lo[i], index[i]}; }
+  __device__ __forceinline__ void set(int i, const Rank& r) { hi[i] = r.hi, lo[i] = r.lo, index[i] = r.index; }
+  // Adds r where `add` holds (whole warp).
+  __device__ __forceinline__ void append(int* count, bool add, const Rank& r) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t all = __ballot_sync(0xffffffffu, add);
+    if (all == 0) return;
+    int at = 0;
+    if (lane == 0) at = atomicAdd(count, __popc(all));
+    at = __shfl_sync(0xffffffffu, at, 0) + __popc(all & ((1u << lane) - 1u));
+    if (add) set(at, r);
+  }
 };
 
-// The keys among n (any order) that reach a lower bound of their K-th best one, to
-// the list from `to` on; sh.count of them.  Each of 128 groups of keys has a best
-// one; the K-th best of those is the bound, and at most K groups have keys that
-// reach it: K * n / 128, and for keys in no particular order hardly more than K.
-// Whole CTA.
-template <class F>
-__device__ __forceinline__ void reach(Pick& sh, int keep, int n, int to, F key) {
-  const Rank none = {0, 0xffffffffu};
-  Rank mine = none;
-  for (int i = threadIdx.x; i < n; i += kPickThreads) {
-    const Rank r = key(i);
-    if (r.key != 0 && better(r, mine)) mine = r;
-  }
-  sh.group[threadIdx.x] = mine;
-  if (threadIdx.x == 0) {
-    sh.count = 0;
-    sh.bound = none;
-  }
-  __syncthreads();
-  // eight threads a group: its best one, and a share of the comparisons with the others
-  constexpr int kEach = kPickThreads / kGroups;
-  const int group = threadIdx.x / kEach, lane = threadIdx.x % kEach;
-  mine = sh.group[lane * kGroups + group];
-#pragma unroll
-  for (int o = 1; o < kEach; o *= 2) {
-    const Rank r = {__shfl_xor_sync(0xffffffffu, mine.key, o), __shfl_xor_sync(0xffffffffu, mine.index, o)};
-    if (better(r, mine)) mine = r;
-  }
-  __syncthreads();
-  if (lane == 0) sh.group[group] = mine;
+struct Pick {
+  List list, reached;
+  __align__(16) uint32_t group[kGroups];
+  Rank exact[kPickThreads];
+  Rank best[SMLA_MAX_BEAM_OUT], bound;
+  int2 chosen[SMLA_MAX_BEAM_OUT];                 // beam, number within it
+  Beam beam[SMLA_MAX_BEAMS];
+  float cut[SMLA_MAX_BEAMS];                      // logits under it do not reach `least`
+  bool single[SMLA_MAX_BEAMS];                    // finished: one continuation
+  uint32_t least;                                 // hi of the K-th best of a step: a bound for the next one; 0: none
+  int count, reaching, found;
+};
+
+// What a beam's logits have to be at least for a score of `least` or more: 2^-20 of
+// what is added up below it, for fp32's roundings.
+__device__ __forceinline__ float logit_cut(const Beam& c, uint32_t least) {
+  const float score = unordered(least), cut = (score - c.hi) + c.top;
+  return least == 0 ? -INFINITY : cut - 0x1p-20f * (fabsf(score) + fabsf(c.hi) + fabsf(c.top));
+}
+
+// The entries of sh.reached (n, more than kMany: equal scores) that reach the K-th best
+// one of the groups' best ones by index, too, to sh.list: K * n / kPickThreads at most.
+__device__ __noinline__ int narrow(Pick& sh, int keep, int n) {
+  __syncthreads();                                // (n has been read)
+  Rank mine = {0, 0, 0xffffffffu};
+  for (int i = threadIdx.x; i < n; i += kPickThreads)
+    if (better(sh.reached.get(i), mine)) mine = sh.reached.get(i);
+  sh.exact[threadIdx.x] = mine;
+  if (threadIdx.x == 0) sh.bound = {0, 0, 0xffffffffu}, sh.reaching = 0;
   __syncthreads();
   int rank = 0;
-#pragma unroll
-  for (int k = lane; k < kGroups; k += kEach) rank += better(sh.group[k], mine);
-#pragma unroll
-  for (int o = 1; o < kEach; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-  if (lane == 0 && rank == keep - 1 && mine.key != 0) sh.bound = mine;
+  for (int k = 0; k < kPickThreads && rank < keep; ++k) rank += better(sh.exact[k], mine);
+  if (rank == keep - 1 && mine.hi != 0) sh.bound = mine;
   __syncthreads();
   const Rank bound = sh.bound;
-  for (int i = threadIdx.x; i < n; i += kPickThreads) {
-    const Rank r = key(i);
-    if (r.key != 0 && !better(bound, r)) {
-      const int at = to + atomicAdd(&sh.count, 1);
-      sh.key[at] = r.key;
-      sh.index[at] = r.index;
-    }
+  for (int base = 0; base < n; base += kPickThreads) {
+    const int i = base + (int)threadIdx.x;
+    const Rank r = sh.reached.get(min(i, n - 1));
+    sh.list.append(&sh.reaching, i < n && !better(bound, r), r);
   }
   __syncthreads();
+  return sh.reaching;
 }
 
-// The K best of the list's entries [from, from + count), in order, to sh.best: each
-// entry's rank is the number of better ones, counted by eight threads.
-__device__ __forceinline__ void rank_list(Pick& sh, int keep, int from, int count) {
-  constexpr int kEach = 8;
-  const int lane = threadIdx.x % kEach;
-  for (int base = 0; base < count; base += kPickThreads / kEach) {
-    const int i = base + (int)threadIdx.x / kEach;
-    const Rank mine = {sh.key[from + min(i, count - 1)], sh.index[from + min(i, count - 1)]};
-    int rank = 0;
-    for (int k = lane; k < count; k += kEach) rank += better({sh.key[from + k], sh.index[from + k]}, mine);
+// The K best of sh.list's `count` entries, in order, to sh.best; sh.chosen are those in
+// rising order of their indices (beam * per_beam + number), so that positions in what
+// they stand for compare like (beam, token); sh.cut what the K-th best asks of the next
+// step's logits.  Each of 128 groups of entries has a best score; the K-th best of
+// those is a lower bound of the K-th best of all, which for entries in no particular
+// order hardly more than K reach; an entry's rank is then the number of better ones.
+// Whole CTA.  (Out of line, once for all steps: what this kernel costs is latency, of
+// which instructions fetched for the first time are a part.)
+__device__ __noinline__ void settle(Pick& sh, int keep, int count, int per_beam, int beams) {
+  List* list = &sh.list;
+  if (count > kDirect) {
+    const int group = threadIdx.x / 8, lane = threadIdx.x % 8;
+    uint32_t top = 0;
+    for (int i = lane * kGroups + group; i < count; i += kPickThreads) top = max(top, sh.list.hi[i]);
 #pragma unroll
-    for (int o = 1; o < kEach; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-    if (lane == 0 && i < count && rank < keep) sh.best[rank] = mine;
-  }
-  if (threadIdx.x == 0) sh.found = min(keep, count);
-  __syncthreads();
-}
-
-// The K best of n keys, a tile at a time beside the best ones so far.
-template <class F>
-__device__ __forceinline__ void pick(Pick& sh, int keep, int64_t n, F key) {
-  int found = 0;
-  for (int64_t base = 0; base < n; base += kTile) {
-    reach(sh, keep, (int)min((int64_t)kTile, n - base), 0, [&](int i) { return key(base + i); });
-    const int count = sh.count;
-    if (threadIdx.x < found) {
-      sh.key[count + threadIdx.x] = sh.best[threadIdx.x].key;
-      sh.index[count + threadIdx.x] = sh.best[threadIdx.x].index;
+    for (int o = 1; o < 8; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) sh.group[group] = top;
+    if (threadIdx.x == 0) sh.reaching = 0;
+    __syncthreads();
+    int rank = 0;
+#pragma unroll
+    for (int k = 0; k < kGroups / 32; ++k) {
+      const int at = 4 * (lane + 8 * k);
+      const uint4 v = *reinterpret_cast<const uint4*>(sh.group + at);
+      rank += (v.x > top) + (v.y > top) + (v.z > top) + (v.w > top);
+      rank += (v.x == top && at < group) + (v.y == top && at + 1 < group) + (v.z == top && at + 2 < group) +
+              (v.w == top && at + 3 < group);
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (lane == 0 && rank == keep - 1) sh.bound.hi = top;
+    __syncthreads();
+    const uint32_t bound = max(sh.bound.hi, 1u);
+    for (int base = 0; base < count; base += kPickThreads) {
+      const int i = base + (int)threadIdx.x;
+      const Rank r = sh.list.get(min(i, count - 1));
+      sh.reached.append(&sh.reaching, i < count && r.hi >= bound, r);
     }
     __syncthreads();
-    rank_list(sh, keep, 0, count + found);
-    found = sh.found;
+    count = sh.reaching;
+    list = &sh.reached;
+    if (count > kMany) {
+      count = narrow(sh, keep, count);
+      list = &sh.list;
+    }
   }
-  if (threadIdx.x == 0) sh.found = found;
-  __syncthreads();
-}
-
-// The K best of n keys of which at least K are `least` or more, if it is not 0: those
-// are gathered, and what is left to rank is little more than K, but for ties.
-template <class F>
-__device__ __forceinline__ void pick_from(Pick& sh, int keep, int n, uint64_t least, F key) {
-  if (threadIdx.x == 0) sh.count = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kPickThreads) {
-    const Rank r = key(i);
-    if (r.key != 0 && r.key >= least) {
-      const int at = atomicAdd(&sh.count, 1);
-      if (at < kGathered) {
-        sh.key[at] = r.key;
-        sh.index[at] = r.index;
+  {
+    const int lane = threadIdx.x % 8;
+    for (int base = 0; base < count; base += kPickThreads / 8) {
+      const int i = base + (int)threadIdx.x / 8;
+      const Rank mine = list->get(min(i, count - 1));
+      int rank = 0;
+#pragma unroll 4
+      for (int k = lane; k < count; k += 8) {
+        const uint32_t hi = list->hi[k];
+        if (hi > mine.hi) ++rank;
+        else if (hi == mine.hi && k != i) rank += better(list->get(k), mine);
       }
+#pragma unroll
+      for (int o = 1; o < 8; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+      if (lane == 0 && i < count && rank < keep) sh.best[rank] = mine;
     }
   }
   __syncthreads();
-  const int count = sh.count;
-  __syncthreads();
-  if (count <= kDirect) {
-    rank_list(sh, keep, 0, count);
-  } else if (count <= kGathered) {
-    reach(sh, keep, count, kGathered, [&](int i) -> Rank { return {sh.key[i], sh.index[i]}; });
-    rank_list(sh, keep, kGathered, sh.count);
-  } else {
-    pick(sh, keep, n, [&](int64_t i) { return key((int)i); });
+  const int found = min(keep, count);
+  const uint32_t least = found == keep ? sh.best[keep - 1].hi : 0;
+  {
+    constexpr int kEach = kPickThreads / SMLA_MAX_BEAM_OUT;      // threads for each
+    const int i = threadIdx.x / kEach, lane = threadIdx.x % kEach;
+    const uint32_t mine = i < found ? sh.best[i].index : 0;
+    int at = 0;
+    for (int k = lane; k < found; k += kEach) at += sh.best[k].index < mine;
+#pragma unroll
+    for (int o = 1; o < kEach; o *= 2) at += __shfl_xor_sync(0xffffffffu, at, o);
+    if (lane == 0 && i < found) {
+      const uint32_t beam = mine / (uint32_t)per_beam;
+      sh.chosen[at] = make_int2((int)beam, (int)(mine - beam * per_beam));
+    }
   }
+  for (int i = kPickThreads - 1 - (int)threadIdx.x; i < beams; i += kPickThreads) sh.cut[i] = logit_cut(sh.beam[i], least);
+  if (threadIdx.x == 0) {
+    sh.found = found;
+    sh.least = least;
+  }
+  __syncthreads();
 }
 
-// sh.best's indices in rising order to sh.chosen; so that positions in what they
-// stand for compare like (beam, token).
-__device__ __forceinline__ void sort_chosen(Pick& sh) {
-  const int found = sh.found;
-  if (threadIdx.x < found) {
-    const uint32_t mine = sh.best[threadIdx.x].index;
-    int at = 0;
-    for (int k = 0; k < found; ++k) at += sh.best[k].index < mine;
-    sh.chosen[at] = mine;
+// The K best of n keys, of which at least K reach sh.least where that is not 0: a tile
+// of keys at a time is gathered (those that are enough) and settled beside the best
+// ones so far.  load(i) is the number that key(i, number) is made of, always read, so
+// that four a thread are on their way at a time.  Keys that reach the bound are little
+// more than K, but for ties.
+template <class L, class F>
+__device__ __forceinline__ void pick(Pick& sh, int keep, int64_t n, int per_beam, int beams, L load, F key) {
+  int found = 0;
+  for (int64_t tile = 0; tile < n || tile == 0; tile += kTile) {
+    const int here = (int)min(n - tile, (int64_t)kTile);
+    const uint32_t least = sh.least;
+    if (threadIdx.x == 0) sh.count = found;
+    if (threadIdx.x < found) sh.list.set(threadIdx.x, sh.best[threadIdx.x]);
+    float x[kTile / kPickThreads];
+#pragma unroll
+    for (int k = 0; k < kTile / kPickThreads; ++k)
+      x[k] = k * kPickThreads < here ? load(tile + min(k * kPickThreads + (int)threadIdx.x, here - 1)) : 0.f;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kTile / kPickThreads; ++k) {
+      const int i = k * kPickThreads + (int)threadIdx.x;
+      if (k * kPickThreads >= here) break;
+      Rank r = {0, 0, 0};
+      if (i < here) r = key(tile + i, x[k]);
+      sh.list.append(&sh.count, r.hi != 0 && r.hi >= least, r);
+    }
+    __syncthreads();
+    settle(sh, keep, sh.count, per_beam, beams);
+    found = sh.found;
   }
-  __syncthreads();
 }
 
 template <class T>
@@ -379,33 +482,45 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
   await_prior_kernel();
   admit_next_kernel();
 
+  if (threadIdx.x == 0) sh.least = 0;
   // the beams, a warp each
   for (int i = warp; i < p.beams; i += kPickThreads / 32) {
     const float s = fetch(p.scores + row0 + i);
     const bool done = p.finished != nullptr && p.finished[row0 + i] != 0;
     bool bad = isnan(s) || s == INFINITY;
-    double c = NAN;
-    float m = 0.f;
+    Beam c = {NAN, 0.f, 0.f};
     if (done) {
-      if (!bad && s > -INFINITY) c = s;
+      if (!bad && s > -INFINITY) c.hi = s;
     } else if (live_beam(p, row0 + i)) {
       const float2* part = p.partial + (row0 + i) * p.plan.units;
-      m = -INFINITY;
+      float m = -INFINITY;
       for (int k = lane; k < p.plan.units; k += 32) m = fmaxf(m, fetch(part + k).x);
       m = ptx::warp_max(m);
-      double sum = 0;
+      float hi = 0.f, lo = 0.f;                   // the sum, as two numbers
       for (int k = lane; k < p.plan.units; k += 32) {
         const float2 v = fetch(part + k);
-        if (!(v.x == -INFINITY && v.y == 0.f)) sum += (double)(v.y * fast_exp2((v.x - m) * kLog2e));
+        if (!(v.x == -INFINITY && v.y == 0.f)) add_exact(hi, lo, v.y * fast_exp2((v.x - m) * kLog2e));
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      bad = isnan(sum);
-      if (!bad && m > -INFINITY) c = (double)s - log(sum);
+      for (int o = 16; o > 0; o >>= 1) {
+        const float h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
+        add_exact(hi, lo, h);
+        lo += l;
+      }
+      bad = isnan(hi);
+      if (!bad && m > -INFINITY) {
+        // log of the sum: e log 2 + log f for 2^e f with f in [0.75, 1.5), so that the second term is small
+        const int e = (__float_as_int(hi) - 0x3f400000) >> 23;
+        const float down = __int_as_float((127 - e) << 23), f = hi * down;
+        c.hi = s;
+        add_exact(c.hi, c.lo, -(float)e * kLog2Hi);
+        add_exact(c.hi, c.lo, -(logf(f) + (lo * down) / f));
+        c.lo -= (float)e * kLog2Lo;
+        c.top = m;
+      }
     }
     if (lane == 0) {
-      const float hi = (float)c;
-      sh.beam[i] = {hi, (float)(c - (double)hi), m};
+      sh.beam[i] = c;
       sh.single[i] = done;
       if (bad && p.err != nullptr) atomicOr(p.err, SMLA_DEVERR_BAD_LOGITS);
     }
@@ -413,53 +528,67 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
   __syncthreads();
 
   // the best units, the best blocks of those, the best elements of those
-  const int keep = p.num_out, per = p.plan.unit_blocks, units = p.plan.units;
+  const int keep = p.num_out, shift = p.plan.unit_shift, units = p.plan.units, blocks = p.plan.blocks;
   const float2* part = p.partial + row0 * units;
-  pick(sh, keep, (int64_t)p.beams * units, [&](int64_t at) -> Rank {
-    const uint32_t i = (uint32_t)at / (uint32_t)units;
-    const Beam c = sh.beam[i];
-    if (isnan(c.hi)) return {0, 0};
-    if (sh.single[i]) return {at == (int64_t)i * units ? score_key(c, 0.f) : 0, (uint32_t)at};
-    return {score_key(c, fetch(&part[at].x)), (uint32_t)at};
-  });
-  uint64_t least = sh.found == keep ? sh.best[keep - 1].key : 0;
-  sort_chosen(sh);
-  const float* top = p.block_max + row0 * p.plan.blocks;
-  pick_from(sh, keep, sh.found * per, least, [&](int at) -> Rank {
-    const uint32_t unit = sh.chosen[at / per], i = unit / (uint32_t)units;
-    const int j = (int)(unit - i * units) * per + at % per;
-    Rank r = {0, i * (uint32_t)p.plan.blocks + j};
-    if (sh.single[i]) r.key = j == 0 ? score_key(sh.beam[i], 0.f) : 0;
-    else if (j < p.plan.blocks) r.key = score_key(sh.beam[i], fetch(top + r.index));
-    return r;
-  });
-  least = sh.found == keep ? sh.best[keep - 1].key : 0;
-  sort_chosen(sh);
+  pick(
+      sh, keep, (int64_t)p.beams * units, units, p.beams, [&](int64_t at) { return fetch(&part[at].x); },
+      [&](int64_t at, float x) -> Rank {
+        const uint32_t i = (uint32_t)at / (uint32_t)units;
+        if (sh.single[i] && at != (int64_t)i * units) return {0, 0, 0};
+        return score_rank(sh.beam[i], sh.single[i] ? 0.f : x, (uint32_t)at);
+      });
+  const float* top = p.block_max + row0 * blocks;
+  pick(
+      sh, keep, sh.found << shift, blocks, p.beams,
+      [&](int64_t at) {
+        const int2 unit = sh.chosen[(int)at >> shift];
+        return fetch(top + unit.x * blocks + min((unit.y << shift) + ((int)at & ((1 << shift) - 1)), blocks - 1));
+      },
+      [&](int64_t at, float x) -> Rank {
+        const int2 unit = sh.chosen[(int)at >> shift];
+        const int j = (unit.y << shift) + ((int)at & ((1 << shift) - 1));
+        const bool single = sh.single[unit.x];
+        if (single ? j != 0 : j >= blocks || x < sh.cut[unit.x]) return {0, 0, 0};
+        return score_rank(sh.beam[unit.x], single ? 0.f : x, (uint32_t)(unit.x * blocks + j));
+      });
+  // (the blocks' elements: where they lie, which of them are the row's)
   constexpr int kBlock = Vec<T>::kBlock;
-  pick_from(sh, keep, sh.found * kBlock, least, [&](int at) -> Rank {
-    const uint32_t block = sh.chosen[at / kBlock], i = block / (uint32_t)p.plan.blocks;
-    Rank r = {0, (uint32_t)at};
-    if (sh.single[i]) {
-      if (at % kBlock == 0) r.key = score_key(sh.beam[i], 0.f);
-    } else {
-      const Row<T> row = logits_row<T>(p, row0 + i);
-      const int64_t j = (int64_t)(block - i * p.plan.blocks) * kBlock + at % kBlock;
-      if (j >= row.before && j < (int64_t)row.before + p.vocab) r.key = score_key(sh.beam[i], element(row.base + j));
-    }
-    return r;
-  });
+  __shared__ const T* s_base[SMLA_MAX_BEAM_OUT];
+  __shared__ int s_beam[SMLA_MAX_BEAM_OUT], s_from[SMLA_MAX_BEAM_OUT], s_to[SMLA_MAX_BEAM_OUT], s_token[SMLA_MAX_BEAM_OUT];
+  if (threadIdx.x < sh.found) {
+    const int k = threadIdx.x;
+    const int2 block = sh.chosen[k];
+    const Row<T> row = logits_row<T>(p, row0 + block.x);
+    const int64_t j = (int64_t)block.y * kBlock;
+    s_base[k] = row.base + j;
+    s_beam[k] = block.x;
+    s_from[k] = (int)max(row.before - j, (int64_t)0);
+    s_to[k] = (int)min(row.before + (int64_t)p.vocab - j, (int64_t)kBlock);
+    s_token[k] = (int)(j - row.before);
+    if (sh.single[block.x]) s_to[k] = s_from[k] + 1;   // (one of a finished beam's stands for it)
+  }
+  __syncthreads();
+  pick(
+      sh, keep, sh.found * kBlock, 1, p.beams,
+      [&](int64_t at) {
+        const int k = (int)at / kBlock;
+        return element(s_base[k] + min(max((int)at % kBlock, s_from[k]), s_to[k] - 1));
+      },
+      [&](int64_t at, float x) -> Rank {
+        const int k = (int)at / kBlock, e = (int)at % kBlock, i = s_beam[k];
+        const bool single = sh.single[i];
+        if (e < s_from[k] || e >= s_to[k] || (!single && x < sh.cut[i])) return {0, 0, 0};
+        return score_rank(sh.beam[i], single ? 0.f : x, (uint32_t)at);
+      });
   if (threadIdx.x < p.num_out) {
     float score = -INFINITY;
     int parent = -1, token = -1;
     if (threadIdx.x < sh.found) {
       const Rank r = sh.best[threadIdx.x];
-      const uint32_t block = sh.chosen[r.index / kBlock];
-      const int i = (int)(block / (uint32_t)p.plan.blocks);
-      score = unordered((uint32_t)(r.key >> 32));
-      parent = (int)(row0 + i);
-      token = sh.single[i] ? p.end_token
-                           : (int)((int64_t)(block % (uint32_t)p.plan.blocks) * kBlock + r.index % kBlock -
-                                   logits_row<T>(p, row0 + i).before);
+      const int k = r.index / kBlock;
+      score = unordered(r.hi);
+      parent = (int)(row0 + s_beam[k]);
+      token = sh.single[s_beam[k]] ? p.end_token : s_token[k] + (int)(r.index % kBlock);
     }
     const int64_t at = (int64_t)blockIdx.x * p.num_out + threadIdx.x;
     p.out_scores[at] = score;
@@ -469,10 +598,12 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
 }
 
 template <class T>
-cudaError_t launch(const BeamParams& p, cudaStream_t stream) {
+cudaError_t launch(const BeamParams& p, int sms, cudaStream_t stream) {
   const int64_t units = (int64_t)p.batch * p.beams * p.plan.units, ctas = (units + kScanThreads / 32 - 1) / (kScanThreads / 32);
-  cudaError_t e = launch_overlapped(beam_scan_kernel<T>, dim3((unsigned)(ctas < (1 << 20) ? ctas : 1 << 20)), kScanThreads, 0,
-                                    stream, p);
+  cudaError_t e = cudaFuncSetAttribute(beam_scan_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScanSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_overlapped(beam_scan_kernel<T>, dim3((unsigned)std::min<int64_t>(ctas, (int64_t)sms * kScanCtas)), kScanThreads,
+                        kScanSmem, stream, p);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(beam_pick_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Pick));
   if (e != cudaSuccess) return e;
@@ -481,10 +612,10 @@ cudaError_t launch(const BeamParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_beam_select(const BeamParams& p, cudaStream_t stream) {
-  if (p.dtype == SMLA_LOGITS_BF16) return launch<__nv_bfloat16>(p, stream);
-  if (p.dtype == SMLA_LOGITS_FP16) return launch<__half>(p, stream);
-  return launch<float>(p, stream);
+cudaError_t launch_beam_select(const BeamParams& p, int sms, cudaStream_t stream) {
+  if (p.dtype == SMLA_LOGITS_BF16) return launch<__nv_bfloat16>(p, sms, stream);
+  if (p.dtype == SMLA_LOGITS_FP16) return launch<__half>(p, sms, stream);
+  return launch<float>(p, sms, stream);
 }
 
 }  // namespace smla

@@ -112,7 +112,6 @@ __host__ __device__ inline int cache_box_shift(int page_size) { return page_size
 // only its end, cuts), then for shared prefixes and their tokens by unit and share.
 constexpr int kPlanTile = 4, kPlanUnit = 11;      // cost of a tile; of a unit's query, sums and results
 constexpr int kMaxShares = 256;
-constexpr int kFewPieces = 16;
 __host__ __device__ inline int64_t plan_cost(int tiles) { return kPlanUnit + (int64_t)(tiles > 0 ? tiles : 1) * kPlanTile; }
 struct PrefixPlan {
   int32_t groups, shares;
@@ -120,13 +119,13 @@ struct PrefixPlan {
   const int32_t* prefix_lens;           // [groups]
   int64_t* share_cost;                  // [1]
   uint64_t* share_by;                   // [1] 2^64 / share_cost, rounded up
-  int32_t* few;                         // [1] no block in more than kFewPieces
   int64_t* cost_of;                     // [groups + T + 1] where a group's prefix, a token begins
   int32_t* unit_of;                     // [groups + T + 1] its first unit
   int32_t* shared_of;                   // [groups + T] the units of shared prefixes and their tokens before it
   int4* share;                          // [shares] first unit, units, the first one's segment
   int4* group;                          // [groups] first request, first token, (token, head) rows, prefix (0: not shared)
   int4* token;                          // [T] request, its group's first one (or sign and group: shared), position, prefix
+  int4* prefix_of;                      // [T] of a shared prefix: cost_of (two words), shared_of, the token's first row in it
   int32_t* limit;                       // [groups] positions that all the group's tokens see
 };
 

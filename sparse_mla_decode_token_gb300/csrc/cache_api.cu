@@ -203,7 +203,7 @@ smla_status check_prefix(const smla_prefix_args* a) {
 struct PrefixLayout {
   int64_t parts;
   int shares;
-  size_t lse, header, cost_of, unit_of, shared_of, share, group, token, limit, bytes;
+  size_t lse, header, cost_of, unit_of, shared_of, share, group, token, prefix_of, limit, bytes;
 };
 PrefixLayout prefix_layout(const smla_prefix_args* a, int sms) {
   const int64_t T = a->sum_q, heads = (a->num_heads + kWindowHeads - 1) / kWindowHeads;
@@ -221,13 +221,14 @@ PrefixLayout prefix_layout(const smla_prefix_args* a, int sms) {
   };
   take(rows * kHeadDim * sizeof(float));
   l.lse = take(rows * sizeof(float));
-  l.header = take(2 * sizeof(int64_t) + sizeof(int32_t));
+  l.header = take(2 * sizeof(int64_t));
   l.cost_of = take((segments + 1) * sizeof(int64_t));
   l.unit_of = take((segments + 1) * sizeof(int32_t));
   l.shared_of = take(segments * sizeof(int32_t));
   l.share = take((size_t)l.shares * sizeof(int4));
   l.group = take((size_t)a->num_groups * sizeof(int4));
   l.token = take((size_t)T * sizeof(int4));
+  l.prefix_of = take((size_t)T * sizeof(int4));
   l.limit = take((size_t)a->num_groups * sizeof(int32_t));
   l.bytes = at;
   return l;
@@ -394,13 +395,13 @@ smla_status smla_prefix_attention(const smla_prefix_args* a, void* stream) {
   plan.prefix_lens = a->prefix_lens;
   plan.share_cost = reinterpret_cast<int64_t*>(ws + l.header);
   plan.share_by = reinterpret_cast<uint64_t*>(ws + l.header + sizeof(int64_t));
-  plan.few = reinterpret_cast<int32_t*>(ws + l.header + 2 * sizeof(int64_t));
   plan.cost_of = reinterpret_cast<int64_t*>(ws + l.cost_of);
   plan.unit_of = reinterpret_cast<int32_t*>(ws + l.unit_of);
   plan.shared_of = reinterpret_cast<int32_t*>(ws + l.shared_of);
   plan.share = reinterpret_cast<int4*>(ws + l.share);
   plan.group = reinterpret_cast<int4*>(ws + l.group);
   plan.token = reinterpret_cast<int4*>(ws + l.token);
+  plan.prefix_of = reinterpret_cast<int4*>(ws + l.prefix_of);
   plan.limit = reinterpret_cast<int32_t*>(ws + l.limit);
   return launched("prefix attention", launch_prefix_attention(p, plan, static_cast<cudaStream_t>(stream)));
 }

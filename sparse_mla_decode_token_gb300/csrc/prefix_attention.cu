@@ -27,9 +27,9 @@
 namespace smla {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kNearGroups = 512, kNearSegments = 2048;   // of which the plan's arrays lie in shared memory
+constexpr int kNearGroups = 512, kNearSegments = 1024;   // of which the plan's arrays lie in shared memory
 
 __device__ __forceinline__ void flag(int32_t* err, int bit) {
   if (err != nullptr) atomicOr(err, bit);
@@ -82,7 +82,7 @@ __device__ __forceinline__ void scan(Scan& sh, int64_t& a, int64_t& b, int64_t* 
   }
   if (lane == 31) sh.a[warp] = a, sh.b[warp] = b;
   __syncthreads();
-  int64_t wa = sh.a[lane], wb = sh.b[lane];
+  int64_t wa = lane < kWarps ? sh.a[lane] : 0, wb = lane < kWarps ? sh.b[lane] : 0;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int64_t x = __shfl_up_sync(0xffffffffu, wa, d), y = __shfl_up_sync(0xffffffffu, wb, d);
@@ -106,9 +106,10 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
   __shared__ int4 s_group[kNearGroups];
   __shared__ int64_t s_cost[kNearSegments + 1];
   __shared__ int s_unit[kNearSegments + 1];
+  __shared__ int4 s_token[kNearSegments];
+  __shared__ int s_shared[kNearSegments];
   __shared__ int s_first[kMaxShares + 1], s_end[kMaxShares + 1], s_segment[kMaxShares + 1];
   __shared__ Scan s_scan;
-  __shared__ int s_most;
   const CacheView& c = p.c;
   const int lane = threadIdx.x & 31;
   const int sms = plan.shares, heads = blocks_of(p.H), cap = c.max_pages * c.page_size, T = c.sum_q, segments = plan.groups + T;
@@ -119,7 +120,13 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
   int* const limit = near ? s_limit : plan.limit;
 
   // what is out of order shares nothing
-  bool bad = false, unordered = false;
+  const bool near_segments = segments <= kNearSegments;
+  int4* const token = near_segments ? s_token : plan.token;
+  const int b0 = threadIdx.x, g0 = threadIdx.x;   // the thread's first request and group: looked up at once
+  Request mine = {0, 0, 0, 0, 0};
+  if (b0 < c.batch) mine = request_of(c, b0);
+  const int prefix0 = g0 < plan.groups ? fetch(plan.prefix_lens + g0) : 0;
+  bool bad = false, unordered = mine.count < 0;
   for (int g = threadIdx.x; g < plan.groups; g += kThreads) {
     const int lo = fetch(plan.group_starts + g), hi = fetch(plan.group_starts + g + 1);
     bad |= lo < 0 || hi < lo || hi > c.batch;
@@ -130,9 +137,8 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
     }
   }
   if (c.cum != nullptr)
-    for (int b = threadIdx.x; b < c.batch; b += kThreads) unordered |= fetch(c.cum + b) > fetch(c.cum + b + 1);
-  for (int t = threadIdx.x; t < T; t += kThreads) plan.token[t] = make_int4(-1, 0, -1, 0);
-  if (threadIdx.x == 0) s_most = 1;
+    for (int b = b0 + kThreads; b < c.batch; b += kThreads) unordered |= fetch(c.cum + b) > fetch(c.cum + b + 1);
+  for (int t = threadIdx.x; t < T; t += kThreads) token[t] = make_int4(-1, 0, -1, 0);
   if (bad) flag(p.err, SMLA_DEVERR_PAGE_STATE);
   const int groups = __syncthreads_or(bad || unordered) ? 0 : plan.groups;
   auto group_of = [&](int b) {
@@ -141,7 +147,9 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
   };
 
   // the positions that all of a group's tokens see
-  for (int b = threadIdx.x; b < c.batch && groups > 0; b += kThreads) {
+  const int group0 = mine.t1 > mine.t0 ? group_of(b0) : -1;
+  if (group0 >= 0) atomicMin(limit + group0, max(0, mine.len - mine.count + 1));
+  for (int b = b0 + kThreads; b < c.batch && groups > 0; b += kThreads) {
     const Request r = request_of(c, b);
     const int g = r.t1 > r.t0 ? group_of(b) : -1;
     if (g >= 0) atomicMin(limit + g, max(0, r.len - r.count + 1));
@@ -152,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
     int prefix = 0;
     if (groups > 0 && limit[g] != 0x7fffffff) {
       const int lo = starts[g], hi = starts[g + 1];
-      prefix = min(min(max(fetch(plan.prefix_lens + g), 0), limit[g]), cap);
+      prefix = min(min(max(g == g0 ? prefix0 : fetch(plan.prefix_lens + g), 0), limit[g]), cap);
       int t0 = lo * (T / c.batch), t1 = hi * (T / c.batch);
       if (c.cum != nullptr) t0 = fetch(c.cum + lo), t1 = fetch(c.cum + hi);
       t0 = min(max(t0, 0), T), t1 = min(max(t1, t0), T);
@@ -160,7 +168,6 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
       v = make_int4(lo, t0, (t1 - t0) * p.H, 0);
       if ((int64_t)((t1 - t0) * heads - blocks) * tiles > 3 * (int64_t)blocks) {
         v.w = prefix;
-        atomicMax(&s_most, tiles);
       }
     }
     plan.group[g] = v;
@@ -173,36 +180,36 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
   // the requests' tokens
   for (int base = 0; base < c.batch; base += kThreads) {
     const int b = base + threadIdx.x;
-    Request r = {0, 0, 0, 0, 0};
-    int prefix = 0, from = 0;
-    if (b < c.batch) {
-      r = request_of(c, b);
-      if (r.t1 > r.t0) {
-        const int g = group_of(b);
-        prefix = g >= 0 ? limit[g] : 0;
-        const int4 v = g >= 0 ? group[g] : make_int4(b, 0, 0, 0);
-        from = v.w > 0 ? g | (int)0x80000000 : v.x;
-        atomicMax(&s_most, tiles_of(from < 0 ? 0 : prefix, prefix, r.len - r.count + (r.t1 - 1 - r.first), cap, shift));
-      }
+    Request r = mine;
+    int g = group0, prefix = 0, from = 0;
+    if (base > 0) {
+      r = {0, 0, 0, 0, 0};
+      if (b < c.batch) r = request_of(c, b);
+      g = r.t1 > r.t0 ? group_of(b) : -1;
+    }
+    if (r.t1 > r.t0) {
+      prefix = g >= 0 ? limit[g] : 0;
+      const int4 v = g >= 0 ? group[g] : make_int4(b, 0, 0, 0);
+      from = v.w > 0 ? g | (int)0x80000000 : v.x;
     }
     const int pos0 = r.len - r.count - r.first;
     const bool many = r.t1 - r.t0 > 8;
     if (!many)
-      for (int t = r.t0; t < r.t1; ++t) plan.token[t] = make_int4(b, from, pos0 + t, prefix);
+      for (int t = r.t0; t < r.t1; ++t) token[t] = make_int4(b, from, pos0 + t, prefix);
     for (uint32_t left = __ballot_sync(0xffffffffu, many); left != 0; left &= left - 1) {
       const int at = __ffs(left) - 1;
       const int t0 = __shfl_sync(0xffffffffu, r.t0, at), t1 = __shfl_sync(0xffffffffu, r.t1, at);
       const int4 v = make_int4(__shfl_sync(0xffffffffu, b, at), __shfl_sync(0xffffffffu, from, at),
                                __shfl_sync(0xffffffffu, pos0, at), __shfl_sync(0xffffffffu, prefix, at));
-      for (int t = t0 + lane; t < t1; t += 32) plan.token[t] = make_int4(v.x, v.y, v.z + t, v.w);
+      for (int t = t0 + lane; t < t1; t += 32) token[t] = make_int4(v.x, v.y, v.z + t, v.w);
     }
   }
   __syncthreads();
 
   // where the segments begin: in cost, in units (blocks of 64 rows), in units whose results are partial in any case
-  const bool near_segments = segments <= kNearSegments;
   int64_t* const cost_of = near_segments ? s_cost : plan.cost_of;
   int* const unit_of = near_segments ? s_unit : plan.unit_of;
+  int* const shared_of = near_segments ? s_shared : plan.shared_of;
   int64_t cost0 = 0;
   int unit0 = 0, shared0 = 0;
   for (int base = 0; base < segments; base += kThreads) {
@@ -217,7 +224,8 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
         units = blocks_of(v.z);
       }
     } else if (s < segments) {
-      const int4 v = plan.token[s - plan.groups];
+      const int4 v = token[s - plan.groups];
+      if (near_segments) plan.token[s - plan.groups] = v;
       if (v.x >= 0) {
         shared = v.y < 0;
         tiles = tiles_of(shared ? 0 : v.w, v.w, v.z, cap, shift);
@@ -232,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
       const int unit = unit0 + (int)(counts & 0xffffffff);
       plan.cost_of[s] = cost_of[s] = cost0 + cost;
       plan.unit_of[s] = unit_of[s] = unit;
-      plan.shared_of[s] = shared0 + (int)(counts >> 32);
+      plan.shared_of[s] = shared_of[s] = shared0 + (int)(counts >> 32);
     }
     cost0 += all_cost;
     unit0 += (int)(all_counts & 0xffffffff);
@@ -264,21 +272,30 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
     s_end[i] = end;
     s_segment[i] = s;
   }
+  // what the merge needs of its group's prefix, for each token
+  for (int t = threadIdx.x; t < T && groups > 0; t += kThreads) {
+    const int4 v = token[t];
+    if (v.x < 0 || v.y >= 0) continue;
+    const int g = v.y & 0x7fffffff;
+    const int64_t cost = cost_of[g];
+    plan.prefix_of[t] = make_int4((int)(cost & 0xffffffff), (int)(cost >> 32), shared_of[g], (t - group[g].y) * p.H);
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < sms; i += kThreads)
     plan.share[i] = make_int4(s_first[i], max(0, s_end[i + 1] - s_first[i]), s_segment[i], 0);
   if (threadIdx.x == 0) {
     *plan.share_cost = share;
     *plan.share_by = cost0 >> 34 == 0 && share >> 29 == 0 ? ~0ull / (uint64_t)share + 1 : 0;
-    *plan.few = (int64_t)s_most * kPlanTile / share + 2 <= kFewPieces;
   }
 }
 
 // ------------------------------------------------------------------- merge
-// Weights 2^(LSE_s - LSE) of a head's partials, then the sink and bmm2.  A warp a
-// head, 16 dims a lane, where no list has more than kFewPieces; else the eight warps
-// of a CTA share a head's partials.
+// Weights 2^(LSE_s - LSE) of a head's partials, then the sink and bmm2.  A warp a head,
+// 16 dims a lane; where there are many partials, the eight warps of a CTA share those
+// of one head after another.  (A CTA a head, four teams of threads to share its partials:
+// 60 us more, for starting CTAs that find nothing to do.)
 constexpr int kMergeWarps = 8;
+constexpr int kManyPartials = 24;
 
 // A head's partials: of the prefix, then of the token's own list; one for each share
 // that the block has tiles in.
@@ -294,136 +311,160 @@ __device__ __forceinline__ int64_t partial_row(const Partials& q, int s) {
   return (int64_t)(q.own + s * q.own_step + (s == 0 ? q.own_first : 0)) * kWindowHeads + q.own_row;
 }
 
-__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const WindowParams p, const PrefixPlan plan) {
-  __shared__ float s_weight[kMergeWarps][2 * kFewPieces];
-  __shared__ float s_all[2 * kMaxShares];
+// Items: where prefixes can be shared, eight heads of each token; then, for shares 1 and
+// up, sixteen heads of a block that the share's beginning cuts (the second share of the
+// block merges it).
+constexpr int kCutHeads = 2 * kMergeWarps, kCutItems = kWindowHeads / kCutHeads, kMergeCtas = 3;
+
+__global__ void __launch_bounds__(kMergeWarps * 32, kMergeCtas) prefix_merge_kernel(const WindowParams p, const PrefixPlan plan, int64_t token_items) {
   __shared__ float4 s_share[kMergeWarps][kHeadDim / 4];
-  __shared__ float s_top[kMergeWarps], s_sum[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sms = plan.shares, T = p.c.sum_q;
+  const int shares = plan.shares, per_token = (p.H + kMergeWarps - 1) / kMergeWarps;
   const int shift = cache_box_shift(p.c.page_size), cap = p.c.max_pages * p.c.page_size;
   await_prior_kernel();
   admit_next_kernel();
-  const int64_t share = __ldcg(plan.share_cost);
+  const int64_t share = __ldcg(plan.share_cost), items = token_items + (shares - 1) * kCutItems;
   const uint64_t by = __ldcg(plan.share_by);
-  const bool few = __ldcg(plan.few) != 0;
-  const int each = few ? kMergeWarps : 1, items = (p.H + each - 1) / each;      // heads of a CTA, of a token
-  for (int64_t i = blockIdx.x; i < (int64_t)T * items; i += gridDim.x) {
-    const int t = (int)(i / items), h = (int)(i - (int64_t)t * items) * each + (few ? warp : 0);
-    const int4 v = __ldcg(plan.token + t);
-    const int64_t cost = __ldcg(plan.cost_of + plan.groups + t);
-    const int unit = __ldcg(plan.unit_of + plan.groups + t), shared = __ldcg(plan.shared_of + plan.groups + t);
-    if (v.x < 0 || (few && h >= p.H)) continue;
-    Partials q = {};
-    const int tiles = tiles_of(v.y < 0 ? 0 : v.w, v.w, v.z, cap, shift);
-    if (tiles > 0) {
-      const int block = h / kWindowHeads;
-      const int64_t at = cost + block * plan_cost(tiles) + kPlanUnit;
-      const int c0 = share_of(at, share, by), c1 = share_of(at + (int64_t)(tiles - 1) * kPlanTile, share, by);
-      q.own_row = h % kWindowHeads;
-      q.owns = c1 - c0 + 1;
-      if (v.y < 0) {
-        q.own = 2 * sms + shared + block + c0;
-        q.own_step = 1;
-      } else if (q.owns == 1) {
-        q.owns = 0;                               // done whole
-      } else {
-        q.own = 2 * c0;
-        q.own_step = 2;
-        q.own_first = __ldcg(plan.share + c0).x != unit + block;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    int t, h0, heads = kMergeWarps, tiles, own = 0, owns = 0, own_first = 0, own_step = 1, row0 = -1, prefix_tiles = 0, shared = 0;
+    int64_t prefix_at = 0;
+    if (item >= token_items) {
+      const int cut = (int)(item - token_items), i = 1 + cut / kCutItems;
+      const int4 mine = __ldcg(plan.share + i);
+      const int before = __ldcg(plan.share + i - 1).x;
+      if (mine.y == 0 || mine.z < plan.groups) continue;
+      t = mine.z - plan.groups;
+      const int4 v = __ldcg(plan.token + t);
+      const int block = mine.x - __ldcg(plan.unit_of + mine.z);
+      tiles = tiles_of(v.w, v.w, v.z, cap, shift);
+      const int64_t at = __ldcg(plan.cost_of + mine.z) + block * plan_cost(tiles) + kPlanUnit;
+      if (v.y < 0 || at >= i * share || at < (i - 1) * share) continue;   // shared, or not its second one
+      h0 = block * kWindowHeads + cut % kCutItems * kCutHeads;
+      heads = kCutHeads;
+      own = 2 * (i - 1);
+      own_step = 2;
+      own_first = before != mine.x;
+      owns = share_of(at + (int64_t)(tiles - 1) * kPlanTile, share, by) - (i - 1) + 1;
+    } else {
+      t = (int)(item / per_token);
+      h0 = (int)(item - (int64_t)t * per_token) * kMergeWarps;
+      const int4 v = __ldcg(plan.token + t), w = __ldcg(plan.prefix_of + t);
+      const int64_t cost = __ldcg(plan.cost_of + plan.groups + t);
+      const int units = __ldcg(plan.shared_of + plan.groups + t);
+      if (v.x < 0 || v.y >= 0) continue;
+      tiles = tiles_of(0, v.w, v.z, cap, shift);
+      if (tiles > 0) {
+        const int block = h0 / kWindowHeads;      // (eight heads from a multiple of eight lie in one)
+        const int64_t at = cost + block * plan_cost(tiles) + kPlanUnit;
+        const int c0 = share_of(at, share, by);
+        own = 2 * shares + units + block + c0;
+        owns = share_of(at + (int64_t)(tiles - 1) * kPlanTile, share, by) - c0 + 1;
       }
+      row0 = w.w;
+      shared = w.z;
+      prefix_at = ((int64_t)w.y << 32 | (uint32_t)w.x) + kPlanUnit;
+      prefix_tiles = tiles_of(v.w, 0, -1, cap, shift);
     }
-    if (v.y < 0) {
-      const int g = v.y & 0x7fffffff;
-      const int4 w = __ldcg(plan.group + g);
-      const int row = (t - w.y) * p.H + h, block = row / kWindowHeads;
-      const int n = tiles_of(w.w, 0, -1, cap, shift);
-      const int64_t at = __ldcg(plan.cost_of + g) + block * plan_cost(n) + kPlanUnit;
-      const int c0 = share_of(at, share, by);
-      q.prefixes = share_of(at + (int64_t)(n - 1) * kPlanTile, share, by) - c0 + 1;
-      q.prefix = 2 * sms + __ldcg(plan.shared_of + g) + block + c0;
-      q.prefix_row = row % kWindowHeads;
-    }
-    const int n = q.prefixes + q.owns;
-    if (n == 0) continue;
-    const int first = few ? lane : (int)threadIdx.x, step = few ? 32 : kMergeWarps * 32;
-    float* const weight = few ? s_weight[warp] : s_all;
-    float top = -INFINITY, sum = 0.f;
-    bool nan = false;
-    for (int s = first; s < n; s += step) {
-      const float l = __ldcg(p.part_lse + partial_row(q, s));
-      weight[s] = l;
-      nan |= isnan(l);
-      top = fmaxf(top, l);
-    }
-    top = ptx::warp_max(top);
-    if (few) {
+    const auto head = [&](int h) {                // the partials of head h
+      Partials q = {0, 0, own, owns, own_first, own_step, 0, h % kWindowHeads};
+      if (row0 >= 0) {
+        const int row = row0 + h, block = row / kWindowHeads;
+        const int64_t at = prefix_at + block * plan_cost(prefix_tiles);
+        const int c0 = share_of(at, share, by);
+        q.prefix = 2 * shares + shared + block + c0;
+        q.prefixes = share_of(at + (int64_t)(prefix_tiles - 1) * kPlanTile, share, by) - c0 + 1;
+        q.prefix_row = row % kWindowHeads;
+      }
+      return q;
+    };
+    // (the same for all the CTA's heads, whose prefix blocks may differ by a piece)
+    const bool many = owns + (int)(prefix_tiles * kPlanTile / share) > kManyPartials;
+    for (int h = h0 + (many ? 0 : warp); h < min(h0 + heads, p.H); h += many ? 1 : kMergeWarps) {
+      const Partials q = head(h);
+      const int n = q.prefixes + q.owns;
+      float top = -INFINITY, sum = 0.f;
+      bool nan = false;
+      for (int s = lane; s < n; s += 32) {
+        const float l = fetch(p.part_lse + partial_row(q, s));
+        nan |= isnan(l);
+        top = fmaxf(top, l);
+      }
+      top = ptx::warp_max(top);
       nan = __any_sync(0xffffffffu, nan);
-    } else {
-      if (lane == 0) s_top[warp] = top;
-      nan = __syncthreads_or(nan);
-#pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, s_top[w]);
-    }
-    for (int s = first; s < n; s += step) {
-      const float w = weight[s] == -INFINITY ? 0.f : fast_exp2(weight[s] - top);
-      weight[s] = w;
-      sum += w;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (few) {
-      __syncwarp();
-    } else {
-      if (lane == 0) s_sum[warp] = sum;
-      __syncthreads();
-      sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) sum += s_sum[w];
-    }
-    float4 acc[4] = {};
-#pragma unroll 2
-    for (int s = few ? 0 : warp; s < n; s += few ? 1 : kMergeWarps) {
-      const float w = weight[s];
-      if (w == 0.f) continue;                     // an empty partial is not written
-      const float4* o = reinterpret_cast<const float4*>(p.part_o + partial_row(q, s) * kHeadDim) + lane;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 x = __ldcg(o + 32 * k);
-        acc[k].x = fmaf(w, x.x, acc[k].x), acc[k].y = fmaf(w, x.y, acc[k].y);
-        acc[k].z = fmaf(w, x.z, acc[k].z), acc[k].w = fmaf(w, x.w, acc[k].w);
-      }
-    }
-    float lse = -INFINITY, f = 0.f;
-    if (top != -INFINITY || nan) {
-      lse = nan ? NAN : top + fast_log2(sum);
-      f = fetch_scale(p.bmm2, p.bmm2_dev) / sum;
-      if (p.sinks != nullptr) f *= 1.f / (1.f + fast_exp2(fetch(p.sinks + h) * kLog2e - lse));
-    }
-    const int64_t th = (int64_t)t * p.H + h;
-    if (!few) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s_share[warp][lane + 32 * k] = acc[k];
-      __syncthreads();
-      if (threadIdx.x < kHeadDim / 4) {
-        float4 a = s_share[0][threadIdx.x];
-#pragma unroll
-        for (int w = 1; w < kMergeWarps; ++w) {
-          const float4 x = s_share[w][threadIdx.x];
-          a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+      float4 acc[4] = {};
+      const int first = many ? warp : 0, step = many ? kMergeWarps : 1;
+      for (int s0 = first; s0 < n; s0 += 32 * step) {
+        // lane k's partial is s0 + k * step
+        const int mine = s0 + lane * step;
+        float w = 0.f;
+        if (mine < n) {
+          const float l = fetch(p.part_lse + partial_row(q, mine));
+          w = l == -INFINITY ? 0.f : fast_exp2(l - top);
+          sum += w;
         }
-        *reinterpret_cast<uint2*>(p.out + th * kHeadDim + threadIdx.x * 4) =
-            make_uint2(tc::pack_bf16x2(a.x * f, a.y * f), tc::pack_bf16x2(a.z * f, a.w * f));
-      }
-      if (threadIdx.x == 0 && p.out_lse) p.out_lse[th] = lse;
-      __syncthreads();
-    } else {
+        const int here = min(32, (n - s0 + step - 1) / step);
+#pragma unroll 1
+        for (int k = 0; k < here; k += 2) {
+          float weight[2];
+          float4 o[2][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint2*>(p.out + th * kHeadDim + (lane + 32 * k) * 4) =
-            make_uint2(tc::pack_bf16x2(acc[k].x * f, acc[k].y * f), tc::pack_bf16x2(acc[k].z * f, acc[k].w * f));
-      if (lane == 0 && p.out_lse) p.out_lse[th] = lse;
-      __syncwarp();
+          for (int e = 0; e < 2; ++e) {
+            weight[e] = __shfl_sync(0xffffffffu, w, (k + e) & 31);
+            if (k + e >= here) weight[e] = 0.f;
+            const float4* from = reinterpret_cast<const float4*>(p.part_o + partial_row(q, s0 + (k + e) * step) * kHeadDim) + lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {         // (an empty partial is not written)
+              o[e][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (weight[e] != 0.f) o[e][i] = __ldcg(from + 32 * i);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              acc[i].x = fmaf(weight[e], o[e][i].x, acc[i].x), acc[i].y = fmaf(weight[e], o[e][i].y, acc[i].y);
+              acc[i].z = fmaf(weight[e], o[e][i].z, acc[i].z), acc[i].w = fmaf(weight[e], o[e][i].w, acc[i].w);
+            }
+        }
+      }
+      if (many) {                                 // (each warp has the weights of its own partials)
+        sum = 0.f;
+        for (int s = lane; s < n; s += 32) {
+          const float l = fetch(p.part_lse + partial_row(q, s));
+          if (l != -INFINITY) sum += fast_exp2(l - top);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      float lse = -INFINITY, f = 0.f;
+      if (top != -INFINITY || nan) {
+        lse = nan ? NAN : top + fast_log2(sum);
+        f = fetch_scale(p.bmm2, p.bmm2_dev) / sum;
+        if (p.sinks != nullptr) f *= 1.f / (1.f + fast_exp2(fetch(p.sinks + h) * kLog2e - lse));
+      }
+      const int64_t th = (int64_t)t * p.H + h;
+      if (many) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s_share[warp][lane + 32 * i] = acc[i];
+        __syncthreads();
+        if (threadIdx.x < kHeadDim / 4) {
+          float4 a = s_share[0][threadIdx.x];
+#pragma unroll
+          for (int w = 1; w < kMergeWarps; ++w) {
+            const float4 x = s_share[w][threadIdx.x];
+            a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+          }
+          *reinterpret_cast<uint2*>(p.out + th * kHeadDim + threadIdx.x * 4) =
+              make_uint2(tc::pack_bf16x2(a.x * f, a.y * f), tc::pack_bf16x2(a.z * f, a.w * f));
+        }
+        __syncthreads();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint2*>(p.out + th * kHeadDim + (lane + 32 * i) * 4) =
+              make_uint2(tc::pack_bf16x2(acc[i].x * f, acc[i].y * f), tc::pack_bf16x2(acc[i].z * f, acc[i].w * f));
+      }
+      if (lane == 0 && (!many || warp == 0) && p.out_lse) p.out_lse[th] = lse;
     }
   }
 }
@@ -434,9 +475,12 @@ cudaError_t launch_prefix_attention(const WindowParams& p, const PrefixPlan& pla
   cudaError_t e = launch_overlapped(prefix_plan_kernel, dim3(1), kThreads, 0, stream, p, plan, cache_box_shift(p.c.page_size));
   if (e == cudaSuccess) e = launch_planned_attention(p, plan, stream);
   if (e != cudaSuccess) return e;
-  const int64_t rows = (int64_t)p.c.sum_q * p.H;
-  return launch_overlapped(prefix_merge_kernel, dim3((unsigned)std::min<int64_t>(rows, (int64_t)plan.shares * 8)), kMergeWarps * 32, 0,
-                           stream, p, plan);
+  const int64_t token_items = plan.groups > 0 && p.H % kWindowHeads != 0
+                                  ? (int64_t)p.c.sum_q * ((p.H + kMergeWarps - 1) / kMergeWarps) : 0;
+  const int64_t items = token_items + (plan.shares - 1) * kCutItems;
+  if (items == 0) return cudaSuccess;
+  return launch_overlapped(prefix_merge_kernel, dim3((unsigned)std::min<int64_t>(items, (int64_t)plan.shares * kMergeCtas)),
+                           kMergeWarps * 32, 0, stream, p, plan, token_items);
 }
 
 }  // namespace smla

@@ -43,13 +43,13 @@ struct SparseSlotsParams {
 cudaError_t launch_sparse_slots(const SparseSlotsParams& p, int sms, cudaStream_t stream);
 
 // How a call's logits are cut: blocks of the 512 bytes that a warp loads at once,
-// of which only the maxima are kept; units of `unit_blocks` consecutive blocks of
+// of which only the maxima are kept; units of 2^unit_shift consecutive blocks of
 // a row, a warp each, which give the partial sums.
 struct BeamPlan {
-  int32_t blocks, unit_blocks, units;
+  int32_t blocks, unit_shift, units;
 };
 constexpr int kBeamBlockBytes = 512;
-constexpr int kMaxUnitBlocks = 32;
+constexpr int kMinUnitShift = 2, kMaxUnitShift = 4;
 constexpr int64_t kMaxBeamBlocks = 1ll << 30;   // of a request
 
 struct BeamParams {
@@ -67,6 +67,6 @@ struct BeamParams {
   float2* partial;                   // [rows, units] maximum, sum of e^(x - maximum)
   int32_t* err;
 };
-cudaError_t launch_beam_select(const BeamParams& p, cudaStream_t stream);
+cudaError_t launch_beam_select(const BeamParams& p, int sms, cudaStream_t stream);
 
 }  // namespace smla

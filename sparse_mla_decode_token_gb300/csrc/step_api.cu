@@ -47,15 +47,16 @@ smla_status check_beam(const smla_beam_args* a) {
   return SMLA_OK;
 }
 
-// Units of up to 32 blocks, shorter ones where there would not be sixteen warps
-// of them for each SM.
+// Units of up to 16 blocks, shorter ones where there would not be 32 of them for
+// each SM (as many as it holds warps).
 BeamPlan beam_plan(const smla_beam_args* a, int sms) {
   const int size = a->dtype == SMLA_LOGITS_FP32 ? 4 : 2, block = kBeamBlockBytes / size;
   BeamPlan plan;
   plan.blocks = (int32_t)(((int64_t)a->vocab + 16 / size - 1 + block - 1) / block);   // (a row begins up to 15 bytes behind a boundary)
   const int64_t all = (int64_t)plan.blocks * a->batch * a->beams;
-  plan.unit_blocks = (int32_t)std::min<int64_t>(kMaxUnitBlocks, std::max<int64_t>(4, all / ((int64_t)sms * 16)));
-  plan.units = (plan.blocks + plan.unit_blocks - 1) / plan.unit_blocks;
+  plan.unit_shift = kMaxUnitShift;
+  while (plan.unit_shift > kMinUnitShift && all >> plan.unit_shift < (int64_t)sms * 32) --plan.unit_shift;
+  plan.units = (plan.blocks + (1 << plan.unit_shift) - 1) >> plan.unit_shift;
   return plan;
 }
 
@@ -185,8 +186,9 @@ smla_status smla_beam_select(const smla_beam_args* a, void* stream) {
   BeamParams p;
   memset(&p, 0, sizeof(p));
   p.plan = beam_plan(a, sms);
-  if ((int64_t)p.plan.blocks * a->beams > kMaxBeamBlocks)
-    return fail(SMLA_ERR_UNSUPPORTED, "%d beams over a vocabulary of %d are too many blocks", a->beams, a->vocab);
+  if ((int64_t)p.plan.blocks * a->beams > kMaxBeamBlocks || (int64_t)p.plan.units * a->beams * a->batch > 0x7fffffff)
+    return fail(SMLA_ERR_UNSUPPORTED, "%d requests of %d beams over a vocabulary of %d are too many blocks", a->batch,
+                a->beams, a->vocab);
   const BeamLayout layout = beam_layout(a, p.plan);
   SMLA_TRY(need_workspace(a->workspace, a->workspace_bytes, layout.bytes));
   p.batch = a->batch;
@@ -205,7 +207,7 @@ smla_status smla_beam_select(const smla_beam_args* a, void* stream) {
   p.block_max = static_cast<float*>(a->workspace);
   p.partial = reinterpret_cast<float2*>(static_cast<char*>(a->workspace) + layout.partial);
   p.err = a->error_word;
-  return launched("beam select", launch_beam_select(p, static_cast<cudaStream_t>(stream)));
+  return launched("beam select", launch_beam_select(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -153,7 +153,7 @@ def test_beam_finished(dtype):
     logits, scores = likely(g, 24, 1500, dtype), -torch.rand(3, 8, generator=g, device=DEV) * 8
     finished = torch.rand(3, 8, generator=g, device=DEV) < 0.5
     finished[1], finished[2] = True, False
-    logits[8:16] = math.nan                                          # (a finished beam's logits are not read)
+    logits[8:16] = math.nan                                          # (a finished beam's logits do not count)
     got = select(logits, scores, 12, finished, end=1499)
     check(got, logits, scores, 12, finished, 1499)
     assert np.isfinite(got[0][1]).sum() == 8 and np.all(got[2][1, :8] == 1499)

@@ -64,6 +64,20 @@ __device__ __forceinline__ void unpack(uint4 v, float (&x)[8], const __half*) {
   }
 }
 
+// Four elements, at a multiple of four from a 16-byte boundary.
+__device__ __forceinline__ void load_four(const float* at, float (&x)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(at);
+  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+}
+template <class T>
+__device__ __forceinline__ void load_four(const T* at, float (&x)[4]) {
+  const uint2 v = *reinterpret_cast<const uint2*>(at);
+  float y[8];
+  unpack(make_uint4(v.x, v.y, 0, 0), y, at);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = y[e];
+}
+
 // A row's logits from the 16-byte boundary at or before its first: element e of
 // the row is element e + before of `base`.
 template <class T>
@@ -289,8 +303,9 @@ constexpr int kPickThreads = 1024;
 constexpr int kGroups = kPickThreads / 8;         // of entries, whose best ones bound the K-th best of all
 constexpr int kDirect = 64;                       // entries ranked without such a bound
 constexpr int kMany = 512;                        // entries that are not ranked before equal ones are told apart
-constexpr int kTile = 4096;                       // keys gathered at a time
-constexpr int kGathered = kTile + SMLA_MAX_BEAM_OUT;
+constexpr int kTile = 8192;                       // keys looked at at a time,
+constexpr int kSureTile = 4096;                   // at a time that may all be enough (equal scores)
+constexpr int kGathered = kSureTile + SMLA_MAX_BEAM_OUT;
 static_assert(kGroups >= SMLA_MAX_BEAM_OUT, "a K-th best group");
 
 struct List {
@@ -306,7 +321,7 @@ struct List {
     int at = 0;
     if (lane == 0) at = atomicAdd(count, __popc(all));
     at = __shfl_sync(0xffffffffu, at, 0) + __popc(all & ((1u << lane) - 1u));
-    if (add) set(at, r);
+    if (add && at < kGathered) set(at, r);
   }
 };
 
@@ -354,15 +369,17 @@ __device__ __noinline__ int narrow(Pick& sh, int keep, int n) {
   return sh.reaching;
 }
 
-// The K best of sh.list's `count` entries, in order, to sh.best; sh.chosen are those in
-// rising order of their indices (beam * per_beam + number), so that positions in what
-// they stand for compare like (beam, token); sh.cut what the K-th best asks of the next
-// step's logits.  Each of 128 groups of entries has a best score; the K-th best of
-// those is a lower bound of the K-th best of all, which for entries in no particular
-// order hardly more than K reach; an entry's rank is then the number of better ones.
-// Whole CTA.  (Out of line, once for all steps: what this kernel costs is latency, of
-// which instructions fetched for the first time are a part.)
-__device__ __noinline__ void settle(Pick& sh, int keep, int count, int per_beam, int beams) {
+// What is left of sh.list's `count` entries: the K best, in order, in sh.best; or a few
+// more, up to `room`, in no order.  sh.chosen
+// are those in rising order of their indices (beam * per_beam + number), so that
+// positions in what they stand for compare like (beam, token); sh.cut what the next
+// step's logits have to be.  Each of 128 groups of entries has a best score; the K-th
+// best of those is a lower bound of the K-th best of all, which for entries in no
+// particular order hardly more than K reach; an entry's rank is then the number of
+// better ones.  Whole CTA.  (Out of line, once for all steps: what this kernel costs is
+// latency, of which instructions fetched for the first time are a part.)
+__device__ __noinline__ void settle(Pick& sh, int keep, int count, int per_beam, int beams, int room) {
+  uint32_t least = sh.least;
   List* list = &sh.list;
   if (count > kDirect) {
     const int group = threadIdx.x / 8, lane = threadIdx.x % 8;
@@ -387,6 +404,7 @@ __device__ __noinline__ void settle(Pick& sh, int keep, int count, int per_beam,
     if (lane == 0 && rank == keep - 1) sh.bound.hi = top;
     __syncthreads();
     const uint32_t bound = max(sh.bound.hi, 1u);
+    least = max(least, bound);
     for (int base = 0; base < count; base += kPickThreads) {
       const int i = base + (int)threadIdx.x;
       const Rank r = sh.list.get(min(i, count - 1));
@@ -400,7 +418,7 @@ __device__ __noinline__ void settle(Pick& sh, int keep, int count, int per_beam,
       list = &sh.list;
     }
   }
-  {
+  if (count > room) {
     const int lane = threadIdx.x % 8;
     for (int base = 0; base < count; base += kPickThreads / 8) {
       const int i = base + (int)threadIdx.x / 8;
@@ -416,10 +434,14 @@ __device__ __noinline__ void settle(Pick& sh, int keep, int count, int per_beam,
       for (int o = 1; o < 8; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
       if (lane == 0 && i < count && rank < keep) sh.best[rank] = mine;
     }
+    __syncthreads();
+    if (count >= keep) least = max(least, sh.best[keep - 1].hi);
+    count = min(keep, count);
+  } else {
+    if (threadIdx.x < count) sh.best[threadIdx.x] = list->get(threadIdx.x);
+    __syncthreads();
   }
-  __syncthreads();
-  const int found = min(keep, count);
-  const uint32_t least = found == keep ? sh.best[keep - 1].hi : 0;
+  const int found = count;
   {
     constexpr int kEach = kPickThreads / SMLA_MAX_BEAM_OUT;      // threads for each
     const int i = threadIdx.x / kEach, lane = threadIdx.x % kEach;
@@ -443,33 +465,54 @@ __device__ __noinline__ void settle(Pick& sh, int keep, int count, int per_beam,
 
 // The K best of n keys, of which at least K reach sh.least where that is not 0: a tile
 // of keys at a time is gathered (those that are enough) and settled beside the best
-// ones so far.  load(i) is the number that key(i, number) is made of, always read, so
-// that four a thread are on their way at a time.  Keys that reach the bound are little
-// more than K, but for ties.
-template <class L, class F>
-__device__ __forceinline__ void pick(Pick& sh, int keep, int64_t n, int per_beam, int beams, L load, F key) {
-  int found = 0;
-  for (int64_t tile = 0; tile < n || tile == 0; tile += kTile) {
-    const int here = (int)min(n - tile, (int64_t)kTile);
+// ones so far.  load(i, x) gives the numbers of keys i .. i + kEach - 1, always, so that
+// all of a thread's are on their way at a time; enough(i, number) says whether key i may
+// count, rank(i, number) is its rank.  Keys that reach the bound are little more than K,
+// but for ties.  `room`: keys that the next step takes; 0: this is the last.
+template <int kEach, class L, class E, class F>
+__device__ __forceinline__ void pick(Pick& sh, int keep, int64_t n, int per_beam, int beams, int room, L load, E enough, F rank) {
+  constexpr int kRounds = kTile / kPickThreads / kEach;
+  int found = 0, most = kTile;
+  for (int64_t tile = 0; tile < n || tile == 0;) {
+    const int here = (int)min(n - tile, (int64_t)most);
     const uint32_t least = sh.least;
     if (threadIdx.x == 0) sh.count = found;
     if (threadIdx.x < found) sh.list.set(threadIdx.x, sh.best[threadIdx.x]);
-    float x[kTile / kPickThreads];
+    float x[kRounds][kEach];
 #pragma unroll
-    for (int k = 0; k < kTile / kPickThreads; ++k)
-      x[k] = k * kPickThreads < here ? load(tile + min(k * kPickThreads + (int)threadIdx.x, here - 1)) : 0.f;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kTile / kPickThreads; ++k) {
-      const int i = k * kPickThreads + (int)threadIdx.x;
-      if (k * kPickThreads >= here) break;
-      Rank r = {0, 0, 0};
-      if (i < here) r = key(tile + i, x[k]);
-      sh.list.append(&sh.count, r.hi != 0 && r.hi >= least, r);
+    for (int k = 0; k < kRounds; ++k) {
+      const int i = (k * kPickThreads + (int)threadIdx.x) * kEach;
+      if (k * kPickThreads * kEach < here) load(tile + min(i, here - kEach), x[k]);
     }
     __syncthreads();
-    settle(sh, keep, sh.count, per_beam, beams);
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+      const int i = (k * kPickThreads + (int)threadIdx.x) * kEach;
+      if (k * kPickThreads * kEach >= here) break;
+      uint32_t maybe = 0;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) maybe |= (uint32_t)(i < here && enough(tile + i + e, x[k][e])) << e;
+      if (kEach > 1 && !__any_sync(0xffffffffu, maybe != 0)) continue;
+#pragma unroll 1
+      for (int e = 0; e < kEach; ++e) {           // (few get here, where there are many)
+        float y = x[k][0];
+#pragma unroll
+        for (int c = 1; c < kEach; ++c) y = e == c ? x[k][c] : y;
+        Rank r = {0, 0, 0};
+        if (maybe >> e & 1) r = rank(tile + i + e, y);
+        sh.list.append(&sh.count, r.hi != 0 && r.hi >= least, r);
+      }
+    }
+    __syncthreads();
+    const int count = sh.count;
+    if (count > kGathered) {                      // once more, in tiles that are sure to fit
+      most = kSureTile;
+      __syncthreads();
+      continue;
+    }
+    settle(sh, keep, count, per_beam, beams, n > here ? 0 : room);
     found = sh.found;
+    tile += here > 0 ? here : 1;
   }
 }
 
@@ -528,32 +571,38 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
   __syncthreads();
 
   // the best units, the best blocks of those, the best elements of those
+  constexpr int kBlock = Vec<T>::kBlock;
   const int keep = p.num_out, shift = p.plan.unit_shift, units = p.plan.units, blocks = p.plan.blocks;
   const float2* part = p.partial + row0 * units;
-  pick(
-      sh, keep, (int64_t)p.beams * units, units, p.beams, [&](int64_t at) { return fetch(&part[at].x); },
+  pick<1>(
+      sh, keep, (int64_t)p.beams * units, units, p.beams, SMLA_MAX_BEAM_OUT,
+      [&](int64_t at, float (&x)[1]) { x[0] = fetch(&part[at].x); },
+      [&](int64_t, float) { return true; },
       [&](int64_t at, float x) -> Rank {
         const uint32_t i = (uint32_t)at / (uint32_t)units;
         if (sh.single[i] && at != (int64_t)i * units) return {0, 0, 0};
         return score_rank(sh.beam[i], sh.single[i] ? 0.f : x, (uint32_t)at);
       });
   const float* top = p.block_max + row0 * blocks;
-  pick(
-      sh, keep, sh.found << shift, blocks, p.beams,
-      [&](int64_t at) {
+  pick<1>(
+      sh, keep, sh.found << shift, blocks, p.beams, kSureTile / kBlock,
+      [&](int64_t at, float (&x)[1]) {
         const int2 unit = sh.chosen[(int)at >> shift];
-        return fetch(top + unit.x * blocks + min((unit.y << shift) + ((int)at & ((1 << shift) - 1)), blocks - 1));
+        x[0] = fetch(top + unit.x * blocks + min((unit.y << shift) + ((int)at & ((1 << shift) - 1)), blocks - 1));
+      },
+      [&](int64_t at, float x) {
+        const int2 unit = sh.chosen[(int)at >> shift];
+        const int j = (unit.y << shift) + ((int)at & ((1 << shift) - 1));
+        return sh.single[unit.x] ? j == 0 : j < blocks && !(x < sh.cut[unit.x]);
       },
       [&](int64_t at, float x) -> Rank {
         const int2 unit = sh.chosen[(int)at >> shift];
-        const int j = (unit.y << shift) + ((int)at & ((1 << shift) - 1));
-        const bool single = sh.single[unit.x];
-        if (single ? j != 0 : j >= blocks || x < sh.cut[unit.x]) return {0, 0, 0};
-        return score_rank(sh.beam[unit.x], single ? 0.f : x, (uint32_t)(unit.x * blocks + j));
+        return score_rank(sh.beam[unit.x], sh.single[unit.x] ? 0.f : x,
+                          (uint32_t)(unit.x * blocks + (unit.y << shift) + ((int)at & ((1 << shift) - 1))));
       });
   // (the blocks' elements: where they lie, which of them are the row's)
-  constexpr int kBlock = Vec<T>::kBlock;
   __shared__ const T* s_base[SMLA_MAX_BEAM_OUT];
+  __shared__ float s_cut[SMLA_MAX_BEAM_OUT];
   __shared__ int s_beam[SMLA_MAX_BEAM_OUT], s_from[SMLA_MAX_BEAM_OUT], s_to[SMLA_MAX_BEAM_OUT], s_token[SMLA_MAX_BEAM_OUT];
   if (threadIdx.x < sh.found) {
     const int k = threadIdx.x;
@@ -565,20 +614,32 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
     s_from[k] = (int)max(row.before - j, (int64_t)0);
     s_to[k] = (int)min(row.before + (int64_t)p.vocab - j, (int64_t)kBlock);
     s_token[k] = (int)(j - row.before);
-    if (sh.single[block.x]) s_to[k] = s_from[k] + 1;   // (one of a finished beam's stands for it)
+    s_cut[k] = sh.cut[block.x];
+    if (sh.single[block.x]) {                     // (one of a finished beam's stands for it)
+      s_to[k] = s_from[k] + 1;
+      s_cut[k] = -INFINITY;
+    }
   }
   __syncthreads();
-  pick(
-      sh, keep, sh.found * kBlock, 1, p.beams,
-      [&](int64_t at) {
-        const int k = (int)at / kBlock;
-        return element(s_base[k] + min(max((int)at % kBlock, s_from[k]), s_to[k] - 1));
+  pick<4>(
+      sh, keep, sh.found * kBlock, 1, p.beams, 0,
+      [&](int64_t at, float (&x)[4]) {
+        const int k = (int)at / kBlock, e = (int)at % kBlock;
+        const T* from = s_base[k] + e;
+        if (e >= s_from[k] && e + 4 <= s_to[k]) {
+          load_four(from, x);
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) x[i] = e + i >= s_from[k] && e + i < s_to[k] ? element(from + i) : 0.f;
+        }
+      },
+      [&](int64_t at, float x) {
+        const int k = (int)at / kBlock, e = (int)at % kBlock;
+        return e >= s_from[k] && e < s_to[k] && !(x < s_cut[k]);
       },
       [&](int64_t at, float x) -> Rank {
-        const int k = (int)at / kBlock, e = (int)at % kBlock, i = s_beam[k];
-        const bool single = sh.single[i];
-        if (e < s_from[k] || e >= s_to[k] || (!single && x < sh.cut[i])) return {0, 0, 0};
-        return score_rank(sh.beam[i], single ? 0.f : x, (uint32_t)at);
+        const int i = s_beam[(int)at / kBlock];
+        return score_rank(sh.beam[i], sh.single[i] ? 0.f : x, (uint32_t)at);
       });
   if (threadIdx.x < p.num_out) {
     float score = -INFINITY;

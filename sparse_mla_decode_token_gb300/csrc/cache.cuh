@@ -80,6 +80,9 @@ __device__ __forceinline__ int last_request(int batch, int lane, F before) {
   return lo;
 }
 
+constexpr int kWindowHeads = 64;      // heads of one token that a CTA takes
+constexpr int kWindowTile = 128;      // cache rows of one tile
+
 struct WindowParams {
   CacheView c;
   int32_t H, window, first_tokens;
@@ -97,20 +100,29 @@ struct WindowParams {
   int32_t* err;
 };
 
-constexpr int kWindowHeads = 64;      // heads of one token that a CTA takes
-constexpr int kWindowTile = 128;      // cache rows of one tile
 constexpr int kMaxWindowSplits = 256;
 
 // log2 of a TMA box's rows: the highest box that pages hold whole, up to a quarter
 // of a tile (fewer copies to issue).
 __host__ __device__ inline int cache_box_shift(int page_size) { return page_size % 32 == 0 ? 5 : page_size % 16 == 0 ? 4 : 3; }
 
+// What a CTA works on at a time: 64 heads of a token, a range of tiles of its chunk list.
+// In a plan, also 64 (token, head) rows of a group, and lists whose first chunks are
+// another request's.
+struct Unit {
+  int t, h0, heads, part, b;                      // part: its partial's number, or -1 (it writes the output)
+  int first_chunks, window_chunk, chunks;         // list: [0, first_chunks), then from window_chunk on
+  int pos, lo;                                    // last and first visible position of the window
+  int tile0, tiles;
+  int b0, first;                                  // plan: the request of the list's first chunks, their rows
+};
+
 // Plan of a batch whose groups share prefixes, made on the device (prefix_attention.cu).
 // Units are blocks of 64 (token, head) rows: those of the groups' shared prefixes,
 // then those of the tokens, all laid end to end by cost and cut into a share for each
 // SM.  Partials are numbered: two for each share (a block that its beginning, or
 // only its end, cuts), then for shared prefixes and their tokens by unit and share.
-constexpr int kPlanTile = 4, kPlanUnit = 11;      // cost of a tile; of a unit's query, sums and results
+constexpr int kPlanTile = 4, kPlanUnit = 9;       // cost of a tile; of a unit's query, sums and results
 constexpr int kMaxShares = 256;
 __host__ __device__ inline int64_t plan_cost(int tiles) { return kPlanUnit + (int64_t)(tiles > 0 ? tiles : 1) * kPlanTile; }
 struct PrefixPlan {
@@ -123,11 +135,60 @@ struct PrefixPlan {
   int32_t* unit_of;                     // [groups + T + 1] its first unit
   int32_t* shared_of;                   // [groups + T] the units of shared prefixes and their tokens before it
   int4* share;                          // [shares] first unit, units, the first one's segment
+  int4* first;                          // [shares][4] the first unit
   int4* group;                          // [groups] first request, first token, (token, head) rows, prefix (0: not shared)
   int4* token;                          // [T] request, its group's first one (or sign and group: shared), position, prefix
   int4* prefix_of;                      // [T] of a shared prefix: cost_of (two words), shared_of, the token's first row in it
   int32_t* limit;                       // [groups] positions that all the group's tokens see
 };
+
+// Unit `unit`, of `segment`, as far as it is share `share`'s; later: not the share's
+// first one.  (The arrays are given apart, as the plan's kernel has them in shared memory.)
+__device__ __forceinline__ Unit plan_unit(const CacheView& c, const PrefixPlan& plan, int H, int shift, int share,
+                                          int64_t share_cost, int unit, int segment, bool later, int32_t* err,
+                                          const int64_t* cost_of, const int* unit_of, const int* shared_of, const int4* group,
+                                          const int4* token) {
+  const int block = unit - fetch(unit_of + segment), shared = fetch(shared_of + segment);
+  int64_t at = fetch(cost_of + segment);
+  Unit u;
+  u.h0 = block * kWindowHeads;
+  bool partial = true;
+  if (segment < plan.groups) {                    // a group's prefix
+    const int4 g = fetch(group + segment);
+    const int row = g.y * H + u.h0;
+    u.heads = min(kWindowHeads, g.z - u.h0);
+    u.t = row / H;
+    u.h0 = row - u.t * H;
+    u.b = u.b0 = g.x;
+    u.first = g.w;
+    u.pos = -1;
+    u.lo = 0;
+  } else {
+    const int4 r = fetch(token + (segment - plan.groups));
+    partial = r.y < 0;
+    u.t = segment - plan.groups;
+    u.heads = min(kWindowHeads, H - u.h0);
+    u.b = r.x;
+    u.b0 = partial ? r.x : r.y;
+    u.first = partial ? 0 : r.w;                  // (a shared prefix is its group's)
+    u.pos = r.z;
+    u.lo = r.w;
+  }
+  const int last = min(u.pos, c.max_pages * c.page_size - 1);
+  if (u.pos > last && err != nullptr) atomicOr(err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
+  u.first_chunks = (u.first + (1 << shift) - 1) >> shift;
+  u.window_chunk = u.lo >> shift;
+  u.chunks = u.first_chunks + (last >= u.lo ? (last >> shift) - u.window_chunk + 1 : 0);
+  const int tiles = (u.chunks + (kWindowTile >> shift) - 1) >> (7 - shift);
+  at += block * plan_cost(tiles) + kPlanUnit;     // where its first tile begins
+  auto from = [&](int s) {                        // its first tile that begins in share s or behind it
+    return (int)min(max((s * share_cost - at + kPlanTile - 1) / kPlanTile, (int64_t)0), (int64_t)tiles);
+  };
+  u.tile0 = from(share);
+  u.tiles = from(share + 1) - u.tile0;
+  u.part = partial ? 2 * plan.shares + shared + block + share : u.tiles < tiles ? 2 * share + later : -1;
+  return u;
+}
 
 cudaError_t launch_planned_attention(const WindowParams& p, const PrefixPlan& plan, cudaStream_t stream);
 cudaError_t launch_prefix_attention(const WindowParams& p, const PrefixPlan& plan, cudaStream_t stream);

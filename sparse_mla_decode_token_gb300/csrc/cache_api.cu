@@ -203,7 +203,7 @@ smla_status check_prefix(const smla_prefix_args* a) {
 struct PrefixLayout {
   int64_t parts;
   int shares;
-  size_t lse, header, cost_of, unit_of, shared_of, share, group, token, prefix_of, limit, bytes;
+  size_t lse, header, cost_of, unit_of, shared_of, share, first, group, token, prefix_of, limit, bytes;
 };
 PrefixLayout prefix_layout(const smla_prefix_args* a, int sms) {
   const int64_t T = a->sum_q, heads = (a->num_heads + kWindowHeads - 1) / kWindowHeads;
@@ -226,6 +226,7 @@ PrefixLayout prefix_layout(const smla_prefix_args* a, int sms) {
   l.unit_of = take((segments + 1) * sizeof(int32_t));
   l.shared_of = take(segments * sizeof(int32_t));
   l.share = take((size_t)l.shares * sizeof(int4));
+  l.first = take((size_t)l.shares * 4 * sizeof(int4));
   l.group = take((size_t)a->num_groups * sizeof(int4));
   l.token = take((size_t)T * sizeof(int4));
   l.prefix_of = take((size_t)T * sizeof(int4));
@@ -399,6 +400,7 @@ smla_status smla_prefix_attention(const smla_prefix_args* a, void* stream) {
   plan.unit_of = reinterpret_cast<int32_t*>(ws + l.unit_of);
   plan.shared_of = reinterpret_cast<int32_t*>(ws + l.shared_of);
   plan.share = reinterpret_cast<int4*>(ws + l.share);
+  plan.first = reinterpret_cast<int4*>(ws + l.first);
   plan.group = reinterpret_cast<int4*>(ws + l.group);
   plan.token = reinterpret_cast<int4*>(ws + l.token);
   plan.prefix_of = reinterpret_cast<int4*>(ws + l.prefix_of);

@@ -14,7 +14,7 @@
 // prefix through the table of the group's first request.
 //
 // The lengths are on the device, so the plan is made there, by one CTA.  Each block
-// of 64 rows costs 2.75 tiles' time for its query, sums and results and one for each
+// of 64 rows costs 2.25 tiles' time for its query, sums and results and one for each
 // tile; all blocks laid end to end are cut into equal shares, one for each SM (a
 // tile is the CTA's in whose share it begins).  A block that a cut goes through is
 // given in pieces and merged.
@@ -281,8 +281,19 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
     plan.prefix_of[t] = make_int4((int)(cost & 0xffffffff), (int)(cost >> 32), shared_of[g], (t - group[g].y) * p.H);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < sms; i += kThreads)
-    plan.share[i] = make_int4(s_first[i], max(0, s_end[i + 1] - s_first[i]), s_segment[i], 0);
+  for (int i = threadIdx.x; i < sms; i += kThreads) {
+    const int units = max(0, s_end[i + 1] - s_first[i]);
+    plan.share[i] = make_int4(s_first[i], units, s_segment[i], 0);
+    if (units == 0) continue;
+    union {
+      int4 words[4];
+      Unit unit;
+    } first;
+    first.unit = plan_unit(c, plan, p.H, shift, i, share, s_first[i], s_segment[i], false, p.err, cost_of, unit_of, shared_of,
+                           group, token);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) plan.first[i * 4 + k] = first.words[k];
+  }
   if (threadIdx.x == 0) {
     *plan.share_cost = share;
     *plan.share_by = cost0 >> 34 == 0 && share >> 29 == 0 ? ~0ull / (uint64_t)share + 1 : 0;

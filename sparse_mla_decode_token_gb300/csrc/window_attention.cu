@@ -136,17 +136,6 @@ constexpr int kOffSmall = kOffP + 4 * kPHalf;
 // splits; by the plan of a batch whose groups share prefixes (prefix_attention.cu).
 constexpr int kPairs = 0, kSplitPairs = 1, kPlanned = 2;
 
-// What a CTA works on at a time: 64 heads of a token, a range of tiles of its chunk list.
-// In a plan, also 64 (token, head) rows of a group, and lists whose first chunks are
-// another request's.
-struct Unit {
-  int t, h0, heads, part, b;                      // part: its partial's number, or -1 (it writes the output)
-  int b0, first;                                  // plan: the request of the list's first chunks, their rows
-  int first_chunks, window_chunk, chunks;         // list: [0, first_chunks), then from window_chunk on
-  int pos, lo;                                    // last and first visible position of the window
-  int tile0, tiles;
-};
-
 struct alignas(16) Small {
   float qscale[kNH];                              // bmm1 log2(e) 2^-k of each head
   float negref[kNH];                              // headroom - reference of each head
@@ -189,60 +178,17 @@ __device__ __forceinline__ void unit_heads(const KernelParams& kp, int x, Unit* 
   u->heads = min(kNH, p.H - u->h0);
 }
 
-// Unit x of the CTA's share of a plan.
+// Unit x > 0 of the CTA's share of a plan (the first one stands in it).
 template <int kShift>
 __device__ __forceinline__ Unit planned_unit(const KernelParams& kp, int x, int lane) {
-  const WindowParams& p = kp.p;
-  const CacheView& c = p.c;
+  const CacheView& c = kp.p.c;
   const PrefixPlan& plan = kp.plan;
-  const int share = blockIdx.x;
-  const int4 mine = __ldcg(plan.share + share);
-  const int64_t share_cost = __ldcg(plan.share_cost);
+  const int4 mine = __ldcg(plan.share + blockIdx.x);
   const int unit = mine.x + x;
-  int segment = mine.z;
-  if (x > 0)
-    segment += last_request(plan.groups + c.sum_q - segment, lane, [&](int s) { return __ldcg(plan.unit_of + mine.z + s) <= unit; });
-  const int block = unit - __ldcg(plan.unit_of + segment);
-  const int shared = __ldcg(plan.shared_of + segment);
-  int64_t at = __ldcg(plan.cost_of + segment);
-  Unit u;
-  u.h0 = block * kNH;
-  bool partial = true;
-  if (segment < plan.groups) {                    // a group's prefix
-    const int4 g = __ldcg(plan.group + segment);
-    const int row = g.y * p.H + u.h0;
-    u.heads = min(kNH, g.z - u.h0);
-    u.t = row / p.H;
-    u.h0 = row - u.t * p.H;
-    u.b = u.b0 = g.x;
-    u.first = g.w;
-    u.pos = -1;
-    u.lo = 0;
-  } else {
-    const int4 r = __ldcg(plan.token + (segment - plan.groups));
-    partial = r.y < 0;
-    u.t = segment - plan.groups;
-    u.heads = min(kNH, p.H - u.h0);
-    u.b = r.x;
-    u.b0 = partial ? r.x : r.y;
-    u.first = partial ? 0 : r.w;                  // (a shared prefix is its group's)
-    u.pos = r.z;
-    u.lo = r.w;
-  }
-  const int last = min(u.pos, c.max_pages * c.page_size - 1);
-  if (u.pos > last && lane == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
-  u.first_chunks = (u.first + (1 << kShift) - 1) >> kShift;
-  u.window_chunk = u.lo >> kShift;
-  u.chunks = u.first_chunks + (last >= u.lo ? (last >> kShift) - u.window_chunk + 1 : 0);
-  const int tiles = (u.chunks + (kRows >> kShift) - 1) >> (7 - kShift);
-  at += block * plan_cost(tiles) + kPlanUnit;     // where its first tile begins
-  auto from = [&](int s) {                        // its first tile that begins in share s or behind it
-    return (int)min(max((s * share_cost - at + kPlanTile - 1) / kPlanTile, (int64_t)0), (int64_t)tiles);
-  };
-  u.tile0 = from(share);
-  u.tiles = from(share + 1) - u.tile0;
-  u.part = partial ? 2 * plan.shares + shared + block + share : u.tiles < tiles ? 2 * share + (x > 0) : -1;
-  return u;
+  const int segment = mine.z + last_request(plan.groups + c.sum_q - mine.z, lane,
+                                            [&](int s) { return __ldcg(plan.unit_of + mine.z + s) <= unit; });
+  return plan_unit(c, plan, kp.p.H, kShift, blockIdx.x, __ldcg(plan.share_cost), unit, segment, x > 0, lane == 0 ? kp.p.err : nullptr,
+                   plan.cost_of, plan.unit_of, plan.shared_of, plan.group, plan.token);
 }
 
 template <int kShift, int kMode>
@@ -357,18 +303,20 @@ __device__ __forceinline__ void split_query(const KernelParams& kp, const Unit& 
                                             int lane) {
   const WindowParams& p = kp.p;
   constexpr int kHeads = kNH / kSoftmaxWarps;
-  const int h = warp * kHeads;
+  // (a plan's units often have a few rows only: those are every warp's, one by one)
+  constexpr int kEach = kMode == kPlanned ? kSoftmaxWarps : 1;
+  const int h = kMode == kPlanned ? warp : warp * kHeads;
   const __nv_bfloat16* q = p.q + (int64_t)u.t * p.q_stride_token + (int64_t)(u.h0 + h) * kHeadDim + lane * 16;
-  auto at = [&](int i) {                          // the lane's dims of the unit's row h + i
+  auto at = [&](int i) {                          // the lane's dims of the warp's row i
     if constexpr (kMode != kPlanned) return q + i * kHeadDim;
-    const int row = u.h0 + h + i, t = row / p.H;  // (a plan's rows may run through several tokens)
+    const int row = u.h0 + h + i * kEach, t = row / p.H;   // (a plan's rows may run through several tokens)
     return p.q + (int64_t)(u.t + t) * p.q_stride_token + (int64_t)(row - t * p.H) * kHeadDim + lane * 16;
   };
   const float scale = fetch_scale(p.bmm1, p.bmm1_dev) * kLog2e;
   auto load = [&](int i, uint4* v) {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      v[k] = h + i < u.heads ? fetch(reinterpret_cast<const uint4*>(at(i)) + k) : make_uint4(0, 0, 0, 0);
+      v[k] = h + i * kEach < u.heads ? fetch(reinterpret_cast<const uint4*>(at(i)) + k) : make_uint4(0, 0, 0, 0);
   };
   uint4 next[2][2];                               // two heads ahead
   load(0, next[0]);
@@ -389,7 +337,7 @@ __device__ __forceinline__ void split_query(const KernelParams& kp, const Unit& 
     const int e = min(max((int)(m >> 7), 8), 254);
     const int k = 134 - e;
     const float up = __uint_as_float((uint32_t)(k + 127) << 23), down = __uint_as_float((uint32_t)(127 - k) << 23);
-    if (lane == 0) sm.qscale[h + i] = scale * down;
+    if (lane == 0) sm.qscale[h + i * kEach] = scale * down;
     uint32_t hi[8], lo[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x)
@@ -401,8 +349,8 @@ __device__ __forceinline__ void split_query(const KernelParams& kp, const Unit& 
       l16 = make_uint4(0, 0, 0, 0);
     }
     uint8_t* to = sq + (lane >> 3) * kQBlock;     // column block; 16-byte chunk lane % 8 of it
-    *reinterpret_cast<uint4*>(to + sw128_offset(h + i, lane & 7)) = h16;
-    *reinterpret_cast<uint4*>(to + sw128_offset(h + i + kNH, lane & 7)) = l16;
+    *reinterpret_cast<uint4*>(to + sw128_offset(h + i * kEach, lane & 7)) = h16;
+    *reinterpret_cast<uint4*>(to + sw128_offset(h + i * kEach + kNH, lane & 7)) = l16;
   }
 }
 
@@ -453,6 +401,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
   // too, and take q_full in turn: behind a first unit without tiles the second
   // unit's may be there before the first products' warp has waited for the first
   // one's, but no third is before it has waited for both.
+  union {
+    int4 words[4];
+    Unit unit;
+  } first;                                        // of a plan
+  if (kMode == kPlanned && warp == kLoadWarp)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) first.words[k] = __ldcg(kp.plan.first + blockIdx.x * 4 + k);
   const int mine = kMode == kPlanned ? __ldcg(kp.plan.share + blockIdx.x).y
                                      : (kp.units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
   if (kMode == kPlanned && mine <= 0) {
@@ -465,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     constexpr int kBoxes = kRows >> kShift;       // of a tile
     int n = 0;
     bool ok = true;
-    Unit ahead = make_unit<kShift, kMode>(kp, kMode == kPlanned ? 0 : blockIdx.x, lane);
+    Unit ahead = kMode == kPlanned ? first.unit : make_unit<kShift, kMode>(kp, blockIdx.x, lane);
     auto prefetch_query = [&](const Unit& u) {
       if constexpr (kMode == kPlanned) {          // rows of several tokens: one by one
         for (int i = lane; u.tiles > 0 && i < u.heads; i += 32) {
@@ -479,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         bulk_prefetch_l2(p.q + (int64_t)u.t * p.q_stride_token + (int64_t)u.h0 * kHeadDim, u.heads * kHeadDim * 2);
       __syncwarp();
     };
-    prefetch_query(ahead);
+    if constexpr (kMode != kPlanned) prefetch_query(ahead);   // (a plan's first unit: the softmax waits for it, and loads them then)
     for (int x = 0; ok && x < mine; ++x) {
       const Unit u = ahead;
       if (x >= 2) ok = warp_wait(cx, bar(sm.unit_empty[x & 1]), ((x >> 1) - 1) & 1);
@@ -969,15 +924,18 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
       }
       named_bar_sync(1, kSoftmaxThreads);
       if (__builtin_expect(!whole, 0)) {
+        // (a plan's units of up to 16 rows: 128 dims of all of them a warpgroup)
+        const bool few = kMode == kPlanned && heads <= kHW;
+        const int h0 = few ? 0 : hw;
 #pragma unroll 1
-        for (int m = 0; m < 4; ++m) {             // dims 128 m .. + 127, one a thread
+        for (int m = few ? hw / kHW : 0; m < (few ? hw / kHW + 1 : 4); ++m) {   // dims 128 m .. + 127, one a thread
           uint32_t o[kHW];
-          tmem_ld16(lane_base + kOCol + m * kNH + hw, o);
+          tmem_ld16(lane_base + kOCol + m * kNH + h0, o);
           tmem_wait_ld();
-          float* dst = p.part_o + (part + hw) * kHeadDim + m * 128 + r;
+          float* dst = p.part_o + (part + h0) * kHeadDim + m * 128 + r;
 #pragma unroll
           for (int h = 0; h < kHW; ++h)
-            if (hw + h < heads) dst[h * kHeadDim] = __uint_as_float(o[h]) * sm.wmax[1][hw + h];
+            if (h0 + h < heads) dst[h * kHeadDim] = __uint_as_float(o[h]) * sm.wmax[1][h0 + h];
         }
       } else {
         // 8 x 8 fragments, transposed on their way into a P buffer: [64 heads][64 dims] BF16 twice, 128-byte

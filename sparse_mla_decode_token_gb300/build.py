@@ -87,7 +87,7 @@ def _link_torch_ext(obj: str) -> None:
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = TORCH_EXT + ".tmp"
     _run("link", ["g++", "-shared", "-o", tmp, obj, "-L", BUILD, "-lsmla", "-Wl,-rpath,$ORIGIN", "-L", libs, "-lc10",
-                  "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+                  "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"])
     os.replace(tmp, TORCH_EXT)
 
 

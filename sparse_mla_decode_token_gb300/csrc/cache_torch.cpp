@@ -10,8 +10,7 @@
 
 #include <vector>
 
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -173,14 +172,14 @@ PyObject* attention(PyObject* const* a, int at, Set set, Run run) {
   need((a[2] != Py_None && a[3] != Py_None) || stream == call.stream(Py_None));
   at::Tensor out, lse;                      // those that are not given
   if (a[2] == Py_None) {
-    out = at::empty_like(q, q.options(), c10::MemoryFormat::Contiguous);
+    out = at::detail::empty_cuda({T, H, kDim}, c10::kBFloat16, q.device(), std::nullopt);   // (at::empty without its dispatch)
     w.out = out.data_ptr();
   } else {
     w.out = call.array(a[2], c10::kBFloat16, T * H * kDim, false);
     need(THPVariable_Unpack(a[2]).numel() == T * H * kDim);
   }
   if (a[3] == Py_None) {
-    lse = at::empty({T, H}, q.options().dtype(c10::kFloat));
+    lse = at::detail::empty_cuda({T, H}, c10::kFloat, q.device(), std::nullopt);
     w.out_lse = static_cast<float*>(lse.data_ptr());
   } else {
     w.out_lse = static_cast<float*>(call.array(a[3], c10::kFloat, T * H, false));
@@ -385,7 +384,7 @@ struct Output {
       data = call.array(o, type, entries, false);
       given = o;
     } else {
-      fresh = at::empty(sizes, like.options().dtype(type));
+      fresh = at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
       data = fresh.data_ptr();
     }
   }

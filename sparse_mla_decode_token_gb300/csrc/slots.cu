@@ -106,7 +106,7 @@ __device__ __forceinline__ int slot_row(const SlotTable& t, const int32_t* row, 
 }
 
 template <bool kVector, int kWarps>
-__global__ void __launch_bounds__(kSparseThreads) sparse_slots_kernel(const SparseSlotsParams p) {
+__global__ void __launch_bounds__(kSparseThreads, 3) sparse_slots_kernel(const SparseSlotsParams p) {
   __shared__ int s_last[kSparseThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * (kSparseThreads / 32 / kWarps) + warp / kWarps;
@@ -116,6 +116,20 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_slots_kernel(const Spar
     if constexpr (kWarps > 1) __syncthreads();
     return;
   }
+  // the first selected positions, on their way while the request is looked up
+  constexpr int kAhead = 2;
+  const int columns = kSwaCols + p.num_selected, c0 = (warp % kWarps * 32 + lane) * 4;
+  const int32_t* pick = p.selected + t * p.selected_stride - kSwaCols;
+  auto select = [&](int c) {
+    if (c < kSwaCols || c >= columns) return make_int4(-1, -1, -1, -1);
+    if (p.selected == nullptr) return make_int4(c - kSwaCols, c - kSwaCols + 1, c - kSwaCols + 2, c - kSwaCols + 3);
+    if (kVector) return *reinterpret_cast<const int4*>(pick + c);
+    return make_int4(fetch(pick + c), c + 1 < columns ? fetch(pick + c + 1) : -1, c + 2 < columns ? fetch(pick + c + 2) : -1,
+                     c + 3 < columns ? fetch(pick + c + 3) : -1);
+  };
+  int4 next[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) next[k] = select(c0 + k * kWarps * 128);
   int b, first, count;
   if (p.cum != nullptr) {
     b = last_request(p.batch, lane, [&](int x) { return fetch(p.cum + x) <= t; });
@@ -132,41 +146,36 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_slots_kernel(const Spar
   const int limit = pos >= 0 ? (int)(((int64_t)pos + 1) / p.ratio) : 0;
   const int32_t* swa = p.swa.bt + b * p.swa.stride;
   const int32_t* comp = p.comp.bt + b * p.comp.stride;
-  const int32_t* pick = p.selected + t * p.selected_stride;
   int32_t* out = p.out + t * p.out_stride;
-  const int columns = kSwaCols + p.num_selected;
   int last = 0;
   bool bad = false;
-#pragma unroll 2
-  for (int c0 = (warp % kWarps * 32 + lane) * 4; c0 < columns; c0 += kWarps * 128) {
-    int v[4], c[4];
-    if (c0 < kSwaCols) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) c[e] = lo + c0 + e <= pos ? lo + c0 + e : -1;
-    } else if (p.selected == nullptr) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) c[e] = c0 - kSwaCols + e;
-    } else if (kVector) {
-      const int4 q = *reinterpret_cast<const int4*>(pick + (c0 - kSwaCols));
-      c[0] = q.x, c[1] = q.y, c[2] = q.z, c[3] = q.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) c[e] = c0 + e < columns ? fetch(pick + (c0 - kSwaCols + e)) : -1;
-    }
-    const bool window = c0 < kSwaCols;
+  auto rows = [&](int at, int4 q) {               // four columns from `at` on
+    if (at >= columns) return;
+    int v[4], c[4] = {q.x, q.y, q.z, q.w};
+    const bool window = at < kSwaCols;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const bool seen = window ? c[e] >= 0 : c[e] >= 0 && c[e] < limit && c0 + e < columns;
+      if (window) c[e] = lo + at + e <= pos ? lo + at + e : -1;
+      const bool seen = c[e] >= 0 && (window || (c[e] < limit && at + e < columns));
       v[e] = seen ? slot_row(window ? p.swa : p.comp, window ? swa : comp, c[e], &bad) : -1;
-      if (!window && v[e] >= 0) last = max(last, c0 + e + 1 - kSwaCols);
+      if (!window && v[e] >= 0) last = max(last, at + e + 1 - kSwaCols);
     }
     if (kVector) {
-      *reinterpret_cast<int4*>(out + c0) = make_int4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<int4*>(out + at) = make_int4(v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (c0 + e < columns) out[c0 + e] = v[e];
+        if (at + e < columns) out[at + e] = v[e];
     }
+  };
+  for (int base = c0; base < columns; base += kAhead * kWarps * 128) {
+    int4 now[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) now[k] = next[k];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) next[k] = select(base + (kAhead + k) * kWarps * 128);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) rows(base + k * kWarps * 128, now[k]);
   }
   if (bad) flag(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
   last = __reduce_max_sync(0xffffffffu, last);

@@ -117,9 +117,9 @@ __device__ __noinline__ uint4 load_edge(const T* base, int before, uint32_t at, 
 
 // Is the beam of this row one whose logits count?
 __device__ __forceinline__ bool live_beam(const BeamParams& p, int64_t row) {
-  if (p.finished != nullptr && p.finished[row] != 0) return false;
   const float s = fetch(p.scores + row);
-  return s > -INFINITY && s < INFINITY;
+  const bool done = p.finished != nullptr && fetch(p.finished + row) != 0;
+  return (s > -INFINITY) & (s < INFINITY) & !done;
 }
 
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {

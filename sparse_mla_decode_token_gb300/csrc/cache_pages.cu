@@ -211,16 +211,16 @@ __device__ __forceinline__ int sum_counts(const int32_t* counts, int chunks, Sha
   return n;
 }
 
-// Calls f(row, first column, one past the last) for pieces of up to 128 table
+// Calls f(row, first column, one past the last) for pieces of up to kPiece table
 // entries of the rows' ranges [range(row).x, range(row).y), dealt out to the warps.
-template <class R, class F>
+template <int kPiece = 128, class R, class F>
 __device__ __forceinline__ void pieces(const PagesParams& p, const Team& w, R range, F f) {
-  const int per_row = (p.max_pages + 127) / 128;
+  const int per_row = (p.max_pages + kPiece - 1) / kPiece;
   const int64_t all = (int64_t)p.rows * per_row;
   for (int64_t i = w.gw; i < all; i += w.warps) {
-    const int b = (int)(i / per_row), c0 = (int)(i - (int64_t)b * per_row) * 128;
+    const int b = (int)(i / per_row), c0 = (int)(i - (int64_t)b * per_row) * kPiece;
     const int2 r = range(b);
-    const int from = max(r.x, c0), to = min(r.y, c0 + 128);
+    const int from = max(r.x, c0), to = min(r.y, c0 + kPiece);
     if (from < to) f(b, from, to);
   }
 }
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(const PagesParams p) {
 //      all of 1, so that no page that stays in use passes through 0).
 // Both phases compare the same two entries: a row is changed by the thread that
 // compared it only.
-constexpr int kReorderPer = 4;                        // columns a lane takes at a time
+constexpr int kReorderPer = 8;                        // columns a lane takes at a time
 
 // Row b's parent, b itself for one that stays (one that is not a row is flagged), -1 for one that ends.
 __device__ __forceinline__ int parent_of(const PagesParams& p, int b, bool* bad) {
@@ -485,60 +485,49 @@ __device__ __forceinline__ Reorder reorder_row(const PagesParams& p, int b) {
   return r;
 }
 
-__device__ __forceinline__ void reorder_save(const PagesParams& p, const Team& w) {
-  pieces(p, w,
-         [&](int b) {
-           const Reorder r = reorder_row(p, b);
-           return make_int2(0, r.parent == b ? 0 : r.theirs);
-         },
-         [&](int b, int from, int to) {
-           const Reorder r = reorder_row(p, b);
-           const int32_t* theirs = p.bt + (int64_t)r.parent * p.bt_stride;
-           const int32_t* mine = p.bt + (int64_t)b * p.bt_stride;
-           int now[kReorderPer], old[kReorderPer];
+template <bool kWrite>
+__device__ __forceinline__ void reorder_phase(const PagesParams& p, const Team& w) {
+  Reorder r;
+  pieces<32 * kReorderPer>(
+      p, w,
+      [&](int b) {
+        r = reorder_row(p, b);
+        return make_int2(0, r.parent == b ? 0 : kWrite ? max(r.mine, r.theirs) : r.theirs);
+      },
+      [&](int b, int from, int to) {
+        int32_t* const mine = p.bt + (int64_t)b * p.bt_stride;
+        int32_t* const saved = p.ws + (int64_t)b * p.max_pages;
+        const int32_t* const theirs = kWrite ? saved : p.bt + (int64_t)r.parent * p.bt_stride;
+        int now[kReorderPer], old[kReorderPer];
 #pragma unroll
-           for (int k = 0; k < kReorderPer; ++k) {
-             const int c = from + k * 32 + w.lane;
-             now[k] = c < to ? __ldcg(theirs + c) : 0;
-             old[k] = c < to && c < r.mine ? __ldcg(mine + c) : -1;
-           }
+        for (int k = 0; k < kReorderPer; ++k) {
+          const int c = from + k * 32 + w.lane;
+          now[k] = c < to && c < r.theirs ? __ldcg(theirs + c) : -1;
+          old[k] = c < to && c < r.mine ? __ldcg(mine + c) : -1;
+        }
 #pragma unroll
-           for (int k = 0; k < kReorderPer; ++k) {
-             const int c = from + k * 32 + w.lane;
-             if (c >= to) continue;
-             p.ws[(int64_t)b * p.max_pages + c] = now[k];
-             if (c < r.mine && old[k] == now[k]) continue;
-             if (in_pool(p, now[k])) atomicAdd(p.refs + now[k], 1);
-             else flag(p.err, SMLA_DEVERR_PAGE_STATE);
-           }
-         });
+        for (int k = 0; k < kReorderPer; ++k) {
+          const int c = from + k * 32 + w.lane;
+          if (c >= to) continue;
+          const bool same = c < r.mine && c < r.theirs && old[k] == now[k];
+          if constexpr (!kWrite) {
+            saved[c] = now[k];
+            if (same) continue;
+            if (in_pool(p, now[k])) atomicAdd(p.refs + now[k], 1);
+            else flag(p.err, SMLA_DEVERR_PAGE_STATE);
+          } else if (!same) {
+            mine[c] = now[k];
+            if (c < r.mine) drop_ref(p, old[k]);
+          }
+        }
+      });
 }
 
+__device__ __forceinline__ void reorder_save(const PagesParams& p, const Team& w) { reorder_phase<false>(p, w); }
 __device__ __forceinline__ void reorder_write(const PagesParams& p, const Team& w) {
-  pieces(p, w,
-         [&](int b) {
-           const Reorder r = reorder_row(p, b);
-           return make_int2(0, r.parent == b ? 0 : max(r.mine, r.theirs));
-         },
-         [&](int b, int from, int to) {
-           const Reorder r = reorder_row(p, b);
-           int32_t* mine = p.bt + (int64_t)b * p.bt_stride;
-           int now[kReorderPer], old[kReorderPer];
-#pragma unroll
-           for (int k = 0; k < kReorderPer; ++k) {
-             const int c = from + k * 32 + w.lane;
-             now[k] = c < to && c < r.theirs ? __ldcg(p.ws + (int64_t)b * p.max_pages + c) : -1;
-             old[k] = c < to && c < r.mine ? __ldcg(mine + c) : -1;
-           }
-#pragma unroll
-           for (int k = 0; k < kReorderPer; ++k) {
-             const int c = from + k * 32 + w.lane;
-             if (c >= to || (c < r.mine && c < r.theirs && old[k] == now[k])) continue;
-             if (c < r.mine) drop_ref(p, old[k]);
-             mine[c] = now[k];
-           }
-         });
-  for (int b = w.cta * kPlanThreads + (int)threadIdx.x; b < p.rows; b += w.ctas * kPlanThreads) {
+  reorder_phase<true>(p, w);
+  // (from the CTA's last warp on, which the pieces reach last)
+  for (int b = w.cta + (kPlanThreads - 1 - (int)threadIdx.x) * w.ctas; b < p.rows; b += w.ctas * kPlanThreads) {
     bool bad = false;
     const int parent = parent_of(p, b, &bad);
     p.out_lens[b] = parent >= 0 ? fetch(p.lens + parent) : 0;
@@ -823,7 +812,8 @@ cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t stream) {
 cudaError_t launch_pages_reorder(const PagesParams& p, int sms, cudaStream_t stream) {
   if ((int64_t)p.rows * p.max_pages <= kClusterEntries)
     return launch_overlapped(pages_reorder_kernel, dim3(kClusterCtas), kPlanThreads, 0, stream, p);
-  const dim3 tables(phase_ctas((int64_t)p.rows * ((p.max_pages + 127) / 128), sms));
+  constexpr int kPiece = 32 * kReorderPer;
+  const dim3 tables(phase_ctas((int64_t)p.rows * ((p.max_pages + kPiece - 1) / kPiece), sms));
   cudaError_t e = launch_overlapped(pages_reorder_phase_kernel<0>, tables, kPlanThreads, 0, stream, p);
   if (e == cudaSuccess) e = launch_overlapped(pages_reorder_phase_kernel<1>, tables, kPlanThreads, 0, stream, p);
   return e;

@@ -97,10 +97,16 @@ constexpr int kSparseThreads = 512;
 
 // Row of position j >= 0, or -1 (*bad set).
 __device__ __forceinline__ int slot_row(const SlotTable& t, const int32_t* row, int j, bool* bad) {
-  const int column = t.shift >= 0 ? j >> t.shift : j / t.page_size;
-  const int page = column < t.max_pages ? fetch(row + column) : -1;
-  const int64_t at = (int64_t)page * t.page_size + (j - column * t.page_size);
-  if (page >= 0 && at <= 0x7fffffff) return (int)at;
+  if (t.shift >= 0) {
+    const int column = j >> t.shift;
+    const int page = column < t.max_pages ? fetch(row + column) : -1;
+    if ((uint32_t)page >> (31 - t.shift) == 0) return page << t.shift | (j & (t.page_size - 1));
+  } else {
+    const int column = j / t.page_size;
+    const int page = column < t.max_pages ? fetch(row + column) : -1;
+    const int64_t at = (int64_t)page * t.page_size + (j - column * t.page_size);
+    if (page >= 0 && at <= 0x7fffffff) return (int)at;
+  }
   *bad = true;
   return -1;
 }

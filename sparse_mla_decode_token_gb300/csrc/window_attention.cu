@@ -133,7 +133,8 @@ constexpr int kOffP = kOffK + 2 * kTileBytes;
 constexpr int kOffSmall = kOffP + 4 * kPHalf;
 
 // How the work is cut: each pair of a token and 64 heads by one CTA; some pairs in
-// splits; by the plan of a batch whose groups share prefixes (prefix_attention.cu).
+// splits; by the plan of a batch whose groups share prefixes (prefix_attention.cu, which
+// says what that measures).
 constexpr int kPairs = 0, kSplitPairs = 1, kPlanned = 2;
 
 struct alignas(16) Small {

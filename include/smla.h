@@ -422,8 +422,9 @@ smla_status smla_window_attention(const smla_window_args* args, void* stream);
  * Attention of a batch whose groups share long prefixes: plain causal attention
  * (token i of request b sees the rows j <= pos = seq_lens[b] - q_len_b + i), for
  * which the first P_g rows of every request of group g, group_starts[g] <= b <
- * group_starts[g + 1], are read through the page table of the group's first
- * request, once for all of them where that saves work (H not a multiple of 64);
+ * group_starts[g + 1], are read through the page table of the first request of
+ * the group that has new tokens, once for all of them where that saves work (H
+ * not a multiple of 64);
  *
  *   P_g = min(prefix_lens[g], seq_lens[b] - q_len_b + 1 over the group's requests with new tokens),
  *
@@ -668,7 +669,8 @@ smla_status smla_sparse_slots(const smla_sparse_slots_args* args, void* stream);
  * and out_tokens; among equal ones the lower (i, v) is first.  Scores that agree
  * to 2^-45 of their logit or of s_i - log sum, whichever is larger, may count as
  * equal.  Continuations of -infinity are none; places that none is left for
- * hold -infinity, -1 and -1.  A beam with a score of -infinity (an empty place)
+ * hold -infinity, -1 and -1.  out_scores may be `scores` itself where num_out is
+ * beams.  A beam with a score of -infinity (an empty place)
  * has no continuation; its logits do not count, whatever they are, nor do a
  * finished beam's.
  * A NaN or +infinity among the logits or for the score leaves the beam without

@@ -349,7 +349,7 @@ def prefix_attention(q: torch.Tensor, rows: torch.Tensor, scales: torch.Tensor, 
     """Causal attention of BF16 queries ``[T, H, 512]`` over the cached tokens of
     their request, of which the requests ``group_starts[g] <= b <
     group_starts[g + 1]`` share the first ``prefix_lens[g]`` (read through the
-    first one's table, once for all); returns ``(out, out_lse)``, allocated when
+    table of the first one with new tokens, once for all); returns ``(out, out_lse)``, allocated when
     not given (as ``stream``'s memory, where that is another than the current one)."""
     done = (_extension or extension()).prefix_attention(
         q, rows, scales, block_tables, seq_lens, workspace_buffer, cum_seq_lens_q, sinks, group_starts, prefix_lens,

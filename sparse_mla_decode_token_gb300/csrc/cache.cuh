@@ -136,10 +136,11 @@ struct PrefixPlan {
   int32_t* shared_of;                   // [groups + T] the units of shared prefixes and their tokens before it
   int4* share;                          // [shares] first unit, units, the first one's segment
   int4* first;                          // [shares][4] the first unit
-  int4* group;                          // [groups] first request, first token, (token, head) rows, prefix (0: not shared)
-  int4* token;                          // [T] request, its group's first one (or sign and group: shared), position, prefix
+  int4* group;                          // [groups] first request with tokens, its first token, (token, head) rows, prefix (0: not shared)
+  int4* token;                          // [T] request, the one that holds its prefix (or sign and group: shared), position, prefix
   int4* prefix_of;                      // [T] of a shared prefix: cost_of (two words), shared_of, the token's first row in it
-  int32_t* limit;                       // [groups] positions that all the group's tokens see
+  int32_t* limit;                       // [groups] positions that all the group's tokens see (where groups are many)
+  int32_t* lead;                        // [groups] its first request with tokens
 };
 
 // Unit `unit`, of `segment`, as far as it is share `share`'s; later: not the share's

@@ -203,7 +203,7 @@ smla_status check_prefix(const smla_prefix_args* a) {
 struct PrefixLayout {
   int64_t parts;
   int shares;
-  size_t lse, header, cost_of, unit_of, shared_of, share, first, group, token, prefix_of, limit, bytes;
+  size_t lse, header, cost_of, unit_of, shared_of, share, first, group, token, prefix_of, limit, lead, bytes;
 };
 PrefixLayout prefix_layout(const smla_prefix_args* a, int sms) {
   const int64_t T = a->sum_q, heads = (a->num_heads + kWindowHeads - 1) / kWindowHeads;
@@ -231,6 +231,7 @@ PrefixLayout prefix_layout(const smla_prefix_args* a, int sms) {
   l.token = take((size_t)T * sizeof(int4));
   l.prefix_of = take((size_t)T * sizeof(int4));
   l.limit = take((size_t)a->num_groups * sizeof(int32_t));
+  l.lead = take((size_t)a->num_groups * sizeof(int32_t));
   l.bytes = at;
   return l;
 }
@@ -405,6 +406,7 @@ smla_status smla_prefix_attention(const smla_prefix_args* a, void* stream) {
   plan.token = reinterpret_cast<int4*>(ws + l.token);
   plan.prefix_of = reinterpret_cast<int4*>(ws + l.prefix_of);
   plan.limit = reinterpret_cast<int32_t*>(ws + l.limit);
+  plan.lead = reinterpret_cast<int32_t*>(ws + l.lead);
   return launched("prefix attention", launch_prefix_attention(p, plan, static_cast<cudaStream_t>(stream)));
 }
 

@@ -11,7 +11,7 @@
 //
 // A group is split so where it saves tiles: with heads in multiples of 64, or one
 // token, there is nothing to save, and its tokens go through one list of rows, the
-// prefix through the table of the group's first request.
+// prefix through the table of the first request of the group that has new tokens.
 //
 // The lengths are on the device, so the plan is made there, by one CTA.  Each block
 // of 64 rows costs 2.25 tiles' time for its query, sums and results and one for each
@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kNearGroups = 512, kNearSegments = 1024;   // of which the plan's arrays lie in shared memory
+constexpr int kNearGroups = 256, kNearSegments = 1024;   // of which the plan's arrays lie in shared memory
 
 __device__ __forceinline__ void flag(int32_t* err, int bit) {
   if (err != nullptr) atomicOr(err, bit);
@@ -112,7 +112,7 @@ __device__ __forceinline__ int share_of(int64_t at, int64_t share_cost, uint64_t
 }
 
 __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParams p, const PrefixPlan plan, int shift) {
-  __shared__ int s_starts[kNearGroups + 1], s_limit[kNearGroups];
+  __shared__ int s_starts[kNearGroups + 1], s_limit[kNearGroups], s_lead[kNearGroups];
   __shared__ int4 s_group[kNearGroups];
   __shared__ int64_t s_cost[kNearSegments + 1];
   __shared__ int s_unit[kNearSegments + 1];
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
   const bool near = plan.groups <= kNearGroups;
   const int* const starts = near ? s_starts : plan.group_starts;
   int* const limit = near ? s_limit : plan.limit;
+  int* const lead = near ? s_lead : plan.lead;
 
   // what is out of order shares nothing
   const bool near_segments = segments <= kNearSegments;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
   for (int g = threadIdx.x; g < plan.groups; g += kThreads) {
     const int lo = fetch(plan.group_starts + g), hi = fetch(plan.group_starts + g + 1);
     bad |= lo < 0 || hi < lo || hi > c.batch;
-    limit[g] = 0x7fffffff;
+    limit[g] = lead[g] = 0x7fffffff;
     if (near) {
       s_starts[g] = lo;
       s_starts[g + 1] = hi;                       // (both threads that write it write the same)
@@ -156,13 +157,18 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
     return g >= 0 && b < starts[g + 1] ? g : -1;
   };
 
-  // the positions that all of a group's tokens see
+  // the positions that all of a group's tokens see, and the first request that has any
   const int group0 = mine.t1 > mine.t0 ? group_of(b0) : -1;
-  if (group0 >= 0) atomicMin(limit + group0, max(0, mine.len - mine.count + 1));
+  if (group0 >= 0) {
+    atomicMin(limit + group0, max(0, mine.len - mine.count + 1));
+    atomicMin(lead + group0, b0);
+  }
   for (int b = b0 + kThreads; b < c.batch && groups > 0; b += kThreads) {
     const Request r = request_of(c, b);
     const int g = r.t1 > r.t0 ? group_of(b) : -1;
-    if (g >= 0) atomicMin(limit + g, max(0, r.len - r.count + 1));
+    if (g < 0) continue;
+    atomicMin(limit + g, max(0, r.len - r.count + 1));
+    atomicMin(lead + g, b);
   }
   __syncthreads();
   for (int g = threadIdx.x; g < plan.groups; g += kThreads) {
@@ -175,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
       if (c.cum != nullptr) t0 = fetch(c.cum + lo), t1 = fetch(c.cum + hi);
       t0 = min(max(t0, 0), T), t1 = min(max(t1, t0), T);
       const int tiles = tiles_of(prefix, 0, -1, cap, shift), blocks = blocks_of((t1 - t0) * p.H);
-      v = make_int4(lo, t0, (t1 - t0) * p.H, 0);
+      v = make_int4(lead[g], t0, (t1 - t0) * p.H, 0);
       if ((int64_t)((t1 - t0) * heads - blocks) * tiles > 3 * (int64_t)blocks) {
         v.w = prefix;
       }

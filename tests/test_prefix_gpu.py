@@ -29,15 +29,16 @@ def i32(a):
 
 
 class Grouped(R.Cache):
-    """Rows before a group's prefix come from its first request's pages."""
+    """Rows before a group's prefix come from the pages of its first request that has new tokens."""
 
     def groups(self, starts, prefix):
         self.first, self.prefix = np.arange(len(self.lens)), np.zeros(len(self.lens), dtype=int)
         for g, p in enumerate(prefix):
             of = range(starts[g], starts[g + 1])
             seen = [int(self.lens[b]) - int(self.cum[b + 1] - self.cum[b]) + 1 for b in of if self.cum[b + 1] > self.cum[b]]
+            lead = min([b for b in of if self.cum[b + 1] > self.cum[b]], default=starts[g])
             for b in of:
-                self.first[b], self.prefix[b] = starts[g], max(0, min([int(p)] + seen))
+                self.first[b], self.prefix[b] = lead, max(0, min([int(p)] + seen))
         return self
 
     def page(self, b, j):
@@ -277,6 +278,37 @@ def test_deterministic_captured_and_on_another_stream():
     torch.cuda.synchronize()
     cache.groups(starts, [64, 17])
     check(cache, q, [t.double().cpu().numpy() for t in outs[0]])
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+def test_requests_without_tokens_lead_no_group(heads):
+    """The group's first request has ended: its table is empty, its prefix is the next one's."""
+    cache, starts, q, _ = make(17, [4, 3], [200, 130], [1, 2, 9, 4, 1, 2, 3], [0, 1, 1, 1, 0, 0, 1], heads=heads, shared=True)
+    for b in (0, 4, 5):
+        cache.tables[b], cache.lens[b] = -1, 0
+    cache.groups(starts, [200, 130])
+    check(cache, q, run(cache, starts, [200, 130], q))
+
+
+@pytest.mark.parametrize("cum", [[0, 3, 1, 4], [2, 0, 9, 4], [0, 4, 4, -3]])
+def test_offsets_that_fall_stay_in_range(cum):
+    cache, starts, q, _ = make(18, [3], [70], [2, 3, 4], [1, 2, 1], heads=16, shared=True)
+    qt = queries(q)[0]
+    g = on_gpu(cache)
+    out, lse = torch.full((6, 16, 512), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((6, 16), 7.0, device=DEV)
+    ws = torch.empty(C.prefix_workspace_size(qt, *g, group_starts=i32(starts), cum_seq_lens_q=i32(cum)), dtype=torch.uint8, device=DEV)
+    guard = torch.full((4096,), 99, dtype=torch.uint8, device=DEV)
+    C.prefix_attention(qt, *g, ws, group_starts=i32(starts), prefix_lens=i32([70]), cum_seq_lens_q=i32(cum), bmm1_scale=SCALE,
+                       out=out[1:5], out_lse=lse[1:5])
+    torch.cuda.synchronize()
+    assert bool((out[0] == 7).all()) and bool((out[5] == 7).all()) and bool((lse[0] == 7).all()) and bool((lse[5] == 7).all())
+    assert bool((guard == 99).all())
+
+
+def test_more_groups_than_the_plan_keeps_near():
+    n = 600
+    cache, starts, q, _ = make(19, [2] * n, [24] * n, [1, 2] * n, [1] * (2 * n), heads=3, page_size=8, block=8)
+    check(cache, q, run(cache, starts, [24] * n, q))
 
 
 def test_many_tokens():

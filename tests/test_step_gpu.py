@@ -196,6 +196,18 @@ def test_beam_rising_and_falling_logits():
         check(select(logits, scores, 32), logits, scores, 32)
 
 
+def test_beam_scores_in_place_and_many_requests():
+    g = torch.Generator(device=DEV).manual_seed(12)
+    logits, scores = likely(g, 3000, 700, "fp16"), -torch.rand(1500, 2, generator=g, device=DEV)
+    before = scores.clone()
+    ws = torch.empty(search.beam_workspace_size(logits, scores), dtype=torch.uint8, device=DEV)
+    rest = [torch.empty(1500, 2, dtype=torch.int32, device=DEV) for _ in range(2)]
+    best = search.beam_select(logits, scores, ws, out=search.BeamChoice(scores, *rest))
+    torch.cuda.synchronize()
+    assert best.scores is scores
+    check([t.cpu().numpy() for t in best], logits, before, 2)
+
+
 def test_beam_deterministic_and_captured_on_a_stream():
     g = torch.Generator(device=DEV).manual_seed(9)
     logits, scores = likely(g, 32, 20011, "bf16"), -torch.rand(4, 8, generator=g, device=DEV)

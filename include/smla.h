@@ -423,8 +423,7 @@ smla_status smla_window_attention(const smla_window_args* args, void* stream);
  * (token i of request b sees the rows j <= pos = seq_lens[b] - q_len_b + i), for
  * which the first P_g rows of every request of group g, group_starts[g] <= b <
  * group_starts[g + 1], are read through the page table of the first request of
- * the group that has new tokens, once for all of them where that saves work (H
- * not a multiple of 64);
+ * the group that has new tokens, once for all of them where that saves work;
  *
  *   P_g = min(prefix_lens[g], seq_lens[b] - q_len_b + 1 over the group's requests with new tokens),
  *

@@ -124,6 +124,7 @@ struct Unit {
 // only its end, cuts), then for shared prefixes and their tokens by unit and share.
 constexpr int kPlanTile = 4, kPlanUnit = 9;       // cost of a tile; of a unit's query, sums and results
 constexpr int kMaxShares = 256;
+constexpr int kManyPieces = 16;
 __host__ __device__ inline int64_t plan_cost(int tiles) { return kPlanUnit + (int64_t)(tiles > 0 ? tiles : 1) * kPlanTile; }
 struct PrefixPlan {
   int32_t groups, shares;
@@ -131,6 +132,7 @@ struct PrefixPlan {
   const int32_t* prefix_lens;           // [groups]
   int64_t* share_cost;                  // [1]
   uint64_t* share_by;                   // [1] 2^64 / share_cost, rounded up
+  int32_t* many;                        // [1] a block may be in more than kManyPieces shares
   int64_t* cost_of;                     // [groups + T + 1] where a group's prefix, a token begins
   int32_t* unit_of;                     // [groups + T + 1] its first unit
   int32_t* shared_of;                   // [groups + T] the units of shared prefixes and their tokens before it
@@ -194,7 +196,8 @@ __device__ __forceinline__ Unit plan_unit(const CacheView& c, const PrefixPlan& 
 cudaError_t launch_planned_attention(const WindowParams& p, const PrefixPlan& plan, cudaStream_t stream);
 cudaError_t launch_prefix_attention(const WindowParams& p, const PrefixPlan& plan, cudaStream_t stream);
 
-cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t stream);
+struct PrefixPlan;
+cudaError_t launch_pair_attention(const WindowParams& p, const PrefixPlan* plan, int sms, cudaStream_t stream);
 
 struct AppendParams {
   CacheView c;

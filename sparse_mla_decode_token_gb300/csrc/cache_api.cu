@@ -133,7 +133,8 @@ smla_status check_window(const smla_window_args* a) {
   return SMLA_OK;
 }
 
-int head_groups(const smla_window_args* a) { return (a->num_heads + kWindowHeads - 1) / kWindowHeads; }
+template <class Args>
+int head_groups(const Args* a) { return (a->num_heads + kWindowHeads - 1) / kWindowHeads; }
 
 // How the (token, head group) pairs are worked through: the first `whole` each by
 // one CTA, the others in `splits` ranges of their tiles that a second kernel
@@ -163,17 +164,13 @@ int cheapest_splits(int64_t pairs, int64_t tiles, int sms) {
   return best;
 }
 
-WindowPlan window_plan(const smla_window_args* a, int sms) {
+// Pairs of up to `tiles` tiles, in `splits` if that is not 0.
+WindowPlan pair_plan(int64_t pairs, int64_t tiles, int splits, int sms) {
   WindowPlan w;
-  const int64_t pairs = (int64_t)a->sum_q * head_groups(a);
-  if (a->num_splits > 0) {
-    w.splits = a->num_splits;
+  if (splits > 0) {
+    w.splits = splits;
     w.whole = w.splits > 1 ? 0 : pairs;
   } else {
-    const int64_t page = a->cache.page_size, chunk = page % 32 == 0 ? 32 : page % 16 == 0 ? 16 : 8;   // rows of a box
-    const int64_t all = ((int64_t)a->cache.max_pages * page + chunk - 1) / chunk;
-    const int64_t seen = ((int64_t)a->window + chunk - 2) / chunk + 1 + ((int64_t)a->first_tokens + chunk - 1) / chunk;
-    const int64_t tiles = (std::min(all, seen) * chunk + kWindowTile - 1) / kWindowTile;
     // The pairs of the last, partly filled turn of the SMs are the ones worth splitting (160 pairs of 9 tiles: 61 us
     // whole, 49 so; 772: 182 and 171; 1232 of 5: 170.5 and 168.5).  Behind more turns they are a small part, and the
     // kernel with splits is 3 % slower (1864 of 5: 240 us whole, 243 so; 2448: 305 and 307; of 9: 382 and 372, 485 and 479).
@@ -188,6 +185,26 @@ WindowPlan window_plan(const smla_window_args* a, int sms) {
   return w;
 }
 
+// Rows of a page's boxes that a request may hold, and the tiles of `rows` of them.
+int64_t box_rows(const smla_cache& c) { return 1ll << cache_box_shift(c.page_size); }
+int64_t table_chunks(const smla_cache& c) { return ((int64_t)c.max_pages * c.page_size + box_rows(c) - 1) / box_rows(c); }
+int64_t chunk_tiles(const smla_cache& c, int64_t chunks) { return (chunks * box_rows(c) + kWindowTile - 1) / kWindowTile; }
+
+WindowPlan window_plan(const smla_window_args* a, int sms) {
+  const int64_t chunk = box_rows(a->cache);
+  const int64_t seen = ((int64_t)a->window + chunk - 2) / chunk + 1 + ((int64_t)a->first_tokens + chunk - 1) / chunk;
+  return pair_plan((int64_t)a->sum_q * head_groups(a), chunk_tiles(a->cache, std::min(table_chunks(a->cache), seen)),
+                   a->num_splits, sms);
+}
+
+void set_parts(WindowParams* p, const WindowPlan& plan, void* workspace) {
+  p->whole = (int32_t)plan.whole;
+  p->num_splits = plan.splits;
+  if (plan.bytes == 0) return;
+  p->part_o = static_cast<float*>(workspace);
+  p->part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.lse);
+}
+
 // ----------------------------------------------------------------- prefix
 
 smla_status check_prefix(const smla_prefix_args* a) {
@@ -198,8 +215,25 @@ smla_status check_prefix(const smla_prefix_args* a) {
   return SMLA_OK;
 }
 
-// The workspace's parts: fp32 partials (two for each SM; where prefixes can be
-// shared, one more for each block of 64 rows and each cut through them), then the plan.
+// Prefixes are computed once for a group's tokens where that can save more than the
+// plan and the merge cost: 6 tiles an SM, by what the tables allow.  Measured on a GB300
+// (shared, each by itself): 64 tokens of 8 heads over 1300 rows 29.1 us and 26.4 (4.1
+// tiles an SM saved), over 2500 29.6 and 35.4 (7.4); of 32 heads over 2500 37.5 and 37.6
+// (4.2), over 4900 51.0 and 57.9 (8.2); 16 of 32 heads over 16000 48.3 and 46.7 (6.6).
+constexpr double kSavedTiles = 6;
+bool shares_prefixes(const smla_prefix_args* a, int sms) {
+  if (a->num_groups == 0) return false;
+  const double empty = head_groups(a) - (double)a->num_heads / kWindowHeads;   // of a token's blocks of 64 rows
+  return a->sum_q * empty * (double)chunk_tiles(a->cache, table_chunks(a->cache)) > kSavedTiles * sms;
+}
+
+// Else each token by itself: a list has a chunk more, where the prefix ends within one.
+WindowPlan grouped_plan(const smla_prefix_args* a, int sms) {
+  return pair_plan((int64_t)a->sum_q * head_groups(a), chunk_tiles(a->cache, table_chunks(a->cache) + 1), 0, sms);
+}
+
+// The workspace's parts: fp32 partials (two for each SM; where prefixes are shared, one
+// more for each block of 64 rows and each cut through them), then the plan.
 struct PrefixLayout {
   int64_t parts;
   int shares;
@@ -209,9 +243,7 @@ PrefixLayout prefix_layout(const smla_prefix_args* a, int sms) {
   const int64_t T = a->sum_q, heads = (a->num_heads + kWindowHeads - 1) / kWindowHeads;
   PrefixLayout l;
   l.shares = std::min(sms, kMaxShares);
-  l.parts = 2 * (int64_t)l.shares;
-  if (a->num_heads % kWindowHeads != 0 && a->num_groups > 0)
-    l.parts += T * heads + T * a->num_heads / kWindowHeads + a->num_groups + l.shares;
+  l.parts = 3 * (int64_t)l.shares + T * heads + T * a->num_heads / kWindowHeads + a->num_groups;
   const size_t rows = (size_t)l.parts * kWindowHeads, segments = (size_t)a->num_groups + T;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -221,7 +253,7 @@ PrefixLayout prefix_layout(const smla_prefix_args* a, int sms) {
   };
   take(rows * kHeadDim * sizeof(float));
   l.lse = take(rows * sizeof(float));
-  l.header = take(2 * sizeof(int64_t));
+  l.header = take(2 * sizeof(int64_t) + sizeof(int32_t));
   l.cost_of = take((segments + 1) * sizeof(int64_t));
   l.unit_of = take((segments + 1) * sizeof(int32_t));
   l.shared_of = take(segments * sizeof(int32_t));
@@ -355,13 +387,8 @@ smla_status smla_window_attention(const smla_window_args* a, void* stream) {
   WindowParams p = attention_params(a);
   p.window = a->window;
   p.first_tokens = a->first_tokens;
-  p.whole = (int32_t)plan.whole;
-  p.num_splits = plan.splits;
-  if (plan.bytes > 0) {
-    p.part_o = static_cast<float*>(a->workspace);
-    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + plan.lse);
-  }
-  return launched("window attention", launch_window_attention(p, sms, static_cast<cudaStream_t>(stream)));
+  set_parts(&p, plan, a->workspace);
+  return launched("window attention", launch_pair_attention(p, nullptr, sms, static_cast<cudaStream_t>(stream)));
 }
 
 smla_status smla_prefix_workspace_size(const smla_prefix_args* args, int device, size_t* bytes) {
@@ -369,7 +396,7 @@ smla_status smla_prefix_workspace_size(const smla_prefix_args* args, int device,
   SMLA_TRY(check_prefix(args));
   int sms = 0;
   SMLA_TRY(device_sms(device, &sms));
-  *bytes = args->sum_q == 0 ? 0 : prefix_layout(args, sms).bytes;
+  *bytes = args->sum_q == 0 ? 0 : shares_prefixes(args, sms) ? prefix_layout(args, sms).bytes : grouped_plan(args, sms).bytes;
   return SMLA_OK;
 }
 
@@ -381,22 +408,31 @@ smla_status smla_prefix_attention(const smla_prefix_args* a, void* stream) {
   SMLA_TRY(need_words("prefix_lens", a->prefix_lens, a->num_groups > 0));
   int sms = 0;
   SMLA_TRY(current_sms(&sms));
+  WindowParams p = attention_params(a);
+  PrefixPlan plan;
+  memset(&plan, 0, sizeof(plan));
+  plan.groups = a->num_groups;
+  plan.group_starts = a->group_starts;
+  plan.prefix_lens = a->prefix_lens;
+  if (!shares_prefixes(a, sms)) {
+    const WindowPlan w = grouped_plan(a, sms);
+    if (w.units > 0x7fffffff || (int64_t)a->sum_q * head_groups(a) > 0x7fffffff / kWindowHeads)
+      return fail(SMLA_ERR_UNSUPPORTED, "%lld units are too many", (long long)w.units);
+    SMLA_TRY(need_workspace(a->workspace, a->workspace_bytes, w.bytes));
+    set_parts(&p, w, a->workspace);
+    return launched("prefix attention", launch_pair_attention(p, &plan, sms, static_cast<cudaStream_t>(stream)));
+  }
   const PrefixLayout l = prefix_layout(a, sms);
   if (l.parts + 2 * (int64_t)a->sum_q > 0x7fffffff / kWindowHeads)
     return fail(SMLA_ERR_UNSUPPORTED, "%d tokens are too many", a->sum_q);
   SMLA_TRY(need_workspace(a->workspace, a->workspace_bytes, l.bytes));
-  WindowParams p = attention_params(a);
   char* const ws = static_cast<char*>(a->workspace);
   p.part_o = static_cast<float*>(a->workspace);
   p.part_lse = reinterpret_cast<float*>(ws + l.lse);
-  PrefixPlan plan;
-  memset(&plan, 0, sizeof(plan));
-  plan.groups = a->num_groups;
   plan.shares = l.shares;
-  plan.group_starts = a->group_starts;
-  plan.prefix_lens = a->prefix_lens;
   plan.share_cost = reinterpret_cast<int64_t*>(ws + l.header);
   plan.share_by = reinterpret_cast<uint64_t*>(ws + l.header + sizeof(int64_t));
+  plan.many = reinterpret_cast<int32_t*>(ws + l.header + 2 * sizeof(int64_t));
   plan.cost_of = reinterpret_cast<int64_t*>(ws + l.cost_of);
   plan.unit_of = reinterpret_cast<int32_t*>(ws + l.unit_of);
   plan.shared_of = reinterpret_cast<int32_t*>(ws + l.shared_of);

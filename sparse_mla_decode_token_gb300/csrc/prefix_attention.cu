@@ -12,6 +12,8 @@
 // A group is split so where it saves tiles: with heads in multiples of 64, or one
 // token, there is nothing to save, and its tokens go through one list of rows, the
 // prefix through the table of the first request of the group that has new tokens.
+// Where a call can save little in all, there is no plan: its tokens are the window
+// attention's pairs, with such lists (kGroupedPairs; cache_api.cu chooses).
 //
 // The lengths are on the device, so the plan is made there, by one CTA.  Each block
 // of 64 rows costs 2.25 tiles' time for its query, sums and results and one for each
@@ -22,12 +24,12 @@
 // What bounds it: the tile's chain in the kernel (window_attention.cu; 2.4 us a tile,
 // its tensor instructions 1.37), 8 us to a CTA's first scores and 4 of results, and
 // before and behind it the plan (4.5 us: trips to L2 and barriers of one CTA; with
-// 1024 threads 6) and the merge (3.5 us: four trips).  Measured on a GB300: 4 samples of
-// 16 heads behind 510 tokens 21.4 us; 64 samples of 16 heads behind 8 prompts of 4 to 8
+// 1024 threads 6) and the merge (3.5 us: four trips).  Measured on a GB300: 64 samples of 16 heads behind 8 prompts of 4 to 8
 // thousand 43.1 us, 309 TFLOP/s; 128 beams of 8 heads behind 4 documents of 16 thousand
-// 65.5 us, 523 TFLOP/s; 160 tokens of 128 heads over 1000 to 2560 rows 116.9 us, 640
-// TFLOP/s.  (Pieces of one size, the best of 32 by a cost model, in turns of the SMs:
-// 54.6, 78.4 and 168 us for the last three where shares took 46.7, 69.8 and 126.)
+// 65.5 us, 523 TFLOP/s (each token by itself: 81.6 and 276).  Without a plan: 4 samples of
+// 16 heads behind 510 tokens 14.0 us (21.4 with one); 160 tokens of 128 heads over 1000 to
+// 2560 rows 113 us, 662 TFLOP/s (117).  (Pieces of one size, the best of 32 by a cost
+// model, in turns of the SMs: 54.6, 78.4 and 168 us where shares took 46.7, 69.8 and 126.)
 #include <algorithm>
 
 #include "cache.cuh"
@@ -120,6 +122,7 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
   __shared__ int s_shared[kNearSegments];
   __shared__ int s_first[kMaxShares + 1], s_end[kMaxShares + 1], s_segment[kMaxShares + 1];
   __shared__ Scan s_scan;
+  __shared__ int s_most;                          // tiles of the longest list
   const CacheView& c = p.c;
   const int lane = threadIdx.x & 31;
   const int sms = plan.shares, heads = blocks_of(p.H), cap = c.max_pages * c.page_size, T = c.sum_q, segments = plan.groups + T;
@@ -151,6 +154,7 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
     for (int b = b0 + kThreads; b < c.batch; b += kThreads) unordered |= fetch(c.cum + b) > fetch(c.cum + b + 1);
   for (int t = threadIdx.x; t < T; t += kThreads) token[t] = make_int4(-1, 0, -1, 0);
   if (bad) flag(p.err, SMLA_DEVERR_PAGE_STATE);
+  if (threadIdx.x == 0) s_most = 1;
   const int groups = __syncthreads_or(bad || unordered) ? 0 : plan.groups;
   auto group_of = [&](int b) {
     const int g = last_of(groups, [&](int x) { return starts[x] <= b; });
@@ -250,6 +254,7 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
     }
     // (units and shared units in one word: both are under 2^31)
     int64_t cost = (int64_t)units * plan_cost(tiles), counts = units | (int64_t)(shared ? units : 0) << 32;
+    if (units > 0) atomicMax(&s_most, tiles);
     int64_t all_cost, all_counts;
     scan(s_scan, cost, counts, &all_cost, &all_counts);
     if (s < segments) {
@@ -312,17 +317,17 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
   }
   if (threadIdx.x == 0) {
     *plan.share_cost = share;
+    *plan.many = (int64_t)s_most * kPlanTile / share + 2 > kManyPieces;
     *plan.share_by = cost0 >> 34 == 0 && share >> 29 == 0 ? ~0ull / (uint64_t)share + 1 : 0;
   }
 }
 
 // ------------------------------------------------------------------- merge
 // Weights 2^(LSE_s - LSE) of a head's partials, then the sink and bmm2.  A warp a head,
-// 16 dims a lane; where there are many partials, the eight warps of a CTA share those
-// of one head after another.  (A CTA a head, four teams of threads to share its partials:
-// 60 us more, for starting CTAs that find nothing to do.)
+// 16 dims a lane; where blocks may be in many shares, a CTA a head, its eight warps
+// sharing the partials.  (A CTA a head always, four teams of threads to share its
+// partials: 60 us more, for starting CTAs that find nothing to do.)
 constexpr int kMergeWarps = 8;
-constexpr int kManyPartials = 24;
 
 // A head's partials: of the prefix, then of the token's own list; one for each share
 // that the block has tiles in.
@@ -338,75 +343,104 @@ __device__ __forceinline__ int64_t partial_row(const Partials& q, int s) {
   return (int64_t)(q.own + s * q.own_step + (s == 0 ? q.own_first : 0)) * kWindowHeads + q.own_row;
 }
 
-// Items: where prefixes can be shared, eight heads of each token; then, for shares 1 and
-// up, sixteen heads of a block that the share's beginning cuts (the second share of the
-// block merges it).
-constexpr int kCutHeads = 2 * kMergeWarps, kCutItems = kWindowHeads / kCutHeads, kMergeCtas = 3;
+// Items: `each` heads of each token; then, for shares 1 and up, 2 * each heads of a block
+// that the share's beginning cuts (the second share of the block merges it).
+constexpr int kMergeCtas = 3;
 
-__global__ void __launch_bounds__(kMergeWarps * 32, kMergeCtas) prefix_merge_kernel(const WindowParams p, const PrefixPlan plan, int64_t token_items) {
+struct MergeItem {
+  int t, h0, heads, tiles, own, owns, own_first, own_step;
+  int row0, prefix_tiles, shared;                 // row0 < 0: no prefix
+  int64_t prefix_at;
+};
+
+// What the plan says of an item; `loaded` between its trips to L2 and the rest.  heads = 0: nothing to do.
+template <class F>
+__device__ __forceinline__ MergeItem merge_item(const WindowParams& p, const PrefixPlan& plan, int64_t item, int each, F loaded) {
+  const int per_token = (p.H + each - 1) / each;
+  const int64_t token_items = (int64_t)p.c.sum_q * per_token;
+  const int shift = cache_box_shift(p.c.page_size), cap = p.c.max_pages * p.c.page_size;
+  MergeItem m = {};
+  m.row0 = -1;
+  m.own_step = 1;
+  if (item >= token_items) {
+    const int per_share = kWindowHeads / (2 * each);
+    const int cut = (int)(item - token_items), i = 1 + cut / per_share;
+    const int4 mine = __ldcg(plan.share + i);
+    const int before = __ldcg(plan.share + i - 1).x;
+    if (mine.y == 0 || mine.z < plan.groups) return m;
+    m.t = mine.z - plan.groups;
+    const int4 v = __ldcg(plan.token + m.t);
+    const int block = mine.x - __ldcg(plan.unit_of + mine.z);
+    const int64_t cost = __ldcg(plan.cost_of + mine.z);
+    const auto [share, by] = loaded();
+    m.tiles = tiles_of(v.w, v.w, v.z, cap, shift);
+    const int64_t at = cost + block * plan_cost(m.tiles) + kPlanUnit;
+    if (v.y < 0 || at >= i * share || at < (i - 1) * share) return m;   // shared, or not its second one
+    m.h0 = block * kWindowHeads + cut % per_share * 2 * each;
+    m.heads = 2 * each;
+    m.own = 2 * (i - 1);
+    m.own_step = 2;
+    m.own_first = before != mine.x;
+    m.owns = share_of(at + (int64_t)(m.tiles - 1) * kPlanTile, share, by) - (i - 1) + 1;
+  } else {
+    m.t = (int)(item / per_token);
+    m.h0 = (int)(item - (int64_t)m.t * per_token) * each;
+    const int4 v = __ldcg(plan.token + m.t), w = __ldcg(plan.prefix_of + m.t);
+    const int64_t cost = __ldcg(plan.cost_of + plan.groups + m.t);
+    const int units = __ldcg(plan.shared_of + plan.groups + m.t);
+    if (v.x < 0 || v.y >= 0) return m;
+    const auto [share, by] = loaded();
+    m.heads = each;
+    m.tiles = tiles_of(0, v.w, v.z, cap, shift);
+    if (m.tiles > 0) {
+      const int block = m.h0 / kWindowHeads;      // (eight heads from a multiple of eight lie in one)
+      const int64_t at = cost + block * plan_cost(m.tiles) + kPlanUnit;
+      const int c0 = share_of(at, share, by);
+      m.own = 2 * plan.shares + units + block + c0;
+      m.owns = share_of(at + (int64_t)(m.tiles - 1) * kPlanTile, share, by) - c0 + 1;
+    }
+    m.row0 = w.w;
+    m.shared = w.z;
+    m.prefix_at = ((int64_t)w.y << 32 | (uint32_t)w.x) + kPlanUnit;
+    m.prefix_tiles = tiles_of(v.w, 0, -1, cap, shift);
+  }
+  return m;
+}
+
+struct ShareCost {
+  int64_t cost;
+  uint64_t by;
+};
+
+__global__ void __launch_bounds__(kMergeWarps * 32, kMergeCtas) prefix_merge_kernel(const WindowParams p, const PrefixPlan plan) {
   __shared__ float4 s_share[kMergeWarps][kHeadDim / 4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int shares = plan.shares, per_token = (p.H + kMergeWarps - 1) / kMergeWarps;
-  const int shift = cache_box_shift(p.c.page_size), cap = p.c.max_pages * p.c.page_size;
+  const int shares = plan.shares;
   await_prior_kernel();
   admit_next_kernel();
-  const int64_t share = __ldcg(plan.share_cost), items = token_items + (shares - 1) * kCutItems;
-  const uint64_t by = __ldcg(plan.share_by);
+  const ShareCost cost = {__ldcg(plan.share_cost), __ldcg(plan.share_by)};
+  const bool many = __ldcg(plan.many) != 0;
+  const int64_t share = cost.cost;
+  const uint64_t by = cost.by;
+  const auto loaded = [&] { return cost; };
+  const int each = many ? 1 : kMergeWarps;
+  const int64_t items = (int64_t)p.c.sum_q * ((p.H + each - 1) / each) + (shares - 1) * (kWindowHeads / (2 * each));
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    int t, h0, heads = kMergeWarps, tiles, own = 0, owns = 0, own_first = 0, own_step = 1, row0 = -1, prefix_tiles = 0, shared = 0;
-    int64_t prefix_at = 0;
-    if (item >= token_items) {
-      const int cut = (int)(item - token_items), i = 1 + cut / kCutItems;
-      const int4 mine = __ldcg(plan.share + i);
-      const int before = __ldcg(plan.share + i - 1).x;
-      if (mine.y == 0 || mine.z < plan.groups) continue;
-      t = mine.z - plan.groups;
-      const int4 v = __ldcg(plan.token + t);
-      const int block = mine.x - __ldcg(plan.unit_of + mine.z);
-      tiles = tiles_of(v.w, v.w, v.z, cap, shift);
-      const int64_t at = __ldcg(plan.cost_of + mine.z) + block * plan_cost(tiles) + kPlanUnit;
-      if (v.y < 0 || at >= i * share || at < (i - 1) * share) continue;   // shared, or not its second one
-      h0 = block * kWindowHeads + cut % kCutItems * kCutHeads;
-      heads = kCutHeads;
-      own = 2 * (i - 1);
-      own_step = 2;
-      own_first = before != mine.x;
-      owns = share_of(at + (int64_t)(tiles - 1) * kPlanTile, share, by) - (i - 1) + 1;
-    } else {
-      t = (int)(item / per_token);
-      h0 = (int)(item - (int64_t)t * per_token) * kMergeWarps;
-      const int4 v = __ldcg(plan.token + t), w = __ldcg(plan.prefix_of + t);
-      const int64_t cost = __ldcg(plan.cost_of + plan.groups + t);
-      const int units = __ldcg(plan.shared_of + plan.groups + t);
-      if (v.x < 0 || v.y >= 0) continue;
-      tiles = tiles_of(0, v.w, v.z, cap, shift);
-      if (tiles > 0) {
-        const int block = h0 / kWindowHeads;      // (eight heads from a multiple of eight lie in one)
-        const int64_t at = cost + block * plan_cost(tiles) + kPlanUnit;
-        const int c0 = share_of(at, share, by);
-        own = 2 * shares + units + block + c0;
-        owns = share_of(at + (int64_t)(tiles - 1) * kPlanTile, share, by) - c0 + 1;
-      }
-      row0 = w.w;
-      shared = w.z;
-      prefix_at = ((int64_t)w.y << 32 | (uint32_t)w.x) + kPlanUnit;
-      prefix_tiles = tiles_of(v.w, 0, -1, cap, shift);
-    }
+    const MergeItem m = many ? merge_item(p, plan, item, 1, loaded) : merge_item(p, plan, item, kMergeWarps, loaded);
+    if (m.heads == 0) continue;
     const auto head = [&](int h) {                // the partials of head h
-      Partials q = {0, 0, own, owns, own_first, own_step, 0, h % kWindowHeads};
-      if (row0 >= 0) {
-        const int row = row0 + h, block = row / kWindowHeads;
-        const int64_t at = prefix_at + block * plan_cost(prefix_tiles);
+      Partials q = {0, 0, m.own, m.owns, m.own_first, m.own_step, 0, h % kWindowHeads};
+      if (m.row0 >= 0) {
+        const int row = m.row0 + h, block = row / kWindowHeads;
+        const int64_t at = m.prefix_at + block * plan_cost(m.prefix_tiles);
         const int c0 = share_of(at, share, by);
-        q.prefix = 2 * shares + shared + block + c0;
-        q.prefixes = share_of(at + (int64_t)(prefix_tiles - 1) * kPlanTile, share, by) - c0 + 1;
+        q.prefix = 2 * shares + m.shared + block + c0;
+        q.prefixes = share_of(at + (int64_t)(m.prefix_tiles - 1) * kPlanTile, share, by) - c0 + 1;
         q.prefix_row = row % kWindowHeads;
       }
       return q;
     };
-    // (the same for all the CTA's heads, whose prefix blocks may differ by a piece)
-    const bool many = owns + (int)(prefix_tiles * kPlanTile / share) > kManyPartials;
-    for (int h = h0 + (many ? 0 : warp); h < min(h0 + heads, p.H); h += many ? 1 : kMergeWarps) {
+    for (int h = m.h0 + (many ? 0 : warp); h < min(m.h0 + m.heads, p.H); h += many ? 1 : kMergeWarps) {
       const Partials q = head(h);
       const int n = q.prefixes + q.owns;
       float top = -INFINITY, sum = 0.f;
@@ -469,7 +503,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kMergeCtas) prefix_merge_ker
         f = fetch_scale(p.bmm2, p.bmm2_dev) / sum;
         if (p.sinks != nullptr) f *= 1.f / (1.f + fast_exp2(fetch(p.sinks + h) * kLog2e - lse));
       }
-      const int64_t th = (int64_t)t * p.H + h;
+      const int64_t th = (int64_t)m.t * p.H + h;
       if (many) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) s_share[warp][lane + 32 * i] = acc[i];
@@ -502,12 +536,10 @@ cudaError_t launch_prefix_attention(const WindowParams& p, const PrefixPlan& pla
   cudaError_t e = launch_overlapped(prefix_plan_kernel, dim3(1), kThreads, 0, stream, p, plan, cache_box_shift(p.c.page_size));
   if (e == cudaSuccess) e = launch_planned_attention(p, plan, stream);
   if (e != cudaSuccess) return e;
-  const int64_t token_items = plan.groups > 0 && p.H % kWindowHeads != 0
-                                  ? (int64_t)p.c.sum_q * ((p.H + kMergeWarps - 1) / kMergeWarps) : 0;
-  const int64_t items = token_items + (plan.shares - 1) * kCutItems;
-  if (items == 0) return cudaSuccess;
+  // (as many CTAs as the GPU holds at once, or as there may be heads)
+  const int64_t items = (int64_t)p.c.sum_q * p.H + (int64_t)(plan.shares - 1) * (kWindowHeads / 2);
   return launch_overlapped(prefix_merge_kernel, dim3((unsigned)std::min<int64_t>(items, (int64_t)plan.shares * kMergeCtas)),
-                           kMergeWarps * 32, 0, stream, p, plan, token_items);
+                           kMergeWarps * 32, 0, stream, p, plan);
 }
 
 }  // namespace smla

@@ -135,7 +135,10 @@ constexpr int kOffSmall = kOffP + 4 * kPHalf;
 // How the work is cut: each pair of a token and 64 heads by one CTA; some pairs in
 // splits; by the plan of a batch whose groups share prefixes (prefix_attention.cu, which
 // says what that measures).
-constexpr int kPairs = 0, kSplitPairs = 1, kPlanned = 2;
+// Pairs of a batch with groups have lists of two tables, as a plan's.
+constexpr int kPairs = 0, kSplitPairs = 1, kPlanned = 2, kGroupedPairs = 3, kGroupedSplitPairs = 4;
+constexpr bool has_parts(int mode) { return mode == kSplitPairs || mode == kPlanned || mode == kGroupedSplitPairs; }
+constexpr bool two_tables(int mode) { return mode >= kPlanned; }
 
 struct alignas(16) Small {
   float qscale[kNH];                              // bmm1 log2(e) 2^-k of each head
@@ -192,10 +195,46 @@ __device__ __forceinline__ Unit planned_unit(const KernelParams& kp, int x, int 
                    plan.cost_of, plan.unit_of, plan.shared_of, plan.group, plan.token);
 }
 
+// Do the groups' starts fall, or lie outside the batch?  (Whole warp.)
+__device__ __forceinline__ bool groups_out_of_order(const KernelParams& kp, int lane) {
+  bool bad = false;
+  for (int g = lane; g < kp.plan.groups; g += 32) {
+    const int lo = fetch(kp.plan.group_starts + g), hi = fetch(kp.plan.group_starts + g + 1);
+    bad |= lo < 0 || hi < lo || hi > kp.p.c.batch;
+  }
+  return __any_sync(0xffffffffu, bad);
+}
+
+// The prefix that request b's group shares (0: none), and the request that holds it:
+// the first one of the group with new tokens.  (Whole warp; starts in order.)
+__device__ __forceinline__ int group_prefix(const KernelParams& kp, int b, int lane, int* lead) {
+  const CacheView& c = kp.p.c;
+  *lead = b;
+  if (kp.plan.groups == 0) return 0;
+  const int g = last_request(kp.plan.groups, lane, [&](int x) { return fetch(kp.plan.group_starts + x) <= b; });
+  const int lo = fetch(kp.plan.group_starts + g), hi = fetch(kp.plan.group_starts + g + 1);
+  if (b < lo || b >= hi) return 0;
+  int first = 0x7fffffff, limit = 0x7fffffff;
+  for (int x = lo + lane; x < hi; x += 32) {
+    int at, count;
+    request_tokens(c, x, &at, &count);
+    const int len = fetch(c.seq_lens + x);
+    if (count > 0 && at < c.sum_q && (int64_t)at + count > 0) {
+      first = min(first, x);
+      limit = min(limit, max(0, len - count + 1));
+    }
+  }
+  first = __reduce_min_sync(0xffffffffu, first);
+  limit = __reduce_min_sync(0xffffffffu, limit);
+  if (first == 0x7fffffff) return 0;
+  *lead = first;
+  return min(min(max(fetch(kp.plan.prefix_lens + g), 0), limit), c.max_pages * c.page_size);
+}
+
 template <int kShift, int kMode>
-__device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lane) {
+__device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lane, bool alone = false) {
   if constexpr (kMode == kPlanned) return planned_unit<kShift>(kp, x, lane);
-  constexpr bool kParts = kMode != kPairs;
+  constexpr bool kParts = has_parts(kMode);
   const WindowParams& p = kp.p;
   const CacheView& c = p.c;
   Unit u;
@@ -211,7 +250,14 @@ __device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lan
   u.first_chunks = u.window_chunk = u.chunks = 0;
   const int cap = c.max_pages * c.page_size, last = min(u.pos, cap - 1);
   if (u.pos >= cap && lane == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
-  if (last >= 0) {
+  if constexpr (two_tables(kMode)) {
+    u.first = owned && u.pos >= 0 && !alone ? group_prefix(kp, u.b, lane, &u.b0) : 0;   // (the same in all lanes)
+    if (u.first == 0) u.b0 = u.b;
+    u.lo = u.first;
+    u.first_chunks = (u.first + (1 << kShift) - 1) >> kShift;
+    u.window_chunk = u.lo >> kShift;
+    u.chunks = u.first_chunks + (last >= u.lo ? (last >> kShift) - u.window_chunk + 1 : 0);
+  } else if (last >= 0) {
     u.first_chunks = (min(p.first_tokens, last + 1) + (1 << kShift) - 1) >> kShift;
     u.window_chunk = max(u.lo >> kShift, u.first_chunks);
     u.chunks = u.first_chunks + max(0, (last >> kShift) - u.window_chunk + 1);
@@ -231,7 +277,7 @@ __device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lan
 // read past L1, of which the tiles leave a few KB (by L1: prompts 593 us against 581).
 template <int kMode>
 __device__ __forceinline__ const int32_t* chunk_table(const KernelParams& kp, const Unit& u, int k) {
-  return kp.p.c.bt + (kMode == kPlanned && k < u.first_chunks ? u.b0 : u.b) * kp.p.c.bt_stride;
+  return kp.p.c.bt + (two_tables(kMode) && k < u.first_chunks ? u.b0 : u.b) * kp.p.c.bt_stride;
 }
 template <int kShift, int kMode>
 __device__ __forceinline__ int chunk_page(const KernelParams& kp, const Unit& u, int k) {
@@ -361,7 +407,7 @@ __device__ __forceinline__ void split_query(const KernelParams& kp, const Unit& 
 template <int kShift, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_constant__ KernelParams kp) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr bool kParts = kMode != kPairs;
+  constexpr bool kParts = has_parts(kMode);
   Small& sm = *reinterpret_cast<Small*>(smem + kOffSmall);
   const WindowParams& p = kp.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -421,7 +467,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
     constexpr int kBoxes = kRows >> kShift;       // of a tile
     int n = 0;
     bool ok = true;
-    Unit ahead = kMode == kPlanned ? first.unit : make_unit<kShift, kMode>(kp, blockIdx.x, lane);
+    bool alone = false;                           // groups out of order share nothing
+    if constexpr (kMode == kGroupedPairs || kMode == kGroupedSplitPairs) {
+      alone = groups_out_of_order(kp, lane);
+      if (alone && lane == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_PAGE_STATE);
+    }
+    Unit ahead = kMode == kPlanned ? first.unit : make_unit<kShift, kMode>(kp, blockIdx.x, lane, alone);
     auto prefetch_query = [&](const Unit& u) {
       if constexpr (kMode == kPlanned) {          // rows of several tokens: one by one
         for (int i = lane; u.tiles > 0 && i < u.heads; i += 32) {
@@ -480,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         ok = __all_sync(0xffffffffu, good);
         n += i >= 0;
         if (i == min(1, u.tiles - 1) && x + 1 < mine) {       // the next unit and its queries' way to L2
-          ahead = make_unit<kShift, kMode>(kp, kMode == kPlanned ? x + 1 : blockIdx.x + (x + 1) * gridDim.x, lane);
+          ahead = make_unit<kShift, kMode>(kp, kMode == kPlanned ? x + 1 : blockIdx.x + (x + 1) * gridDim.x, lane, alone);
           prefetch_query(ahead);
         }
       }
@@ -508,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_kernel(const __grid_consta
         for (int y = 0; y < kY; ++y) {
           const int r = y * 32 + lane, k = (u.tile0 + i) * per_tile + (r >> kShift);
           const uint32_t j = (uint32_t)((chunk_at(u, min(k, u.chunks - 1)) << kShift) + (r & ((1 << kShift) - 1)));
-          if constexpr (kMode == kPlanned)
+          if constexpr (two_tables(kMode))
             seen[y] = k < u.chunks && (k < u.first_chunks ? (int)j < u.first : (int)j >= u.lo && (int)j <= u.pos);
           else
             seen[y] = k < u.chunks && (int)j <= u.pos && ((int)j >= u.lo || (int)j < p.first_tokens);
@@ -1124,9 +1175,27 @@ cudaError_t encode_out_map(CUtensorMap* map, const WindowParams& p) {
 
 }  // namespace
 
-cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t stream) {
+namespace {
+
+template <int kMode>
+cudaError_t launch_window_kernel(const KernelParams& kp, unsigned grid, int shift, cudaStream_t stream) {
+  auto launch = [&](auto kernel) -> cudaError_t {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (err != cudaSuccess) return err;
+    return launch_overlapped(kernel, dim3(grid), kThreads, kSmemBytes, stream, kp);
+  };
+  if (shift == 5) return launch(window_kernel<5, kMode>);
+  if (shift == 4) return launch(window_kernel<4, kMode>);
+  return launch(window_kernel<3, kMode>);
+}
+
+}  // namespace
+
+// plan: its groups, or nullptr for the window attention.
+cudaError_t launch_pair_attention(const WindowParams& p, const PrefixPlan* plan, int sms, cudaStream_t stream) {
   KernelParams kp;
   kp.p = p;
+  if (plan != nullptr) kp.plan = *plan;
   kp.groups = (p.H + kNH - 1) / kNH;
   const int pairs = (int)((int64_t)p.c.sum_q * kp.groups);
   kp.units = p.whole + (pairs - p.whole) * p.num_splits;
@@ -1134,15 +1203,13 @@ cudaError_t launch_window_attention(const WindowParams& p, int sms, cudaStream_t
   cudaError_t e = encode_cache_map(&kp.map, p.c, 1 << shift);
   if (e == cudaSuccess && p.whole > 0) e = encode_out_map(&kp.out_map, p);   // (partials are stored by threads)
   if (e != cudaSuccess) return e;
-  auto launch = [&](auto kernel) -> cudaError_t {
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (err != cudaSuccess) return err;
-    return launch_overlapped(kernel, dim3((unsigned)std::min(kp.units, sms)), kThreads, kSmemBytes, stream, kp);
-  };
   const bool parts = pairs > p.whole;
-  if (shift == 5) e = parts ? launch(window_kernel<5, kSplitPairs>) : launch(window_kernel<5, kPairs>);
-  else if (shift == 4) e = parts ? launch(window_kernel<4, kSplitPairs>) : launch(window_kernel<4, kPairs>);
-  else e = parts ? launch(window_kernel<3, kSplitPairs>) : launch(window_kernel<3, kPairs>);
+  const unsigned grid = (unsigned)std::min(kp.units, sms);
+  if (plan == nullptr)
+    e = parts ? launch_window_kernel<kSplitPairs>(kp, grid, shift, stream) : launch_window_kernel<kPairs>(kp, grid, shift, stream);
+  else
+    e = parts ? launch_window_kernel<kGroupedSplitPairs>(kp, grid, shift, stream)
+              : launch_window_kernel<kGroupedPairs>(kp, grid, shift, stream);
   if (e != cudaSuccess || !parts) return e;
   const dim3 heads((unsigned)((pairs - p.whole) * (int64_t)kNH));
   if (p.num_splits > 8)                           // what one team loads at a time
@@ -1160,14 +1227,7 @@ cudaError_t launch_planned_attention(const WindowParams& p, const PrefixPlan& pl
   cudaError_t e = encode_cache_map(&kp.map, p.c, 1 << shift);
   if (e == cudaSuccess) e = encode_out_map(&kp.out_map, p);
   if (e != cudaSuccess) return e;
-  auto launch = [&](auto kernel) -> cudaError_t {
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (err != cudaSuccess) return err;
-    return launch_overlapped(kernel, dim3((unsigned)plan.shares), kThreads, kSmemBytes, stream, kp);
-  };
-  if (shift == 5) return launch(window_kernel<5, kPlanned>);
-  if (shift == 4) return launch(window_kernel<4, kPlanned>);
-  return launch(window_kernel<3, kPlanned>);
+  return launch_window_kernel<kPlanned>(kp, (unsigned)plan.shares, shift, stream);
 }
 
 }  // namespace smla

@@ -90,7 +90,26 @@ def queries(q):
     return t.to(DEV), t.to(torch.float64).numpy()
 
 
-def run(cache, starts, prefix, q, *, sinks=None, bmm1=SCALE, bmm2=1.0, flag=0, uniform=False, cum=None, stream=None):
+def widened(tables, tokens, heads):
+    """The tables with as many more columns (no pages) as make the call long enough, by what it knows of the lengths, to
+    compute shared prefixes once for all: shorter ones take each token by itself."""
+    empty = -(-heads // 64) - heads / 64                   # of a token's blocks of 64 rows: what sharing may save
+    columns = int(5 * 152 * 128 / 8 / (tokens * empty)) + 1 if empty else 3
+    return np.concatenate([tables, np.full((tables.shape[0], columns), -77, dtype=np.int32)], axis=1)
+
+
+def run(cache, *args, **kw):
+    """The results of the call as it is, and on widened tables."""
+    q, tables = args[2], cache.tables
+    first = run_one(cache, *args, **kw)
+    try:
+        cache.tables = widened(tables, q.shape[0], q.shape[1])
+        return first, run_one(cache, *args, **kw)
+    finally:
+        cache.tables = tables
+
+
+def run_one(cache, starts, prefix, q, *, sinks=None, bmm1=SCALE, bmm2=1.0, flag=0, uniform=False, cum=None, stream=None):
     qt = q if isinstance(q, torch.Tensor) else queries(q)[0]
     g = on_gpu(cache)
     cum = None if uniform else i32(cache.cum) if cum is None else cum
@@ -107,8 +126,13 @@ def run(cache, starts, prefix, q, *, sinks=None, bmm1=SCALE, bmm2=1.0, flag=0, u
     return out.to(torch.float64).cpu().numpy(), lse.to(torch.float64).cpu().numpy()
 
 
-def check(cache, q, got, **kw):
-    out, lse, tol_o, tol_l = R.window(cache, queries(q)[1], window=1 << 30, bmm1=kw.pop("bmm1", SCALE), **kw)
+def check(cache, q, results, **kw):
+    want = R.window(cache, queries(q)[1], window=1 << 30, bmm1=kw.pop("bmm1", SCALE), **kw)
+    for got in results:
+        check_one(got, *want)
+
+
+def check_one(got, out, lse, tol_o, tol_l):
     empty = np.isneginf(lse)
     assert np.array_equal(np.isneginf(got[1]), empty) and np.all(got[0][empty] == 0)
     bad = ~(np.abs(got[0] - out) <= tol_o) & ~empty[..., None]
@@ -168,7 +192,7 @@ def test_a_prefix_past_what_all_see_ends_there(heads):
     got = run(cache, starts, [5000], q)
     check(cache, q, got)
     assert cache.prefix.max() == 103
-    assert np.array_equal(first[0], got[0])
+    assert all(np.array_equal(a[0], b[0]) for a, b in zip(first, got))
     cache.groups(starts, [-5])
     check(cache, q, run(cache, starts, [-5], q))
 
@@ -192,7 +216,7 @@ def test_a_token_of_nothing_but_the_prefix():
 
 def test_equal_to_the_window_attention_on_shared_pages():
     cache, starts, q, _ = make(8, [8, 8], [640, 320], [1 + i for i in range(16)], [1] * 16, heads=16, shared=True)
-    got = run(cache, starts, [640, 320], q)
+    results = run(cache, starts, [640, 320], q)
     g, qt = on_gpu(cache), queries(q)[0]
     prefix = i32([-1, -1])
     C.pages_shared_prefix(g[2], g[3], i32(starts), prefix, page_size=64)
@@ -201,17 +225,18 @@ def test_equal_to_the_window_attention_on_shared_pages():
     out, lse = C.window_attention(qt, *g, ws, window=1 << 20, bmm1_scale=SCALE)
     torch.cuda.synchronize()
     # both within 2^-7 of the value (weights and output rounded to BF16) of each other, and of the weighted rows' size
-    limit = 2.0 ** -7 * np.abs(got[0]) + 2.0 ** -8 * np.sqrt((got[0] ** 2).mean(axis=-1, keepdims=True)) * 8
-    assert np.all(np.abs(out.double().cpu().numpy() - got[0]) <= limit)
-    assert np.all(np.abs(lse.double().cpu().numpy() - got[1]) <= 2.0 ** -15 * np.abs(got[1]))
+    for got in results:
+        limit = 2.0 ** -7 * np.abs(got[0]) + 2.0 ** -8 * np.sqrt((got[0] ** 2).mean(axis=-1, keepdims=True)) * 8
+        assert np.all(np.abs(out.double().cpu().numpy() - got[0]) <= limit)
+        assert np.all(np.abs(lse.double().cpu().numpy() - got[1]) <= 2.0 ** -15 * np.abs(got[1]))
 
 
 def test_padded_batches_leave_their_outputs_alone():
     cache, starts, q, rng = make(3, [4], [150], [1, 2, 30, 4], [1, 2, 1, 1], heads=16)
     pad = np.concatenate([rng.normal(size=(2, 16, 512)), q, rng.normal(size=(3, 16, 512))])
-    got = run(cache, starts, [150], pad, cum=i32(cache.cum + 2))
-    assert np.isnan(got[0][:2]).all() and np.isnan(got[0][-3:]).all() and np.isnan(got[1][:2]).all()
-    check(cache, q, (got[0][2:-3], got[1][2:-3]))
+    for got in run(cache, starts, [150], pad, cum=i32(cache.cum + 2)):
+        assert np.isnan(got[0][:2]).all() and np.isnan(got[0][-3:]).all() and np.isnan(got[1][:2]).all()
+        check(cache, q, [(got[0][2:-3], got[1][2:-3])])
 
 
 def test_strided_queries_and_one_group_per_request():
@@ -242,15 +267,18 @@ def test_pages_that_are_none_are_masked_and_flagged():
 def test_a_prefix_row_of_nan_reaches_its_group_only():
     cache, starts, q, _ = make(12, [3, 3], [200, 200], [1, 2, 3, 1, 2, 3], [1] * 6, heads=16)
     cache.rows[cache.tables[0, 1], 3] = 0x7F
-    got = run(cache, starts, [200, 200], q)
-    assert np.isnan(got[0][:3]).all() and np.isnan(got[1][:3]).all()
     out, lse, tol_o, tol_l = R.window(cache, queries(q)[1], window=1 << 30, bmm1=SCALE)
-    assert np.all(np.abs(got[0] - out)[3:] <= tol_o[3:]) and np.all(np.abs(got[1] - lse)[3:] <= tol_l[3:])
+    for got in run(cache, starts, [200, 200], q):
+        assert np.isnan(got[0][:3]).all() and np.isnan(got[1][:3]).all()
+        assert np.all(np.abs(got[0] - out)[3:] <= tol_o[3:]) and np.all(np.abs(got[1] - lse)[3:] <= tol_l[3:])
 
 
-def test_deterministic_captured_and_on_another_stream():
+@pytest.mark.parametrize("wide", [False, True])
+def test_deterministic_captured_and_on_another_stream(wide):
     prefix, q_lens = [900, 300], [1, 2, 1, 1, 3, 1, 1, 1]
     cache, starts, q, rng = make(13, [4, 4], prefix, [1, 9, 3, 4, 50, 6, 7, 8], q_lens, heads=16)
+    if wide:
+        cache.tables = widened(cache.tables, q.shape[0], 16)
     g, qt, s, p, cum = on_gpu(cache), queries(q)[0], i32(starts), i32(prefix), i32(cache.cum)
     ws = torch.empty(C.prefix_workspace_size(qt, *g, group_starts=s, cum_seq_lens_q=cum), dtype=torch.uint8, device=DEV)
     call = lambda **kw: C.prefix_attention(qt, *g, ws, group_starts=s, prefix_lens=p, cum_seq_lens_q=cum, bmm1_scale=SCALE, **kw)
@@ -277,7 +305,7 @@ def test_deterministic_captured_and_on_another_stream():
     graphs[0].replay()
     torch.cuda.synchronize()
     cache.groups(starts, [64, 17])
-    check(cache, q, [t.double().cpu().numpy() for t in outs[0]])
+    check(cache, q, [[t.double().cpu().numpy() for t in outs[0]]])
 
 
 @pytest.mark.parametrize("heads", [16, 64])
@@ -290,9 +318,12 @@ def test_requests_without_tokens_lead_no_group(heads):
     check(cache, q, run(cache, starts, [200, 130], q))
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("cum", [[0, 3, 1, 4], [2, 0, 9, 4], [0, 4, 4, -3]])
-def test_offsets_that_fall_stay_in_range(cum):
+def test_offsets_that_fall_stay_in_range(cum, wide):
     cache, starts, q, _ = make(18, [3], [70], [2, 3, 4], [1, 2, 1], heads=16, shared=True)
+    if wide:
+        cache.tables = widened(cache.tables, 4, 16)
     qt = queries(q)[0]
     g = on_gpu(cache)
     out, lse = torch.full((6, 16, 512), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((6, 16), 7.0, device=DEV)

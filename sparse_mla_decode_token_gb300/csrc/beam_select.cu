@@ -35,8 +35,13 @@ namespace {
 
 constexpr int kScanThreads = 256, kScanCtas = 4;  // threads of a CTA, CTAs of an SM
 constexpr int kScanBatch = 4;                     // blocks that a warp takes at a time
-constexpr int kScanStages = 3;                    // batches in its ring
-constexpr int kScanSmem = kScanThreads / 32 * kScanStages * kScanBatch * kBeamBlockBytes;
+
+// Batches in a warp's ring: copies run one or two ahead.  (16-bit logits, which take more
+// instructions a byte: 38.6 us with two, 39.2 with three; fp32: 53.6 and 51.5.)
+template <class T>
+constexpr int kScanStages = sizeof(T) == 4 ? 3 : 2;
+template <class T>
+constexpr int kScanSmem = kScanThreads / 32 * kScanStages<T> * kScanBatch * kBeamBlockBytes;
 
 template <class T>
 struct Vec {
@@ -159,14 +164,14 @@ struct Cursor {
 
 // Maxima of a unit's blocks, and the sum of e^(x - m) with the largest of them as m.
 // Each lane copies 16 bytes of every block into a ring of its warp's and reads them
-// there itself, so nothing but its own copies is waited for; the copies run two
-// batches ahead, through the ends of units.
+// there itself, so nothing but its own copies is waited for; the copies run
+// ahead through the ends of units.
 template <class T>
 __global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan_kernel(const BeamParams p) {
   extern __shared__ __align__(16) uint8_t ring[];
-  constexpr int kLane = Vec<T>::kLane, kStage = kScanBatch * kBeamBlockBytes;
+  constexpr int kLane = Vec<T>::kLane, kStage = kScanBatch * kBeamBlockBytes, kStages = kScanStages<T>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* const mine = ring + warp * (kScanStages * kStage) + lane * 16;
+  uint8_t* const mine = ring + warp * (kStages * kStage) + lane * 16;
   const uint32_t all = (uint32_t)(p.batch * p.beams) * p.plan.units;
   // (units that follow one another go to different CTAs)
   const uint32_t step = gridDim.x * (kScanThreads / 32);
@@ -195,12 +200,12 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan_kernel(cons
     copy_commit();
   };
 #pragma unroll 1
-  for (int k = 0; k < kScanStages - 1; ++k) load(k);
+  for (int k = 0; k < kStages - 1; ++k) load(k);
   float m = -INFINITY, keep = -INFINITY;
   uint64_t sum = 0;                               // two sums
   for (int stage = 0; at.unit < all;) {
-    load(stage == 0 ? kScanStages - 1 : stage - 1);
-    copy_wait<kScanStages - 1>();
+    load(stage == 0 ? kStages - 1 : stage - 1);
+    copy_wait<kStages - 1>();
     const uint8_t* const from = mine + stage * kStage;
     uint4 v[kScanBatch];
     float top = m;
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan_kernel(cons
       sum = 0;
     }
     at.next(p, all, step);
-    stage = stage == kScanStages - 1 ? 0 : stage + 1;
+    stage = stage == kStages - 1 ? 0 : stage + 1;
   }
 }
 
@@ -382,7 +387,7 @@ __device__ __noinline__ int narrow(Pick& sh, int keep, int n) {
 // particular order hardly more than K reach; an entry's rank is then the number of
 // better ones.  Whole CTA.  (Out of line, once for all steps: what this kernel costs is
 // latency, of which instructions fetched for the first time are a part.)
-__device__ __noinline__ void settle(Pick& sh, int keep, int count, int per_beam, int beams, int room) {
+__device__ __noinline__ void settle(Pick& sh, int keep, int count, int per_beam, int beams, int room, bool again) {
   uint32_t least = sh.least;
   List* list = &sh.list;
   if (count > kDirect) {
@@ -446,7 +451,7 @@ __device__ __noinline__ void settle(Pick& sh, int keep, int count, int per_beam,
     __syncthreads();
   }
   const int found = count;
-  {
+  if (room > 0) {
     constexpr int kEach = kPickThreads / SMLA_MAX_BEAM_OUT;      // threads for each
     const int i = threadIdx.x / kEach, lane = threadIdx.x % kEach;
     const uint32_t mine = i < found ? sh.best[i].index : 0;
@@ -459,7 +464,8 @@ __device__ __noinline__ void settle(Pick& sh, int keep, int count, int per_beam,
       sh.chosen[at] = make_int2((int)beam, (int)(mine - beam * per_beam));
     }
   }
-  for (int i = kPickThreads - 1 - (int)threadIdx.x; i < beams; i += kPickThreads) sh.cut[i] = logit_cut(sh.beam[i], least);
+  if (room > 0 || again)
+    for (int i = kPickThreads - 1 - (int)threadIdx.x; i < beams; i += kPickThreads) sh.cut[i] = logit_cut(sh.beam[i], least);
   if (threadIdx.x == 0) {
     sh.found = found;
     sh.least = least;
@@ -514,7 +520,8 @@ __device__ __forceinline__ void pick(Pick& sh, int keep, int64_t n, int per_beam
       __syncthreads();
       continue;
     }
-    settle(sh, keep, count, per_beam, beams, n > here ? 0 : room);
+    const bool more = tile + here < n;
+    settle(sh, keep, count, per_beam, beams, more ? 0 : room, more);
     found = sh.found;
     tile += here > 0 ? here : 1;
   }
@@ -665,10 +672,10 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
 template <class T>
 cudaError_t launch(const BeamParams& p, int sms, cudaStream_t stream) {
   const int64_t units = (int64_t)p.batch * p.beams * p.plan.units, ctas = (units + kScanThreads / 32 - 1) / (kScanThreads / 32);
-  cudaError_t e = cudaFuncSetAttribute(beam_scan_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScanSmem);
+  cudaError_t e = cudaFuncSetAttribute(beam_scan_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScanSmem<T>);
   if (e != cudaSuccess) return e;
   e = launch_overlapped(beam_scan_kernel<T>, dim3((unsigned)std::min<int64_t>(ctas, (int64_t)sms * kScanCtas)), kScanThreads,
-                        kScanSmem, stream, p);
+                        kScanSmem<T>, stream, p);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(beam_pick_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Pick));
   if (e != cudaSuccess) return e;

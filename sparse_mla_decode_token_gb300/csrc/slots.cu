@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kSlotThreads) token_slots_kernel(const TokenSl
     if (b < p.batch) {
       const int32_t old = fetch(p.lens + b), now = fetch(p.new_lens + b);
       if (old < 0 || now < 0) flag(p.err, SMLA_DEVERR_PAGE_STATE);
-      n = max(0, now - max(0, old));
+      n = max(0, max(0, now) - max(0, old));         // (each at least 0: their difference is an int)
     }
     int64_t sum = n;
 #pragma unroll
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kSparseThreads, 3) sparse_slots_kernel(const S
     first = b * count;
   }
   const bool owned = t >= first && t - first < count;
-  const int pos = owned ? fetch(p.seq_lens + b) - count + (t - first) : -1;
+  const int pos = owned ? max(0, fetch(p.seq_lens + b)) - count + (t - first) : -1;
   const int lo = max(0, pos - (kSwaCols - 1));
   const int limit = pos >= 0 ? (int)(((int64_t)pos + 1) / p.ratio) : 0;
   const int32_t* swa = p.swa.bt + b * p.swa.stride;

@@ -377,6 +377,20 @@ def test_token_slots_flags():
     assert empty.cum_seq_lens_q.cpu().tolist() == [0] and empty.requests.cpu().tolist() == [-1] * 3
 
 
+def test_lengths_of_the_least_number_are_no_tokens():
+    least = -2**31
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = slots.token_slots(i32([5, least, 3]), i32([least, 2, 5]), i32([[1], [2], [3]]), max_tokens=6, page_size=8,
+                            error_word=err)
+    table, topk = slots.sparse_slots(i32([least, 3]), i32([[4], [5]]), 6, page_size=8, cum_seq_lens_q=i32([0, 3, 6]))
+    torch.cuda.synchronize()
+    assert int(err.item()) == B.DEVERR_PAGE_STATE and got.cum_seq_lens_q.cpu().tolist() == [0, 0, 2, 4]
+    assert got.requests.cpu().tolist() == [1, 1, 2, 2, -1, -1] and got.positions.cpu().tolist() == [0, 1, 3, 4, -1, -1]
+    assert got.slots.cpu().tolist() == [16, 17, 27, 28, -1, -1]
+    assert topk.cpu().tolist() == [0, 0, 0, 128, 128, 128] and bool((table[:3] == -1).all())
+    assert table[5, :4].cpu().tolist() == [40, 41, 42, -1]
+
+
 def test_token_slots_past_32_bits():
     got = slots.token_slots(i32([70000]), i32([70003]), i32([[0, 2 ** 31 - 1]]), max_tokens=3, page_size=65536)
     torch.cuda.synchronize()

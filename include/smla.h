@@ -646,7 +646,7 @@ typedef struct smla_sparse_slots_args {
   int64_t comp_table_stride;        /* [comp_max_pages] */
   int32_t comp_max_pages, comp_page_size;
   int32_t compress_ratio;           /* tokens of a compressed row >= 1 */
-  int32_t num_selected;             /* compressed columns >= 0 */
+  int32_t num_selected;             /* compressed columns: 0 .. 2^30 */
   const int32_t* selected;          /* [sum_q, num_selected] compressed positions, or NULL = the first ones */
   int64_t selected_stride;          /* [num_selected] */
   int32_t* sparse_indices;          /* [sum_q, 128 + num_selected] */

@@ -120,8 +120,8 @@ smla_status smla_sparse_slots(const smla_sparse_slots_args* a, void* stream) {
   if (a->cum_seq_lens_q == nullptr && a->sum_q % a->batch != 0)
     return fail(SMLA_ERR_INVALID_ARG, "sum_q %d is not a multiple of batch %d (pass cum_seq_lens_q)", a->sum_q, a->batch);
   SMLA_TRY(check_slot_table("swa_tables", a->swa_table_stride, a->swa_max_pages, a->swa_page_size));
-  if (a->num_selected < 0 || a->num_selected > 0x7fffffff - 2 * kSwaCols)
-    return fail(SMLA_ERR_INVALID_ARG, "num_selected %d is outside 0 .. 2^31 - 257", a->num_selected);
+  if (a->num_selected < 0 || a->num_selected > 1 << 30)                 // (the kernel counts columns past a row's end)
+    return fail(SMLA_ERR_INVALID_ARG, "num_selected %d is outside 0 .. 2^30", a->num_selected);
   if (a->compress_ratio < 1) return fail(SMLA_ERR_INVALID_ARG, "compress_ratio %d < 1", a->compress_ratio);
   if (a->num_selected > 0)
     SMLA_TRY(check_slot_table("comp_tables", a->comp_table_stride, a->comp_max_pages, a->comp_page_size));

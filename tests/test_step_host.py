@@ -131,7 +131,7 @@ def sparse_struct():
     ("sum_q", -1, "sum_q"), ("sum_q", 9, "multiple of batch"), ("batch", 0, "batch"), ("swa_max_pages", 0, "swa_tables"),
     ("swa_page_size", 0, "swa_tables"), ("swa_table_stride", 3, "swa_tables"), ("comp_max_pages", 0, "comp_tables"),
     ("comp_page_size", -1, "comp_tables"), ("comp_max_pages", 1 << 26, "2^31"), ("compress_ratio", 0, "compress_ratio"),
-    ("num_selected", -1, "num_selected"), ("selected_stride", 15, "selected_stride"),
+    ("num_selected", -1, "num_selected"), ("num_selected", (1 << 30) + 1, "2^30"), ("selected_stride", 15, "selected_stride"),
     ("indices_row_stride", 143, "indices_row_stride"), ("seq_lens", None, "seq_lens is required"),
     ("swa_tables", None, "swa_tables is required"), ("comp_tables", None, "comp_tables is required"),
     ("selected", 0x2, "selected must be"), ("sparse_indices", None, "sparse_indices is required"),

@@ -525,6 +525,7 @@ smla_status smla_cache_append(const smla_append_args* args, void* stream);
  *   group_starts[g + 1], with lens[b] > 0 hold in the same columns (the shortest
  *   one's whole pages at most; 0 for a group without such a request).  Looks at
  *   block_tables, lens and page_size only; num_pages and ref_counts are not used.
+ *   prefix_lens overlaps neither lens nor group_starts.
  * smla_pages_compact: the n pages in use move to pages 0 .. n - 1: the k-th
  *   page in use at or past n to the k-th free page before it.  Tables and
  *   counts are renumbered and the pairs (from, to) written to the moves: copy
@@ -548,7 +549,7 @@ typedef struct smla_pages_args {
   const int32_t* lens;          /* [rows] tokens before the call */
   const int32_t* new_lens;      /* [rows] resize: tokens after it */
   const int32_t* parents;       /* [rows] fork: request to share with, or < 0; reorder: request to become, or < 0 */
-  int32_t* out_lens;            /* [rows] fork, reorder: lengths after it; does not overlap lens */
+  int32_t* out_lens;            /* [rows] fork, reorder: lengths after it; overlaps neither lens nor (reorder) parents */
   int32_t* move_src;            /* [move_capacity] resize, compact */
   int32_t* move_dst;            /* [move_capacity] */
   int32_t* move_count;          /* [1] */
@@ -600,7 +601,7 @@ smla_status smla_pages_copy(const smla_pool* pools, int32_t num_pools, int64_t n
  * position past the table, or one whose entry is negative, has slot -1
  * (SMLA_DEVERR_INDEX_OUT_OF_RANGE).  More new tokens than max_tokens set
  * SMLA_DEVERR_TOO_MANY_TOKENS; the offsets are then still those of the whole
- * step (2^31 - 1 at most).
+ * step (2^31 - 1 at most).  No output overlaps lens or new_lens.
  */
 typedef struct smla_token_slots_args {
   const int32_t* lens;          /* [batch] tokens before the step */
@@ -633,7 +634,8 @@ smla_status smla_token_slots(const smla_token_slots_args* args, void* stream);
  * A token of no request (a padded batch) and one with pos < 0 get -1 everywhere
  * and topk_lens 0.  A position past its table, an entry that is negative or a
  * row that is no 32-bit number is -1 and sets SMLA_DEVERR_INDEX_OUT_OF_RANGE
- * (as smla_decode does for rows past its pools).
+ * (as smla_decode does for rows past its pools).  `selected` may be the columns
+ * from 128 on of sparse_indices itself, which then become rows in place.
  */
 typedef struct smla_sparse_slots_args {
   int32_t sum_q, batch;             /* tokens (0 = nothing to do), requests >= 1 */
@@ -669,7 +671,7 @@ smla_status smla_sparse_slots(const smla_sparse_slots_args* args, void* stream);
  * to 2^-45 of their logit or of s_i - log sum, whichever is larger, may count as
  * equal.  Continuations of -infinity are none; places that none is left for
  * hold -infinity, -1 and -1.  out_scores may be `scores` itself where num_out is
- * beams.  A beam with a score of -infinity (an empty place)
+ * beams, and does not overlap it otherwise.  A beam with a score of -infinity (an empty place)
  * has no continuation; its logits do not count, whatever they are, nor do a
  * finished beam's.
  * A NaN or +infinity among the logits or for the score leaves the beam without

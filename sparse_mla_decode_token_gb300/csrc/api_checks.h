@@ -29,6 +29,11 @@ inline smla_status fail(smla_status st, const char* fmt, ...) {
   } while (0)
 
 inline bool aligned(const void* ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
+// Do a[0 .. na) and b[0 .. nb), in bytes, have memory in common?
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + nb && y < x + na;
+}
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 inline smla_status need_words(const char* name, const void* ptr, bool required) {

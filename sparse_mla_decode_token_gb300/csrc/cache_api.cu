@@ -306,8 +306,8 @@ smla_status check_page_pointers(const smla_pages_args* a) {
 smla_status check_parents(const smla_pages_args* a) {
   SMLA_TRY(need_words("parents", a->parents, true));
   SMLA_TRY(need_words("out_lens", a->out_lens, true));
-  const uintptr_t out = reinterpret_cast<uintptr_t>(a->out_lens), in = reinterpret_cast<uintptr_t>(a->lens);
-  if ((out > in ? out - in : in - out) < (uintptr_t)a->rows * sizeof(int32_t))
+  const size_t bytes = (size_t)a->rows * sizeof(int32_t);
+  if (overlap(a->out_lens, bytes, a->lens, bytes))
     return fail(SMLA_ERR_INVALID_ARG, "out_lens must not be lens or overlap it");
   return SMLA_OK;
 }
@@ -505,6 +505,8 @@ smla_status smla_pages_reorder(const smla_pages_args* a, void* stream) {
   if (a->rows == 0) return SMLA_OK;
   SMLA_TRY(check_page_pointers(a));
   SMLA_TRY(check_parents(a));
+  if (overlap(a->out_lens, (size_t)a->rows * sizeof(int32_t), a->parents, (size_t)a->rows * sizeof(int32_t)))
+    return fail(SMLA_ERR_INVALID_ARG, "out_lens must not be parents or overlap them");
   SMLA_TRY(need_workspace(a->workspace, a->workspace_bytes, reorder_workspace(a)));
   int sms = 0;
   SMLA_TRY(current_sms(&sms));
@@ -523,6 +525,10 @@ smla_status smla_pages_shared_prefix(const smla_pages_args* a, const int32_t* gr
     SMLA_TRY(need_words("block_tables", a->block_tables, true));
     SMLA_TRY(need_words("lens", a->lens, true));
   }
+  const size_t groups = (size_t)num_groups * sizeof(int32_t);
+  if (overlap(prefix_lens, groups, group_starts, groups + sizeof(int32_t)) ||
+      overlap(prefix_lens, groups, a->lens, (size_t)a->rows * sizeof(int32_t)))
+    return fail(SMLA_ERR_INVALID_ARG, "prefix_lens must not overlap lens or group_starts");
   return launched("pages shared prefix", launch_pages_shared_prefix(pages_params(a), group_starts, num_groups, prefix_lens,
                                                                     static_cast<cudaStream_t>(stream)));
 }

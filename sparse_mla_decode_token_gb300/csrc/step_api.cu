@@ -95,6 +95,11 @@ smla_status smla_token_slots(const smla_token_slots_args* a, void* stream) {
   SMLA_TRY(need_words("requests", a->requests, false));
   SMLA_TRY(need_words("positions", a->positions, false));
   SMLA_TRY(need_words("error_word", a->error_word, false));
+  const size_t lens = (size_t)a->batch * 4, tokens = (size_t)a->max_tokens * 4;
+  for (const void* in : {a->lens, a->new_lens})
+    if (overlap(a->cum_seq_lens_q, lens + 4, in, lens) || overlap(a->requests, tokens, in, lens) ||
+        overlap(a->positions, tokens, in, lens))
+      return fail(SMLA_ERR_INVALID_ARG, "cum_seq_lens_q, requests and positions must not overlap lens or new_lens");
   TokenSlotsParams p;
   memset(&p, 0, sizeof(p));
   p.lens = a->lens;
@@ -181,6 +186,10 @@ smla_status smla_beam_select(const smla_beam_args* a, void* stream) {
   SMLA_TRY(need_words("out_parents", a->out_parents, true));
   SMLA_TRY(need_words("out_tokens", a->out_tokens, true));
   SMLA_TRY(need_words("error_word", a->error_word, false));
+  const size_t requests = a->batch;
+  if (!(a->out_scores == a->scores && a->num_out == a->beams) &&
+      overlap(a->out_scores, requests * a->num_out * 4, a->scores, requests * a->beams * 4))
+    return fail(SMLA_ERR_INVALID_ARG, "out_scores must be scores (num_out = beams) or not overlap it");
   int sms = 0;
   SMLA_TRY(current_sms(&sms));
   BeamParams p;

@@ -435,6 +435,22 @@ def test_sparse_slots(batch, q_max, keep, page_size, ratio, pad):
     assert int(err.item()) == 0
 
 
+@pytest.mark.parametrize("pad,keep,tokens", [(0, 512, 40), (0, 1040, 3), (3, 37, 300)])
+def test_sparse_slots_of_a_selection_in_place(pad, keep, tokens):
+    rng = np.random.default_rng(17)
+    lens, swa = rng.integers(tokens, 900, 1).astype(np.int32), rng.permutation(20).astype(np.int32)[None]
+    comp = rng.permutation(40).astype(np.int32)[None]
+    picks = rng.integers(-1, 300, (tokens, keep)).astype(np.int32)
+    kw = dict(page_size=64, compressed_tables=i32(comp), compressed_page_size=16, compress_ratio=4)
+    want = slots.sparse_slots(i32(lens), i32(swa), tokens, selected=i32(picks), **kw)
+    table = torch.full((tokens, 128 + keep + pad), -7, dtype=torch.int32, device=DEV)
+    table[:, 128:128 + keep] = i32(picks)
+    got = slots.sparse_slots(i32(lens), i32(swa), tokens, selected=table[:, 128:128 + keep],
+                             sparse_indices=table[:, :128 + keep], **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and bool((table[:, 128 + keep:] == -7).all())
+
+
 def test_sparse_slots_flags_and_uniform_batches():
     err = torch.zeros(1, dtype=torch.int32, device=DEV)
     swa, comp = i32([[3, -1], [2 ** 30, 1]]), i32([[0], [1]])

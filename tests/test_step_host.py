@@ -75,6 +75,8 @@ INVALID, UNSUPPORTED = B.SMLA_ERR_INVALID_ARG, B.SMLA_ERR_UNSUPPORTED
     ("out_scores", None, INVALID, "out_scores is required"),
     ("out_parents", 0x20002, INVALID, "out_parents must be 4-byte"),
     ("out_tokens", None, INVALID, "out_tokens is required"),
+    ("out_scores", 0x20010, INVALID, "out_scores must be scores"),
+    ("out_scores", 0x1fff0, INVALID, "out_scores must be scores"),
     ("error_word", 0x20002, INVALID, "error_word must be 4-byte"),
 ])
 def test_beam_errors(lib, field, value, code, needle):
@@ -110,7 +112,8 @@ def token_struct():
     ("max_pages", 1 << 26, "2^31"), ("block_table_stride", 3, "stride"), ("block_tables", None, "block_tables is required"),
     ("slots", 0x70004, "8-byte"), ("lens", None, "lens is required"), ("new_lens", 0x2, "new_lens must be 4-byte"),
     ("cum_seq_lens_q", None, "cum_seq_lens_q is required"), ("requests", 0x2, "requests must be"),
-    ("positions", 0x2, "positions must be"), ("error_word", 0x2, "error_word must be"),
+    ("positions", 0x2, "positions must be"), ("cum_seq_lens_q", 0xfff0, "overlap"), ("requests", 0x2000c, "overlap"),
+    ("positions", 0xffc8, "overlap"), ("error_word", 0x2, "error_word must be"),
 ])
 def test_token_slots_errors(lib, field, value, needle):
     a = token_struct()
@@ -155,7 +158,7 @@ def pages_struct():
 @pytest.mark.parametrize("field,value,code,needle", [
     ("rows", -1, INVALID, "rows"), ("max_pages", 0, INVALID, "max_pages"), ("num_pages", 0, INVALID, "num_pages"),
     ("parents", None, INVALID, "parents is required"), ("out_lens", 0x30004, INVALID, "overlap"),
-    ("ref_counts", None, INVALID, "ref_counts is required"), ("workspace", None, B.SMLA_ERR_WORKSPACE_TOO_SMALL, "workspace"),
+    ("out_lens", 0x5001c, INVALID, "parents"), ("ref_counts", None, INVALID, "ref_counts is required"), ("workspace", None, B.SMLA_ERR_WORKSPACE_TOO_SMALL, "workspace"),
     ("workspace_bytes", 127, B.SMLA_ERR_WORKSPACE_TOO_SMALL, "256 needed"), ("workspace", 0x100010, INVALID, "256-byte"),
     ("block_table_stride", 3, INVALID, "block_table_stride"),
 ])
@@ -170,6 +173,8 @@ def test_shared_prefix_errors(lib):
     refused(lib.smla_pages_shared_prefix(ctypes.byref(a), 0x1000, -1, 0x2000, None), INVALID, "num_groups")
     refused(lib.smla_pages_shared_prefix(ctypes.byref(a), None, 2, 0x2000, None), INVALID, "group_starts is required")
     refused(lib.smla_pages_shared_prefix(ctypes.byref(a), 0x1000, 2, 0x2001, None), INVALID, "prefix_lens must be")
+    refused(lib.smla_pages_shared_prefix(ctypes.byref(a), 0x1000, 2, 0x1008, None), INVALID, "overlap")
+    refused(lib.smla_pages_shared_prefix(ctypes.byref(a), 0x1000, 2, 0x3001c, None), INVALID, "overlap")
     a.block_tables = None
     refused(lib.smla_pages_shared_prefix(ctypes.byref(a), 0x1000, 2, 0x2000, None), INVALID, "block_tables is required")
 

@@ -35,9 +35,10 @@ namespace {
 
 constexpr int kScanThreads = 256, kScanCtas = 4;  // threads of a CTA, CTAs of an SM
 constexpr int kScanBatch = 4;                     // blocks that a warp takes at a time
+static_assert((1 << kMinUnitShift) % kScanBatch == 0, "units are whole batches");
 
 // Batches in a warp's ring: copies run one or two ahead.  (16-bit logits, which take more
-// instructions a byte: 38.6 us with two, 39.2 with three; fp32: 53.6 and 51.5.)
+// instructions a byte: 33.3 us with two, 34.1 with three; fp32: 53.6 and 51.5.)
 template <class T>
 constexpr int kScanStages = sizeof(T) == 4 ? 3 : 2;
 template <class T>
@@ -71,6 +72,18 @@ __device__ __forceinline__ void unpack(uint4 v, float (&x)[8], const __half*) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
     x[2 * k] = f.x, x[2 * k + 1] = f.y;
   }
+}
+
+// The largest of a lane's elements (16-bit ones in pairs); NaN are passed over.
+__device__ __forceinline__ float largest(uint4 v, const float*) {
+  return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+template <class T>
+__device__ __forceinline__ float largest(uint4 v, const T*) {
+  using Two = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+  const auto two = [](const uint32_t& w) { return *reinterpret_cast<const Two*>(&w); };
+  const Two t = __hmax2(__hmax2(two(v.x), two(v.y)), __hmax2(two(v.z), two(v.w)));
+  return fmaxf(element(&t.x), element(&t.y));
 }
 
 // Four elements, at a multiple of four from a 16-byte boundary.
@@ -187,13 +200,18 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan_kernel(cons
     if (ahead.unit < all) {
       const uint32_t end = (uint32_t)r.before + (uint32_t)p.vocab;
       uint8_t* const to = mine + stage * kStage;
-      uint32_t e = (uint32_t)ahead.j * Vec<T>::kBlock + lane * kLane;
+      const uint32_t first = (uint32_t)ahead.j * Vec<T>::kBlock;
+      if (first >= r.before && first + kScanBatch * Vec<T>::kBlock <= end) {   // (units are whole batches, but for a row's end)
+        const T* const from = r.base + first + lane * kLane;
 #pragma unroll
-      for (int k = 0; k < kScanBatch; ++k, e += Vec<T>::kBlock) {
-        if (ahead.j + k < ahead.j1 && e >= r.before && e + kLane <= end)
-          copy_async(ptx::smem_addr(to + k * kBeamBlockBytes), r.base + e);
-        else
-          *reinterpret_cast<uint4*>(to + k * kBeamBlockBytes) = load_edge(r.base, r.before, e, ahead.j + k < ahead.j1 ? end : 0);
+        for (int k = 0; k < kScanBatch; ++k) copy_async(ptx::smem_addr(to) + k * kBeamBlockBytes, from + k * Vec<T>::kBlock);
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < kScanBatch; ++k) {
+          const uint32_t e = first + k * Vec<T>::kBlock + lane * kLane;
+          if (e >= r.before && e + kLane <= end) copy_async(ptx::smem_addr(to) + k * kBeamBlockBytes, r.base + e);
+          else *reinterpret_cast<uint4*>(to + k * kBeamBlockBytes) = load_edge(r.base, r.before, e, end);
+        }
       }
       if (ahead.next(p, all, step) && ahead.unit < all) r = logits_row<T>(p, ahead.row);
     }
@@ -212,12 +230,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan_kernel(cons
 #pragma unroll
     for (int k = 0; k < kScanBatch; ++k) {
       v[k] = *reinterpret_cast<const uint4*>(from + k * kBeamBlockBytes);
-      float x[kLane];
-      unpack(v[k], x, r.base);
-      float t = x[0];
-#pragma unroll
-      for (int e = 1; e < kLane; ++e) t = fmaxf(t, x[e]);
-      t = ptx::warp_max(t);
+      const float t = ptx::warp_max(largest(v[k], r.base));
       if (lane == at.j + k - at.j0) keep = t;
       top = fmaxf(top, t);
     }

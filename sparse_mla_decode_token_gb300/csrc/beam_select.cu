@@ -517,14 +517,16 @@ __device__ __forceinline__ void pick(Pick& sh, int keep, int64_t n, int per_beam
       for (int e = 0; e < kEach; ++e) maybe |= (uint32_t)(i < here && enough(tile + i + e, x[k][e])) << e;
       if (kEach > 1 && !__any_sync(0xffffffffu, maybe != 0)) continue;
 #pragma unroll 1
-      for (int e = 0; e < kEach; ++e) {           // (few get here, where there are many)
+      do {                                        // each lane's next one (where there are many, few get here)
+        const int e = __ffs(maybe) - 1;
         float y = x[k][0];
 #pragma unroll
         for (int c = 1; c < kEach; ++c) y = e == c ? x[k][c] : y;
         Rank r = {0, 0, 0};
-        if (maybe >> e & 1) r = rank(tile + i + e, y);
+        if (maybe != 0) r = rank(tile + i + e, y);
         sh.list.append(&sh.count, r.hi != 0 && r.hi >= least, r);
-      }
+        maybe &= maybe - 1;
+      } while (kEach > 1 && __any_sync(0xffffffffu, maybe != 0));
     }
     __syncthreads();
     const int count = sh.count;
@@ -653,7 +655,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
         if (e >= s_from[k] && e + 4 <= s_to[k]) {
           load_four(from, x);
         } else {
-#pragma unroll 1
+#pragma unroll
           for (int i = 0; i < 4; ++i) x[i] = e + i >= s_from[k] && e + i < s_to[k] ? element(from + i) : 0.f;
         }
       },

@@ -17,11 +17,11 @@
 // fp64, which has a fiftieth of fp32's rate, the second kernel takes 15 us for the
 // 32 beams of a request alone.)
 //
-// What bounds it: the first kernel reads each logit once (118 MB in 24 us, 4.9 TB/s; a
-// kernel that only reads them takes 20), the second is a dozen dependent phases of one
-// CTA a request.  Measured on a GB300: 64 requests of 8 beams over 128000 BF16 logits, 16
-// kept: 37.3 us (the choice 11); 8 of 32 beams over 151001 FP32 logits, 64 kept: 48.9
-// (21); one of 4 beams over 32000: 12.6 (9).
+// What bounds it: the first kernel reads each logit once (116 MB in 22 us, 5.3 TB/s; a
+// kernel that only reads them takes 20) with two thirds of the issue slots taken, the
+// second is a dozen dependent phases of one CTA a request.  Measured on a GB300: 64
+// requests of 8 beams over 128000 BF16 logits, 16 kept: 33.2 us (the choice 11); 8 of 32
+// beams over 151001 FP32 logits, 64 kept: 45.8 (19); one of 4 beams over 32000: 12.2 (9).
 #include <cuda_fp16.h>
 
 #include <algorithm>

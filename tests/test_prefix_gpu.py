@@ -94,7 +94,7 @@ def widened(tables, tokens, heads):
     """The tables with as many more columns (no pages) as make the call long enough, by what it knows of the lengths, to
     compute shared prefixes once for all: shorter ones take each token by itself."""
     empty = -(-heads // 64) - heads / 64                   # of a token's blocks of 64 rows: what sharing may save
-    columns = int(5 * 152 * 128 / 8 / (tokens * empty)) + 1 if empty else 3
+    columns = int(7 * 152 * 128 / 8 / (tokens * empty)) + 1 if empty else 3
     return np.concatenate([tables, np.full((tables.shape[0], columns), -77, dtype=np.int32)], axis=1)
 
 
@@ -306,6 +306,28 @@ def test_deterministic_captured_and_on_another_stream(wide):
     torch.cuda.synchronize()
     cache.groups(starts, [64, 17])
     check(cache, q, [[t.double().cpu().numpy() for t in outs[0]]])
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_two_calls_at_once_on_two_streams(wide):
+    prefix, q_lens = [700, 130], [1, 1, 2, 1, 1, 5]
+    calls, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for seed in (31, 32):
+        cache, starts, q, rng = make(seed, [3, 3], prefix, [1, 90, 3, 4, 50, 6], q_lens, heads=16)
+        if wide:
+            cache.tables = widened(cache.tables, q.shape[0], 16)
+        g, qt, s, p, cum = on_gpu(cache), queries(q)[0], i32(starts), i32(prefix), i32(cache.cum)
+        ws = torch.empty(C.prefix_workspace_size(qt, *g, group_starts=s, cum_seq_lens_q=cum), dtype=torch.uint8, device=DEV)
+        kw = dict(group_starts=s, prefix_lens=p, cum_seq_lens_q=cum, bmm1_scale=SCALE)
+        calls.append(((qt, *g, ws), kw, [t.clone() for t in C.prefix_attention(qt, *g, ws, **kw)],
+                      torch.empty_like(qt), torch.empty(qt.shape[:2], device=DEV)))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (args, kw, _, out, lse), stream in zip(calls, streams):
+            C.prefix_attention(*args, **kw, out=out, out_lse=lse, stream=stream.cuda_stream)
+    torch.cuda.synchronize()
+    for _, _, first, out, lse in calls:
+        assert torch.equal(first[0], out) and torch.equal(first[1], lse)
 
 
 @pytest.mark.parametrize("heads", [16, 64])

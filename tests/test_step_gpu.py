@@ -234,6 +234,23 @@ def test_beam_deterministic_and_captured_on_a_stream():
     assert all(torch.equal(a, b) for a, b in zip(other, out))
 
 
+def test_beam_two_calls_at_once_on_two_streams():
+    g = torch.Generator(device=DEV).manual_seed(77)
+    calls, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for dtype in ("bf16", "fp32"):
+        logits, scores = likely(g, 40, 32003, dtype), -torch.rand(5, 8, generator=g, device=DEV)
+        ws = torch.empty(search.beam_workspace_size(logits, scores, num_out=16), dtype=torch.uint8, device=DEV)
+        first = [t.clone() for t in search.beam_select(logits, scores, ws, num_out=16)]
+        calls.append((logits, scores, ws, first, search.BeamChoice(*(torch.empty_like(t) for t in first))))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (logits, scores, ws, _, out), stream in zip(calls, streams):
+            search.beam_select(logits, scores, ws, num_out=16, out=out, stream=stream.cuda_stream)
+    torch.cuda.synchronize()
+    for _, _, _, first, out in calls:
+        assert all(torch.equal(a, b) for a, b in zip(first, out))
+
+
 # ------------------------------------------------------- reordering, shared prefix
 
 def beams_state(rng, groups, beams, width, page_size, pages):

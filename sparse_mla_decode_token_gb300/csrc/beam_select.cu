@@ -20,7 +20,7 @@
 // What bounds it: the first kernel reads each logit once (116 MB in 22 us, 5.3 TB/s; a
 // kernel that only reads them takes 20) with two thirds of the issue slots taken, the
 // second is a dozen dependent phases of one CTA a request.  Measured on a GB300: 64
-// requests of 8 beams over 128000 BF16 logits, 16 kept: 33.2 us (the choice 11); 8 of 32
+// requests of 8 beams over 128000 BF16 logits, 16 kept: 32.6 us (the choice 11); 8 of 32
 // beams over 151001 FP32 logits, 64 kept: 45.8 (19); one of 4 beams over 32000: 12.2 (9).
 #include <cuda_fp16.h>
 
@@ -33,7 +33,7 @@
 namespace smla {
 namespace {
 
-constexpr int kScanThreads = 256, kScanCtas = 4;  // threads of a CTA, CTAs of an SM
+constexpr int kScanThreads = 256;
 constexpr int kScanBatch = 4;                     // blocks that a warp takes at a time
 static_assert((1 << kMinUnitShift) % kScanBatch == 0, "units are whole batches");
 
@@ -41,6 +41,10 @@ static_assert((1 << kMinUnitShift) % kScanBatch == 0, "units are whole batches")
 // instructions a byte: 33.3 us with two, 34.1 with three; fp32: 53.6 and 51.5.)
 template <class T>
 constexpr int kScanStages = sizeof(T) == 4 ? 3 : 2;
+// CTAs of an SM (16-bit logits: 32.6 us with five, 33.0 with four; fp32, whose ring is
+// longer: 49.7 and 47.0).
+template <class T>
+constexpr int kScanCtas = sizeof(T) == 4 ? 4 : 5;
 template <class T>
 constexpr int kScanSmem = kScanThreads / 32 * kScanStages<T> * kScanBatch * kBeamBlockBytes;
 
@@ -180,7 +184,7 @@ struct Cursor {
 // there itself, so nothing but its own copies is waited for; the copies run
 // ahead through the ends of units.
 template <class T>
-__global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan_kernel(const BeamParams p) {
+__global__ void __launch_bounds__(kScanThreads, kScanCtas<T>) beam_scan_kernel(const BeamParams p) {
   extern __shared__ __align__(16) uint8_t ring[];
   constexpr int kLane = Vec<T>::kLane, kStage = kScanBatch * kBeamBlockBytes, kStages = kScanStages<T>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -689,7 +693,7 @@ cudaError_t launch(const BeamParams& p, int sms, cudaStream_t stream) {
   const int64_t units = (int64_t)p.batch * p.beams * p.plan.units, ctas = (units + kScanThreads / 32 - 1) / (kScanThreads / 32);
   cudaError_t e = cudaFuncSetAttribute(beam_scan_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScanSmem<T>);
   if (e != cudaSuccess) return e;
-  e = launch_overlapped(beam_scan_kernel<T>, dim3((unsigned)std::min<int64_t>(ctas, (int64_t)sms * kScanCtas)), kScanThreads,
+  e = launch_overlapped(beam_scan_kernel<T>, dim3((unsigned)std::min<int64_t>(ctas, (int64_t)sms * kScanCtas<T>)), kScanThreads,
                         kScanSmem<T>, stream, p);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(beam_pick_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Pick));

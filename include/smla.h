@@ -635,7 +635,8 @@ smla_status smla_token_slots(const smla_token_slots_args* args, void* stream);
  * and topk_lens 0.  A position past its table, an entry that is negative or a
  * row that is no 32-bit number is -1 and sets SMLA_DEVERR_INDEX_OUT_OF_RANGE
  * (as smla_decode does for rows past its pools).  `selected` may be the columns
- * from 128 on of sparse_indices itself, which then become rows in place.
+ * from 128 on of sparse_indices itself (its row stride then the table's), which
+ * become rows in place; otherwise the outputs overlap no input and not one another.
  */
 typedef struct smla_sparse_slots_args {
   int32_t sum_q, batch;             /* tokens (0 = nothing to do), requests >= 1 */

@@ -34,6 +34,31 @@ inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a != nullptr && b != nullptr && x < y + nb && y < x + na;
 }
+// `rows` pieces of `width` bytes, `stride` apart (at least `width`).
+struct Area {
+  const void* at;
+  int64_t rows, width, stride;
+};
+inline Area area(const void* at, int64_t bytes) { return {at, 1, bytes, bytes}; }
+inline Area area(const void* at, int64_t rows, int64_t width, int64_t stride) {
+  return rows > 1 && stride > width ? Area{at, rows, width, stride} : area(at, rows * width);
+}
+// Have they memory in common?  Exact, but for rows of different strides that lie
+// between one another (taken to have).
+inline bool overlap(const Area& a, const Area& b) {
+  if (a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1 ||
+      !overlap(a.at, (a.rows - 1) * a.stride + a.width, b.at, (b.rows - 1) * b.stride + b.width))
+    return false;
+  if (a.rows > 1 && b.rows > 1 && a.stride != b.stride) return true;
+  const Area& r = a.rows > 1 ? a : b;
+  const Area& x = a.rows > 1 ? b : a;
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(x.at) - reinterpret_cast<uintptr_t>(r.at));
+  const int64_t row = d >= 0 ? d / r.stride : -((r.stride - 1 - d) / r.stride), in = d - row * r.stride;
+  if (x.rows == 1 && d < 0) return true;                     // (it reaches r's first row)
+  // x's row j begins `in` bytes behind the beginning of r's row j + row
+  const auto meets = [&](int64_t by) { return by > -x.rows && by < r.rows; };
+  return (in < r.width && meets(row)) || (in + x.width > r.stride && meets(row + 1));
+}
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 inline smla_status need_words(const char* name, const void* ptr, bool required) {

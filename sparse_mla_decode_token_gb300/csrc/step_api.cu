@@ -3,6 +3,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "api_checks.h"
 #include "step.cuh"
@@ -28,6 +29,21 @@ SlotTable slot_table(const int32_t* bt, int64_t stride, int32_t max_pages, int32
   t.page_size = page_size;
   t.shift = page_size > 0 && (page_size & (page_size - 1)) == 0 ? __builtin_ctz((unsigned)page_size) : -1;
   return t;
+}
+
+// Outputs that overlap an input, which other threads still read, or one another.
+smla_status check_outputs(const char* what, std::initializer_list<Area> outputs, std::initializer_list<Area> inputs) {
+  for (const Area* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Area& in : inputs)
+      if (overlap(*o, in)) return fail(SMLA_ERR_INVALID_ARG, "%s must not overlap an input", what);
+    for (const Area* other = outputs.begin(); other != o; ++other)
+      if (overlap(*o, *other)) return fail(SMLA_ERR_INVALID_ARG, "%s must not overlap one another", what);
+  }
+  return SMLA_OK;
+}
+
+Area table_area(const SlotTable& t, int64_t rows) {
+  return area(t.bt, rows, (int64_t)t.max_pages * 4, t.stride * 4);
 }
 
 smla_status check_beam(const smla_beam_args* a) {
@@ -161,6 +177,16 @@ smla_status smla_sparse_slots(const smla_sparse_slots_args* a, void* stream) {
   p.out_stride = a->indices_row_stride ? a->indices_row_stride : columns;
   p.topk = a->topk_lens;
   p.err = a->error_word;
+  // (a selection in place: each thread reads its own columns before it writes them)
+  const bool in_place = p.selected == p.out + kSwaCols && (p.sum_q == 1 || p.selected_stride == p.out_stride);
+  const Area out = area(p.out, p.sum_q, (int64_t)columns * 4, p.out_stride * 4), topk = area(p.topk, (int64_t)p.sum_q * 4),
+             picks = area(p.selected, p.selected != nullptr ? p.sum_q : 0, (int64_t)p.num_selected * 4, p.selected_stride * 4);
+  if (!in_place && overlap(out, picks))
+    return fail(SMLA_ERR_INVALID_ARG, "selected must be the columns from %d on of sparse_indices or not overlap it", kSwaCols);
+  if (overlap(topk, picks)) return fail(SMLA_ERR_INVALID_ARG, "topk_lens must not overlap an input");
+  SMLA_TRY(check_outputs("sparse_indices and topk_lens", {out, topk},
+                         {area(p.seq_lens, (int64_t)p.batch * 4), area(p.cum, p.cum != nullptr ? ((int64_t)p.batch + 1) * 4 : 0),
+                          table_area(p.swa, p.batch), table_area(p.comp, p.num_selected > 0 ? p.batch : 0)}));
   int sms = 0;
   SMLA_TRY(current_sms(&sms));
   return launched("sparse slots", launch_sparse_slots(p, sms, static_cast<cudaStream_t>(stream)));

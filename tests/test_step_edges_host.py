@@ -1,0 +1,56 @@
+"""A step's calls beside the attention that are refused without a GPU: outputs that
+would overwrite what other threads still read."""
+import ctypes
+
+import pytest
+
+from sparse_mla_decode_token_gb300 import binding as B
+from test_step_host import INVALID, lib, refused, sparse_struct  # noqa: F401  (lib: the library, built once a module)
+
+PASSED = B.SMLA_ERR_CUDA                                             # all checks passed, and there is no GPU
+
+
+def sparse(fields):
+    """8 tokens of 4 requests, 16 columns selected; tables of 4 columns.  Addresses in bytes."""
+    a = sparse_struct()
+    for k, v in fields.items():
+        setattr(a, k, v)
+    return a
+
+
+OUT, ROW = 0x50000, 144 * 4                                          # sparse_indices and its rows
+SPARSE = [
+    # the selection elsewhere in the table: the front columns, one column on, a row on, other rows' strides
+    dict(selected=OUT, selected_stride=144), dict(selected=OUT + 129 * 4, selected_stride=144),
+    dict(selected=OUT + 127 * 4, selected_stride=144), dict(selected=OUT + ROW + 128 * 4, selected_stride=144),
+    dict(selected=OUT + 128 * 4), dict(selected=OUT + 128 * 4, selected_stride=288), dict(selected=OUT - 4),
+    dict(selected=OUT + 8 * ROW - 4), dict(selected=OUT + 128 * 4, selected_stride=144, indices_row_stride=160),
+    # the last of a wider table's gaps is not wide enough for it
+    dict(selected=OUT + 144 * 4, selected_stride=159, indices_row_stride=159),
+    dict(topk_lens=0x10000), dict(topk_lens=0x10000 - 28), dict(topk_lens=0x1000c), dict(sparse_indices=0x10000),
+    dict(cum_seq_lens_q=0x60000), dict(cum_seq_lens_q=0x60000 - 16), dict(cum_seq_lens_q=OUT + 4),
+    dict(topk_lens=0x20000), dict(topk_lens=0x2003c), dict(sparse_indices=0x20010), dict(sparse_indices=0x30000),
+    dict(swa_table_stride=100, topk_lens=0x20000 + 400), dict(topk_lens=0x3003c), dict(topk_lens=0x40000),
+    dict(topk_lens=0x40000 + 8 * 64 - 4), dict(topk_lens=OUT), dict(topk_lens=OUT + 8 * ROW - 4),
+    dict(indices_row_stride=150, topk_lens=OUT + 149 * 4),
+]
+
+
+@pytest.mark.parametrize("fields", SPARSE)
+def test_sparse_slots_that_would_overwrite_what_is_read(lib, fields):
+    refused(lib.smla_sparse_slots(ctypes.byref(sparse(fields)), None), INVALID, "overlap")
+
+
+@pytest.mark.parametrize("fields", [
+    {},
+    dict(selected=OUT + 128 * 4, selected_stride=144), dict(selected=OUT + 128 * 4, selected_stride=200, indices_row_stride=200),
+    dict(selected=OUT + 128 * 4, sum_q=1, batch=1), dict(selected=OUT + 144 * 4, selected_stride=160, indices_row_stride=160),
+    dict(selected=OUT + 8 * ROW), dict(selected=OUT - 8 * 64), dict(selected=None), dict(topk_lens=0x10010),
+    dict(topk_lens=0x10000 - 32), dict(cum_seq_lens_q=0x60020), dict(num_selected=0, comp_tables=OUT, selected=OUT),
+    dict(swa_table_stride=100, topk_lens=0x20000 + 16), dict(indices_row_stride=152, topk_lens=OUT + 144 * 4),
+])
+def test_sparse_slots_beside_one_another_pass(lib, fields):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are none of a GPU's")
+    assert lib.smla_sparse_slots(ctypes.byref(sparse(fields)), None) == PASSED, B.smla_last_error()

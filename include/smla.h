@@ -601,7 +601,8 @@ smla_status smla_pages_copy(const smla_pool* pools, int32_t num_pools, int64_t n
  * position past the table, or one whose entry is negative, has slot -1
  * (SMLA_DEVERR_INDEX_OUT_OF_RANGE).  More new tokens than max_tokens set
  * SMLA_DEVERR_TOO_MANY_TOKENS; the offsets are then still those of the whole
- * step (2^31 - 1 at most).  No output overlaps lens or new_lens.
+ * step (2^31 - 1 at most).  No output overlaps lens, new_lens, the tables that
+ * its slots are looked up in, or another output.
  */
 typedef struct smla_token_slots_args {
   const int32_t* lens;          /* [batch] tokens before the step */

@@ -111,11 +111,14 @@ smla_status smla_token_slots(const smla_token_slots_args* a, void* stream) {
   SMLA_TRY(need_words("requests", a->requests, false));
   SMLA_TRY(need_words("positions", a->positions, false));
   SMLA_TRY(need_words("error_word", a->error_word, false));
-  const size_t lens = (size_t)a->batch * 4, tokens = (size_t)a->max_tokens * 4;
-  for (const void* in : {a->lens, a->new_lens})
-    if (overlap(a->cum_seq_lens_q, lens + 4, in, lens) || overlap(a->requests, tokens, in, lens) ||
-        overlap(a->positions, tokens, in, lens))
-      return fail(SMLA_ERR_INVALID_ARG, "cum_seq_lens_q, requests and positions must not overlap lens or new_lens");
+  const int64_t lens = (int64_t)a->batch * 4, tokens = (int64_t)a->max_tokens * 4;
+  const auto given = [](const void* at, int64_t bytes) { return area(at, at != nullptr ? bytes : 0); };
+  const SlotTable tables = slot_table(a->block_tables, a->block_table_stride, a->max_pages, a->page_size);
+  SMLA_TRY(check_outputs("cum_seq_lens_q, requests, positions and slots",
+                         {area(a->cum_seq_lens_q, lens + 4), given(a->requests, tokens), given(a->positions, tokens),
+                          given(a->slots, 2 * tokens)},
+                         {given(a->lens, lens), given(a->new_lens, lens),
+                          table_area(tables, a->slots != nullptr ? a->batch : 0)}));
   TokenSlotsParams p;
   memset(&p, 0, sizeof(p));
   p.lens = a->lens;

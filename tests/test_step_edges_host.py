@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 from sparse_mla_decode_token_gb300 import binding as B
-from test_step_host import INVALID, lib, refused, sparse_struct  # noqa: F401  (lib: the library, built once a module)
+from test_step_host import INVALID, lib, refused, sparse_struct, token_struct  # noqa: F401  (lib: the library, built once a module)
 
 PASSED = B.SMLA_ERR_CUDA                                             # all checks passed, and there is no GPU
 
@@ -39,6 +39,38 @@ SPARSE = [
 @pytest.mark.parametrize("fields", SPARSE)
 def test_sparse_slots_that_would_overwrite_what_is_read(lib, fields):
     refused(lib.smla_sparse_slots(ctypes.byref(sparse(fields)), None), INVALID, "overlap")
+
+
+# 16 tokens of 4 requests, tables of 4 columns: lens 0x10000, new_lens 0x20000, tables 0x30000, outputs 0x40000 and on
+TOKENS = [
+    dict(slots=0x10000), dict(slots=0x10008), dict(slots=0x10000 - 120), dict(slots=0x20000 - 8), dict(slots=0x30038),
+    dict(cum_seq_lens_q=0x30000 - 16), dict(requests=0x3003c), dict(positions=0x30000 - 60),
+    dict(block_table_stride=10, requests=0x30000 + 160 - 28), dict(requests=0x60000), dict(positions=0x70000),
+    dict(requests=0x70000 + 124), dict(slots=0x40008), dict(cum_seq_lens_q=0x6003c),
+]
+
+
+@pytest.mark.parametrize("fields", TOKENS)
+def test_token_slots_that_would_overwrite_what_is_read(lib, fields):
+    a = token_struct()
+    for k, v in fields.items():
+        setattr(a, k, v)
+    refused(lib.smla_token_slots(ctypes.byref(a), None), INVALID, "overlap")
+
+
+@pytest.mark.parametrize("fields", [
+    {}, dict(slots=0x10010), dict(slots=0x10000 - 128), dict(cum_seq_lens_q=0x30000 - 20), dict(requests=0x30040),
+    dict(slots=None, requests=0x30000), dict(requests=None, positions=None), dict(max_tokens=0, requests=0x10000),
+    dict(batch=0, slots=0x10000),
+])
+def test_token_slots_beside_one_another_pass(lib, fields):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are none of a GPU's")
+    a = token_struct()
+    for k, v in fields.items():
+        setattr(a, k, v)
+    assert lib.smla_token_slots(ctypes.byref(a), None) == PASSED, B.smla_last_error()
 
 
 @pytest.mark.parametrize("fields", [

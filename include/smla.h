@@ -673,9 +673,9 @@ smla_status smla_sparse_slots(const smla_sparse_slots_args* args, void* stream);
  * to 2^-45 of their logit or of s_i - log sum, whichever is larger, may count as
  * equal.  Continuations of -infinity are none; places that none is left for
  * hold -infinity, -1 and -1.  out_scores may be `scores` itself where num_out is
- * beams, and does not overlap it otherwise.  A beam with a score of -infinity (an empty place)
- * has no continuation; its logits do not count, whatever they are, nor do a
- * finished beam's.
+ * beams; otherwise the outputs overlap no input and not one another.  A beam with
+ * a score of -infinity (an empty place) has no continuation; its logits do not
+ * count, whatever they are, nor do a finished beam's.
  * A NaN or +infinity among the logits or for the score leaves the beam without
  * continuations and sets SMLA_DEVERR_BAD_LOGITS.  Deterministic.
  */

@@ -208,17 +208,24 @@ smla_status smla_beam_select(const smla_beam_args* a, void* stream) {
   SMLA_TRY(check_beam(a));
   if (a->batch == 0) return SMLA_OK;
   if (a->logits == nullptr) return fail(SMLA_ERR_INVALID_ARG, "logits is required");
-  const size_t size = a->dtype == SMLA_LOGITS_FP32 ? 4 : 2;
-  if (!aligned(a->logits, size)) return fail(SMLA_ERR_INVALID_ARG, "logits must be %zu-byte aligned", size);
+  const int64_t size = a->dtype == SMLA_LOGITS_FP32 ? 4 : 2;
+  if (!aligned(a->logits, size)) return fail(SMLA_ERR_INVALID_ARG, "logits must be %d-byte aligned", (int)size);
   SMLA_TRY(need_words("scores", a->scores, true));
   SMLA_TRY(need_words("out_scores", a->out_scores, true));
   SMLA_TRY(need_words("out_parents", a->out_parents, true));
   SMLA_TRY(need_words("out_tokens", a->out_tokens, true));
   SMLA_TRY(need_words("error_word", a->error_word, false));
-  const size_t requests = a->batch;
-  if (!(a->out_scores == a->scores && a->num_out == a->beams) &&
-      overlap(a->out_scores, requests * a->num_out * 4, a->scores, requests * a->beams * 4))
+  const int64_t rows = (int64_t)a->batch * a->beams, places = (int64_t)a->batch * a->num_out * 4;
+  const Area out_scores = area(a->out_scores, places), scores = area(a->scores, rows * 4);
+  // (in place: a request's scores are read by the CTA alone that writes them)
+  if (!(a->out_scores == a->scores && a->num_out == a->beams) && overlap(out_scores, scores))
     return fail(SMLA_ERR_INVALID_ARG, "out_scores must be scores (num_out = beams) or not overlap it");
+  const Area parents = area(a->out_parents, places), tokens = area(a->out_tokens, places);
+  if (overlap(parents, scores) || overlap(tokens, scores))
+    return fail(SMLA_ERR_INVALID_ARG, "out_parents and out_tokens must not overlap scores");
+  SMLA_TRY(check_outputs("out_scores, out_parents and out_tokens", {out_scores, parents, tokens},
+                         {area(a->logits, rows, a->vocab * size, (a->logits_stride ? a->logits_stride : a->vocab) * size),
+                          area(a->finished, a->finished != nullptr ? rows : 0)}));
   int sms = 0;
   SMLA_TRY(current_sms(&sms));
   BeamParams p;

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 from sparse_mla_decode_token_gb300 import binding as B
-from test_step_host import INVALID, lib, refused, sparse_struct, token_struct  # noqa: F401  (lib: the library, built once a module)
+from test_step_host import INVALID, beam_struct, lib, refused, sparse_struct, token_struct  # noqa: F401  (lib: the library, built once a module)
 
 PASSED = B.SMLA_ERR_CUDA                                             # all checks passed, and there is no GPU
 
@@ -86,3 +86,34 @@ def test_sparse_slots_beside_one_another_pass(lib, fields):
     if torch.cuda.is_available():
         pytest.skip("the addresses are none of a GPU's")
     assert lib.smla_sparse_slots(ctypes.byref(sparse(fields)), None) == PASSED, B.smla_last_error()
+
+
+# 2 requests of 4 beams over 1000 BF16 logits: logits 0x10000 to 0x13e80, scores 0x20000, outputs of 32 bytes from 0x30000 on
+BEAMS = [
+    dict(out_parents=0x20000), dict(out_parents=0x2001c), dict(out_tokens=0x20000 - 28), dict(out_scores=0x20000, out_tokens=0x20004),
+    dict(finished=0x30000), dict(finished=0x4001f), dict(finished=0x50000 - 4), dict(out_tokens=0x10000), dict(out_parents=0x13e7c),
+    dict(out_scores=0x13000), dict(logits_stride=1002, out_tokens=0x10000 + 7 * 2004 + 1996), dict(logits_stride=1008, out_parents=0x10000 + 2008),
+    dict(out_parents=0x30000), dict(out_tokens=0x4001c), dict(out_scores=0x50000), dict(out_scores=0x20000, num_out=3),
+]
+
+
+@pytest.mark.parametrize("fields", BEAMS)
+def test_beam_outputs_that_would_overwrite_what_is_read(lib, fields):
+    a = beam_struct()
+    for k, v in fields.items():
+        setattr(a, k, v)
+    refused(lib.smla_beam_select(ctypes.byref(a), None), INVALID, "overlap")
+
+
+@pytest.mark.parametrize("fields", [
+    {}, dict(out_scores=0x20000), dict(out_parents=0x20020), dict(out_tokens=0x20000 - 32), dict(finished=0x30020),
+    dict(finished=0x50000 - 8), dict(out_parents=0x13e80), dict(logits_stride=1020, out_parents=0x10000 + 2004), dict(num_out=3),
+])
+def test_beam_outputs_beside_one_another_pass(lib, fields):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are none of a GPU's")
+    a = beam_struct()
+    for k, v in fields.items():
+        setattr(a, k, v)
+    assert lib.smla_beam_select(ctypes.byref(a), None) == PASSED, B.smla_last_error()

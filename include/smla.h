@@ -525,7 +525,7 @@ smla_status smla_cache_append(const smla_append_args* args, void* stream);
  *   group_starts[g + 1], with lens[b] > 0 hold in the same columns (the shortest
  *   one's whole pages at most; 0 for a group without such a request).  Looks at
  *   block_tables, lens and page_size only; num_pages and ref_counts are not used.
- *   prefix_lens overlaps neither lens nor group_starts.
+ *   prefix_lens overlaps none of block_tables, lens and group_starts.
  * smla_pages_compact: the n pages in use move to pages 0 .. n - 1: the k-th
  *   page in use at or past n to the k-th free page before it.  Tables and
  *   counts are renumbered and the pairs (from, to) written to the moves: copy
@@ -549,7 +549,8 @@ typedef struct smla_pages_args {
   const int32_t* lens;          /* [rows] tokens before the call */
   const int32_t* new_lens;      /* [rows] resize: tokens after it */
   const int32_t* parents;       /* [rows] fork: request to share with, or < 0; reorder: request to become, or < 0 */
-  int32_t* out_lens;            /* [rows] fork, reorder: lengths after it; overlaps neither lens nor (reorder) parents */
+  int32_t* out_lens;            /* [rows] fork, reorder: lengths after it; does not overlap lens, nor (reorder) parents,
+                                   block_tables or ref_counts */
   int32_t* move_src;            /* [move_capacity] resize, compact */
   int32_t* move_dst;            /* [move_capacity] */
   int32_t* move_count;          /* [1] */

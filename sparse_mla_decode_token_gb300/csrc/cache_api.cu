@@ -312,6 +312,11 @@ smla_status check_parents(const smla_pages_args* a) {
   return SMLA_OK;
 }
 
+Area tables_area(const smla_pages_args* a) {
+  const int64_t stride = a->block_table_stride ? a->block_table_stride : a->max_pages;
+  return area(a->block_tables, a->rows, (int64_t)a->max_pages * 4, stride * 4);
+}
+
 size_t reorder_workspace(const smla_pages_args* a) {
   return align_up((size_t)a->rows * a->max_pages * sizeof(int32_t), 256);
 }
@@ -507,6 +512,9 @@ smla_status smla_pages_reorder(const smla_pages_args* a, void* stream) {
   SMLA_TRY(check_parents(a));
   if (overlap(a->out_lens, (size_t)a->rows * sizeof(int32_t), a->parents, (size_t)a->rows * sizeof(int32_t)))
     return fail(SMLA_ERR_INVALID_ARG, "out_lens must not be parents or overlap them");
+  if (overlap(area(a->out_lens, (int64_t)a->rows * 4), tables_area(a)) ||
+      overlap(area(a->out_lens, (int64_t)a->rows * 4), area(a->ref_counts, a->num_pages * 4)))
+    return fail(SMLA_ERR_INVALID_ARG, "out_lens must not overlap block_tables or ref_counts");
   SMLA_TRY(need_workspace(a->workspace, a->workspace_bytes, reorder_workspace(a)));
   int sms = 0;
   SMLA_TRY(current_sms(&sms));
@@ -527,8 +535,9 @@ smla_status smla_pages_shared_prefix(const smla_pages_args* a, const int32_t* gr
   }
   const size_t groups = (size_t)num_groups * sizeof(int32_t);
   if (overlap(prefix_lens, groups, group_starts, groups + sizeof(int32_t)) ||
-      overlap(prefix_lens, groups, a->lens, (size_t)a->rows * sizeof(int32_t)))
-    return fail(SMLA_ERR_INVALID_ARG, "prefix_lens must not overlap lens or group_starts");
+      overlap(prefix_lens, groups, a->lens, (size_t)a->rows * sizeof(int32_t)) ||
+      overlap(area(prefix_lens, (int64_t)groups), tables_area(a)))
+    return fail(SMLA_ERR_INVALID_ARG, "prefix_lens must not overlap block_tables, lens or group_starts");
   return launched("pages shared prefix", launch_pages_shared_prefix(pages_params(a), group_starts, num_groups, prefix_lens,
                                                                     static_cast<cudaStream_t>(stream)));
 }

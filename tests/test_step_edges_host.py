@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 from sparse_mla_decode_token_gb300 import binding as B
-from test_step_host import INVALID, beam_struct, lib, refused, sparse_struct, token_struct  # noqa: F401  (lib: the library, built once a module)
+from test_step_host import INVALID, beam_struct, lib, pages_struct, refused, sparse_struct, token_struct  # noqa: F401  (lib: the library, built once a module)
 
 PASSED = B.SMLA_ERR_CUDA                                             # all checks passed, and there is no GPU
 
@@ -117,3 +117,23 @@ def test_beam_outputs_beside_one_another_pass(lib, fields):
     for k, v in fields.items():
         setattr(a, k, v)
     assert lib.smla_beam_select(ctypes.byref(a), None) == PASSED, B.smla_last_error()
+
+
+@pytest.mark.parametrize("fields", [
+    dict(out_lens=0x10000), dict(out_lens=0x1007c), dict(out_lens=0x20000 - 28), dict(out_lens=0x20000 + 396),
+    dict(block_table_stride=100, out_lens=0x10000 + 2800),
+])
+def test_reordered_lengths_over_tables_or_counts(lib, fields):
+    """8 requests of 4 columns: tables 0x10000, 100 counts 0x20000."""
+    a = pages_struct()
+    for k, v in fields.items():
+        setattr(a, k, v)
+    refused(lib.smla_pages_reorder(ctypes.byref(a), None), INVALID, "out_lens")
+
+
+def test_shared_prefixes_over_the_tables(lib):
+    a = pages_struct()
+    for at in (0x10000, 0x1007c, 0x10000 - 4):
+        refused(lib.smla_pages_shared_prefix(ctypes.byref(a), 0x1000, 2, at, None), INVALID, "overlap")
+    a.block_table_stride = 100
+    refused(lib.smla_pages_shared_prefix(ctypes.byref(a), 0x1000, 2, 0x10000 + 396, None), INVALID, "overlap")

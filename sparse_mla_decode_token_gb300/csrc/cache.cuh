@@ -148,9 +148,8 @@ struct PrefixPlan {
 // Unit `unit`, of `segment`, as far as it is share `share`'s; later: not the share's
 // first one.  (The arrays are given apart, as the plan's kernel has them in shared memory.)
 __device__ __forceinline__ Unit plan_unit(const CacheView& c, const PrefixPlan& plan, int H, int shift, int share,
-                                          int64_t share_cost, int unit, int segment, bool later, int32_t* err,
-                                          const int64_t* cost_of, const int* unit_of, const int* shared_of, const int4* group,
-                                          const int4* token) {
+                                          int64_t share_cost, int unit, int segment, bool later, const int64_t* cost_of,
+                                          const int* unit_of, const int* shared_of, const int4* group, const int4* token) {
   const int block = unit - fetch(unit_of + segment), shared = fetch(shared_of + segment);
   int64_t at = fetch(cost_of + segment);
   Unit u;
@@ -178,7 +177,6 @@ __device__ __forceinline__ Unit plan_unit(const CacheView& c, const PrefixPlan& 
     u.lo = r.w;
   }
   const int last = min(u.pos, c.max_pages * c.page_size - 1);
-  if (u.pos > last && err != nullptr) atomicOr(err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);
   u.first_chunks = (u.first + (1 << shift) - 1) >> shift;
   u.window_chunk = u.lo >> shift;
   u.chunks = u.first_chunks + (last >= u.lo ? (last >> shift) - u.window_chunk + 1 : 0);

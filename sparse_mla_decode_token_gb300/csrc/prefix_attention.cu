@@ -248,6 +248,7 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
       const int4 v = token[s - plan.groups];
       if (near_segments) plan.token[s - plan.groups] = v;
       if (v.x >= 0) {
+        if (v.z >= cap) flag(p.err, SMLA_DEVERR_INDEX_OUT_OF_RANGE);   // (here, as such a token may have no unit)
         shared = v.y < 0;
         tiles = tiles_of(shared ? 0 : v.w, v.w, v.z, cap, shift);
         units = shared && tiles == 0 ? 0 : heads;
@@ -311,8 +312,8 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const WindowParam
       int4 words[4];
       Unit unit;
     } first;
-    first.unit = plan_unit(c, plan, p.H, shift, i, share, s_first[i], s_segment[i], false, p.err, cost_of, unit_of, shared_of,
-                           group, token);
+    first.unit = plan_unit(c, plan, p.H, shift, i, share, s_first[i], s_segment[i], false, cost_of, unit_of, shared_of, group,
+                           token);
 #pragma unroll
     for (int k = 0; k < 4; ++k) plan.first[i * 4 + k] = first.words[k];
   }

@@ -191,8 +191,8 @@ __device__ __forceinline__ Unit planned_unit(const KernelParams& kp, int x, int 
   const int unit = mine.x + x;
   const int segment = mine.z + last_request(plan.groups + c.sum_q - mine.z, lane,
                                             [&](int s) { return __ldcg(plan.unit_of + mine.z + s) <= unit; });
-  return plan_unit(c, plan, kp.p.H, kShift, blockIdx.x, __ldcg(plan.share_cost), unit, segment, x > 0, lane == 0 ? kp.p.err : nullptr,
-                   plan.cost_of, plan.unit_of, plan.shared_of, plan.group, plan.token);
+  return plan_unit(c, plan, kp.p.H, kShift, blockIdx.x, __ldcg(plan.share_cost), unit, segment, x > 0, plan.cost_of,
+                   plan.unit_of, plan.shared_of, plan.group, plan.token);
 }
 
 // Do the groups' starts fall, or lie outside the batch?  (Whole warp.)

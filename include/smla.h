@@ -366,7 +366,7 @@ typedef struct smla_cache {
   int64_t block_table_stride;     /* row stride in elements [max_pages] */
   int32_t max_pages;              /* page-table columns >= 1; max_pages * page_size < 2^31 */
   int32_t batch;                  /* requests B >= 1 */
-  const int32_t* seq_lens;        /* [B] tokens of each request, this call's new tokens included */
+  const int32_t* seq_lens;        /* [B] tokens of each request, this call's new tokens included; less than 0 is none */
   const int32_t* cum_seq_lens_q;  /* [B+1] offsets of each request's new tokens, or NULL = uniform sum_q / B; tokens before the
                                      first offset and from the last one on (a padded batch) are no request's: the
                                      calls write nothing for them */

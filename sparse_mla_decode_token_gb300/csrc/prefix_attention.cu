@@ -75,7 +75,7 @@ struct Request {
 __device__ __forceinline__ Request request_of(const CacheView& c, int b) {
   Request r;
   request_tokens(c, b, &r.first, &r.count);
-  r.len = fetch(c.seq_lens + b);
+  r.len = max(fetch(c.seq_lens + b), 0);          // (negative: none; what is subtracted from it stays an int)
   r.t0 = min(max(r.first, 0), c.sum_q);
   r.t1 = r.count > 0 ? min(max(r.first + r.count, r.t0), c.sum_q) : r.t0;
   return r;

@@ -218,7 +218,7 @@ __device__ __forceinline__ int group_prefix(const KernelParams& kp, int b, int l
   for (int x = lo + lane; x < hi; x += 32) {
     int at, count;
     request_tokens(c, x, &at, &count);
-    const int len = fetch(c.seq_lens + x);
+    const int len = max(fetch(c.seq_lens + x), 0);
     if (count > 0 && at < c.sum_q && (int64_t)at + count > 0) {
       first = min(first, x);
       limit = min(limit, max(0, len - count + 1));
@@ -245,7 +245,7 @@ __device__ __forceinline__ Unit make_unit(const KernelParams& kp, int x, int lan
   request_tokens(c, u.b, &first, &count);
   const bool owned = u.t >= first && u.t - first < count;   // else a token of no request: its outputs are left alone
   if (!owned) u.heads = 0;
-  u.pos = owned ? fetch(c.seq_lens + u.b) - count + (u.t - first) : -1;
+  u.pos = owned ? max(fetch(c.seq_lens + u.b), 0) - count + (u.t - first) : -1;   // (negative lengths: none)
   u.lo = (int)max((int64_t)u.pos - p.window + 1, (int64_t)0);
   u.first_chunks = u.window_chunk = u.chunks = 0;
   const int cap = c.max_pages * c.page_size, last = min(u.pos, cap - 1);

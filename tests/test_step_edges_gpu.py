@@ -51,3 +51,20 @@ def test_tokens_past_a_table_that_their_prefix_fills(members, past):
     close(*both(cache, starts, [4096], q, 0))
     cache.lens[members - 2] += past
     close(*both(cache, starts, [4096], q, B.DEVERR_INDEX_OUT_OF_RANGE))
+
+
+@pytest.mark.parametrize("members,heads", [(40, 16), (5, 16), (5, 64)])
+@pytest.mark.parametrize("least", [-2 ** 31, -2 ** 31 + 1, -1])
+def test_lengths_under_zero_are_none(members, heads, least):
+    """Requests of a negative length, one of a group and one of none: their tokens see nothing, and as the group's tokens
+    share what all of them see, it shares nothing.  (Prefixes of whole pages, which the members hold alike.)"""
+    own, q_lens = [3 + b for b in range(members)], [1 + b % 3 for b in range(members)]
+    cache, starts, q, _ = make(heads, [members, 2], [4032, 128], own + [4, 2], q_lens + [2, 1, 2], heads=heads, shared=True,
+                               outside=[200])
+    cache.lens[2] = cache.lens[members + 2] = least
+    results = both(cache, starts, [4032, 128], q, 0)
+    close(*results)
+    for out, lse in results:
+        for b in (2, members + 2):
+            t = slice(cache.cum[b], cache.cum[b + 1])
+            assert np.all(out[t] == 0) and np.all(np.isneginf(lse[t]))

@@ -10,7 +10,10 @@
 
 #include <vector>
 
+#include <ATen/Context.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -143,6 +146,17 @@ smla_status unlocked(F f) {
   return s;
 }
 
+// A new output.  at::empty without its dispatch (1 us a tensor), but where that does
+// more than allocate: it fills new memory where deterministic algorithms are asked
+// for (calls leave the outputs of tokens of no request alone), and modes see it.
+at::Tensor new_output(at::IntArrayRef sizes, c10::ScalarType type, c10::Device device) {
+  const at::Context& context = at::globalContext();
+  if ((context.deterministicAlgorithms() && context.deterministicFillUninitializedMemory()) ||
+      c10::impl::TorchDispatchModeTLS::any_modes_set())
+    return at::empty(sizes, at::TensorOptions().dtype(type).device(device));
+  return at::detail::empty_cuda(sizes, type, device, std::nullopt);
+}
+
 // What the two attention calls have alike: (q, rows, scales, block_tables, seq_lens, workspace, cum_seq_lens_q, sinks,
 // then what the caller sets, then from a[at] on bmm1_scale, bmm2_scale, out, out_lse, error_word, stream) ->
 // (out, out_lse), a status that is not 0, or None
@@ -172,14 +186,14 @@ PyObject* attention(PyObject* const* a, int at, Set set, Run run) {
   need((a[2] != Py_None && a[3] != Py_None) || stream == call.stream(Py_None));
   at::Tensor out, lse;                      // those that are not given
   if (a[2] == Py_None) {
-    out = at::detail::empty_cuda({T, H, kDim}, c10::kBFloat16, q.device(), std::nullopt);   // (at::empty without its dispatch)
+    out = new_output({T, H, kDim}, c10::kBFloat16, q.device());
     w.out = out.data_ptr();
   } else {
     w.out = call.array(a[2], c10::kBFloat16, T * H * kDim, false);
     need(THPVariable_Unpack(a[2]).numel() == T * H * kDim);
   }
   if (a[3] == Py_None) {
-    lse = at::detail::empty_cuda({T, H}, c10::kFloat, q.device(), std::nullopt);
+    lse = new_output({T, H}, c10::kFloat, q.device());
     w.out_lse = static_cast<float*>(lse.data_ptr());
   } else {
     w.out_lse = static_cast<float*>(call.array(a[3], c10::kFloat, T * H, false));
@@ -384,7 +398,7 @@ struct Output {
       data = call.array(o, type, entries, false);
       given = o;
     } else {
-      fresh = at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
+      fresh = new_output(sizes, type, like.device());
       data = fresh.data_ptr();
     }
   }

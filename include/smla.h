@@ -413,7 +413,9 @@ typedef struct smla_window_args {
   int32_t* error_word;              /* optional device int32; kernels OR SMLA_DEVERR_* bits into it */
 } smla_window_args;
 
-/* Workspace bytes smla_window_attention will need for these shapes on `device` (pointers are not looked at). */
+/* Workspace bytes that smla_window_attention needs for these shapes on `device` (pointers are not looked at), and for
+ * fewer tokens, shorter windows or narrower tables of the same heads, pages and num_splits: sized for a server's
+ * largest step, one workspace serves them all.  A call itself may need less. */
 smla_status smla_window_workspace_size(const smla_window_args* args, int device, size_t* bytes);
 
 smla_status smla_window_attention(const smla_window_args* args, void* stream);
@@ -457,7 +459,8 @@ typedef struct smla_prefix_args {
   int32_t* error_word;              /* optional device int32; kernels OR SMLA_DEVERR_* bits into it */
 } smla_prefix_args;
 
-/* Workspace bytes smla_prefix_attention will need for these shapes on `device` (pointers are not looked at). */
+/* Workspace bytes that smla_prefix_attention needs for these shapes on `device` (pointers are not looked at), and for
+ * fewer tokens, groups or table columns of the same heads and pages.  A call itself may need less. */
 smla_status smla_prefix_workspace_size(const smla_prefix_args* args, int device, size_t* bytes);
 
 smla_status smla_prefix_attention(const smla_prefix_args* args, void* stream);

@@ -150,8 +150,11 @@ struct WindowPlan {
 // the merge: 1.3 tiles' time and a 7000th of one for each partial row of 512 values
 // (1 token x 64 heads, 2 tiles: 12.3 us whole, 12.9 in two; 3 tiles: 15.8 against
 // 13.5 in three; 32 x 128, 5 tiles: 22.5 against 24.2 in two, 9: 33.2 against 30.0).
+int64_t most_splits(int64_t pairs, int64_t tiles, int sms) {
+  return std::min<int64_t>({sms / pairs, tiles, kMaxWindowSplits});
+}
 int cheapest_splits(int64_t pairs, int64_t tiles, int sms) {
-  const int64_t most = std::min<int64_t>({sms / pairs, tiles, kMaxWindowSplits});
+  const int64_t most = most_splits(pairs, tiles, sms);
   int best = 1;
   double cost = (double)tiles;
   for (int64_t s = 2; s <= most; ++s) {
@@ -162,6 +165,11 @@ int cheapest_splits(int64_t pairs, int64_t tiles, int sms) {
     }
   }
   return best;
+}
+
+// fp32 values, `each` for every row of so many partials.
+size_t parts_bytes(int64_t parts, int each) {
+  return align_up((size_t)parts * kWindowHeads * each * sizeof(float), 256);
 }
 
 // Pairs of up to `tiles` tiles, in `splits` if that is not 0.
@@ -179,10 +187,22 @@ WindowPlan pair_plan(int64_t pairs, int64_t tiles, int splits, int sms) {
     w.whole = w.splits > 1 ? pairs - rest : pairs;
   }
   w.units = w.whole + (pairs - w.whole) * w.splits;
-  const size_t rows = (size_t)(pairs - w.whole) * w.splits * kWindowHeads;
-  w.lse = align_up(rows * kHeadDim * sizeof(float), 256);
-  w.bytes = w.lse + align_up(rows * sizeof(float), 256);
+  const int64_t parts = (pairs - w.whole) * w.splits;
+  w.lse = parts_bytes(parts, kHeadDim);
+  w.bytes = w.lse + parts_bytes(parts, 1);
   return w;
+}
+
+// Workspace of every such plan of at most so many pairs and tiles: one that is sized
+// for a server's largest step serves the smaller ones, which may be split more.
+size_t pair_workspace(int64_t pairs, int64_t tiles, int splits, int sms) {
+  if (splits > 0) return pair_plan(pairs, tiles, splits, sms).bytes;
+  int64_t parts = 0;
+  for (int64_t rest = 1; rest <= std::min<int64_t>(pairs, sms - 1); ++rest) {
+    const int64_t most = most_splits(rest, tiles, sms);
+    if (most > 1) parts = std::max(parts, rest * most);
+  }
+  return parts_bytes(parts, kHeadDim) + parts_bytes(parts, 1);
 }
 
 // Rows of a page's boxes that a request may hold, and the tiles of `rows` of them.
@@ -190,11 +210,17 @@ int64_t box_rows(const smla_cache& c) { return 1ll << cache_box_shift(c.page_siz
 int64_t table_chunks(const smla_cache& c) { return ((int64_t)c.max_pages * c.page_size + box_rows(c) - 1) / box_rows(c); }
 int64_t chunk_tiles(const smla_cache& c, int64_t chunks) { return (chunks * box_rows(c) + kWindowTile - 1) / kWindowTile; }
 
-WindowPlan window_plan(const smla_window_args* a, int sms) {
+template <class Args>
+int64_t pairs_of(const Args* a) { return (int64_t)a->sum_q * head_groups(a); }
+
+int64_t window_tiles(const smla_window_args* a) {
   const int64_t chunk = box_rows(a->cache);
   const int64_t seen = ((int64_t)a->window + chunk - 2) / chunk + 1 + ((int64_t)a->first_tokens + chunk - 1) / chunk;
-  return pair_plan((int64_t)a->sum_q * head_groups(a), chunk_tiles(a->cache, std::min(table_chunks(a->cache), seen)),
-                   a->num_splits, sms);
+  return chunk_tiles(a->cache, std::min(table_chunks(a->cache), seen));
+}
+
+WindowPlan window_plan(const smla_window_args* a, int sms) {
+  return pair_plan(pairs_of(a), window_tiles(a), a->num_splits, sms);
 }
 
 void set_parts(WindowParams* p, const WindowPlan& plan, void* workspace) {
@@ -228,9 +254,8 @@ bool shares_prefixes(const smla_prefix_args* a, int sms) {
 }
 
 // Else each token by itself: a list has a chunk more, where the prefix ends within one.
-WindowPlan grouped_plan(const smla_prefix_args* a, int sms) {
-  return pair_plan((int64_t)a->sum_q * head_groups(a), chunk_tiles(a->cache, table_chunks(a->cache) + 1), 0, sms);
-}
+int64_t grouped_tiles(const smla_prefix_args* a) { return chunk_tiles(a->cache, table_chunks(a->cache) + 1); }
+WindowPlan grouped_plan(const smla_prefix_args* a, int sms) { return pair_plan(pairs_of(a), grouped_tiles(a), 0, sms); }
 
 // The workspace's parts: fp32 partials (two for each SM; where prefixes are shared, one
 // more for each block of 64 rows and each cut through them), then the plan.
@@ -375,7 +400,7 @@ smla_status smla_window_workspace_size(const smla_window_args* args, int device,
   SMLA_TRY(check_window(args));
   int sms = 0;
   SMLA_TRY(device_sms(device, &sms));
-  *bytes = window_plan(args, sms).bytes;
+  *bytes = pair_workspace(pairs_of(args), window_tiles(args), args->num_splits, sms);
   return SMLA_OK;
 }
 
@@ -386,7 +411,7 @@ smla_status smla_window_attention(const smla_window_args* a, void* stream) {
   int sms = 0;
   SMLA_TRY(current_sms(&sms));
   const WindowPlan plan = window_plan(a, sms);
-  if (plan.units > 0x7fffffff || (int64_t)a->sum_q * head_groups(a) > 0x7fffffff / kWindowHeads)
+  if (plan.units > 0x7fffffff || pairs_of(a) > 0x7fffffff / kWindowHeads)
     return fail(SMLA_ERR_UNSUPPORTED, "%lld units are too many", (long long)plan.units);
   SMLA_TRY(need_workspace(a->workspace, a->workspace_bytes, plan.bytes));
   WindowParams p = attention_params(a);
@@ -401,7 +426,9 @@ smla_status smla_prefix_workspace_size(const smla_prefix_args* args, int device,
   SMLA_TRY(check_prefix(args));
   int sms = 0;
   SMLA_TRY(device_sms(device, &sms));
-  *bytes = args->sum_q == 0 ? 0 : shares_prefixes(args, sms) ? prefix_layout(args, sms).bytes : grouped_plan(args, sms).bytes;
+  // (smaller calls may take each token by itself; where this one does, all of them do)
+  *bytes = pair_workspace(pairs_of(args), grouped_tiles(args), 0, sms);
+  if (shares_prefixes(args, sms)) *bytes = std::max(*bytes, prefix_layout(args, sms).bytes);
   return SMLA_OK;
 }
 
@@ -421,7 +448,7 @@ smla_status smla_prefix_attention(const smla_prefix_args* a, void* stream) {
   plan.prefix_lens = a->prefix_lens;
   if (!shares_prefixes(a, sms)) {
     const WindowPlan w = grouped_plan(a, sms);
-    if (w.units > 0x7fffffff || (int64_t)a->sum_q * head_groups(a) > 0x7fffffff / kWindowHeads)
+    if (w.units > 0x7fffffff || pairs_of(a) > 0x7fffffff / kWindowHeads)
       return fail(SMLA_ERR_UNSUPPORTED, "%lld units are too many", (long long)w.units);
     SMLA_TRY(need_workspace(a->workspace, a->workspace_bytes, w.bytes));
     set_parts(&p, w, a->workspace);

@@ -708,7 +708,8 @@ typedef struct smla_beam_args {
   int32_t* error_word;
 } smla_beam_args;
 
-/* Workspace bytes of smla_beam_select for these shapes and dtype on `device` (pointers are not looked at). */
+/* Workspace bytes that smla_beam_select needs for these shapes and dtype on `device` (pointers are not looked at), and
+ * for fewer requests or beams or a smaller vocabulary.  A call itself may need less. */
 smla_status smla_beam_workspace_size(const smla_beam_args* args, int device, size_t* bytes);
 smla_status smla_beam_select(const smla_beam_args* args, void* stream);
 

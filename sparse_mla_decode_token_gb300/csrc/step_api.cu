@@ -63,6 +63,8 @@ smla_status check_beam(const smla_beam_args* a) {
   return SMLA_OK;
 }
 
+int32_t units_of(int32_t blocks, int shift) { return (blocks + (1 << shift) - 1) >> shift; }
+
 // Units of up to 16 blocks, shorter ones where there would not be 32 of them for
 // each SM (as many as it holds warps).
 BeamPlan beam_plan(const smla_beam_args* a, int sms) {
@@ -72,7 +74,7 @@ BeamPlan beam_plan(const smla_beam_args* a, int sms) {
   const int64_t all = (int64_t)plan.blocks * a->batch * a->beams;
   plan.unit_shift = kMaxUnitShift;
   while (plan.unit_shift > kMinUnitShift && all >> plan.unit_shift < (int64_t)sms * 32) --plan.unit_shift;
-  plan.units = (plan.blocks + (1 << plan.unit_shift) - 1) >> plan.unit_shift;
+  plan.units = units_of(plan.blocks, plan.unit_shift);
   return plan;
 }
 
@@ -200,7 +202,10 @@ smla_status smla_beam_workspace_size(const smla_beam_args* args, int device, siz
   SMLA_TRY(check_beam(args));
   int sms = 0;
   SMLA_TRY(device_sms(device, &sms));
-  *bytes = args->batch == 0 ? 0 : beam_layout(args, beam_plan(args, sms)).bytes;
+  // (smaller calls may have shorter units, so more of them a row: a size that serves those, too)
+  BeamPlan plan = beam_plan(args, sms);
+  plan.units = units_of(plan.blocks, kMinUnitShift);
+  *bytes = beam_layout(args, plan).bytes;
   return SMLA_OK;
 }
 

@@ -121,3 +121,13 @@ def test_attention_workspaces_cover_calls_that_are_smaller_in_all(sizes):
             calls = [big] + [tuple(rng.randint(min(1, v), v) for v in big) for _ in range(40)]
             got = sizes([(kind, t, heads, pages, page_size, groups, window, 0) for t, pages, groups, window in calls])
             assert got[0][0] >= max(need for _, need in got), (kind, heads, page_size, big)
+
+
+@pytest.mark.parametrize("dtype", [0, 2])
+def test_beam_workspaces_cover_smaller_calls(sizes, dtype):
+    for beams, vocab in ((8, 128000), (1, 32000), (64, 151001), (4, 500)):
+        covers(sizes, at(1), ("beam", 1, beams, vocab, dtype), range(1, 130))
+    for batch, vocab in ((1, 128000), (20, 50000), (64, 128000)):
+        covers(sizes, at(2), ("beam", batch, 1, vocab, dtype), range(1, 65))
+    for batch, beams in ((1, 1), (19, 8), (64, 8)):
+        covers(sizes, at(3), ("beam", batch, beams, 1, dtype), [*range(1, 5000, 97), *range(5000, 200000, 2311)])

@@ -1,5 +1,6 @@
 """Edges of a step's calls on the GPU: positions past the tables behind shared prefixes, lengths that are none,
 workspaces bracketed by memory that no call may write."""
+import re
 
 import numpy as np
 import pytest
@@ -9,10 +10,11 @@ from torch.utils._python_dispatch import TorchDispatchMode
 from sparse_mla_decode_token_gb300 import binding as B
 from sparse_mla_decode_token_gb300 import cache as C
 from sparse_mla_decode_token_gb300 import search, slots
-from test_prefix_gpu import SCALE, built, i32, make, on_gpu, queries  # noqa: F401  (built: the library, once a module)
+from test_prefix_gpu import SCALE, built, i32, make, on_gpu, queries, widened  # noqa: F401  (built: the library, once a module)
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+GUARD = 1 << 16
 
 
 def both(cache, starts, prefix, q, flag):
@@ -120,3 +122,101 @@ def test_dispatch_modes_see_new_outputs():
             call()
         assert seen.empty == outputs, name
     torch.cuda.synchronize()
+
+
+def bracketed(call, size):
+    """A workspace of junk, of exactly the bytes that `call` needs (at most `size`, which may cover other calls), and the
+    bytes before and behind it that no call may write."""
+    try:
+        call(None)
+        need = 0
+    except B.SmlaError as e:
+        need = int(re.search(r"0 bytes given, (\d+) needed", str(e)).group(1))
+    assert need <= size
+    memory = torch.full((need + 2 * GUARD,), 0xFF, dtype=torch.uint8, device=DEV)
+    memory[:GUARD] = memory[GUARD + need:] = 99
+    return memory[GUARD:GUARD + need], (memory[:GUARD], memory[GUARD + need:])
+
+
+def untouched(guards):
+    return all(bool((g == 99).all()) for g in guards)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("cum", [None, [0, 3, 1, 4], [2, 0, 9, 4], [0, 4, 4, -3], [-5, 1, 2, 9]])
+@pytest.mark.parametrize("heads", [16, 100])
+def test_prefix_attention_stays_in_its_workspace(cum, wide, heads):
+    """Offsets in order and offsets that fall or lie outside the batch."""
+    cache, starts, q, _ = make(18, [3], [70], [2, 3, 4], [1, 2, 1], heads=heads, shared=True)
+    if wide:
+        cache.tables = widened(cache.tables, 4, heads)
+    qt, g, s = queries(q)[0], on_gpu(cache), i32(starts)
+    c = i32(cache.cum if cum is None else cum)
+    call = lambda ws: C.prefix_attention(qt, *g, ws, group_starts=s, prefix_lens=i32([70]), cum_seq_lens_q=c, bmm1_scale=SCALE)
+    ws, guards = bracketed(call, C.prefix_workspace_size(qt, *g, group_starts=s, cum_seq_lens_q=c))
+    call(ws)
+    torch.cuda.synchronize()
+    assert untouched(guards)
+
+
+@pytest.mark.parametrize("members,prefix,heads", [([9, 2], [3000, 40], 16), ([40], [1000], 33), ([1], [9000], 64), ([3, 3], [130, 4000], 128)])
+def test_long_prefixes_stay_in_their_workspace(members, prefix, heads):
+    n = sum(members)
+    cache, starts, q, _ = make(21, members, prefix, [1 + 37 * b % 300 for b in range(n)], [1] * n, heads=heads, shared=True)
+    for tables in (cache.tables, widened(cache.tables, n, heads)):
+        cache.tables = tables
+        qt, g, s = queries(q)[0], on_gpu(cache), i32(starts)
+        call = lambda ws: C.prefix_attention(qt, *g, ws, group_starts=s, prefix_lens=i32(prefix), bmm1_scale=SCALE)
+        ws, guards = bracketed(call, C.prefix_workspace_size(qt, *g, group_starts=s))
+        call(ws)
+        torch.cuda.synchronize()
+        assert untouched(guards)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("batch,beams,vocab,keep", [(1, 1, 1, 1), (3, 2, 255, 5), (2, 64, 777, 64), (1, 7, 50021, 33), (40, 3, 2000, 3)])
+def test_beam_selection_stays_in_its_workspace(batch, beams, vocab, keep, dtype):
+    logits, scores = torch.randn(batch * beams, vocab, device=DEV).to(dtype), torch.zeros(batch, beams, device=DEV)
+    call = lambda ws: search.beam_select(logits, scores, ws, num_out=keep)
+    ws, guards = bracketed(call, search.beam_workspace_size(logits, scores, num_out=keep))
+    call(ws)
+    torch.cuda.synchronize()
+    assert untouched(guards)
+
+
+@pytest.mark.parametrize("rows,width", [(1, 1), (7, 33), (64, 130), (300, 600)])
+def test_reordering_stays_in_its_workspace(rows, width):
+    rng = np.random.default_rng(rows)
+    tables = i32(rng.permutation(rows * width).reshape(rows, width))
+    counts, lens, out = i32(np.ones(rows * width)), i32(rng.integers(0, width * 8 + 1, rows)), i32(np.zeros(rows))
+    parents, nothing = i32(rng.integers(-1, rows, rows)), torch.empty(0, dtype=torch.uint8, device=DEV)
+    call = lambda ws: C.pages_reorder(tables, counts, lens, parents, out, nothing if ws is None else ws, page_size=8)
+    ws, guards = bracketed(call, C.reorder_workspace_size(tables))
+    call(ws)
+    torch.cuda.synchronize()
+    assert untouched(guards)
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+def test_one_workspace_for_steps_of_fewer_tokens(heads):
+    """Sized for the largest step; the smaller ones, which are split more, give what they give in one of their own."""
+    cache, starts, q, _ = make(6, [40], [2000], [1 + b for b in range(40)], [1] * 40, heads=heads, shared=True)
+    g, qt, s, p = on_gpu(cache), queries(q)[0], i32([0, 40]), i32([2000])
+    large = torch.empty(C.prefix_workspace_size(qt, *g, group_starts=s), dtype=torch.uint8, device=DEV)
+    window = torch.empty(C.window_workspace_size(qt, *g, window=1 << 20), dtype=torch.uint8, device=DEV)
+    for n in (40, 39, 20, 3, 1):
+        part = (g[0], g[1], g[2][:n], g[3][:n])
+        for shared in (True, False):
+            kw = dict(group_starts=i32([0, n]), prefix_lens=p) if shared else dict(window=1 << 20)
+            call = C.prefix_attention if shared else C.window_attention
+            want = call(qt[:n], *part, torch.empty(1 << 26, dtype=torch.uint8, device=DEV), bmm1_scale=SCALE, **kw)
+            got = call(qt[:n], *part, large if shared else window, bmm1_scale=SCALE, **kw)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), (n, shared)
+    logits, scores = torch.randn(160, 128000, device=DEV).to(torch.bfloat16), torch.zeros(20, 8, device=DEV)
+    ws = torch.empty(search.beam_workspace_size(logits, scores), dtype=torch.uint8, device=DEV)
+    for n in (20, 19, 1):
+        want = search.beam_select(logits[:8 * n], scores[:n], torch.empty(1 << 24, dtype=torch.uint8, device=DEV))
+        got = search.beam_select(logits[:8 * n], scores[:n], ws)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), n

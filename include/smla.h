@@ -673,9 +673,12 @@ smla_status smla_sparse_slots(const smla_sparse_slots_args* args, void* stream);
  *
  * and a finished beam has one continuation, end_token, with its own score.  The
  * num_out best, in order, go to out_scores, out_parents (the row r * beams + i)
- * and out_tokens; among equal ones the lower (i, v) is first.  Scores that agree
- * to 2^-45 of their logit or of s_i - log sum, whichever is larger, may count as
- * equal.  Continuations of -infinity are none; places that none is left for
+ * and out_tokens; among equal ones the lower (i, v) is first.  A beam's own
+ * continuations stand in the order of its logits, but that scores which agree to
+ * 2^-45 of their logit or of s_i - log sum, whichever is larger, may count as
+ * equal.  A beam's log sum is off by less than 2^-17, the same for all of its
+ * continuations: those of different beams whose scores are closer than 2^-16 may
+ * stand in either order.  Continuations of -infinity are none; places that none is left for
  * hold -infinity, -1 and -1.  out_scores may be `scores` itself where num_out is
  * beams; otherwise the outputs overlap no input and not one another.  A beam with
  * a score of -infinity (an empty place) has no continuation; its logits do not

@@ -12,10 +12,14 @@
 // the best K of those: some thousand keys in place of a million logits.
 //
 // Ranks are over (score, index) with the score as an unevaluated sum of two fp32
-// numbers (48 bits), to which x adds without an error.  Sums are fp32 over at most 64
-// terms a lane, then such pairs over the units; e^x is off by 2^-22 of itself.  (In
-// fp64, which has a fiftieth of fp32's rate, the second kernel takes 15 us for the
-// 32 beams of a request alone.)
+// numbers (48 bits), to which x adds without an error: one beam's continuations rank
+// like its logits.  Between beams ranks carry the error of their log sums, under 2^-17:
+// five values of e^x, each off by 2^-22 of itself, and four products on a term's way to
+// the sum, 24 additions (fp32 over at most 64 terms a lane, a warp's lanes, then such
+// pairs over the units) and one logarithm are 49 times 2^-24; arguments of e^x, rounded
+// three times, add 2.25 times 2^-24 of their mean size, at most log V by the weights
+// that they have.  (In fp64, which has a fiftieth of fp32's rate, the second kernel takes
+// 15 us for the 32 beams of a request alone.)
 //
 // What bounds it: the first kernel reads each logit once (116 MB in 22 us, 5.3 TB/s; a
 // kernel that only reads them takes 20) with two thirds of the issue slots taken, the
@@ -303,7 +307,8 @@ __device__ __forceinline__ float unordered(uint32_t b) {
 struct Beam {
   float hi, lo, top;
 };
-// The score's rank: the sum of four numbers as two, the first one rounded.
+// The score's rank: the sum of four numbers as two, the first one rounded.  (Each
+// difference's rounding is found by Knuth's two-sum, as in add_exact.)
 __device__ __noinline__ Rank score_rank(Beam c, float x, uint32_t index) {
   if (!(x > -INFINITY) || isnan(c.hi)) return {0, 0, index};
   const float d = __fsub_rn(x, c.top), dx = __fadd_rn(d, c.top);
@@ -316,7 +321,7 @@ __device__ __noinline__ Rank score_rank(Beam c, float x, uint32_t index) {
   return {ordered(hi), ordered(lo), index};
 }
 
-// hi + lo += x, the rounding of hi kept in lo.
+// hi + lo += x, the rounding of hi kept in lo (two-sum).
 __device__ __forceinline__ void add_exact(float& hi, float& lo, float x) {
   const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
   lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b));

@@ -1,5 +1,5 @@
-"""Edges of a step's calls on the GPU: positions past the tables behind shared prefixes, lengths that are none,
-workspaces bracketed by memory that no call may write."""
+"""Edges of a step's calls on the GPU: positions past the tables behind shared prefixes, lengths that are none, log sums,
+new outputs, workspaces bracketed by memory that no call may write."""
 import re
 
 import numpy as np
@@ -220,3 +220,30 @@ def test_one_workspace_for_steps_of_fewer_tokens(heads):
         got = search.beam_select(logits[:8 * n], scores[:n], ws)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), n
+
+
+@pytest.mark.parametrize("dtype,spread", [(torch.bfloat16, 2.0), (torch.float32, 0.0), (torch.float32, 6.0), (torch.float16, 0.5)])
+def test_log_sums_of_beams_within_their_bound(dtype, spread):
+    """Scores are off by less than 2^-17 and their own rounding, and continuations of different beams are out of order by
+    less than 2^-16 at most; one beam's stand in the order of its logits."""
+    gen = torch.Generator(device=DEV).manual_seed(41)
+    batch, beams, vocab, keep = 6, 16, 150001, 64
+    logits = (torch.randn(batch * beams, vocab, generator=gen, device=DEV) * spread + 3).to(dtype)
+    scores = -torch.rand(batch, beams, generator=gen, device=DEV) * 2.0 ** -14          # beams that are hardly apart
+    ws = torch.empty(search.beam_workspace_size(logits, scores, num_out=keep), dtype=torch.uint8, device=DEV)
+    best = search.beam_select(logits, scores, ws, num_out=keep)
+    torch.cuda.synchronize()
+    x = logits.double()
+    total = (x - torch.logsumexp(x, dim=1, keepdim=True) + scores.double().view(-1, 1)).view(batch, -1)
+    want = torch.topk(total, keep).values
+    parents, tokens = best.parents.long(), best.tokens.long()
+    mine = total.gather(1, (parents % beams) * vocab + tokens)                          # the chosen ones' own scores
+    half = 2.0 ** -24 * mine.abs()
+    assert bool(((best.scores.double() - mine).abs() <= 2.0 ** -17 + half).all())
+    assert bool(((mine - want).abs() <= 2.0 ** -16).all()) and bool((mine[:, 1:] - mine[:, :-1] <= 2.0 ** -16).all())
+    for r in range(batch):
+        chosen = list(zip(parents[r].tolist(), tokens[r].tolist()))
+        assert len(set(chosen)) == keep
+        for p in set(parents[r].tolist()):
+            of = [t for q, t in chosen if q == p]
+            assert of == torch.sort(x[p], descending=True, stable=True).indices[:len(of)].tolist()

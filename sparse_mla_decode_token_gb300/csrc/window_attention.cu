@@ -1193,7 +1193,7 @@ cudaError_t launch_window_kernel(const KernelParams& kp, unsigned grid, int shif
 
 // plan: its groups, or nullptr for the window attention.
 cudaError_t launch_pair_attention(const WindowParams& p, const PrefixPlan* plan, int sms, cudaStream_t stream) {
-  KernelParams kp;
+  KernelParams kp = {};
   kp.p = p;
   if (plan != nullptr) kp.plan = *plan;
   kp.groups = (p.H + kNH - 1) / kNH;
@@ -1218,7 +1218,7 @@ cudaError_t launch_pair_attention(const WindowParams& p, const PrefixPlan* plan,
 }
 
 cudaError_t launch_planned_attention(const WindowParams& p, const PrefixPlan& plan, cudaStream_t stream) {
-  KernelParams kp;
+  KernelParams kp = {};
   kp.p = p;
   kp.plan = plan;
   kp.groups = (p.H + kNH - 1) / kNH;

@@ -279,7 +279,8 @@ def window_workspace_size(q: torch.Tensor, rows: torch.Tensor, scales: torch.Ten
                           cum_seq_lens_q: Optional[torch.Tensor] = None, num_splits: int = 0,
                           device: Optional[int] = None) -> int:
     """Workspace bytes of ``window_attention`` for these shapes (no device memory is
-    read), on ``device``, by default q's."""
+    read) and for fewer tokens, shorter windows or narrower tables, on ``device``, by
+    default q's."""
     a = _window_args(q, rows, scales, block_tables, seq_lens, cum_seq_lens_q, None, window, first_tokens, num_splits)
     n = ctypes.c_size_t(0)
     if device is None:
@@ -331,7 +332,7 @@ def prefix_workspace_size(q: torch.Tensor, rows: torch.Tensor, scales: torch.Ten
                           seq_lens: torch.Tensor, *, group_starts: torch.Tensor,
                           cum_seq_lens_q: Optional[torch.Tensor] = None, device: Optional[int] = None) -> int:
     """Workspace bytes of ``prefix_attention`` for these shapes (no device memory is
-    read), on ``device``, by default q's."""
+    read) and for fewer tokens, groups or table columns, on ``device``, by default q's."""
     a = _prefix_args(q, rows, scales, block_tables, seq_lens, cum_seq_lens_q, None, group_starts, None)
     n = ctypes.c_size_t(0)
     if device is None:

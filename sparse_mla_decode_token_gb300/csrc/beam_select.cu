@@ -21,11 +21,14 @@
 // that they have.  (In fp64, which has a fiftieth of fp32's rate, the second kernel takes
 // 15 us for the 32 beams of a request alone.)
 //
-// What bounds it: the first kernel reads each logit once (116 MB in 22 us, 5.3 TB/s; a
-// kernel that only reads them takes 20) with two thirds of the issue slots taken, the
-// second is a dozen dependent phases of one CTA a request.  Measured on a GB300: 64
-// requests of 8 beams over 128000 BF16 logits, 16 kept: 32.6 us (the choice 11); 8 of 32
-// beams over 151001 FP32 logits, 64 kept: 45.8 (19); one of 4 beams over 32000: 12.2 (9).
+// What bounds it: the first kernel reads each logit once with two thirds of the issue
+// slots taken (116 MB in 21.5 us, 5.4 TB/s, replayed behind itself, so that some of them
+// are still in L2; a kernel that only reads them takes 20; 25.1 us with flushed caches
+// under the profiler), the second is a dozen dependent phases of one CTA a request.
+// Measured on a GB300, replayed from a graph: 64 requests of 8 beams over 128000 BF16
+// logits, 16 kept: 32.7 us (the choice 11); 8 of 32 beams over 151001 FP32 logits, 64
+// kept: 45.4 (19); one of 4 beams over 32000: 12.1 (9).  As calls on other logits each
+// time: 34.5, 46.5 and 12.7.
 #include <cuda_fp16.h>
 
 #include <algorithm>

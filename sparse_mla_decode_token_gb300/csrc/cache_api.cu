@@ -145,14 +145,14 @@ struct WindowPlan {
   size_t lse, bytes;   // workspace: offset of the partials' LSEs, all of it
 };
 
+int64_t most_splits(int64_t pairs, int64_t tiles, int sms) {
+  return std::min<int64_t>({sms / pairs, tiles, kMaxWindowSplits});
+}
 // Splits that cost `pairs` pairs of `tiles` tiles least on `sms` SMs, one CTA each
 // at a time.  Measured on a GB300, a tile costs a CTA 2.5 us, and a second split
 // the merge: 1.3 tiles' time and a 7000th of one for each partial row of 512 values
 // (1 token x 64 heads, 2 tiles: 12.3 us whole, 12.9 in two; 3 tiles: 15.8 against
 // 13.5 in three; 32 x 128, 5 tiles: 22.5 against 24.2 in two, 9: 33.2 against 30.0).
-int64_t most_splits(int64_t pairs, int64_t tiles, int sms) {
-  return std::min<int64_t>({sms / pairs, tiles, kMaxWindowSplits});
-}
 int cheapest_splits(int64_t pairs, int64_t tiles, int sms) {
   const int64_t most = most_splits(pairs, tiles, sms);
   int best = 1;
@@ -246,6 +246,9 @@ smla_status check_prefix(const smla_prefix_args* a) {
 // (shared, each by itself): 64 tokens of 8 heads over 1300 rows 29.1 us and 26.4 (4.1
 // tiles an SM saved), over 2500 29.6 and 35.4 (7.4); of 32 heads over 2500 37.5 and 37.6
 // (4.2), over 4900 51.0 and 57.9 (8.2); 16 of 32 heads over 16000 48.3 and 46.7 (6.6).
+// Those tables were about as wide as the requests are long; the lengths are on the
+// device, so short requests of wide tables are shared, too (4 samples of 16 heads behind
+// 510 tokens: 14.0 us on tables of 10 pages, 22.8 on tables of 1024).
 constexpr double kSavedTiles = 6;
 bool shares_prefixes(const smla_prefix_args* a, int sms) {
   if (a->num_groups == 0) return false;

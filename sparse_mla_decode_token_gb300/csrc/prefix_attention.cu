@@ -24,11 +24,12 @@
 // What bounds it: the tile's chain in the kernel (window_attention.cu; 2.4 us a tile, its
 // tensor instructions 1.37), 8 us to a CTA's first scores and 4 of results, and before
 // and behind it the plan (4.5 us: trips to L2 and barriers of one CTA; with 1024 threads
-// 6) and the merge (3.5 us: four trips). Measured on a GB300: 64 samples of 16 heads
-// behind 8 prompts of 4 to 8 thousand 43.1 us, 309 TFLOP/s; 128 beams of 8 heads behind 4
-// documents of 16 thousand 65.5 us, 523 TFLOP/s (each token by itself: 81.6 and 276).
-// Without a plan: 4 samples of 16 heads behind 510 tokens 14.0 us (21.4 with one); 160
-// tokens of 128 heads over 1000 to 2560 rows 113 us, 662 TFLOP/s (117).  (Pieces of one
+// 6) and the merge (3.5 us: four trips). Measured on a GB300, replayed from a graph: 64
+// samples of 16 heads behind 8 prompts of 4 to 8 thousand 43.6 us, 305 TFLOP/s; 128 beams
+// of 8 heads behind 4 documents of 16 thousand 66.4 us, 516 TFLOP/s (each token by itself:
+// 81.6 and 274).  As calls on other inputs each time: 47.2 and 71.6.  Without a plan: 4
+// samples of 16 heads behind 510 tokens 14.0 us (22.8 with one); 160 tokens of 128 heads
+// over 1000 to 2560 rows 113.5 us, 659 TFLOP/s (117).  (Pieces of one
 // size, the best of 32 by a cost model, in turns of the SMs: 54.6, 78.4 and 168 us where
 // shares took 46.7, 69.8 and 126.)
 #include <algorithm>

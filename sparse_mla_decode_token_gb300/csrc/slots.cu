@@ -1,8 +1,8 @@
 // Slot maps of a step: offsets, positions and physical slots of its new tokens
 // from the requests' lengths, and the sparse decode's index table from page
 // tables.  Integer arithmetic and look-ups, bound by their latency.  Measured on a
-// GB300, both calls: 128 tokens with 2048 selected rows 6.2 us; 6704 tokens with 512
-// selected rows 12.7 us, 31 MB read and written.
+// GB300, both calls, replayed from a graph: 128 tokens with 2048 selected rows 6.2 us;
+// 6704 tokens with 512 selected rows 12.8 us, 31 MB read and written.
 #include "step.cuh"
 
 namespace smla {

@@ -71,9 +71,9 @@
 // rest is the chain second product -> free quarter -> rows -> first product ->
 // softmax of a buffer, which two 64 KB tiles (Q takes 64 KB, P 32) cannot hide
 // whole, and 7 us a unit for its query, sums and results.  Measured on a GB300:
-// 128 requests of one token, 128 heads, 2052 rows: 99 us, 696 TFLOP/s of the
+// 128 requests of one token, 128 heads, 2052 rows: 98.3 us, 701 TFLOP/s of the
 // plain products' count; 2049 tokens of four prompts, 128 heads, a window of 512:
-// 613 us, 452 TFLOP/s; two requests of 64 heads and 2 tiles: 12.4 us.  Logits so wide
+// 624 us, 444 TFLOP/s; two requests of 64 heads and 2 tiles: 13.4 us.  Logits so wide
 // that nearly every tile moves the reference (queries twice as long): decode 112 us;
 // codes all under 16, which takes a look at whole rows where it moves: 111 us.
 //

@@ -61,7 +61,8 @@ def _beam_args(logits: torch.Tensor, scores: torch.Tensor, num_out: Optional[int
 def beam_workspace_size(logits: torch.Tensor, scores: torch.Tensor, *, num_out: Optional[int] = None,
                         device: Optional[int] = None) -> int:
     """Workspace bytes of ``beam_select`` for these shapes (no device memory is
-    read), on ``device``, by default the logits'."""
+    read) and for fewer requests or beams or a smaller vocabulary, on ``device``, by
+    default the logits'."""
     a = _beam_args(logits, scores, num_out)
     n = ctypes.c_size_t(0)
     if device is None:

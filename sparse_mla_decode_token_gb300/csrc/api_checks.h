@@ -40,14 +40,19 @@ struct Area {
   int64_t rows, width, stride;
 };
 inline Area area(const void* at, int64_t bytes) { return {at, 1, bytes, bytes}; }
+// Bytes from the first piece's beginning to the last one's end (2^63 - 1 where that is more).
+inline int64_t span(int64_t rows, int64_t width, int64_t stride) {
+  int64_t n = 0;
+  return __builtin_mul_overflow(rows - 1, stride, &n) || __builtin_add_overflow(n, width, &n) ? INT64_MAX : n;
+}
 inline Area area(const void* at, int64_t rows, int64_t width, int64_t stride) {
-  return rows > 1 && stride > width ? Area{at, rows, width, stride} : area(at, rows * width);
+  return rows > 1 && stride > width ? Area{at, rows, width, stride} : area(at, rows < 1 ? 0 : span(rows, width, width));
 }
 // Have they memory in common?  Exact, but for rows of different strides that lie
 // between one another (taken to have).
 inline bool overlap(const Area& a, const Area& b) {
   if (a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1 ||
-      !overlap(a.at, (a.rows - 1) * a.stride + a.width, b.at, (b.rows - 1) * b.stride + b.width))
+      !overlap(a.at, span(a.rows, a.width, a.stride), b.at, span(b.rows, b.width, b.stride)))
     return false;
   if (a.rows > 1 && b.rows > 1 && a.stride != b.stride) return true;
   const Area& r = a.rows > 1 ? a : b;

@@ -137,3 +137,12 @@ def test_shared_prefixes_over_the_tables(lib):
         refused(lib.smla_pages_shared_prefix(ctypes.byref(a), 0x1000, 2, at, None), INVALID, "overlap")
     a.block_table_stride = 100
     refused(lib.smla_pages_shared_prefix(ctypes.byref(a), 0x1000, 2, 0x10000 + 396, None), INVALID, "overlap")
+
+
+def test_logits_of_more_bytes_than_a_number_holds(lib):
+    """2^31 rows of 2^31 fp32 logits: too many, whatever lies where; from the first one on they hold all that is behind."""
+    a = beam_struct()
+    a.batch, a.beams, a.vocab, a.dtype, a.num_out = (1 << 25) - 1, 64, (1 << 31) - 1, 2, 1
+    refused(lib.smla_beam_select(ctypes.byref(a), None), INVALID, "overlap")
+    a.logits_stride = (1 << 61) - 1
+    refused(lib.smla_beam_select(ctypes.byref(a), None), INVALID, "overlap")

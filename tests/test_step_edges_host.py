@@ -143,6 +143,7 @@ def test_logits_of_more_bytes_than_a_number_holds(lib):
     """2^31 rows of 2^31 fp32 logits: too many, whatever lies where; from the first one on they hold all that is behind."""
     a = beam_struct()
     a.batch, a.beams, a.vocab, a.dtype, a.num_out = (1 << 25) - 1, 64, (1 << 31) - 1, 2, 1
+    a.out_scores, a.out_parents, a.out_tokens, a.scores = 1 << 40, 1 << 41, 1 << 42, 1 << 43
     refused(lib.smla_beam_select(ctypes.byref(a), None), INVALID, "overlap")
     a.logits_stride = (1 << 61) - 1
     refused(lib.smla_beam_select(ctypes.byref(a), None), INVALID, "overlap")

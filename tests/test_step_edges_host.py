@@ -145,5 +145,6 @@ def test_logits_of_more_bytes_than_a_number_holds(lib):
     a.batch, a.beams, a.vocab, a.dtype, a.num_out = (1 << 25) - 1, 64, (1 << 31) - 1, 2, 1
     a.out_scores, a.out_parents, a.out_tokens, a.scores = 1 << 40, 1 << 41, 1 << 42, 1 << 43
     refused(lib.smla_beam_select(ctypes.byref(a), None), INVALID, "overlap")
-    a.logits_stride = (1 << 61) - 1
+    a.logits, a.logits_stride = 0x10000, (1 << 61) - 1               # rows so far apart that all lies behind the first
+    a.out_tokens = 0x10000 + (1 << 33) - 8
     refused(lib.smla_beam_select(ctypes.byref(a), None), INVALID, "overlap")
